@@ -388,6 +388,102 @@ int snk_forward_csr_noalloc(int64_t out_features, int64_t in_features, int64_t n
                             const float* X, int64_t batch, const float* bias, float* Y,
                             void* stream);
 
+/*
+ * 8-bit activations.  No page has a counterpart: [SNACK] and [PCSR] keep
+ * activations in fp32, and in a block of truly sparse layers those kept for
+ * the backward pass outweigh the weights.  The calls below write and read a
+ * matrix [rows, cols] as one byte per element (`codes`, row-major, contiguous)
+ * and one fp32 scale per group of `group` consecutive columns of a row
+ * (`scales`, [rows, ceil(cols / group)]; the last group of a row may be
+ * short).  Element (r, c) stands for scales[r, c / group] * code.
+ *   format  SNK_Q8_INT8: codes are int8 in [-127, 127], Q = 127;
+ *           SNK_Q8_E4M3: codes are 8-bit floats (4 exponent bits, 3 mantissa
+ *           bits, no infinities), Q = 448.
+ *   group   32, 64, 128 or 256; 0 = one scale for the whole row.
+ *   With m the largest magnitude of a group: scale = m / Q and code = y * (Q / m)
+ *   rounded to the nearest code, half to even (both quotients rounded to
+ *   fp32).  m < 2^-100 gives scale 0 and codes 0.  A group that holds an inf or
+ *   NaN gets scale NaN and codes 0: each of its values reads as NaN.
+ * Other matrices of these calls have the element type `dtype` (SNK_F32,
+ * SNK_F16 or SNK_BF16), row-major and contiguous; gains, scales, reciprocal
+ * norms and sums are fp32 whatever the type.  Pointers need the alignment of
+ * their element.  rows == 0 is a no-op (dgain is then zero).  cols >= 1; rows
+ * and cols < 2^31 and rows * ceil(cols / 256) < 2^31 (SNK_ERR_LIMIT).  The
+ * calls without a handle allocate nothing, use no state and only enqueue
+ * kernels, so they may be captured into a CUDA graph.  Results do not depend
+ * on timing: repeated calls give the same bits.
+ */
+#define SNK_F32 0
+#define SNK_F16 1
+#define SNK_BF16 2
+#define SNK_Q8_INT8 0
+#define SNK_Q8_E4M3 1
+
+/* codes, scales of x [rows, cols].  Errors: SNK_ERR_ARG, SNK_ERR_LIMIT, SNK_ERR_CUDA. */
+int snk_q8_pack(const void* x, int dtype, int64_t rows, int64_t cols, int format, int group,
+                void* codes, float* scales, void* stream);
+
+/* x = scale * code.  Errors as above. */
+int snk_q8_unpack(const void* codes, const float* scales, int64_t rows, int64_t cols, int format,
+                  int group, void* x, int dtype, void* stream);
+
+/*
+ * codes, scales of gelu(x) = x Phi(x), Phi the normal distribution function;
+ * kept_codes, kept_scales (both or neither): those of x itself, in the same
+ * format, which snk_gelu_backward_q8 takes.  Errors as above.
+ */
+int snk_gelu_q8(const void* x, int dtype, int64_t rows, int64_t cols, int format, int group,
+                void* codes, float* scales, void* kept_codes, float* kept_scales, void* stream);
+
+/*
+ * dh = da * (Phi(h) + h phi(h)) with h = scale * code, phi the normal density:
+ * the gradient at the input that the 8-bit matrix kept (the rounding to 8 bits
+ * is passed through as the identity).  dh may be da.  Errors as above.
+ */
+int snk_gelu_backward_q8(const void* da, int dtype, const void* codes, const float* scales,
+                         int64_t rows, int64_t cols, int format, int group, void* dh,
+                         void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and an 8-bit output:
+ *   r = x + residual, rounded to dtype and written to `total`;
+ *   rstd = 1 / sqrt(mean(r^2) + eps) for each row, written to rstd [rows];
+ *   codes, scales of r * rstd * gain (gain [cols]).
+ * residual NULL: r = x, and total must be NULL too.  total may be x or
+ * residual.  eps > 0.  Errors as above.
+ */
+int snk_rmsnorm_q8(const void* x, const void* residual, int dtype, const float* gain, int64_t rows,
+                   int64_t cols, float eps, int format, int group, void* codes, float* scales,
+                   void* total, float* rstd, void* stream);
+
+/*
+ * Its gradient (the rounding to 8 bits passed through).  With n = total * rstd
+ * (total is x itself where there was no residual):
+ *   dx = rstd * (gain dy - n * mean(gain dy n)) + dtotal
+ *   dgain = sum over the rows of dy n
+ * dy [rows, cols] fp32 is the gradient of the norm's output, dtotal (dtype, or
+ * NULL for none) that of `total` on its other path; dx is the gradient of x
+ * and of residual alike.  dx may be dtotal or total.  dgain [cols] or NULL.
+ * scratch: snk_rmsnorm_backward_scratch(rows, cols) bytes, 32-byte aligned
+ * (not needed when dgain is NULL).  Errors as above.
+ */
+int64_t snk_rmsnorm_backward_scratch(int64_t rows, int64_t cols);
+int snk_rmsnorm_backward(const float* dy, const void* total, int dtype, const float* rstd,
+                         const float* gain, const void* dtotal, int64_t rows, int64_t cols,
+                         void* dx, float* dgain, void* scratch, void* stream);
+
+/*
+ * snk_forward and snk_backward_weight with an 8-bit X [batch, in] (codes,
+ * scales, format, group as above): the same products, dispatch, numerics and
+ * rules of capture, with X[beta, c] = scale * code (rounded to fp32).  No fp32
+ * copy of the whole X is made.  Errors: SNK_ERR_ARG, SNK_ERR_OOM, SNK_ERR_CUDA.
+ */
+int snk_forward_q8(snk_handle handle, const void* codes, const float* scales, int format,
+                   int group, int64_t batch, const float* bias, float* Y, void* stream);
+int snk_backward_weight_q8(snk_handle handle, const void* codes, const float* scales, int format,
+                           int group, const float* dY, int64_t batch, float* dW, float* db,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,8 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "snk.h")
 
 SNK_OK, SNK_ERR_ARG, SNK_ERR_DUP, SNK_ERR_RANGE = 0, 1, 2, 3
 SNK_ERR_CUDA, SNK_ERR_OOM, SNK_ERR_NOSPACE, SNK_ERR_LIMIT = 4, 5, 6, 7
+SNK_F32, SNK_F16, SNK_BF16 = 0, 1, 2
+SNK_Q8_INT8, SNK_Q8_E4M3 = 0, 1
 
 _lock = threading.Lock()
 _lib = None
@@ -64,11 +66,23 @@ def lib():
         L.snk_pcsr_delete.argtypes = [P, i64, P, P, P]
         L.snk_pcsr_compact.argtypes = [P, P]
         L.snk_pcsr_export.argtypes = [P, P, P, P, i64, ctypes.POINTER(i64), P]
+        L.snk_q8_pack.argtypes = [P, I, i64, i64, I, I, P, P, P]
+        L.snk_q8_unpack.argtypes = [P, P, i64, i64, I, I, P, I, P]
+        L.snk_gelu_q8.argtypes = [P, I, i64, i64, I, I, P, P, P, P, P]
+        L.snk_gelu_backward_q8.argtypes = [P, I, P, P, i64, i64, I, I, P, P]
+        L.snk_rmsnorm_q8.argtypes = [P, P, I, P, i64, i64, f32, I, I, P, P, P, P, P]
+        L.snk_rmsnorm_backward_scratch.argtypes = [i64, i64]
+        L.snk_rmsnorm_backward_scratch.restype = i64
+        L.snk_rmsnorm_backward.argtypes = [P, P, I, P, P, P, i64, i64, P, P, P, P]
+        L.snk_forward_q8.argtypes = [P, P, P, I, I, i64, P, P, P]
+        L.snk_backward_weight_q8.argtypes = [P, P, P, I, I, P, i64, P, P, P]
         for name in ("snk_create", "snk_forward", "snk_backward_input", "snk_backward_weight",
                      "snk_prune_regrow", "snk_prune_regrow_gradient", "snk_destroy",
                      "snk_get_shape", "snk_copy_topology", "snk_check", "snk_forward_csr_noalloc",
                      "snk_pcsr_build", "snk_pcsr_info", "snk_pcsr_copy", "snk_pcsr_insert",
-                     "snk_pcsr_delete", "snk_pcsr_compact", "snk_pcsr_export"):
+                     "snk_pcsr_delete", "snk_pcsr_compact", "snk_pcsr_export", "snk_q8_pack",
+                     "snk_q8_unpack", "snk_gelu_q8", "snk_gelu_backward_q8", "snk_rmsnorm_q8",
+                     "snk_rmsnorm_backward", "snk_forward_q8", "snk_backward_weight_q8"):
             getattr(L, name).restype = I
         _lib = L
         return L
@@ -224,6 +238,62 @@ def snk_pcsr_export(handle: int, values, rows, cols, stream=None) -> int:
     return n.value
 
 
+def snk_q8_pack(x, dtype: int, rows: int, cols: int, format: int, group: int, codes, scales,
+                stream=None):
+    _check(lib().snk_q8_pack(_ptr(x), dtype, rows, cols, format, group, _ptr(codes), _ptr(scales),
+                             _stream(stream)), "snk_q8_pack")
+
+
+def snk_q8_unpack(codes, scales, rows: int, cols: int, format: int, group: int, x, dtype: int,
+                  stream=None):
+    _check(lib().snk_q8_unpack(_ptr(codes), _ptr(scales), rows, cols, format, group, _ptr(x), dtype,
+                               _stream(stream)), "snk_q8_unpack")
+
+
+def snk_gelu_q8(x, dtype: int, rows: int, cols: int, format: int, group: int, codes, scales,
+                kept_codes=None, kept_scales=None, stream=None):
+    _check(lib().snk_gelu_q8(_ptr(x), dtype, rows, cols, format, group, _ptr(codes), _ptr(scales),
+                             _ptr(kept_codes), _ptr(kept_scales), _stream(stream)), "snk_gelu_q8")
+
+
+def snk_gelu_backward_q8(da, dtype: int, codes, scales, rows: int, cols: int, format: int,
+                         group: int, dh, stream=None):
+    _check(lib().snk_gelu_backward_q8(_ptr(da), dtype, _ptr(codes), _ptr(scales), rows, cols, format,
+                                      group, _ptr(dh), _stream(stream)), "snk_gelu_backward_q8")
+
+
+def snk_rmsnorm_q8(x, residual, dtype: int, gain, rows: int, cols: int, eps: float, format: int,
+                   group: int, codes, scales, total, rstd, stream=None):
+    _check(lib().snk_rmsnorm_q8(_ptr(x), _ptr(residual), dtype, _ptr(gain), rows, cols, eps, format,
+                                group, _ptr(codes), _ptr(scales), _ptr(total), _ptr(rstd),
+                                _stream(stream)), "snk_rmsnorm_q8")
+
+
+def snk_rmsnorm_backward_scratch(rows: int, cols: int) -> int:
+    """Bytes of scratch that snk_rmsnorm_backward needs."""
+    return lib().snk_rmsnorm_backward_scratch(rows, cols)
+
+
+def snk_rmsnorm_backward(dy, total, dtype: int, rstd, gain, dtotal, rows: int, cols: int, dx, dgain,
+                         scratch, stream=None):
+    _check(lib().snk_rmsnorm_backward(_ptr(dy), _ptr(total), dtype, _ptr(rstd), _ptr(gain),
+                                      _ptr(dtotal), rows, cols, _ptr(dx), _ptr(dgain), _ptr(scratch),
+                                      _stream(stream)), "snk_rmsnorm_backward")
+
+
+def snk_forward_q8(handle: int, codes, scales, format: int, group: int, batch: int, bias, Y,
+                   stream=None):
+    _check(lib().snk_forward_q8(handle, _ptr(codes), _ptr(scales), format, group, batch, _ptr(bias),
+                                _ptr(Y), _stream(stream)), "snk_forward_q8")
+
+
+def snk_backward_weight_q8(handle: int, codes, scales, format: int, group: int, dY, batch: int, dW,
+                           db=None, stream=None):
+    _check(lib().snk_backward_weight_q8(handle, _ptr(codes), _ptr(scales), format, group, _ptr(dY),
+                                        batch, _ptr(dW), _ptr(db), _stream(stream)),
+           "snk_backward_weight_q8")
+
+
 class SparseLinear:
     """Convenience owner of one layer: keeps the caller-side tensors alive for
     the handle's lifetime and allocates outputs with torch."""
@@ -260,6 +330,26 @@ class SparseLinear:
         dW = out if out is not None else torch.empty_like(self.values)
         db = torch.empty(self.out_features, dtype=torch.float32, device=dY.device) if with_bias else None
         snk_backward_weight(self.handle, X, dY, dW, db, stream)
+        return (dW, db) if with_bias else dW
+
+    def forward_q8(self, X, bias=None, out=None, stream=None):
+        """forward() with X an 8-bit matrix (q8.Q8Tensor, [batch, in])."""
+        import torch
+        X.require(self.in_features)
+        Y = out if out is not None else torch.empty((X.rows, self.out_features),
+                                                    dtype=torch.float32, device=X.codes.device)
+        snk_forward_q8(self.handle, X.codes, X.scales, X.format_id, X.group, X.rows, bias, Y, stream)
+        return Y
+
+    def backward_weight_q8(self, X, dY, with_bias: bool = False, out=None, stream=None):
+        """backward_weight() with X an 8-bit matrix (q8.Q8Tensor, [batch, in])."""
+        import torch
+        X.require(self.in_features)
+        if dY.dtype != torch.float32 or dY.numel() != X.rows * self.out_features:
+            raise ValueError(f"dY is float32 [{X.rows}, {self.out_features}]: got {dY.dtype} {tuple(dY.shape)}")
+        dW = out if out is not None else torch.empty_like(self.values)
+        db = torch.empty(self.out_features, dtype=torch.float32, device=dY.device) if with_bias else None
+        snk_backward_weight_q8(self.handle, X.codes, X.scales, X.format_id, X.group, dY, X.rows, dW, db, stream)
         return (dW, db) if with_bias else dW
 
     def prune_regrow(self, zeta: float, seed: int, stream=None):

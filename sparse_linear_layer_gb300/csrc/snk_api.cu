@@ -5,7 +5,7 @@
 
 #include <algorithm>
 
-#include "snk_internal.cuh"
+#include "snk_q8.cuh"
 
 namespace snk {
 
@@ -15,6 +15,10 @@ namespace snk {
 static bool fault(const char* what) {
     const char* f = getenv("SNK_FAULT");
     return f && strcmp(f, what) == 0;
+}
+
+static bool bad_q8(int format, int group) {
+    return (format != SNK_Q8_INT8 && format != SNK_Q8_E4M3) || !q8_group_ok(group);
 }
 
 static bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -143,7 +147,7 @@ int snk_forward(snk_handle h, const float* X, int64_t batch, const float* bias, 
     if (batch == 0) return SNK_OK;
     if (!X || !Y || !aligned(X, 4) || !aligned(Y, 4) || !aligned(bias, 4)) return SNK_ERR_ARG;
     if (fault("launch")) return SNK_ERR_CUDA;
-    return launch_forward(L, X, batch, bias, Y, (cudaStream_t)stream);
+    return launch_forward(L, X, nullptr, batch, bias, Y, (cudaStream_t)stream);
 }
 
 int snk_backward_input(snk_handle h, const float* dY, int64_t batch, float* dX, void* stream) {
@@ -164,7 +168,30 @@ int snk_backward_weight(snk_handle h, const float* X, const float* dY, int64_t b
     if (!aligned(X, 4) || !aligned(dY, 4) || !aligned(dW, 16) || !aligned(db, 4))
         return SNK_ERR_ARG;
     if (fault("launch")) return SNK_ERR_CUDA;
-    return launch_backward_weight(L, X, dY, batch, dW, db, (cudaStream_t)stream);
+    return launch_backward_weight(L, X, nullptr, dY, batch, dW, db, (cudaStream_t)stream);
+}
+
+int snk_forward_q8(snk_handle h, const void* codes, const float* scales, int format, int group, int64_t batch,
+                   const float* bias, float* Y, void* stream) {
+    Layer* L = reinterpret_cast<Layer*>(h);
+    if (!L || batch < 0 || bad_q8(format, group)) return SNK_ERR_ARG;
+    if (batch == 0) return SNK_OK;
+    if (!codes || !scales || !Y || !aligned(scales, 4) || !aligned(Y, 4) || !aligned(bias, 4)) return SNK_ERR_ARG;
+    if (fault("launch")) return SNK_ERR_CUDA;
+    const Q8In q{(const uint8_t*)codes, scales, format, q8_gshift(group), q8_groups(L->in_f, group), L->in_f};
+    return launch_forward(L, nullptr, &q, batch, bias, Y, (cudaStream_t)stream);
+}
+
+int snk_backward_weight_q8(snk_handle h, const void* codes, const float* scales, int format, int group,
+                           const float* dY, int64_t batch, float* dW, float* db, void* stream) {
+    Layer* L = reinterpret_cast<Layer*>(h);
+    if (!L || batch < 0 || bad_q8(format, group)) return SNK_ERR_ARG;
+    if (batch == 0) return SNK_OK;
+    if (!codes || !scales || !dY || (!dW && L->nnz > 0)) return SNK_ERR_ARG;
+    if (!aligned(scales, 4) || !aligned(dY, 4) || !aligned(dW, 16) || !aligned(db, 4)) return SNK_ERR_ARG;
+    if (fault("launch")) return SNK_ERR_CUDA;
+    const Q8In q{(const uint8_t*)codes, scales, format, q8_gshift(group), q8_groups(L->in_f, group), L->in_f};
+    return launch_backward_weight(L, nullptr, &q, dY, batch, dW, db, (cudaStream_t)stream);
 }
 
 int snk_prune_regrow(snk_handle h, float zeta, uint64_t seed, void* stream) {

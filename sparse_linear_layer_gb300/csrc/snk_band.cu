@@ -354,8 +354,12 @@ __global__ void k_band_transpose(const float* __restrict__ X, int64_t n, int b, 
 namespace {
 
 template <int BP>
-int launch_band_bp(Layer* L, BandArgs a, const BandTable* t, const float* X, cudaStream_t s) {
-    k_band_transpose<BP><<<L->num_sms * 4, 256, 0, s>>>(X, L->in_f, a.b, L->xt);
+int launch_band_bp(Layer* L, BandArgs a, const BandTable* t, const float* X, const Q8In* q, cudaStream_t s) {
+    if (q) {
+        if (int st = launch_q8_transposed(*q, a.b, BP, L->xt, L->num_sms, s); st != SNK_OK) return st;
+    } else {
+        k_band_transpose<BP><<<L->num_sms * 4, 256, 0, s>>>(X, L->in_f, a.b, L->xt);
+    }
     a.xt = L->xt;
     a.run = t->run;
     a.cut = t->cut;
@@ -373,7 +377,7 @@ int launch_band_bp(Layer* L, BandArgs a, const BandTable* t, const float* X, cud
 
 }  // namespace
 
-int band_backward_weight(Layer* L, int bp, const float* X, const float* dY, int b, float* dW, bool accumulate,
+int band_backward_weight(Layer* L, int bp, const float* X, const Q8In* q, const float* dY, int b, float* dW, bool accumulate,
                          const float* dY_all, int64_t b_all, float* db, cudaStream_t s, bool* done) {
     *done = false;
     int st = SNK_OK;
@@ -392,10 +396,10 @@ int band_backward_weight(Layer* L, int bp, const float* X, const float* dY, int 
     a.db = db;
     *done = true;
     switch (t->bp) {
-        case 8: return launch_band_bp<8>(L, a, t, X, s);
-        case 16: return launch_band_bp<16>(L, a, t, X, s);
-        case 32: return launch_band_bp<32>(L, a, t, X, s);
-        default: return launch_band_bp<64>(L, a, t, X, s);
+        case 8: return launch_band_bp<8>(L, a, t, X, q, s);
+        case 16: return launch_band_bp<16>(L, a, t, X, q, s);
+        case 32: return launch_band_bp<32>(L, a, t, X, q, s);
+        default: return launch_band_bp<64>(L, a, t, X, q, s);
     }
 }
 

@@ -148,6 +148,37 @@ struct Layer {
 
 void free_pcsr(Layer* L);
 
+// An 8-bit matrix as the products read it (snk_q8.cuh): scale * code.
+struct Q8In {
+    const uint8_t* codes;    // [rows, cols]
+    const float* scales;     // [rows, n_groups]
+    int format;
+    int gshift;              // log2(columns per scale); 31: one scale per row
+    int64_t n_groups;
+    int64_t cols;
+    Q8In from_row(int64_t r) const {
+        Q8In q = *this;
+        q.codes += r * cols;
+        q.scales += r * n_groups;
+        return q;
+    }
+};
+
+// A dense operand read one value at a time: fp32, or an 8-bit matrix.
+struct SrcF32 {
+    const float* p;
+    int64_t cols;
+    __device__ __forceinline__ float at(int64_t r, int64_t c) const { return __ldg(p + r * cols + c); }
+    SrcF32 from_row(int64_t r) const { return SrcF32{p + r * cols, cols}; }
+    bool rows_of_4() const { return cols % 4 == 0 && ((uintptr_t)p & 15) == 0; }
+};
+struct SrcQ8 {
+    Q8In q;
+    __device__ __forceinline__ float at(int64_t r, int64_t c) const;
+    SrcQ8 from_row(int64_t r) const { return SrcQ8{q.from_row(r)}; }
+    bool rows_of_4() const { return q.cols % 4 == 0 && ((uintptr_t)q.codes & 3) == 0; }
+};
+
 // ---- column sweep of the transposed product (snk_sweep.cu) ---------------
 // Every column of a block gets its own lanes, as many as its share of the
 // block's entries; see snk_sweep.cu for the tables' layout.
@@ -172,7 +203,8 @@ bool sweep_view(const Layer* L, SweepView* v);
 // memory: each block stages one band of the transposed operand and walks the
 // runs of its rows in that band.  *done says whether the layer took this path
 // (false: no bands for it; the caller goes on).
-int band_backward_weight(Layer* L, int bp, const float* X, const float* dY, int b, float* dW, bool accumulate,
+// X is fp32 [b, in], or the 8-bit matrix q when that is given.
+int band_backward_weight(Layer* L, int bp, const float* X, const Q8In* q, const float* dY, int b, float* dW, bool accumulate,
                          const float* dY_all, int64_t b_all, float* db, cudaStream_t s, bool* done);
 // The band count and width for a batch tile of bp columns; false when the
 // layer takes no bands (operand fits, runs too short, or too few entries).
@@ -185,11 +217,11 @@ void free_bands(Layer* L);
 bool tc_eligible(const Layer* L, int64_t b);
 // Y[b, n_seg] = D[b, K] times the rows (columns = false) or the columns of W,
 // + bias.  Allocates and builds the tile-ordered view on first use.
-int run_tc(Layer* L, bool columns, const float* D, int64_t b, const float* bias, float* Y,
-           cudaStream_t s);
+template <class Src>
+int run_tc(Layer* L, bool columns, const Src& D, int64_t b, const float* bias, float* Y, cudaStream_t s);
 // dW on the entries of W (and db = column sums of dY) for a large batch.
-int run_tc_sddmm(Layer* L, const float* X, const float* dY, int64_t b, float* dW, float* db,
-                 cudaStream_t s);
+template <class Src>
+int run_tc_sddmm(Layer* L, const Src& X, const float* dY, int64_t b, float* dW, float* db, cudaStream_t s);
 int refresh_tc_views(Layer* L, cudaStream_t s);
 
 // The tensor path's fp16 split holds a value x of a row scaled by 2^e to
@@ -221,19 +253,21 @@ struct TcSide {
 };
 // snk_tc_exact.cu: Y[rows[i], o] for every segment o (rows relative to D and
 // Y), for i < *n_rows.
-int launch_exact_rows(const TcSide& sd, int64_t n_seg, const float* D, int64_t K,
-                      const float* bias, float* Y, const int32_t* rows, const uint32_t* n_rows,
+template <class Src>
+int launch_exact_rows(const TcSide& sd, int64_t n_seg, const Src& D, const float* bias, float* Y, const int32_t* rows, const uint32_t* n_rows,
                       int num_sms, cudaStream_t s);
 // Y[beta, o] for every beta < b and every candidate segment o that
 // tc_needs_exact confirms against other[0] (largest L1 norm of the dense rows)
 // and other[1] (their largest magnitude), both fp32 bit patterns.
-int launch_exact_segs(const TcSide& sd, int64_t n_seg, const float* D, int64_t K, int64_t b,
+template <class Src>
+int launch_exact_segs(const TcSide& sd, int64_t n_seg, const Src& D, int64_t b,
                       const float* bias, float* Y, const int32_t* cand, const uint32_t* n_cand,
                       const int32_t* seg_exp, const int32_t* seg_code, const uint32_t* other,
                       int num_sms, cudaStream_t s);
 // dW for every entry of the listed rows (values below out) and columns
 // (out + column) of W, over the whole batch.
-int launch_exact_dw(const Layer* L, const float* X, const float* dY, int64_t b, float* dW,
+template <class Src>
+int launch_exact_dw(const Layer* L, const Src& X, const float* dY, int64_t b, float* dW,
                     const int32_t* list, const uint32_t* n_list, cudaStream_t s);
 void mark_tc_views(Layer* L);
 void free_tc(Layer* L);
@@ -267,11 +301,16 @@ int sort_pairs_u32(uint32_t* keys, uint32_t* vals, uint32_t* keys_alt, uint32_t*
                    int total_bits, int32_t* hist, int64_t hist_len, cudaStream_t s, bool* flipped);
 
 // ---- kernels launched by the API ----------------------------------------
-int launch_forward(Layer* L, const float* X, int64_t b, const float* bias, float* Y,
+// X is fp32, or the 8-bit matrix q when that is given (X is then not read).
+int launch_forward(Layer* L, const float* X, const Q8In* q, int64_t b, const float* bias, float* Y,
                    cudaStream_t s);
 int launch_backward_input(Layer* L, const float* dY, int64_t b, float* dX, cudaStream_t s);
-int launch_backward_weight(Layer* L, const float* X, const float* dY, int64_t b, float* dW,
+int launch_backward_weight(Layer* L, const float* X, const Q8In* q, const float* dY, int64_t b, float* dW,
                            float* db, cudaStream_t s);
+// snk_q8.cu: rows [0, b) of an 8-bit matrix as fp32 [b, cols], and transposed
+// into dst[cols][bp] (zero columns from b on; bp a power of two up to 64).
+int launch_q8_rows(const Q8In& q, int64_t b, float* dst, cudaStream_t s);
+int launch_q8_transposed(const Q8In& q, int b, int bp, float* dst, int num_sms, cudaStream_t s);
 int run_prune_regrow(Layer* L, float zeta, uint64_t seed, cudaStream_t s);
 int run_prune_regrow_gradient(Layer* L, float zeta, const float* X, const float* dY, int64_t b,
                               cudaStream_t s);

@@ -211,19 +211,23 @@ __global__ void k_bias_grad_only(const float* __restrict__ dY, int64_t b, int64_
 }
 
 template <int BP>
-static int launch_bp(Layer* L, SddmmArgs a, cudaStream_t s) {
+static int launch_bp(Layer* L, SddmmArgs a, const Q8In* q, cudaStream_t s) {
     const size_t smem = (size_t)a.in_f * BP * sizeof(float);
     const int grid = a.n_blocks;
     if constexpr (BP >= 8 && SNK_BANDS) {
         // an operand too wide for shared memory: row runs over column bands
         if (smem > (size_t)L->max_smem) {
             bool done = false;
-            const int st = band_backward_weight(L, BP, a.X, a.dY, a.b, a.dW, a.accumulate, a.dY_all, a.b_all,
+            const int st = band_backward_weight(L, BP, a.X, q, a.dY, a.b, a.dW, a.accumulate, a.dY_all, a.b_all,
                                                 a.db, s, &done);
             if (st != SNK_OK || done) return st;
         }
     }
     if (smem <= (size_t)L->max_smem && a.col16) {
+        if (q) {
+            if (int st = launch_q8_rows(*q, a.b, L->xt, s); st != SNK_OK) return st;
+            a.X = L->xt;
+        }
         auto fn = k_sddmm<BP, true>;
         if (smem > 48 * 1024 &&
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -231,14 +235,18 @@ static int launch_bp(Layer* L, SddmmArgs a, cudaStream_t s) {
             return SNK_ERR_CUDA;
         fn<<<grid, kThreads, smem, s>>>(a);
     } else {
-        k_transpose_x<BP><<<L->num_sms * 4, 256, 0, s>>>(a.X, a.in_f, a.b, L->xt);
+        if (q) {
+            if (int st = launch_q8_transposed(*q, a.b, BP, L->xt, L->num_sms, s); st != SNK_OK) return st;
+        } else {
+            k_transpose_x<BP><<<L->num_sms * 4, 256, 0, s>>>(a.X, a.in_f, a.b, L->xt);
+        }
         a.xt = L->xt;
         k_sddmm<BP, false><<<grid, kThreads, 0, s>>>(a);
     }
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
 
-int launch_backward_weight(Layer* L, const float* X, const float* dY, int64_t b, float* dW,
+int launch_backward_weight(Layer* L, const float* X, const Q8In* q, const float* dY, int64_t b, float* dW,
                            float* db, cudaStream_t s) {
     if (L->nnz == 0) {
         if (db) {
@@ -247,7 +255,9 @@ int launch_backward_weight(Layer* L, const float* X, const float* dY, int64_t b,
         }
         return SNK_OK;
     }
-    if (tc_eligible(L, b)) return run_tc_sddmm(L, X, dY, b, dW, db, s);
+    if (tc_eligible(L, b))
+        return q ? run_tc_sddmm(L, SrcQ8{*q}, dY, b, dW, db, s)
+                 : run_tc_sddmm(L, SrcF32{X, L->in_f}, dY, b, dW, db, s);
     SddmmArgs a{};
     a.col = L->c;
     a.col16 = L->c16;
@@ -263,19 +273,22 @@ int launch_backward_weight(Layer* L, const float* X, const float* dY, int64_t b,
     for (int64_t t0 = 0; t0 < b; t0 += kMaxBatchTile) {
         const int64_t bt = std::min<int64_t>(kMaxBatchTile, b - t0);
         a.b = (int)bt;
-        a.X = X + t0 * L->in_f;
+        Q8In qt{};
+        if (q) qt = q->from_row(t0);
+        else a.X = X + t0 * L->in_f;
+        const Q8In* qp = q ? &qt : nullptr;
         a.dY = dY + t0 * L->out_f;
         a.accumulate = t0 > 0;
         a.db = (t0 == 0) ? db : nullptr;
         int st;
         switch (batch_tile(bt)) {
-            case 1: st = launch_bp<1>(L, a, s); break;
-            case 2: st = launch_bp<2>(L, a, s); break;
-            case 4: st = launch_bp<4>(L, a, s); break;
-            case 8: st = launch_bp<8>(L, a, s); break;
-            case 16: st = launch_bp<16>(L, a, s); break;
-            case 32: st = launch_bp<32>(L, a, s); break;
-            default: st = launch_bp<64>(L, a, s); break;
+            case 1: st = launch_bp<1>(L, a, qp, s); break;
+            case 2: st = launch_bp<2>(L, a, qp, s); break;
+            case 4: st = launch_bp<4>(L, a, qp, s); break;
+            case 8: st = launch_bp<8>(L, a, qp, s); break;
+            case 16: st = launch_bp<16>(L, a, qp, s); break;
+            case 32: st = launch_bp<32>(L, a, qp, s); break;
+            default: st = launch_bp<64>(L, a, qp, s); break;
         }
         if (st != SNK_OK) return st;
     }

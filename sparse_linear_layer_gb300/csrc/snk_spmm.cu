@@ -675,7 +675,7 @@ static int set_smem(F fn, size_t smem) {
 }
 
 template <int BP, bool GATHER>
-static int launch_bp(Layer* L, SpmmArgs a, cudaStream_t s) {
+static int launch_bp(Layer* L, SpmmArgs a, const Q8In* q, cudaStream_t s) {
     constexpr int NT = SpmmShape<GATHER>::kNT;
     const size_t slots = spmm_slot_bytes<BP, GATHER>();
     const size_t smem = operand_floats(a.n_src, BP) * sizeof(float) + slots;
@@ -717,11 +717,19 @@ static int launch_bp(Layer* L, SpmmArgs a, cudaStream_t s) {
         }
     }
     if (smem <= (size_t)L->max_smem && a.idx16) {
+        if (q) {
+            if (int st = launch_q8_rows(*q, a.b, L->xt, s); st != SNK_OK) return st;
+            a.X = L->xt;
+        }
         auto fn = k_spmm<BP, GATHER, true>;
         if (set_smem(fn, smem) != SNK_OK) return SNK_ERR_CUDA;
         fn<<<a.n_blocks, NT, smem, s>>>(a);
     } else {
-        k_transpose<BP><<<L->num_sms * 4, 256, 0, s>>>(a.X, a.n_src, a.b, L->xt);
+        if (q) {
+            if (int st = launch_q8_transposed(*q, a.b, BP, L->xt, L->num_sms, s); st != SNK_OK) return st;
+        } else {
+            k_transpose<BP><<<L->num_sms * 4, 256, 0, s>>>(a.X, a.n_src, a.b, L->xt);
+        }
         a.xt = L->xt;
         auto fn = k_spmm<BP, GATHER, false>;
         if (set_smem(fn, slots) != SNK_OK) return SNK_ERR_CUDA;
@@ -731,33 +739,35 @@ static int launch_bp(Layer* L, SpmmArgs a, cudaStream_t s) {
 }
 
 template <bool GATHER>
-static int launch_tile(Layer* L, const SpmmArgs& a, int bp, cudaStream_t s) {
+static int launch_tile(Layer* L, const SpmmArgs& a, int bp, const Q8In* q, cudaStream_t s) {
     switch (bp) {
-        case 1: return launch_bp<1, GATHER>(L, a, s);
-        case 2: return launch_bp<2, GATHER>(L, a, s);
-        case 4: return launch_bp<4, GATHER>(L, a, s);
-        case 8: return launch_bp<8, GATHER>(L, a, s);
-        case 16: return launch_bp<16, GATHER>(L, a, s);
-        case 32: return launch_bp<32, GATHER>(L, a, s);
-        default: return launch_bp<64, GATHER>(L, a, s);
+        case 1: return launch_bp<1, GATHER>(L, a, q, s);
+        case 2: return launch_bp<2, GATHER>(L, a, q, s);
+        case 4: return launch_bp<4, GATHER>(L, a, q, s);
+        case 8: return launch_bp<8, GATHER>(L, a, q, s);
+        case 16: return launch_bp<16, GATHER>(L, a, q, s);
+        case 32: return launch_bp<32, GATHER>(L, a, q, s);
+        default: return launch_bp<64, GATHER>(L, a, q, s);
     }
 }
 
 template <bool GATHER>
-static int run_spmm(Layer* L, SpmmArgs a, int64_t b, cudaStream_t s) {
+static int run_spmm(Layer* L, SpmmArgs a, const Q8In* q, int64_t b, cudaStream_t s) {
     const float* X0 = a.X;
     float* Y0 = a.Y;
     for (int64_t t0 = 0; t0 < b; t0 += kMaxBatchTile) {
         const int64_t bt = std::min<int64_t>(kMaxBatchTile, b - t0);
         a.b = (int)bt;
-        a.X = X0 + t0 * a.n_src;
+        Q8In qt{};
+        if (q) qt = q->from_row(t0);
+        else a.X = X0 + t0 * a.n_src;
         a.Y = Y0 + t0 * a.n_seg;
         if (a.nnz == 0) {
             k_fill_bias<<<L->num_sms * 4, 256, 0, s>>>(a.Y, bt, a.n_seg, a.bias);
             if (cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
             continue;
         }
-        int st = launch_tile<GATHER>(L, a, batch_tile(bt), s);
+        int st = launch_tile<GATHER>(L, a, batch_tile(bt), q ? &qt : nullptr, s);
         if (st != SNK_OK) return st;
     }
     return SNK_OK;
@@ -864,23 +874,25 @@ static SpmmArgs layer_args(Layer* L, bool columns) {
     return a;
 }
 
-int launch_forward(Layer* L, const float* X, int64_t b, const float* bias, float* Y,
+int launch_forward(Layer* L, const float* X, const Q8In* q, int64_t b, const float* bias, float* Y,
                    cudaStream_t s) {
-    if (tc_eligible(L, b)) return run_tc(L, false, X, b, bias, Y, s);
+    if (tc_eligible(L, b))
+        return q ? run_tc(L, false, SrcQ8{*q}, b, bias, Y, s)
+                 : run_tc(L, false, SrcF32{X, L->in_f}, b, bias, Y, s);
     SpmmArgs a = layer_args(L, false);
     a.X = X;
     a.bias = bias;
     a.Y = Y;
-    return run_spmm<false>(L, a, b, s);
+    return run_spmm<false>(L, a, q, b, s);
 }
 
 int launch_backward_input(Layer* L, const float* dY, int64_t b, float* dX, cudaStream_t s) {
-    if (tc_eligible(L, b)) return run_tc(L, true, dY, b, nullptr, dX, s);
+    if (tc_eligible(L, b)) return run_tc(L, true, SrcF32{dY, L->out_f}, b, nullptr, dX, s);
     SpmmArgs a = layer_args(L, true);
     a.X = dY;
     a.bias = nullptr;
     a.Y = dX;
-    return run_spmm<true>(L, a, b, s);
+    return run_spmm<true>(L, a, nullptr, b, s);
 }
 
 }  // namespace snk

@@ -44,7 +44,7 @@
 
 #include <algorithm>
 
-#include "snk_internal.cuh"
+#include "snk_q8.cuh"
 
 namespace snk {
 
@@ -605,6 +605,17 @@ __global__ void k_tc_split_sum(const float* __restrict__ part, int full, int spl
     }
 }
 
+// Columns k .. k + 3 of row r (k a multiple of 4, rows_of_4()).
+__device__ __forceinline__ float4 load4(const SrcF32& D, int64_t r, int64_t k) {
+    return __ldg(reinterpret_cast<const float4*>(D.p + r * D.cols + k));
+}
+__device__ __forceinline__ float4 load4(const SrcQ8& D, int64_t r, int64_t k) {
+    float v[4];
+    q_values4(__ldg(reinterpret_cast<const uint32_t*>(D.q.codes + r * D.q.cols + k)), D.q.format, v);
+    const float s = __ldg(D.q.scales + r * D.q.n_groups + (k >> D.q.gshift));
+    return make_float4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+}
+
 // Dense operand, once per call: per row the scale exponent of its largest
 // finite magnitude, and the scaled values split into fp16 hi / lo at row
 // stride ks (one block per row; non-finite values are split as zeros).  The
@@ -613,14 +624,13 @@ __global__ void k_tc_split_sum(const float* __restrict__ part, int full, int spl
 // (tc_needs_exact); a row that fails is listed in rows[] for the exact
 // recomputation.  The row's sum of finite magnitudes and its largest one go
 // into the running maxima that the segments' own check uses.
-template <bool VEC>
-__global__ void k_tc_split(const float* __restrict__ D, int64_t len, int64_t ks, int32_t* __restrict__ e_out,
+template <bool VEC, class Src>
+__global__ void k_tc_split(const Src D, int64_t len, int64_t ks, int32_t* __restrict__ e_out,
                            __half* __restrict__ dh, __half* __restrict__ dl, int32_t* __restrict__ rows,
                            uint32_t* __restrict__ fix) {
     __shared__ float red[3][32];
     __shared__ int red_n[32];
     const int64_t r = blockIdx.x;
-    const float* p = D + r * len;
     const int w = threadIdx.x >> 5, nw = blockDim.x >> 5, lane = threadIdx.x & 31;
     float m = 0.f, sum = 0.f, nf = 0.f;
     auto take = [&](float x) {
@@ -634,14 +644,14 @@ __global__ void k_tc_split(const float* __restrict__ D, int64_t len, int64_t ks,
     };
     if (VEC) {
         for (int64_t k = 4 * threadIdx.x; k < len; k += 4 * blockDim.x) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p + k));
+            const float4 v = load4(D, r, k);
             take(v.x);
             take(v.y);
             take(v.z);
             take(v.w);
         }
     } else {
-        for (int64_t k = threadIdx.x; k < len; k += blockDim.x) take(p[k]);
+        for (int64_t k = threadIdx.x; k < len; k += blockDim.x) take(D.at(r, k));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -676,7 +686,7 @@ __global__ void k_tc_split(const float* __restrict__ D, int64_t len, int64_t ks,
     __half* ol = dl + r * ks;
     if (VEC) {
         for (int64_t k = 4 * threadIdx.x; k < len; k += 4 * blockDim.x) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p + k));
+            const float4 v = load4(D, r, k);
             __half h0, h1, h2, h3, l0, l1, l2, l3;
             split16(scaled(v.x), h0, l0);
             split16(scaled(v.y), h1, l1);
@@ -693,7 +703,7 @@ __global__ void k_tc_split(const float* __restrict__ D, int64_t len, int64_t ks,
     } else {
         for (int64_t k = threadIdx.x; k < len; k += blockDim.x) {
             __half h, l;
-            split16(scaled(p[k]), h, l);
+            split16(scaled(D.at(r, k)), h, l);
             oh[k] = h;
             ol[k] = l;
         }
@@ -975,8 +985,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
 // or added when accumulate), summed in runs of 32 rows and then pairwise so
 // no fp32 chain exceeds ~45 terms; an inf or NaN propagates into that sum as
 // it does in the definition.
-template <bool SUM>
-__global__ void __launch_bounds__(256) k_tc_colstats(const float* __restrict__ D, int64_t rows, int64_t n,
+template <bool SUM, class Src>
+__global__ void __launch_bounds__(256) k_tc_colstats(const Src D, int64_t rows, int64_t n,
                                                      int32_t* __restrict__ e_out, int32_t* __restrict__ code,
                                                      uint32_t* __restrict__ l1max, float* __restrict__ sum,
                                                      int accumulate) {
@@ -989,7 +999,7 @@ __global__ void __launch_bounds__(256) k_tc_colstats(const float* __restrict__ D
             float part = 0.f;
             const int64_t r1 = min(rows, g * 32 + 32);
             for (int64_t r = g * 32; r < r1; ++r) {
-                const float x = D[r * n + col];
+                const float x = D.at(r, col);
                 const float ax = fabsf(x);
                 if (isfinite(ax)) {
                     m = fmaxf(m, ax);
@@ -1053,7 +1063,8 @@ __global__ void k_tc_dw_decide(const int32_t* __restrict__ e_row, const int32_t*
 // scaled fp16 pieces (row stride bs) the weight-gradient product loads
 // (non-finite values are split as zeros); each column's count of nonzero
 // values below 2^-3 after scaling is added into its code (2 per value).
-__global__ void k_tc_tsplit(const float* __restrict__ D, int64_t rows, int64_t n, const int32_t* __restrict__ e,
+template <class Src>
+__global__ void k_tc_tsplit(const Src D, int64_t rows, int64_t n, const int32_t* __restrict__ e,
                             int64_t bs, __half* __restrict__ oh, __half* __restrict__ ol,
                             int32_t* __restrict__ code) {
     __shared__ float tile[32][33];
@@ -1062,7 +1073,7 @@ __global__ void k_tc_tsplit(const float* __restrict__ D, int64_t rows, int64_t n
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t r = r0 + ty + 8 * i, c = c0 + tx;
-        tile[ty + 8 * i][tx] = (r < rows && c < n) ? D[r * n + c] : 0.f;
+        tile[ty + 8 * i][tx] = (r < rows && c < n) ? D.at(r, c) : 0.f;
     }
     __syncthreads();
 #pragma unroll
@@ -1497,8 +1508,8 @@ int ensure_tc(Layer* L) {
 
 }  // namespace
 
-int run_tc(Layer* L, bool columns, const float* D, int64_t b, const float* bias, float* Y,
-           cudaStream_t s) {
+template <class Src>
+int run_tc(Layer* L, bool columns, const Src& D, int64_t b, const float* bias, float* Y, cudaStream_t s) {
     int st0 = ensure_tc(L);
     if (st0 != SNK_OK) return st0;
     TcState* T = L->tc;
@@ -1520,20 +1531,20 @@ int run_tc(Layer* L, bool columns, const float* D, int64_t b, const float* bias,
     k_tc_seg_cand<<<grid_for(n_seg, TH, L->num_sms), TH, 0, s>>>(T->seg_code, n_seg, T->cand, T->fix);
     if (cudaFuncSetAttribute(k_tc_spmm, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem) != cudaSuccess)
         return SNK_ERR_CUDA;
-    const bool vec = (k_len % 4) == 0 && ((uintptr_t)D & 15) == 0;
+    const bool vec = D.rows_of_4();
     // the entries of the segments, for the exact recomputation of flagged outputs
     TcSide side{columns ? L->col_ptr : L->row_ptr, columns ? L->rows_c : L->c, columns ? L->perm : nullptr,
                 L->v};
     for (int64_t c0 = 0; c0 < b; c0 += kTcChunk) {
         const int bc = (int)std::min<int64_t>(kTcChunk, b - c0);
-        const float* Dc = D + c0 * k_len;
+        const Src Dc = D.from_row(c0);
         if (c0 > 0 && cudaMemsetAsync(T->fix + kFixRows, 0, sizeof(uint32_t), s) != cudaSuccess)
             return SNK_ERR_CUDA;
         if (vec)
-            k_tc_split<true><<<bc, TH, 0, s>>>(Dc, k_len, T->k_stride, T->row_exp, T->dh, T->dl, T->frows,
+            k_tc_split<true, Src><<<bc, TH, 0, s>>>(Dc, k_len, T->k_stride, T->row_exp, T->dh, T->dl, T->frows,
                                                T->fix);
         else
-            k_tc_split<false><<<bc, TH, 0, s>>>(Dc, k_len, T->k_stride, T->row_exp, T->dh, T->dl, T->frows,
+            k_tc_split<false, Src><<<bc, TH, 0, s>>>(Dc, k_len, T->k_stride, T->row_exp, T->dh, T->dl, T->frows,
                                                 T->fix);
         CUtensorMap mh, ml;
         if (!encode_map(&mh, T->dh, k_len, bc, T->k_stride) || !encode_map(&ml, T->dl, k_len, bc, T->k_stride))
@@ -1571,17 +1582,17 @@ int run_tc(Layer* L, bool columns, const float* D, int64_t b, const float* bias,
                 T->part, a.full, a.split, a.n_mt, a.n_nt, bc, n_seg, bias, Y + c0 * n_seg);
         // dense rows of this chunk that the split cannot carry: every output
         // of theirs again, per stored entry
-        int st = launch_exact_rows(side, n_seg, Dc, k_len, bias, Y + c0 * n_seg, T->frows,
+        int st = launch_exact_rows(side, n_seg, Dc, bias, Y + c0 * n_seg, T->frows,
                                    T->fix + kFixRows, L->num_sms, s);
         if (st != SNK_OK) return st;
     }
     // segments of W that the split cannot carry, for every dense row
-    return launch_exact_segs(side, n_seg, D, k_len, b, bias, Y, T->cand, T->fix + kFixCand, T->seg_exp,
+    return launch_exact_segs(side, n_seg, D, b, bias, Y, T->cand, T->fix + kFixCand, T->seg_exp,
                              T->seg_code, T->fix + kFixRowL1, L->num_sms, s);
 }
 
-int run_tc_sddmm(Layer* L, const float* X, const float* dY, int64_t b, float* dW, float* db,
-                 cudaStream_t s) {
+template <class Src>
+int run_tc_sddmm(Layer* L, const Src& X, const float* dY, int64_t b, float* dW, float* db, cudaStream_t s) {
     int st = ensure_tc(L);
     if (st != SNK_OK) return st;
     TcState* T = L->tc;
@@ -1603,18 +1614,18 @@ int run_tc_sddmm(Layer* L, const float* X, const float* dY, int64_t b, float* dW
     for (int64_t c0 = 0; c0 < b; c0 += chunk) {
         const int64_t bc = std::min<int64_t>(chunk, b - c0);
         const int64_t bs = ceil_div(bc, 8) * 8;
-        const float* dYc = dY + c0 * out_f;
-        const float* Xc = X + c0 * in_f;
+        const SrcF32 dYc{dY + c0 * out_f, out_f};
+        const Src Xc = X.from_row(c0);
         const int acc = c0 > 0;
         if (c0 > 0 && cudaMemsetAsync(T->fix + kFixDyL1, 0, 4 * sizeof(uint32_t), s) != cudaSuccess)
             return SNK_ERR_CUDA;
         if (db)
-            k_tc_colstats<true><<<(unsigned)ceil_div(out_f, 32), 256, 0, s>>>(
+            k_tc_colstats<true, SrcF32><<<(unsigned)ceil_div(out_f, 32), 256, 0, s>>>(
                 dYc, bc, out_f, T->seg_exp, T->seg_code, T->fix + kFixDyL1, db, acc);
         else
-            k_tc_colstats<false><<<(unsigned)ceil_div(out_f, 32), 256, 0, s>>>(
+            k_tc_colstats<false, SrcF32><<<(unsigned)ceil_div(out_f, 32), 256, 0, s>>>(
                 dYc, bc, out_f, T->seg_exp, T->seg_code, T->fix + kFixDyL1, nullptr, 0);
-        k_tc_colstats<false><<<(unsigned)ceil_div(in_f, 32), 256, 0, s>>>(Xc, bc, in_f, T->col_exp, T->col_code,
+        k_tc_colstats<false, Src><<<(unsigned)ceil_div(in_f, 32), 256, 0, s>>>(Xc, bc, in_f, T->col_exp, T->col_code,
                                                                           T->fix + kFixXL1, nullptr, 0);
         __half* ah = T->dh;
         __half* al = T->dl;
@@ -1654,5 +1665,10 @@ int run_tc_sddmm(Layer* L, const float* X, const float* dY, int64_t b, float* dW
     // rows and columns of W flagged by any chunk: their entries again, over the whole batch
     return launch_exact_dw(L, X, dY, b, dW, T->dw_list, T->fix + kFixDwList, s);
 }
+
+template int run_tc<SrcF32>(Layer*, bool, const SrcF32&, int64_t, const float*, float*, cudaStream_t);
+template int run_tc<SrcQ8>(Layer*, bool, const SrcQ8&, int64_t, const float*, float*, cudaStream_t);
+template int run_tc_sddmm<SrcF32>(Layer*, const SrcF32&, const float*, int64_t, float*, float*, cudaStream_t);
+template int run_tc_sddmm<SrcQ8>(Layer*, const SrcQ8&, const float*, int64_t, float*, float*, cudaStream_t);
 
 }  // namespace snk

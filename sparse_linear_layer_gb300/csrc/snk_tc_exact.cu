@@ -20,20 +20,21 @@
 // kernels holds.  An output reached from both a flagged row and a flagged
 // segment is computed twice by the same routine, so both writes carry the
 // same bits.
-#include "snk_internal.cuh"
+#include "snk_q8.cuh"
 
 namespace snk {
 namespace {
 
 // Warp-wide sum of val(j) * d[idx[j]] over the entries [j0, j1) of one
-// segment: lane l takes entries j0 + l, j0 + l + 32, ...; the 32 partial sums
+// segment and row `row` of the operand D: lane l takes entries j0 + l, j0 + l + 32, ...; the 32 partial sums
 // are added by a shuffle tree (every lane gets the result).
-__device__ __forceinline__ float seg_dot(const TcSide& sd, int64_t j0, int64_t j1,
-                                         const float* __restrict__ d, int lane) {
+template <class Src>
+__device__ __forceinline__ float seg_dot(const TcSide& sd, int64_t j0, int64_t j1, const Src& D,
+                                         int64_t row, int lane) {
     float acc = 0.f;
     for (int64_t j = j0 + lane; j < j1; j += 32) {
         const float w = sd.perm ? __ldg(sd.val + __ldg(sd.perm + j)) : __ldg(sd.val + j);
-        acc = fmaf(w, __ldg(d + __ldg(sd.idx + j)), acc);
+        acc = fmaf(w, D.at(row, __ldg(sd.idx + j)), acc);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
@@ -42,9 +43,9 @@ __device__ __forceinline__ float seg_dot(const TcSide& sd, int64_t j0, int64_t j
 
 // Flagged dense rows: Y[rows[i], o] for every segment o, one warp per
 // (row, segment) item, consecutive warps on consecutive segments of a row.
+template <class Src>
 __global__ void __launch_bounds__(256) k_exact_rows(const TcSide sd, int64_t n_seg,
-                                                    const float* __restrict__ D, int64_t K,
-                                                    const float* __restrict__ bias,
+                                                    const Src D, const float* __restrict__ bias,
                                                     float* __restrict__ Y,
                                                     const int32_t* __restrict__ rows,
                                                     const uint32_t* __restrict__ n_rows) {
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(256) k_exact_rows(const TcSide sd, int64_t n_s
          it += warps) {
         const int64_t beta = rows[it / n_seg];
         const int64_t o = it % n_seg;
-        const float y = seg_dot(sd, sd.ptr[o], sd.ptr[o + 1], D + beta * K, lane);
+        const float y = seg_dot(sd, sd.ptr[o], sd.ptr[o + 1], D, beta, lane);
         if (lane == 0) Y[beta * n_seg + o] = y + (bias ? bias[o] : 0.f);
     }
 }
@@ -64,9 +65,9 @@ __global__ void __launch_bounds__(256) k_exact_rows(const TcSide sd, int64_t n_s
 // fp16 floor): each block takes candidates in turn, confirms the flag against
 // the dense rows' largest L1 norm and magnitude, and its warps recompute the
 // segment's output for every dense row.
+template <class Src>
 __global__ void __launch_bounds__(256) k_exact_segs(const TcSide sd, int64_t n_seg,
-                                                    const float* __restrict__ D, int64_t K,
-                                                    int64_t b, const float* __restrict__ bias,
+                                                    const Src D, int64_t b, const float* __restrict__ bias,
                                                     float* __restrict__ Y,
                                                     const int32_t* __restrict__ cand,
                                                     const uint32_t* __restrict__ n_cand,
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(256) k_exact_segs(const TcSide sd, int64_t n_s
         const int64_t j0 = sd.ptr[o], j1 = sd.ptr[o + 1];
         const float bo = bias ? bias[o] : 0.f;
         for (int64_t beta = warp; beta < b; beta += nw) {
-            const float y = seg_dot(sd, j0, j1, D + beta * K, lane);
+            const float y = seg_dot(sd, j0, j1, D, beta, lane);
             if (lane == 0) Y[beta * n_seg + o] = y + bo;
         }
     }
@@ -91,14 +92,14 @@ __global__ void __launch_bounds__(256) k_exact_segs(const TcSide sd, int64_t n_s
 // dW_k = sum_beta dY[beta, r_k] X[beta, c_k] over the whole batch, one warp
 // per entry, lane l taking beta = l, l + 32, ...; for every entry of the
 // listed rows of W (list values below out) and columns (out + column).
+template <class Src>
 __global__ void __launch_bounds__(256) k_exact_dw(const int32_t* __restrict__ row_ptr,
                                                   const int32_t* __restrict__ cols,
                                                   const int32_t* __restrict__ col_ptr,
                                                   const int32_t* __restrict__ rows_c,
                                                   const int32_t* __restrict__ perm,
-                                                  const float* __restrict__ X,
-                                                  const float* __restrict__ dY, int64_t b,
-                                                  int64_t out_f, int64_t in_f,
+                                                  const Src X, const float* __restrict__ dY,
+                                                  int64_t b, int64_t out_f,
                                                   float* __restrict__ dW,
                                                   const int32_t* __restrict__ list,
                                                   const uint32_t* __restrict__ n_list) {
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(256) k_exact_dw(const int32_t* __restrict__ ro
             const int64_t c = is_row ? cols[j] : item - out_f;
             float acc = 0.f;
             for (int64_t beta = lane; beta < b; beta += 32)
-                acc = fmaf(__ldg(dY + beta * out_f + r), __ldg(X + beta * in_f + c), acc);
+                acc = fmaf(__ldg(dY + beta * out_f + r), X.at(beta, c), acc);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
             if (lane == 0) dW[k] = acc;
@@ -125,27 +126,41 @@ __global__ void __launch_bounds__(256) k_exact_dw(const int32_t* __restrict__ ro
 
 }  // namespace
 
-int launch_exact_rows(const TcSide& sd, int64_t n_seg, const float* D, int64_t K,
-                      const float* bias, float* Y, const int32_t* rows, const uint32_t* n_rows,
+template <class Src>
+int launch_exact_rows(const TcSide& sd, int64_t n_seg, const Src& D, const float* bias, float* Y, const int32_t* rows, const uint32_t* n_rows,
                       int num_sms, cudaStream_t s) {
-    k_exact_rows<<<num_sms * 4, 256, 0, s>>>(sd, n_seg, D, K, bias, Y, rows, n_rows);
+    k_exact_rows<<<num_sms * 4, 256, 0, s>>>(sd, n_seg, D, bias, Y, rows, n_rows);
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
 
-int launch_exact_segs(const TcSide& sd, int64_t n_seg, const float* D, int64_t K, int64_t b,
+template <class Src>
+int launch_exact_segs(const TcSide& sd, int64_t n_seg, const Src& D, int64_t b,
                       const float* bias, float* Y, const int32_t* cand, const uint32_t* n_cand,
                       const int32_t* seg_exp, const int32_t* seg_code, const uint32_t* other,
                       int num_sms, cudaStream_t s) {
-    k_exact_segs<<<num_sms * 2, 256, 0, s>>>(sd, n_seg, D, K, b, bias, Y, cand, n_cand, seg_exp,
+    k_exact_segs<<<num_sms * 2, 256, 0, s>>>(sd, n_seg, D, b, bias, Y, cand, n_cand, seg_exp,
                                              seg_code, other);
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
 
-int launch_exact_dw(const Layer* L, const float* X, const float* dY, int64_t b, float* dW,
+template <class Src>
+int launch_exact_dw(const Layer* L, const Src& X, const float* dY, int64_t b, float* dW,
                     const int32_t* list, const uint32_t* n_list, cudaStream_t s) {
     k_exact_dw<<<L->num_sms * 2, 256, 0, s>>>(L->row_ptr, L->c, L->col_ptr, L->rows_c, L->perm,
-                                              X, dY, b, L->out_f, L->in_f, dW, list, n_list);
+                                              X, dY, b, L->out_f, dW, list, n_list);
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
+
+#define SNK_EXACT(Src)                                                                                         \
+    template int launch_exact_rows<Src>(const TcSide&, int64_t, const Src&, const float*, float*,              \
+                                        const int32_t*, const uint32_t*, int, cudaStream_t);                   \
+    template int launch_exact_segs<Src>(const TcSide&, int64_t, const Src&, int64_t, const float*, float*,     \
+                                        const int32_t*, const uint32_t*, const int32_t*, const int32_t*,       \
+                                        const uint32_t*, int, cudaStream_t);                                   \
+    template int launch_exact_dw<Src>(const Layer*, const Src&, const float*, int64_t, float*, const int32_t*, \
+                                      const uint32_t*, cudaStream_t);
+SNK_EXACT(SrcF32)
+SNK_EXACT(SrcQ8)
+#undef SNK_EXACT
 
 }  // namespace snk
