@@ -24,6 +24,7 @@ SNK_Q8_INT8, SNK_Q8_E4M3 = 0, 1
 
 _lock = threading.Lock()
 _lib = None
+_raw_stream = None
 
 
 class SnkError(RuntimeError):
@@ -35,6 +36,8 @@ class SnkError(RuntimeError):
 def lib():
     """Load libsnk.so (built by ``sparse_linear_layer_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -113,10 +116,21 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return current_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def current_stream(device: int) -> int:
+    """The handle of torch's current stream on the device."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        # without building a Stream object, where torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
 
 
 def snk_status_string(status: int) -> str:
@@ -335,7 +349,8 @@ class SparseLinear:
     def forward_q8(self, X, bias=None, out=None, stream=None):
         """forward() with X an 8-bit matrix (q8.Q8Tensor, [batch, in])."""
         import torch
-        X.require(self.in_features)
+        if X.cols != self.in_features:
+            raise ValueError(f"X has {self.in_features} columns: got {tuple(X.shape)}")
         Y = out if out is not None else torch.empty((X.rows, self.out_features),
                                                     dtype=torch.float32, device=X.codes.device)
         snk_forward_q8(self.handle, X.codes, X.scales, X.format_id, X.group, X.rows, bias, Y, stream)
@@ -344,7 +359,8 @@ class SparseLinear:
     def backward_weight_q8(self, X, dY, with_bias: bool = False, out=None, stream=None):
         """backward_weight() with X an 8-bit matrix (q8.Q8Tensor, [batch, in])."""
         import torch
-        X.require(self.in_features)
+        if X.cols != self.in_features:
+            raise ValueError(f"X has {self.in_features} columns: got {tuple(X.shape)}")
         if dY.dtype != torch.float32 or dY.numel() != X.rows * self.out_features:
             raise ValueError(f"dY is float32 [{X.rows}, {self.out_features}]: got {dY.dtype} {tuple(dY.shape)}")
         dW = out if out is not None else torch.empty_like(self.values)

@@ -273,7 +273,7 @@ void mark_tc_views(Layer* L);
 void free_tc(Layer* L);
 
 // ---- small helpers -------------------------------------------------------
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int batch_tile(int64_t b) {
     int bp = 1;
     while (bp < b) bp <<= 1;

@@ -14,7 +14,7 @@
 // load to its last store; the only exchanges are the row's sum of squares (or
 // the gradient's dot product) and, for one scale per row, its largest
 // magnitude.  All sums are fp32: a lane adds at most 8 K squares, lanes are
-// added by a tree, warps in order.  Rows of more than 32768 columns are read
+// added by a tree, warps in order.  Rows of more than 16384 columns are read
 // again for each step (k_norm_long, k_norm_grad_long).
 //
 // The gain's gradient needs a sum over the rows.  A block walks rows
@@ -33,111 +33,192 @@ struct NormArgs {
     const void* residual;   // null: r = x, and total is not written
     const float* gain;
     int64_t rows, cols;
+    float inv_cols;         // 1 / cols
     float eps;
     void* total;
     float* rstd;
     Q8Out out;
 };
 
-template <typename T, bool VEC, int K>
-__global__ void __launch_bounds__(1024) k_norm(const NormArgs a, int W, int slots) {
-    __shared__ float red[kMaxSlots * 32];
-    __shared__ uint32_t redm[kMaxSlots * 32];
-    const RowSlot rs(W);
-    const int64_t r = (int64_t)blockIdx.x * slots + rs.slot;
-    if (r >= a.rows) return;
-    const int64_t off = r * a.cols;
-    float v[K][8];
-    float ss = 0.f;
+// 1 / sqrt(x): the approximate one and a Newton step, within an ulp.
+__device__ __forceinline__ float inv_sqrt(float x) {
+    float y;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    const float h = 0.5f * y;
+    const float e = fmaf(-x * y, h, 0.5f);
+    return isfinite(e) ? fmaf(y, e, y) : y;
+}
+
+// The sum of a lane's 8 values.
+__device__ __forceinline__ float sum8(const F8& v) {
+    const float2 h = __fadd2_rn(__fadd2_rn(v.p[0], v.p[1]), __fadd2_rn(v.p[2], v.p[3]));
+    return h.x + h.y;
+}
+
+// From the row in v (r = x + residual, rounded): its norm's codes and scales.
+// gain, codes: at the lane's first element of the row; scales: the first scale of
+// the warp's first tile; left: the columns from that tile on.
+template <bool VEC, int K, bool ONE>
+__device__ __forceinline__ void norm_row(const NormArgs& a, const RowSlot<ONE>& rs, F8 (&v)[K], const float* gain,
+                                         uint8_t* codes, float* scales, float* rstd_out, int left, float* red,
+                                         float* redm) {
+    F8 sq;
+    sq.clear();
+#pragma unroll
+    for (int k = 0; k < K; ++k) sq.fma(v[k], v[k]);
+    const float ss = rs.sum(sum8(sq), red);
+    const float rstd = inv_sqrt(fmaf(ss, a.inv_cols, a.eps));
+    if (rs.w == 0 && rs.lane == 0) *rstd_out = rstd;
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        F8 g;
+        load_tile<float, VEC>(gain + k * kQTile, left - k * kQTile, rs.lane, g);
+        v[k].mul(rstd);
+        v[k].mul(g);
+        if (a.out.gshift < 31)
+            pack_tile_groups<VEC>(a.out.format, a.out.gshift, codes + k * kQTile, scales + ((k * kQTile) >> a.out.gshift),
+                                  left - k * kQTile, rs.lane, v[k]);
+        else
+            m = amax8(v[k], m);
+    }
+    if (a.out.gshift < 31) return;
+    const QScale s = q_scale(rs.max_of(m, redm), a.out.format);
+    if (rs.w == 0 && rs.lane == 0) *scales = s.scale;
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        load_tile<T, VEC>((const T*)a.x + off, (int64_t)(k * W + rs.w) * kQTile, a.cols, rs.lane, v[k]);
+        pack_tile_row<VEC>(a.out.format, codes + k * kQTile, left - k * kQTile, rs.lane, v[k], s.inv);
+}
+
+// One row per slot, straight from memory: rows that are not aligned, calls of
+// too few rows to keep any in flight, and rows over many warps.
+template <typename T, bool VEC, int K, bool ONE>
+__global__ void __launch_bounds__(ONE ? 32 * kRowsPerBlock : 1024) k_norm(const NormArgs a) {
+    __shared__ float red[32], redm[32];
+    const RowSlot<ONE> rs;
+    const int64_t r = rs.first_row();
+    if (r >= a.rows) return;
+    const int c0 = rs.w * K * kQTile, left = (int)a.cols - c0, c = c0 + lane_col<VEC>(rs.lane);
+    const int64_t e = r * a.cols + c;
+    F8 v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        load_tile<T, VEC>((const T*)a.x + e + k * kQTile, left - k * kQTile, rs.lane, v[k]);
     if (a.residual) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t c0 = (int64_t)(k * W + rs.w) * kQTile;
-            float t[8];
-            load_tile<T, VEC>((const T*)a.residual + off, c0, a.cols, rs.lane, t);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = to_f32(from_f32<T>(v[k][j] + t[j]));
-            store_tile<T, VEC>((T*)a.total + off, c0, a.cols, rs.lane, v[k]);
+            F8 t;
+            load_tile<T, VEC>((const T*)a.residual + e + k * kQTile, left - k * kQTile, rs.lane, t);
+            v[k].add(t);
+            v[k].template round<T>();
+            store_tile<T, VEC>((T*)a.total + e + k * kQTile, left - k * kQTile, rs.lane, v[k]);
         }
     }
+    norm_row<VEC, K, ONE>(a, rs, v, a.gain + c, a.out.codes + e, a.out.scales + r * a.out.n_groups + (c0 >> a.out.gshift),
+                          a.rstd + r, left, red, redm);
+}
+
+// Many aligned rows: each slot walks rows, the next row's tiles in flight.
+template <typename T, int K, bool ONE>
+__global__ void __launch_bounds__(ONE ? 32 * kRowsPerBlock : 1024, ONE ? 3 : 1) k_norm_ring(const NormArgs a) {
+    extern __shared__ uint4 ring[];
+    // two turns use two halves: a warp may still be reading this row's sums
+    // when another is at the next row's
+    __shared__ float red[2][32], redm[2][32];
+    const RowSlot<ONE> rs;
+    const int units = (a.residual ? 2 : 1) * K * Ring<T>::kUnits;
+    const int c0 = rs.w * K * kQTile, left = (int)a.cols - c0, c = c0 + 8 * rs.lane;
+    const int64_t step = (int64_t)gridDim.x * rs.slots;
+    auto request = [&](int64_t r, int stage) {
+        if (r < a.rows) {
+            uint4* st = ring + stage * units * blockDim.x;
+            const int64_t e = r * a.cols + c;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+            for (int k = 0; k < K; ++k) {
+                Ring<T>::copy(st, k, (const T*)a.x + e + k * kQTile, left - k * kQTile, rs.lane);
+                if (a.residual)
+                    Ring<T>::copy(st, K + k, (const T*)a.residual + e + k * kQTile, left - k * kQTile, rs.lane);
+            }
+        }
+        ring_commit();
+    };
+    int64_t r = rs.first_row();
+    request(r, 0);
+    for (int turn = 0; r < a.rows; r += step, turn ^= 1) {
+        request(r + step, turn ^ 1);
+        ring_wait<1>();
+        const uint4* st = ring + turn * units * blockDim.x;
+        const int64_t e = r * a.cols + c;
+        F8 v[K];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[k][j], v[k][j], ss);
-    ss = rs.sum(ss, red);
-    const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
-    if (rs.w == 0 && rs.lane == 0) a.rstd[r] = rstd;
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int64_t c0 = (int64_t)(k * W + rs.w) * kQTile;
-        float g[8];
-        load_tile<float, VEC>(a.gain, c0, a.cols, rs.lane, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * rstd * g[j];
-        if (a.out.gshift < 31) pack_tile_groups<VEC>(a.out, r, c0, a.cols, rs.lane, v[k]);
-        else m = max(m, tile_amax(v[k]));
+        for (int k = 0; k < K; ++k) {
+            if (a.residual) {
+                Ring<T>::read_sum(st, k, K + k, v[k]);
+                store_tile<T, true>((T*)a.total + e + k * kQTile, left - k * kQTile, rs.lane, v[k]);
+            } else {
+                Ring<T>::read(st, k, v[k]);
+            }
+        }
+        norm_row<true, K, ONE>(a, rs, v, a.gain + c, a.out.codes + e,
+                               a.out.scales + r * a.out.n_groups + (c0 >> a.out.gshift), a.rstd + r, left, red[turn],
+                               redm[turn]);
     }
-    if (a.out.gshift < 31) return;
-    const QScale s = q_scale(rs.max_of(m, redm), q_top(a.out.format));
-    if (rs.w == 0 && rs.lane == 0) a.out.scales[r] = s.scale;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        pack_tile_row<VEC>(a.out, r, (int64_t)(k * W + rs.w) * kQTile, a.cols, rs.lane, v[k], s.inv);
 }
 
 // Rows of any length: a block of 32 warps, the row read once for each step.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a) {
-    __shared__ float red[32];
-    __shared__ uint32_t redm[32];
-    const RowSlot rs(32);
-    const int64_t r = blockIdx.x, off = r * a.cols;
+    __shared__ float red[32], redm[32];
+    const RowSlot<false> rs;
+    const int64_t r = blockIdx.x, row = r * a.cols;
+    const int lc = lane_col<VEC>(rs.lane);
     // the summed row is re-read by the thread that wrote it
-    const T* src = a.residual ? (const T*)a.total + off : (const T*)a.x + off;
+    const T* src = a.residual ? (const T*)a.total : (const T*)a.x;
     float ss = 0.f;
-    for (int64_t c0 = (int64_t)rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
-        float v[8];
-        load_tile<T, VEC>((const T*)a.x + off, c0, a.cols, rs.lane, v);
+    for (int64_t c0 = rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
+        const int left = (int)(a.cols - c0);
+        F8 v, sq;
+        load_tile<T, VEC>((const T*)a.x + row + c0 + lc, left, rs.lane, v);
         if (a.residual) {
-            float t[8];
-            load_tile<T, VEC>((const T*)a.residual + off, c0, a.cols, rs.lane, t);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_f32(from_f32<T>(v[j] + t[j]));
-            store_tile<T, VEC>((T*)a.total + off, c0, a.cols, rs.lane, v);
+            F8 u;
+            load_tile<T, VEC>((const T*)a.residual + row + c0 + lc, left, rs.lane, u);
+            v.add(u);
+            v.template round<T>();
+            store_tile<T, VEC>((T*)a.total + row + c0 + lc, left, rs.lane, v);
         }
-        float part = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) part = fmaf(v[j], v[j], part);
-        ss += part;
+        sq.clear();
+        sq.fma(v, v);
+        ss += sum8(sq);
     }
     ss = rs.sum(ss, red);
-    const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
+    const float rstd = inv_sqrt(fmaf(ss, a.inv_cols, a.eps));
     if (threadIdx.x == 0) a.rstd[r] = rstd;
-    auto normed = [&](int64_t c0, float (&v)[8]) {
-        float g[8];
-        load_tile<T, VEC>(src, c0, a.cols, rs.lane, v);
-        load_tile<float, VEC>(a.gain, c0, a.cols, rs.lane, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * g[j];
+    auto normed = [&](int64_t c0, int left, F8& v) {
+        F8 g;
+        load_tile<T, VEC>(src + row + c0 + lc, left, rs.lane, v);
+        load_tile<float, VEC>(a.gain + c0 + lc, left, rs.lane, g);
+        v.mul(rstd);
+        v.mul(g);
     };
-    uint32_t m = 0;
-    for (int64_t c0 = (int64_t)rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
-        float v[8];
-        normed(c0, v);
-        if (a.out.gshift < 31) pack_tile_groups<VEC>(a.out, r, c0, a.cols, rs.lane, v);
-        else m = max(m, tile_amax(v));
+    float m = 0.f;
+    for (int64_t c0 = rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
+        const int left = (int)(a.cols - c0);
+        F8 v;
+        normed(c0, left, v);
+        if (a.out.gshift < 31)
+            pack_tile_groups<VEC>(a.out.format, a.out.gshift, a.out.codes + row + c0 + lc,
+                                  a.out.scales + r * a.out.n_groups + (c0 >> a.out.gshift), left, rs.lane, v);
+        else
+            m = amax8(v, m);
     }
     if (a.out.gshift < 31) return;
-    const QScale s = q_scale(rs.max_of(m, redm), q_top(a.out.format));
+    const QScale s = q_scale(rs.max_of(m, redm), a.out.format);
     if (threadIdx.x == 0) a.out.scales[r] = s.scale;
-    for (int64_t c0 = (int64_t)rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
-        float v[8];
-        normed(c0, v);
-        pack_tile_row<VEC>(a.out, r, c0, a.cols, rs.lane, v, s.inv);
+    for (int64_t c0 = rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
+        const int left = (int)(a.cols - c0);
+        F8 v;
+        normed(c0, left, v);
+        pack_tile_row<VEC>(a.out.format, a.out.codes + row + c0 + lc, left, rs.lane, v, s.inv);
     }
 }
 
@@ -148,79 +229,125 @@ struct NormGradArgs {
     const float* gain;
     const void* dtotal;   // or null
     int64_t rows, cols;
+    float inv_cols;       // 1 / cols
     void* dx;
     float* part;          // [gridDim.x][cols], or null: no gain gradient
 };
 
-template <typename T, bool VEC, int K>
-__global__ void __launch_bounds__(K == 1 ? 1024 : 512) k_norm_grad(const NormGradArgs a, int W, int slots) {
-    extern __shared__ float cols_sm[];                    // [W * K * 256] when slots > 1
-    __shared__ float red[2][kMaxSlots * 32];
-    const RowSlot rs(W);
-    float acc[K][8];
+// A slot walks rows; with RING (aligned rows) the next row's tiles are in flight.
+template <typename T, bool VEC, int K, bool ONE, bool RING>
+__global__ void __launch_bounds__(ONE ? 32 * kRowsPerBlock : 1024)
+    k_norm_grad(const NormGradArgs a) {
+    // RING: two stages of the rows; then, for ONE, [K * 256] column sums
+    extern __shared__ uint4 ring[];
+    __shared__ float red[2][32];
+    const RowSlot<ONE> rs;
+    constexpr int U4 = Ring<float>::kUnits, UT = RING ? Ring<T>::kUnits : 0;
+    const int units = K * (U4 + (a.dtotal ? 2 : 1) * UT);
+    const int c0 = rs.w * K * kQTile, left = (int)a.cols - c0, c = c0 + lane_col<VEC>(rs.lane);
+    const int64_t step = (int64_t)gridDim.x * rs.slots;
+    auto request = [&](int64_t r, int stage) {
+        if constexpr (RING) {
+            if (r < a.rows) {
+                uint4* st = ring + stage * units * blockDim.x;
+                uint4* st_t = st + K * U4 * blockDim.x;
+                const int64_t e = r * a.cols + c;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[k][j] = 0.f;
-    int turn = 0;
-    for (int64_t r = (int64_t)blockIdx.x * slots + rs.slot; r < a.rows; r += (int64_t)gridDim.x * slots, turn ^= 1) {
-        const int64_t off = r * a.cols;
-        const float rstd = __ldg(a.rstd + r);
-        float g[K][8], n[K][8], add[K][8];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int64_t c0 = (int64_t)(k * W + rs.w) * kQTile;
-            load_tile<float, VEC>(a.dy + off, c0, a.cols, rs.lane, g[k]);
-            load_tile<T, VEC>((const T*)a.total + off, c0, a.cols, rs.lane, n[k]);
-            if (a.dtotal) load_tile<T, VEC>((const T*)a.dtotal + off, c0, a.cols, rs.lane, add[k]);
-        }
-        float dot = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float w[8];
-            load_tile<float, VEC>(a.gain, (int64_t)(k * W + rs.w) * kQTile, a.cols, rs.lane, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                n[k][j] *= rstd;
-                acc[k][j] = fmaf(g[k][j], n[k][j], acc[k][j]);
-                g[k][j] *= w[j];
-                dot = fmaf(g[k][j], n[k][j], dot);
+                for (int k = 0; k < K; ++k) {
+                    const int l = left - k * kQTile;
+                    Ring<float>::copy(st, k, a.dy + e + k * kQTile, l, rs.lane);
+                    Ring<T>::copy(st_t, k, (const T*)a.total + e + k * kQTile, l, rs.lane);
+                    if (a.dtotal) Ring<T>::copy(st_t, K + k, (const T*)a.dtotal + e + k * kQTile, l, rs.lane);
+                }
             }
+            ring_commit();
+        }
+    };
+    F8 acc[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) acc[k].clear();
+    int64_t r = rs.first_row();
+    request(r, 0);
+    float rstd_next = r < a.rows ? __ldg(a.rstd + r) : 0.f;
+    for (int turn = 0; r < a.rows; r += step, turn ^= 1) {
+        request(r + step, turn ^ 1);
+        const float rstd = rstd_next;
+        if (r + step < a.rows) rstd_next = __ldg(a.rstd + r + step);
+        const int64_t e = r * a.cols + c;
+        const uint4* st = nullptr;
+        const uint4* st_t = nullptr;
+        if constexpr (RING) {
+            ring_wait<1>();
+            st = ring + turn * units * blockDim.x;
+            st_t = st + K * U4 * blockDim.x;
+        }
+        F8 g[K], n[K], add[RING ? 1 : K];
+        if constexpr (!RING) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int l = left - k * kQTile;
+                load_tile<float, VEC>(a.dy + e + k * kQTile, l, rs.lane, g[k]);
+                load_tile<T, VEC>((const T*)a.total + e + k * kQTile, l, rs.lane, n[k]);
+                if (a.dtotal) load_tile<T, VEC>((const T*)a.dtotal + e + k * kQTile, l, rs.lane, add[k]);
+            }
+        }
+        F8 dots;
+        dots.clear();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if constexpr (RING) {
+                Ring<float>::read(st, k, g[k]);
+                Ring<T>::read(st_t, k, n[k]);
+            }
+            F8 w;
+            load_tile<float, VEC>(a.gain + c + k * kQTile, left - k * kQTile, rs.lane, w);
+            n[k].mul(rstd);
+            acc[k].fma(g[k], n[k]);
+            g[k].mul(w);
+            dots.fma(g[k], n[k]);
         }
         // two turns share no `red`, so a warp still reading this turn's sums
         // is past them before anyone writes there again
-        dot = __fdiv_rn(rs.sum(dot, red[turn]), (float)a.cols);
+        const float mean = rs.sum(sum8(dots), red[turn]) * a.inv_cols;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                g[k][j] = rstd * (g[k][j] - n[k][j] * dot);
-                if (a.dtotal) g[k][j] += add[k][j];
+            n[k].mul(-mean);
+            g[k].add(n[k]);
+            g[k].mul(rstd);
+            if (a.dtotal) {
+                if constexpr (RING) Ring<T>::read(st_t, K + k, add[0]);
+                g[k].add(add[RING ? 0 : k]);
             }
-            store_tile<T, VEC>((T*)a.dx + off, (int64_t)(k * W + rs.w) * kQTile, a.cols, rs.lane, g[k]);
+            store_tile<T, VEC>((T*)a.dx + e + k * kQTile, left - k * kQTile, rs.lane, g[k]);
         }
     }
     if (!a.part) return;
-    // the slots' sums in slot order
-    float* dst = a.part + (int64_t)blockIdx.x * a.cols;
-    for (int s = 0; s < slots; ++s) {
-        if (rs.slot == s) {
+    float* dst = a.part + blockIdx.x * a.cols + c;
+    if constexpr (!ONE) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int t = k * W + rs.w;
-                if (s > 0) {
+        for (int k = 0; k < K; ++k) store_tile<float, VEC>(dst + k * kQTile, left - k * kQTile, rs.lane, acc[k]);
+    } else {
+        // the warps' sums in warp order
+        float* cols_sm = reinterpret_cast<float*>(ring + (RING ? 2 * units * blockDim.x : 0)) + rs.lane;
+        for (int s = 0; s < rs.slots; ++s) {
+            if (rs.slot == s) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[k][j] += cols_sm[t * kQTile + j * 32 + rs.lane];
-                }
-                if (s + 1 < slots) {
+                for (int k = 0; k < K; ++k) {
+                    float* mine = cols_sm + k * kQTile;
+                    if (s > 0) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) cols_sm[t * kQTile + j * 32 + rs.lane] = acc[k][j];
-                } else {
-                    store_tile<float, VEC>(dst, (int64_t)t * kQTile, a.cols, rs.lane, acc[k]);
+                        for (int j = 0; j < 8; ++j) acc[k].set(j, acc[k].at(j) + mine[j * 32]);
+                    }
+                    if (s + 1 < rs.slots) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) mine[j * 32] = acc[k].at(j);
+                    } else {
+                        store_tile<float, VEC>(dst + k * kQTile, left - k * kQTile, rs.lane, acc[k]);
+                    }
                 }
             }
+            __syncthreads();
         }
-        if (slots > 1) __syncthreads();
     }
 }
 
@@ -228,53 +355,50 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) k_norm_grad(const NormGra
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) k_norm_grad_long(const NormGradArgs a) {
     __shared__ float red[2][32];
-    const RowSlot rs(32);
-    float* dst = a.part ? a.part + (int64_t)blockIdx.x * a.cols : nullptr;
+    const RowSlot<false> rs;
+    const int lc = lane_col<VEC>(rs.lane);
     int turn = 0;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
-        const int64_t off = r * a.cols;
         const float rstd = __ldg(a.rstd + r);
         const bool first = r == blockIdx.x;
-        auto load = [&](int64_t c0, float (&g)[8], float (&n)[8]) {
-            load_tile<float, VEC>(a.dy + off, c0, a.cols, rs.lane, g);
-            load_tile<T, VEC>((const T*)a.total + off, c0, a.cols, rs.lane, n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) n[j] *= rstd;
+        const int64_t row = r * a.cols;
+        auto load = [&](int64_t c0, int left, F8& g, F8& n, F8& w) {
+            load_tile<float, VEC>(a.dy + row + c0 + lc, left, rs.lane, g);
+            load_tile<T, VEC>((const T*)a.total + row + c0 + lc, left, rs.lane, n);
+            load_tile<float, VEC>(a.gain + c0 + lc, left, rs.lane, w);
+            n.mul(rstd);
         };
         float dot = 0.f;
-        for (int64_t c0 = (int64_t)rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
-            float g[8], n[8], w[8];
-            load(c0, g, n);
-            load_tile<float, VEC>(a.gain, c0, a.cols, rs.lane, w);
-            float part = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) part = fmaf(g[j] * w[j], n[j], part);
-            dot += part;
-            if (dst) {
-                float d[8];
-                if (first) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) d[j] = 0.f;
-                } else {
-                    load_tile<float, VEC>(dst, c0, a.cols, rs.lane, d);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = fmaf(g[j], n[j], d[j]);
-                store_tile<float, VEC>(dst, c0, a.cols, rs.lane, d);
+        for (int64_t c0 = rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
+            const int left = (int)(a.cols - c0);
+            F8 g, n, w, d;
+            load(c0, left, g, n, w);
+            if (a.part) {
+                float* dst = a.part + blockIdx.x * a.cols + c0 + lc;
+                d.clear();
+                if (!first) load_tile<float, VEC>(dst, left, rs.lane, d);
+                d.fma(g, n);
+                store_tile<float, VEC>(dst, left, rs.lane, d);
             }
+            d.clear();
+            g.mul(w);
+            d.fma(g, n);
+            dot += sum8(d);
         }
-        dot = __fdiv_rn(rs.sum(dot, red[turn]), (float)a.cols);
-        for (int64_t c0 = (int64_t)rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
-            float g[8], n[8], w[8], add[8];
-            load(c0, g, n);
-            load_tile<float, VEC>(a.gain, c0, a.cols, rs.lane, w);
-            if (a.dtotal) load_tile<T, VEC>((const T*)a.dtotal + off, c0, a.cols, rs.lane, add);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                g[j] = rstd * (g[j] * w[j] - n[j] * dot);
-                if (a.dtotal) g[j] += add[j];
+        const float mean = rs.sum(dot, red[turn]) * a.inv_cols;
+        for (int64_t c0 = rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
+            const int left = (int)(a.cols - c0);
+            F8 g, n, w;
+            load(c0, left, g, n, w);
+            g.mul(w);
+            n.mul(-mean);
+            g.add(n);
+            g.mul(rstd);
+            if (a.dtotal) {
+                load_tile<T, VEC>((const T*)a.dtotal + row + c0 + lc, left, rs.lane, w);
+                g.add(w);
             }
-            store_tile<T, VEC>((T*)a.dx + off, c0, a.cols, rs.lane, g);
+            store_tile<T, VEC>((T*)a.dx + row + c0 + lc, left, rs.lane, g);
         }
     }
 }
@@ -287,8 +411,10 @@ __global__ void __launch_bounds__(1024) k_dgain_sum(const float* __restrict__ pa
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + x;
     float t = 0.f;
-    if (c < cols)
+    if (c < cols) {
+#pragma unroll 8
         for (int i = y; i < n; i += 32) t += part[(int64_t)i * cols + c];
+    }
     sm[y][x] = t;
     __syncthreads();
     t = sm[x][y];
@@ -298,42 +424,112 @@ __global__ void __launch_bounds__(1024) k_dgain_sum(const float* __restrict__ pa
     if (x == 0 && cc < cols) dgain[cc] = t;
 }
 
+template <typename F>
+bool allow_smem(F fn, size_t bytes) {
+    return bytes <= 32 * 1024 ||   // the kernels have static arrays beside it
+           cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
+constexpr size_t kSmSmem = 227 * 1024;   // shared memory of an SM that blocks can take
+constexpr int64_t kSms = 152;
+
+// Blocks of the kernel that an SM holds at once.
+template <typename F>
+int64_t blocks_per_sm(F fn, int threads, size_t smem) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) cudaGetLastError();
+    return std::max(1, n);
+}
+
+template <typename T, bool VEC, int K, bool ONE>
+int launch_norm_k(const NormArgs& a, const RowShape& f, cudaStream_t s) {
+    const int threads = f.threads();
+    if constexpr (VEC) {
+        const size_t smem = (size_t)2 * (a.residual ? 2 : 1) * K * Ring<T>::kUnits * 16 * threads;
+        // Rows in flight pay for one warp's rows and for two tiles per warp (768
+        // bf16 columns: 33 us a training batch against 39; 10000: 33 against
+        // 54), not for one tile per warp (5000 fp32 columns: 48 against 41),
+        // given rows for more than one turn of every slot and room for two stages.
+        if ((ONE || K == 2) && smem <= kSmSmem - 8192 && a.rows >= 2 * kSms * f.slots()) {
+            auto fn = k_norm_ring<T, K, ONE>;
+            if (!allow_smem(fn, smem)) return SNK_ERR_CUDA;
+            const int64_t bps = blocks_per_sm(fn, threads, smem);
+            const int64_t turns = ceil_div(a.rows, kSms * bps * f.slots());
+            fn<<<(unsigned)ceil_div(a.rows, turns * f.slots()), threads, smem, s>>>(a);
+            return SNK_OK;
+        }
+    }
+    k_norm<T, VEC, K, ONE><<<(unsigned)ceil_div(a.rows, f.slots()), threads, 0, s>>>(a);
+    return SNK_OK;
+}
+
 template <typename T, bool VEC>
 int launch_norm(const NormArgs& a, cudaStream_t s) {
     const int64_t tpr = ceil_div(a.cols, kQTile);
-    if (tpr <= 128) {
-        const bool short_rows = tpr <= 2 || (a.rows <= 256 && tpr <= 32);
-        const int K = short_rows ? 1 : 4;
-        const int W = (int)ceil_div(tpr, K), slots = std::max(1, std::min(kMaxSlots, 8 / W));
-        const unsigned grid = (unsigned)ceil_div(a.rows, slots);
-        if (K == 1) k_norm<T, VEC, 1><<<grid, slots * W * 32, 0, s>>>(a, W, slots);
-        else k_norm<T, VEC, 4><<<grid, slots * W * 32, 0, s>>>(a, W, slots);
+    int st = SNK_OK;
+    if (tpr <= kRegisterTiles) {
+        // few rows: one tile per warp, for the shortest time of a row; unaligned
+        // ones too (their 8 accesses per tile want warps, not registers)
+        const RowShape f = row_shape(tpr, VEC && a.rows > 256 ? 3 : 1);
+        if (!f.one()) {
+            st = f.K == 1 ? launch_norm_k<T, VEC, 1, false>(a, f, s) : launch_norm_k<T, VEC, 2, false>(a, f, s);
+        } else if constexpr (VEC) {
+            st = f.K == 1   ? launch_norm_k<T, VEC, 1, true>(a, f, s)
+                 : f.K == 2 ? launch_norm_k<T, VEC, 2, true>(a, f, s)
+                            : launch_norm_k<T, VEC, 3, true>(a, f, s);
+        } else {
+            st = launch_norm_k<T, VEC, 1, true>(a, f, s);
+        }
     } else {
         k_norm_long<T, VEC><<<(unsigned)a.rows, 1024, 0, s>>>(a);
     }
-    return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
+    return st != SNK_OK || cudaGetLastError() == cudaSuccess ? st : SNK_ERR_CUDA;
 }
 
-// Blocks of the gradient kernel: a scratch row each.
-constexpr int kGradBlocks = 304;
+// Most blocks of the gradient kernel: a scratch row each.
+constexpr int64_t kGradBlocks = 8 * kSms;
+
+template <typename T, bool VEC, int K, bool ONE>
+int launch_norm_grad_k(const NormGradArgs& a, const RowShape& f, int64_t* grid, cudaStream_t s) {
+    const int threads = f.threads();
+    const size_t sums = ONE ? (size_t)K * kQTile * sizeof(float) : 0;
+    auto blocks = [&](int64_t bps) {   // blocks of equally many rows
+        const int64_t turns = ceil_div(a.rows, std::min<int64_t>(kGradBlocks / kSms, bps) * kSms * f.slots());
+        return ceil_div(a.rows, turns * f.slots());
+    };
+    if constexpr (VEC) {
+        const size_t smem = (size_t)2 * K * (2 + (a.dtotal ? 2 : 1) * Ring<T>::kUnits) * 16 * threads + sums;
+        if (smem <= kSmSmem - 8192 && a.rows >= 2 * kSms * f.slots()) {
+            auto fn = k_norm_grad<T, true, K, ONE, true>;
+            if (!allow_smem(fn, smem)) return SNK_ERR_CUDA;
+            *grid = blocks(blocks_per_sm(fn, threads, smem));
+            fn<<<(unsigned)*grid, threads, smem, s>>>(a);
+            return SNK_OK;
+        }
+    }
+    auto fn = k_norm_grad<T, VEC, K, ONE, false>;
+    *grid = blocks(blocks_per_sm(fn, threads, sums));
+    fn<<<(unsigned)*grid, threads, sums, s>>>(a);
+    return SNK_OK;
+}
 
 template <typename T, bool VEC>
 int launch_norm_grad(const NormGradArgs& a, float* dgain, cudaStream_t s) {
     const int64_t tpr = ceil_div(a.cols, kQTile);
-    int64_t grid;
-    if (tpr <= 64) {
-        const bool k1 = tpr <= 2 || a.rows <= 152;
-        const int K = k1 && tpr <= 32 ? 1 : 4;
-        const int W = (int)ceil_div(tpr, K), slots = std::max(1, std::min(kMaxSlots, 8 / W));
-        grid = std::min<int64_t>(kGradBlocks, ceil_div(a.rows, slots));
-        const size_t smem = slots > 1 ? (size_t)W * K * kQTile * sizeof(float) : 0;
-        if (K == 1) k_norm_grad<T, VEC, 1><<<(unsigned)grid, slots * W * 32, smem, s>>>(a, W, slots);
-        else k_norm_grad<T, VEC, 4><<<(unsigned)grid, slots * W * 32, smem, s>>>(a, W, slots);
+    int64_t grid = 0;
+    int st = SNK_OK;
+    if (tpr <= kRegisterTiles) {
+        // one tile per warp (768 bf16 columns: 50 us a training batch, against 57
+        // with the row's three in one warp, whose registers leave 16 warps per SM)
+        const RowShape f = row_shape(tpr, 1);
+        if (f.one()) st = launch_norm_grad_k<T, VEC, 1, true>(a, f, &grid, s);
+        else if (f.K == 1) st = launch_norm_grad_k<T, VEC, 1, false>(a, f, &grid, s);
+        else st = launch_norm_grad_k<T, VEC, 2, false>(a, f, &grid, s);
     } else {
-        grid = std::min<int64_t>(kGradBlocks, a.rows);
+        grid = std::min<int64_t>(2 * kSms, a.rows);
         k_norm_grad_long<T, VEC><<<(unsigned)grid, 1024, 0, s>>>(a);
     }
-    if (cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
+    if (st != SNK_OK || cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
     if (dgain) {
         k_dgain_sum<<<(unsigned)ceil_div(a.cols, 32), 1024, 0, s>>>(a.part, (int)grid, a.cols, dgain);
         if (cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
@@ -360,7 +556,7 @@ int snk_rmsnorm_q8(const void* x, const void* residual, int dtype, const float* 
         !q8_aligned(scales, 4) || !q8_aligned(rstd, 4))
         return SNK_ERR_ARG;
     if (rows > INT32_MAX || cols > INT32_MAX) return SNK_ERR_LIMIT;
-    const NormArgs a{x, residual, gain, rows, cols, eps, total, rstd,
+    const NormArgs a{x, residual, gain, rows, cols, 1.f / (float)cols, eps, total, rstd,
                      Q8Out{(uint8_t*)codes, scales, format, q8_gshift(group), q8_groups(cols, group)}};
     const uintptr_t al = dtype == SNK_F32 ? 32 : 16;
     const bool vec = cols % 8 == 0 && q8_aligned(x, al) && q8_aligned(residual, al) && q8_aligned(total, al) &&
@@ -395,7 +591,7 @@ int snk_rmsnorm_backward(const float* dy, const void* total, int dtype, const fl
         !q8_aligned(dtotal, e) || !q8_aligned(dx, e) || !q8_aligned(scratch, 32))
         return SNK_ERR_ARG;
     if (rows > INT32_MAX || cols > INT32_MAX) return SNK_ERR_LIMIT;
-    const NormGradArgs a{dy, total, rstd, gain, dtotal, rows, cols, dx, dgain ? (float*)scratch : nullptr};
+    const NormGradArgs a{dy, total, rstd, gain, dtotal, rows, cols, 1.f / (float)cols, dx, dgain ? (float*)scratch : nullptr};
     const uintptr_t al = dtype == SNK_F32 ? 32 : 16;
     const bool vec = cols % 8 == 0 && q8_aligned(dy, 32) && q8_aligned(total, al) && q8_aligned(dtotal, al) &&
                      q8_aligned(dx, al) && q8_aligned(gain, 32);

@@ -10,7 +10,7 @@
 // 32..256 columns never leaves its warp, and its largest magnitude is a few
 // shuffles.  A scale for the whole row needs the row's largest magnitude
 // before the first code: the row then stays in registers over W warps
-// (k_pack_row), up to 32768 columns; longer rows are read twice (k_pack_long).
+// (k_pack_row), up to 16384 columns; longer rows are read twice (k_pack_long).
 #include <algorithm>
 
 #include "snk_q8.cuh"
@@ -18,9 +18,50 @@
 namespace snk {
 namespace {
 
-__device__ __forceinline__ float gelu(float x) { return 0.5f * x * (1.f + erff(x * 0.70710678f)); }
-__device__ __forceinline__ float gelu_slope(float x) {
-    return 0.5f * (1.f + erff(x * 0.70710678f)) + x * 0.39894228f * expf(-0.5f * x * x);
+// Phi(-|x|) and exp(-x^2 / 2) of two values, from nax = -|x|.  Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26: erfc(z) = (a1 t + ... +
+// a5 t^5) exp(-z^2), t = 1 / (1 + p z), to 1.5e-7 for z >= 0; here z = |x| /
+// sqrt(2), the a_i are halved, and the exponential also serves the gradient.
+// With erff and expf the arithmetic, not the bytes, set GELU's time.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg_abs(float2 x) {
+    return make_float2(__uint_as_float(__float_as_uint(x.x) | 0x80000000u),
+                       __uint_as_float(__float_as_uint(x.y) | 0x80000000u));
+}
+__device__ __forceinline__ float2 normal_tail(float2 nax, float2& e) {
+    const float2 d = __ffma2_rn(nax, both(-0.3275911f * 0.70710678f), both(1.f));
+    const float2 z = __fmul2_rn(__fmul2_rn(nax, nax), both(-0.72134752f));   // -x^2 / 2 in powers of 2
+    float2 t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(d.y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+    float2 p = __ffma2_rn(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+    p = __ffma2_rn(t, p, both(0.5f * 1.421413741f));
+    p = __ffma2_rn(t, p, both(0.5f * -0.284496736f));
+    p = __ffma2_rn(t, p, both(0.5f * 0.254829592f));
+    return __fmul2_rn(__fmul2_rn(p, t), e);
+}
+// x Phi(x) = max(x, 0) - |x| Phi(-|x|)
+__device__ __forceinline__ void gelu(F8& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = v.p[i], nax = neg_abs(x);
+        float2 e;
+        const float2 q = normal_tail(nax, e);
+        v.p[i] = __ffma2_rn(nax, q, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+    }
+}
+// Phi(x) + x phi(x)
+__device__ __forceinline__ void gelu_slope(F8& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = v.p[i];
+        float2 e;
+        const float2 q = normal_tail(neg_abs(x), e);
+        const float2 phi = make_float2(x.x >= 0.f ? 1.f - q.x : q.x, x.y >= 0.f ? 1.f - q.y : q.y);
+        v.p[i] = __ffma2_rn(__fmul2_rn(x, both(0.39894228f)), e, phi);
+    }
 }
 
 struct PackArgs {
@@ -31,131 +72,126 @@ struct PackArgs {
     Q8Out keep;    // x itself (codes null: not kept)
 };
 
-// Groups of 32..256 columns: a warp takes kU tiles at a time, independent of
-// one another.
-constexpr int kU = 4;
+// A warp's tile of a flat grid over matrices of `tpr` tiles per row: its row, its
+// first column, and the columns of it that lie in the row.  One tile per warp:
+// the registers of more cost more warps than their loads in flight gain (GELU's
+// gradient at 16384 x 3072 takes 70 us with 1, 79 with 2, 115 with 4).
+struct FlatTile {
+    int64_t row;   // first element of the row
+    int64_t c0;
+    uint32_t r;
+    int left;
+};
+__device__ __forceinline__ bool flat_tile(uint32_t tiles, uint32_t tpr, int64_t cols, FlatTile& t) {
+    const uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    t.r = tpr == tiles ? 0 : i / tpr;
+    t.row = (int64_t)t.r * cols;
+    t.c0 = (int64_t)(i - t.r * tpr) * kQTile;
+    t.left = (int)min((int64_t)kQTile, cols - t.c0);
+    return i < tiles;
+}
+
+// Groups of 32..256 columns: tiles are independent of one another.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_pack_groups(const PackArgs a, uint32_t tiles, uint32_t tpr) {
+    FlatTile t;
+    if (!flat_tile(tiles, tpr, a.cols, t)) return;
     const int lane = threadIdx.x & 31;
-    const uint32_t t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kU;
-    float v[kU][8];
-    int64_t r[kU], c0[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        const uint32_t t = t0 + u;
-        r[u] = t / tpr;
-        c0[u] = (int64_t)(t - (uint32_t)r[u] * tpr) * kQTile;
-        if (t < tiles) load_tile<T, VEC>((const T*)a.x + r[u] * a.cols, c0[u], a.cols, lane, v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        if (t0 + u >= tiles) break;
-        if (a.keep.codes) pack_tile_groups<VEC>(a.keep, r[u], c0[u], a.cols, lane, v[u]);
-        if (a.act) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[u][j] = gelu(v[u][j]);
-        }
-        pack_tile_groups<VEC>(a.out, r[u], c0[u], a.cols, lane, v[u]);
-    }
+    const int64_t e = t.row + t.c0 + lane_col<VEC>(lane);
+    const int64_t sc = (int64_t)t.r * a.out.n_groups + (t.c0 >> a.out.gshift);
+    F8 v;
+    load_tile<T, VEC>((const T*)a.x + e, t.left, lane, v);
+    if (a.keep.codes)
+        pack_tile_groups<VEC>(a.keep.format, a.keep.gshift, a.keep.codes + e, a.keep.scales + sc, t.left, lane, v);
+    if (a.act) gelu(v);
+    pack_tile_groups<VEC>(a.out.format, a.out.gshift, a.out.codes + e, a.out.scales + sc, t.left, lane, v);
 }
 
 // One scale per row: the row in the registers of W warps, K tiles each.
-template <typename T, bool VEC, int K>
-__global__ void __launch_bounds__(1024) k_pack_row(const PackArgs a, int W, int slots) {
-    __shared__ uint32_t red[2][kMaxSlots * 32];
-    const RowSlot rs(W);
-    const int64_t r = (int64_t)blockIdx.x * slots + rs.slot;
+template <typename T, bool VEC, int K, bool ONE>
+__global__ void __launch_bounds__(ONE ? 32 * kRowsPerBlock : 1024) k_pack_row(const PackArgs a) {
+    __shared__ float red[2][32];
+    const RowSlot<ONE> rs;
+    const int64_t r = rs.first_row();
     if (r >= a.rows) return;
-    float v[K][8];
+    const int c0 = rs.w * K * kQTile;
+    const int64_t e = r * a.cols + c0 + lane_col<VEC>(rs.lane);
+    const int left = (int)a.cols - c0;
+    F8 v[K];
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        load_tile<T, VEC>((const T*)a.x + r * a.cols, (int64_t)(k * W + rs.w) * kQTile, a.cols, rs.lane, v[k]);
-    auto pack = [&](const Q8Out& q, uint32_t* rd) {
-        uint32_t m = 0;
+        load_tile<T, VEC>((const T*)a.x + e + k * kQTile, left - k * kQTile, rs.lane, v[k]);
+    auto pack = [&](const Q8Out& q, float* rd) {
+        float m = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) m = max(m, tile_amax(v[k]));
-        const QScale s = q_scale(rs.max_of(m, rd), q_top(q.format));
+        for (int k = 0; k < K; ++k) m = amax8(v[k], m);
+        const QScale s = q_scale(rs.max_of(m, rd), q.format);
         if (rs.w == 0 && rs.lane == 0) q.scales[r] = s.scale;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            pack_tile_row<VEC>(q, r, (int64_t)(k * W + rs.w) * kQTile, a.cols, rs.lane, v[k], s.inv);
+            pack_tile_row<VEC>(q.format, q.codes + e + k * kQTile, left - k * kQTile, rs.lane, v[k], s.inv);
     };
     if (a.keep.codes) pack(a.keep, red[0]);
     if (a.act) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = gelu(v[k][j]);
+        for (int k = 0; k < K; ++k) gelu(v[k]);
     }
     pack(a.out, red[1]);
 }
 
-// One scale per row, rows of more than 32768 columns: a block of 32 warps
+// One scale per row, rows of more than 16384 columns: a block of 32 warps
 // reads the row once for its magnitudes and once for its codes.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) k_pack_long(const PackArgs a) {
-    __shared__ uint32_t red[2][32];
-    const RowSlot rs(32);
+    __shared__ float red[2][32];
+    const RowSlot<false> rs;
     const int64_t r = blockIdx.x;
-    const T* x = (const T*)a.x + r * a.cols;
-    uint32_t mk = 0, mo = 0;
-    for (int64_t c0 = (int64_t)rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
-        float v[8];
-        load_tile<T, VEC>(x, c0, a.cols, rs.lane, v);
-        mk = max(mk, tile_amax(v));
+    float mk = 0.f, mo = 0.f;
+    for (int64_t c0 = rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
+        F8 v;
+        load_tile<T, VEC>((const T*)a.x + r * a.cols + c0 + lane_col<VEC>(rs.lane), (int)(a.cols - c0), rs.lane, v);
+        mk = amax8(v, mk);
         if (a.act) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = gelu(v[j]);
-            mo = max(mo, tile_amax(v));
+            gelu(v);
+            mo = amax8(v, mo);
         } else {
             mo = mk;
         }
     }
-    const QScale sk = q_scale(rs.max_of(mk, red[0]), q_top(a.keep.format));
-    const QScale so = q_scale(rs.max_of(mo, red[1]), q_top(a.out.format));
+    const QScale sk = q_scale(rs.max_of(mk, red[0]), a.keep.format);
+    const QScale so = q_scale(rs.max_of(mo, red[1]), a.out.format);
     if (threadIdx.x == 0) {
         if (a.keep.codes) a.keep.scales[r] = sk.scale;
         a.out.scales[r] = so.scale;
     }
-    for (int64_t c0 = (int64_t)rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
-        float v[8];
-        load_tile<T, VEC>(x, c0, a.cols, rs.lane, v);
-        if (a.keep.codes) pack_tile_row<VEC>(a.keep, r, c0, a.cols, rs.lane, v, sk.inv);
-        if (a.act) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = gelu(v[j]);
-        }
-        pack_tile_row<VEC>(a.out, r, c0, a.cols, rs.lane, v, so.inv);
+    for (int64_t c0 = rs.w * kQTile; c0 < a.cols; c0 += 32 * kQTile) {
+        const int64_t e = r * a.cols + c0 + lane_col<VEC>(rs.lane);
+        const int left = (int)(a.cols - c0);
+        F8 v;
+        load_tile<T, VEC>((const T*)a.x + e, left, rs.lane, v);
+        if (a.keep.codes) pack_tile_row<VEC>(a.keep.format, a.keep.codes + e, left, rs.lane, v, sk.inv);
+        if (a.act) gelu(v);
+        pack_tile_row<VEC>(a.out.format, a.out.codes + e, left, rs.lane, v, so.inv);
     }
 }
 
 // unpack (GRAD false: x = scale * code) and GELU's gradient (GRAD: x = da
-// times the slope at scale * code), kU tiles per warp.
+// times the slope at scale * code).
 template <typename T, bool VEC, bool GRAD>
 __global__ void __launch_bounds__(256) k_unpack(const Q8In q, const T* da, T* x, uint32_t tiles, uint32_t tpr) {
+    FlatTile t;
+    if (!flat_tile(tiles, tpr, q.cols, t)) return;
     const int lane = threadIdx.x & 31;
-    const uint32_t t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kU;
-    float v[kU][8], g[GRAD ? kU : 1][8];
-    int64_t r[kU], c0[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        const uint32_t t = t0 + u;
-        r[u] = t / tpr;
-        c0[u] = (int64_t)(t - (uint32_t)r[u] * tpr) * kQTile;
-        if (t < tiles) {
-            load_values<VEC>(q, r[u], c0[u], lane, v[u]);
-            if constexpr (GRAD) load_tile<T, VEC>(da + r[u] * q.cols, c0[u], q.cols, lane, g[u]);
-        }
+    const int64_t e = t.row + t.c0 + lane_col<VEC>(lane);
+    F8 v, g;
+    if constexpr (GRAD) load_tile<T, VEC>(da + e, t.left, lane, g);
+    load_values<VEC>(q.format, q.gshift, q.codes + e, q.scales + (int64_t)t.r * q.n_groups + (t.c0 >> q.gshift), t.left,
+                     lane, v);
+    if constexpr (GRAD) {
+        gelu_slope(v);
+        v.mul(g);
     }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        if (t0 + u >= tiles) break;
-        if constexpr (GRAD) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[u][j] = g[u][j] * gelu_slope(v[u][j]);
-        }
-        store_tile<T, VEC>(x + r[u] * q.cols, c0[u], q.cols, lane, v[u]);
-    }
+    store_tile<T, VEC>(x + e, t.left, lane, v);
 }
 
 // dst[c * bp + beta] = row beta's value at column c, 0 for beta >= b: four rows
@@ -184,15 +220,18 @@ int launch_pack(const PackArgs& a, int group, cudaStream_t s) {
     if (group != 0) {
         const int64_t tiles = a.rows * tpr;
         if (tiles > INT32_MAX) return SNK_ERR_LIMIT;
-        k_pack_groups<T, VEC><<<(unsigned)ceil_div(tiles, 8 * kU), 256, 0, s>>>(a, (uint32_t)tiles, (uint32_t)tpr);
-    } else if (tpr <= 128) {
-        // few rows: one tile per warp, for the shortest time of a row
-        const bool short_rows = tpr <= 8 || (a.rows <= 256 && tpr <= 32);
-        const int K = short_rows ? 1 : 4;
-        const int W = (int)ceil_div(tpr, K), slots = std::max(1, std::min(kMaxSlots, 8 / W));
-        const unsigned grid = (unsigned)ceil_div(a.rows, slots);
-        if (K == 1) k_pack_row<T, VEC, 1><<<grid, slots * W * 32, 0, s>>>(a, W, slots);
-        else k_pack_row<T, VEC, 4><<<grid, slots * W * 32, 0, s>>>(a, W, slots);
+        k_pack_groups<T, VEC><<<(unsigned)ceil_div(tiles, 8), 256, 0, s>>>(a, (uint32_t)tiles, (uint32_t)tpr);
+    } else if (tpr <= kRegisterTiles) {
+        const RowShape f = row_shape(tpr, a.rows <= 256 ? 1 : 4);
+        const unsigned grid = (unsigned)ceil_div(a.rows, f.slots()), threads = f.threads();
+        switch (f.K + (f.one() ? 2 : 0)) {
+            case 1: k_pack_row<T, VEC, 1, false><<<grid, threads, 0, s>>>(a); break;
+            case 2: k_pack_row<T, VEC, 2, false><<<grid, threads, 0, s>>>(a); break;
+            case 3: k_pack_row<T, VEC, 1, true><<<grid, threads, 0, s>>>(a); break;
+            case 4: k_pack_row<T, VEC, 2, true><<<grid, threads, 0, s>>>(a); break;
+            case 5: k_pack_row<T, VEC, 3, true><<<grid, threads, 0, s>>>(a); break;
+            default: k_pack_row<T, VEC, 4, true><<<grid, threads, 0, s>>>(a); break;
+        }
     } else {
         k_pack_long<T, VEC><<<(unsigned)a.rows, 1024, 0, s>>>(a);
     }
@@ -232,7 +271,7 @@ int launch_unpack(Q8In q, int64_t rows, int group, const void* da, void* x, cuda
     if (tiles > INT32_MAX) return SNK_ERR_LIMIT;
     const uintptr_t al = sizeof(T) == 4 ? 32 : 16;
     const bool vec = q.cols % 8 == 0 && q8_aligned(q.codes, 8) && q8_aligned(x, al) && q8_aligned(da, al);
-    const unsigned grid = (unsigned)ceil_div(tiles, 8 * kU);
+    const unsigned grid = (unsigned)ceil_div(tiles, 8);
     if (vec)
         k_unpack<T, true, GRAD><<<grid, 256, 0, s>>>(q, (const T*)da, (T*)x, (uint32_t)tiles, (uint32_t)tpr);
     else

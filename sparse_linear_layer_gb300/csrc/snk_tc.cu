@@ -610,10 +610,10 @@ __device__ __forceinline__ float4 load4(const SrcF32& D, int64_t r, int64_t k) {
     return __ldg(reinterpret_cast<const float4*>(D.p + r * D.cols + k));
 }
 __device__ __forceinline__ float4 load4(const SrcQ8& D, int64_t r, int64_t k) {
-    float v[4];
-    q_values4(__ldg(reinterpret_cast<const uint32_t*>(D.q.codes + r * D.q.cols + k)), D.q.format, v);
+    float2 a, b;
+    q_values4(__ldg(reinterpret_cast<const uint32_t*>(D.q.codes + r * D.q.cols + k)), D.q.format, a, b);
     const float s = __ldg(D.q.scales + r * D.q.n_groups + (k >> D.q.gshift));
-    return make_float4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+    return make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
 }
 
 // Dense operand, once per call: per row the scale exponent of its largest
