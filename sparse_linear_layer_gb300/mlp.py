@@ -1,0 +1,97 @@
+"""A pre-norm MLP block of two truly sparse layers whose activations are kept in
+8 bits:
+
+    total = x + residual
+    y     = down(gelu(up(rmsnorm(total) * gain)))
+
+The norm writes its output in 8 bits and the first layer multiplies that; GELU
+reads the first layer's output once and writes both its own output and that input
+in 8 bits, and the second layer multiplies the former.  The backward pass takes
+both layers' weight gradients, and GELU's slope, from the 8-bit matrices, so a
+block keeps one byte per activation (with fp32 layers: four) beside the residual
+stream.  Roundings to 8 bits are passed through as the identity.
+
+  "Beyond Masked Sparsity: SNACK Enables Truly Sparse Neural Networks on GPU",
+    Tables 4-5: the GPT-2 MLP stack (768 -> 3072 -> 768, GELU) with truly
+    sparse layers; the norm and the 8-bit activations are this library's.
+
+Everything numeric runs in libsnk's kernels; this file wires them into autograd.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import q8
+from .module import SparseLinear
+
+
+class _SparseMLPFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gain, up_values, up_bias, down_values, down_bias, block):
+        ctx.set_materialize_grads(False)
+        n, total, rstd = q8.rmsnorm(x, gain, residual=residual, eps=block.eps, format=block.format,
+                                    group=block.group)
+        h = block.up._h.forward_q8(n, up_bias)
+        a, kept = q8.gelu(h, format=block.format, group=block.group, keep=True)
+        y = block.down._h.forward_q8(a, down_bias)
+        ctx.block, ctx.has_residual = block, residual is not None
+        ctx.save_for_backward(total, rstd, gain, n.codes, n.scales, kept.codes, kept.scales, a.codes, a.scales)
+        return (y, total) if ctx.has_residual else y
+
+    @staticmethod
+    def backward(ctx, dy, dtotal=None):
+        block = ctx.block
+        total, rstd, gain, n_codes, n_scales, k_codes, k_scales, a_codes, a_scales = ctx.saved_tensors
+        n = q8.Q8Tensor(n_codes, n_scales, block.group)
+        kept = q8.Q8Tensor(k_codes, k_scales, block.group)
+        a = q8.Q8Tensor(a_codes, a_scales, block.group)
+        if dtotal is not None:
+            dtotal = dtotal.contiguous()
+        if dy is None:   # only total was used
+            return (dtotal, dtotal if ctx.has_residual else None) + (None,) * 6
+        dy = dy.contiguous()
+        up, down = block.up, block.down
+        da = down._h.backward_input(dy)
+        d_down, d_down_bias = down._h.backward_weight_q8(a, dy, with_bias=True)
+        dh = q8.gelu_backward(da, kept, out=da)
+        dn = up._h.backward_input(dh)
+        d_up, d_up_bias = up._h.backward_weight_q8(n, dh, with_bias=True)
+        dx, dgain = q8.rmsnorm_backward(dn, total, rstd, gain, dtotal=dtotal)
+        return (dx, dx if ctx.has_residual else None, dgain, d_up, d_up_bias if up.bias is not None else None,
+                d_down, d_down_bias if down.bias is not None else None, None)
+
+
+class SparseMLP(torch.nn.Module):
+    """forward(x) gives y; forward(x, residual) gives (y, total), total being
+    the residual stream that the next block adds y to.  x and residual [...,
+    features] are float32, float16 or bfloat16; y has their type.  format and
+    group are those of every 8-bit matrix of the block (see q8)."""
+
+    def __init__(self, features: int, hidden: int, sparsity: float, bias: bool = True, eps: float = 1e-5,
+                 format: str = "int8", group: int = 0, seed: int = 0, device=None):
+        super().__init__()
+        self.up = SparseLinear(features, hidden, sparsity, bias=bias, seed=seed, device=device)
+        self.down = SparseLinear(hidden, features, sparsity, bias=bias, seed=seed + 2, device=device)
+        self.gain = torch.nn.Parameter(torch.ones(features, device=self.up.values.device))
+        self.eps, self.format, self.group = eps, format, group
+
+    def forward(self, x, residual=None):
+        features = self.up.in_features
+        x2 = x.reshape(-1, features).contiguous()
+        args = (self.gain, self.up.values, self.up.bias, self.down.values, self.down.bias, self)
+        if residual is None:
+            return _SparseMLPFn.apply(x2, None, *args).to(x.dtype).reshape(x.shape)
+        r2 = residual.reshape(-1, features).contiguous()
+        y, total = _SparseMLPFn.apply(x2, r2, *args)
+        return y.to(x.dtype).reshape(x.shape), total.reshape(x.shape)
+
+    def sparse_layers(self):
+        """The block's layers, for SET."""
+        return [self.up, self.down]
+
+    def extra_repr(self) -> str:
+        return f"eps={self.eps}, format={self.format!r}, group={self.group}"
+
+    def close(self):
+        self.up.close()
+        self.down.close()

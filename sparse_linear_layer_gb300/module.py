@@ -20,7 +20,7 @@ from __future__ import annotations
 
 import torch
 
-from . import binding, synth
+from . import binding, q8, synth
 
 
 class _SparseLinearFn(torch.autograd.Function):
@@ -32,24 +32,32 @@ class _SparseLinearFn(torch.autograd.Function):
         ctx.layer = layer
         ctx.has_bias = bias is not None
         ctx.shape = x.shape
-        ctx.save_for_backward(x2)
+        if layer.keep is None:
+            ctx.save_for_backward(x2)
+        else:
+            kept = q8.pack(x2, layer.keep, layer.keep_group)
+            ctx.save_for_backward(kept.codes, kept.scales)
         return y.reshape(*x.shape[:-1], layer.out_features)
 
     @staticmethod
     def backward(ctx, gy):
-        (x2,) = ctx.saved_tensors
         layer = ctx.layer
+        kept = None if layer.keep is None else q8.Q8Tensor(*ctx.saved_tensors, layer.keep_group)
         gy2 = gy.reshape(-1, layer.out_features).contiguous().float()
         gx = gvalues = gbias = None
         if ctx.needs_input_grad[0]:
-            gx = torch.empty_like(x2)
+            gx = torch.empty((gy2.shape[0], layer.in_features), dtype=torch.float32, device=gy.device)
             binding.snk_backward_input(layer._h.handle, gy2, gx)
             gx = gx.reshape(ctx.shape)
         if ctx.needs_input_grad[1] or (ctx.has_bias and ctx.needs_input_grad[2]):
             gvalues = torch.empty_like(layer.values)
             gb = torch.empty(layer.out_features, dtype=torch.float32, device=gy.device) \
                 if ctx.has_bias else None
-            binding.snk_backward_weight(layer._h.handle, x2, gy2, gvalues, gb)
+            if kept is None:
+                binding.snk_backward_weight(layer._h.handle, *ctx.saved_tensors, gy2, gvalues, gb)
+            else:
+                binding.snk_backward_weight_q8(layer._h.handle, kept.codes, kept.scales, kept.format_id,
+                                               kept.group, gy2, kept.rows, gvalues, gb)
             gbias = gb if ctx.has_bias and ctx.needs_input_grad[2] else None
             if not ctx.needs_input_grad[1]:
                 gvalues = None
@@ -61,11 +69,23 @@ class SparseLinear(torch.nn.Module):
 
     SparseLinear(in_features, out_features, sparsity) draws a uniform random
     support of round(out*in*(1 - sparsity)) positions and values
-    N(0, 1/(in*density)); from_triple() binds an existing triple."""
+    N(0, 1/(in*density)); from_triple() binds an existing triple.
+
+    keep "int8" or "e4m3": the input kept for the backward pass is an 8-bit
+    matrix with a scale per row, or per keep_group columns (see q8): one byte
+    per element for four.  The forward pass and the input's gradient do not
+    change; the weight's gradient is taken from the 8-bit input."""
+
+    keep = None
+    keep_group = 0
 
     def __init__(self, in_features: int, out_features: int, sparsity: float, bias: bool = True,
-                 seed: int = 0, device=None):
+                 seed: int = 0, device=None, keep: str | None = None, keep_group: int = 0):
         super().__init__()
+        if keep not in (None, "int8", "e4m3") or keep_group not in (0, 32, 64, 128, 256):
+            raise ValueError(f"keep is None, 'int8' or 'e4m3' and keep_group 0, 32, 64, 128 or 256: "
+                             f"got {keep!r}, {keep_group}")
+        self.keep, self.keep_group = keep, keep_group
         device = torch.device(device if device is not None else "cuda")
         density = 1.0 - sparsity
         nnz = synth.nnz_for(out_features, in_features, 100.0 * sparsity)
