@@ -34,353 +34,13 @@
 //    time and its lanes split the BP batch columns.  Each lane accumulates
 //    its own partial sums (at least 32 per output for BP <= 4), reduced at the
 //    segment end with __shfl_xor_sync.
-#include "snk_device.cuh"
+#include "snk_spmm.cuh"
 
 namespace snk {
 
-struct SpmmArgs {
-    const float* val;        // stored values, canonical order
-    const int32_t* perm;     // column-order -> canonical slot (transposed product) or null
-    const int32_t* idx;      // operand index per stored entry (col, or row in column order)
-    const uint16_t* idx16;   // the same as 16-bit, zero padded (shared-memory path)
-    const int32_t* seg_ptr;  // [n_seg+1]
-    const int4* cdesc;       // [n_blocks * kWarpsPerBlock] (k0, k1, first seg, end seg)
-    const BlockDesc* bdesc;  // [n_blocks]
-    const int32_t* bnd;      // [n_blocks+1] first entry of each block
-    int64_t nnz;
-    int64_t n_seg;           // output length per batch row
-    int64_t n_src;           // operand length per batch row
-    int b;                   // batch columns of this tile (<= BP)
-    int n_blocks;
-    const float* X;          // [b, n_src] row-major
-    const float* xt;         // [n_src][BP] transposed copy (global-memory path)
-    const float* bias;       // [n_seg] or null
-    float* Y;                // [b, n_seg] row-major
-    float* part;             // [n_blocks][2][BP] cross-block partial sums
-    int32_t* cnt;            // [n_seg] arrival counters
-    // column sweep of the transposed product (k_sweep only)
-    const int4* sw_blk;      // per block: two records
-    const int2* sw_col;      // per block and column: (first virtual lane, lanes)
-    const int4* sw_lane;     // per virtual lane: (first quad, quad stride, first entry, end entry)
-    float* sw_gpart;         // partials of virtual lanes beyond the block's threads
-    const int* sw_split;     // [boundary][lane] resume quad of each lane at each table boundary
-    int64_t sw_nlane;        // lanes per boundary in sw_split
-    int sw_rows;             // operand rows staged per phase (a multiple of 4)
-    int sw_phases;           // phases of this launch
-    int sw_stride;           // table boundaries per phase of this launch
-};
-
-// A segment cut by a chunk boundary, whose partial sum this warp stored in
-// its shared-memory slot (0: the segment entered the chunk from before,
-// 1: it starts in the chunk and leaves it).
-struct Pending {
-    int r;
-    uint32_t rs, re;
-};
-
-// Shared memory: [transposed operand (shared-memory path)][partials
-// [warps][2][BP]][segment ids [warps][2]].
-template <bool GATHER>
-struct SpmmShape {
-    static constexpr int kNT = GATHER ? kThreadsDx : kThreads;
-    static constexpr int kW = kNT / kWarp;
-};
-template <int BP, bool GATHER>
-__host__ __device__ constexpr size_t spmm_slot_bytes() {
-    return (size_t)SpmmShape<GATHER>::kW * 2 * BP * sizeof(float) +
-           (size_t)SpmmShape<GATHER>::kW * 2 * sizeof(int);
-}
-__host__ __device__ inline size_t operand_floats(int64_t n_src, int bp) {
-    return ((size_t)n_src * bp + 3) & ~(size_t)3;
-}
-
-// Finish one output segment: reduce the per-lane partial sums across the
-// warp's groups; write the result, or, for a segment cut by a chunk boundary,
-// store this warp's partial in its shared slot.
-template <int BP>
-__device__ __forceinline__ void finish_segment(const SpmmArgs& a, float (&acc)[Tile<BP>::VEC],
-                                               int r, uint32_t rs, uint32_t re, uint32_t k0,
-                                               uint32_t k1, float bo, int lane, int sub,
-                                               float* my_slots, Pending (&pend)[2]) {
-    using TL = Tile<BP>;
-    constexpr int VEC = TL::VEC, LPE = TL::LPE;
-#pragma unroll
-    for (int o = LPE; o < kWarp; o <<= 1) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-    }
-    if (rs >= k0 && re <= k1) {
-        if (lane < LPE) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int beta = TL::beta(sub, j);
-                if (beta < a.b) a.Y[(int64_t)beta * a.n_seg + r] = acc[j] + bo;
-            }
-        }
-    } else {
-        const int slot = (rs < k0) ? 0 : 1;
-        if (lane < LPE) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) my_slots[slot * BP + sub * VEC + j] = acc[j];
-        }
-        pend[slot] = Pending{r, rs, re};
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
-}
-
-// A segment cut between blocks: store this block's partial, count the
-// arrival, and let the last arriving block add the partials of the non-empty
-// blocks first..last in block order (the first block's is in its slot 1).
-template <int BP>
-__device__ __noinline__ void cross_block(const SpmmArgs& a, int r, int slot,
-                                         const float (&sum)[Tile<BP>::VEC], int first, int last,
-                                         int n_contrib, int lane, int sub) {
-    using TL = Tile<BP>;
-    constexpr int VEC = TL::VEC, LPE = TL::LPE;
-    if (lane < LPE) {
-        float* my = a.part + ((int64_t)blockIdx.x * 2 + slot) * BP + sub * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) my[j] = sum[j];
-    }
-    __threadfence();
-    __syncwarp();
-    int old = 0;
-    if (lane == 0) old = atomicAdd(a.cnt + r, 1);
-    old = __shfl_sync(0xffffffffu, old, 0);
-    if (old != n_contrib - 1) return;
-    __threadfence();
-    if (lane < LPE) {
-        float tot[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) tot[j] = 0.f;
-        for (int c = first; c <= last; ++c) {
-            if (__ldg(a.bnd + c + 1) == __ldg(a.bnd + c)) continue;
-            const float* pp = a.part + ((int64_t)c * 2 + (c == first ? 1 : 0)) * BP + sub * VEC;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) tot[j] += __ldcg(pp + j);
-        }
-        const float bo = a.bias ? __ldg(a.bias + r) : 0.f;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int beta = TL::beta(sub, j);
-            if (beta < a.b) a.Y[(int64_t)beta * a.n_seg + r] = tot[j] + bo;
-        }
-    }
-    if (lane == 0) a.cnt[r] = 0;
-}
-
-// After the block barrier: the warp where a cut segment starts adds the
-// partials of the following warps that continue it (warp order) and writes
-// the result, unless the segment leaves the block; warp 0 does the same for
-// the segment that entered the block from before.  Segments that cross a
-// block boundary continue in cross_block.
-template <int BP, int W>
-__device__ __forceinline__ void block_combine(const SpmmArgs& a, const float* sp, const int* srow,
-                                              const Pending (&pend)[2], int warp, int lane,
-                                              int sub) {
-    using TL = Tile<BP>;
-    constexpr int VEC = TL::VEC, LPE = TL::LPE;
-    if (pend[1].r < 0 && !(warp == 0 && pend[0].r >= 0)) return;
-    const BlockDesc bd = a.bdesc[blockIdx.x];
-#pragma unroll
-    for (int which = 1; which >= 0; --which) {
-        const int slot = which;
-        if (slot == 0 && warp != 0) continue;
-        const int r = pend[slot].r;
-        if (r < 0) continue;
-        float sum[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-            sum[j] = lane < LPE ? sp[(warp * 2 + slot) * BP + sub * VEC + j] : 0.f;
-        for (int w2 = warp + 1; w2 < W && srow[w2 * 2] == r; ++w2) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                if (lane < LPE) sum[j] += sp[(w2 * 2) * BP + sub * VEC + j];
-        }
-        const bool ends_here = pend[slot].re <= (uint32_t)bd.k1;
-        if (slot == 1) {
-            if (ends_here) {
-                if (lane < LPE) {
-                    const float bo = a.bias ? __ldg(a.bias + r) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const int beta = TL::beta(sub, j);
-                        if (beta < a.b) a.Y[(int64_t)beta * a.n_seg + r] = sum[j] + bo;
-                    }
-                }
-            } else {
-                cross_block<BP>(a, r, 1, sum, blockIdx.x, bd.tail_last, bd.n_tail, lane, sub);
-            }
-        } else {
-            if (ends_here)
-                cross_block<BP>(a, r, 0, sum, bd.head_first, blockIdx.x, bd.n_head, lane, sub);
-            else
-                cross_block<BP>(a, r, 0, sum, bd.head_first, bd.tail_last,
-                                bd.n_head + bd.n_tail - 1, lane, sub);
-        }
-    }
-}
-
-// One warp per chunk.  The chunk's entries [k0, k1) are streamed as a flat
-// sequence of blocks of 4*GPW entries from the multiple of 4 at or below k0
-// (each group of LPE lanes owns 4 consecutive entries of a block).  Blocks
-// sit in D+1 register slots: while block j is consumed, blocks j+1 .. j+D
-// are in flight (and, for the transposed product, the values of blocks
-// j+1 .. j+G are being gathered).  The loop over slots is unrolled so every slot index
-// is a compile-time constant.  A block inside one segment is consumed
-// without masks; a block that straddles segment or chunk boundaries is
-// consumed once per segment it touches, with masks.
-template <int BP, bool GATHER, bool SMEM, bool I16 = SMEM && SNK_IDX16>
-__global__ void __launch_bounds__(SpmmShape<GATHER>::kNT, 1) k_spmm(const SpmmArgs a) {
-    constexpr int NT = SpmmShape<GATHER>::kNT;
-    constexpr int W = SpmmShape<GATHER>::kW;
-    using TL = Tile<BP>;
-    constexpr int VEC = TL::VEC, LPE = TL::LPE, GPW = TL::GPW;
-    constexpr uint32_t BLK = 4 * GPW;
-    constexpr int D = GATHER ? (BP == 16 ? SNK_PIPE_DX16 : SNK_PIPE_DX) : (BP == 1 ? SNK_PIPE_FWD_NARROW : SNK_PIPE_FWD);
-    constexpr int NS = D + 1;
-    // blocks whose values are gathered ahead of the consumed one (the
-    // permutation of a block arrives NS - G blocks before its gather)
-    constexpr int G = GATHER ? (SNK_GATHER_LEAD < D ? SNK_GATHER_LEAD : D) : 0;
-    extern __shared__ float4 smem4[];
-    float* xs = reinterpret_cast<float*>(smem4);
-    float* sp = xs + (SMEM ? operand_floats(a.n_src, BP) : 0);
-    int* srow = reinterpret_cast<int*>(sp + W * 2 * BP);
-
-    const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
-    const int grp = lane / LPE;
-    const int sub = lane % LPE;
-    const uint32_t nnz = (uint32_t)a.nnz;
-    const int4 cd = a.cdesc[blockIdx.x * W + warp];
-    const uint32_t k0 = (uint32_t)cd.x, k1 = (uint32_t)cd.y;
-    const uint32_t base_first = k0 & ~3u;
-    float* my_slots = sp + warp * 2 * BP;
-
-    IdxBlk<I16> ib[NS];
-    float wb[NS][4];
-    int pb[NS][4];
-    auto issue = [&](int s, uint32_t blk0) {
-        const uint32_t base = blk0 + 4 * grp;
-        if constexpr (I16) ib[s].load(a.idx16, base);
-        else ib[s].load(a.idx, base, nnz);
-        if constexpr (GATHER) padded4(a.perm, base, pb[s]);
-        else stream4(a.val, base, nnz, wb[s]);
-    };
-    // The value gather hits L1 when another entry of the same row (in the
-    // block's column range) brought its sector in, so it goes through L1;
-    // except with a 4-column operand in shared memory (160 KB at out =
-    // 10000), where the L1 left is small and caching the gathered sectors
-    // only in L2 is faster (measured: 56 against 60 us at 10000^2, 90%).
-    constexpr bool kGatherL2Only = SMEM && BP == 4;
-    auto gather = [&](int s, uint32_t blk0) {
-        const uint32_t base = blk0 + 4 * grp;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            wb[s][j] = (base + j < k1) ? (kGatherL2Only ? __ldcg(a.val + pb[s][j]) : __ldg(a.val + pb[s][j])) : 0.f;
-    };
-
-    // Everything that only depends on the chunk is requested before the
-    // operand staging: the first blocks of the stream and the first window of
-    // segment starts (and biases).
-    if (k0 < k1) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-            if (base_first + s * BLK < k1) issue(s, base_first + s * BLK);
-    }
-    SegWindow win{cd.z, cd.w - cd.z, 0, 0u, 0.f};
-    if (win.nrows > 0) win.load(0, lane, a.seg_ptr, a.bias);
-    if constexpr (SMEM) stage_transposed<BP>(xs, a.X, a.n_src, a.b, a.n_src, threadIdx.x, NT);
-    __syncthreads();
-    const float* xsrc = SMEM ? xs : a.xt;
-
-    Pending pend[2] = {Pending{-1, 0u, 0u}, Pending{-1, 0u, 0u}};
-    if (win.nrows > 0) {
-        if constexpr (GATHER) {
-#pragma unroll
-            for (int s = 0; s < G; ++s)
-                if (k0 < k1 && base_first + s * BLK < k1) gather(s, base_first + s * BLK);
-        }
-        const int r_begin = win.r_begin;
-        int i = 0;
-        uint32_t rs = win.bnd(0, lane, a.seg_ptr, a.bias), re = win.bnd(1, lane, a.seg_ptr, a.bias);
-        float acc[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
-
-        auto consume = [&](int s, uint32_t blk0) {
-            const uint32_t base = blk0 + 4 * grp;
-            if (rs <= blk0 && k0 <= blk0 && blk0 + BLK < re && blk0 + BLK <= k1) {
-                // interior block: every entry belongs to the current segment,
-                // which continues past the block
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float x[VEC];
-                    const float* px = xsrc + ib[s].get(j) * BP;
-                    if constexpr (SMEM) TL::load(px, sub, x);
-                    else TL::ldg(px, sub, x);
-#pragma unroll
-                    for (int t = 0; t < VEC; ++t) acc[t] = fmaf(wb[s][j], x[t], acc[t]);
-                }
-                return;
-            }
-            const uint32_t blk_end = min(blk0 + BLK, k1);
-            while (true) {
-                const uint32_t lo_k = max(max(rs, k0), blk0), hi_k = min(re, blk_end);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t k = base + j;
-                    if (k >= lo_k && k < hi_k) {
-                        float x[VEC];
-                        const float* px = xsrc + ib[s].get(j) * BP;
-                        if constexpr (SMEM) TL::load(px, sub, x);
-                        else TL::ldg(px, sub, x);
-#pragma unroll
-                        for (int t = 0; t < VEC; ++t) acc[t] = fmaf(wb[s][j], x[t], acc[t]);
-                    }
-                }
-                if (min(re, k1) > blk_end) break;  // segment continues in the next block
-                finish_segment<BP>(a, acc, r_begin + i, rs, re, k0, k1, win.bias_of(i), lane, sub,
-                                   my_slots, pend);
-                if (++i >= win.nrows) break;
-                rs = re;
-                re = win.bnd(i + 1, lane, a.seg_ptr, a.bias);
-                if (rs >= blk_end) break;
-            }
-        };
-
-        if (k0 < k1) {
-            for (uint32_t base0 = base_first; base0 < k1; base0 += NS * BLK) {
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    const uint32_t blk0 = base0 + s * BLK;
-                    if (blk0 < k1) {
-                        if constexpr (GATHER) {
-                            if (blk0 + G * BLK < k1) gather((s + G) % NS, blk0 + G * BLK);
-                        }
-                        consume(s, blk0);
-                        if (blk0 + NS * BLK < k1) issue(s, blk0 + NS * BLK);
-                    }
-                }
-            }
-        }
-        // segments that start at the end of the chunk (empty here)
-        while (i < win.nrows) {
-            finish_segment<BP>(a, acc, r_begin + i, rs, re, k0, k1, win.bias_of(i), lane, sub,
-                               my_slots, pend);
-            if (++i >= win.nrows) break;
-            rs = re;
-            re = win.bnd(i + 1, lane, a.seg_ptr, a.bias);
-        }
-    }
-    if (lane == 0) {
-        srow[warp * 2 + 0] = pend[0].r;
-        srow[warp * 2 + 1] = pend[1].r;
-    }
-    __syncthreads();
-    block_combine<BP, W>(a, sp, srow, pend, warp, lane, sub);
-}
+// snk_q8_sparse.cuh: one batch tile of an 8-bit operand with a scale per row.
+template <int FMT>
+int q8_forward_tile(Layer* L, const SpmmArgs& a, int bp, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Column sweep of the transposed product (batch tile BP <= 4, operand in
@@ -635,7 +295,7 @@ __global__ void __launch_bounds__(kThreadsDx, 1) k_sweep(const SpmmArgs a) {
         float sum[BP];
         sweep_sum<BP>(red, gred, cr.x, cr.y, sum);
         // in the chunk walk's lane layout: lane sub < LPE holds its VEC columns
-        using TL = Tile<BP>;
+        using TL = TileF32<BP>;
         const int sub = lane % TL::LPE;
         float mine[TL::VEC];
 #pragma unroll
@@ -643,11 +303,11 @@ __global__ void __launch_bounds__(kThreadsDx, 1) k_sweep(const SpmmArgs a) {
         const BlockDesc bd = a.bdesc[blockIdx.x];
         if (warp == 0) {
             if (__ldg(a.seg_ptr + c + 1) <= bd.k1)
-                cross_block<BP>(a, c, 0, mine, bd.head_first, blockIdx.x, bd.n_head, lane, sub);
+                cross_block<TL>(a, c, 0, mine, bd.head_first, blockIdx.x, bd.n_head, lane, sub);
             else
-                cross_block<BP>(a, c, 0, mine, bd.head_first, bd.tail_last, bd.n_head + bd.n_tail - 1, lane, sub);
+                cross_block<TL>(a, c, 0, mine, bd.head_first, bd.tail_last, bd.n_head + bd.n_tail - 1, lane, sub);
         } else {
-            cross_block<BP>(a, c, 1, mine, blockIdx.x, bd.tail_last, bd.n_tail, lane, sub);
+            cross_block<TL>(a, c, 1, mine, blockIdx.x, bd.tail_last, bd.n_tail, lane, sub);
         }
     }
 }
@@ -721,7 +381,7 @@ static int launch_bp(Layer* L, SpmmArgs a, const Q8In* q, cudaStream_t s) {
             if (int st = launch_q8_rows(*q, a.b, L->xt, s); st != SNK_OK) return st;
             a.X = L->xt;
         }
-        auto fn = k_spmm<BP, GATHER, true>;
+        auto fn = k_spmm<TileF32<BP>, GATHER, true>;
         if (set_smem(fn, smem) != SNK_OK) return SNK_ERR_CUDA;
         fn<<<a.n_blocks, NT, smem, s>>>(a);
     } else {
@@ -731,7 +391,7 @@ static int launch_bp(Layer* L, SpmmArgs a, const Q8In* q, cudaStream_t s) {
             k_transpose<BP><<<L->num_sms * 4, 256, 0, s>>>(a.X, a.n_src, a.b, L->xt);
         }
         a.xt = L->xt;
-        auto fn = k_spmm<BP, GATHER, false>;
+        auto fn = k_spmm<TileF32<BP>, GATHER, false>;
         if (set_smem(fn, slots) != SNK_OK) return SNK_ERR_CUDA;
         fn<<<a.n_blocks, NT, slots, s>>>(a);
     }
@@ -767,7 +427,15 @@ static int run_spmm(Layer* L, SpmmArgs a, const Q8In* q, int64_t b, cudaStream_t
             if (cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
             continue;
         }
-        int st = launch_tile<GATHER>(L, a, batch_tile(bt), q ? &qt : nullptr, s);
+        int st;
+        if (q && q->gshift == 31) {
+            a.codes = qt.codes;
+            a.row_scale = qt.scales;
+            st = q->format == SNK_Q8_INT8 ? q8_forward_tile<SNK_Q8_INT8>(L, a, batch_tile(bt), s)
+                                          : q8_forward_tile<SNK_Q8_E4M3>(L, a, batch_tile(bt), s);
+        } else {
+            st = launch_tile<GATHER>(L, a, batch_tile(bt), q ? &qt : nullptr, s);
+        }
         if (st != SNK_OK) return st;
     }
     return SNK_OK;
@@ -780,7 +448,7 @@ template <int BP>
 static int launch_csr_bp(SpmmArgs a, int max_smem, cudaStream_t s) {
     const size_t smem = operand_floats(a.n_src, BP) * sizeof(float) + spmm_slot_bytes<BP, false>();
     if (smem > (size_t)max_smem) return SNK_ERR_LIMIT;
-    auto fn = k_spmm<BP, false, true, false>;
+    auto fn = k_spmm<TileF32<BP>, false, true, false>;
     if (set_smem(fn, smem) != SNK_OK) return SNK_ERR_CUDA;
     fn<<<a.n_blocks, kThreads, smem, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
