@@ -3,6 +3,7 @@
 // a lane reads its batch columns (as in snk_spmm.cuh):
 //   stage()      the transposed X into shared memory
 //   dy()         a value of dY as the lane multiplies it
+//   Dy           the lane's values of a row of dY
 //   dot<SMEM>()  the lane's share of an entry's dot product
 #pragma once
 
@@ -36,6 +37,10 @@ struct DwTileF32 : Tile<B> {
     using TL = Tile<B>;
     using Elem = float;
     static constexpr int BP = B;
+    struct Dy {
+        float v[TL::VEC];
+        __device__ __forceinline__ void set(int j, float x) { v[j] = x; }
+    };
     __host__ __device__ static size_t bytes(int64_t n) { return (size_t)n * B * sizeof(float); }
     __device__ __forceinline__ static void stage(float* xs, const SddmmArgs& a, int tid, int nthreads) {
         stage_transposed<B>(xs, a.X, a.in_f, a.b, a.in_f, tid, nthreads);
@@ -44,23 +49,23 @@ struct DwTileF32 : Tile<B> {
         return __ldg(a.dY + (int64_t)beta * a.out_f + r);
     }
     template <bool SMEM>
-    __device__ __forceinline__ static float dot(const float* xsrc, int idx, int sub, const float (&d)[TL::VEC]) {
+    __device__ __forceinline__ static float dot(const float* xsrc, int idx, int sub, const Dy& d) {
         float x[TL::VEC];
         if constexpr (SMEM) TL::load(xsrc + idx * B, sub, x);
         else TL::ldg(xsrc + idx * B, sub, x);
         float p = 0.f;
 #pragma unroll
-        for (int t = 0; t < TL::VEC; ++t) p = fmaf(d[t], x[t], p);
+        for (int t = 0; t < TL::VEC; ++t) p = fmaf(d.v[t], x[t], p);
         return p;
     }
 };
 
 template <class TL>
-__device__ __forceinline__ void load_dy_row(const SddmmArgs& a, int r, int sub, float (&d)[TL::VEC]) {
+__device__ __forceinline__ void load_dy_row(const SddmmArgs& a, int r, int sub, typename TL::Dy& d) {
 #pragma unroll
     for (int j = 0; j < TL::VEC; ++j) {
         const int beta = TL::beta(sub, j);
-        d[j] = beta < a.b ? TL::dy(a, beta, r) : 0.f;
+        d.set(j, beta < a.b ? TL::dy(a, beta, r) : 0.f);
     }
 }
 
@@ -69,9 +74,8 @@ __device__ __forceinline__ void load_dy_row(const SddmmArgs& a, int r, int sub, 
 // consumed; the slot loop is unrolled so slot indices are constants).  The dY
 // values of the current row are in registers and the next row's are
 // requested one row ahead.
-template <class TL, bool SMEM>
+template <class TL, bool SMEM, bool I16 = SMEM && SNK_IDX16>
 __global__ void __launch_bounds__(kThreads, 1) k_sddmm(const SddmmArgs a) {
-    constexpr bool I16 = SMEM && SNK_IDX16;
     using Elem = typename TL::Elem;
     constexpr int VEC = TL::VEC, LPE = TL::LPE, GPW = TL::GPW, BP = TL::BP;
     constexpr uint32_t BLK = 4 * GPW;
@@ -119,10 +123,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_sddmm(const SddmmArgs a) {
     const int r_begin = win.r_begin;
     int i = 0;
     uint32_t rs = win.bnd(0, lane, a.row_ptr, nullptr), re = win.bnd(1, lane, a.row_ptr, nullptr);
-    float dyr[VEC], dyn[VEC];
+    typename TL::Dy dyr, dyn;
     load_dy_row<TL>(a, r_begin, sub, dyr);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) dyn[j] = 0.f;
+    for (int j = 0; j < VEC; ++j) dyn.set(j, 0.f);
     if (win.nrows > 1) load_dy_row<TL>(a, r_begin + 1, sub, dyn);
 
     auto consume = [&](int s, uint32_t blk0) {
@@ -157,8 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_sddmm(const SddmmArgs a) {
             if (++i >= win.nrows) break;
             rs = re;
             re = win.bnd(i + 1, lane, a.row_ptr, nullptr);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) dyr[j] = dyn[j];
+            dyr = dyn;
             if (i + 1 < win.nrows) load_dy_row<TL>(a, r_begin + i + 1, sub, dyn);
             if (rs >= blk_end) break;
         }
