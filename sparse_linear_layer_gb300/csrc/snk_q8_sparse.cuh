@@ -217,7 +217,8 @@ static int q8_smem(F fn, size_t smem) {
 
 // From this size on, the codes are transposed once by a kernel of their own and
 // every block copies the result with 16-byte accesses; below it every block
-// transposes them itself and the launch is saved (10000 x 16: 42 -> 33 us).
+// transposes them itself and the launch is saved (forward, 10000 x 16 at 99%:
+// 23.6 -> 14.6 us).
 constexpr size_t kStageCopy = 48 * 1024;
 
 template <int BP, int FMT>

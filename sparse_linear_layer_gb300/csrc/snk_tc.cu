@@ -43,6 +43,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "snk_q8.cuh"
 
@@ -121,6 +122,12 @@ constexpr int kRecCap = 1536;      // entries staged per window (the rest are re
 // by one (measured at 1200 entries per window: 13% faster; at 120: slower).
 constexpr int64_t kZeroFillEntries = 400;
 constexpr int kTcPeriod = 8;       // windows per accumulator turn
+// ... of the products with an 8-bit operand: as its codes (two products a window),
+// and in general (three).  The truncating accumulation is most of the error, in
+// proportion to the MMA steps of a turn: 32 and 36 of them leave 4.7e-7 and 7.1e-7
+// of the result where 96 leave 1.9e-6 (weight gradient at 10000^2, 90%, b = 512),
+// and shorter turns start to wait for the drains (16 steps: 195 us against 167).
+constexpr int kCodesPeriod = 4, kQPeriod = 3;
 constexpr int kTcGroupM = 8;       // dense-row tiles per raster group
 constexpr int kTcChunk = 8192;     // dense rows per launch
 constexpr int kPieceA = kTcM * kTcK * 2;          // 16 KB
@@ -282,6 +289,7 @@ struct TcArgs {
     int b;                    // dense rows in this launch
     int64_t K_len;            // reduction length
     const int32_t* row_exp;   // [b]
+    const float* row_scale;   // 8-bit operand with a scale per row: [b], instead of row_exp
     const uint16_t* off;      // sparse entries in tile order: tile offsets
     const uint32_t* hl;       // and fp16 pieces
     int zero_fill;            // clear whole stages (dense windows) or entry by entry
@@ -307,6 +315,10 @@ __device__ __forceinline__ void tc_tile_of(int id, int n_mt, int n_nt, int& mt, 
     nt = (id % gsz) / gm;
 }
 
+// PERIOD: windows per accumulator turn.  CODES: the dense operand is 8-bit codes,
+// exact in one fp16 piece (map_h), so a window takes two products instead of three
+// and half the dense bytes.
+template <int PERIOD, bool CODES>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_tc_spmm(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_l,
               const TcArgs a) {
@@ -395,9 +407,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 }
                 unsigned char* st = sa + s * kStageA;
-                mbar_expect_tx(&full_a[s], kStageA);
+                mbar_expect_tx(&full_a[s], CODES ? kPieceA : kStageA);
                 tma_load_2d(st, &map_h, (w0 + w) * kTcK, (int)r0, &full_a[s]);
-                tma_load_2d(st + kPieceA, &map_l, (w0 + w) * kTcK, (int)r0, &full_a[s]);
+                if (!CODES) tma_load_2d(st + kPieceA, &map_l, (w0 + w) * kTcK, (int)r0, &full_a[s]);
             }
             if (!ok) drain_ring(full_a, kStagesA, w);
         }
@@ -436,8 +448,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) {
             for (int w = 0; w < n_win; ++w) {
                 const int s_a = w % kStagesA, s_b = w % kStagesB;
-                const int q = w / kTcPeriod, ab = q & 1;
-                const bool first = (w % kTcPeriod) == 0;
+                const int q = w / PERIOD, ab = q & 1;
+                const bool first = (w % PERIOD) == 0;
                 if (!mbar_wait(&full_a[s_a], (w / kStagesA) & 1) ||
                     !mbar_wait(&full_b[s_b], (w / kStagesB) & 1) ||
                     (first && q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1))) {
@@ -453,11 +465,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t o = 32 * kk;
                     mma_f16(d, desc_sw128(ah + o), desc_sw128(bh + o), (first && kk == 0) ? 0u : 1u);
                     mma_f16(d, desc_sw128(ah + o), desc_sw128(bl + o), 1u);
-                    mma_f16(d, desc_sw128(al + o), desc_sw128(bh + o), 1u);
+                    if (!CODES) mma_f16(d, desc_sw128(al + o), desc_sw128(bh + o), 1u);
                 }
                 if (w + kStagesA < n_win) mma_commit(&empty_a[s_a]);
                 if (w + kStagesB < n_win) mma_commit(&empty_b[s_b]);
-                if ((w % kTcPeriod) == kTcPeriod - 1 || w == n_win - 1) mma_commit(&accf[ab]);
+                if ((w % PERIOD) == PERIOD - 1 || w == n_win - 1) mma_commit(&accf[ab]);
             }
             // every MMA issued has completed once fin completes (also after
             // an early stop: TMEM and the stages are released only then)
@@ -472,7 +484,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float acc[kColsPerThread];
 #pragma unroll
         for (int j = 0; j < kColsPerThread; ++j) acc[j] = 0.f;
-        const int n_per = (n_win + kTcPeriod - 1) / kTcPeriod;
+        const int n_per = (n_win + PERIOD - 1) / PERIOD;
         int drained = 0;
         // add accumulator turn q into the registers and hand the accumulator back;
         // the whole warp reads TMEM or none of it does
@@ -497,7 +509,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int s = w % kStagesB, r = w % kRecSlots;
             if (w >= kStagesB && !mbar_wait(&empty_b[s], ((w / kStagesB) - 1) & 1)) ok = false;
             // turn q is complete once window (q+1)P - 1 has left its stage
-            if (drained < n_per && w == (drained + 1) * kTcPeriod + kStagesB - 1) {
+            if (drained < n_per && w == (drained + 1) * PERIOD + kStagesB - 1) {
                 if (!drain(drained)) ok = false;
                 ++drained;
             }
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // undo the two power-of-two scalings (each factor a normal float);
             // a slice of a shared tile leaves its partial sum, in tile
             // coordinates, for k_tc_split_sum
-            const float ir = ok ? ldexpf(1.f, -a.row_exp[rr]) : __int_as_float(0x7fc00000);
+            const float ir = !ok ? __int_as_float(0x7fc00000) : CODES ? a.row_scale[rr] : ldexpf(1.f, -a.row_exp[rr]);
             float* yrow = whole ? a.Y + rr * a.n_seg + s0 : a.part + ((int64_t)jt * kTcM + row) * kTcN;
             const float* bias = whole ? a.bias : nullptr;
             const int c0 = kColsPerThread * half;
@@ -602,6 +614,81 @@ __global__ void k_tc_split_sum(const float* __restrict__ part, int full, int spl
         float y = 0.f;
         for (int k = 0; k < split; ++k) y += part[((int64_t)(tl * split + k) * kTcM + row) * kTcN + col];
         Y[rr * n_seg + sg] = bias ? y + bias[sg] : y;
+    }
+}
+
+// dY with a scale per batch row (that of an 8-bit X's rows).
+struct SrcScaled {
+    SrcF32 d;
+    const float* s;
+    __device__ __forceinline__ float at(int64_t r, int64_t c) const { return d.at(r, c) * __ldg(s + r); }
+};
+// The value whose column sum is db, given x = D.at(r, c).
+template <class Src>
+__device__ __forceinline__ float raw(const Src&, int64_t, int64_t, float x) { return x; }
+__device__ __forceinline__ float raw(const SrcScaled& D, int64_t r, int64_t c, float) { return D.d.at(r, c); }
+
+// Four codes as fp16 (exact), the first in the low half of x.
+__device__ __forceinline__ uint2 codes_f16(uint32_t w, int format) {
+    float2 a, b;
+    q_values4(w, format, a, b);
+    const __half2 lo = __floats2half2_rn(a.x, a.y), hi = __floats2half2_rn(b.x, b.y);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+__device__ __forceinline__ uint32_t code_word(const uint8_t* row, int64_t k, int64_t len, bool words) {
+    if (words) return __ldg(reinterpret_cast<const uint32_t*>(row + k));
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (k + j < len) w |= (uint32_t)__ldg(row + k + j) << (8 * j);
+    return w;
+}
+
+// The dense operand from codes with a scale per row, once per call (one block per
+// row): the codes as fp16 at row stride ks, and the row's largest magnitude and
+// sum of magnitudes into the running maxima that W's segments are checked
+// against.  A row whose scale is not finite is listed for the exact
+// recomputation (a product with a stored zero of a densified tile would reach
+// outputs that none of its entries does).
+__global__ void k_tc_codes(const Q8In q, int64_t ks, __half* __restrict__ dh, int32_t* __restrict__ rows,
+                           uint32_t* __restrict__ fix) {
+    __shared__ float red[2][32];
+    const int64_t r = blockIdx.x, len = q.cols;
+    const int w = threadIdx.x >> 5, nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+    const uint8_t* p = q.codes + r * len;
+    const bool words = len % 4 == 0 && ((uintptr_t)q.codes & 3) == 0;
+    float m = 0.f, sum = 0.f;
+    for (int64_t k = 4 * threadIdx.x; k < len; k += 4 * blockDim.x) {
+        const uint32_t c = code_word(p, k, len, words);
+        float2 a, b;
+        q_values4(c, q.format, a, b);
+        m = fmaxf(fmaxf(m, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+        sum += (fabsf(a.x) + fabsf(a.y)) + (fabsf(b.x) + fabsf(b.y));
+        // (the row stride is a multiple of 8; columns past len are never loaded)
+        *reinterpret_cast<uint2*>(dh + r * ks + k) = codes_f16(c, q.format);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (lane == 0) {
+        red[0][w] = m;
+        red[1][w] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < nw; ++i) {
+            m = fmaxf(m, red[0][i]);
+            sum += red[1][i];
+        }
+        const float s = fabsf(q.scales[r]);
+        if (isfinite(s)) {
+            atomicMax(fix + kFixRowL1, __float_as_uint(s * sum));
+            atomicMax(fix + kFixRowMax, __float_as_uint(s * m));
+        } else {
+            rows[atomicAdd(fix + kFixRows, 1u)] = (int32_t)r;
+        }
     }
 }
 
@@ -757,37 +844,51 @@ struct TcwArgs {
 };
 
 constexpr int kWThreads = kTcBuilders + 64;       // 8 drain warps, a TMA warp, an MMA warp
-constexpr int kWStage = kStageA + kStageB;        // one batch window of A and B
+// One batch window of A and B: two fp16 pieces each; CODES: X is 8-bit codes with a
+// scale per row.  The scale goes into dY (A) and the codes are one exact piece
+// (B), so a window takes two products for three and 56 KB for 80, and a third
+// stage fits.
+template <bool CODES>
+struct WStage {
+    static constexpr int kBytes = kStageA + (CODES ? kPieceB : kStageB);
+    static constexpr int kCount = CODES ? 3 : 2;
+};
 constexpr int kWChunks = kTcN / 32;               // 32-column chunks per block
 constexpr int kWGroups = 32;                      // group slots per block: quarter * kWChunks + chunk
 constexpr int kWScratch = 32 * 33;                // floats per builder warp: one chunk, rows padded
 constexpr int kWUnroll = 4;                       // entries per lane whose loads are in flight together
-constexpr int kWSmem = 2 * kWStage + (kTcBuilders / 32) * kWScratch * 4 + 1024;
+template <bool CODES>
+constexpr int kWSmem = WStage<CODES>::kCount * WStage<CODES>::kBytes + (kTcBuilders / 32) * kWScratch * 4 + 1024;
 static_assert((kTcM / 32) * kWChunks <= kWGroups, "quarters and chunks fit the group slots");
 static_assert(kColsPerThread == 3 * 32, "each builder warp owns three chunks");
-static_assert(kWSmem <= 227 * 1024 - 4096, "stages and scratch exceed shared memory");
+static_assert(kWSmem<false> <= 227 * 1024 - 4096 && kWSmem<true> <= 227 * 1024 - 4096,
+              "stages and scratch exceed shared memory");
 
+template <int PERIOD, bool CODES>
 __global__ void __launch_bounds__(kWThreads, 1)
     k_tc_sddmm(const __grid_constant__ CUtensorMap map_ah, const __grid_constant__ CUtensorMap map_al,
                const __grid_constant__ CUtensorMap map_bh, const __grid_constant__ CUtensorMap map_bl,
                const TcwArgs a) {
     extern __shared__ __align__(1024) unsigned char tc_raw[];
     unsigned char* sm = tc_raw + ((1024 - (smem_u32(tc_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[2], empty[2], accf[2], acce[2], fin;
+    constexpr int S = WStage<CODES>::kCount, kWStage = WStage<CODES>::kBytes;
+    __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int n_win = a.n_win;
-    const int n_per = (n_win + kTcPeriod - 1) / kTcPeriod;
+    const int n_per = (n_win + PERIOD - 1) / PERIOD;
     const int tiles = a.n_ot * a.n_it;
     const int grid = (int)gridDim.x, first = (int)blockIdx.x;
     const int mine = (tiles - first + grid - 1) / grid;   // blocks of this CTA (grid <= tiles)
 
     if (t == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&accf[i], 1);
             mbar_init(&acce[i], kTcBuilders);
         }
@@ -816,8 +917,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 tc_tile_of(first + i * grid, a.n_ot, a.n_it, ot, it);
                 const int y0 = ot * kTcM, x0 = it * kTcN;
                 for (int w = 0; w < n_win; ++w, ++gw) {
-                    const int s = gw & 1;
-                    if (gw >= 2 && !mbar_wait(&empty[s], ((gw >> 1) - 1) & 1)) {
+                    const int s = gw % S;
+                    if (gw >= S && !mbar_wait(&empty[s], ((gw / S) - 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -826,10 +927,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
                     tma_load_2d(st, &map_ah, w * kTcK, y0, &full[s]);
                     tma_load_2d(st + kPieceA, &map_al, w * kTcK, y0, &full[s]);
                     tma_load_2d(st + kStageA, &map_bh, w * kTcK, x0, &full[s]);
-                    tma_load_2d(st + kStageA + kPieceB, &map_bl, w * kTcK, x0, &full[s]);
+                    if (!CODES) tma_load_2d(st + kStageA + kPieceB, &map_bl, w * kTcK, x0, &full[s]);
                 }
             }
-            if (!ok) drain_ring(full, 2, gw);
+            if (!ok) drain_ring(full, S, gw);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -838,10 +939,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
             int gw = 0;
             for (int i = 0; i < mine && ok; ++i) {
                 for (int w = 0; w < n_win; ++w, ++gw) {
-                    const int s = gw & 1;
-                    const int q = i * n_per + w / kTcPeriod, ab = q & 1;   // accumulator turn
-                    const bool turn0 = (w % kTcPeriod) == 0;
-                    if (!mbar_wait(&full[s], (gw >> 1) & 1) ||
+                    const int s = gw % S;
+                    const int q = i * n_per + w / PERIOD, ab = q & 1;   // accumulator turn
+                    const bool turn0 = (w % PERIOD) == 0;
+                    if (!mbar_wait(&full[s], (gw / S) & 1) ||
                         (turn0 && q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1))) {
                         ok = false;
                         break;
@@ -854,11 +955,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
                     for (int kk = 0; kk < kTcK / 16; ++kk) {
                         const uint32_t o = 32 * kk;
                         mma_f16(d, desc_sw128(ah + o), desc_sw128(bh + o), (turn0 && kk == 0) ? 0u : 1u);
-                        mma_f16(d, desc_sw128(ah + o), desc_sw128(bl + o), 1u);
+                        if (!CODES) mma_f16(d, desc_sw128(ah + o), desc_sw128(bl + o), 1u);
                         mma_f16(d, desc_sw128(al + o), desc_sw128(bh + o), 1u);
                     }
-                    if (gw + 2 < total) mma_commit(&empty[s]);
-                    if ((w % kTcPeriod) == kTcPeriod - 1 || w == n_win - 1) mma_commit(&accf[ab]);
+                    if (gw + S < total) mma_commit(&empty[s]);
+                    if ((w % PERIOD) == PERIOD - 1 || w == n_win - 1) mma_commit(&accf[ab]);
                 }
             }
             mma_commit(&fin);
@@ -868,7 +969,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     } else {
         const int lq = warp & 3, half = warp >> 2;
         const int row = 32 * lq + lane;
-        float* scr = reinterpret_cast<float*>(sm + 2 * kWStage) + warp * kWScratch;
+        float* scr = reinterpret_cast<float*>(sm + S * kWStage) + warp * kWScratch;
         // false once one of this warp's waits has run out (the same in every
         // lane): from then on its entries get NaN, so none is left stale
         bool wok = true;
@@ -1001,13 +1102,13 @@ __global__ void __launch_bounds__(256) k_tc_colstats(const Src D, int64_t rows, 
             for (int64_t r = g * 32; r < r1; ++r) {
                 const float x = D.at(r, col);
                 const float ax = fabsf(x);
+                if (SUM) part += raw(D, r, col, x);
                 if (isfinite(ax)) {
                     m = fmaxf(m, ax);
                     ab += ax;
                 } else {
                     nf = 1.f;
                 }
-                if (SUM) part += x;
             }
             if (SUM) tot += part;
         }
@@ -1094,6 +1195,146 @@ __global__ void k_tc_tsplit(const Src D, int64_t rows, int64_t n, const int32_t*
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n_tiny += __shfl_xor_sync(0xffffffffu, n_tiny, o);
         if (tx == 0 && n_tiny) atomicAdd(code + c, 2 * n_tiny);
+    }
+}
+
+// The codes of rows [0, rows) transposed as fp16: oh[c * bs + r], exact, so the
+// columns need no scale: their exponents and flags are zero.  The bounds on a
+// column's sum of magnitudes and on a magnitude are the format's.  Tiles of 64
+// rows x 128 columns, two rows per store.
+__global__ void __launch_bounds__(256) k_tc_tcodes(const Q8In q, int64_t rows, int64_t bs, __half* __restrict__ oh,
+                                                   int32_t* __restrict__ e_out, int32_t* __restrict__ code,
+                                                   uint32_t* __restrict__ l1max) {
+    __shared__ __half tile[64][134];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;   // 32 x 8
+    const int64_t n = q.cols, c0 = (int64_t)blockIdx.x * 128, r0 = (int64_t)blockIdx.y * 64;
+    const bool words = n % 4 == 0 && ((uintptr_t)q.codes & 3) == 0;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + ty + 8 * i, c = c0 + 4 * tx;
+        w[i] = r < rows && c < n ? code_word(q.codes + r * n, c, n, words) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint2 h = codes_f16(w[i], q.format);
+        uint32_t* d = reinterpret_cast<uint32_t*>(&tile[ty + 8 * i][4 * tx]);
+        d[0] = h.x;
+        d[1] = h.y;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t c = c0 + ty + 8 * i, r = r0 + 2 * tx;
+        // (bs is a multiple of 8: a pair past the last row stays in the column's space)
+        if (c < n && r < rows)
+            *reinterpret_cast<__half2*>(oh + c * bs + r) = __halves2half2(tile[2 * tx][ty + 8 * i], tile[2 * tx + 1][ty + 8 * i]);
+    }
+    if (blockIdx.y == 0 && threadIdx.x < 128 && c0 + threadIdx.x < n) {
+        e_out[c0 + threadIdx.x] = 0;
+        code[c0 + threadIdx.x] = 0;
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+        const float top = q.format == SNK_Q8_INT8 ? 127.f : 448.f;
+        l1max[0] = __float_as_uint(top * (float)rows);
+        l1max[1] = __float_as_uint(top);
+    }
+}
+
+// k_tc_colstats and k_tc_tsplit of D[r][c] * s[r] in one pass, 32 columns per
+// block, for batches whose 32 columns fit shared memory ([rows][33] floats): the
+// values are read once (b = 512, 10000 columns: 32 us for the two kernels).  db
+// is the plain column sum of D.
+constexpr int64_t kColRows = 1536;
+__global__ void __launch_bounds__(512) k_tc_colsplit(const float* __restrict__ D, const float* __restrict__ s, int rows,
+                                                     int64_t n, int64_t bs, int32_t* __restrict__ e_out,
+                                                     int32_t* __restrict__ code, uint32_t* __restrict__ l1max,
+                                                     float* __restrict__ sum, int accumulate, __half* __restrict__ oh,
+                                                     __half* __restrict__ ol) {
+    extern __shared__ float cols[];   // [rows][33]
+    __shared__ float red[4][16][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t c0 = (int64_t)blockIdx.x * 32, col = c0 + lane;
+    float m = 0.f, ab = 0.f, nf = 0.f, tot = 0.f;
+    for (int g = 8 * w; g < rows; g += 128) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = g + i < rows && col < n ? __ldg(D + (int64_t)(g + i) * n + col) : 0.f;
+        float part = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (g + i < rows) {
+                part += x[i];
+                const float v = x[i] * __ldg(s + g + i), av = fabsf(v);
+                if (isfinite(av)) {
+                    m = fmaxf(m, av);
+                    ab += av;
+                } else {
+                    nf = 1.f;
+                }
+                cols[(g + i) * 33 + lane] = v;
+            }
+        }
+        tot += part;
+    }
+    red[0][w][lane] = m;
+    red[1][w][lane] = ab;
+    red[2][w][lane] = nf;
+    red[3][w][lane] = tot;
+    __syncthreads();
+    // every warp reduces its columns' statistics in warp order
+    m = 0.f;
+    ab = 0.f;
+    nf = 0.f;
+    tot = 0.f;
+    for (int i = 0; i < 16; ++i) {
+        m = fmaxf(m, red[0][i][lane]);
+        ab += red[1][i][lane];
+        nf = fmaxf(nf, red[2][i][lane]);
+        tot += red[3][i][lane];
+    }
+    const int e = tc_exponent(m);
+    // column ty of the block per warp at a time: 32 rows per store, two per lane
+    for (int c = w; c < 32; c += 16) {
+        const int64_t cc = c0 + c;
+        const int ec = __shfl_sync(0xffffffffu, e, c);
+        const float pw = ldexpf(1.f, ec), tiny = ldexpf(0.125f, -ec);
+        int n_tiny = 0;
+        if (cc < n) {
+            for (int r = 2 * lane; r < rows; r += 64) {
+                float v[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float x = r + k < rows ? cols[(r + k) * 33 + c] : 0.f;
+                    const float ax = fabsf(x);
+                    n_tiny += (ax > 0.f && ax < tiny) ? 1 : 0;
+                    v[k] = isfinite(x) ? x * pw : 0.f;
+                }
+                __half h0, h1, l0, l1;
+                split16(v[0], h0, l0);
+                split16(v[1], h1, l1);
+                *reinterpret_cast<__half2*>(oh + cc * bs + r) = __halves2half2(h0, h1);
+                *reinterpret_cast<__half2*>(ol + cc * bs + r) = __halves2half2(l0, l1);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n_tiny += __shfl_xor_sync(0xffffffffu, n_tiny, o);
+        if (lane == c && cc < n) {
+            e_out[cc] = e;
+            code[cc] = (nf > 0.f ? 1 : 0) | (n_tiny << 1);
+            if (sum) sum[cc] = accumulate ? sum[cc] + tot : tot;
+        }
+    }
+    if (w == 0) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            ab = fmaxf(ab, __shfl_xor_sync(0xffffffffu, ab, o));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        if (lane == 0) {
+            atomicMax(l1max, __float_as_uint(ab));
+            atomicMax(l1max + 1, __float_as_uint(m));
+        }
     }
 }
 
@@ -1508,6 +1749,47 @@ int ensure_tc(Layer* L) {
 
 }  // namespace
 
+// The scale of each row of an operand whose rows have one; null otherwise.
+static const float* codes_scale(const SrcF32&) { return nullptr; }
+static const float* codes_scale(const SrcQ8& D) { return D.q.gshift == 31 ? D.q.scales : nullptr; }
+static void launch_codes(const SrcF32&, int, int64_t, __half*, int32_t*, uint32_t*, cudaStream_t) {}
+static void launch_codes(const SrcQ8& D, int rows, int64_t ks, __half* dh, int32_t* list, uint32_t* fix,
+                         cudaStream_t s) {
+    k_tc_codes<<<rows, 256, 0, s>>>(D.q, ks, dh, list, fix);
+}
+// The weight gradient's operands from dY and an 8-bit X with a scale per row, for
+// batch rows [0, rows): the pieces of (s dY)^T, the codes of X^T, and their
+// statistics.
+static int split_codes(TcState*, const SrcF32&, const SrcF32&, int64_t, int64_t, float*, int, __half*, __half*, __half*,
+                       cudaStream_t) {
+    return SNK_ERR_ARG;   // (an fp32 X has no codes)
+}
+static int split_codes(TcState* T, const SrcQ8& X, const SrcF32& dY, int64_t rows, int64_t bs, float* db, int acc,
+                       __half* ah, __half* al, __half* bh, cudaStream_t s) {
+    const unsigned gy = (unsigned)ceil_div(dY.cols, 32);
+    uint32_t* dy_max = T->fix + kFixDyL1;
+    if (rows <= kColRows) {
+        const int smem = (int)rows * 33 * (int)sizeof(float);
+        if (smem > 40 * 1024 &&
+            cudaFuncSetAttribute(k_tc_colsplit, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return SNK_ERR_CUDA;
+        k_tc_colsplit<<<gy, 512, smem, s>>>(dY.p, X.q.scales, (int)rows, dY.cols, bs, T->seg_exp, T->seg_code, dy_max, db,
+                                            acc, ah, al);
+    } else {
+        const SrcScaled dYs{dY, X.q.scales};
+        if (db)
+            k_tc_colstats<true, SrcScaled><<<gy, 256, 0, s>>>(dYs, rows, dY.cols, T->seg_exp, T->seg_code, dy_max, db, acc);
+        else
+            k_tc_colstats<false, SrcScaled><<<gy, 256, 0, s>>>(dYs, rows, dY.cols, T->seg_exp, T->seg_code, dy_max,
+                                                              nullptr, 0);
+        k_tc_tsplit<<<dim3(gy, (unsigned)ceil_div(rows, 32)), dim3(32, 8), 0, s>>>(dYs, rows, dY.cols, T->seg_exp, bs, ah,
+                                                                                al, T->seg_code);
+    }
+    k_tc_tcodes<<<dim3((unsigned)ceil_div(X.q.cols, 128), (unsigned)ceil_div(rows, 64)), 256, 0, s>>>(
+        X.q, rows, bs, bh, T->col_exp, T->col_code, T->fix + kFixXL1);
+    return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
+}
+
 template <class Src>
 int run_tc(Layer* L, bool columns, const Src& D, int64_t b, const float* bias, float* Y, cudaStream_t s) {
     int st0 = ensure_tc(L);
@@ -1529,7 +1811,12 @@ int run_tc(Layer* L, bool columns, const Src& D, int64_t b, const float* bias, f
     k_tc_values<<<grid_for(L->nnz, TH, L->num_sms), TH, 0, s>>>(L->v, V.perm_t, columns ? L->c : L->r,
                                                                 T->seg_exp, L->nnz, T->hl, T->seg_code);
     k_tc_seg_cand<<<grid_for(n_seg, TH, L->num_sms), TH, 0, s>>>(T->seg_code, n_seg, T->cand, T->fix);
-    if (cudaFuncSetAttribute(k_tc_spmm, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem) != cudaSuccess)
+    // an 8-bit operand with a scale per row is multiplied as its codes
+    const float* row_scale = codes_scale(D);
+    auto fn = row_scale                       ? k_tc_spmm<kCodesPeriod, true>
+              : std::is_same<Src, SrcQ8>::value ? k_tc_spmm<kQPeriod, false>
+                                              : k_tc_spmm<kTcPeriod, false>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem) != cudaSuccess)
         return SNK_ERR_CUDA;
     const bool vec = D.rows_of_4();
     // the entries of the segments, for the exact recomputation of flagged outputs
@@ -1540,7 +1827,9 @@ int run_tc(Layer* L, bool columns, const Src& D, int64_t b, const float* bias, f
         const Src Dc = D.from_row(c0);
         if (c0 > 0 && cudaMemsetAsync(T->fix + kFixRows, 0, sizeof(uint32_t), s) != cudaSuccess)
             return SNK_ERR_CUDA;
-        if (vec)
+        if (row_scale)
+            launch_codes(Dc, bc, T->k_stride, T->dh, T->frows, T->fix, s);
+        else if (vec)
             k_tc_split<true, Src><<<bc, TH, 0, s>>>(Dc, k_len, T->k_stride, T->row_exp, T->dh, T->dl, T->frows,
                                                T->fix);
         else
@@ -1553,6 +1842,7 @@ int run_tc(Layer* L, bool columns, const Src& D, int64_t b, const float* bias, f
         a.b = bc;
         a.K_len = k_len;
         a.row_exp = T->row_exp;
+        a.row_scale = row_scale ? row_scale + c0 : nullptr;
         a.off = V.off;
         a.hl = T->hl;
         // dense windows are cleared whole, sparse ones entry by entry
@@ -1576,7 +1866,7 @@ int run_tc(Layer* L, bool columns, const Src& D, int64_t b, const float* bias, f
             a.full = tiles;
             a.split = 1;
         }
-        k_tc_spmm<<<a.full + (tiles - a.full) * a.split, kTcThreads, kTcSmem, s>>>(mh, ml, a);
+        fn<<<a.full + (tiles - a.full) * a.split, kTcThreads, kTcSmem, s>>>(mh, ml, a);
         if (a.full < tiles)
             k_tc_split_sum<<<dim3((unsigned)(tiles - a.full), kTcM * kTcN / 256), 256, 0, s>>>(
                 T->part, a.full, a.split, a.n_mt, a.n_nt, bc, n_seg, bias, Y + c0 * n_seg);
@@ -1602,7 +1892,13 @@ int run_tc_sddmm(Layer* L, const Src& X, const float* dY, int64_t b, float* dW, 
         if (st != SNK_OK) return st;
         V.version = L->topology_version;
     }
-    if (cudaFuncSetAttribute(k_tc_sddmm, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem) != cudaSuccess)
+    // an 8-bit X with a scale per row is multiplied as its codes, the scale in dY
+    const float* row_scale = codes_scale(X);
+    const int smem = row_scale ? kWSmem<true> : kWSmem<false>;
+    auto fn = row_scale                       ? k_tc_sddmm<kCodesPeriod, true>
+              : std::is_same<Src, SrcQ8>::value ? k_tc_sddmm<kQPeriod, false>
+                                              : k_tc_sddmm<kTcPeriod, false>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return SNK_ERR_CUDA;
     const int64_t out_f = L->out_f, in_f = L->in_f;
     if (cudaMemsetAsync(T->fix, 0, kFixWords * sizeof(uint32_t), s) != cudaSuccess ||
@@ -1619,23 +1915,28 @@ int run_tc_sddmm(Layer* L, const Src& X, const float* dY, int64_t b, float* dW, 
         const int acc = c0 > 0;
         if (c0 > 0 && cudaMemsetAsync(T->fix + kFixDyL1, 0, 4 * sizeof(uint32_t), s) != cudaSuccess)
             return SNK_ERR_CUDA;
-        if (db)
-            k_tc_colstats<true, SrcF32><<<(unsigned)ceil_div(out_f, 32), 256, 0, s>>>(
-                dYc, bc, out_f, T->seg_exp, T->seg_code, T->fix + kFixDyL1, db, acc);
-        else
-            k_tc_colstats<false, SrcF32><<<(unsigned)ceil_div(out_f, 32), 256, 0, s>>>(
-                dYc, bc, out_f, T->seg_exp, T->seg_code, T->fix + kFixDyL1, nullptr, 0);
-        k_tc_colstats<false, Src><<<(unsigned)ceil_div(in_f, 32), 256, 0, s>>>(Xc, bc, in_f, T->col_exp, T->col_code,
-                                                                          T->fix + kFixXL1, nullptr, 0);
         __half* ah = T->dh;
         __half* al = T->dl;
         __half* bh = T->dh + out_f * bs;
         __half* bl = T->dl + out_f * bs;
-        const dim3 tb(32, 8);
-        k_tc_tsplit<<<dim3((unsigned)ceil_div(out_f, 32), (unsigned)ceil_div(bc, 32)), tb, 0, s>>>(
-            dYc, bc, out_f, T->seg_exp, bs, ah, al, T->seg_code);
-        k_tc_tsplit<<<dim3((unsigned)ceil_div(in_f, 32), (unsigned)ceil_div(bc, 32)), tb, 0, s>>>(
-            Xc, bc, in_f, T->col_exp, bs, bh, bl, T->col_code);
+        if (row_scale) {
+            st = split_codes(T, Xc, dYc, bc, bs, db, acc, ah, al, bh, s);
+            if (st != SNK_OK) return st;
+        } else {
+            if (db)
+                k_tc_colstats<true, SrcF32><<<(unsigned)ceil_div(out_f, 32), 256, 0, s>>>(
+                    dYc, bc, out_f, T->seg_exp, T->seg_code, T->fix + kFixDyL1, db, acc);
+            else
+                k_tc_colstats<false, SrcF32><<<(unsigned)ceil_div(out_f, 32), 256, 0, s>>>(
+                    dYc, bc, out_f, T->seg_exp, T->seg_code, T->fix + kFixDyL1, nullptr, 0);
+            k_tc_colstats<false, Src><<<(unsigned)ceil_div(in_f, 32), 256, 0, s>>>(
+                Xc, bc, in_f, T->col_exp, T->col_code, T->fix + kFixXL1, nullptr, 0);
+            const dim3 tb(32, 8);
+            k_tc_tsplit<<<dim3((unsigned)ceil_div(out_f, 32), (unsigned)ceil_div(bc, 32)), tb, 0, s>>>(
+                dYc, bc, out_f, T->seg_exp, bs, ah, al, T->seg_code);
+            k_tc_tsplit<<<dim3((unsigned)ceil_div(in_f, 32), (unsigned)ceil_div(bc, 32)), tb, 0, s>>>(
+                Xc, bc, in_f, T->col_exp, bs, bh, bl, T->col_code);
+        }
         k_tc_dw_decide<<<grid_for(out_f + in_f, 256, L->num_sms), 256, 0, s>>>(
             T->seg_exp, T->seg_code, T->col_exp, T->col_code, out_f, in_f, (float)ceil_div(b, chunk),
             T->dw_flag, T->dw_list, T->fix);
@@ -1659,7 +1960,7 @@ int run_tc_sddmm(Layer* L, const Src& X, const float* dY, int64_t b, float* dW, 
         a.status = L->status;
         // persistent: one CTA per SM, each taking every grid-th block
         const int grid = (int)std::min<int64_t>((int64_t)a.n_ot * a.n_it, L->num_sms);
-        k_tc_sddmm<<<grid, kWThreads, kWSmem, s>>>(mah, mal, mbh, mbl, a);
+        fn<<<grid, kWThreads, smem, s>>>(mah, mal, mbh, mbl, a);
     }
     if (cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
     // rows and columns of W flagged by any chunk: their entries again, over the whole batch
