@@ -77,28 +77,29 @@ struct PackArgs {
 // the registers of more cost more warps than their loads in flight gain (GELU's
 // gradient at 16384 x 3072 takes 70 us with 1, 79 with 2, 115 with 4).
 struct FlatTile {
-    int64_t row;   // first element of the row
-    int64_t c0;
-    uint32_t r;
+    int64_t e0;    // the tile's first element
+    int64_t s0;    // its first scale
     int left;
 };
-__device__ __forceinline__ bool flat_tile(uint32_t tiles, uint32_t tpr, int64_t cols, FlatTile& t) {
-    const uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5);
-    t.r = tpr == tiles ? 0 : i / tpr;
-    t.row = (int64_t)t.r * cols;
-    t.c0 = (int64_t)(i - t.r * tpr) * kQTile;
-    t.left = (int)min((int64_t)kQTile, cols - t.c0);
-    return i < tiles;
+// ROWS false: the matrix is one row (its rows are whole groups).
+template <bool ROWS>
+__device__ __forceinline__ FlatTile flat_tile(uint32_t i, uint32_t tpr, int64_t cols, int64_t n_groups, int gshift) {
+    if constexpr (!ROWS) {
+        const int64_t e0 = (int64_t)i * kQTile, left = cols - e0;
+        return FlatTile{e0, gshift == 31 ? 0 : (int64_t)i << (8 - gshift), (int)min((int64_t)kQTile, left)};
+    }
+    const uint32_t r = i / tpr, c0 = (i - r * tpr) * kQTile;
+    return FlatTile{(int64_t)r * cols + c0, (int64_t)r * n_groups + (c0 >> gshift), min(kQTile, (int)cols - (int)c0)};
 }
 
 // Groups of 32..256 columns: tiles are independent of one another.
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool ROWS>
 __global__ void __launch_bounds__(256) k_pack_groups(const PackArgs a, uint32_t tiles, uint32_t tpr) {
-    FlatTile t;
-    if (!flat_tile(tiles, tpr, a.cols, t)) return;
+    const uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (i >= tiles) return;
     const int lane = threadIdx.x & 31;
-    const int64_t e = t.row + t.c0 + lane_col<VEC>(lane);
-    const int64_t sc = (int64_t)t.r * a.out.n_groups + (t.c0 >> a.out.gshift);
+    const FlatTile t = flat_tile<ROWS>(i, tpr, a.cols, a.out.n_groups, a.out.gshift);
+    const int64_t e = t.e0 + lane_col<VEC>(lane), sc = t.s0;
     F8 v;
     load_tile<T, VEC>((const T*)a.x + e, t.left, lane, v);
     if (a.keep.codes)
@@ -177,16 +178,16 @@ __global__ void __launch_bounds__(1024) k_pack_long(const PackArgs a) {
 
 // unpack (GRAD false: x = scale * code) and GELU's gradient (GRAD: x = da
 // times the slope at scale * code).
-template <typename T, bool VEC, bool GRAD>
+template <typename T, bool VEC, bool GRAD, bool ROWS>
 __global__ void __launch_bounds__(256) k_unpack(const Q8In q, const T* da, T* x, uint32_t tiles, uint32_t tpr) {
-    FlatTile t;
-    if (!flat_tile(tiles, tpr, q.cols, t)) return;
+    const uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (i >= tiles) return;
     const int lane = threadIdx.x & 31;
-    const int64_t e = t.row + t.c0 + lane_col<VEC>(lane);
+    const FlatTile t = flat_tile<ROWS>(i, tpr, q.cols, q.n_groups, q.gshift);
+    const int64_t e = t.e0 + lane_col<VEC>(lane);
     F8 v, g;
     if constexpr (GRAD) load_tile<T, VEC>(da + e, t.left, lane, g);
-    load_values<VEC>(q.format, q.gshift, q.codes + e, q.scales + (int64_t)t.r * q.n_groups + (t.c0 >> q.gshift), t.left,
-                     lane, v);
+    load_values<VEC>(q.format, q.gshift, q.codes + e, q.scales + t.s0, t.left, lane, v);
     if constexpr (GRAD) {
         gelu_slope(v);
         v.mul(g);
@@ -220,7 +221,9 @@ int launch_pack(const PackArgs& a, int group, cudaStream_t s) {
     if (group != 0) {
         const int64_t tiles = a.rows * tpr;
         if (tiles > INT32_MAX) return SNK_ERR_LIMIT;
-        k_pack_groups<T, VEC><<<(unsigned)ceil_div(tiles, 8), 256, 0, s>>>(a, (uint32_t)tiles, (uint32_t)tpr);
+        const unsigned grid = (unsigned)ceil_div(tiles, 8);
+        if (a.rows == 1) k_pack_groups<T, VEC, false><<<grid, 256, 0, s>>>(a, (uint32_t)tiles, (uint32_t)tpr);
+        else k_pack_groups<T, VEC, true><<<grid, 256, 0, s>>>(a, (uint32_t)tiles, (uint32_t)tpr);
     } else if (tpr <= kRegisterTiles) {
         const RowShape f = row_shape(tpr, a.rows <= 256 ? 1 : 4);
         const unsigned grid = (unsigned)ceil_div(a.rows, f.slots()), threads = f.threads();
@@ -272,10 +275,9 @@ int launch_unpack(Q8In q, int64_t rows, int group, const void* da, void* x, cuda
     const uintptr_t al = sizeof(T) == 4 ? 32 : 16;
     const bool vec = q.cols % 8 == 0 && q8_aligned(q.codes, 8) && q8_aligned(x, al) && q8_aligned(da, al);
     const unsigned grid = (unsigned)ceil_div(tiles, 8);
-    if (vec)
-        k_unpack<T, true, GRAD><<<grid, 256, 0, s>>>(q, (const T*)da, (T*)x, (uint32_t)tiles, (uint32_t)tpr);
-    else
-        k_unpack<T, false, GRAD><<<grid, 256, 0, s>>>(q, (const T*)da, (T*)x, (uint32_t)tiles, (uint32_t)tpr);
+    auto fn = vec ? (rows == 1 ? k_unpack<T, true, GRAD, false> : k_unpack<T, true, GRAD, true>)
+                  : (rows == 1 ? k_unpack<T, false, GRAD, false> : k_unpack<T, false, GRAD, true>);
+    fn<<<grid, 256, 0, s>>>(q, (const T*)da, (T*)x, (uint32_t)tiles, (uint32_t)tpr);
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
 
