@@ -403,25 +403,33 @@ __global__ void __launch_bounds__(1024) k_norm_grad_long(const NormGradArgs a) {
     }
 }
 
-// dgain[c] = the blocks' partial sums of column c: 32 threads take every 32nd
-// of them, a tree adds the 32.
+// dgain[c] = the blocks' partial sums of column c.  C columns per block: 1024 / C
+// threads share a column's n sums, a shuffle tree adds theirs.  8 columns (one
+// sector) where there are many sums per column, so that a thread has few loads
+// one after another; else 32.
+template <int C>
 __global__ void __launch_bounds__(1024) k_dgain_sum(const float* __restrict__ part, int n, int64_t cols,
                                                     float* __restrict__ dgain) {
-    __shared__ float sm[32][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + x;
+    constexpr int Y = 1024 / C;
+    __shared__ float sm[Y][C + 1];
+    const int x = threadIdx.x % C, y = threadIdx.x / C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * C + x;
     float t = 0.f;
     if (c < cols) {
-#pragma unroll 8
-        for (int i = y; i < n; i += 32) t += part[(int64_t)i * cols + c];
+#pragma unroll 10
+        for (int i = y; i < n; i += Y) t += part[(int64_t)i * cols + c];
     }
     sm[y][x] = t;
     __syncthreads();
-    t = sm[x][y];
+    if (warp < C) {
+        t = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const int64_t cc = (int64_t)blockIdx.x * 32 + y;
-    if (x == 0 && cc < cols) dgain[cc] = t;
+        for (int k = lane; k < Y; k += 32) t += sm[k][warp];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        const int64_t cw = (int64_t)blockIdx.x * C + warp;
+        if (lane == 0 && cw < cols) dgain[cw] = t;
+    }
 }
 
 template <typename F>
@@ -531,7 +539,8 @@ int launch_norm_grad(const NormGradArgs& a, float* dgain, cudaStream_t s) {
     }
     if (st != SNK_OK || cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
     if (dgain) {
-        k_dgain_sum<<<(unsigned)ceil_div(a.cols, 32), 1024, 0, s>>>(a.part, (int)grid, a.cols, dgain);
+        if (grid > 320) k_dgain_sum<8><<<(unsigned)ceil_div(a.cols, 8), 1024, 0, s>>>(a.part, (int)grid, a.cols, dgain);
+        else k_dgain_sum<32><<<(unsigned)ceil_div(a.cols, 32), 1024, 0, s>>>(a.part, (int)grid, a.cols, dgain);
         if (cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
     }
     return SNK_OK;
