@@ -307,6 +307,10 @@ int launch_forward(Layer* L, const float* X, const Q8In* q, int64_t b, const flo
 int launch_backward_input(Layer* L, const float* dY, int64_t b, float* dX, cudaStream_t s);
 int launch_backward_weight(Layer* L, const float* X, const Q8In* q, const float* dY, int64_t b, float* dW,
                            float* db, cudaStream_t s);
+// snk_q8_light.cu: the products of a layer with few entries and an 8-bit X.
+bool light_layer(const Layer* L, const Q8In& q, int64_t b, bool weight);
+int light_forward(Layer* L, const Q8In& q, int64_t b, const float* bias, float* Y, cudaStream_t s);
+int light_weight(Layer* L, const Q8In& q, const float* dY, int64_t b, float* dW, float* db, cudaStream_t s);
 // snk_q8.cu: rows [0, b) of an 8-bit matrix as fp32 [b, cols], and transposed
 // into dst[cols][bp] (zero columns from b on; bp a power of two up to 64).
 int launch_q8_rows(const Q8In& q, int64_t b, float* dst, cudaStream_t s);

@@ -68,6 +68,36 @@ def test_batch_tiles(torch, fmt, group, b):
     check(torch, lay, b, fmt, group, 203 + b)
 
 
+@pytest.mark.parametrize("fmt,group", [("int8", 0), ("e4m3", 0), ("int8", 32), ("e4m3", 128)])
+@pytest.mark.parametrize("b", [33, 64, 65])
+def test_wide_batch_tiles(torch, monkeypatch, fmt, group, b):
+    """The 64-row tiles, which a layer of few entries leaves by itself at b > 32."""
+    monkeypatch.setenv("SNK_LARGE_BATCH", "off")
+    check(torch, synth.make_layer(300, 203, 90, 0.1, 201, 202), b, fmt, group, 203 + b)
+    check(torch, synth.make_layer(96, 1003, 95, 0.1, 204, 205), b, fmt, group, 206 + b)
+
+
+@pytest.mark.parametrize("fmt,group", [("int8", 0), ("e4m3", 0), ("int8", 32), ("e4m3", 64), ("int8", 256)])
+@pytest.mark.parametrize("b", [33, 127, 192, 193, 256, 257, 400])
+def test_few_entries(torch, fmt, group, b):
+    """Layers of few entries at b > 32: passes of 256 (192) batch rows, rows of W
+    without entries, long rows, widths that are no whole words."""
+    check(torch, synth.make_layer(300, 203, 90, 0.1, 301, 302), b, fmt, group, 303 + b)
+    check(torch, synth.make_layer(700, 64, 99, 0.1, 304, 305), b, fmt, group, 306 + b, bias=False)
+    check(torch, synth.make_layer(97, 1240, 95, 0.1, 307, 308, zipf_s=1.2), b, fmt, group, 309 + b)
+
+
+def test_few_entries_and_spoiled_rows(torch):
+    def spoil(x):
+        x[3] = 0
+        x[5, 70] = np.inf
+        x[200, 3] = np.nan
+        x[7] *= np.float32(1e-20)
+
+    for fmt, group in (("int8", 0), ("e4m3", 32)):
+        check(torch, synth.make_layer(150, 200, 99, 0.1, 311, 312), 300, fmt, group, 313, spoil)
+
+
 @pytest.mark.parametrize("shape", [(1, 1), (1, 700), (700, 1), (97, 1003), (64, 64)])
 def test_odd_shapes(torch, shape):
     out_f, in_f = shape
