@@ -25,6 +25,7 @@ SNK_Q8_INT8, SNK_Q8_E4M3 = 0, 1
 _lock = threading.Lock()
 _lib = None
 _raw_stream = None
+_ops = None
 
 
 class SnkError(RuntimeError):
@@ -89,6 +90,21 @@ def lib():
             getattr(L, name).restype = I
         _lib = L
         return L
+
+
+def ops():
+    """The native module that makes the 8-bit activation calls on torch tensors
+    (csrc/q8_ops.cpp), bound to the same library."""
+    global _ops
+    if _ops is None:
+        lib()
+        try:
+            from . import _q8ops
+        except ImportError as e:
+            raise RuntimeError("_q8ops.so is not built; run sparse_linear_layer_gb300.build.build() first") from e
+        _q8ops.load(LIB_PATH, SnkError)
+        _ops = _q8ops
+    return _ops
 
 
 def declared_symbols():
@@ -348,24 +364,13 @@ class SparseLinear:
 
     def forward_q8(self, X, bias=None, out=None, stream=None):
         """forward() with X an 8-bit matrix (q8.Q8Tensor, [batch, in])."""
-        import torch
-        if X.cols != self.in_features:
-            raise ValueError(f"X has {self.in_features} columns: got {tuple(X.shape)}")
-        Y = out if out is not None else torch.empty((X.rows, self.out_features),
-                                                    dtype=torch.float32, device=X.codes.device)
-        snk_forward_q8(self.handle, X.codes, X.scales, X.format_id, X.group, X.rows, bias, Y, stream)
-        return Y
+        return ops().forward(self.handle, self.out_features, self.in_features, X.codes, X.scales, X.group, bias, out,
+                             stream)
 
     def backward_weight_q8(self, X, dY, with_bias: bool = False, out=None, stream=None):
         """backward_weight() with X an 8-bit matrix (q8.Q8Tensor, [batch, in])."""
-        import torch
-        if X.cols != self.in_features:
-            raise ValueError(f"X has {self.in_features} columns: got {tuple(X.shape)}")
-        if dY.dtype != torch.float32 or dY.numel() != X.rows * self.out_features:
-            raise ValueError(f"dY is float32 [{X.rows}, {self.out_features}]: got {dY.dtype} {tuple(dY.shape)}")
-        dW = out if out is not None else torch.empty_like(self.values)
-        db = torch.empty(self.out_features, dtype=torch.float32, device=dY.device) if with_bias else None
-        snk_backward_weight_q8(self.handle, X.codes, X.scales, X.format_id, X.group, dY, X.rows, dW, db, stream)
+        dW, db = ops().backward_weight(self.handle, self.out_features, self.in_features, self.nnz, X.codes, X.scales,
+                                       X.group, dY, with_bias, out, stream)
         return (dW, db) if with_bias else dW
 
     def prune_regrow(self, zeta: float, seed: int, stream=None):

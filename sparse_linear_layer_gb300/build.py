@@ -2,7 +2,8 @@
 
 Each .cu file compiles in its own nvcc process, in parallel; the objects are
 linked into ``sparse_linear_layer_gb300/libsnk.so`` with the CUDA runtime
-linked statically, so the library only needs the driver at run time.
+linked statically, so the library only needs the driver at run time.  Beside it
+g++ builds ``_q8ops.so``, the Python module that calls it on torch tensors.
 """
 from __future__ import annotations
 
@@ -19,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsnk.so")
+OPS_SRC = os.path.join(CSRC, "q8_ops.cpp")
+OPS = os.path.join(PKG, "_q8ops.so")   # the torch side of the 8-bit activation calls
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{INCLUDE}", f"-I{CSRC}",
          "--expt-relaxed-constexpr"]
@@ -40,10 +43,11 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(OPS):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t, o = os.path.getmtime(LIB), os.path.getmtime(OPS)
+    return (all(os.path.getmtime(p) <= t for p in _deps()) and
+            max(os.path.getmtime(OPS_SRC), os.path.getmtime(os.path.join(INCLUDE, "snk.h"))) <= o)
 
 
 def _compile(src: str, verbose: bool, obj_dir: str, extra) -> str:
@@ -57,6 +61,25 @@ def _compile(src: str, verbose: bool, obj_dir: str, extra) -> str:
     if verbose:
         sys.stderr.write(r.stderr)
     return obj
+
+
+def _build_ops() -> None:
+    """_q8ops.so: g++ against torch's headers (no torch build tools)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"), INCLUDE]
+    tmp = OPS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in inc), OPS_SRC,
+           "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {OPS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPS)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str | None = None) -> str:
@@ -80,8 +103,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str
 
 def _build_locked(verbose: bool, extra, lib: str, obj_dir: str) -> str:
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        ops = ex.submit(_build_ops) if lib == LIB else None
         objs = list(ex.map(lambda s: _compile(s, verbose, obj_dir, extra), srcs))
+        if ops is not None:
+            ops.result()
     tmp = lib + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
