@@ -465,7 +465,8 @@ int snk_rmsnorm_q8(const void* x, const void* residual, int dtype, const float* 
  * NULL for none) that of `total` on its other path; dx is the gradient of x
  * and of residual alike.  dx may be dtotal or total.  dgain [cols] or NULL.
  * scratch: snk_rmsnorm_backward_scratch(rows, cols) bytes, 32-byte aligned
- * (not needed when dgain is NULL).  Errors as above.
+ * (may be NULL when that is 0, as for a few rows, or dgain is NULL).  Errors as
+ * above.
  */
 int64_t snk_rmsnorm_backward_scratch(int64_t rows, int64_t cols);
 int snk_rmsnorm_backward(const float* dy, const void* total, int dtype, const float* rstd,

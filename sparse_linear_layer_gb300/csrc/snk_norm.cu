@@ -351,6 +351,62 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowsPerBlock : 1024)
     }
 }
 
+// Few rows, in one launch and without scratch: block r < rows computes row r of dx;
+// the blocks after them take 32 columns of dgain each, their warps sharing the
+// rows, from dy and total again (which L2 then holds).  Up to 256 rows and 2^20
+// elements: beyond, the second reading costs more than a launch.
+inline bool few_rows(int64_t rows, int64_t cols) {
+    return rows <= 256 && rows * cols <= (1 << 20) && cols <= kRegisterTiles * kQTile;
+}
+template <typename T, bool VEC, int K>
+__global__ void __launch_bounds__(1024) k_norm_grad_few(const NormGradArgs a, float* __restrict__ dgain) {
+    __shared__ float red[32][33];
+    const RowSlot<false> rs;
+    if (blockIdx.x >= a.rows) {
+        const int64_t c = ((int64_t)blockIdx.x - a.rows) * 32 + rs.lane;
+        float t = 0.f;
+        if (c < a.cols) {
+#pragma unroll 8
+            for (int64_t r = rs.w; r < a.rows; r += rs.W)
+                t = fmaf(__ldg(a.dy + r * a.cols + c),
+                         to_f32(static_cast<const T*>(a.total)[r * a.cols + c]) * __ldg(a.rstd + r), t);
+        }
+        red[rs.w][rs.lane] = t;
+        __syncthreads();
+        if (rs.w == 0 && c < a.cols) {
+            for (int i = 1; i < rs.W; ++i) t += red[i][rs.lane];
+            dgain[c] = t;
+        }
+        return;
+    }
+    const int c0 = rs.w * K * kQTile, left = (int)a.cols - c0, c = c0 + lane_col<VEC>(rs.lane);
+    const int64_t e = (int64_t)blockIdx.x * a.cols + c;
+    const float rstd = __ldg(a.rstd + blockIdx.x);
+    F8 g[K], n[K], add[K], dots;
+    dots.clear();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int l = left - k * kQTile;
+        load_tile<float, VEC>(a.dy + e + k * kQTile, l, rs.lane, g[k]);
+        load_tile<T, VEC>((const T*)a.total + e + k * kQTile, l, rs.lane, n[k]);
+        if (a.dtotal) load_tile<T, VEC>((const T*)a.dtotal + e + k * kQTile, l, rs.lane, add[k]);
+        F8 w;
+        load_tile<float, VEC>(a.gain + c + k * kQTile, l, rs.lane, w);
+        n[k].mul(rstd);
+        g[k].mul(w);
+        dots.fma(g[k], n[k]);
+    }
+    const float mean = rs.sum(sum8(dots), red[0]) * a.inv_cols;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        n[k].mul(-mean);
+        g[k].add(n[k]);
+        g[k].mul(rstd);
+        if (a.dtotal) g[k].add(add[k]);
+        store_tile<T, VEC>((T*)a.dx + e + k * kQTile, left - k * kQTile, rs.lane, g[k]);
+    }
+}
+
 // Rows of any length; the gain's partial sums live in the block's scratch row.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) k_norm_grad_long(const NormGradArgs a) {
@@ -526,6 +582,15 @@ int launch_norm_grad(const NormGradArgs& a, float* dgain, cudaStream_t s) {
     const int64_t tpr = ceil_div(a.cols, kQTile);
     int64_t grid = 0;
     int st = SNK_OK;
+    if (few_rows(a.rows, a.cols)) {
+        // 8 warps at least, for the blocks of dgain
+        const RowShape f = row_shape(tpr, 1);
+        const unsigned threads = 32 * std::max(8, f.W);
+        const unsigned blocks = (unsigned)(a.rows + (dgain ? ceil_div(a.cols, 32) : 0));
+        if (f.K == 1) k_norm_grad_few<T, VEC, 1><<<blocks, threads, 0, s>>>(a, dgain);
+        else k_norm_grad_few<T, VEC, 2><<<blocks, threads, 0, s>>>(a, dgain);
+        return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
+    }
     if (tpr <= kRegisterTiles) {
         // one tile per warp (768 bf16 columns: 50 us a training batch, against 57
         // with the row's three in one warp, whose registers leave 16 warps per SM)
@@ -579,7 +644,7 @@ int snk_rmsnorm_q8(const void* x, const void* residual, int dtype, const float* 
 }
 
 int64_t snk_rmsnorm_backward_scratch(int64_t rows, int64_t cols) {
-    if (rows < 1 || cols < 1) return 0;
+    if (rows < 1 || cols < 1 || few_rows(rows, cols)) return 0;
     return std::min<int64_t>(rows, kGradBlocks) * ((cols + 7) & ~(int64_t)7) * (int64_t)sizeof(float);
 }
 
@@ -595,7 +660,8 @@ int snk_rmsnorm_backward(const float* dy, const void* total, int dtype, const fl
         return SNK_OK;
     }
     const size_t e = elt_size(dtype);
-    if (!dy || !total || !rstd || !gain || !dx || (dgain && !scratch)) return SNK_ERR_ARG;
+    if (!dy || !total || !rstd || !gain || !dx) return SNK_ERR_ARG;
+    if (dgain && !scratch && snk_rmsnorm_backward_scratch(rows, cols) > 0) return SNK_ERR_ARG;
     if (!q8_aligned(dy, 4) || !q8_aligned(total, e) || !q8_aligned(rstd, 4) || !q8_aligned(gain, 4) ||
         !q8_aligned(dtotal, e) || !q8_aligned(dx, e) || !q8_aligned(scratch, 32))
         return SNK_ERR_ARG;

@@ -53,7 +53,7 @@ def test_rmsnorm(L):
 
 
 def test_rmsnorm_backward(L):
-    def grad(dy=P, total=P, dtype=F32, rstd=P, gain=P, dtotal=P, rows=1, cols=8, dx=P, dgain=P, scratch=P):
+    def grad(dy=P, total=P, dtype=F32, rstd=P, gain=P, dtotal=P, rows=1000, cols=8, dx=P, dgain=P, scratch=P):
         return L.snk_rmsnorm_backward(dy, total, dtype, rstd, gain, dtotal, rows, cols, dx, dgain, scratch, None)
 
     for bad in [dict(dy=None), dict(total=None), dict(rstd=None), dict(gain=None), dict(dx=None),
@@ -61,7 +61,9 @@ def test_rmsnorm_backward(L):
                 dict(dtotal=P + 2)]:
         assert grad(**bad) == ARG, bad
     assert L.snk_rmsnorm_backward_scratch(0, 8) == 0
-    assert L.snk_rmsnorm_backward_scratch(5, 7) == 5 * 8 * 4
+    assert L.snk_rmsnorm_backward_scratch(5, 7) == 0                     # a few rows need none
+    assert L.snk_rmsnorm_backward_scratch(300, 7) == 300 * 8 * 4
+    assert L.snk_rmsnorm_backward_scratch(5, 20000) == 5 * 20000 * 4     # but long ones do
 
 
 def test_products(L):
