@@ -24,8 +24,7 @@
 namespace snk {
 namespace {
 
-constexpr int kLightRows = 256;     // batch rows per pass with a scale per row
-constexpr int kLightRowsG = 192;    // ... with scales per group, whose table shares the space
+constexpr int kLightRows = 256;     // batch rows per pass, at most
 constexpr int kLightWarps = 8;
 constexpr int kLightEntries = 8;    // per warp of the weight gradient
 
@@ -84,6 +83,9 @@ struct LightArgs {
     const float* dY;     // weight gradient: [rows, out]
     float* dW;
     int accumulate;
+    int64_t b_all;       // with db: the rows of the whole batch, from dY on
+    float* db;           // or null
+    unsigned blocks;     // blocks of the weight gradient; db's follow
 };
 
 // Values of 4 batch rows of column c from their codes (group scales applied unless
@@ -159,6 +161,28 @@ __global__ void __launch_bounds__(32 * kLightWarps) k_light_forward(const LightA
 template <bool ROW>
 __global__ void __launch_bounds__(256) k_light_weight(const LightArgs a) {
     const int lane = threadIdx.x & 31;
+    if (blockIdx.x >= a.blocks) {   // db: 32 columns, the warps sharing the rows
+        __shared__ float sm[8][33];
+        const int y = threadIdx.x >> 5;
+        const int64_t c = (int64_t)(blockIdx.x - a.blocks) * 32 + lane;
+        float t = 0.f;
+        if (c < a.out_f) {
+            for (int64_t i0 = y; i0 < a.b_all; i0 += 256) {   // 32 terms to a running sum
+                float u = 0.f;
+                const int64_t i1 = min(a.b_all, i0 + 256);
+#pragma unroll 8
+                for (int64_t i = i0; i < i1; i += 8) u += __ldg(a.dY + i * a.out_f + c);
+                t += u;
+            }
+        }
+        sm[y][lane] = t;
+        __syncthreads();
+        if (y == 0 && c < a.out_f) {
+            for (int i = 1; i < 8; ++i) t += sm[i][lane];
+            a.db[c] = t;
+        }
+        return;
+    }
     const int64_t e0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kLightEntries;
     if (e0 >= a.nnz) return;
     const int n = (int)min((int64_t)kLightEntries, a.nnz - e0);
@@ -218,29 +242,9 @@ __global__ void __launch_bounds__(256) k_light_weight(const LightArgs a) {
     if (lane < n) a.dW[e0 + lane] = a.accumulate ? a.dW[e0 + lane] + mine : mine;
 }
 
-// db: 32 columns per block, 32 threads to a column.
-__global__ void __launch_bounds__(1024) k_light_bias(const float* __restrict__ dY, int64_t b, int64_t n,
-                                                     float* __restrict__ db) {
-    __shared__ float sm[32][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + x;
-    float t = 0.f;
-    if (c < n) {
-#pragma unroll 8
-        for (int64_t i = y; i < b; i += 32) t += __ldg(dY + i * n + c);
-    }
-    sm[y][x] = t;
-    __syncthreads();
-    t = sm[x][y];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const int64_t cc = (int64_t)blockIdx.x * 32 + y;
-    if (x == 0 && cc < n) db[cc] = t;
-}
-
 // The transposed codes and scales of batch rows [r0, r0 + rows), in the handle's
 // operand space (256 bytes per column of the larger dimension): cb rows of codes
-// and cb scales per group of at least 32 columns.
+// for each column and, for group scales, cb scales for each group.
 int light_operand(Layer* L, const Q8In& q, int64_t r0, int rows, LightArgs* a, cudaStream_t s) {
     a->rows = rows;
     a->cb = (int)ceil_div(rows, 32) * 32;
@@ -268,7 +272,13 @@ int light_operand(Layer* L, const Q8In& q, int64_t r0, int rows, LightArgs* a, c
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
 
-int64_t pass_rows(const Q8In& q) { return q.gshift == 31 ? kLightRows : kLightRowsG; }
+// Batch rows that fit there, a multiple of 32 (at least 192: a group has 32 columns
+// or more, and the layer 64).
+int64_t pass_rows(const Layer* L, const Q8In& q) {
+    const int64_t table = q.gshift == 31 ? 0 : q.n_groups * (int64_t)sizeof(float);
+    const int64_t space = std::max(L->out_f, L->in_f) * kMaxBatchTile * (int64_t)sizeof(float);
+    return std::min<int64_t>(kLightRows, space / (L->in_f + table) / 32 * 32);
+}
 
 }  // namespace
 
@@ -289,7 +299,7 @@ bool light_layer(const Layer* L, const Q8In& q, int64_t b, bool weight) {
 }
 
 int light_forward(Layer* L, const Q8In& q, int64_t b, const float* bias, float* Y, cudaStream_t s) {
-    const int64_t step = pass_rows(q);
+    const int64_t step = pass_rows(L, q);
     for (int64_t r0 = 0; r0 < b; r0 += step) {
         const int rows = (int)std::min<int64_t>(step, b - r0);
         LightArgs a{};
@@ -305,11 +315,7 @@ int light_forward(Layer* L, const Q8In& q, int64_t b, const float* bias, float* 
 }
 
 int light_weight(Layer* L, const Q8In& q, const float* dY, int64_t b, float* dW, float* db, cudaStream_t s) {
-    const int64_t step = pass_rows(q);
-    if (db) {
-        k_light_bias<<<(unsigned)ceil_div(L->out_f, 32), 1024, 0, s>>>(dY, b, L->out_f, db);
-        if (cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
-    }
+    const int64_t step = pass_rows(L, q);
     for (int64_t r0 = 0; r0 < b; r0 += step) {
         const int rows = (int)std::min<int64_t>(step, b - r0);
         LightArgs a{};
@@ -317,7 +323,10 @@ int light_weight(Layer* L, const Q8In& q, const float* dY, int64_t b, float* dW,
         a.dY = dY + r0 * L->out_f;
         a.dW = dW;
         a.accumulate = r0 > 0;
-        const unsigned grid = (unsigned)ceil_div(L->nnz, 8 * kLightEntries);
+        a.blocks = (unsigned)ceil_div(L->nnz, 8 * kLightEntries);
+        a.db = r0 == 0 ? db : nullptr;
+        a.b_all = b;
+        const unsigned grid = a.blocks + (a.db ? (unsigned)ceil_div(L->out_f, 32) : 0);
         if (q.gshift == 31) k_light_weight<true><<<grid, 256, 0, s>>>(a);
         else k_light_weight<false><<<grid, 256, 0, s>>>(a);
         if (cudaGetLastError() != cudaSuccess) return SNK_ERR_CUDA;
