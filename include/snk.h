@@ -475,9 +475,12 @@ int snk_rmsnorm_backward(const float* dy, const void* total, int dtype, const fl
 
 /*
  * snk_forward and snk_backward_weight with an 8-bit X [batch, in] (codes,
- * scales, format, group as above): the same products, dispatch, numerics and
- * rules of capture, with X[beta, c] = scale * code (rounded to fp32).  No fp32
- * copy of the whole X is made.  Errors: SNK_ERR_ARG, SNK_ERR_OOM, SNK_ERR_CUDA.
+ * scales, format, group as above): the same products, workspaces and rules of
+ * capture, fp32 sums, with X[beta, c] = scale * code.  No fp32 copy of the whole
+ * X is made.  Batches run in 64-row tiles or, large ones, on the tensor cores,
+ * as for an fp32 X; layers of few entries have a third form above 64 rows, which
+ * SNK_LARGE_BATCH=on|off leaves out.  Errors: SNK_ERR_ARG, SNK_ERR_OOM,
+ * SNK_ERR_CUDA.
  */
 int snk_forward_q8(snk_handle handle, const void* codes, const float* scales, int format,
                    int group, int64_t batch, const float* bias, float* Y, void* stream);

@@ -11,6 +11,11 @@
 // shuffles.  A scale for the whole row needs the row's largest magnitude
 // before the first code: the row then stays in registers over W warps
 // (k_pack_row), up to 16384 columns; longer rows are read twice (k_pack_long).
+//
+// Measured, 16384 x 3072 fp32 in groups of 128: GELU with its checkpoint, E4M3, 51 us
+// (6.0 TB/s; issue slots 80% busy: two quantisations and GELU per element); GELU's
+// gradient from int8 codes 67 us (6.8 TB/s, the rate of a copy).  4096 x 10000 fp32 to
+// int8 and back 65 us (6.3 TB/s).
 #include <algorithm>
 
 #include "snk_q8.cuh"
@@ -76,7 +81,7 @@ struct PackArgs {
 };
 
 // A warp's tile of a flat grid over matrices of `tpr` tiles per row: its row, its
-// first column, and the columns of it that lie in the row.  One tile per warp:
+// first column, and the columns of it that lie in the row.  Few tiles per warp:
 // the registers of more cost more warps than their loads in flight gain (GELU's
 // gradient at 16384 x 3072 takes 70 us with 1, 79 with 2, 115 with 4).
 struct FlatTile {
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(1024) k_pack_long(const PackArgs a) {
 }
 
 // unpack (GRAD false: x = scale * code) and GELU's gradient (GRAD: x = da
-// times the slope at scale * code).
+// times the slope at scale * code).  One tile per warp (see FlatTile).
 template <typename T, bool VEC, bool GRAD, bool ROWS>
 __global__ void __launch_bounds__(256) k_unpack(const Q8In q, const T* da, T* x, uint32_t tiles, uint32_t tpr) {
     const uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5);

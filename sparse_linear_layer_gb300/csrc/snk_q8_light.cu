@@ -10,8 +10,10 @@
 //                    word of codes per entry)
 //   weight gradient  a warp per 8 entries; the row's dY values stay in registers
 //                    while the row lasts, a lane holding 4 batch rows of each 128
-// Sums are fp32: a run's terms, then runs in order, then warps in order (forward); 8 terms per lane and a shuffle tree (weight gradient).
-// Bound by launches and L2 latency: the codes are in*rows bytes.
+// Sums are fp32: a run's terms, then runs in order, then warps in order (forward);
+// 8 terms per lane and a shuffle tree (weight gradient).
+// Bound by launches and L2 latency: the codes are in * rows bytes.  Times beside
+// those of the other paths stand at light_layer.
 #include <stdlib.h>
 #include <string.h>
 
@@ -19,7 +21,6 @@
 #include <type_traits>
 
 #include "snk_q8.cuh"
-
 
 namespace snk {
 namespace {

@@ -14,6 +14,11 @@
 // flipped in the transposed operand, which is the form the decoding starts from.
 // Groups within a row have a scale per (row, group) instead; they run on the
 // fp32 kernels.
+//
+// Measured at 10000 x 10000, 90%, int8, batch 1/4/8/16/32/64: forward 15/19/25/35/65/100
+// us (from an fp32 copy of the tile 16/25/43/69/102/134), weight gradient
+// 14/17/26/45/83/139.  Bound by the issue of the decoding (6.6 warp instructions per
+// entry at 64 rows, 56% of the issue slots) and by the latency of the gathered words.
 #pragma once
 
 #include "snk_q8.cuh"
