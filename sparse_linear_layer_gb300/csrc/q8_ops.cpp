@@ -1,7 +1,7 @@
 // Python entry points of the 8-bit activation calls on torch tensors: argument
 // checks, outputs, the current stream, and the call into libsnk, in one native
 // step.  (Through ctypes and torch's Python API a call took 16 to 24 us of host
-// time, most of a decoding step; here 6 to 9.)  The module is built against torch's
+// time, most of a decoding step; here 4 to 9.)  The module is built against torch's
 // headers beside libsnk.so, which load() opens; q8.py and binding.py are its
 // only users.  Wrong tensors raise ValueError, a status from libsnk raises
 // binding.SnkError.
@@ -108,15 +108,37 @@ void require_codes(const Matrix& m, const at::Tensor& codes, const at::Tensor& s
     require_f32(scales, m.rows * groups(m.cols, group), codes.device(), "scales");
 }
 
-void* stream_of(PyObject* o, const at::Device& device) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
-    if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-    if (!h) throw Wrong("stream is None, a stream or a stream handle");
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    return p;
-}
+// The call's device and stream, both current while it lives: outputs and scratch then
+// come from the allocator's blocks of that stream, which no work of another stream
+// still uses or takes over.
+class OnStream {
+public:
+    OnStream(PyObject* o, const at::Device& device) : device_(device) {
+        if (o == Py_None) {
+            handle_ = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+            return;
+        }
+        if (PyLong_Check(o)) {
+            handle_ = (cudaStream_t)PyLong_AsVoidPtr(o);
+        } else {
+            PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+            if (!h) throw Wrong("stream is None, a stream or a stream handle");
+            handle_ = (cudaStream_t)PyLong_AsVoidPtr(h);
+            Py_DECREF(h);
+        }
+        if (PyErr_Occurred()) throw Wrong("stream is None, a stream or a stream handle");
+        // (cudaStreamLegacy is the default stream's other name)
+        stream_.reset_stream(handle_ == nullptr || handle_ == cudaStreamLegacy
+                                 ? c10::cuda::getDefaultCUDAStream(device.index())
+                                 : c10::cuda::getStreamFromExternal(handle_, device.index()));
+    }
+    void* get() const { return handle_; }
+
+private:
+    c10::cuda::CUDAGuard device_;
+    c10::cuda::OptionalCUDAStreamGuard stream_;
+    cudaStream_t handle_ = nullptr;
+};
 void check(int status, const char* call) {
     if (status != SNK_OK) throw Status{status, call};
 }
@@ -180,10 +202,10 @@ PyObject* op_pack(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& x = tensor(a[0], "x");
         const int d = dtype_of(x), format = (int)integer(a[1]), group = group_of(a[2]);
         const Matrix m(x);
-        const c10::cuda::CUDAGuard guard(x.device());
+        const OnStream on(a[3], x.device());
         Packed p = new_packed(x, m, format, group);
         check(g.pack(x.data_ptr(), d, m.rows, m.cols, format, group, p.codes.data_ptr(), (float*)p.scales.data_ptr(),
-                     stream_of(a[3], x.device())),
+                     on.get()),
               "snk_q8_pack");
         return tuple(std::move(p.codes), std::move(p.scales));
     });
@@ -199,12 +221,12 @@ PyObject* op_unpack(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (d < SNK_F32 || d > SNK_BF16) throw Wrong("float32, float16 or bfloat16 is needed");
         const Matrix m(codes);
         require_codes(m, codes, scales, group);
-        const c10::cuda::CUDAGuard guard(codes.device());
+        const OnStream on(a[4], codes.device());
         at::Tensor x = at::empty(codes.sizes(), codes.options().dtype(d == SNK_F32   ? at::kFloat
                                                                       : d == SNK_F16 ? at::kHalf
                                                                                      : at::kBFloat16));
         check(g.unpack(codes.data_ptr(), (const float*)scales.data_ptr(), m.rows, m.cols, format, group, x.data_ptr(), d,
-                       stream_of(a[4], codes.device())),
+                       on.get()),
               "snk_q8_unpack");
         return THPVariable_Wrap(std::move(x));
     });
@@ -216,11 +238,11 @@ PyObject* op_gelu(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& x = tensor(a[0], "x");
         const int d = dtype_of(x), format = (int)integer(a[1]), group = group_of(a[2]);
         const Matrix m(x);
-        const c10::cuda::CUDAGuard guard(x.device());
+        const OnStream on(a[4], x.device());
         Packed p = new_packed(x, m, format, group), kept;
         if (PyObject_IsTrue(a[3])) kept = new_packed(x, m, format, group);
         check(g.gelu(x.data_ptr(), d, m.rows, m.cols, format, group, p.codes.data_ptr(), (float*)p.scales.data_ptr(),
-                     ptr(kept.codes), (float*)ptr(kept.scales), stream_of(a[4], x.device())),
+                     ptr(kept.codes), (float*)ptr(kept.scales), on.get()),
               "snk_gelu_q8");
         return tuple(std::move(p.codes), std::move(p.scales), std::move(kept.codes), std::move(kept.scales));
     });
@@ -237,12 +259,12 @@ PyObject* op_gelu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (da.sizes() != codes.sizes() || da.device() != codes.device() || !codes.is_contiguous())
             throw Wrong("da has the shape and device of the kept input (" + what(codes) + "): " + what(da));
         require_codes(m, codes, scales, group);
-        const c10::cuda::CUDAGuard guard(da.device());
+        const OnStream on(a[5], da.device());
         at::Tensor out = optional(a[4], "out");
         if (out.defined()) require_like(out, da, "out");
         else out = at::empty(da.sizes(), da.options().requires_grad(false));
         check(g.gelu_backward(da.data_ptr(), d, codes.data_ptr(), (const float*)scales.data_ptr(), m.rows, m.cols, format,
-                              group, out.data_ptr(), stream_of(a[5], da.device())),
+                              group, out.data_ptr(), on.get()),
               "snk_gelu_backward_q8");
         return THPVariable_Wrap(std::move(out));
     });
@@ -260,7 +282,7 @@ PyObject* op_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int d = dtype_of(x), format = (int)integer(a[4]), group = group_of(a[5]);
         const Matrix m(x);
         require_f32(gain, m.cols, x.device(), "gain");
-        const c10::cuda::CUDAGuard guard(x.device());
+        const OnStream on(a[6], x.device());
         const auto options = x.options().requires_grad(false);
         at::Tensor total;
         if (residual.defined()) {
@@ -271,7 +293,7 @@ PyObject* op_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor rstd = at::empty(x.sizes().slice(0, x.dim() - 1), options.dtype(at::kFloat));
         check(g.rmsnorm(x.data_ptr(), ptr(residual), d, (const float*)gain.data_ptr(), m.rows, m.cols, (float)eps, format,
                         group, p.codes.data_ptr(), (float*)p.scales.data_ptr(), ptr(total), (float*)rstd.data_ptr(),
-                        stream_of(a[6], x.device())),
+                        on.get()),
               "snk_rmsnorm_q8");
         return tuple(std::move(p.codes), std::move(p.scales), std::move(total), std::move(rstd));
     });
@@ -291,7 +313,7 @@ PyObject* op_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         require_f32(rstd, m.rows, total.device(), "rstd");
         require_f32(gain, m.cols, total.device(), "gain");
         if (dtotal.defined()) require_like(dtotal, total, "dtotal");
-        const c10::cuda::CUDAGuard guard(total.device());
+        const OnStream on(a[5], total.device());
         const auto options = total.options().requires_grad(false);
         at::Tensor dx = at::empty(total.sizes(), options);
         at::Tensor dgain = at::empty(gain.sizes(), options.dtype(at::kFloat)), scratch;
@@ -299,7 +321,7 @@ PyObject* op_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (bytes > 0) scratch = at::empty({bytes}, options.dtype(at::kByte));
         check(g.rmsnorm_backward((const float*)dy.data_ptr(), total.data_ptr(), d, (const float*)rstd.data_ptr(),
                                  (const float*)gain.data_ptr(), ptr(dtotal), m.rows, m.cols, dx.data_ptr(),
-                                 (float*)dgain.data_ptr(), ptr(scratch), stream_of(a[5], total.device())),
+                                 (float*)dgain.data_ptr(), ptr(scratch), on.get()),
               "snk_rmsnorm_backward");
         return tuple(std::move(dx), std::move(dgain));
     });
@@ -324,13 +346,13 @@ PyObject* op_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const LayerInput x(a[3], a[4], a[5], integer(a[2]));
         const at::Tensor bias = optional(a[6], "bias");
         if (bias.defined()) require_f32(bias, out_f, x.codes.device(), "bias");
-        const c10::cuda::CUDAGuard guard(x.codes.device());
+        const OnStream on(a[8], x.codes.device());
         at::Tensor y = optional(a[7], "out");
         if (y.defined()) require_f32(y, x.m.rows * out_f, x.codes.device(), "out");
         else y = at::empty({x.m.rows, out_f}, x.codes.options().dtype(at::kFloat));
         check(g.forward((snk_handle)PyLong_AsVoidPtr(a[0]), x.codes.data_ptr(), (const float*)x.scales.data_ptr(), x.format,
                         x.group, x.m.rows, (const float*)ptr(bias), (float*)y.data_ptr(),
-                        stream_of(a[8], x.codes.device())),
+                        on.get()),
               "snk_forward_q8");
         return THPVariable_Wrap(std::move(y));
     });
@@ -344,7 +366,7 @@ PyObject* op_backward_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const LayerInput x(a[4], a[5], a[6], integer(a[2]));
         const at::Tensor& dy = tensor(a[7], "dY");
         require_f32(dy, x.m.rows * out_f, x.codes.device(), "dY");
-        const c10::cuda::CUDAGuard guard(x.codes.device());
+        const OnStream on(a[10], x.codes.device());
         const auto options = x.codes.options().dtype(at::kFloat);
         at::Tensor dw = optional(a[9], "out"), db;
         if (dw.defined()) require_f32(dw, nnz, x.codes.device(), "out");
@@ -352,7 +374,7 @@ PyObject* op_backward_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (PyObject_IsTrue(a[8])) db = at::empty({out_f}, options);
         check(g.backward_weight((snk_handle)PyLong_AsVoidPtr(a[0]), x.codes.data_ptr(), (const float*)x.scales.data_ptr(),
                                 x.format, x.group, (const float*)dy.data_ptr(), x.m.rows, (float*)dw.data_ptr(),
-                                (float*)ptr(db), stream_of(a[10], x.codes.device())),
+                                (float*)ptr(db), on.get()),
               "snk_backward_weight_q8");
         return tuple(std::move(dw), std::move(db));
     });

@@ -13,6 +13,9 @@ Leading dimensions are rows: a tensor [..., cols] is a matrix of its last
 dimension.  Tensors are CUDA tensors, contiguous, float32 / float16 / bfloat16
 for activations and float32 for gains and statistics; anything else raises
 ValueError.  The arithmetic is libsnk's; nothing falls back to torch.
+
+A call runs on torch's current stream, or on `stream` (a stream or its handle), as
+if that were current: new tensors then belong to it.
 """
 from __future__ import annotations
 

@@ -325,6 +325,34 @@ def test_results_repeat_and_streams(torch):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+def test_stream_argument_owns_what_the_call_allocates(torch):
+    """Memory that the current stream still writes is not taken for another stream's
+    outputs or scratch."""
+    from sparse_linear_layer_gb300 import q8
+    rows, cols = 2048, 768
+    x = torch.randn(rows, cols, device="cuda")
+    gain = torch.ones(cols, device="cuda")
+    want, _, rstd = q8.rmsnorm(x, gain)
+    grads = q8.rmsnorm_backward(x, x, rstd, gain)
+    nbytes = sorted({rows * cols, rows * 4, rows * cols * 4, cols * 4, 1 << 21})
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        pending = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in nbytes for _ in range(3)]
+        torch.cuda._sleep(50_000_000)   # some 25 ms
+        for t in pending:
+            t.fill_(77)
+        del pending, t                  # free for the current stream, still to be written
+        q, _, r = q8.rmsnorm(x, gain, stream=stream)
+        dx, dgain = q8.rmsnorm_backward(x, x, r, gain, stream=stream)
+        back = q8.unpack(q, stream=stream)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales) and torch.equal(r, rstd)
+        assert torch.equal(dx, grads[0]) and torch.equal(dgain, grads[1])
+        assert torch.equal(back, q8.unpack(want))
+
+
 def test_graph_capture(torch):
     from sparse_linear_layer_gb300 import q8
     x = torch.randn(64, 3072, device="cuda")
