@@ -479,7 +479,9 @@ int snk_rmsnorm_backward(const float* dy, const void* total, int dtype, const fl
  * capture, fp32 sums, with X[beta, c] = scale * code.  No fp32 copy of the whole
  * X is made.  Batches run in 64-row tiles or, large ones, on the tensor cores,
  * as for an fp32 X; layers of few entries have a third form above 64 rows, which
- * SNK_LARGE_BATCH=on|off leaves out.  Errors: SNK_ERR_ARG, SNK_ERR_OOM,
+ * SNK_LARGE_BATCH=on|off leaves out.  Where X has one scale per row it is applied
+ * to the finished sum (forward) or to dY (weight gradient), so |scale dY| and |code
+ * values| are to be finite in fp32.  Errors: SNK_ERR_ARG, SNK_ERR_OOM,
  * SNK_ERR_CUDA.
  */
 int snk_forward_q8(snk_handle handle, const void* codes, const float* scales, int format,

@@ -280,6 +280,33 @@ inline int batch_tile(int64_t b) {
     return bp;
 }
 
+// A batch tile of an 8-bit X, in [in][bp] order: whether the products read the codes
+// (else an fp32 copy of the tile).  Codes need a quarter of the bytes but are decoded
+// at every entry.  With group scales an entry reads its scales too, 4 bp bytes, which
+// pays up to bp = 16 (us, codes against the copy, 10000 x 10000 at 90%: forward 43
+// against 67, dW 65 against 85; bp = 32: 112 against 99, 152 against 106).  Few entries
+// per column do not repay wider tiles of staged codes (at 99%, 100 per column:
+// forward 15 against 12 at bp = 8, 28 against 24 at 64 with a scale per row, dW 17
+// against 15 at 16 with groups).
+inline bool q8_codes_tile(const Q8In& q, int bp, int64_t nnz, int64_t in_f, bool weight) {
+    const bool row = q.gshift == 31;
+    if (bp <= 4 || (weight && row)) return true;
+    return nnz >= 200 * in_f && (row || bp <= 16);
+}
+// Rows of the next batch tile of an 8-bit X: a few rows more than 16 or 32 run as a
+// tile of their own, as the next wider one costs more (10000 x 10000 at 95%, us: forward
+// of 17 rows 31 against 45, dW 39 against 53; with groups 42 against 58, 51 against 64;
+// 24 rows 40 against 45 and 47 against 53), except the forward of 32 with groups (33
+// rows 69 against 72, 40 rows 80) and layers whose launches weigh as much as their
+// entries (2.5 million, forward of 20 rows: 25 against 23).
+inline int64_t q8_tile_rows(const Q8In& q, int64_t left, int64_t nnz, bool weight) {
+    const int64_t rows = left < kMaxBatchTile ? left : kMaxBatchTile;
+    if (nnz < 4000000) return rows;
+    if (rows > 16 && rows <= 24) return 16;
+    if (rows > 32 && rows <= 40 && (weight || q.gshift == 31)) return 32;
+    return rows;
+}
+
 // ---- topology (snk_topology.cu) -----------------------------------------
 // Sort + validate + write back the canonical triple + CSR + CSC + chunk tables.
 // Returns an SNK_* status; synchronises `s`.

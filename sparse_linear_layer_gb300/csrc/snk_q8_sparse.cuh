@@ -1,24 +1,27 @@
-// The batch-tiled products on an 8-bit X with one scale per row: the chunk-walk
-// SpMM (snk_spmm.cuh) and the row-order weight gradient (snk_sddmm.cuh) with the
-// codes themselves as the operand.
+// The batch-tiled products on an 8-bit X: the chunk-walk SpMM (snk_spmm.cuh) and the
+// row-order weight gradient (snk_sddmm.cuh) with the codes themselves as the operand.
 //
 //     Y[beta, o] = s_beta * sum_k w_k q[beta, c_k] + bias
 //     dW_k       = sum_beta (s_beta dY[beta, r_k]) q[beta, c_k]
 //
-// The row's scale leaves the sum (forward) or goes into dY (weight gradient), so
-// an entry reads BP bytes of the transposed codes where the fp32 operand has 4 BP:
+// With one scale per row, as written here, the scale leaves the sum (forward) or goes
+// into dY (weight gradient), so an entry reads BP bytes of the transposed codes where
+// the fp32 operand has 4 BP:
 // a tile of 16 columns at in = 10000 then fits shared memory (160 KB), and a wider
 // one, gathered through L1, moves a quarter of the bytes.  A lane decodes the codes
 // of up to 16 batch columns itself, 4 per instruction word, exactly (see
 // q_values4), and accumulates in fp32.  int8 codes are kept with their sign bit
 // flipped in the transposed operand, which is the form the decoding starts from.
-// Groups within a row have a scale per (row, group) instead; they run on the
-// fp32 kernels.
+// Groups within a row have a scale per (row, group) instead: a table of them, groups x
+// BP, follows the transposed codes, an entry reads its column's BP scales from it and
+// multiplies the decoded values.  That pays up to 16 columns; wider tiles, and layers
+// of few entries per column, run on the fp32 kernels (q8_codes_tile).
 //
-// Measured at 10000 x 10000, 90%, int8, batch 1/4/8/16/32/64: forward 15/19/25/35/65/100
-// us (from an fp32 copy of the tile 16/25/43/69/102/134), weight gradient
-// 14/17/26/45/83/139.  Bound by the issue of the decoding (6.6 warp instructions per
-// entry at 64 rows, 56% of the issue slots) and by the latency of the gathered words.
+// Measured at 10000 x 10000, 90%, int8, batch 1/4/8/16/32/64: forward 15/17/23/34/64/97
+// us (from an fp32 copy of the tile 14/23/42/67/99/129), weight gradient
+// 17/21/28/47/87/138 (23/29/53/85/106/184); in groups of 128, batch 4/8/16: 19/28/43 and
+// 27/37/65.  Bound by the issue of the decoding (6.6 warp instructions per entry at 64
+// rows, 56% of the issue slots) and by the latency of the gathered words.
 #pragma once
 
 #include "snk_q8.cuh"
@@ -86,16 +89,30 @@ __device__ __forceinline__ void stage_codes(uint8_t* dst, const uint8_t* __restr
     }
 }
 
+// dst[g * BP + beta] = scale (beta, g), 0 for b <= beta < BP.
+template <int BP>
+__device__ __forceinline__ void stage_scales(float* dst, const float* __restrict__ src, int64_t groups, int b, int tid,
+                                             int nthreads) {
+    for (int64_t i = tid; i < groups * BP; i += nthreads) {
+        const int beta = (int)(i % BP);
+        dst[i] = beta < b ? __ldg(src + beta * groups + i / BP) : 0.f;
+    }
+}
+
+// scales null: the codes only
 template <int BP, int FMT>
-__global__ void k_codes_transposed(const uint8_t* __restrict__ src, int64_t n, int b, uint8_t* __restrict__ dst) {
-    stage_codes<BP, FMT>(dst, src, n, b, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+__global__ void k_codes_transposed(const uint8_t* __restrict__ src, int64_t n, int b, uint8_t* __restrict__ dst,
+                                   const float* __restrict__ scales, int64_t groups, int64_t table) {
+    const int tid = blockIdx.x * blockDim.x + threadIdx.x, nthreads = gridDim.x * blockDim.x;
+    stage_codes<BP, FMT>(dst, src, n, b, tid, nthreads);
+    if (scales) stage_scales<BP>(reinterpret_cast<float*>(dst + table), scales, groups, b, tid, nthreads);
 }
 
 // Lane layout: a lane holds up to 16 batch columns of an entry (8 at BP = 16, which
 // is faster there: 10000^2, 90%: forward 38 -> 35 us, dW 48 -> 45; at BP = 64 8
 // columns take 120 and 176 us against 100 and 139).  Loading the next block's words
 // before decoding this one's was slower throughout (registers).
-template <int B, int FMT>
+template <int B, int FMT, bool GROUPED>
 struct TileQ {
     using Elem = uint8_t;
     static constexpr int BP = B;
@@ -111,7 +128,15 @@ struct TileQ {
         }
     };
     __host__ __device__ static constexpr int beta(int sub, int j) { return sub * VEC + j; }
-    __host__ __device__ static size_t bytes(int64_t n) { return ((size_t)n * B + 15) & ~(size_t)15; }
+    // the codes, and with group scales a table [groups][B] of them
+    template <class Args>
+    __host__ __device__ static size_t codes_bytes(const Args& a) {
+        return ((size_t)columns(a) * B + 15) & ~(size_t)15;
+    }
+    template <class Args>
+    __host__ __device__ static size_t bytes(const Args& a) {
+        return codes_bytes(a) + (GROUPED ? ((size_t)a.groups * B * sizeof(float) + 15) & ~(size_t)15 : 0);
+    }
 
     // pair i of a word's 4 values
     __device__ __forceinline__ static float2 pair(uint32_t w, int i) {
@@ -150,33 +175,61 @@ struct TileQ {
             w[3] = t.w;
         }
     }
+    // the lane's scales of operand row idx
+    template <bool SMEM, class Args>
+    __device__ __forceinline__ static void load_scales(const Args& a, const uint8_t* xsrc, int idx, int sub,
+                                                       float2 (&s)[(VEC + 1) / 2]) {
+        const float* p = reinterpret_cast<const float*>(xsrc + a.table) + (size_t)(idx >> a.gshift) * B + sub * VEC;
+        if constexpr (VEC == 1) {
+            s[0].x = SMEM ? *p : __ldg(p);
+        } else if constexpr (VEC == 2) {
+            s[0] = SMEM ? *reinterpret_cast<const float2*>(p) : __ldg(reinterpret_cast<const float2*>(p));
+        } else {
+#pragma unroll
+            for (int t = 0; t < VEC / 4; ++t) {
+                const float4 v = SMEM ? reinterpret_cast<const float4*>(p)[t] : __ldg(reinterpret_cast<const float4*>(p) + t);
+                s[2 * t] = make_float2(v.x, v.y);
+                s[2 * t + 1] = make_float2(v.z, v.w);
+            }
+        }
+    }
     template <bool SMEM>
-    __device__ __forceinline__ static void axpy(const uint8_t* xsrc, int idx, int sub, float wt, float (&acc)[VEC]) {
+    __device__ __forceinline__ static void axpy(const SpmmArgs& a, const uint8_t* xsrc, int idx, int sub, float wt,
+                                                float (&acc)[VEC]) {
         uint32_t w[WORDS];
         load<SMEM>(xsrc, idx, sub, w);
+        float2 sc[(VEC + 1) / 2];
+        if constexpr (GROUPED) load_scales<SMEM>(a, xsrc, idx, sub, sc);
         if constexpr (VEC == 1) {
-            acc[0] = fmaf(wt, one(w[0]), acc[0]);
+            acc[0] = fmaf(wt, GROUPED ? one(w[0]) * sc[0].x : one(w[0]), acc[0]);
         } else {
 #pragma unroll
             for (int t = 0; t < VEC; t += 2) {
-                const float2 r = __ffma2_rn(pair(w[t / 4], (t >> 1) & 1), make_float2(wt, wt),
-                                            make_float2(acc[t], acc[t + 1]));
+                float2 x = pair(w[t / 4], (t >> 1) & 1);
+                if constexpr (GROUPED) x = __fmul2_rn(x, sc[t >> 1]);
+                const float2 r = __ffma2_rn(x, make_float2(wt, wt), make_float2(acc[t], acc[t + 1]));
                 acc[t] = r.x;
                 acc[t + 1] = r.y;
             }
         }
     }
     template <bool SMEM>
-    __device__ __forceinline__ static float dot(const uint8_t* xsrc, int idx, int sub, const Dy& d) {
+    __device__ __forceinline__ static float dot(const SddmmArgs& a, const uint8_t* xsrc, int idx, int sub,
+                                                const Dy& d) {
         uint32_t w[WORDS];
         load<SMEM>(xsrc, idx, sub, w);
+        float2 sc[(VEC + 1) / 2];
+        if constexpr (GROUPED) load_scales<SMEM>(a, xsrc, idx, sub, sc);
         if constexpr (VEC == 1) {
-            return d.p[0].x * one(w[0]);
+            return d.p[0].x * (GROUPED ? one(w[0]) * sc[0].x : one(w[0]));
         } else {
             float2 p = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int t = 0; t < VEC; t += 2)
-                p = __ffma2_rn(pair(w[t / 4], (t >> 1) & 1), d.p[t >> 1], p);
+            for (int t = 0; t < VEC; t += 2) {
+                float2 x = pair(w[t / 4], (t >> 1) & 1);
+                if constexpr (GROUPED) x = __fmul2_rn(x, sc[t >> 1]);
+                p = __ffma2_rn(x, d.p[t >> 1], p);
+            }
             return p.x + p.y;
         }
     }
@@ -185,12 +238,14 @@ struct TileQ {
     __device__ __forceinline__ static void stage(uint8_t* xs, const Args& a, int tid, int nthreads) {
         if (!a.xt) {
             stage_codes<B, FMT>(xs, a.codes, columns(a), a.b, tid, nthreads);
+            if constexpr (GROUPED)
+                stage_scales<B>(reinterpret_cast<float*>(xs + a.table), a.scales, a.groups, a.b, tid, nthreads);
             return;
         }
         constexpr int U = 6;   // loads in flight per thread
         const uint4* src = static_cast<const uint4*>(a.xt);
         uint4* dst = reinterpret_cast<uint4*>(xs);
-        const int n = (int)(bytes(columns(a)) / 16);
+        const int n = (int)(bytes(a) / 16);
         for (int i0 = tid; i0 < n; i0 += U * nthreads) {
             uint4 v[U];
 #pragma unroll
@@ -201,14 +256,16 @@ struct TileQ {
                 if (i0 + u * nthreads < n) dst[i0 + u * nthreads] = v[u];
         }
     }
-    __device__ __forceinline__ static int64_t columns(const SpmmArgs& a) { return a.n_src; }
-    __device__ __forceinline__ static int64_t columns(const SddmmArgs& a) { return a.in_f; }
+    __host__ __device__ static int64_t columns(const SpmmArgs& a) { return a.n_src; }
+    __host__ __device__ static int64_t columns(const SddmmArgs& a) { return a.in_f; }
     // an output of a row of W with no entries is its bias, whatever the scale
     __device__ __forceinline__ static float out(const SpmmArgs& a, int beta, float sum, bool empty) {
-        return empty ? 0.f : sum * __ldg(a.row_scale + beta);
+        if constexpr (GROUPED) return sum;
+        return empty ? 0.f : sum * __ldg(a.scales + beta);
     }
     __device__ __forceinline__ static float dy(const SddmmArgs& a, int beta, int r) {
-        return __ldg(a.dY + (int64_t)beta * a.out_f + r) * __ldg(a.row_scale + beta);
+        const float d = __ldg(a.dY + (int64_t)beta * a.out_f + r);
+        return GROUPED ? d : d * __ldg(a.scales + beta);
     }
 };
 
@@ -226,16 +283,18 @@ static int q8_smem(F fn, size_t smem) {
 // 23.6 -> 14.6 us).
 constexpr size_t kStageCopy = 48 * 1024;
 
-template <int BP, int FMT>
+template <int BP, int FMT, bool GROUPED>
 static int q8_forward_bp(Layer* L, SpmmArgs a, cudaStream_t s) {
-    using TL = TileQ<BP, FMT>;
+    using TL = TileQ<BP, FMT, GROUPED>;
+    a.table = (int64_t)TL::codes_bytes(a);
     const size_t slots = spmm_slot_bytes<BP, false>();
-    const size_t smem = TL::bytes(a.n_src) + slots;
+    const size_t smem = TL::bytes(a) + slots;
     uint8_t* xt = reinterpret_cast<uint8_t*>(L->xt);
     const bool fits = smem <= (size_t)L->max_smem && a.idx16;
     a.xt = nullptr;
-    if (!fits || TL::bytes(a.n_src) >= kStageCopy) {
-        k_codes_transposed<BP, FMT><<<L->num_sms * 4, 256, 0, s>>>(a.codes, a.n_src, a.b, xt);
+    if (!fits || TL::bytes(a) >= kStageCopy) {
+        k_codes_transposed<BP, FMT><<<L->num_sms * 4, 256, 0, s>>>(a.codes, a.n_src, a.b, xt,
+                                                                  GROUPED ? a.scales : nullptr, a.groups, a.table);
         a.xt = xt;
     }
     if (fits) {
@@ -252,15 +311,17 @@ static int q8_forward_bp(Layer* L, SpmmArgs a, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
 
-template <int BP, int FMT>
+template <int BP, int FMT, bool GROUPED>
 static int q8_weight_bp(Layer* L, SddmmArgs a, cudaStream_t s) {
-    using TL = TileQ<BP, FMT>;
-    const size_t smem = TL::bytes(a.in_f);
+    using TL = TileQ<BP, FMT, GROUPED>;
+    a.table = (int64_t)TL::codes_bytes(a);
+    const size_t smem = TL::bytes(a);
     uint8_t* xt = reinterpret_cast<uint8_t*>(L->xt);
     const bool fits = smem <= (size_t)L->max_smem && a.col16;
     a.xt = nullptr;
     if (!fits || smem >= kStageCopy) {
-        k_codes_transposed<BP, FMT><<<L->num_sms * 4, 256, 0, s>>>(a.codes, a.in_f, a.b, xt);
+        k_codes_transposed<BP, FMT><<<L->num_sms * 4, 256, 0, s>>>(a.codes, a.in_f, a.b, xt,
+                                                                  GROUPED ? a.scales : nullptr, a.groups, a.table);
         a.xt = xt;
     }
     if (fits) {
@@ -274,37 +335,59 @@ static int q8_weight_bp(Layer* L, SddmmArgs a, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
 
-// One batch tile (a.b rows, codes and row_scale set); one translation unit per
-// format.
-template <int FMT>
+// One batch tile (a.b rows; codes, scales, groups and gshift set); a translation unit
+// per format and kind of scale.
+template <int FMT, bool GROUPED>
 int q8_forward_tile(Layer* L, const SpmmArgs& a, int bp, cudaStream_t s);
-template <int FMT>
+template <int FMT, bool GROUPED>
 int q8_weight_tile(Layer* L, const SddmmArgs& a, int bp, cudaStream_t s);
 
-#define SNK_Q8_TILES(FMT)                                                              \
-    template <>                                                                        \
-    int q8_forward_tile<FMT>(Layer * L, const SpmmArgs& a, int bp, cudaStream_t s) {   \
-        switch (bp) {                                                                  \
-            case 1: return q8_forward_bp<1, FMT>(L, a, s);                             \
-            case 2: return q8_forward_bp<2, FMT>(L, a, s);                             \
-            case 4: return q8_forward_bp<4, FMT>(L, a, s);                             \
-            case 8: return q8_forward_bp<8, FMT>(L, a, s);                             \
-            case 16: return q8_forward_bp<16, FMT>(L, a, s);                           \
-            case 32: return q8_forward_bp<32, FMT>(L, a, s);                           \
-            default: return q8_forward_bp<64, FMT>(L, a, s);                           \
-        }                                                                              \
-    }                                                                                  \
-    template <>                                                                        \
-    int q8_weight_tile<FMT>(Layer * L, const SddmmArgs& a, int bp, cudaStream_t s) {   \
-        switch (bp) {                                                                  \
-            case 1: return q8_weight_bp<1, FMT>(L, a, s);                              \
-            case 2: return q8_weight_bp<2, FMT>(L, a, s);                              \
-            case 4: return q8_weight_bp<4, FMT>(L, a, s);                              \
-            case 8: return q8_weight_bp<8, FMT>(L, a, s);                              \
-            case 16: return q8_weight_bp<16, FMT>(L, a, s);                            \
-            case 32: return q8_weight_bp<32, FMT>(L, a, s);                            \
-            default: return q8_weight_bp<64, FMT>(L, a, s);                            \
-        }                                                                              \
+#define SNK_Q8_ROW_TILES(FMT)                                                                       \
+    template <>                                                                                     \
+    int q8_forward_tile<FMT, false>(Layer * L, const SpmmArgs& a, int bp, cudaStream_t s) {         \
+        switch (bp) {                                                                               \
+            case 1: return q8_forward_bp<1, FMT, false>(L, a, s);                                   \
+            case 2: return q8_forward_bp<2, FMT, false>(L, a, s);                                   \
+            case 4: return q8_forward_bp<4, FMT, false>(L, a, s);                                   \
+            case 8: return q8_forward_bp<8, FMT, false>(L, a, s);                                   \
+            case 16: return q8_forward_bp<16, FMT, false>(L, a, s);                                 \
+            case 32: return q8_forward_bp<32, FMT, false>(L, a, s);                                 \
+            default: return q8_forward_bp<64, FMT, false>(L, a, s);                                 \
+        }                                                                                           \
+    }                                                                                               \
+    template <>                                                                                     \
+    int q8_weight_tile<FMT, false>(Layer * L, const SddmmArgs& a, int bp, cudaStream_t s) {         \
+        switch (bp) {                                                                               \
+            case 1: return q8_weight_bp<1, FMT, false>(L, a, s);                                    \
+            case 2: return q8_weight_bp<2, FMT, false>(L, a, s);                                    \
+            case 4: return q8_weight_bp<4, FMT, false>(L, a, s);                                    \
+            case 8: return q8_weight_bp<8, FMT, false>(L, a, s);                                    \
+            case 16: return q8_weight_bp<16, FMT, false>(L, a, s);                                  \
+            case 32: return q8_weight_bp<32, FMT, false>(L, a, s);                                  \
+            default: return q8_weight_bp<64, FMT, false>(L, a, s);                                  \
+        }                                                                                           \
+    }
+// (q8_codes_tile)
+#define SNK_Q8_GROUP_TILES(FMT)                                                                     \
+    template <>                                                                                     \
+    int q8_forward_tile<FMT, true>(Layer * L, const SpmmArgs& a, int bp, cudaStream_t s) {          \
+        switch (bp) {                                                                               \
+            case 1: return q8_forward_bp<1, FMT, true>(L, a, s);                                    \
+            case 2: return q8_forward_bp<2, FMT, true>(L, a, s);                                    \
+            case 4: return q8_forward_bp<4, FMT, true>(L, a, s);                                    \
+            case 8: return q8_forward_bp<8, FMT, true>(L, a, s);                                    \
+            default: return q8_forward_bp<16, FMT, true>(L, a, s);                                  \
+        }                                                                                           \
+    }                                                                                               \
+    template <>                                                                                     \
+    int q8_weight_tile<FMT, true>(Layer * L, const SddmmArgs& a, int bp, cudaStream_t s) {          \
+        switch (bp) {                                                                               \
+            case 1: return q8_weight_bp<1, FMT, true>(L, a, s);                                     \
+            case 2: return q8_weight_bp<2, FMT, true>(L, a, s);                                     \
+            case 4: return q8_weight_bp<4, FMT, true>(L, a, s);                                     \
+            case 8: return q8_weight_bp<8, FMT, true>(L, a, s);                                     \
+            default: return q8_weight_bp<16, FMT, true>(L, a, s);                                   \
+        }                                                                                           \
     }
 
 }  // namespace snk

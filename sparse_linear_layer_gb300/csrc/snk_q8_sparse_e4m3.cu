@@ -3,5 +3,5 @@
 #include "snk_q8_sparse.cuh"
 
 namespace snk {
-SNK_Q8_TILES(SNK_Q8_E4M3)
+SNK_Q8_ROW_TILES(SNK_Q8_E4M3)
 }  // namespace snk

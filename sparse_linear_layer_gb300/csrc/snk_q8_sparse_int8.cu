@@ -3,5 +3,5 @@
 #include "snk_q8_sparse.cuh"
 
 namespace snk {
-SNK_Q8_TILES(SNK_Q8_INT8)
+SNK_Q8_ROW_TILES(SNK_Q8_INT8)
 }  // namespace snk

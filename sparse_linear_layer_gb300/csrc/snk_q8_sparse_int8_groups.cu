@@ -1,0 +1,7 @@
+// The batch-tiled products on int8 codes with a scale per group (see
+// snk_q8_sparse.cuh).
+#include "snk_q8_sparse.cuh"
+
+namespace snk {
+SNK_Q8_GROUP_TILES(SNK_Q8_INT8)
+}  // namespace snk

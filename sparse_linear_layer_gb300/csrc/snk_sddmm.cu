@@ -21,8 +21,8 @@
 
 namespace snk {
 
-// snk_q8_sparse.cuh: one batch tile of an 8-bit X with a scale per row.
-template <int FMT>
+// snk_q8_sparse.cuh: one batch tile of an 8-bit X.
+template <int FMT, bool GROUPED>
 int q8_weight_tile(Layer* L, const SddmmArgs& a, int bp, cudaStream_t s);
 
 template <int BP>
@@ -102,8 +102,8 @@ int launch_backward_weight(Layer* L, const float* X, const Q8In* q, const float*
     a.dW = dW;
     a.b_all = b;
     a.dY_all = dY;
-    for (int64_t t0 = 0; t0 < b; t0 += kMaxBatchTile) {
-        const int64_t bt = std::min<int64_t>(kMaxBatchTile, b - t0);
+    for (int64_t t0 = 0, bt; t0 < b; t0 += bt) {
+        bt = q ? q8_tile_rows(*q, b - t0, L->nnz, true) : std::min<int64_t>(kMaxBatchTile, b - t0);
         a.b = (int)bt;
         Q8In qt{};
         if (q) qt = q->from_row(t0);
@@ -113,11 +113,17 @@ int launch_backward_weight(Layer* L, const float* X, const Q8In* q, const float*
         a.accumulate = t0 > 0;
         a.db = (t0 == 0) ? db : nullptr;
         int st;
-        if (q && q->gshift == 31) {
+        if (q && q8_codes_tile(*q, batch_tile(bt), L->nnz, L->in_f, true)) {
             a.codes = qt.codes;
-            a.row_scale = qt.scales;
-            st = q->format == SNK_Q8_INT8 ? q8_weight_tile<SNK_Q8_INT8>(L, a, batch_tile(bt), s)
-                                          : q8_weight_tile<SNK_Q8_E4M3>(L, a, batch_tile(bt), s);
+            a.scales = qt.scales;
+            a.groups = qt.n_groups;
+            a.gshift = qt.gshift;
+            const int bp = batch_tile(bt);
+            const bool int8 = q->format == SNK_Q8_INT8;
+            if (q->gshift == 31)
+                st = int8 ? q8_weight_tile<SNK_Q8_INT8, false>(L, a, bp, s) : q8_weight_tile<SNK_Q8_E4M3, false>(L, a, bp, s);
+            else
+                st = int8 ? q8_weight_tile<SNK_Q8_INT8, true>(L, a, bp, s) : q8_weight_tile<SNK_Q8_E4M3, true>(L, a, bp, s);
             if (st != SNK_OK) return st;
             continue;
         }

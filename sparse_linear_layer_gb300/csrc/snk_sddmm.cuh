@@ -21,8 +21,11 @@ struct SddmmArgs {
     int n_blocks;
     const float* X;         // [b, in] (tile)
     const void* xt;         // [in][BP] (global path)
-    const float* row_scale; // 8-bit X: the scale of each batch row
+    const float* scales;    // 8-bit X: [b, groups], its scales
     const uint8_t* codes;   // and its codes [b, in]
+    int64_t groups;         // groups of a row
+    int gshift;             // log2 of their columns
+    int64_t table;          // byte offset of the transposed scales in the operand
     const float* dY;        // [b, out] (tile)
     float* dW;              // [nnz]
     bool accumulate;        // add to dW (later batch tiles)
@@ -41,7 +44,6 @@ struct DwTileF32 : Tile<B> {
         float v[TL::VEC];
         __device__ __forceinline__ void set(int j, float x) { v[j] = x; }
     };
-    __host__ __device__ static size_t bytes(int64_t n) { return (size_t)n * B * sizeof(float); }
     __device__ __forceinline__ static void stage(float* xs, const SddmmArgs& a, int tid, int nthreads) {
         stage_transposed<B>(xs, a.X, a.in_f, a.b, a.in_f, tid, nthreads);
     }
@@ -49,7 +51,7 @@ struct DwTileF32 : Tile<B> {
         return __ldg(a.dY + (int64_t)beta * a.out_f + r);
     }
     template <bool SMEM>
-    __device__ __forceinline__ static float dot(const float* xsrc, int idx, int sub, const Dy& d) {
+    __device__ __forceinline__ static float dot(const SddmmArgs&, const float* xsrc, int idx, int sub, const Dy& d) {
         float x[TL::VEC];
         if constexpr (SMEM) TL::load(xsrc + idx * B, sub, x);
         else TL::ldg(xsrc + idx * B, sub, x);
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_sddmm(const SddmmArgs a) {
                 // continues past the block
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float p = TL::template dot<SMEM>(xsrc, ib[s].get(j), sub, dyr);
+                    float p = TL::template dot<SMEM>(a, xsrc, ib[s].get(j), sub, dyr);
 #pragma unroll
                     for (int o = 1; o < LPE; o <<= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
                     res[j] = p;
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_sddmm(const SddmmArgs a) {
             for (int j = 0; j < 4; ++j) {
                 const uint32_t k = base + j;
                 const bool ok = k >= lo_k && k < hi_k;
-                float p = TL::template dot<SMEM>(xsrc, ok ? ib[s].get(j) : 0, sub, dyr);
+                float p = TL::template dot<SMEM>(a, xsrc, ok ? ib[s].get(j) : 0, sub, dyr);
 #pragma unroll
                 for (int o = 1; o < LPE; o <<= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
                 if (ok) res[j] = p;

@@ -38,8 +38,8 @@
 
 namespace snk {
 
-// snk_q8_sparse.cuh: one batch tile of an 8-bit operand with a scale per row.
-template <int FMT>
+// snk_q8_sparse.cuh: one batch tile of an 8-bit operand.
+template <int FMT, bool GROUPED>
 int q8_forward_tile(Layer* L, const SpmmArgs& a, int bp, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
@@ -415,8 +415,8 @@ template <bool GATHER>
 static int run_spmm(Layer* L, SpmmArgs a, const Q8In* q, int64_t b, cudaStream_t s) {
     const float* X0 = a.X;
     float* Y0 = a.Y;
-    for (int64_t t0 = 0; t0 < b; t0 += kMaxBatchTile) {
-        const int64_t bt = std::min<int64_t>(kMaxBatchTile, b - t0);
+    for (int64_t t0 = 0, bt; t0 < b; t0 += bt) {
+        bt = q ? q8_tile_rows(*q, b - t0, a.nnz, false) : std::min<int64_t>(kMaxBatchTile, b - t0);
         a.b = (int)bt;
         Q8In qt{};
         if (q) qt = q->from_row(t0);
@@ -428,11 +428,17 @@ static int run_spmm(Layer* L, SpmmArgs a, const Q8In* q, int64_t b, cudaStream_t
             continue;
         }
         int st;
-        if (q && q->gshift == 31) {
+        if (q && q8_codes_tile(*q, batch_tile(bt), a.nnz, a.n_src, false)) {
             a.codes = qt.codes;
-            a.row_scale = qt.scales;
-            st = q->format == SNK_Q8_INT8 ? q8_forward_tile<SNK_Q8_INT8>(L, a, batch_tile(bt), s)
-                                          : q8_forward_tile<SNK_Q8_E4M3>(L, a, batch_tile(bt), s);
+            a.scales = qt.scales;
+            a.groups = qt.n_groups;
+            a.gshift = qt.gshift;
+            const int bp = batch_tile(bt);
+            const bool int8 = q->format == SNK_Q8_INT8;
+            if (q->gshift == 31)
+                st = int8 ? q8_forward_tile<SNK_Q8_INT8, false>(L, a, bp, s) : q8_forward_tile<SNK_Q8_E4M3, false>(L, a, bp, s);
+            else
+                st = int8 ? q8_forward_tile<SNK_Q8_INT8, true>(L, a, bp, s) : q8_forward_tile<SNK_Q8_E4M3, true>(L, a, bp, s);
         } else {
             st = launch_tile<GATHER>(L, a, batch_tile(bt), q ? &qt : nullptr, s);
         }

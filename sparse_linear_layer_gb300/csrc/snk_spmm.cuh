@@ -28,8 +28,11 @@ struct SpmmArgs {
     int n_blocks;
     const float* X;          // [b, n_src] row-major
     const void* xt;          // [n_src][BP] transposed copy (global-memory path)
-    const float* row_scale;  // 8-bit operand: the scale of each batch row
+    const float* scales;     // 8-bit operand: [b, groups], its scales
     const uint8_t* codes;    // and its codes [b, n_src]
+    int64_t groups;          // groups of a row
+    int gshift;              // log2 of their columns
+    int64_t table;           // byte offset of the transposed scales in the operand
     const float* bias;       // [n_seg] or null
     float* Y;                // [b, n_seg] row-major
     float* part;             // [n_blocks][2][BP] cross-block partial sums
@@ -76,12 +79,13 @@ struct TileF32 : Tile<B> {
     using TL = Tile<B>;
     using Elem = float;
     static constexpr int BP = B;
-    __host__ __device__ static size_t bytes(int64_t n_src) { return operand_floats(n_src, B) * sizeof(float); }
+    __host__ __device__ static size_t bytes(const SpmmArgs& a) { return operand_floats(a.n_src, B) * sizeof(float); }
     __device__ __forceinline__ static void stage(float* xs, const SpmmArgs& a, int tid, int nthreads) {
         stage_transposed<B>(xs, a.X, a.n_src, a.b, a.n_src, tid, nthreads);
     }
     template <bool SMEM>
-    __device__ __forceinline__ static void axpy(const float* xsrc, int idx, int sub, float w, float (&acc)[TL::VEC]) {
+    __device__ __forceinline__ static void axpy(const SpmmArgs&, const float* xsrc, int idx, int sub, float w,
+                                                float (&acc)[TL::VEC]) {
         float x[TL::VEC];
         if constexpr (SMEM) TL::load(xsrc + idx * B, sub, x);
         else TL::ldg(xsrc + idx * B, sub, x);
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(SpmmShape<GATHER>::kNT, 1) k_spmm(const SpmmAr
     constexpr int G = GATHER ? (SNK_GATHER_LEAD < D ? SNK_GATHER_LEAD : D) : 0;
     extern __shared__ float4 smem4[];
     Elem* xs = reinterpret_cast<Elem*>(smem4);
-    float* sp = reinterpret_cast<float*>(reinterpret_cast<char*>(smem4) + (SMEM ? TL::bytes(a.n_src) : 0));
+    float* sp = reinterpret_cast<float*>(reinterpret_cast<char*>(smem4) + (SMEM ? TL::bytes(a) : 0));
     int* srow = reinterpret_cast<int*>(sp + W * 2 * BP);
 
     const int lane = threadIdx.x & 31;
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(SpmmShape<GATHER>::kNT, 1) k_spmm(const SpmmAr
                 // interior block: every entry belongs to the current segment,
                 // which continues past the block
 #pragma unroll
-                for (int j = 0; j < 4; ++j) TL::template axpy<SMEM>(xsrc, ib[s].get(j), sub, wb[s][j], acc);
+                for (int j = 0; j < 4; ++j) TL::template axpy<SMEM>(a, xsrc, ib[s].get(j), sub, wb[s][j], acc);
                 return;
             }
             const uint32_t blk_end = min(blk0 + BLK, k1);
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(SpmmShape<GATHER>::kNT, 1) k_spmm(const SpmmAr
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t k = base + j;
-                    if (k >= lo_k && k < hi_k) TL::template axpy<SMEM>(xsrc, ib[s].get(j), sub, wb[s][j], acc);
+                    if (k >= lo_k && k < hi_k) TL::template axpy<SMEM>(a, xsrc, ib[s].get(j), sub, wb[s][j], acc);
                 }
                 if (min(re, k1) > blk_end) break;  // segment continues in the next block
                 finish_segment<TL>(a, acc, r_begin + i, rs, re, k0, k1, win.bias_of(i), lane, sub,

@@ -116,6 +116,45 @@ def test_wide_operand(torch, b, fmt, group):
     check(torch, synth.make_layer(640, 10001, 99, 0.1, 224, 225), b, fmt, group, 226 + b)
 
 
+@pytest.mark.parametrize("fmt,group", [("int8", 0), ("e4m3", 0), ("int8", 32), ("e4m3", 64), ("int8", 128),
+                                       ("e4m3", 256)])
+@pytest.mark.parametrize("b", [1, 2, 3, 4, 5, 8, 11, 16, 20, 33, 64])
+def test_many_entries_per_column(torch, b, fmt, group):
+    """More than 200 entries per column: wider tiles read the codes too (with groups
+    up to 16 columns)."""
+    check(torch, synth.make_layer(520, 301, 50, 0.1, 321, 322), b, fmt, group, 323 + b)
+
+
+@pytest.mark.parametrize("fmt,group", [("int8", 0), ("e4m3", 64), ("int8", 128)])
+@pytest.mark.parametrize("b", [4, 16])
+def test_many_entries_wide_operand(torch, b, fmt, group):
+    """Codes (and their scales) beyond shared memory."""
+    check(torch, synth.make_layer(420, 15001, 50, 0.1, 331, 332), b, fmt, group, 333 + b)
+    check(torch, synth.make_layer(40, 70001, 99, 0.1, 334, 335), b, fmt, group, 336 + b)
+
+
+@pytest.mark.parametrize("fmt,group", [("int8", 0), ("e4m3", 0), ("int8", 128), ("e4m3", 32)])
+@pytest.mark.parametrize("b", [17, 24, 25, 33, 40, 41, 64 + 18])
+def test_rows_past_a_tile(torch, monkeypatch, b, fmt, group):
+    """Large layers run a few rows more than 16 or 32 as a tile of their own."""
+    monkeypatch.setenv("SNK_LARGE_BATCH", "off")
+    check(torch, synth.make_layer(4100, 2000, 50, 0.1, 341, 342), b, fmt, group, 343 + b)
+
+
+def test_groups_of_nan_in_small_batches(torch):
+    def spoil(x):
+        x[1] = 0
+        x[2, 70] = np.inf
+        x[3, 250:] = np.nan
+        x[4] *= np.float32(1e-20)
+        x[5, :100] *= np.float32(1e-5)
+
+    for b in (6, 8, 13, 20):
+        for fmt in ("int8", "e4m3"):
+            check(torch, synth.make_layer(520, 301, 50, 0.1, 351, 352), b, fmt, 64, 353 + b, spoil)
+            check(torch, synth.make_layer(97, 301, 99, 0.1, 354, 355), b, fmt, 32, 356 + b, spoil)
+
+
 def test_columns_past_16_bits(torch):
     """in > 65536: 32-bit column indices."""
     check(torch, synth.make_layer(40, 70000, 99, 0.1, 231, 232), 3, "int8", 0, 233)
