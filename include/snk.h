@@ -477,8 +477,10 @@ int snk_rmsnorm_backward(const float* dy, const void* total, int dtype, const fl
  * snk_forward and snk_backward_weight with an 8-bit X [batch, in] (codes,
  * scales, format, group as above): the same products, workspaces and rules of
  * capture, fp32 sums, with X[beta, c] = scale * code.  No fp32 copy of the whole
- * X is made.  Batches run in 64-row tiles or, large ones, on the tensor cores,
- * as for an fp32 X; layers of few entries have a third form above 64 rows, which
+ * X is made.  Batches run in 64-row tiles or, large ones, on the tensor cores, each
+ * product from a batch of its own (the weight gradient from 41 rows at 10% stored and
+ * 2 million entries, the forward from 96 to 192 rows there, later for sparser and
+ * smaller layers); layers of few entries have a third form above 64 rows, which
  * SNK_LARGE_BATCH=on|off leaves out.  Where X has one scale per row it is applied
  * to the finished sum (forward) or to dY (weight gradient), so |scale dY| and |code
  * values| are to be finite in fp32.  Errors: SNK_ERR_ARG, SNK_ERR_OOM,

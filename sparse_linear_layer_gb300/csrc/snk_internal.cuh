@@ -215,6 +215,7 @@ void free_bands(Layer* L);
 
 // ---- large-batch path on the tensor cores (snk_tc.cu) ---------------------
 bool tc_eligible(const Layer* L, int64_t b);
+bool tc_eligible(const Layer* L, const Q8In& q, int64_t b, bool weight);   // an 8-bit X
 // Y[b, n_seg] = D[b, K] times the rows (columns = false) or the columns of W,
 // + bias.  Allocates and builds the tile-ordered view on first use.
 template <class Src>

@@ -280,20 +280,28 @@ int64_t pass_rows(const Layer* L, const Q8In& q) {
     const int64_t space = std::max(L->out_f, L->in_f) * kMaxBatchTile * (int64_t)sizeof(float);
     return std::min<int64_t>(kLightRows, space / (L->in_f + table) / 32 * 32);
 }
+// Rows of the next pass where `left` are left: what no longer fits one pass but two of
+// 128 runs as two of 128 (1000 x 3000 at 90% with groups, forward of 256 rows: 192 + 64
+// take 61 us, the second pass costs as much as one of 128).
+int64_t next_pass(int64_t step, int64_t left) {
+    if (left <= step) return left;
+    return step >= 128 && left <= 256 ? 128 : step;
+}
 
 }  // namespace
 
 // More than one 64-row tile, and few enough entries (measured, us, this path
 // against the others): forward, 1000 x 1000 at 90%, b = 128: 10 against 48; 5000 x
 // 5000 at 99.5%, b = 128: 16 against 27; 3000 x 1000 at 90% (300,000 entries), b = 70:
-// 18 against 18, with group scales 23 against 19.  Weight gradient, 768 x 3072 at
+// 18 against 18, with group scales 23 against 19 (24 against 22 at b = 96, 3072 x 768
+// 20 against 30: more entries from there).  Weight gradient, 768 x 3072 at
 // 99%, b = 128: 11 against 30; 500 x 500 at 80% (50,000 entries), b = 70: 12 against
 // 14; 1000 x 1000 at 90% (100,000), b = 70: 17 against 15.  Where the tensor cores
 // take the layer, whose time hardly grows with the batch, the work is limited too.
 bool light_layer(const Layer* L, const Q8In& q, int64_t b, bool weight) {
     if (L->nnz == 0 || b <= 64 || L->in_f < 64) return false;
-    const bool tc = tc_eligible(L, b);
-    if (L->nnz > (weight ? 65536 : (tc || q.gshift == 31) ? 400000 : 131072)) return false;
+    const bool tc = tc_eligible(L, q, b, weight);
+    if (L->nnz > (weight ? 65536 : (b >= 96 || q.gshift == 31) ? 400000 : 131072)) return false;
     const char* f = getenv("SNK_LARGE_BATCH");   // forces one of the other two
     if (f && (strcmp(f, "on") == 0 || strcmp(f, "off") == 0)) return false;
     return !tc || L->nnz * b <= (weight ? 16000000 : 80000000);
@@ -301,10 +309,10 @@ bool light_layer(const Layer* L, const Q8In& q, int64_t b, bool weight) {
 
 int light_forward(Layer* L, const Q8In& q, int64_t b, const float* bias, float* Y, cudaStream_t s) {
     const int64_t step = pass_rows(L, q);
-    for (int64_t r0 = 0; r0 < b; r0 += step) {
-        const int rows = (int)std::min<int64_t>(step, b - r0);
+    for (int64_t r0 = 0, rows; r0 < b; r0 += rows) {
+        rows = next_pass(step, b - r0);
         LightArgs a{};
-        if (int st = light_operand(L, q, r0, rows, &a, s); st != SNK_OK) return st;
+        if (int st = light_operand(L, q, r0, (int)rows, &a, s); st != SNK_OK) return st;
         a.bias = bias;
         a.Y = Y + r0 * L->out_f;
         const dim3 grid((unsigned)L->out_f, (unsigned)ceil_div(rows, 128));
@@ -317,10 +325,10 @@ int light_forward(Layer* L, const Q8In& q, int64_t b, const float* bias, float* 
 
 int light_weight(Layer* L, const Q8In& q, const float* dY, int64_t b, float* dW, float* db, cudaStream_t s) {
     const int64_t step = pass_rows(L, q);
-    for (int64_t r0 = 0; r0 < b; r0 += step) {
-        const int rows = (int)std::min<int64_t>(step, b - r0);
+    for (int64_t r0 = 0, rows; r0 < b; r0 += rows) {
+        rows = next_pass(step, b - r0);
         LightArgs a{};
-        if (int st = light_operand(L, q, r0, rows, &a, s); st != SNK_OK) return st;
+        if (int st = light_operand(L, q, r0, (int)rows, &a, s); st != SNK_OK) return st;
         a.dY = dY + r0 * L->out_f;
         a.dW = dW;
         a.accumulate = r0 > 0;

@@ -87,7 +87,7 @@ int launch_backward_weight(Layer* L, const float* X, const Q8In* q, const float*
         return SNK_OK;
     }
     if (q && light_layer(L, *q, b, true)) return light_weight(L, *q, dY, b, dW, db, s);
-    if (tc_eligible(L, b))
+    if (q ? tc_eligible(L, *q, b, true) : tc_eligible(L, b))
         return q ? run_tc_sddmm(L, SrcQ8{*q}, dY, b, dW, db, s)
                  : run_tc_sddmm(L, SrcF32{X, L->in_f}, dY, b, dW, db, s);
     SddmmArgs a{};

@@ -551,7 +551,7 @@ static SpmmArgs layer_args(Layer* L, bool columns) {
 int launch_forward(Layer* L, const float* X, const Q8In* q, int64_t b, const float* bias, float* Y,
                    cudaStream_t s) {
     if (q && light_layer(L, *q, b, false)) return light_forward(L, *q, b, bias, Y, s);
-    if (tc_eligible(L, b))
+    if (q ? tc_eligible(L, *q, b, false) : tc_eligible(L, b))
         return q ? run_tc(L, false, SrcQ8{*q}, b, bias, Y, s)
                  : run_tc(L, false, SrcF32{X, L->in_f}, b, bias, Y, s);
     SpmmArgs a = layer_args(L, false);

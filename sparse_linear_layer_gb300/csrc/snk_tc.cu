@@ -1597,32 +1597,76 @@ int build_view(Layer* L, int mode, cudaStream_t s) {
 
 // Which path: SNK_LARGE_BATCH=on|off forces it (tests); otherwise the
 // measured crossover with 64-row batch tiling (10000^2 and 5000^2 layers,
-// forward + dX + dW): from kTcTierBatch[t] rows at density
-// 1 / kTcTierDiv[t] and above, for any tier t.
+// forward + dX + dW): from a tier's batch rows at density 1 / div and above, for any
+// tier.
 //   10% (10000^2 and 5000^2): tiled at 64, tensor from 96;  5%: tiled at 64,
 //   tensor from 96 (3% ahead there);  3%: tiled at 128, tensor at 192;
 //   2%: tiled at 192, tensor at 256;  1%: tiled to 384, tie at 512,
 //   tensor at 640.
-constexpr int kTcTiers = 4;
-constexpr int64_t kTcTierBatch[kTcTiers] = {96, 192, 256, 512};
-constexpr int64_t kTcTierDiv[kTcTiers] = {20, 34, 50, 100};
+struct TcTier {
+    int64_t batch, div;
+    int64_t nnz = 0;   // and so many entries
+};
+constexpr TcTier kTcTiers[] = {{96, 20}, {192, 34}, {256, 50}, {512, 100}};
+// On an 8-bit X both sides cost less and each product has its own crossover (us, tiled
+// against tensor cores; layers of 10000^2 unless said).
+//   Forward, a scale per row: 10%: 194 against 189 at 128, 291 against 252 at 192
+//   (5000^2: 70 against 79, 107 against 102); 5%: 185 against 207 at 192, 246 against
+//   207 at 256 (5000^2: 98 against 92); 3%: 232 against 247 at 320, 281 against 257 at
+//   384; 2%: a tie at 512.
+//   Forward, groups: 10%: 227 against 187 at 96 (5000^2: 74 against 75; 3072 x 768: 35
+//   against 51 at 128, 51 against 53 at 192); 5%: 215 against 221 at 192, 287 against
+//   222 at 256; the rest as above.
+//   Weight gradient, which hardly grows with the batch there: 10%: 137 against 111 at
+//   48 (5000^2: 44 against 41; 3072 x 768: 14 against 21 at 64, 22 against 21 at 80);
+//   5%: 82 against 94 at 64, 116 against 97 at 80; 3%: 80 against 94 at 80, 121 against
+//   95 at 128; 2%: 74 against 91 at 96, 93 against 92 at 128; 1%: a tie at 192.  Small
+//   layers start later, with groups (three products) most: 2000 x 2000 at 5%: 23
+//   against 25 at 128, with groups 25 against 33 and 35 against 34 at 160; 3072 x 768
+//   with groups 36 against 30 at 112; 5000^2 at 1% with groups 61 against 61 at 256.
+// (densities from a little below 10, 5, 3, 2 and 1%)
+constexpr int64_t M = 1000000;
+constexpr TcTier kTcForwardRow[] = {{192, 11}, {256, 21}, {384, 36}, {512, 53}, {1024, 106}};
+constexpr TcTier kTcForwardGroup[] = {{96, 11, 2 * M}, {192, 11}, {256, 21}, {384, 36}, {512, 53}, {1024, 106}};
+constexpr TcTier kTcWeightRow[] = {{41, 11, 2 * M}, {65, 21, M}, {96, 21}, {96, 36, M}, {128, 53}, {192, 106}};
+constexpr TcTier kTcWeightGroup[] = {{41, 11, 2 * M}, {65, 21, M}, {112, 11},    {144, 21},
+                                     {96, 36, M},     {128, 53, M}, {192, 53}, {256, 106}};
+
+template <size_t N>
+bool reaches(const Layer* L, int64_t b, const TcTier (&tiers)[N]) {
+    for (const TcTier& t : tiers)
+        if (b >= t.batch && L->nnz >= t.nnz && L->nnz * t.div >= L->out_f * L->in_f) return true;
+    return false;
+}
+
+// The choice that the layer or SNK_LARGE_BATCH makes for every batch: 0 tiled, 1
+// tensor cores, -1 none.
+int tc_forced(const Layer* L) {
+    if (L->nnz == 0) return 0;
+    const int64_t n_tiles = ceil_div(L->out_f, kTcN) * ceil_div(L->in_f, kTcK) +
+                            ceil_div(L->in_f, kTcN) * ceil_div(L->out_f, kTcK) +
+                            ceil_div(L->out_f, kTcM) * ceil_div(L->in_f, kTcN);
+    if (n_tiles > INT32_MAX / 2) return 0;
+    // the weight-gradient view's (block, group) keys
+    if (ceil_div(L->out_f, kTcM) * ceil_div(L->in_f, kTcN) * kWGroups > INT32_MAX) return 0;
+    const char* f = getenv("SNK_LARGE_BATCH");
+    if (f && strcmp(f, "off") == 0) return 0;
+    if (f && strcmp(f, "on") == 0) return 1;
+    return -1;
+}
 
 }  // namespace
 
 bool tc_eligible(const Layer* L, int64_t b) {
-    if (L->nnz == 0) return false;
-    const int64_t n_tiles = ceil_div(L->out_f, kTcN) * ceil_div(L->in_f, kTcK) +
-                            ceil_div(L->in_f, kTcN) * ceil_div(L->out_f, kTcK) +
-                            ceil_div(L->out_f, kTcM) * ceil_div(L->in_f, kTcN);
-    if (n_tiles > INT32_MAX / 2) return false;
-    // the weight-gradient view's (block, group) keys
-    if (ceil_div(L->out_f, kTcM) * ceil_div(L->in_f, kTcN) * kWGroups > INT32_MAX) return false;
-    const char* f = getenv("SNK_LARGE_BATCH");
-    if (f && strcmp(f, "off") == 0) return false;
-    if (f && strcmp(f, "on") == 0) return true;
-    for (int t = 0; t < kTcTiers; ++t)
-        if (b >= kTcTierBatch[t] && L->nnz * kTcTierDiv[t] >= L->out_f * L->in_f) return true;
-    return false;
+    const int f = tc_forced(L);
+    return f >= 0 ? f == 1 : reaches(L, b, kTcTiers);
+}
+
+bool tc_eligible(const Layer* L, const Q8In& q, int64_t b, bool weight) {
+    const int f = tc_forced(L);
+    if (f >= 0) return f == 1;
+    if (q.gshift == 31) return weight ? reaches(L, b, kTcWeightRow) : reaches(L, b, kTcForwardRow);
+    return weight ? reaches(L, b, kTcWeightGroup) : reaches(L, b, kTcForwardGroup);
 }
 
 void free_tc(Layer* L) {

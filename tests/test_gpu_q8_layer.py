@@ -175,6 +175,22 @@ def test_tensor_cores(torch, monkeypatch, fmt, group, b):
     check(torch, synth.make_layer(517, 1003, 95, 0.1, 254, 255), b, fmt, group, 256 + b, bias=False)
 
 
+@pytest.mark.parametrize("fmt,group", [("int8", 0), ("e4m3", 0), ("int8", 32), ("e4m3", 256)])
+@pytest.mark.parametrize("b", [1, 41, 64, 65])
+def test_tensor_cores_small_batch(torch, monkeypatch, fmt, group, b):
+    monkeypatch.setenv("SNK_LARGE_BATCH", "on")
+    check(torch, synth.make_layer(517, 1003, 90, 0.1, 361, 362), b, fmt, group, 363 + b)
+
+
+@pytest.mark.parametrize("fmt,group", [("int8", 0), ("e4m3", 128)])
+@pytest.mark.parametrize("sparsity,out_f,b", [(90, 4500, 40), (90, 4500, 41), (90, 1500, 96), (95, 1500, 65), (97, 1500, 100),
+                                              (98, 1500, 128), (99, 1500, 193)])
+def test_choice_by_batch(torch, fmt, group, sparsity, out_f, b):
+    """On both sides of the batches where a product takes the tensor cores by itself
+    (the forward and the weight gradient each have their own)."""
+    check(torch, synth.make_layer(out_f, 5000, sparsity, 0.1, 371, 372), b, fmt, group, 373 + b)
+
+
 @pytest.mark.parametrize("large", ["on", "off"])
 def test_no_entries(torch, monkeypatch, large):
     from sparse_linear_layer_gb300 import binding, q8
