@@ -1597,17 +1597,16 @@ int build_view(Layer* L, int mode, cudaStream_t s) {
 
 // Which path: SNK_LARGE_BATCH=on|off forces it (tests); otherwise the
 // measured crossover with 64-row batch tiling (10000^2 and 5000^2 layers,
-// forward + dX + dW): from a tier's batch rows at density 1 / div and above, for any
-// tier.
+// forward + dX + dW): from kTcTierBatch[t] rows at density
+// 1 / kTcTierDiv[t] and above, for any tier t.
 //   10% (10000^2 and 5000^2): tiled at 64, tensor from 96;  5%: tiled at 64,
 //   tensor from 96 (3% ahead there);  3%: tiled at 128, tensor at 192;
 //   2%: tiled at 192, tensor at 256;  1%: tiled to 384, tie at 512,
 //   tensor at 640.
-struct TcTier {
-    int64_t batch, div;
-    int64_t nnz = 0;   // and so many entries
-};
-constexpr TcTier kTcTiers[] = {{96, 20}, {192, 34}, {256, 50}, {512, 100}};
+constexpr int kTcTiers = 4;
+constexpr int64_t kTcTierBatch[kTcTiers] = {96, 192, 256, 512};
+constexpr int64_t kTcTierDiv[kTcTiers] = {20, 34, 50, 100};
+
 // On an 8-bit X both sides cost less and each product has its own crossover (us, tiled
 // against tensor cores; layers of 10000^2 unless said).
 //   Forward, a scale per row: 10%: 194 against 189 at 128, 291 against 252 at 192
@@ -1624,6 +1623,10 @@ constexpr TcTier kTcTiers[] = {{96, 20}, {192, 34}, {256, 50}, {512, 100}};
 //   layers start later, with groups (three products) most: 2000 x 2000 at 5%: 23
 //   against 25 at 128, with groups 25 against 33 and 35 against 34 at 160; 3072 x 768
 //   with groups 36 against 30 at 112; 5000^2 at 1% with groups 61 against 61 at 256.
+struct TcTier {
+    int64_t batch, div;
+    int64_t nnz = 0;   // and so many entries
+};
 // (densities from a little below 10, 5, 3, 2 and 1%)
 constexpr int64_t M = 1000000;
 constexpr TcTier kTcForwardRow[] = {{192, 11}, {256, 21}, {384, 36}, {512, 53}, {1024, 106}};
@@ -1659,7 +1662,10 @@ int tc_forced(const Layer* L) {
 
 bool tc_eligible(const Layer* L, int64_t b) {
     const int f = tc_forced(L);
-    return f >= 0 ? f == 1 : reaches(L, b, kTcTiers);
+    if (f >= 0) return f == 1;
+    for (int t = 0; t < kTcTiers; ++t)
+        if (b >= kTcTierBatch[t] && L->nnz * kTcTierDiv[t] >= L->out_f * L->in_f) return true;
+    return false;
 }
 
 bool tc_eligible(const Layer* L, const Q8In& q, int64_t b, bool weight) {
