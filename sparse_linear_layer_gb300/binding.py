@@ -15,6 +15,7 @@ import threading
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # the in-tree library that build.py writes; nothing selects another one
 LIB_PATH = os.path.join(_PKG, "libsnk.so")
+OPS_PATH = os.path.join(_PKG, "_q8ops.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "snk.h")
 
 SNK_OK, SNK_ERR_ARG, SNK_ERR_DUP, SNK_ERR_RANGE = 0, 1, 2, 3
@@ -98,10 +99,11 @@ def ops():
     global _ops
     if _ops is None:
         lib()
-        try:
-            from . import _q8ops
-        except ImportError as e:
-            raise RuntimeError("_q8ops.so is not built; run sparse_linear_layer_gb300.build.build() first") from e
+        if not os.path.exists(OPS_PATH):
+            raise RuntimeError(f"_q8ops.so is not built ({OPS_PATH}); run "
+                               "sparse_linear_layer_gb300.build.build() first")
+        import torch  # noqa: F401  (the module has no run path: torch's libraries have to be there already)
+        from . import _q8ops
         _q8ops.load(LIB_PATH, SnkError)
         _ops = _q8ops
     return _ops
