@@ -355,20 +355,22 @@ __global__ void __launch_bounds__(ONE ? 32 * kRowsPerBlock : 1024)
     }
 }
 
-// Few rows, in one launch and without scratch: block r < rows computes row r of dx;
-// the blocks after them take 32 columns of dgain each, their warps sharing the
-// rows, from dy and total again (which L2 then holds).  Up to 256 rows and 2^20
+// Few rows, in one launch and without scratch: block r < row_blocks computes row r of
+// dx; the blocks after them take 32 columns of dgain each, their warps sharing the
+// rows, from dy and total again (which L2 then holds).  Where dx is total itself, dgain's
+// blocks are a launch of their own before the rows': nothing orders the blocks of one
+// launch, and these read what the rows' blocks write over.  Up to 256 rows and 2^20
 // elements: beyond, the second reading costs more than a launch (229 x 1152 bf16: 5.1
 // us against 6.4 in two launches; 500 x 1000: 9.0 against 5.4).
 inline bool few_rows(int64_t rows, int64_t cols) {
     return rows <= 256 && rows * cols <= (1 << 20) && cols <= kRegisterTiles * kQTile;
 }
 template <typename T, bool VEC, int K>
-__global__ void __launch_bounds__(1024) k_norm_grad_few(const NormGradArgs a, float* __restrict__ dgain) {
+__global__ void __launch_bounds__(1024) k_norm_grad_few(const NormGradArgs a, unsigned row_blocks, float* __restrict__ dgain) {
     __shared__ float red[32][33];
     const RowSlot<false> rs;
-    if (blockIdx.x >= a.rows) {
-        const int64_t c = ((int64_t)blockIdx.x - a.rows) * 32 + rs.lane;
+    if (blockIdx.x >= row_blocks) {
+        const int64_t c = (int64_t)(blockIdx.x - row_blocks) * 32 + rs.lane;
         float t = 0.f;
         if (c < a.cols) {
 #pragma unroll 8
@@ -591,9 +593,14 @@ int launch_norm_grad(const NormGradArgs& a, float* dgain, cudaStream_t s) {
         // 8 or 32 warps at least, for the blocks of dgain
         const RowShape f = row_shape(tpr, 1);
         const unsigned threads = 32 * std::max(a.rows > 64 ? 32 : 8, f.W);
-        const unsigned blocks = (unsigned)(a.rows + (dgain ? ceil_div(a.cols, 32) : 0));
-        if (f.K == 1) k_norm_grad_few<T, VEC, 1><<<blocks, threads, 0, s>>>(a, dgain);
-        else k_norm_grad_few<T, VEC, 2><<<blocks, threads, 0, s>>>(a, dgain);
+        const unsigned rows = (unsigned)a.rows, sums = dgain ? (unsigned)ceil_div(a.cols, 32) : 0;
+        auto fn = f.K == 1 ? k_norm_grad_few<T, VEC, 1> : k_norm_grad_few<T, VEC, 2>;
+        if (sums && a.dx == a.total) {
+            fn<<<sums, threads, 0, s>>>(a, 0, dgain);
+            fn<<<rows, threads, 0, s>>>(a, rows, dgain);
+        } else {
+            fn<<<rows + sums, threads, 0, s>>>(a, rows, dgain);
+        }
         return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
     }
     if (tpr <= kRegisterTiles) {
