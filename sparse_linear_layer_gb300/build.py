@@ -3,12 +3,14 @@
 Each .cu file compiles in its own nvcc process, in parallel; the objects are
 linked into ``sparse_linear_layer_gb300/libsnk.so`` with the CUDA runtime
 linked statically, so the library only needs the driver at run time.  Beside it
-g++ builds ``_q8ops.so``, the Python module that calls it on torch tensors.
+g++ builds ``_q8ops.so``, the Python module that calls it on torch tensors, for the
+torch that is installed; without one there is only the library.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -42,12 +44,44 @@ def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "snk.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(OPS):
+def _torch_key() -> str | None:
+    """What _q8ops.so is built for: the Python and the torch (None: there is none)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+        return f"{sys.implementation.cache_tag} {spec.origin}\n{f.read()}"
+
+
+def has_torch() -> bool:
+    return _torch_key() is not None
+
+
+def _key_file() -> str:
+    return os.path.join(OBJ, "_q8ops.key")
+
+
+def _lib_up_to_date() -> bool:
+    if not os.path.exists(LIB):
         return False
-    t, o = os.path.getmtime(LIB), os.path.getmtime(OPS)
-    return (all(os.path.getmtime(p) <= t for p in _deps()) and
-            max(os.path.getmtime(OPS_SRC), os.path.getmtime(os.path.join(INCLUDE, "snk.h"))) <= o)
+    t = os.path.getmtime(LIB)
+    return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _ops_up_to_date() -> bool:
+    key = _torch_key()
+    if key is None:
+        return True
+    if not os.path.exists(OPS) or not os.path.exists(_key_file()):
+        return False
+    with open(_key_file()) as f:
+        if f.read() != key:
+            return False
+    return max(os.path.getmtime(p) for p in (OPS_SRC, os.path.join(INCLUDE, "snk.h"))) <= os.path.getmtime(OPS)
+
+
+def up_to_date() -> bool:
+    return _lib_up_to_date() and _ops_up_to_date()
 
 
 def _compile(src: str, verbose: bool, obj_dir: str, extra) -> str:
@@ -68,6 +102,7 @@ def _build_ops() -> None:
     import sysconfig
 
     import torch
+    key = _torch_key()
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
@@ -80,6 +115,8 @@ def _build_ops() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {OPS_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OPS)
+    with open(_key_file(), "w") as f:
+        f.write(key)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str | None = None) -> str:
@@ -98,22 +135,26 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str
         fcntl.flock(lock, fcntl.LOCK_EX)
         if not force and not extra and out is None and up_to_date():
             return LIB
-        return _build_locked(verbose, extra, lib, obj_dir)
+        all_of_it = force or bool(extra) or out is not None
+        with cf.ThreadPoolExecutor(max_workers=1) as ex:
+            # (the library does not depend on the torch module: it is linked whether or not that compiles)
+            ops = ex.submit(_build_ops) if lib == LIB and _torch_key() and (all_of_it or not _ops_up_to_date()) else None
+            if all_of_it or not _lib_up_to_date():
+                _build_lib(verbose, extra, lib, obj_dir)
+            if ops is not None:
+                ops.result()
+        return lib
 
 
-def _build_locked(verbose: bool, extra, lib: str, obj_dir: str) -> str:
+def _build_lib(verbose: bool, extra, lib: str, obj_dir: str) -> None:
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        ops = ex.submit(_build_ops) if lib == LIB else None
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose, obj_dir, extra), srcs))
-        if ops is not None:
-            ops.result()
     tmp = lib + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":
