@@ -1,11 +1,14 @@
-"""The norm and its gradient through the C entry points: outputs on the buffers
-that include/snk.h lets them share, and row counts on both sides of every choice
-of kernel."""
+"""The norm and its gradient: outputs on the buffers that include/snk.h lets them
+share, and row counts on both sides of every choice of kernel.  Tolerances as in
+test_gpu_q8.py: a row's sum has at most 3 * 8 products per lane, 5 additions over
+the lanes and 32 over the warps, under the 32 + 5 + 32 stated there; dgain adds a
+row at a time at worst, (rows + 64) u."""
 import numpy as np
 import pytest
 
-from tests.gpu_util import dev, need_gpu
-from tests.test_gpu_q8 import data, on_gpu
+from tests import q8_ref as ref
+from tests.gpu_util import dev, host, need_gpu
+from tests.test_gpu_q8 import HALF_UNIT, U, check_rounded, data, on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +76,48 @@ def test_norm_over_its_own_inputs(torch, dtype, rows, cols, group):
                                over, rs)
         assert torch.equal(over, total) and torch.equal(rs, rstd)
         assert torch.equal(codes, want.codes) and torch.equal(scales, want.scales)
+
+
+# One warp per row with rows in flight starts at 2 * 152 * 8 = 2432 rows (norm: up to
+# 768 columns, gradient: up to 256), several warps at 304; two tiles per warp from
+# 8200 columns; none of these row counts is a multiple of the slots times the grid.
+MANY_ROWS = [(2500, 768), (5001, 520), (2441, 200), (2433, 256), (300, 200), (700, 77), (257, 768), (310, 10000),
+             (257, 9001), (3001, 301)]
+
+
+@pytest.mark.parametrize("rows,cols", MANY_ROWS)
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+def test_norm_of_many_rows(torch, dtype, rows, cols):
+    from sparse_linear_layer_gb300 import q8
+    rng = np.random.default_rng(23)
+    x, _ = on_gpu(torch, data(rng, rows, cols), dtype)
+    residual, _ = on_gpu(torch, data(rng, rows, cols, 3.0), dtype)
+    gain = (1 + 0.1 * rng.standard_normal(cols)).astype(np.float32)
+    for res in (residual, None):
+        want = x + res if res is not None else x
+        y, rs = ref.rmsnorm(want.double().cpu().numpy(), gain.astype(np.float64), 1e-5)
+        for fmt, group in (("int8", 0), ("e4m3", 128)):
+            q, total, rstd = q8.rmsnorm(x, dev(gain, torch), residual=res, eps=1e-5, format=fmt, group=group)
+            assert torch.equal(total, want), "total"
+            np.testing.assert_allclose(host(rstd), rs, rtol=(32 + 5 + 32 + 4) * U)
+            check_rounded(q, y, (32 + 5 + 32 + 8) * U * np.abs(y), fmt, group, f"norm {rows}x{cols}")
+
+
+@pytest.mark.parametrize("rows,cols", MANY_ROWS)
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+def test_gradient_of_many_rows(torch, dtype, rows, cols):
+    from sparse_linear_layer_gb300 import q8
+    rng = np.random.default_rng(24)
+    total, tv = on_gpu(torch, data(rng, rows, cols), dtype)
+    dt, dtv = on_gpu(torch, data(rng, rows, cols, 1e-2), dtype)
+    dy = data(rng, rows, cols, 1e-2)
+    gain = (1 + 0.1 * rng.standard_normal(cols)).astype(np.float32)
+    rstd = (1 / np.sqrt((tv.astype(np.float64) ** 2).mean(1) + 1e-5)).astype(np.float32)
+    f8 = lambda a: np.asarray(a, np.float64)
+    for d, dv in ((dt, dtv), (None, 0.0 * dtv)):
+        dx, dgain = q8.rmsnorm_backward(dev(dy, torch), total, dev(rstd, torch), dev(gain, torch), dtotal=d)
+        wx, wg, ax, ag = ref.rmsnorm_backward(f8(dy), f8(tv), f8(rstd), f8(gain), f8(dv))
+        bad = np.abs(dx.float().cpu().numpy() - wx) > \
+            96 * U * ax + HALF_UNIT[dtype] * np.abs(wx) + 2.0 ** -25 * (dtype == "float16")
+        assert not bad.any(), f"dx {rows}x{cols}: {int(bad.sum())} off"
+        assert (np.abs(host(dgain) - wg) <= (rows + 64) * U * ag + 1e-40).all(), f"dgain {rows}x{cols}"
