@@ -23,6 +23,13 @@ static bool bad_q8(int format, int group) {
 
 static bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// The weight gradient of no batch rows: a sum over nothing.
+static int zero_gradients(const Layer* L, float* dW, float* db, cudaStream_t s) {
+    if (dW && cudaMemsetAsync(dW, 0, (size_t)L->nnz * sizeof(float), s) != cudaSuccess) return SNK_ERR_CUDA;
+    if (db && cudaMemsetAsync(db, 0, (size_t)L->out_f * sizeof(float), s) != cudaSuccess) return SNK_ERR_CUDA;
+    return SNK_OK;
+}
+
 static void free_layer(Layer* L) {
     if (!L) return;
     free_restructure(L);
@@ -186,7 +193,7 @@ int snk_backward_weight_q8(snk_handle h, const void* codes, const float* scales,
                            const float* dY, int64_t batch, float* dW, float* db, void* stream) {
     Layer* L = reinterpret_cast<Layer*>(h);
     if (!L || batch < 0 || bad_q8(format, group)) return SNK_ERR_ARG;
-    if (batch == 0) return SNK_OK;
+    if (batch == 0) return zero_gradients(L, dW, db, (cudaStream_t)stream);
     if (!codes || !scales || !dY || (!dW && L->nnz > 0)) return SNK_ERR_ARG;
     if (!aligned(scales, 4) || !aligned(dY, 4) || !aligned(dW, 16) || !aligned(db, 4)) return SNK_ERR_ARG;
     if (fault("launch")) return SNK_ERR_CUDA;
