@@ -31,8 +31,9 @@
  *     SNK_ERR_ARG before any work is queued.
  *   - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *     stream).  Calls are asynchronous on that stream unless said otherwise.
- *   - Outputs are overwritten, never accumulated into.  batch == 0 is a
- *     no-op that returns SNK_OK.
+ *   - Outputs are overwritten, never accumulated into.  batch == 0 returns
+ *     SNK_OK; the weight gradient of no rows is zero (dW, db are written), the
+ *     other products are then no-ops.
  *   - A handle is used by one stream at a time; calls on one handle that
  *     overlap on the GPU race on its workspace.
  *   - snk_forward, snk_backward_input and snk_backward_weight only enqueue
@@ -483,8 +484,7 @@ int snk_rmsnorm_backward(const float* dy, const void* total, int dtype, const fl
  * smaller layers); layers of few entries have a third form above 64 rows, which
  * SNK_LARGE_BATCH=on|off leaves out.  Where X has one scale per row it is applied
  * to the finished sum (forward) or to dY (weight gradient), so |scale dY| and |code
- * values| are to be finite in fp32.  The weight gradient of batch == 0 is zero (dW, db
- * are written).  Errors: SNK_ERR_ARG, SNK_ERR_OOM, SNK_ERR_CUDA.
+ * values| are to be finite in fp32.  Errors: SNK_ERR_ARG, SNK_ERR_OOM, SNK_ERR_CUDA.
  */
 int snk_forward_q8(snk_handle handle, const void* codes, const float* scales, int format,
                    int group, int64_t batch, const float* bias, float* Y, void* stream);

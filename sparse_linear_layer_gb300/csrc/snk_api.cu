@@ -170,7 +170,7 @@ int snk_backward_weight(snk_handle h, const float* X, const float* dY, int64_t b
                         float* db, void* stream) {
     Layer* L = reinterpret_cast<Layer*>(h);
     if (!L || batch < 0) return SNK_ERR_ARG;
-    if (batch == 0) return SNK_OK;
+    if (batch == 0) return zero_gradients(L, dW, db, (cudaStream_t)stream);
     if (!X || !dY || (!dW && L->nnz > 0)) return SNK_ERR_ARG;
     if (!aligned(X, 4) || !aligned(dY, 4) || !aligned(dW, 16) || !aligned(db, 4))
         return SNK_ERR_ARG;

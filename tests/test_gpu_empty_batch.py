@@ -59,3 +59,26 @@ def test_layer_that_keeps_8_bits(torch):
     y.sum().backward()
     assert (layer.values.grad == 0).all() and (layer.bias.grad == 0).all()
     layer.close()
+
+
+def test_weight_gradient_in_fp32(torch):
+    from sparse_linear_layer_gb300 import binding
+    g = make_gpu_layer(torch, synth.make_layer(70, 50, 80, 0.1, 303, 304))
+    x, dy = torch.empty(0, 50, device="cuda"), torch.empty(0, 70, device="cuda")
+    dw, db = (torch.full((n,), float("nan"), device="cuda") for n in (g.nnz, 70))
+    binding.snk_backward_weight(g.handle, x, dy, dw, db)
+    assert (dw == 0).all() and (db == 0).all()
+    spoiled(torch, g.nnz, 70)
+    dw, db = g.backward_weight(x, dy, with_bias=True)
+    assert (dw == 0).all() and (db == 0).all()
+    g.close()
+
+
+def test_layer(torch):
+    from sparse_linear_layer_gb300.module import SparseLinear
+    layer = SparseLinear(96, 160, 0.8)
+    y = layer(torch.empty(0, 96, device="cuda"))
+    spoiled(torch, layer.nnz, 160)
+    y.sum().backward()
+    assert (layer.values.grad == 0).all() and (layer.bias.grad == 0).all()
+    layer.close()
