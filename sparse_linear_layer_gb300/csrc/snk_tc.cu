@@ -647,9 +647,9 @@ __device__ __forceinline__ uint32_t code_word(const uint8_t* row, int64_t k, int
 // The dense operand from codes with a scale per row, once per call (one block per
 // row): the codes as fp16 at row stride ks, and the row's largest magnitude and
 // sum of magnitudes into the running maxima that W's segments are checked
-// against.  A row whose scale is not finite is listed for the exact
-// recomputation (a product with a stored zero of a densified tile would reach
-// outputs that none of its entries does).
+// against.  A row whose scale is not finite, or that holds E4M3's NaN code (its sum
+// is then NaN), is listed for the exact recomputation (a product with a stored
+// zero of a densified tile would reach outputs that none of its entries does).
 __global__ void k_tc_codes(const Q8In q, int64_t ks, __half* __restrict__ dh, int32_t* __restrict__ rows,
                            uint32_t* __restrict__ fix) {
     __shared__ float red[2][32];
@@ -683,7 +683,7 @@ __global__ void k_tc_codes(const Q8In q, int64_t ks, __half* __restrict__ dh, in
             sum += red[1][i];
         }
         const float s = fabsf(q.scales[r]);
-        if (isfinite(s)) {
+        if (isfinite(s) && isfinite(sum)) {
             atomicMax(fix + kFixRowL1, __float_as_uint(s * sum));
             atomicMax(fix + kFixRowMax, __float_as_uint(s * m));
         } else {
