@@ -34,7 +34,7 @@ class _SparseMLPFn(torch.autograd.Function):
         h = block.up._h.forward_q8(n, up_bias)
         a, kept = q8.gelu(h, format=block.format, group=block.group, keep=True)
         y = block.down._h.forward_q8(a, down_bias)
-        ctx.block, ctx.has_residual = block, residual is not None
+        ctx.block, ctx.has_residual, ctx.group = block, residual is not None, n.group
         ctx.save_for_backward(total, rstd, gain, n.codes, n.scales, kept.codes, kept.scales, a.codes, a.scales)
         return (y, total) if ctx.has_residual else y
 
@@ -42,9 +42,9 @@ class _SparseMLPFn(torch.autograd.Function):
     def backward(ctx, dy, dtotal=None):
         block = ctx.block
         total, rstd, gain, n_codes, n_scales, k_codes, k_scales, a_codes, a_scales = ctx.saved_tensors
-        n = q8.Q8Tensor(n_codes, n_scales, block.group)
-        kept = q8.Q8Tensor(k_codes, k_scales, block.group)
-        a = q8.Q8Tensor(a_codes, a_scales, block.group)
+        n = q8.Q8Tensor(n_codes, n_scales, ctx.group)
+        kept = q8.Q8Tensor(k_codes, k_scales, ctx.group)
+        a = q8.Q8Tensor(a_codes, a_scales, ctx.group)
         if dtotal is not None:
             dtotal = dtotal.contiguous()
         if dy is None:   # only total was used

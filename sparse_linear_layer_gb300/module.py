@@ -32,17 +32,19 @@ class _SparseLinearFn(torch.autograd.Function):
         ctx.layer = layer
         ctx.has_bias = bias is not None
         ctx.shape = x.shape
+        ctx.kept_group = None   # as the input was kept, whatever the layer says by then
         if layer.keep is None:
             ctx.save_for_backward(x2)
         else:
             kept = q8.pack(x2, layer.keep, layer.keep_group)
+            ctx.kept_group = kept.group
             ctx.save_for_backward(kept.codes, kept.scales)
         return y.reshape(*x.shape[:-1], layer.out_features)
 
     @staticmethod
     def backward(ctx, gy):
         layer = ctx.layer
-        kept = None if layer.keep is None else q8.Q8Tensor(*ctx.saved_tensors, layer.keep_group)
+        kept = None if ctx.kept_group is None else q8.Q8Tensor(*ctx.saved_tensors, ctx.kept_group)
         gy2 = gy.reshape(-1, layer.out_features).contiguous().float()
         gx = gvalues = gbias = None
         if ctx.needs_input_grad[0]:

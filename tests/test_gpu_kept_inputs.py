@@ -1,0 +1,49 @@
+"""What the block and the layer keep in 8 bits between the passes: in the form of
+the forward pass, and only for a backward pass that will read it."""
+import pytest
+
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return need_gpu()
+
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("before,after", [(("int8", 32), (None, 0)), ((None, 0), ("int8", 32)),
+                                          (("int8", 0), ("int8", 64)), (("e4m3", 64), ("int8", 0))])
+def test_layer_changed_between_the_passes(torch, before, after, bias):
+    from sparse_linear_layer_gb300.module import SparseLinear
+    layer = SparseLinear(200, 130, 0.9, bias=bias, seed=41, keep=before[0], keep_group=before[1])
+    x, gy = torch.randn(7, 200, device="cuda"), torch.randn(7, 130, device="cuda")
+    grads = []
+    for changed in (False, True):
+        xs = x.clone().requires_grad_(True)
+        y = layer(xs)
+        if changed:
+            layer.keep, layer.keep_group = after
+        layer.values.grad = None
+        y.backward(gy)
+        grads.append((xs.grad, layer.values.grad))
+    assert torch.equal(grads[0][0], grads[1][0]) and torch.equal(grads[0][1], grads[1][1])
+    layer.close()
+
+
+def test_block_changed_between_the_passes(torch):
+    from sparse_linear_layer_gb300.mlp import SparseMLP
+    block = SparseMLP(96, 200, 0.8, format="int8", group=32, seed=43)
+    x, r, gy = (torch.randn(9, 96, device="cuda") for _ in range(3))
+    grads = []
+    for changed in (False, True):
+        xs = x.clone().requires_grad_(True)
+        y, _ = block(xs, r)
+        if changed:
+            block.format, block.group = "e4m3", 0
+        block.zero_grad()
+        y.backward(gy)
+        grads.append([xs.grad] + [p.grad for p in block.parameters()])
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    block.close()
