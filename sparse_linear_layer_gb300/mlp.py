@@ -27,15 +27,17 @@ from .module import SparseLinear
 
 class _SparseMLPFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, residual, gain, up_values, up_bias, down_values, down_bias, block):
+    def forward(ctx, x, residual, gain, up_values, up_bias, down_values, down_bias, block, grad):
         ctx.set_materialize_grads(False)
         n, total, rstd = q8.rmsnorm(x, gain, residual=residual, eps=block.eps, format=block.format,
                                     group=block.group)
         h = block.up._h.forward_q8(n, up_bias)
-        a, kept = q8.gelu(h, format=block.format, group=block.group, keep=True)
+        a = q8.gelu(h, format=block.format, group=block.group, keep=grad)
+        a, kept = a if grad else (a, None)
         y = block.down._h.forward_q8(a, down_bias)
         ctx.block, ctx.has_residual, ctx.group = block, residual is not None, n.group
-        ctx.save_for_backward(total, rstd, gain, n.codes, n.scales, kept.codes, kept.scales, a.codes, a.scales)
+        if grad:   # else no backward pass comes
+            ctx.save_for_backward(total, rstd, gain, n.codes, n.scales, kept.codes, kept.scales, a.codes, a.scales)
         return (y, total) if ctx.has_residual else y
 
     @staticmethod
@@ -48,7 +50,7 @@ class _SparseMLPFn(torch.autograd.Function):
         if dtotal is not None:
             dtotal = dtotal.contiguous()
         if dy is None:   # only total was used
-            return (dtotal, dtotal if ctx.has_residual else None) + (None,) * 6
+            return (dtotal, dtotal if ctx.has_residual else None) + (None,) * 7
         dy = dy.contiguous()
         up, down = block.up, block.down
         da = down._h.backward_input(dy)
@@ -58,7 +60,7 @@ class _SparseMLPFn(torch.autograd.Function):
         d_up, d_up_bias = up._h.backward_weight_q8(n, dh, with_bias=True)
         dx, dgain = q8.rmsnorm_backward(dn, total, rstd, gain, dtotal=dtotal)
         return (dx, dx if ctx.has_residual else None, dgain, d_up, d_up_bias if up.bias is not None else None,
-                d_down, d_down_bias if down.bias is not None else None, None)
+                d_down, d_down_bias if down.bias is not None else None, None, None)
 
 
 class SparseMLP(torch.nn.Module):
@@ -78,7 +80,8 @@ class SparseMLP(torch.nn.Module):
     def forward(self, x, residual=None):
         features = self.up.in_features
         x2 = x.reshape(-1, features).contiguous()
-        args = (self.gain, self.up.values, self.up.bias, self.down.values, self.down.bias, self)
+        args = (self.gain, self.up.values, self.up.bias, self.down.values, self.down.bias, self,
+                torch.is_grad_enabled())   # (inside the function gradients are off)
         if residual is None:
             return _SparseMLPFn.apply(x2, None, *args).to(x.dtype).reshape(x.shape)
         r2 = residual.reshape(-1, features).contiguous()

@@ -25,7 +25,7 @@ from . import binding, q8, synth
 
 class _SparseLinearFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, values, bias, layer):
+    def forward(ctx, x, values, bias, layer, grad):
         x2 = x.reshape(-1, layer.in_features).contiguous()
         y = torch.empty((x2.shape[0], layer.out_features), dtype=torch.float32, device=x.device)
         binding.snk_forward(layer._h.handle, x2, bias, y)
@@ -35,7 +35,7 @@ class _SparseLinearFn(torch.autograd.Function):
         ctx.kept_group = None   # as the input was kept, whatever the layer says by then
         if layer.keep is None:
             ctx.save_for_backward(x2)
-        else:
+        elif grad and any(ctx.needs_input_grad[1:3]):   # (the weight's gradient alone reads it)
             kept = q8.pack(x2, layer.keep, layer.keep_group)
             ctx.kept_group = kept.group
             ctx.save_for_backward(kept.codes, kept.scales)
@@ -63,7 +63,7 @@ class _SparseLinearFn(torch.autograd.Function):
             gbias = gb if ctx.has_bias and ctx.needs_input_grad[2] else None
             if not ctx.needs_input_grad[1]:
                 gvalues = None
-        return gx, gvalues, gbias, None
+        return gx, gvalues, gbias, None, None
 
 
 class SparseLinear(torch.nn.Module):
@@ -126,7 +126,8 @@ class SparseLinear(torch.nn.Module):
         return self._h.topology_version
 
     def forward(self, x):
-        return _SparseLinearFn.apply(x.float(), self.values, self.bias, self)
+        # (inside the function gradients are off)
+        return _SparseLinearFn.apply(x.float(), self.values, self.bias, self, torch.is_grad_enabled())
 
     @torch.no_grad()
     def prune_regrow(self, zeta: float, seed: int):

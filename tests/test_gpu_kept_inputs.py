@@ -47,3 +47,46 @@ def test_block_changed_between_the_passes(torch):
         grads.append([xs.grad] + [p.grad for p in block.parameters()])
     assert all(torch.equal(a, b) for a, b in zip(*grads))
     block.close()
+
+
+@pytest.fixture
+def calls(torch, monkeypatch):
+    """The 8-bit matrices that the calls write for a backward pass."""
+    from sparse_linear_layer_gb300 import q8
+    made = []
+    gelu, pack = q8.gelu, q8.pack
+
+    def gelu_seen(*a, keep=False, **k):
+        made.extend(["gelu"] * keep)
+        return gelu(*a, keep=keep, **k)
+
+    monkeypatch.setattr(q8, "gelu", gelu_seen)
+    monkeypatch.setattr(q8, "pack", lambda *a, **k: (made.append("pack"), pack(*a, **k))[1])
+    return made
+
+
+def test_nothing_is_kept_without_a_backward_pass(torch, calls):
+    from sparse_linear_layer_gb300.mlp import SparseMLP
+    from sparse_linear_layer_gb300.module import SparseLinear
+    block = SparseMLP(96, 200, 0.8, seed=45)
+    layer = SparseLinear(96, 200, 0.8, seed=47, keep="int8")
+    x, r = (torch.randn(9, 96, device="cuda") for _ in range(2))
+    with torch.no_grad():
+        y0, t0 = block(x, r)
+        z0 = layer(x)
+        assert not y0.requires_grad and not z0.requires_grad
+    with torch.inference_mode():
+        block(x)
+        layer(x)
+    assert calls == []
+    y1, t1 = block(x, r)
+    z1 = layer(x)
+    assert calls == ["gelu", "pack"]
+    assert torch.equal(y0, y1) and torch.equal(t0, t1) and torch.equal(z0, z1)
+    layer.values.requires_grad_(False)
+    layer.bias.requires_grad_(False)
+    xs = x.clone().requires_grad_(True)
+    layer(xs).sum().backward()   # the input's gradient does not read the input
+    assert xs.grad is not None and calls == ["gelu", "pack"]
+    block.close()
+    layer.close()
