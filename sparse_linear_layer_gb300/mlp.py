@@ -29,38 +29,45 @@ class _SparseMLPFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, gain, up_values, up_bias, down_values, down_bias, block, grad):
         ctx.set_materialize_grads(False)
+        # what the backward pass of the inputs that need it reads: the first layer's input, GELU's (for all
+        # that lies before GELU), the second layer's input, the norm's
+        needs = [grad and need for need in ctx.needs_input_grad[:7]]
         n, total, rstd = q8.rmsnorm(x, gain, residual=residual, eps=block.eps, format=block.format,
                                     group=block.group)
         h = block.up._h.forward_q8(n, up_bias)
-        a = q8.gelu(h, format=block.format, group=block.group, keep=grad)
-        a, kept = a if grad else (a, None)
+        a = q8.gelu(h, format=block.format, group=block.group, keep=any(needs[:5]))
+        a, kept = a if any(needs[:5]) else (a, None)
         y = block.down._h.forward_q8(a, down_bias)
         ctx.block, ctx.has_residual, ctx.group = block, residual is not None, n.group
-        if grad:   # else no backward pass comes
-            ctx.save_for_backward(total, rstd, gain, n.codes, n.scales, kept.codes, kept.scales, a.codes, a.scales)
+        held = [*((total, rstd, gain) if any(needs[:3]) else (None,) * 3)]
+        for q, needed in ((n, any(needs[3:5])), (kept, any(needs[:5])), (a, any(needs[5:]))):
+            held += (q.codes, q.scales) if needed else (None, None)
+        ctx.save_for_backward(*held)
         return (y, total) if ctx.has_residual else y
 
     @staticmethod
     def backward(ctx, dy, dtotal=None):
-        block = ctx.block
-        total, rstd, gain, n_codes, n_scales, k_codes, k_scales, a_codes, a_scales = ctx.saved_tensors
-        n = q8.Q8Tensor(n_codes, n_scales, ctx.group)
-        kept = q8.Q8Tensor(k_codes, k_scales, ctx.group)
-        a = q8.Q8Tensor(a_codes, a_scales, ctx.group)
+        up, down, needs = ctx.block.up, ctx.block.down, ctx.needs_input_grad
         if dtotal is not None:
             dtotal = dtotal.contiguous()
         if dy is None:   # only total was used
             return (dtotal, dtotal if ctx.has_residual else None) + (None,) * 7
+        total, rstd, gain, *codes = ctx.saved_tensors
+        n, kept, a = (None if c is None else q8.Q8Tensor(c, s, ctx.group) for c, s in zip(codes[::2], codes[1::2]))
         dy = dy.contiguous()
-        up, down = block.up, block.down
-        da = down._h.backward_input(dy)
-        d_down, d_down_bias = down._h.backward_weight_q8(a, dy, with_bias=True)
-        dh = q8.gelu_backward(da, kept, out=da)
-        dn = up._h.backward_input(dh)
-        d_up, d_up_bias = up._h.backward_weight_q8(n, dh, with_bias=True)
-        dx, dgain = q8.rmsnorm_backward(dn, total, rstd, gain, dtotal=dtotal)
-        return (dx, dx if ctx.has_residual else None, dgain, d_up, d_up_bias if up.bias is not None else None,
-                d_down, d_down_bias if down.bias is not None else None, None, None)
+        dx = dgain = d_up = d_up_bias = d_down = d_down_bias = None
+        if any(needs[5:7]):
+            d_down, d_down_bias = down._h.backward_weight_q8(a, dy, with_bias=True)
+        if any(needs[:5]):
+            da = down._h.backward_input(dy)
+            dh = q8.gelu_backward(da, kept, out=da)
+            if any(needs[3:5]):
+                d_up, d_up_bias = up._h.backward_weight_q8(n, dh, with_bias=True)
+            if any(needs[:3]):
+                dn = up._h.backward_input(dh)
+                dx, dgain = q8.rmsnorm_backward(dn, total, rstd, gain, dtotal=dtotal)
+        grads = (dx, dx, dgain, d_up, d_up_bias, d_down, d_down_bias)
+        return tuple(d if need else None for d, need in zip(grads, needs)) + (None, None)
 
 
 class SparseMLP(torch.nn.Module):

@@ -90,3 +90,43 @@ def test_nothing_is_kept_without_a_backward_pass(torch, calls):
     assert xs.grad is not None and calls == ["gelu", "pack"]
     block.close()
     layer.close()
+
+
+@pytest.mark.parametrize("training", [["x"], ["residual"], ["gain"], ["up.values"], ["up.bias"], ["down.values"],
+                                      ["down.bias"], ["gain", "down.values"], ["x", "up.values", "down.bias"]])
+def test_block_computes_the_gradients_that_are_needed(torch, calls, monkeypatch, training):
+    """Of a partly frozen block: the same bits as of the whole one, no checkpoint or
+    product that only the frozen parts would read, nothing else set."""
+    from sparse_linear_layer_gb300 import binding, q8
+    from sparse_linear_layer_gb300.mlp import SparseMLP
+    block = SparseMLP(96, 200, 0.8, group=32, seed=49)
+    x, r, gy, gt = (torch.randn(9, 96, device="cuda") for _ in range(4))
+
+    def step(names):
+        leaves = dict(block.named_parameters(), x=x.clone(), residual=r.clone())
+        for k in list(leaves):
+            leaves[k].requires_grad_(k in names)
+            leaves[k].grad = None
+        y, total = block(leaves["x"], leaves["residual"])
+        torch.autograd.backward([t for t in (y, total) if t.requires_grad],
+                                [g for t, g in ((y, gy), (total, gt)) if t.requires_grad])
+        return {k: t.grad for k, t in leaves.items()}
+
+    whole = step(["x", "residual", "gain", "up.values", "up.bias", "down.values", "down.bias"])
+    assert all(g is not None for g in whole.values())
+    del calls[:]
+    made = []
+    for cls, names in ((binding.SparseLinear, ("backward_weight_q8", "backward_input")), (q8, ("rmsnorm_backward",))):
+        for name in names:
+            f = getattr(cls, name)
+            monkeypatch.setattr(cls, name, lambda *a, f=f, name=name, **k: (made.append(name), f(*a, **k))[1])
+    some = step(training)
+    assert {k for k, g in some.items() if g is not None} == set(training)
+    assert all(torch.equal(some[k], whole[k]) for k in training)
+    stream = bool({"x", "residual", "gain"} & set(training))
+    first = bool({"up.values", "up.bias"} & set(training))
+    second = bool({"down.values", "down.bias"} & set(training))
+    assert calls == ["gelu"] * (stream or first)
+    assert made.count("backward_weight_q8") == first + second and made.count("rmsnorm_backward") == stream
+    assert made.count("backward_input") == (stream or first) + stream
+    block.close()
