@@ -115,6 +115,7 @@ __global__ void k_codes_transposed(const uint8_t* __restrict__ src, int64_t n, i
 template <int B, int FMT, bool GROUPED>
 struct TileQ {
     using Elem = uint8_t;
+    using DwArgs = SddmmQ8Args;
     static constexpr int BP = B;
     static constexpr int VEC = B < 8 ? B : (B <= 16 ? 8 : 16);
     static constexpr int LPE = B / VEC;
@@ -214,7 +215,7 @@ struct TileQ {
         }
     }
     template <bool SMEM>
-    __device__ __forceinline__ static float dot(const SddmmArgs& a, const uint8_t* xsrc, int idx, int sub,
+    __device__ __forceinline__ static float dot(const SddmmQ8Args& a, const uint8_t* xsrc, int idx, int sub,
                                                 const Dy& d) {
         uint32_t w[WORDS];
         load<SMEM>(xsrc, idx, sub, w);
@@ -257,13 +258,13 @@ struct TileQ {
         }
     }
     __host__ __device__ static int64_t columns(const SpmmArgs& a) { return a.n_src; }
-    __host__ __device__ static int64_t columns(const SddmmArgs& a) { return a.in_f; }
+    __host__ __device__ static int64_t columns(const SddmmQ8Args& a) { return a.in_f; }
     // an output of a row of W with no entries is its bias, whatever the scale
     __device__ __forceinline__ static float out(const SpmmArgs& a, int beta, float sum, bool empty) {
         if constexpr (GROUPED) return sum;
         return empty ? 0.f : sum * __ldg(a.scales + beta);
     }
-    __device__ __forceinline__ static float dy(const SddmmArgs& a, int beta, int r) {
+    __device__ __forceinline__ static float dy(const SddmmQ8Args& a, int beta, int r) {
         const float d = __ldg(a.dY + (int64_t)beta * a.out_f + r);
         return GROUPED ? d : d * __ldg(a.scales + beta);
     }
@@ -312,7 +313,7 @@ static int q8_forward_bp(Layer* L, SpmmArgs a, cudaStream_t s) {
 }
 
 template <int BP, int FMT, bool GROUPED>
-static int q8_weight_bp(Layer* L, SddmmArgs a, cudaStream_t s) {
+static int q8_weight_bp(Layer* L, SddmmQ8Args a, cudaStream_t s) {
     using TL = TileQ<BP, FMT, GROUPED>;
     a.table = (int64_t)TL::codes_bytes(a);
     const size_t smem = TL::bytes(a);
@@ -340,7 +341,7 @@ static int q8_weight_bp(Layer* L, SddmmArgs a, cudaStream_t s) {
 template <int FMT, bool GROUPED>
 int q8_forward_tile(Layer* L, const SpmmArgs& a, int bp, cudaStream_t s);
 template <int FMT, bool GROUPED>
-int q8_weight_tile(Layer* L, const SddmmArgs& a, int bp, cudaStream_t s);
+int q8_weight_tile(Layer* L, const SddmmQ8Args& a, int bp, cudaStream_t s);
 
 #define SNK_Q8_ROW_TILES(FMT)                                                                       \
     template <>                                                                                     \
@@ -356,7 +357,7 @@ int q8_weight_tile(Layer* L, const SddmmArgs& a, int bp, cudaStream_t s);
         }                                                                                           \
     }                                                                                               \
     template <>                                                                                     \
-    int q8_weight_tile<FMT, false>(Layer * L, const SddmmArgs& a, int bp, cudaStream_t s) {         \
+    int q8_weight_tile<FMT, false>(Layer * L, const SddmmQ8Args& a, int bp, cudaStream_t s) {         \
         switch (bp) {                                                                               \
             case 1: return q8_weight_bp<1, FMT, false>(L, a, s);                                    \
             case 2: return q8_weight_bp<2, FMT, false>(L, a, s);                                    \
@@ -380,7 +381,7 @@ int q8_weight_tile(Layer* L, const SddmmArgs& a, int bp, cudaStream_t s);
         }                                                                                           \
     }                                                                                               \
     template <>                                                                                     \
-    int q8_weight_tile<FMT, true>(Layer * L, const SddmmArgs& a, int bp, cudaStream_t s) {          \
+    int q8_weight_tile<FMT, true>(Layer * L, const SddmmQ8Args& a, int bp, cudaStream_t s) {          \
         switch (bp) {                                                                               \
             case 1: return q8_weight_bp<1, FMT, true>(L, a, s);                                     \
             case 2: return q8_weight_bp<2, FMT, true>(L, a, s);                                     \

@@ -23,7 +23,7 @@ namespace snk {
 
 // snk_q8_sparse.cuh: one batch tile of an 8-bit X.
 template <int FMT, bool GROUPED>
-int q8_weight_tile(Layer* L, const SddmmArgs& a, int bp, cudaStream_t s);
+int q8_weight_tile(Layer* L, const SddmmQ8Args& a, int bp, cudaStream_t s);
 
 template <int BP>
 __global__ void k_transpose_x(const float* __restrict__ X, int64_t n, int b, float* __restrict__ xt) {
@@ -45,6 +45,7 @@ template <int BP>
 static int launch_bp(Layer* L, SddmmArgs a, const Q8In* q, cudaStream_t s) {
     const size_t smem = (size_t)a.in_f * BP * sizeof(float);
     const int grid = a.n_blocks;
+    using Args = typename DwTileF32<BP>::DwArgs;
     if constexpr (BP >= 8 && SNK_BANDS) {
         // an operand too wide for shared memory: row runs over column bands
         if (smem > (size_t)L->max_smem) {
@@ -64,7 +65,7 @@ static int launch_bp(Layer* L, SddmmArgs a, const Q8In* q, cudaStream_t s) {
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
                 cudaSuccess)
             return SNK_ERR_CUDA;
-        fn<<<grid, kThreads, smem, s>>>(a);
+        fn<<<grid, kThreads, smem, s>>>(Args(a));
     } else {
         if (q) {
             if (int st = launch_q8_transposed(*q, a.b, BP, L->xt, L->num_sms, s); st != SNK_OK) return st;
@@ -72,7 +73,7 @@ static int launch_bp(Layer* L, SddmmArgs a, const Q8In* q, cudaStream_t s) {
             k_transpose_x<BP><<<L->num_sms * 4, 256, 0, s>>>(a.X, a.in_f, a.b, L->xt);
         }
         a.xt = L->xt;
-        k_sddmm<DwTileF32<BP>, false><<<grid, kThreads, 0, s>>>(a);
+        k_sddmm<DwTileF32<BP>, false><<<grid, kThreads, 0, s>>>(Args(a));
     }
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
@@ -114,16 +115,17 @@ int launch_backward_weight(Layer* L, const float* X, const Q8In* q, const float*
         a.db = (t0 == 0) ? db : nullptr;
         int st;
         if (q && q8_codes_tile(*q, batch_tile(bt), L->nnz, L->in_f, true)) {
-            a.codes = qt.codes;
-            a.scales = qt.scales;
-            a.groups = qt.n_groups;
-            a.gshift = qt.gshift;
+            SddmmQ8Args aq(a);
+            aq.codes = qt.codes;
+            aq.scales = qt.scales;
+            aq.groups = qt.n_groups;
+            aq.gshift = qt.gshift;
             const int bp = batch_tile(bt);
             const bool int8 = q->format == SNK_Q8_INT8;
             if (q->gshift == 31)
-                st = int8 ? q8_weight_tile<SNK_Q8_INT8, false>(L, a, bp, s) : q8_weight_tile<SNK_Q8_E4M3, false>(L, a, bp, s);
+                st = int8 ? q8_weight_tile<SNK_Q8_INT8, false>(L, aq, bp, s) : q8_weight_tile<SNK_Q8_E4M3, false>(L, aq, bp, s);
             else
-                st = int8 ? q8_weight_tile<SNK_Q8_INT8, true>(L, a, bp, s) : q8_weight_tile<SNK_Q8_E4M3, true>(L, a, bp, s);
+                st = int8 ? q8_weight_tile<SNK_Q8_INT8, true>(L, aq, bp, s) : q8_weight_tile<SNK_Q8_E4M3, true>(L, aq, bp, s);
             if (st != SNK_OK) return st;
             continue;
         }

@@ -5,7 +5,10 @@
 //   dy()         a value of dY as the lane multiplies it
 //   Dy           the lane's values of a row of dY
 //   dot<SMEM>()  the lane's share of an entry's dot product
+//   DwArgs       the kernel's arguments
 #pragma once
+
+#include <type_traits>
 
 #include "snk_device.cuh"
 
@@ -21,11 +24,6 @@ struct SddmmArgs {
     int n_blocks;
     const float* X;         // [b, in] (tile)
     const void* xt;         // [in][BP] (global path)
-    const float* scales;    // 8-bit X: [b, groups], its scales
-    const uint8_t* codes;   // and its codes [b, in]
-    int64_t groups;         // groups of a row
-    int gshift;             // log2 of their columns
-    int64_t table;          // byte offset of the transposed scales in the operand
     const float* dY;        // [b, out] (tile)
     float* dW;              // [nnz]
     bool accumulate;        // add to dW (later batch tiles)
@@ -33,12 +31,25 @@ struct SddmmArgs {
     int64_t b_all;
     float* db;              // [out] or null
 };
+// With an 8-bit X.
+struct SddmmQ8Args : SddmmArgs {
+    explicit SddmmQ8Args(const SddmmArgs& a) : SddmmArgs(a) {}
+    const float* scales = nullptr;    // [b, groups]
+    const uint8_t* codes = nullptr;   // [b, in]
+    int64_t groups = 0;     // groups of a row
+    int64_t table = 0;      // byte offset of the transposed scales in the operand
+    int gshift = 0;         // log2 of a group's columns
+};
 
-// The fp32 X.
+// The fp32 X.  How long a kernel's argument block is changes what the compiler spills:
+// with the 8-bit fields in it 16 columns in shared memory are slower (3000 x 3000 at 80%:
+// 23.1 us against 22.4) and 32 and 64 faster (8000 x 800 at 80%, 64: 37.5 against 39.3),
+// so those alone have them.
 template <int B>
 struct DwTileF32 : Tile<B> {
     using TL = Tile<B>;
     using Elem = float;
+    using DwArgs = std::conditional_t<(B >= 32), SddmmQ8Args, SddmmArgs>;
     static constexpr int BP = B;
     struct Dy {
         float v[TL::VEC];
@@ -63,7 +74,7 @@ struct DwTileF32 : Tile<B> {
 };
 
 template <class TL>
-__device__ __forceinline__ void load_dy_row(const SddmmArgs& a, int r, int sub, typename TL::Dy& d) {
+__device__ __forceinline__ void load_dy_row(const typename TL::DwArgs& a, int r, int sub, typename TL::Dy& d) {
 #pragma unroll
     for (int j = 0; j < TL::VEC; ++j) {
         const int beta = TL::beta(sub, j);
@@ -77,7 +88,7 @@ __device__ __forceinline__ void load_dy_row(const SddmmArgs& a, int r, int sub, 
 // values of the current row are in registers and the next row's are
 // requested one row ahead.
 template <class TL, bool SMEM, bool I16 = SMEM && SNK_IDX16>
-__global__ void __launch_bounds__(kThreads, 1) k_sddmm(const SddmmArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_sddmm(const typename TL::DwArgs a) {
     using Elem = typename TL::Elem;
     constexpr int VEC = TL::VEC, LPE = TL::LPE, GPW = TL::GPW, BP = TL::BP;
     constexpr uint32_t BLK = 4 * GPW;
