@@ -283,7 +283,14 @@ inline int batch_tile(int64_t b) {
 
 // A batch tile of an 8-bit X, in [in][bp] order: whether the products read the codes
 // (else an fp32 copy of the tile).  Codes need a quarter of the bytes but are decoded
-// at every entry.  With group scales an entry reads its scales too, 4 bp bytes, which
+// at every entry.  Up to 4 rows that pays: it saves a launch, and with one scale per row
+// costs no more than the copy's products (one row: 10000 x 10000 at 90% 16.0 against
+// 16.7, 95% 10.8 against 11.7; 3072 x 768 at 90% 4.0 against 5.1; two rows of int8 at
+// 99% 8.6 against 8.3 at worst) — except the forward of one or two rows with groups on
+// wide rows, where the scales' staging outweighs the launch (10000 x 10000 at 95%, one
+// row 12.0 against 11.7, two 13.8 against 12.9; 10000 x 6000 at 90% 12.2 against 12.0;
+// 30000 x 10000 at 95% 24.6 against 23.1; the other way 5000 x 5000 at 80% 10.7
+// against 11.2).  With group scales an entry reads its scales too, 4 bp bytes, which
 // pays up to bp = 16 (us, codes against the copy, 10000 x 10000 at 90%: forward 43
 // against 67, dW 65 against 85; bp = 32: 112 against 99, 152 against 106).  Few entries
 // per column do not repay wider tiles of staged codes (at 99%, 100 per column:
@@ -291,6 +298,7 @@ inline int batch_tile(int64_t b) {
 // against 15 at 16 with groups).
 inline bool q8_codes_tile(const Q8In& q, int bp, int64_t nnz, int64_t in_f, bool weight) {
     const bool row = q.gshift == 31;
+    if (!weight && !row && bp <= 2 && in_f >= 6000) return false;
     if (bp <= 4 || (weight && row)) return true;
     return nnz >= 200 * in_f && (row || bp <= 16);
 }

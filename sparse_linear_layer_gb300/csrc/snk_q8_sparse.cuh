@@ -14,14 +14,17 @@
 // flipped in the transposed operand, which is the form the decoding starts from.
 // Groups within a row have a scale per (row, group) instead: a table of them, groups x
 // BP, follows the transposed codes, an entry reads its column's BP scales from it and
-// multiplies the decoded values.  That pays up to 16 columns; wider tiles, and layers
-// of few entries per column, run on the fp32 kernels (q8_codes_tile).
+// multiplies the decoded values.  That pays up to 16 columns; wider tiles, layers
+// of few entries per column, and the forward of one or two wide rows, run on the fp32
+// kernels (q8_codes_tile).
 //
-// Measured at 10000 x 10000, 90%, int8, batch 1/4/8/16/32/64: forward 15/17/23/34/64/97
-// us (from an fp32 copy of the tile 14/23/42/67/99/129), weight gradient
-// 17/21/28/47/87/138 (23/29/53/85/106/184); in groups of 128, batch 4/8/16: 19/28/43 and
-// 27/37/65.  Bound by the issue of the decoding (6.6 warp instructions per entry at 64
-// rows, 56% of the issue slots) and by the latency of the gathered words.
+// Measured at 10000 x 10000, 90%, int8, a scale per row, batch 1/4/8/16/32: forward
+// 16/20/25/36/68 us (from an fp32 copy of the tile 17/25/43/69/103), weight gradient
+// 17/20/29/48/90 (23/29/54/88/108); 64 rows forward 102 (134), weight gradient at 95%, where
+// the tensor cores do not take it, 85 (118).  In groups of 128, batch 4/8/16: forward
+// 21/29/45, weight gradient 27/38/66.  At 64 rows 56% of the issue slots are busy (6.6
+// warp instructions per entry, the decoding); the rest is the latency of the words
+// gathered through L1 and L2.
 #pragma once
 
 #include "snk_q8.cuh"
