@@ -84,10 +84,7 @@ class SparseLinear(torch.nn.Module):
     def __init__(self, in_features: int, out_features: int, sparsity: float, bias: bool = True,
                  seed: int = 0, device=None, keep: str | None = None, keep_group: int = 0):
         super().__init__()
-        if keep not in (None, "int8", "e4m3") or keep_group not in (0, 32, 64, 128, 256):
-            raise ValueError(f"keep is None, 'int8' or 'e4m3' and keep_group 0, 32, 64, 128 or 256: "
-                             f"got {keep!r}, {keep_group}")
-        self.keep, self.keep_group = keep, keep_group
+        self._set_keep(keep, keep_group)
         device = torch.device(device if device is not None else "cuda")
         density = 1.0 - sparsity
         nnz = synth.nnz_for(out_features, in_features, 100.0 * sparsity)
@@ -99,12 +96,19 @@ class SparseLinear(torch.nn.Module):
 
     @classmethod
     def from_triple(cls, in_features: int, out_features: int, values, rows, cols,
-                    bias: bool = True):
+                    bias: bool = True, keep: str | None = None, keep_group: int = 0):
         self = cls.__new__(cls)
         torch.nn.Module.__init__(self)
+        self._set_keep(keep, keep_group)
         self._bind(in_features, out_features, values.float().contiguous(),
                    rows.int().contiguous(), cols.int().contiguous(), bias)
         return self
+
+    def _set_keep(self, keep, keep_group):
+        if keep not in (None, "int8", "e4m3") or keep_group not in (0, 32, 64, 128, 256):
+            raise ValueError(f"keep is None, 'int8' or 'e4m3' and keep_group 0, 32, 64, 128 or 256: "
+                             f"got {keep!r}, {keep_group}")
+        self.keep, self.keep_group = keep, keep_group
 
     def _bind(self, in_features, out_features, values, rows, cols, bias):
         self.in_features, self.out_features = in_features, out_features

@@ -130,3 +130,21 @@ def test_block_computes_the_gradients_that_are_needed(torch, calls, monkeypatch,
     assert made.count("backward_weight_q8") == first + second and made.count("rmsnorm_backward") == stream
     assert made.count("backward_input") == (stream or first) + stream
     block.close()
+
+
+@pytest.mark.parametrize("keep,group", [("int8", 0), ("e4m3", 64)])
+def test_layer_on_an_existing_triple_keeps_its_input(torch, keep, group):
+    from sparse_linear_layer_gb300.module import SparseLinear
+    a = SparseLinear(200, 130, 0.9, seed=51, keep=keep, keep_group=group)
+    b = SparseLinear.from_triple(200, 130, a.values.detach().clone(), a.rows.clone(), a.cols.clone(), keep=keep,
+                                 keep_group=group)
+    x, gy = torch.randn(7, 200, device="cuda"), torch.randn(7, 130, device="cuda")
+    for layer in (a, b):
+        y = layer(x)
+        assert [t.element_size() for t in y.grad_fn.saved_tensors] == [1, 4]
+        y.backward(gy)
+    assert torch.equal(a.values.grad, b.values.grad)
+    with pytest.raises(ValueError):
+        SparseLinear.from_triple(200, 130, a.values.detach(), a.rows, a.cols, keep="int4")
+    a.close()
+    b.close()
