@@ -79,9 +79,24 @@ class SparseMLP(torch.nn.Module):
     def __init__(self, features: int, hidden: int, sparsity: float, bias: bool = True, eps: float = 1e-5,
                  format: str = "int8", group: int = 0, seed: int = 0, device=None):
         super().__init__()
-        self.up = SparseLinear(features, hidden, sparsity, bias=bias, seed=seed, device=device)
-        self.down = SparseLinear(hidden, features, sparsity, bias=bias, seed=seed + 2, device=device)
-        self.gain = torch.nn.Parameter(torch.ones(features, device=self.up.values.device))
+        self._join(SparseLinear(features, hidden, sparsity, bias=bias, seed=seed, device=device),
+                   SparseLinear(hidden, features, sparsity, bias=bias, seed=seed + 2, device=device), eps, format, group)
+
+    @classmethod
+    def from_layers(cls, up: SparseLinear, down: SparseLinear, eps: float = 1e-5, format: str = "int8", group: int = 0):
+        """A block of two layers that exist (SparseLinear.from_triple): up features ->
+        hidden, down hidden -> features."""
+        if (up.in_features, up.out_features) != (down.out_features, down.in_features):
+            raise ValueError(f"up and down are features -> hidden and hidden -> features: got {up.in_features} -> "
+                             f"{up.out_features} and {down.in_features} -> {down.out_features}")
+        self = cls.__new__(cls)
+        torch.nn.Module.__init__(self)
+        self._join(up, down, eps, format, group)
+        return self
+
+    def _join(self, up, down, eps, format, group):
+        self.up, self.down = up, down
+        self.gain = torch.nn.Parameter(torch.ones(up.in_features, device=up.values.device))
         self.eps, self.format, self.group = eps, format, group
 
     def forward(self, x, residual=None):

@@ -148,3 +148,30 @@ def test_layer_on_an_existing_triple_keeps_its_input(torch, keep, group):
         SparseLinear.from_triple(200, 130, a.values.detach(), a.rows, a.cols, keep="int4")
     a.close()
     b.close()
+
+
+def test_block_of_existing_layers(torch):
+    """Skewed triples in a block: the products of its layers on its own 8-bit
+    matrices."""
+    from sparse_linear_layer_gb300 import q8, synth
+    from sparse_linear_layer_gb300.mlp import SparseMLP
+    from sparse_linear_layer_gb300.module import SparseLinear
+
+    def layer(out_f, in_f, seed):
+        lay = synth.make_layer(out_f, in_f, 90, 0.1, seed, seed + 1, zipf_s=1.2)
+        t = [torch.from_numpy(a).cuda() for a in (lay.values, lay.rows, lay.cols)]
+        return SparseLinear.from_triple(in_f, out_f, *t)
+
+    up, down = layer(200, 96, 61), layer(96, 200, 63)
+    block = SparseMLP.from_layers(up, down, group=32)
+    x = torch.randn(9, 96, device="cuda", requires_grad=True)
+    y = block(x)
+    n, _, _ = q8.rmsnorm(x.detach(), block.gain.detach(), group=32)
+    a = q8.gelu(up._h.forward_q8(n, up.bias.detach()), group=32)
+    assert torch.equal(y, down._h.forward_q8(a, down.bias.detach()))
+    y.sum().backward()
+    assert {k for k, p in block.named_parameters() if p.grad is not None} == {
+        "gain", "up.values", "up.bias", "down.values", "down.bias"}
+    with pytest.raises(ValueError):
+        SparseMLP.from_layers(up, up)
+    block.close()
