@@ -27,9 +27,12 @@ namespace {
 // Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26: erfc(z) =
 // (c1 t + ... + cn t^n) exp(-z^2), t = 1 / (1 + p z), z >= 0; here with n = 6, p =
 // 0.39 and coefficients fitted to 8.3e-9 (weighted least squares, iterated towards
-// equal errors; the five printed terms give 1.5e-7, enough to move codes).  z =
+// equal errors; the five printed terms are off by 1.5e-7 in exact arithmetic).  z =
 // |x| / sqrt(2), the c_i are halved, and the exponential also serves the gradient.
-// With erff and expf the arithmetic, not the bytes, set GELU's time.
+// Evaluated in fp32 the tail is within 2.0e-7, worst near x = 0 (3 units of its last
+// place there); over normal inputs GELU's relative error is 3.3e-8 and its slope's
+// 6.1e-8 (root mean squares; 4.0e-8 with erff and expf).  With those the arithmetic,
+// not the bytes, set GELU's time: the gradient at 16384 x 3072 took 128 us for 67.
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 neg_abs(float2 x) {
     return make_float2(__uint_as_float(__float_as_uint(x.x) | 0x80000000u),
