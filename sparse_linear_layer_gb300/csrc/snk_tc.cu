@@ -567,8 +567,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int row = 32 * lq + lane;
         const int64_t rr = r0 + row;
         if (rr < a.b) {
-            // undo the two power-of-two scalings (each factor a normal float);
-            // a slice of a shared tile leaves its partial sum, in tile
+            // undo the two scalings (each factor a normal float) at once where
+            // their product is normal, too: the sums are of values scaled to
+            // 2^14, and for a row of 10^33 times one factor alone overflows.
+            // A slice of a shared tile leaves its partial sum, in tile
             // coordinates, for k_tc_split_sum
             const float ir = !ok ? __int_as_float(0x7fc00000) : CODES ? a.row_scale[rr] : ldexpf(1.f, -a.row_exp[rr]);
             float* yrow = whole ? a.Y + rr * a.n_seg + s0 : a.part + ((int64_t)jt * kTcM + row) * kTcN;
@@ -578,7 +580,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int j = 0; j < kColsPerThread; ++j) {
                 const int64_t sg = s0 + c0 + j;
                 if (sg < a.n_seg) {
-                    float y = (acc[j] * ir) * __frcp_rn(pw_seg[c0 + j]);
+                    // (1 / 2^e, |e| <= 120, by its exponent)
+                    const float ic = __uint_as_float(0x7f000000u - __float_as_uint(pw_seg[c0 + j]));
+                    const float f = ir * ic, af = fabsf(f);
+                    float y = af >= 0x1p-126f && af <= 0x1p127f ? acc[j] * f : (acc[j] * ir) * ic;
                     if (bias) y += bias[sg];
                     yrow[c0 + j] = y;
                 }
