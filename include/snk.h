@@ -497,6 +497,87 @@ int snk_backward_weight_q8(snk_handle handle, const void* codes, const float* sc
                            int group, const float* dY, int64_t batch, float* dW, float* db,
                            void* stream);
 
+/*
+ * 8-bit forms (E4M3) for the dense products below.  snk_q8_pack_both: x [rows, cols] with
+ * a scale for each 128 columns of a row (codes [rows, cols] at row stride ld, scales
+ * [rows, ceil(cols / 128)]: what snk_q8_pack writes) and x transposed with a scale for
+ * each 128 rows of a column (codes_t [cols, rows] at row stride ld_t, scales_t [cols,
+ * ceil(rows / 128)]); and sums [cols], the sums of x's columns in fp32.  Each of the three
+ * may be NULL.  scratch: snk_q8_pack_both_scratch bytes, 4-byte aligned (NULL without
+ * sums).  snk_q8_pack_blocks: w [rows, cols] with one scale for each 128 x 128 block
+ * (scales [ceil(rows / 128), ceil(cols / 128)]), and the same codes and scales
+ * transposed; either pair may be NULL.  Bytes between a row's end and the stride are
+ * left alone.  x has the element type `dtype` and is contiguous.  Scales and codes follow
+ * the rules above, for the group or block.  rows == 0: sums are zero.  Errors: SNK_ERR_ARG,
+ * SNK_ERR_LIMIT, SNK_ERR_CUDA.
+ */
+int64_t snk_q8_pack_both_scratch(int64_t rows, int64_t cols);
+int snk_q8_pack_both(const void* x, int dtype, int64_t rows, int64_t cols, void* codes, int64_t ld,
+                     float* scales, void* codes_t, int64_t ld_t, float* scales_t, float* sums,
+                     void* scratch, void* stream);
+int snk_q8_pack_blocks(const void* w, int dtype, int64_t rows, int64_t cols, void* codes, int64_t ld,
+                       float* scales, void* codes_t, int64_t ld_t, float* scales_t, void* stream);
+
+/*
+ * Dense products of 8-bit matrices: y = A B^T + bias, A [M, K] and B [N, K] of E4M3
+ * codes.  A has one scale for each 128 columns of a row (a matrix of format SNK_Q8_E4M3
+ * and group 128, as above); B the same (b_blocks 0: [N, ceil(K / 128)]), or one for
+ * each 128 x 128 block (b_blocks 1: [ceil(N / 128), ceil(K / 128)]).
+ *   y_mn = sum_g sa[m, g] sb[n, g] (sum over the group's k of a_mk b_nk) + bias_n
+ * The sum of a group is exact up to the tensor cores' fp32 additions, groups are
+ * added in fp32.  y [M, N] has the type `dtype`, rounded once; bias [N] is fp32 or
+ * NULL.  a and b are 16-byte aligned; lda, ldb >= K are their rows' strides in bytes,
+ * and those that are no multiples of 16 cost a copy into the scratch.  scratch:
+ * snk_q8_matmul_scratch bytes, 256-byte aligned (NULL when that is 0).  M == 0 is a
+ * no-op.  No state and no allocation; may be captured; repeated calls give the same
+ * bits.  A wait in a kernel that runs out (about two seconds) leaves NaN.
+ * Errors: SNK_ERR_ARG, SNK_ERR_LIMIT, SNK_ERR_CUDA.
+ */
+int64_t snk_q8_matmul_scratch(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb);
+int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void* b, int64_t ldb,
+                  const float* b_scales, int b_blocks, int64_t M, int64_t N, int64_t K, const float* bias,
+                  void* y, int dtype, void* scratch, void* stream);
+
+/*
+ * The vocabulary head's loss: softmax cross entropy of the logits z = x W^T, which
+ * are never kept, and its gradients.  No page has a counterpart: [SNACK] Tables 4-5
+ * train language models whose MLPs are truly sparse, and beside such MLPs the logits
+ * are the largest array of a training step.
+ *   lse_r = log sum_v exp z_rv,  loss_r = lse_r - z_r,target(r)
+ * x [rows, cols] and weight [vocab, cols] have the type `dtype` (SNK_F16 or SNK_BF16),
+ * 16-byte aligned; target [rows] is int64, and `ignore` a target whose row takes no
+ * part: its loss and lse are zero, and nothing of it, a NaN least of all, reaches
+ * another output.  A target outside [0, vocab) that is not `ignore` gives the loss NaN.
+ * Logits, sums and losses are fp32 (products of 16-bit numbers, exact, accumulated by
+ * the tensor cores, whose fp32 additions truncate).
+ * reduction 0: loss [rows]; 1: [1], their sum; 2: [1], their mean over the rows that
+ * count (NaN where none does).  lse [rows] or NULL is what the gradient needs.
+ *
+ * snk_vocab_loss_backward: with g_r the upstream gradient of row r's loss (dloss
+ * [rows] for reduction 0, dloss [1] for 1 and, over the rows that count, 2)
+ *   dz_rv = g_r (exp(z_rv - lse_r) - [v = target(r)]),  dx = dz W,  dweight = dz^T x
+ * from logits computed again, a piece of the vocabulary at a time; dx [rows, cols] and
+ * dweight [vocab, cols] have the type `dtype`; either may be NULL.  dz is rounded to
+ * `dtype` (scaled by a power of two) before the two products, which accumulate in fp32.
+ * Ignored rows get dx = 0; a row whose target is out of range gets NaN.
+ *
+ * scratch: snk_vocab_loss_scratch(rows, cols, vocab, backward) bytes (backward 0 or 1)
+ * on the current device, 256-byte aligned: at most about 256 MB (or 512 bytes a row) for
+ * dz, and some copies of x and dx; where cols is no multiple of 8, also copies of x and
+ * weight with padded rows.  No state and no allocation: the calls only enqueue work, may be captured into
+ * a graph, and give the same bits when repeated.  rows == 0: dweight and a sum are zero,
+ * a mean is NaN.  A wait in a kernel that runs out (about two seconds) leaves NaN.
+ * Errors: SNK_ERR_ARG, SNK_ERR_LIMIT (sizes of 2^31 and more, or too many tiles), SNK_ERR_CUDA.
+ */
+int64_t snk_vocab_loss_scratch(int64_t rows, int64_t cols, int64_t vocab, int backward);
+int snk_vocab_loss(const void* x, const void* weight, int dtype, const int64_t* target, int64_t ignore,
+                   int64_t rows, int64_t cols, int64_t vocab, int reduction, float* loss, float* lse,
+                   void* scratch, void* stream);
+int snk_vocab_loss_backward(const void* x, const void* weight, int dtype, const int64_t* target,
+                            int64_t ignore, const float* lse, const float* dloss, int64_t rows,
+                            int64_t cols, int64_t vocab, int reduction, void* dx, void* dweight,
+                            void* scratch, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,7 +12,7 @@ not touch the GPU.
 """
 import importlib
 
-__all__ = ["synth", "binding", "q8", "module", "mlp"]
+__all__ = ["synth", "binding", "q8", "module", "mlp", "dense"]
 
 
 def __getattr__(name):

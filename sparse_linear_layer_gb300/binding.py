@@ -81,20 +81,32 @@ def lib():
         L.snk_rmsnorm_backward.argtypes = [P, P, I, P, P, P, i64, i64, P, P, P, P]
         L.snk_forward_q8.argtypes = [P, P, P, I, I, i64, P, P, P]
         L.snk_backward_weight_q8.argtypes = [P, P, P, I, I, P, i64, P, P, P]
+        L.snk_q8_pack_both_scratch.argtypes = [i64, i64]
+        L.snk_q8_pack_both_scratch.restype = i64
+        L.snk_q8_pack_both.argtypes = [P, I, i64, i64, P, i64, P, P, i64, P, P, P, P]
+        L.snk_q8_pack_blocks.argtypes = [P, I, i64, i64, P, i64, P, P, i64, P, P]
+        L.snk_q8_matmul_scratch.argtypes = [i64, i64, i64, i64, i64]
+        L.snk_q8_matmul_scratch.restype = i64
+        L.snk_q8_matmul.argtypes = [P, i64, P, P, i64, P, I, i64, i64, i64, P, P, I, P, P]
+        L.snk_vocab_loss_scratch.argtypes = [i64, i64, i64, I]
+        L.snk_vocab_loss_scratch.restype = i64
+        L.snk_vocab_loss.argtypes = [P, P, I, P, i64, i64, i64, i64, I, P, P, P, P]
+        L.snk_vocab_loss_backward.argtypes = [P, P, I, P, i64, P, P, i64, i64, i64, I, P, P, P, P]
         for name in ("snk_create", "snk_forward", "snk_backward_input", "snk_backward_weight",
                      "snk_prune_regrow", "snk_prune_regrow_gradient", "snk_destroy",
                      "snk_get_shape", "snk_copy_topology", "snk_check", "snk_forward_csr_noalloc",
                      "snk_pcsr_build", "snk_pcsr_info", "snk_pcsr_copy", "snk_pcsr_insert",
                      "snk_pcsr_delete", "snk_pcsr_compact", "snk_pcsr_export", "snk_q8_pack",
                      "snk_q8_unpack", "snk_gelu_q8", "snk_gelu_backward_q8", "snk_rmsnorm_q8",
-                     "snk_rmsnorm_backward", "snk_forward_q8", "snk_backward_weight_q8"):
+                     "snk_rmsnorm_backward", "snk_forward_q8", "snk_backward_weight_q8",
+                     "snk_q8_pack_both", "snk_q8_pack_blocks", "snk_q8_matmul", "snk_vocab_loss", "snk_vocab_loss_backward"):
             getattr(L, name).restype = I
         _lib = L
         return L
 
 
 def ops():
-    """The native module that makes the 8-bit activation calls on torch tensors
+    """The native module that makes the calls on 8-bit matrices and the vocabulary loss on torch tensors
     (csrc/q8_ops.cpp), bound to the same library."""
     global _ops
     if _ops is None:
@@ -324,6 +336,61 @@ def snk_backward_weight_q8(handle: int, codes, scales, format: int, group: int, 
     _check(lib().snk_backward_weight_q8(handle, _ptr(codes), _ptr(scales), format, group, _ptr(dY),
                                         batch, _ptr(dW), _ptr(db), _stream(stream)),
            "snk_backward_weight_q8")
+
+
+def _rows_ptr(t):
+    """(pointer, row stride) of a matrix whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError("a matrix with contiguous rows is needed")
+    return t.data_ptr(), t.stride(0)
+
+
+def snk_q8_pack_both_scratch(rows: int, cols: int) -> int:
+    """Bytes of scratch that snk_q8_pack_both needs for sums."""
+    return lib().snk_q8_pack_both_scratch(rows, cols)
+
+
+def snk_q8_pack_both(x, dtype: int, rows: int, cols: int, codes=None, scales=None, codes_t=None, scales_t=None,
+                     sums=None, scratch=None, stream=None):
+    _check(lib().snk_q8_pack_both(_ptr(x), dtype, rows, cols, *_rows_ptr(codes), _ptr(scales), *_rows_ptr(codes_t),
+                                  _ptr(scales_t), _ptr(sums), _ptr(scratch), _stream(stream)), "snk_q8_pack_both")
+
+
+def snk_q8_pack_blocks(w, dtype: int, rows: int, cols: int, codes=None, scales=None, codes_t=None, scales_t=None,
+                       stream=None):
+    _check(lib().snk_q8_pack_blocks(_ptr(w), dtype, rows, cols, *_rows_ptr(codes), _ptr(scales), *_rows_ptr(codes_t),
+                                    _ptr(scales_t), _stream(stream)), "snk_q8_pack_blocks")
+
+
+def snk_q8_matmul_scratch(m: int, n: int, k: int, lda: int, ldb: int) -> int:
+    """Bytes of scratch that snk_q8_matmul needs."""
+    return lib().snk_q8_matmul_scratch(m, n, k, lda, ldb)
+
+
+def snk_q8_matmul(a, a_scales, b, b_scales, b_blocks: bool, m: int, n: int, k: int, bias, y, dtype: int, scratch=None,
+                  stream=None):
+    _check(lib().snk_q8_matmul(*_rows_ptr(a), _ptr(a_scales), *_rows_ptr(b), _ptr(b_scales), int(b_blocks), m, n, k,
+                               _ptr(bias), _ptr(y), dtype, _ptr(scratch), _stream(stream)), "snk_q8_matmul")
+
+
+def snk_vocab_loss_scratch(rows: int, cols: int, vocab: int, backward: bool) -> int:
+    """Bytes of scratch that snk_vocab_loss (snk_vocab_loss_backward) needs."""
+    return lib().snk_vocab_loss_scratch(rows, cols, vocab, int(backward))
+
+
+def snk_vocab_loss(x, weight, dtype: int, target, ignore: int, rows: int, cols: int, vocab: int, reduction: int,
+                   loss, lse, scratch, stream=None):
+    _check(lib().snk_vocab_loss(_ptr(x), _ptr(weight), dtype, _ptr(target), ignore, rows, cols, vocab, reduction,
+                                _ptr(loss), _ptr(lse), _ptr(scratch), _stream(stream)), "snk_vocab_loss")
+
+
+def snk_vocab_loss_backward(x, weight, dtype: int, target, ignore: int, lse, dloss, rows: int, cols: int, vocab: int,
+                            reduction: int, dx, dweight, scratch, stream=None):
+    _check(lib().snk_vocab_loss_backward(_ptr(x), _ptr(weight), dtype, _ptr(target), ignore, _ptr(lse), _ptr(dloss),
+                                         rows, cols, vocab, reduction, _ptr(dx), _ptr(dweight), _ptr(scratch),
+                                         _stream(stream)), "snk_vocab_loss_backward")
 
 
 class SparseLinear:

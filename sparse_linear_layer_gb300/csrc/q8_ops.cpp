@@ -1,9 +1,9 @@
-// Python entry points of the 8-bit activation calls on torch tensors: argument
-// checks, outputs, the current stream, and the call into libsnk, in one native
+// Python entry points of the 8-bit matrices' calls and of the vocabulary loss on torch
+// tensors: argument checks, outputs, the current stream, and the call into libsnk, in one native
 // step.  (Through ctypes and torch's Python API a call took 16 to 24 us of host
 // time, most of a decoding step; here 4 to 9.)  The module is built against torch's
-// headers beside libsnk.so, which load() opens; q8.py and binding.py are its
-// only users.  Wrong tensors raise ValueError, a status from libsnk raises
+// headers beside libsnk.so, which load() opens; q8.py, dense.py and
+// binding.py are its only users.  Wrong tensors raise ValueError, a status from libsnk raises
 // binding.SnkError.
 #include <Python.h>
 
@@ -31,6 +31,14 @@ struct Calls {
     decltype(&snk_rmsnorm_backward_scratch) scratch = nullptr;
     decltype(&snk_forward_q8) forward = nullptr;
     decltype(&snk_backward_weight_q8) backward_weight = nullptr;
+    decltype(&snk_q8_pack_both_scratch) both_scratch = nullptr;
+    decltype(&snk_q8_pack_both) pack_both = nullptr;
+    decltype(&snk_q8_pack_blocks) pack_blocks = nullptr;
+    decltype(&snk_q8_matmul_scratch) matmul_scratch = nullptr;
+    decltype(&snk_q8_matmul) matmul = nullptr;
+    decltype(&snk_vocab_loss_scratch) vocab_scratch = nullptr;
+    decltype(&snk_vocab_loss) vocab_loss = nullptr;
+    decltype(&snk_vocab_loss_backward) vocab_loss_backward = nullptr;
 } g;
 
 struct Wrong : std::runtime_error {   // becomes ValueError
@@ -380,6 +388,205 @@ PyObject* op_backward_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// The tensor, or a copy of it where it does not start on 16 bytes.
+at::Tensor aligned(const at::Tensor& t) { return ((uintptr_t)t.data_ptr() & 15) ? t.clone() : t; }
+
+int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+// New E4M3 codes [rows, cols] (padded: rows 32 bytes apart, as the products like them, else contiguous).
+at::Tensor new_codes(int64_t rows, int64_t cols, bool padded, const at::TensorOptions& options) {
+    const int64_t ld = padded ? up(cols, 32) : cols;
+    at::Tensor t = at::empty({rows, ld}, options.dtype(at::kFloat8_e4m3fn));
+    return ld == cols ? t : t.narrow(1, 0, cols);
+}
+
+// pack_both(x, want rows, want transposed, want sums, padded, stream)
+//   -> (codes, scales, codes of x^T, scales of x^T, sums), None for what is not wanted
+PyObject* op_pack_both(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&] {
+        const at::Tensor& x = tensor(a[0], "x");
+        const int d = dtype_of(x);
+        const Matrix m(x);
+        const bool padded = PyObject_IsTrue(a[4]);
+        const OnStream on(a[5], x.device());
+        const auto options = x.options().requires_grad(false);
+        at::Tensor codes, scales, codes_t, scales_t, sums, scratch;
+        if (PyObject_IsTrue(a[1])) {
+            codes = new_codes(m.rows, m.cols, padded, options);
+            scales = at::empty({m.rows, groups(m.cols, 128)}, options.dtype(at::kFloat));
+        }
+        if (PyObject_IsTrue(a[2])) {
+            codes_t = new_codes(m.cols, m.rows, padded, options);
+            scales_t = at::empty({m.cols, groups(m.rows, 128)}, options.dtype(at::kFloat));
+        }
+        if (PyObject_IsTrue(a[3])) {
+            sums = at::empty({m.cols}, options.dtype(at::kFloat));
+            scratch = at::empty({g.both_scratch(m.rows, m.cols)}, options.dtype(at::kByte));
+        }
+        // (no codes of an empty matrix: nothing to write)
+        const bool some = m.rows > 0;
+        check(g.pack_both(x.data_ptr(), d, m.rows, m.cols, some ? ptr(codes) : nullptr, codes.defined() ? codes.stride(0) : 0,
+                          some ? (float*)ptr(scales) : nullptr, some ? ptr(codes_t) : nullptr,
+                          codes_t.defined() ? codes_t.stride(0) : 0, some ? (float*)ptr(scales_t) : nullptr,
+                          (float*)ptr(sums), ptr(scratch), on.get()),
+              "snk_q8_pack_both");
+        return tuple(std::move(codes), std::move(scales), std::move(codes_t), std::move(scales_t), std::move(sums));
+    });
+}
+
+// pack_blocks(w, want rows, want transposed, stream) -> (codes, scales, codes of w^T, scales of w^T)
+PyObject* op_pack_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 4, [&] {
+        const at::Tensor& w = tensor(a[0], "w");
+        const int d = dtype_of(w);
+        const Matrix m(w);
+        if (w.dim() != 2 || m.rows < 1) throw Wrong("w is [rows, cols] with rows >= 1: " + what(w));
+        const OnStream on(a[3], w.device());
+        const auto options = w.options().requires_grad(false);
+        const int64_t gr = groups(m.rows, 128), gc = groups(m.cols, 128);
+        at::Tensor codes, scales, codes_t, scales_t;
+        if (PyObject_IsTrue(a[1])) {
+            codes = new_codes(m.rows, m.cols, true, options);
+            scales = at::empty({gr, gc}, options.dtype(at::kFloat));
+        }
+        if (PyObject_IsTrue(a[2])) {
+            codes_t = new_codes(m.cols, m.rows, true, options);
+            scales_t = at::empty({gc, gr}, options.dtype(at::kFloat));
+        }
+        check(g.pack_blocks(w.data_ptr(), d, m.rows, m.cols, ptr(codes), codes.defined() ? codes.stride(0) : 0,
+                            (float*)ptr(scales), ptr(codes_t), codes_t.defined() ? codes_t.stride(0) : 0,
+                            (float*)ptr(scales_t), on.get()),
+              "snk_q8_pack_blocks");
+        return tuple(std::move(codes), std::move(scales), std::move(codes_t), std::move(scales_t));
+    });
+}
+
+// Codes of a product's operand: E4M3, rows of contiguous columns, any stride between rows.
+struct Operand {
+    at::Tensor codes;
+    const at::Tensor& scales;
+    int64_t rows, cols;
+    Operand(PyObject* c, PyObject* s, const char* name) : codes(tensor(c, name)), scales(tensor(s, "scales")) {
+        const bool matrix = codes.dim() == 2 && codes.stride(1) == 1 && codes.stride(0) >= codes.size(1);
+        if (!codes.is_cuda() || codes.scalar_type() != at::kFloat8_e4m3fn || codes.dim() < 1 || codes.size(-1) < 1 ||
+            !(matrix || codes.is_contiguous()))
+            throw Wrong(std::string(name) + " has float8_e4m3fn codes [..., cols] with cols >= 1 on a CUDA device: " + what(codes));
+        cols = codes.size(-1);
+        rows = codes.numel() / cols;
+    }
+};
+
+// matmul(a codes, a scales, b codes, b scales, b in blocks, bias or None, dtype, out or None, stream) -> y
+PyObject* op_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&] {
+        Operand x(a[0], a[1], "a"), w(a[2], a[3], "b");
+        const bool blocks = PyObject_IsTrue(a[4]);
+        const int d = (int)integer(a[6]);
+        if (d < SNK_F32 || d > SNK_BF16) throw Wrong("float32, float16 or bfloat16 is needed");
+        const auto device = x.codes.device();
+        if (w.codes.dim() != 2 || w.rows < 1 || w.cols != x.cols || w.codes.device() != device)
+            throw Wrong("b is [n, " + std::to_string(x.cols) + "] with n >= 1 on a's device: " + what(w.codes));
+        const int64_t gk = groups(x.cols, 128);
+        require_f32(x.scales, x.rows * gk, device, "a's scales");
+        require_f32(w.scales, (blocks ? groups(w.rows, 128) : w.rows) * gk, device, "b's scales");
+        const at::Tensor bias = optional(a[5], "bias");
+        if (bias.defined()) require_f32(bias, w.rows, device, "bias");
+        const OnStream on(a[8], device);
+        const auto options = x.codes.options().requires_grad(false);
+        const auto type = d == SNK_F32 ? at::kFloat : d == SNK_F16 ? at::kHalf : at::kBFloat16;
+        c10::SmallVector<int64_t, 5> shape(x.codes.sizes().begin(), x.codes.sizes().end());
+        shape.back() = w.rows;
+        at::Tensor y = optional(a[7], "out");
+        if (!y.defined()) y = at::empty(shape, options.dtype(type));
+        else if (y.sizes() != at::IntArrayRef(shape) || y.scalar_type() != type || y.device() != device || !y.is_contiguous())
+            throw Wrong("out is contiguous, of the product's shape, type and device: " + what(y));
+        x.codes = aligned(x.codes);
+        w.codes = aligned(w.codes);
+        const int64_t lda = x.codes.is_contiguous() ? x.cols : x.codes.stride(0);
+        const int64_t ldb = w.codes.is_contiguous() ? w.cols : w.codes.stride(0);
+        at::Tensor scratch;
+        const int64_t bytes = g.matmul_scratch(x.rows, w.rows, x.cols, lda, ldb);
+        if (bytes > 0) scratch = at::empty({bytes}, options.dtype(at::kByte));
+        check(g.matmul(x.codes.data_ptr(), lda, (const float*)x.scales.data_ptr(), w.codes.data_ptr(), ldb,
+                       (const float*)w.scales.data_ptr(), blocks, x.rows, w.rows, x.cols, (const float*)ptr(bias), y.data_ptr(),
+                       d, ptr(scratch), on.get()),
+              "snk_q8_matmul");
+        return THPVariable_Wrap(std::move(y));
+    });
+}
+
+// The operands of the vocabulary loss.
+struct Head {
+    at::Tensor x, weight;
+    const at::Tensor& target;
+    int dtype;
+    int64_t ignore, rows, cols, vocab;
+    int reduction;
+    Head(PyObject* px, PyObject* pw, PyObject* pt, PyObject* pi, PyObject* pr)
+        : x(tensor(px, "x")), weight(tensor(pw, "weight")), target(tensor(pt, "target")), ignore(integer(pi)) {
+        const Matrix m(x), w(weight);
+        if ((x.scalar_type() != at::kHalf && x.scalar_type() != at::kBFloat16) || x.scalar_type() != weight.scalar_type())
+            throw Wrong("x and weight are both float16 or both bfloat16: " + what(x) + "; " + what(weight));
+        if (weight.dim() != 2 || w.cols != m.cols || weight.device() != x.device() || w.rows < 1)
+            throw Wrong("weight is [vocab, " + std::to_string(m.cols) + "] with vocab >= 1 on x's device: " + what(weight));
+        if (target.scalar_type() != at::kLong || target.sizes() != x.sizes().slice(0, x.dim() - 1) ||
+            target.device() != x.device() || !target.is_contiguous())
+            throw Wrong("target is contiguous int64 with the leading dimensions of x (" + what(x) + "): " + what(target));
+        dtype = dtype_of(x);
+        rows = m.rows;
+        cols = m.cols;
+        vocab = w.rows;
+        const int64_t r = integer(pr);
+        if (r < 0 || r > 2) throw Wrong("reduction is 0 (none), 1 (sum) or 2 (mean)");
+        reduction = (int)r;
+    }
+    // on the call's stream: copies where an operand is not aligned, and scratch
+    at::Tensor scratch(bool backward) {
+        x = aligned(x);
+        weight = aligned(weight);
+        return at::empty({g.vocab_scratch(rows, cols, vocab, backward)}, x.options().requires_grad(false).dtype(at::kByte));
+    }
+};
+
+// vocab_loss(x, weight, target, ignore, reduction, stream) -> (loss, lse)
+PyObject* op_vocab_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&] {
+        Head h(a[0], a[1], a[2], a[3], a[4]);
+        const OnStream on(a[5], h.x.device());
+        const auto options = h.x.options().requires_grad(false).dtype(at::kFloat);
+        at::Tensor lse = at::empty(h.target.sizes(), options);
+        at::Tensor loss = h.reduction == 0 ? at::empty(h.target.sizes(), options) : at::empty({}, options);
+        const at::Tensor scratch = h.scratch(false);
+        check(g.vocab_loss(h.x.data_ptr(), h.weight.data_ptr(), h.dtype, (const int64_t*)h.target.data_ptr(), h.ignore, h.rows,
+                           h.cols, h.vocab, h.reduction, (float*)loss.data_ptr(), (float*)lse.data_ptr(),
+                           ptr(scratch), on.get()),
+              "snk_vocab_loss");
+        return tuple(std::move(loss), std::move(lse));
+    });
+}
+
+// vocab_loss_backward(x, weight, target, ignore, reduction, lse, dloss, want dx, want dweight, stream)
+//   -> (dx or None, dweight or None)
+PyObject* op_vocab_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        Head h(a[0], a[1], a[2], a[3], a[4]);
+        const at::Tensor& lse = tensor(a[5], "lse");
+        const at::Tensor& dloss = tensor(a[6], "dloss");
+        require_f32(lse, h.rows, h.x.device(), "lse");
+        require_f32(dloss, h.reduction == 0 ? h.rows : 1, h.x.device(), "dloss");
+        const OnStream on(a[9], h.x.device());
+        const auto options = h.x.options().requires_grad(false);
+        at::Tensor dx, dw;
+        if (PyObject_IsTrue(a[7])) dx = at::empty(h.x.sizes(), options);
+        if (PyObject_IsTrue(a[8])) dw = at::empty(h.weight.sizes(), options);
+        const at::Tensor scratch = h.scratch(true);
+        check(g.vocab_loss_backward(h.x.data_ptr(), h.weight.data_ptr(), h.dtype, (const int64_t*)h.target.data_ptr(), h.ignore,
+                                    (const float*)lse.data_ptr(), (const float*)dloss.data_ptr(), h.rows, h.cols, h.vocab,
+                                    h.reduction, ptr(dx), ptr(dw), ptr(scratch), on.get()),
+              "snk_vocab_loss_backward");
+        return tuple(std::move(dx), std::move(dw));
+    });
+}
+
 // load(path of libsnk.so, binding.SnkError)
 PyObject* op_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 2) {
@@ -408,8 +615,16 @@ PyObject* op_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     find(c.scratch, "snk_rmsnorm_backward_scratch");
     find(c.forward, "snk_forward_q8");
     find(c.backward_weight, "snk_backward_weight_q8");
+    find(c.both_scratch, "snk_q8_pack_both_scratch");
+    find(c.pack_both, "snk_q8_pack_both");
+    find(c.pack_blocks, "snk_q8_pack_blocks");
+    find(c.matmul_scratch, "snk_q8_matmul_scratch");
+    find(c.matmul, "snk_q8_matmul");
+    find(c.vocab_scratch, "snk_vocab_loss_scratch");
+    find(c.vocab_loss, "snk_vocab_loss");
+    find(c.vocab_loss_backward, "snk_vocab_loss_backward");
     if (!ok) {
-        PyErr_SetString(PyExc_RuntimeError, "libsnk.so lacks an 8-bit activation call");
+        PyErr_SetString(PyExc_RuntimeError, "libsnk.so lacks a call of this module");
         return nullptr;
     }
     g = c;
@@ -427,6 +642,11 @@ PyMethodDef methods[] = {OP("load", op_load),
                          OP("rmsnorm_backward", op_rmsnorm_backward),
                          OP("forward", op_forward),
                          OP("backward_weight", op_backward_weight),
+                         OP("pack_both", op_pack_both),
+                         OP("pack_blocks", op_pack_blocks),
+                         OP("matmul", op_matmul),
+                         OP("vocab_loss", op_vocab_loss),
+                         OP("vocab_loss_backward", op_vocab_loss_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q8ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

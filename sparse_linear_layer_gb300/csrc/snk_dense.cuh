@@ -1,0 +1,392 @@
+// Dense products of 16-bit matrices on the tensor cores: D = A B^T tile by tile, with
+// the epilogue as a type.  Used by the vocabulary loss (snk_vocab.cu).
+//
+// A is [M, K] and B [N, K], each stored along K (rows of the matrix, "K-major") or along
+// its own dimension ("MN-major": the matrix lies transposed in memory); either way TMA
+// brings 128-byte wide boxes with the 128-byte swizzle.  A tile is 128 CG rows by `bn`
+// columns, CG the CTAs that share it: a pair (CG = 2) runs one MMA of 256 rows over both
+// SMs, each holding its 128 rows of A and half of B's columns, so that B crosses the L2
+// once per pair.  Persistent CTAs, ten warps:
+//   warp 0     TMA loads into a ring of stages (64 columns of K each);
+//   warp 1     issues the MMAs (one thread, of the pair's first CTA) and owns the TMEM
+//              allocation, two accumulators of up to 256 columns that take turns;
+//   warps 2-9  the epilogue: warp w reads the TMEM lanes 32 (w % 4) .. + 31 and, by
+//              w < 6 or not, the first or second half of the columns.
+// Every wait is bounded (kTcWaitCycles); a role whose wait ran out stops, waits for the
+// copies and MMAs that it has issued, and the epilogue writes NaN for every tile that it
+// has not been given.
+#pragma once
+
+#include "snk_q8.cuh"
+#include "snk_tcgen.cuh"
+
+namespace snk {
+
+constexpr int kDenseM = 128;             // rows of a tile per CTA (TMEM lanes)
+constexpr int kDenseN = 256;             // columns of a tile at most
+constexpr int kDenseK = 64;              // columns of K per stage: 128 bytes
+constexpr int kDenseThreads = 320;
+constexpr int kDenseEpilogueWarps = 8;
+constexpr int kDenseBoxBytes = 64 * 128;   // an MN-major box: 64 rows of K, 64 columns
+template <int CG>
+constexpr int kDenseStages = CG == 1 ? 4 : 6;
+template <int CG>
+constexpr int kDenseStageBytes = (kDenseM + kDenseN / CG) * 128;
+template <int CG>
+constexpr int kDenseSmem = kDenseStages<CG> * kDenseStageBytes<CG> + 1024;
+
+struct DenseArgs {
+    int n_mt, n_nt;        // tiles
+    int bn;                // columns of a tile
+    int splits;            // ranges of K, each an item of its own
+    int64_t K;
+    uint32_t idesc;
+    const int32_t* rows;   // on the device: the rows of A (rows_k = 0) or the length of K (1) that count; null: all
+    int rows_k;
+    int group;             // row tiles that sweep the columns together (L2 reuse)
+    int32_t* zero;         // a word that the first CTA clears, or null
+};
+
+// The item of an index: row tile, column tile, range of K.
+struct DenseItem {
+    int mt, nt, split;
+    __device__ __forceinline__ static DenseItem of(int id, int n_mt, int n_nt, int splits, int group) {
+        DenseItem t;
+        const int tiles = n_mt * n_nt;
+        t.split = splits == 1 ? 0 : id / tiles;
+        id -= t.split * tiles;
+        const int gsz = group * n_nt;
+        const int first = (id / gsz) * group;
+        const int gm = min(n_mt - first, group);
+        t.mt = first + (id % gsz) % gm;
+        t.nt = (id % gsz) / gm;
+        return t;
+    }
+};
+
+// kind::f16 instruction descriptor: D fp32, A and B fp16 (0) or bf16 (1).
+inline uint32_t dense_idesc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
+    return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: atoms of 64
+// elements by 8 rows of K, 1024 bytes apart along K, boxes of 64 elements 8 KB apart.
+__device__ __forceinline__ uint64_t desc_mn128(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)(kDenseBoxBytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+template <int CG>
+__device__ __forceinline__ void dense_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+
+// ---- pairs of CTAs -------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of the pair's first CTA's copy of a shared-memory object.
+__device__ __forceinline__ uint32_t first_cta(const void* p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+// (relaxed: what the arrival orders are accumulator reads, by tcgen05.fence; a release at
+// cluster scope waits for all of the warp's memory accesses first, spills and scales among
+// them, and was a third of the 8-bit product's stall cycles)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The MMAs issued so far arrive on the barrier, in both CTAs of a pair.
+template <int CG>
+__device__ __forceinline__ void dense_commit(uint64_t* bar) {
+    if constexpr (CG == 1)
+        mma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+}
+// A 2-d box into this CTA's memory, counted on `bar` (of a pair: the first CTA's).
+template <int CG>
+__device__ __forceinline__ void dense_load(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t cols) {
+    if constexpr (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(at)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(at)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+}
+
+// What the epilogue gets: 32 lanes of a warp hold 32 rows.
+struct DenseTile {
+    int64_t row;       // of this lane, in D
+    int64_t col;       // first column of this warp's half, in D
+    int cols;          // columns of the half
+    int mt, nt, half, split;
+    bool ok;           // false: a wait ran out, write NaN
+    bool none;         // no columns of K: zero
+    int rows;          // rows of A that count (all of them without a device count)
+};
+// 32 accumulator columns.
+__device__ __forceinline__ void dense_read(uint32_t taddr, const DenseTile& t, float (&v)[32]) {
+    uint32_t r[32];
+    tmem_ld32(taddr, r);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+    if (!t.ok || t.none) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = t.ok ? 0.f : __int_as_float(0x7fc00000);
+    }
+}
+
+// Epilogue: a type with Args and static __device__ void run(const Args&, const DenseTile&,
+// uint32_t taddr), taddr the TMEM address of the half's first column on the warp's lanes.
+template <int CG, bool A_MN, bool B_MN, class Epilogue>
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    k_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const DenseArgs a,
+            const typename Epilogue::Args ea) {
+    constexpr int S = kDenseStages<CG>, kStage = kDenseStageBytes<CG>;
+    extern __shared__ __align__(1024) unsigned char dense_raw[];
+    unsigned char* sm = dense_raw + ((1024 - (smem_u32(dense_raw) & 1023)) & 1023);
+    __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin;
+    __shared__ uint32_t tmem_base;
+
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int rank = CG == 1 ? 0 : (int)cluster_rank();
+    if (t == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accf[i], 1);
+            mbar_init(&acce[i], kDenseEpilogueWarps * CG);
+        }
+        mbar_init(&fin, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (a.zero && blockIdx.x == 0) *a.zero = 0;
+    }
+    if (warp == 1) tmem_alloc<CG>(&tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    // a device count of rows shortens M or K; each role finds the same items
+    int n_mt = a.n_mt, rows = 0x7fffffff;
+    int64_t K = a.K;
+    if (a.rows) {
+        const int n = __ldg(a.rows);
+        if (a.rows_k) K = min(K, (int64_t)n);
+        else {
+            n_mt = min(n_mt, (n + kDenseM * CG - 1) / (kDenseM * CG));
+            rows = n;
+        }
+    }
+    const int n_k = (int)((K + kDenseK - 1) / kDenseK);
+    const int items = n_mt * a.n_nt * a.splits;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int half_b = a.bn / CG;   // rows of B that this CTA loads
+    const uint32_t tx = (uint32_t)(kDenseM + half_b) * 128 * CG;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int64_t w = 0;   // stages filled
+            for (int id = first; id < items && ok; id += step) {
+                const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
+                const int k0 = (int)((int64_t)n_k * it.split / a.splits), k1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
+                const int m0 = (it.mt * CG + rank) * kDenseM, n0 = it.nt * a.bn + rank * half_b;
+                for (int k = k0; k < k1; ++k, ++w) {
+                    const int s = (int)(w % S);
+                    if (w >= S && !mbar_wait(&empty[s], (uint32_t)(w / S - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char* sa = sm + s * kStage;
+                    unsigned char* sb = sa + kDenseM * 128;
+                    if (rank == 0) mbar_expect_tx(&full[s], tx);
+                    const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : first_cta(&full[s]);
+                    const int kc = k * kDenseK;
+                    if constexpr (A_MN) {
+                        dense_load<CG>(sa, &map_a, m0, kc, bar);
+                        dense_load<CG>(sa + kDenseBoxBytes, &map_a, m0 + 64, kc, bar);
+                    } else {
+                        dense_load<CG>(sa, &map_a, kc, m0, bar);
+                    }
+                    if constexpr (B_MN) {
+                        for (int j = 0; j < half_b; j += 64)
+                            dense_load<CG>(sb + j * 128, &map_b, n0 + j, kc, bar);
+                    } else {
+                        dense_load<CG>(sb, &map_b, kc, n0, bar);
+                    }
+                }
+            }
+            if (!ok && rank == 0)   // what still lands here, the other CTA's copies among it
+                for (int64_t v = w > S ? w - S : 0; v < w; ++v) mbar_wait(&full[v % S], (uint32_t)(v / S) & 1, kTcDrainCycles);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            bool ok = true;
+            int64_t w = 0;
+            int q = 0;   // accumulators filled
+            for (int id = first; id < items && ok; id += step, ++q) {
+                const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
+                const int k0 = (int)((int64_t)n_k * it.split / a.splits), k1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
+                const int ab = q & 1;
+                if (q >= 2 && !mbar_wait(&acce[ab], (uint32_t)((q >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + ab * kDenseN;
+                for (int k = k0; k < k1; ++k, ++w) {
+                    const int s = (int)(w % S);
+                    if (!mbar_wait(&full[s], (uint32_t)(w / S) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kDenseM * 128;
+#pragma unroll
+                    for (int kk = 0; kk < kDenseK / 16; ++kk) {
+                        // 16 columns of K: 32 bytes along a K-major row, two atoms of an MN-major box
+                        const uint64_t da = A_MN ? desc_mn128(sa + kk * 2048) : desc_sw128(sa + kk * 32);
+                        const uint64_t db = B_MN ? desc_mn128(sb + kk * 2048) : desc_sw128(sb + kk * 32);
+                        dense_mma<CG>(d, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
+                    }
+                    dense_commit<CG>(&empty[s]);
+                }
+                if (ok) dense_commit<CG>(&accf[ab]);
+            }
+            if (!ok) {   // no MMA may still run when the memory is given back
+                dense_commit<CG>(&fin);
+                mbar_wait(&fin, 0, kTcDrainCycles);
+            }
+        }
+    } else {
+        const int half = warp >= 6 ? 1 : 0, quarter = warp & 3;
+        const int hc = a.bn / 2;
+        bool ok = true;
+        int q = 0;
+        for (int id = first; id < items; id += step, ++q) {
+            const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
+            const int ab = q & 1;
+            if (ok) ok = mbar_wait(&accf[ab], (uint32_t)(q >> 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            DenseTile tile;
+            tile.row = (int64_t)(it.mt * CG + rank) * kDenseM + quarter * 32 + lane;
+            tile.col = (int64_t)it.nt * a.bn + half * hc;
+            tile.cols = hc;
+            tile.mt = it.mt;
+            tile.nt = it.nt;
+            tile.half = half;
+            tile.split = it.split;
+            tile.ok = ok;
+            tile.none = (int64_t)n_k * it.split / a.splits == (int64_t)n_k * (it.split + 1) / a.splits;
+            tile.rows = rows;
+            Epilogue::run(ea, tile, tmem + ab * kDenseN + half * hc + ((uint32_t)(quarter * 32) << 16));
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 1) mbar_arrive(&acce[ab]);
+                else mbar_arrive_cluster(first_cta(&acce[ab]));
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();   // no barrier or tile of a CTA goes while the other may still touch it
+    tc_fence_after();
+    if (warp == 1) tmem_free<CG>(tmem, 512);
+}
+
+// 16-bit [rows][len] at row stride ld (a multiple of 8), in boxes of 64 columns by
+// box_rows rows with the 128-byte swizzle; what lies past len or rows reads as zero.
+inline bool dense_map(CUtensorMap* map, const void* base, bool bf16, int64_t len, int64_t rows, int64_t ld, int box_rows) {
+    EncodeTiledFn fn = encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)len, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launch: items run by as many CTAs (pairs) as there are SMs (pairs of SMs), or fewer.
+template <int CG, bool A_MN, bool B_MN, class Epilogue>
+int dense_launch(const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& ea, int num_sms,
+                 cudaStream_t s) {
+    auto* f = k_dense<CG, A_MN, B_MN, Epilogue>;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem<CG>) != cudaSuccess) {
+        cudaGetLastError();
+        return SNK_ERR_CUDA;
+    }
+    const int64_t items = (int64_t)a.n_mt * a.n_nt * a.splits;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));
+    c.blockDim = dim3(kDenseThreads);
+    c.dynamicSmemBytes = kDenseSmem<CG>;
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = CG == 1 ? 0 : 1;
+    if (cudaLaunchKernelEx(&c, f, ma, mb, a, ea) != cudaSuccess) {
+        cudaGetLastError();
+        return SNK_ERR_CUDA;
+    }
+    return SNK_OK;
+}
+
+}  // namespace snk

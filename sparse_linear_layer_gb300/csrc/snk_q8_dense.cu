@@ -1,0 +1,599 @@
+// Dense products of 8-bit matrices, y = A B^T + bias, on the tensor cores.
+//
+// A [M, K] and B [N, K] are E4M3 codes with fp32 scales: A's one for each 128 columns of
+// a row, B's the same or one for each 128 x 128 block:
+//     y_mn = sum_g sa[m, g] sb[n or n / 128, g] (sum_{k in group g} a_mk b_nk) + bias_n
+// Products of two codes are exact in fp32; the sum of a group is the tensor cores' (four
+// MMA steps of 32 columns), the sum over groups is fp32 with rounding, in order.  Since a
+// scale changes every 128 columns, an accumulator lasts one group: two of them in TMEM
+// take turns, and while the tensor cores fill one the epilogue warps multiply the other
+// by its scales into registers.
+//
+// k_q8_dense has the same parts as k_dense (snk_dense.cuh): a stage is one group, 128
+// bytes of a row.  k_q8_rows is for up to 16 rows of A, where the codes of B are read
+// once and nothing else counts.
+#include <algorithm>
+
+#include "snk_dense.cuh"
+
+namespace snk {
+namespace {
+
+// Threads: four warps of roles (TMA, MMA, two that only give up registers) and eight of the
+// epilogue, whose threads keep 128 sums each.  168 registers a thread at launch, redistributed.
+constexpr int kQ8Threads = 384;
+constexpr int kQ8RoleRegs = 72, kQ8SumRegs = 216;
+static_assert(128 * kQ8RoleRegs + 256 * kQ8SumRegs <= kQ8Threads * 168, "the shares come out of the launch's registers");
+template <int R>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+
+struct Q8DenseArgs {
+    int64_t M, N;
+    int n_g;               // groups along K
+    int n_mt, n_nt, splits, group;
+    uint32_t idesc;
+    const float* sa;       // [M, n_g]
+    const float* sb;       // [N, n_g] or [ceil(N / 128), n_g]
+    const float* bias;     // [N] or null
+    void* y;               // [M, N]
+    int dtype;
+    int vec;               // bytes of a store: 32, 16 or an element's, by the rows' alignment
+    float* slab;           // splits > 1: [splits][M, N] sums without bias
+};
+
+template <int CG>
+__device__ __forceinline__ void q8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// Sixteen values of a row from column c on, of which those before `lim` exist.
+template <typename T>
+__device__ __forceinline__ void store16(T* out, int c, int lim, int vec, const float (&v)[16]) {
+    constexpr int E = sizeof(T);
+    uint32_t w[4 * E];
+#pragma unroll
+    for (int i = 0; i < 4 * E; ++i)
+        w[i] = E == 4 ? __float_as_uint(v[i]) : pack2<typename std::conditional<E == 2, T, __half>::type>(
+                                                    make_float2(v[(2 * i) & 15], v[(2 * i + 1) & 15]));
+    if (vec == 32 && c + 16 <= lim) {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = w[8 * i + k];
+            st32(reinterpret_cast<char*>(out + c) + 32 * i, u);
+        }
+    } else if (vec >= 16) {   // whole 16-byte chunks
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (c + i * (16 / E) < lim)
+                *reinterpret_cast<uint4*>(reinterpret_cast<char*>(out + c) + 16 * i) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c + i < lim) out[c + i] = from_f32<T>(v[i]);
+    }
+}
+
+template <int CG, int BN, bool ROWS>
+__global__ void __launch_bounds__(kQ8Threads, 1)
+    k_q8_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Q8DenseArgs a) {
+    constexpr int S = kDenseStages<CG>, kStage = kDenseStageBytes<CG>;
+    constexpr int HB = BN / CG;   // rows of B that a CTA loads
+    constexpr int HC = BN / 2;    // columns of an epilogue warp
+    extern __shared__ __align__(1024) unsigned char q8_raw[];
+    unsigned char* sm = q8_raw + ((1024 - (smem_u32(q8_raw) & 1023)) & 1023);
+    __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin;
+    __shared__ uint32_t tmem_base;
+    __shared__ __align__(16) float sb_s[ROWS ? 2 : 1][BN];   // ROWS: the tile's scales of B, of the current and the next group
+
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int rank = CG == 1 ? 0 : (int)cluster_rank();
+    if (t == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accf[i], 1);
+            mbar_init(&acce[i], kDenseEpilogueWarps * CG);
+        }
+        mbar_init(&fin, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<CG>(&tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const int items = a.n_mt * a.n_nt * a.splits;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+
+    if (warp < 4) {
+        fewer_registers<kQ8RoleRegs>();
+        if (warp == 0 && lane == 0) {
+            bool ok = true;
+            int64_t w = 0;
+            for (int id = first; id < items && ok; id += step) {
+                const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
+                const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
+                const int m0 = (it.mt * CG + rank) * kDenseM, n0 = it.nt * BN + rank * HB;
+                for (int g = g0; g < g1; ++g, ++w) {
+                    const int s = (int)(w % S);
+                    if (w >= S && !mbar_wait(&empty[s], (uint32_t)(w / S - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char* sa = sm + s * kStage;
+                    if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(kDenseM + HB) * 128 * CG);
+                    const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : first_cta(&full[s]);
+                    dense_load<CG>(sa, &map_a, g * 128, m0, bar);
+                    dense_load<CG>(sa + kDenseM * 128, &map_b, g * 128, n0, bar);
+                }
+            }
+            if (!ok && rank == 0)
+                for (int64_t v = w > S ? w - S : 0; v < w; ++v) mbar_wait(&full[v % S], (uint32_t)(v / S) & 1, kTcDrainCycles);
+        }
+        if (warp == 1 && lane == 0 && rank == 0) {
+            bool ok = true;
+            int64_t w = 0;
+            for (int id = first; id < items && ok; id += step) {
+                const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
+                const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
+                for (int g = g0; g < g1; ++g, ++w) {
+                    const int s = (int)(w % S), ab = (int)(w & 1);
+                    if ((w >= 2 && !mbar_wait(&acce[ab], (uint32_t)((w >> 1) - 1) & 1)) ||
+                        !mbar_wait(&full[s], (uint32_t)(w / S) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kDenseM * 128, d = tmem + ab * kDenseN;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        q8_mma<CG>(d, desc_sw128(sa + kk * 32), desc_sw128(sb + kk * 32), a.idesc, kk > 0 ? 1u : 0u);
+                    dense_commit<CG>(&empty[s]);
+                    dense_commit<CG>(&accf[ab]);
+                }
+            }
+            if (!ok) {
+                dense_commit<CG>(&fin);
+                mbar_wait(&fin, 0, kTcDrainCycles);
+            }
+        }
+    } else {
+        more_registers<kQ8SumRegs>();
+        const int half = warp >= 8 ? 1 : 0, quarter = warp & 3, et = t - 128;
+        bool ok = true;
+        int64_t w = 0;
+        for (int id = first; id < items; id += step) {
+            const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
+            const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
+            const int64_t row = (int64_t)(it.mt * CG + rank) * kDenseM + quarter * 32 + lane;
+            const int64_t col = (int64_t)it.nt * BN + half * HC;
+            // rows and columns outside the matrix read the last ones' scales and are not stored
+            const float* pa = a.sa + min(row, a.M - 1) * a.n_g;
+            const float* pb = ROWS ? a.sb + min((int64_t)it.nt * BN + (et < BN ? et : 0), a.N - 1) * a.n_g
+                                   : a.sb + (min(col, a.N - 1) >> 7) * a.n_g;
+            float2 acc[HC / 2];
+#pragma unroll
+            for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+            float na = 0.f, nb = 0.f;
+            if (g0 < g1) {
+                na = __ldg(pa + g0);
+                nb = __ldg(pb + g0);
+            }
+            for (int g = g0; g < g1; ++g, ++w) {
+                const int ab = (int)(w & 1);
+                const float ca = na, cb = nb;
+                if (g + 1 < g1) {
+                    na = __ldg(pa + g + 1);
+                    nb = __ldg(pb + g + 1);
+                }
+                const float* sbp = nullptr;
+                if constexpr (ROWS) {   // (two buffers: a warp may still read the last group's)
+                    if (et < BN) sb_s[ab][et] = cb;
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    sbp = &sb_s[ab][half * HC];
+                }
+                if (ok) ok = mbar_wait(&accf[ab], (uint32_t)(w >> 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                const uint32_t ta = tmem + ab * kDenseN + half * HC + ((uint32_t)(quarter * 32) << 16);
+                const float s = ROWS ? ca : ca * cb;
+                uint32_t r[2][32];   // the next 32 columns are read while these are added
+                tmem_ld32_async(ta, r[0]);
+#pragma unroll
+                for (int c = 0; c < HC; c += 32) {
+                    tmem_wait_ld();
+                    if (c + 32 < HC) tmem_ld32_async(ta + c + 32, r[(c / 32 + 1) & 1]);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const uint32_t(&u)[32] = r[(c / 32) & 1];
+                        const float2 v = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+                        float2 f = make_float2(s, s);
+                        if constexpr (ROWS) f = __fmul2_rn(f, *reinterpret_cast<const float2*>(sbp + c + 2 * j));
+                        acc[c / 2 + j] = __ffma2_rn(v, f, acc[c / 2 + j]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 1) mbar_arrive(&acce[ab]);
+                    else mbar_arrive_cluster(first_cta(&acce[ab]));
+                }
+            }
+            const int lim = row < a.M ? (int)min((int64_t)HC, a.N - col) : 0;
+            if (!ok) {
+#pragma unroll
+                for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
+            }
+            const bool whole = a.splits == 1;
+            const int64_t at = row * a.N + col;
+#pragma unroll
+            for (int c = 0; c < HC; c += 16) {
+                if (c < lim) {
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = (j & 1) ? acc[(c + j) / 2].y : acc[(c + j) / 2].x;
+                    if (whole && a.bias) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (c + j < lim) v[j] += __ldg(a.bias + col + c + j);
+                    }
+                    if (!whole) store16(a.slab + it.split * a.M * a.N + at, c, lim, a.vec, v);
+                    else if (a.dtype == SNK_F32) store16(static_cast<float*>(a.y) + at, c, lim, a.vec, v);
+                    else if (a.dtype == SNK_F16) store16(static_cast<__half*>(a.y) + at, c, lim, a.vec, v);
+                    else store16(static_cast<__nv_bfloat16*>(a.y) + at, c, lim, a.vec, v);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free<CG>(tmem, 512);
+}
+
+// The sum of the splits' parts, in order, and the bias.
+template <typename T>
+__global__ void __launch_bounds__(256) k_q8_join(const float* __restrict__ slab, int splits, int64_t M, int64_t N,
+                                                 const float* __restrict__ bias, T* __restrict__ y) {
+    const int64_t n = M * N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        float v = 0.f;
+        for (int s = 0; s < splits; ++s) v += __ldg(slab + s * n + i);
+        y[i] = from_f32<T>(bias ? v + __ldg(bias + i % N) : v);
+    }
+}
+
+// ---- few rows ---------------------------------------------------------------------
+// Up to 16 rows of A: the call reads B's codes once, N K bytes, and little else, so it is
+// bound by memory and, for small layers, by latency.  A warp takes 16 rows of B and some
+// of the groups; the block's warps share the groups and are added through shared memory.
+// The products are mma.sync m16n8k32 (B's rows as its 16, A's as its 8): a dot product
+// does not care for the order of its columns, so each lane takes 16 consecutive bytes of
+// its two rows of B and of its row of A, 64 columns for four lanes, as the operands of two
+// MMAs.
+constexpr int kRowsMax = 16;
+constexpr int kRowsWarps = 8;
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16 codes of a row from column k on, zeros from K on (what lies there is not read).
+__device__ __forceinline__ uint4 load16(const uint8_t* row, int64_t k, int64_t K) {
+    if (k + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 15; ++i)
+        if (k + i < K) w[i >> 2] |= (uint32_t)row[k + i] << (8 * (i & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct Q8RowsArgs {
+    const uint8_t *a, *b;
+    int64_t lda, ldb;      // multiples of 16
+    int64_t M, N, K;
+    int n_g;
+    const float *sa, *sb;
+    const float* bias;
+    void* y;
+    int dtype;
+    int blocks_b;          // B's scales are of 128 x 128 blocks
+};
+// NT: tiles of 8 rows of A.
+template <int NT, typename T>
+__global__ void __launch_bounds__(32 * kRowsWarps) k_q8_rows(const Q8RowsArgs a) {
+    __shared__ float part[kRowsWarps][16][8 * NT + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t nr0 = n0 + r, nr1 = n0 + r + 8;
+    const uint8_t* b0 = a.b + min(nr0, a.N - 1) * a.ldb;
+    const uint8_t* b1 = a.b + min(nr1, a.N - 1) * a.ldb;
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int g = warp; g < a.n_g; g += kRowsWarps) {
+        float d[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
+        uint4 w0[2], w1[2], x[NT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = (int64_t)g * 128 + h * 64 + q * 16;
+            w0[h] = load16(b0, k, a.K);
+            w1[h] = load16(b1, k, a.K);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) x[i][h] = load16(a.a + min((int64_t)(8 * i + r), a.M - 1) * a.lda, k, a.K);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                mma_e4m3(d[i], w0[h].x, w1[h].x, w0[h].y, w1[h].y, x[i][h].x, x[i][h].y);
+                mma_e4m3(d[i], w0[h].z, w1[h].z, w0[h].w, w1[h].w, x[i][h].z, x[i][h].w);
+            }
+        // d[i]: rows r, r + 8 of B; rows 8 i + 2 q, + 1 of A
+        const float s0 = a.blocks_b ? __ldg(a.sb + (n0 >> 7) * a.n_g + g) : __ldg(a.sb + min(nr0, a.N - 1) * a.n_g + g);
+        const float s1 = a.blocks_b ? s0 : __ldg(a.sb + min(nr1, a.N - 1) * a.n_g + g);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int m = 8 * i + 2 * q;
+            const float t0 = m < a.M ? __ldg(a.sa + (int64_t)m * a.n_g + g) : 0.f;
+            const float t1 = m + 1 < a.M ? __ldg(a.sa + (int64_t)(m + 1) * a.n_g + g) : 0.f;
+            acc[i][0] = fmaf(d[i][0], s0 * t0, acc[i][0]);
+            acc[i][1] = fmaf(d[i][1], s0 * t1, acc[i][1]);
+            acc[i][2] = fmaf(d[i][2], s1 * t0, acc[i][2]);
+            acc[i][3] = fmaf(d[i][3], s1 * t1, acc[i][3]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        part[warp][r][8 * i + 2 * q] = acc[i][0];
+        part[warp][r][8 * i + 2 * q + 1] = acc[i][1];
+        part[warp][r + 8][8 * i + 2 * q] = acc[i][2];
+        part[warp][r + 8][8 * i + 2 * q + 1] = acc[i][3];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * 8 * NT; i += 32 * kRowsWarps) {
+        const int n = i & 15, m = i >> 4;
+        if (n0 + n < a.N && m < a.M) {
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < kRowsWarps; ++k) v += part[k][n][m];
+            if (a.bias) v += __ldg(a.bias + n0 + n);
+            static_cast<T*>(a.y)[m * a.N + n0 + n] = from_f32<T>(v);
+        }
+    }
+}
+
+// Codes [rows, cols] at row stride ld, with rows of whole 16-byte chunks and zeros behind the columns.
+__global__ void __launch_bounds__(256) k_q8_pad(const uint8_t* __restrict__ src, int64_t ld, uint8_t* __restrict__ dst, int64_t rows,
+                                                int64_t cols, int64_t to) {
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8)
+        for (int64_t c = threadIdx.x & 31; c < to; c += 32) dst[r * to + c] = c < cols ? src[r * ld + c] : (uint8_t)0;
+}
+
+// ---- host ------------------------------------------------------------------------------
+
+int64_t up(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
+int sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+int launched() { return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA; }
+
+bool q8_map(CUtensorMap* map, const uint8_t* base, int64_t len, int64_t rows, int64_t ld, int box_rows) {
+    EncodeTiledFn fn = encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)len, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld};
+    cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Q8Plan {
+    bool rows;               // k_q8_rows
+    bool copy_a, copy_b;
+    int cg, bn, n_mt, n_nt, splits;
+    int64_t ld;              // of the copies
+    uint8_t *a, *b;
+    float* slab;
+    int64_t bytes;
+    Q8Plan(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int num_sms, void* scratch) {
+        rows = M <= kRowsMax;
+        copy_a = lda % 16 != 0;
+        copy_b = ldb % 16 != 0;
+        ld = up(K, 16);
+        const int n_g = (int)ceil_div(K, 128);
+        cg = M > 128 && ceil_div(M, 256) * ceil_div(N, 256) >= num_sms / 4 ? 2 : 1;
+        bn = 256;
+        if (cg == 1)
+            while (bn > 64 && ceil_div(M, 128) * ceil_div(N, bn) < num_sms) bn /= 2;
+        n_mt = (int)ceil_div(M, 128 * cg);
+        n_nt = (int)ceil_div(N, bn);
+        const int64_t tiles = (int64_t)n_mt * n_nt, units = num_sms / cg;
+        splits = 1;
+        if (!rows && 2 * tiles <= units) splits = (int)std::max<int64_t>(1, std::min<int64_t>(units / tiles, n_g / 8));
+        char* p = static_cast<char*>(scratch);
+        int64_t used = 0;
+        auto take = [&](int64_t n) {
+            char* q = p + used;
+            used += up(n, 256);
+            return q;
+        };
+        a = reinterpret_cast<uint8_t*>(take(copy_a ? M * ld : 0));
+        b = reinterpret_cast<uint8_t*>(take(copy_b ? N * ld : 0));
+        slab = reinterpret_cast<float*>(take(splits > 1 ? 4 * splits * M * N : 0));
+        bytes = used;
+    }
+};
+
+template <int CG, int BN, bool ROWS>
+int launch_dense(const CUtensorMap& ma, const CUtensorMap& mb, const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
+    auto* f = k_q8_dense<CG, BN, ROWS>;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem<CG>) != cudaSuccess) {
+        cudaGetLastError();
+        return SNK_ERR_CUDA;
+    }
+    const int64_t items = (int64_t)a.n_mt * a.n_nt * a.splits;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));
+    c.blockDim = dim3(kQ8Threads);
+    c.dynamicSmemBytes = kDenseSmem<CG>;
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = CG == 1 ? 0 : 1;
+    if (cudaLaunchKernelEx(&c, f, ma, mb, a) != cudaSuccess) {
+        cudaGetLastError();
+        return SNK_ERR_CUDA;
+    }
+    return SNK_OK;
+}
+template <bool ROWS>
+int launch_dense(const Q8Plan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
+    if (p.cg == 2) return launch_dense<2, 256, ROWS>(ma, mb, a, num_sms, s);
+    if (p.bn == 256) return launch_dense<1, 256, ROWS>(ma, mb, a, num_sms, s);
+    if (p.bn == 128) return launch_dense<1, 128, ROWS>(ma, mb, a, num_sms, s);
+    return launch_dense<1, 64, ROWS>(ma, mb, a, num_sms, s);
+}
+template <typename T>
+int launch_rows(const Q8RowsArgs& r, cudaStream_t s) {
+    const unsigned blocks = (unsigned)ceil_div(r.N, 16);
+    if (r.M <= 8) k_q8_rows<1, T><<<blocks, 32 * kRowsWarps, 0, s>>>(r);
+    else k_q8_rows<2, T><<<blocks, 32 * kRowsWarps, 0, s>>>(r);
+    return launched();
+}
+template <typename T>
+int launch_join(const Q8Plan& p, int64_t M, int64_t N, const float* bias, void* y, int num_sms, cudaStream_t s) {
+    k_q8_join<T><<<(unsigned)std::min<int64_t>(ceil_div(M * N, 256), 8 * num_sms), 256, 0, s>>>(p.slab, p.splits, M, N, bias,
+                                                                                               static_cast<T*>(y));
+    return launched();
+}
+
+int bad_product(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 1 || K < 1) return SNK_ERR_ARG;
+    const int64_t lim = INT32_MAX - 512;
+    if (M > lim || N > lim || K > lim || (double)ceil_div(M, 128) * (double)ceil_div(N, 64) > 1.0e9) return SNK_ERR_LIMIT;
+    return SNK_OK;
+}
+
+}  // namespace
+}  // namespace snk
+
+using namespace snk;
+
+extern "C" {
+
+int64_t snk_q8_matmul_scratch(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
+    if (M < 1 || bad_product(M, N, K) != SNK_OK) return 0;
+    const int n = sms();
+    return n < 1 ? 0 : Q8Plan(M, N, K, lda, ldb, n, nullptr).bytes;
+}
+
+int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void* b, int64_t ldb, const float* b_scales,
+                  int b_blocks, int64_t M, int64_t N, int64_t K, const float* bias, void* y, int dtype, void* scratch,
+                  void* stream) {
+    if (int st = bad_product(M, N, K); st != SNK_OK) return st;
+    if (dtype < SNK_F32 || dtype > SNK_BF16 || lda < K || ldb < K) return SNK_ERR_ARG;
+    auto off = [](const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; };
+    if (!b || !b_scales || off(a, 16) || off(b, 16) || off(a_scales, 4) || off(b_scales, 4) || off(bias, 4) ||
+        off(y, dtype == SNK_F32 ? 4 : 2) || off(scratch, 256))
+        return SNK_ERR_ARG;
+    if (M == 0) return SNK_OK;
+    if (!a || !a_scales || !y) return SNK_ERR_ARG;
+    const int n = sms();
+    if (n < 1) return SNK_ERR_CUDA;
+    const Q8Plan p(M, N, K, lda, ldb, n, scratch);
+    if (p.bytes > 0 && !scratch) return SNK_ERR_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    auto copy = [&](const void* src, int64_t ld, uint8_t* dst, int64_t rows) {
+        k_q8_pad<<<(unsigned)std::min<int64_t>(ceil_div(rows, 8), 8 * n), 256, 0, s>>>(static_cast<const uint8_t*>(src), ld, dst,
+                                                                                    rows, K, p.ld);
+        return launched();
+    };
+    const uint8_t *pa = static_cast<const uint8_t*>(a), *pb = static_cast<const uint8_t*>(b);
+    if (p.copy_a) {
+        if (int st = copy(a, lda, p.a, M); st != SNK_OK) return st;
+        pa = p.a;
+        lda = p.ld;
+    }
+    if (p.copy_b) {
+        if (int st = copy(b, ldb, p.b, N); st != SNK_OK) return st;
+        pb = p.b;
+        ldb = p.ld;
+    }
+    const int n_g = (int)ceil_div(K, 128);
+    if (p.rows) {
+        const Q8RowsArgs r{pa, pb, lda, ldb, M, N, K, n_g, a_scales, b_scales, bias, y, dtype, b_blocks};
+        return dtype == SNK_F32 ? launch_rows<float>(r, s) : dtype == SNK_F16 ? launch_rows<__half>(r, s) : launch_rows<__nv_bfloat16>(r, s);
+    }
+    CUtensorMap ma, mb;
+    if (!q8_map(&ma, pa, K, M, lda, kDenseM) || !q8_map(&mb, pb, K, N, ldb, p.bn / p.cg)) return SNK_ERR_CUDA;
+    Q8DenseArgs q = {};
+    q.M = M;
+    q.N = N;
+    q.n_g = n_g;
+    q.n_mt = p.n_mt;
+    q.n_nt = p.n_nt;
+    q.splits = p.splits;
+    q.group = 16 / p.cg;
+    q.idesc = (1u << 4) | ((uint32_t)(p.bn >> 3) << 17) | ((uint32_t)((128 * p.cg) >> 4) << 24);   // fp32; E4M3, K-major
+    q.sa = a_scales;
+    q.sb = b_scales;
+    q.bias = bias;
+    q.y = y;
+    q.dtype = dtype;
+    q.slab = p.slab;
+    const int e = p.splits > 1 || dtype == SNK_F32 ? 4 : 2;
+    const uintptr_t base = (uintptr_t)(p.splits > 1 ? (void*)p.slab : y) | (uintptr_t)(N * e);
+    q.vec = (base & 31) == 0 ? 32 : ((base & 15) == 0 ? 16 : e);
+    const int st = b_blocks ? launch_dense<false>(p, ma, mb, q, n, s) : launch_dense<true>(p, ma, mb, q, n, s);
+    if (st != SNK_OK || p.splits == 1) return st;
+    return dtype == SNK_F32   ? launch_join<float>(p, M, N, bias, y, n, s)
+           : dtype == SNK_F16 ? launch_join<__half>(p, M, N, bias, y, n, s)
+                              : launch_join<__nv_bfloat16>(p, M, N, bias, y, n, s);
+}
+
+}  // extern "C"

@@ -46,6 +46,7 @@
 #include <type_traits>
 
 #include "snk_q8.cuh"
+#include "snk_tcgen.cuh"
 
 namespace snk {
 
@@ -138,16 +139,6 @@ constexpr int kTcSmem = kStagesA * kStageA + kStagesB * kStageB + kRecSlots * kR
 constexpr uint32_t kAccStride = 256;              // TMEM columns between the two accumulators
 constexpr uint32_t kTmemCols = 512;
 constexpr int kColsPerThread = kTcN / 2;          // accumulator columns each builder drains
-// Limit of a pipeline wait (about two seconds at the boost clock); a build
-// may shorten it (SNK_TC_WAIT_CYCLES) to exercise the abort path.  A wait
-// that runs out stops the CTA's pipeline: every role then waits, with the
-// fixed drain limit, for the copies and MMAs it has issued, the outputs are
-// written as NaN and the status word records kStatLimit.
-#ifndef SNK_TC_WAIT_CYCLES
-#define SNK_TC_WAIT_CYCLES 4000000000LL
-#endif
-constexpr long long kTcWaitCycles = SNK_TC_WAIT_CYCLES;
-constexpr long long kTcDrainCycles = 4000000000LL;
 // kind::f16 instruction descriptor: D fp32, A and B fp16, both K-major,
 // N = kTcN, M = kTcM.
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kTcN >> 3) << 17) | ((uint32_t)(kTcM >> 4) << 24);
@@ -161,10 +152,6 @@ constexpr int kTcPad = 16;         // entries readable past nnz in the tile-orde
 constexpr uint32_t kRankSpan = 512;
 static_assert(kTcN * kTcK / 64 * 2 <= (int)kRankSpan, "rank within a bank fits its field");
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
 // Byte offset of fp16 element (row i, column k < 64) in a K-major tile with
 // the 128-byte swizzle: 8-row atoms of 1024 bytes, 16-byte chunks XORed with
 // the row within the atom (the layout a 128-byte-swizzled TMA load writes).
@@ -172,93 +159,12 @@ __device__ __forceinline__ uint32_t sw128(int i, int k) {
     return (uint32_t)((i >> 3) * 1024 + (i & 7) * 128 + (((k >> 3) ^ (i & 7)) << 4) + (k & 7) * 2);
 }
 
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ void mbar_init(uint64_t* b, int count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes)
-                 : "memory");
-}
-// Bounded wait on a phase; false once `limit` cycles have passed.
-__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, long long limit = kTcWaitCycles) {
-    long long t0 = 0;
-    for (int spin = 0;; ++spin) {
-        uint32_t ok;
-        asm volatile(
-            "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-            : "=r"(ok)
-            : "r"(smem_u32(b)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if (spin == 0)
-            t0 = clock64();
-        else if (clock64() - t0 > limit)
-            return false;
-    }
-}
-// After a pipeline stopped early: wait for the last `issued` uses of a ring of
-// `slots` barriers (window w used barrier w % slots in its (w / slots)-th
-// phase), i.e. for every copy still landing in shared memory.
-__device__ __forceinline__ bool drain_ring(uint64_t* bars, int slots, int issued) {
-    bool ok = true;
-    for (int w = issued > slots ? issued - slots : 0; w < issued; ++w)
-        if (!mbar_wait(&bars[w % slots], (w / slots) & 1, kTcDrainCycles)) ok = false;
-    return ok;
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
         : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
-// 32 consecutive accumulator columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // OR of a flag over the 256 builder threads (named barrier 1).
 __device__ __forceinline__ bool builders_any(bool flag) {
@@ -1738,27 +1644,6 @@ void mark_tc_views(Layer* L) {
 }
 
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, resolved once through the runtime.
-EncodeTiledFn encoder() {
-    static EncodeTiledFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        tried = true;
-        cudaDriverEntryPointQueryResult q;
-        void* f = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(f);
-        cudaGetLastError();
-    }
-    return fn;
-}
 
 // fp16 [rows][len] at row stride ks, loaded in 64 x 128 boxes with the
 // 128-byte swizzle; reads past len or rows come back as zeros.

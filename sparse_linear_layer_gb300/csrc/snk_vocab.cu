@@ -1,0 +1,887 @@
+// Softmax cross entropy over a large vocabulary, loss and gradients, without the logits.
+//
+//   z = x W^T,  lse_r = log sum_v exp z_rv,  loss_r = lse_r - z_r,t(r)
+//   dz_rv = g_r (exp(z_rv - lse_r) - [v = t(r)]),  dx = dz W,  dW = dz^T x
+//
+// x [rows, cols] and W [vocab, cols] are bf16 or fp16, everything else fp32.  A row whose
+// target is `ignore` takes no part: its loss and dx are zero, and neither its x nor its
+// upstream gradient reaches dW, whatever they hold.
+//
+// Four products (snk_dense.cuh), all tiles of 256 logits by 128 or 256 rows:
+//   LseEpilogue    z, and for each row and half tile its largest logit and the sum of
+//                  exp(z - largest): 8 bytes leave the SM for 128 logits; k_vocab_finish
+//                  joins them and takes z_r,t as a dot product of its own
+//   GradEpilogue   z once more, dz rounded to 16 bits for a piece of the vocabulary
+//   SumEpilogue    dx += dz W over the piece, fp32
+//   StoreEpilogue  the piece's rows of dW = dz^T x, complete
+// The gradient's rows are gathered first (k_vocab_rows): the rows that count, side by
+// side, zeros up to a whole tile; ignored rows then cost nothing, and the count stays on
+// the device.  dz is held as c_r 2^13 (p - [v = t]) with c_r = g_r / G, G the power of two
+// next to the largest |g|, so that probabilities down to 2^-37 stay normal fp16 numbers;
+// the rounding of dz to 16 bits is one rounding of half a unit per term of a sum whose
+// result is rounded to the same type.
+#include <algorithm>
+
+#include "snk_dense.cuh"
+
+namespace snk {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kGatherRows = 64;     // rows per block of k_vocab_rows
+constexpr int kDirectRows = 128;    // up to these the forward reads x itself: one row tile either way
+constexpr float kDzScale = 8192.f;  // 2^13
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
+
+// ---- epilogues ------------------------------------------------------------------
+
+struct LseEpilogue {
+    struct Args {
+        float2* part;    // [2 n_nt][ld]: largest logit (times log2 e) and sum of 2^(z log2 e - largest)
+        int64_t ld;
+        int64_t vocab;
+    };
+    __device__ static void run(const Args& a, const DenseTile& t, uint32_t taddr) {
+        const int lim = (int)min((int64_t)t.cols, a.vocab - t.col);   // (may be negative: nothing here)
+        float m = __int_as_float(0xff800000), s = 0.f;
+        for (int c = 0; c < lim; c += 32) {
+            float v[32];
+            dense_read(taddr + c, t, v);
+            if (c + 32 > lim) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c + j >= lim) v[j] = __int_as_float(0xff800000);
+            }
+            float cm = m;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) cm = fmaxf(cm, fmaxf(v[j] * kLog2e, v[j + 1] * kLog2e));
+            const float base = cm == __int_as_float(0xff800000) ? 0.f : cm;   // (all of them -inf: sums stay 0)
+            float s0 = s * exp2_fast(m - base), s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                s0 += exp2_fast(fmaf(v[j], kLog2e, -base));
+                s1 += exp2_fast(fmaf(v[j + 1], kLog2e, -base));
+                s2 += exp2_fast(fmaf(v[j + 2], kLog2e, -base));
+                s3 += exp2_fast(fmaf(v[j + 3], kLog2e, -base));
+            }
+            s = (s0 + s1) + (s2 + s3);
+            m = cm;
+        }
+        a.part[(int64_t)(2 * t.nt + t.half) * a.ld + t.row] = make_float2(m, s);
+    }
+};
+
+// Eight fp32 values as 16-bit ones, and the 32-byte store of sixteen.
+template <typename T>
+__device__ __forceinline__ uint32_t two(float a, float b) { return pack2<T>(make_float2(a, b)); }
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+template <typename T>
+struct GradEpilogue {
+    struct Args {
+        T* dz;                    // [rows, ld]
+        int64_t ld;
+        int64_t width;            // columns of the piece that exist
+        int64_t first;            // vocabulary index of its first column
+        const float* lse2;        // [rows] log2 e times lse
+        const float* g;           // [rows] upstream gradient
+        const int64_t* target;    // [rows]
+        const uint32_t* most;     // bits of the largest finite |g|
+    };
+    __device__ static void run(const Args& a, const DenseTile& t, uint32_t taddr) {
+        float c = 0.f, l2 = 0.f;
+        int64_t at = -1;
+        if (t.row < t.rows) {
+            c = a.g[t.row] * grad_factor(*a.most) * kDzScale;
+            l2 = a.lse2[t.row];
+            at = a.target[t.row] - a.first - t.col;
+        }
+        const int lim = (int)min((int64_t)t.cols, a.width - t.col);
+        const int top = (int)min((int64_t)t.cols, a.ld - t.col);   // a multiple of 16
+        T* out = a.dz + t.row * a.ld + t.col;
+        for (int b = 0; b < top; b += 32) {
+            float v[32];
+            dense_read(taddr + b, t, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = c * exp2_fast(fmaf(v[j], kLog2e, -l2));
+            if (at >= b && at < b + 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (at == b + j) v[j] -= c;
+            }
+            if (b + 32 > lim) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (b + j >= lim) v[j] = 0.f;
+            }
+            if (t.row >= t.rows) {   // (its x is zero, but exp may overflow beside c = 0)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = two<T>(v[j + 2 * i], v[j + 2 * i + 1]);
+                if (b + j < top) store32(out + b + j, w);
+            }
+        }
+    }
+    // 1 / G, G the power of two at or above the largest finite |g| (1 where that is 0 or too small to invert)
+    __device__ static float grad_factor(uint32_t bits) {
+        const int e = (int)(bits >> 23);   // biased exponent: |g| < 2^(e - 126)
+        return e < 2 || e > 252 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
+    }
+};
+
+struct SumEpilogue {
+    struct Args {
+        float* slab;       // [splits][rows, ld]
+        int64_t rows, ld;
+        int add;           // to what is there
+    };
+    __device__ static void run(const Args& a, const DenseTile& t, uint32_t taddr) {
+        const int lim = (int)min((int64_t)t.cols, a.ld - t.col);   // (a multiple of 8)
+        float* out = a.slab + ((int64_t)t.split * a.rows + t.row) * a.ld + t.col;
+        for (int b = 0; b < lim; b += 32) {
+            float v[32];
+            dense_read(taddr + b, t, v);
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                if (b + j < lim) {
+                    F8 f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f.set(i, v[j + i]);
+                    if (a.add) {
+                        F8 o;
+                        load8(out + b + j, o);
+                        f.add(o);
+                    }
+                    store8(out + b + j, f);
+                }
+            }
+        }
+    }
+};
+
+template <typename T>
+struct StoreEpilogue {
+    struct Args {
+        T* out;                  // [width, cols]
+        int64_t width, cols;
+        const uint32_t* most;
+        int vec;                 // elements per store: 16, 8 or 1, by the rows' alignment
+    };
+    __device__ static void run(const Args& a, const DenseTile& t, uint32_t taddr) {
+        const int lim = t.row < a.width ? (int)min((int64_t)t.cols, a.cols - t.col) : 0;
+        const float scale = 1.f / (GradEpilogue<T>::grad_factor(*a.most) * kDzScale);
+        T* out = a.out + t.row * a.cols + t.col;
+        const int top = (int)min((int64_t)t.cols, a.cols - t.col);   // the same in all lanes
+        for (int b = 0; b < top; b += 32) {
+            float v[32];
+            dense_read(taddr + b, t, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= scale;
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = two<T>(v[j + 2 * i], v[j + 2 * i + 1]);
+                if (a.vec == 16 && b + j + 16 <= lim) {
+                    store32(out + b + j, w);
+                } else if (a.vec >= 8) {   // (cols is then a multiple of 8, and so is lim)
+                    if (b + j < lim) *reinterpret_cast<uint4*>(out + b + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (b + j + 8 < lim) *reinterpret_cast<uint4*>(out + b + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (b + j + i < lim) out[b + j + i] = from_f32<T>(v[j + i]);
+                }
+            }
+        }
+    }
+};
+
+// ---- rows that count --------------------------------------------------------------
+
+struct RowsArgs {
+    const void* x;
+    const int64_t* target;
+    int64_t ignore;
+    int64_t rows, cols, vocab, ld, padded;   // padded: rows of the gathered matrix
+    void* xc;                         // [padded, ld] the rows that count, then zeros
+    int32_t* index;                   // [rows] of the gathered row: its row of x
+    int32_t* at;                      // [rows] of the row of x: its gathered row, or -1
+    int64_t* tc;                      // [rows] its target
+    int32_t* count;                   // how many
+    // forward: what ignored rows get
+    float* loss;                      // null: none
+    float* lse_zero;
+    // backward: upstream gradient, lse
+    const float* lse;                 // [rows]
+    const float* dloss;               // [rows] (reduction 0) or [1]
+    int reduction;
+    float* lse2;                      // [rows]
+    float* g;                         // [rows]
+    uint32_t* most;                   // cleared before; the largest finite |g|'s bits
+};
+// A block takes kGatherRows rows; how many count before it and in all it finds out by
+// itself (targets are 8 bytes a row: a second launch would cost more up to about 10^5 rows).
+template <typename T>
+__global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
+    __shared__ int before_s[8], all_s[8], list[kGatherRows];
+    __shared__ int mine_s;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int64_t r0 = (int64_t)blockIdx.x * kGatherRows;
+    int before = 0, all = 0;
+#pragma unroll 4
+    for (int64_t r = t; r < a.rows; r += 256) {
+        const bool in = __ldg(a.target + r) != a.ignore;
+        all += in;
+        before += in && r < r0;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0) {
+        before_s[warp] = before;
+        all_s[warp] = all;
+    }
+    __syncthreads();
+    before = all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        before += before_s[i];
+        all += all_s[i];
+    }
+    if (warp == 0) {   // this block's rows, in order
+        int n = 0;
+        uint32_t most = 0;
+        for (int i = 0; i < kGatherRows; i += 32) {
+            const int64_t r = r0 + i + lane;
+            const int64_t tg = r < a.rows ? a.target[r] : a.ignore;
+            const bool in = r < a.rows && tg != a.ignore;
+            const uint32_t mask = __ballot_sync(0xffffffffu, in);
+            const int k = n + __popc(mask & ((1u << lane) - 1));
+            if (in) {
+                list[k] = i + lane;
+                const int64_t to = before + k;
+                a.index[to] = (int32_t)r;
+                a.tc[to] = tg;
+                if (a.g) {
+                    float g = a.reduction == 0 ? a.dloss[r] : a.dloss[0];
+                    if (a.reduction == 2) g /= (float)all;
+                    if (tg < 0 || tg >= a.vocab) g = nan_f();
+                    a.g[to] = g;
+                    a.lse2[to] = a.lse[r] * kLog2e;
+                    const uint32_t bits = __float_as_uint(g) & 0x7fffffffu;
+                    if (bits < 0x7f800000u) most = max(most, bits);
+                }
+            }
+            if (r < a.rows) {
+                a.at[r] = in ? before + k : -1;
+                if (!in && a.loss) a.loss[r] = 0.f;
+                if (!in && a.lse_zero) a.lse_zero[r] = 0.f;
+            }
+            n += __popc(mask);
+        }
+        if (a.g) {
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0 && most) atomicMax(a.most, most);   // (a maximum: the same in any order)
+        }
+        if (lane == 0) {
+            mine_s = n;
+            if (blockIdx.x == 0) *a.count = all;
+        }
+    }
+    __syncthreads();
+    const int mine = mine_s;
+    T* xc = static_cast<T*>(a.xc);
+    const T* x = static_cast<const T*>(a.x);
+    if (a.ld == a.cols) {   // whole 16-byte chunks
+        const int64_t n16 = a.ld / 8;
+        for (int64_t i = t; i < mine * n16; i += 256) {
+            const int64_t k = i / n16, c = i - k * n16;
+            reinterpret_cast<uint4*>(xc + (before + k) * a.ld)[c] =
+                __ldg(reinterpret_cast<const uint4*>(x + (r0 + list[k]) * a.cols) + c);
+        }
+    } else {
+        for (int64_t i = t; i < mine * a.ld; i += 256) {
+            const int64_t k = i / a.ld, c = i - k * a.ld;
+            xc[(before + k) * a.ld + c] = c < a.cols ? x[(r0 + list[k]) * a.cols + c] : from_f32<T>(0.f);
+        }
+    }
+    // zeros from the last row that counts up to the last tile that holds one
+    const int64_t end = min(a.padded, (int64_t)((all + 255) / 256) * 256);
+    uint4* z = reinterpret_cast<uint4*>(xc + (int64_t)all * a.ld);
+    const int64_t nz = (end - all) * (a.ld / 8);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + t; i < nz; i += (int64_t)gridDim.x * 256) z[i] = make_uint4(0, 0, 0, 0);
+}
+
+// [rows, cols] at row stride ld > cols, zeros behind the columns.
+template <typename T>
+__global__ void __launch_bounds__(256) k_vocab_pad(const T* __restrict__ src, T* __restrict__ dst, int64_t rows, int64_t cols,
+                                                   int64_t ld) {
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8)
+        for (int64_t c = threadIdx.x & 31; c < ld; c += 32) dst[r * ld + c] = c < cols ? src[r * cols + c] : from_f32<T>(0.f);
+}
+
+// ---- the loss from its partial sums -------------------------------------------------
+
+struct FinishArgs {
+    const float2* part;     // [slots][ld]
+    int64_t ld;
+    int slots;
+    const void *x, *w;      // rows of x: gathered ones (ldx), of w: [vocab, cols]
+    int64_t cols, ldx, vocab;
+    const int64_t* target;  // of the gathered rows
+    const int32_t* index;   // null: row r itself
+    const int32_t* count;   // null: `rows` of them
+    int64_t rows;
+    int64_t ignore;
+    float *loss, *lse;      // [rows of x]; loss null: only its sum
+    int reduction;
+    int per_block;          // rows of a block, a power of two up to 32
+    float* sums;            // [2 blocks]: sum of losses, number of rows that count
+    int32_t* arrived;
+    float* out;             // reduction 1, 2: [1]
+};
+template <typename T>
+__global__ void __launch_bounds__(256) k_vocab_finish(const FinishArgs a) {
+    __shared__ float2 sm[256];
+    __shared__ float row_loss[32];
+    __shared__ int row_in[32];
+    __shared__ bool last;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int R = a.per_block, W = 256 / R;   // threads of a row
+    const int64_t n = a.count ? (int64_t)*a.count : a.rows;
+    const int64_t r0 = (int64_t)blockIdx.x * R;
+    const int i = t & (R - 1);
+    const float inf = __int_as_float(0x7f800000);
+    {
+        float m = -inf, s = 0.f;
+        if (r0 + i < n) {
+#pragma unroll 4
+            for (int k = t / R; k < a.slots; k += W) {
+                const float2 p = __ldg(a.part + (int64_t)k * a.ld + r0 + i);
+                const float top = fmaxf(m, p.x), base = top == -inf ? 0.f : top;
+                s = s * exp2_fast(m - base) + p.y * exp2_fast(p.x - base);
+                m = top;
+            }
+        }
+        sm[t] = make_float2(m, s);
+    }
+    __syncthreads();
+    for (int w = W / 2; w > 0; w >>= 1) {   // neighbours of a row are R apart
+        if (t < w * R) {
+            const float2 p = sm[t], q = sm[t + w * R];
+            const float top = fmaxf(p.x, q.x), base = top == -inf ? 0.f : top;
+            sm[t] = make_float2(top, p.y * exp2_fast(p.x - base) + q.y * exp2_fast(q.x - base));
+        }
+        __syncthreads();
+    }
+    for (int k = warp; k < R; k += 8) {
+        const int64_t c = r0 + k;
+        float loss = 0.f;
+        bool in = c < n;
+        if (in) {
+            const int64_t tg = a.target[c], r = a.index ? (int64_t)a.index[c] : c;
+            float l = 0.f;
+            in = tg != a.ignore;
+            if (in) {
+                l = kLn2 * sm[k].x + logf(sm[k].y);
+                if (tg >= 0 && tg < a.vocab) {
+                    const T* x = static_cast<const T*>(a.x) + c * a.ldx;
+                    const T* w = static_cast<const T*>(a.w) + tg * a.cols;
+                    float d0 = 0.f, d1 = 0.f;
+                    int64_t j = 2 * lane;
+                    if ((a.cols & 1) == 0) {
+#pragma unroll 4
+                        for (; j < a.cols; j += 64) {
+                            const float2 p = unpack2<T>(*reinterpret_cast<const uint32_t*>(x + j));
+                            const float2 q = unpack2<T>(*reinterpret_cast<const uint32_t*>(w + j));
+                            d0 = fmaf(p.x, q.x, d0);
+                            d1 = fmaf(p.y, q.y, d1);
+                        }
+                    } else {
+                        for (j = lane; j < a.cols; j += 32) d0 = fmaf(to_f32(x[j]), to_f32(w[j]), d0);
+                    }
+                    d0 += d1;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) d0 += __shfl_xor_sync(0xffffffffu, d0, o);
+                    loss = l - d0;
+                } else {
+                    loss = nan_f();
+                }
+            }
+            if (lane == 0) {
+                if (a.loss) a.loss[r] = loss;
+                if (a.lse) a.lse[r] = l;
+            }
+        }
+        if (lane == 0) {
+            row_loss[k] = loss;
+            row_in[k] = in;
+        }
+    }
+    if (a.reduction == 0) return;
+    __syncthreads();
+    if (t == 0) {
+        float s = 0.f;
+        int in = 0;
+        for (int k = 0; k < R; ++k) {
+            s += row_loss[k];
+            in += row_in[k];
+        }
+        a.sums[2 * blockIdx.x] = s;
+        a.sums[2 * blockIdx.x + 1] = (float)in;   // (at most 32)
+        __threadfence();
+        last = atomicAdd(a.arrived, 1) == (int)gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    // the last block adds all of them, in an order of their own
+    __threadfence();
+    float s = 0.f;
+    int64_t in = 0;
+    for (int64_t b = t; b < gridDim.x; b += 256) {
+        s += __ldcg(a.sums + 2 * b);
+        in += (int64_t)__ldcg(a.sums + 2 * b + 1);
+    }
+    double* ds = reinterpret_cast<double*>(sm);   // (256 x 8 bytes, no longer needed)
+    __shared__ int counts[256];
+    ds[t] = (double)s;
+    counts[t] = (int)in;
+    __syncthreads();
+    for (int w = 128; w > 0; w >>= 1) {
+        if (t < w) {
+            ds[t] += ds[t + w];
+            counts[t] += counts[t + w];
+        }
+        __syncthreads();
+    }
+    if (t == 0) *a.out = (float)(a.reduction == 2 ? ds[0] / (double)counts[0] : ds[0]);
+}
+
+// dx of every row of x from the slabs; ignored rows zero.
+template <typename T>
+__global__ void __launch_bounds__(256) k_vocab_dx(const float* __restrict__ slab, int splits, int64_t stride, int64_t ld,
+                                                  const int32_t* __restrict__ at, const uint32_t* most, int64_t rows, int64_t cols,
+                                                  T* __restrict__ dx) {
+    const float scale = 1.f / (GradEpilogue<T>::grad_factor(*most) * kDzScale);
+    const int64_t n8 = ld / 8, n = rows * n8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / n8, c = (i - r * n8) * 8;
+        const int k = __ldg(at + r);
+        F8 f;
+        f.clear();
+        if (k >= 0) {
+            const float* p = slab + (int64_t)k * ld + c;
+            for (int s = 0; s < splits; ++s) {
+                F8 o;
+                load8(p + s * stride, o);
+                f.add(o);
+            }
+            f.mul(scale);
+        }
+        T* out = dx + r * cols + c;
+        if (ld == cols) {
+            store8(out, f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < cols) out[j] = from_f32<T>(f.at(j));
+        }
+    }
+}
+
+// ---- host -----------------------------------------------------------------------------
+
+int64_t up(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
+int sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+int launched() { return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA; }
+
+// Tile width of a product over `n` columns with few row tiles: the width whose last wave
+// of tiles is fullest.
+int narrow_bn(int64_t n, int units) {
+    int best = 256;
+    int64_t cost = INT64_MAX;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+        const int64_t waves = ceil_div(ceil_div(n, bn), units), c = waves * (bn + 16);
+        if (c < cost) {
+            cost = c;
+            best = bn;
+        }
+    }
+    return best;
+}
+
+// The scratch of a call, in order; take() hands out 256-byte aligned pieces.
+struct Scratch {
+    char* base;
+    int64_t used = 0;
+    explicit Scratch(void* p) : base(static_cast<char*>(p)) {}
+    template <typename T>
+    T* take(int64_t n) {
+        T* p = reinterpret_cast<T*>(base + used);
+        used += up(n * (int64_t)sizeof(T), 256);
+        return p;
+    }
+};
+
+struct Shape {
+    int64_t rows, cols, vocab, ld, padded;   // ld: columns in whole 16-byte chunks
+    Shape(int64_t r, int64_t c, int64_t v) : rows(r), cols(c), vocab(v), ld(up(c, 8)), padded(up(r, 256)) {}
+    bool pads() const { return ld != cols; }
+};
+
+struct ForwardPlan {
+    bool gather;
+    int cg, bn, n_nt, per_block, blocks;
+    void *xc, *wc;
+    int32_t *index, *at, *count, *arrived;
+    int64_t* tc;
+    float2* part;
+    float *sums, *row_lse;
+    int64_t bytes;
+    ForwardPlan(const Shape& h, int num_sms, void* scratch) {
+        gather = h.rows > kDirectRows || h.pads();
+        cg = h.rows > kDirectRows ? 2 : 1;
+        bn = cg == 2 ? 256 : narrow_bn(h.vocab, num_sms);
+        n_nt = (int)ceil_div(h.vocab, bn);
+        per_block = 1;
+        while (per_block < 32 && ceil_div(h.rows, per_block) > num_sms) per_block *= 2;
+        blocks = (int)ceil_div(h.rows, per_block);
+        Scratch s(scratch);
+        count = s.take<int32_t>(2);
+        arrived = count + 1;
+        index = s.take<int32_t>(gather ? h.rows : 0);
+        at = s.take<int32_t>(gather ? h.rows : 0);
+        tc = s.take<int64_t>(gather ? h.rows : 0);
+        xc = s.take<uint16_t>(gather ? h.padded * h.ld : 0);
+        wc = s.take<uint16_t>(h.pads() ? h.vocab * h.ld : 0);
+        part = s.take<float2>((int64_t)2 * n_nt * h.padded);
+        sums = s.take<float>(2 * (int64_t)blocks);
+        row_lse = nullptr;
+        bytes = s.used;
+    }
+};
+
+// Columns of the vocabulary whose dz is held at a time.
+constexpr int64_t kPieceBytes = 256ll << 20;
+
+struct BackwardPlan {
+    int cg, bn_z, bn_x, bn_w, splits;
+    int64_t piece;
+    void *xc, *wc, *dz;
+    int32_t *index, *at, *count;
+    uint32_t* most;
+    int64_t* tc;
+    float *lse2, *g, *slab;
+    int64_t bytes;
+    BackwardPlan(const Shape& h, int num_sms, void* scratch) {
+        cg = h.rows > kDirectRows ? 2 : 1;
+        const int64_t whole = up(h.vocab, 256);
+        piece = std::max<int64_t>(256, std::min(whole, kPieceBytes / (2 * h.padded) / 256 * 256));
+        piece = up(ceil_div(whole, ceil_div(whole, piece)), 256);   // equal ones
+        bn_z = cg == 2 ? 256 : narrow_bn(piece, num_sms);
+        const int step = 64 * cg;
+        bn_x = bn_w = (int)std::min<int64_t>(256, up(h.ld, step));
+        const int units = num_sms / cg;
+        const int64_t tiles = ceil_div(h.rows, 128 * cg) * ceil_div(h.ld, bn_x);
+        // ranges of K for dx: the number, up to one per 512 columns, whose waves are fullest; each costs a slab of dx
+        splits = 1;
+        double best = 0;
+        const int most_splits = (int)std::max<int64_t>(1, std::min<int64_t>(piece / 512, std::max<int64_t>(4, 2 * units / tiles)));
+        for (int n = 1; n <= most_splits; ++n) {
+            const double full = (double)(tiles * n) / (double)(ceil_div(tiles * n, units) * units) - 0.01 * n * (tiles >= units);
+            if (full > best + 0.02) {
+                best = full;
+                splits = n;
+            }
+        }
+        Scratch s(scratch);
+        count = s.take<int32_t>(2);
+        most = reinterpret_cast<uint32_t*>(count + 1);
+        index = s.take<int32_t>(h.rows);
+        at = s.take<int32_t>(h.rows);
+        tc = s.take<int64_t>(h.rows);
+        lse2 = s.take<float>(h.rows);
+        g = s.take<float>(h.rows);
+        xc = s.take<uint16_t>(h.padded * h.ld);
+        wc = s.take<uint16_t>(h.pads() ? h.vocab * h.ld : 0);
+        dz = s.take<uint16_t>(h.padded * piece);
+        slab = s.take<float>((int64_t)splits * h.padded * h.ld);
+        bytes = s.used;
+    }
+};
+
+template <typename T>
+int pad_weight(const Shape& h, const void* w, void* wc, int num_sms, cudaStream_t s) {
+    k_vocab_pad<T><<<(unsigned)std::min<int64_t>(ceil_div(h.vocab, 8), 8 * num_sms), 256, 0, s>>>(
+        static_cast<const T*>(w), static_cast<T*>(wc), h.vocab, h.cols, h.ld);
+    return launched();
+}
+
+template <typename T>
+int forward(const Shape& h, const void* x, const void* w, const int64_t* target, int64_t ignore, int reduction, float* loss,
+            float* lse, void* scratch, int num_sms, cudaStream_t s) {
+    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    ForwardPlan p(h, num_sms, scratch);
+    float* row_loss = reduction == 0 ? loss : nullptr;
+    if (p.gather) {
+        RowsArgs r = {};
+        r.x = x;
+        r.target = target;
+        r.ignore = ignore;
+        r.rows = h.rows;
+        r.cols = h.cols;
+        r.vocab = h.vocab;
+        r.ld = h.ld;
+        r.padded = h.padded;
+        r.xc = p.xc;
+        r.index = p.index;
+        r.at = p.at;
+        r.tc = p.tc;
+        r.count = p.count;
+        r.loss = row_loss;
+        r.lse_zero = lse;
+        k_vocab_rows<T><<<(unsigned)ceil_div(h.rows, kGatherRows), 256, 0, s>>>(r);
+        if (int st = launched(); st != SNK_OK) return st;
+    }
+    const void* wt = w;
+    if (h.pads()) {
+        if (int st = pad_weight<T>(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
+        wt = p.wc;
+    }
+    CUtensorMap ma, mb;
+    const void* xt = p.gather ? p.xc : x;
+    if (!dense_map(&ma, xt, bf, h.ld, p.gather ? h.padded : h.rows, h.ld, kDenseM) ||
+        !dense_map(&mb, wt, bf, h.ld, h.vocab, h.ld, p.bn / p.cg))
+        return SNK_ERR_CUDA;
+    DenseArgs a = {};
+    a.n_mt = (int)ceil_div(h.rows, 128 * p.cg);
+    a.n_nt = p.n_nt;
+    a.bn = p.bn;
+    a.splits = 1;
+    a.K = h.ld;
+    a.idesc = dense_idesc(bf, false, false, 128 * p.cg, p.bn);
+    a.rows = p.gather ? p.count : nullptr;
+    a.group = 16 / p.cg;
+    a.zero = p.arrived;
+    const LseEpilogue::Args ea{p.part, h.padded, h.vocab};
+    const int st = p.cg == 2 ? dense_launch<2, false, false, LseEpilogue>(ma, mb, a, ea, num_sms, s)
+                             : dense_launch<1, false, false, LseEpilogue>(ma, mb, a, ea, num_sms, s);
+    if (st != SNK_OK) return st;
+    FinishArgs f = {};
+    f.part = p.part;
+    f.ld = h.padded;
+    f.slots = 2 * p.n_nt;
+    f.x = xt;
+    f.w = w;
+    f.cols = h.cols;
+    f.ldx = p.gather ? h.ld : h.cols;
+    f.vocab = h.vocab;
+    f.target = p.gather ? p.tc : target;
+    f.index = p.gather ? p.index : nullptr;
+    f.count = p.gather ? p.count : nullptr;
+    f.rows = h.rows;
+    f.ignore = ignore;
+    f.loss = row_loss;
+    f.lse = lse;
+    f.reduction = reduction;
+    f.per_block = p.per_block;
+    f.sums = p.sums;
+    f.arrived = p.arrived;
+    f.out = loss;
+    k_vocab_finish<T><<<(unsigned)p.blocks, 256, 0, s>>>(f);
+    return launched();
+}
+
+template <int CG, typename T>
+int backward(const Shape& h, const BackwardPlan& p, const void* wt, void* dx, void* dw, int num_sms, cudaStream_t s) {
+    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    const int m_tiles = (int)ceil_div(h.rows, 128 * CG);
+    CUtensorMap mx, mx_t, mz, mz_t;
+    if (!dense_map(&mx, p.xc, bf, h.ld, h.padded, h.ld, kDenseM) || !dense_map(&mx_t, p.xc, bf, h.ld, h.padded, h.ld, 64) ||
+        !dense_map(&mz, p.dz, bf, p.piece, h.padded, p.piece, kDenseM) ||
+        !dense_map(&mz_t, p.dz, bf, p.piece, h.padded, p.piece, 64))
+        return SNK_ERR_CUDA;
+    for (int64_t v0 = 0; v0 < h.vocab; v0 += p.piece) {
+        const int64_t width = std::min(p.piece, h.vocab - v0);
+        const T* wp = static_cast<const T*>(wt) + v0 * h.ld;
+        CUtensorMap mw, mw_t;
+        if (!dense_map(&mw, wp, bf, h.ld, width, h.ld, p.bn_z / CG) || !dense_map(&mw_t, wp, bf, h.ld, width, h.ld, 64))
+            return SNK_ERR_CUDA;
+        DenseArgs a = {};
+        a.splits = 1;
+        // dz of the piece
+        a.n_mt = m_tiles;
+        a.n_nt = (int)ceil_div(width, p.bn_z);
+        a.bn = p.bn_z;
+        a.K = h.ld;
+        a.idesc = dense_idesc(bf, false, false, 128 * CG, p.bn_z);
+        a.rows = p.count;
+        a.group = 16 / CG;
+        const typename GradEpilogue<T>::Args eg{static_cast<T*>(p.dz), p.piece, width, v0, p.lse2, p.g, p.tc, p.most};
+        if (int st = dense_launch<CG, false, false, GradEpilogue<T>>(mx, mw, a, eg, num_sms, s); st != SNK_OK) return st;
+        if (dx) {
+            a.n_nt = (int)ceil_div(h.ld, p.bn_x);
+            a.bn = p.bn_x;
+            a.K = width;
+            a.splits = p.splits;
+            a.idesc = dense_idesc(bf, false, true, 128 * CG, p.bn_x);
+            const SumEpilogue::Args es{p.slab, h.padded, h.ld, v0 > 0};
+            if (int st = dense_launch<CG, false, true, SumEpilogue>(mz, mw_t, a, es, num_sms, s); st != SNK_OK) return st;
+        }
+        if (dw) {
+            T* out = static_cast<T*>(dw) + v0 * h.cols;
+            a.n_mt = (int)ceil_div(width, 128 * CG);
+            a.n_nt = (int)ceil_div(h.cols, p.bn_w);
+            a.bn = p.bn_w;
+            a.K = h.rows;
+            a.splits = 1;
+            a.rows_k = 1;
+            a.idesc = dense_idesc(bf, true, true, 128 * CG, p.bn_w);
+            const int vec = h.pads() ? 1 : (h.cols % 16 == 0 && ((uintptr_t)out & 31) == 0 ? 16 : 8);
+            const typename StoreEpilogue<T>::Args eo{out, width, h.cols, p.most, vec};
+            if (int st = dense_launch<CG, true, true, StoreEpilogue<T>>(mz_t, mx_t, a, eo, num_sms, s); st != SNK_OK) return st;
+        }
+    }
+    if (dx) {
+        k_vocab_dx<T><<<(unsigned)std::min<int64_t>(ceil_div(h.rows * (h.ld / 8), 256), 16 * num_sms), 256, 0, s>>>(
+            p.slab, p.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, static_cast<T*>(dx));
+        return launched();
+    }
+    return SNK_OK;
+}
+
+template <typename T>
+int backward_rows(const Shape& h, const BackwardPlan& p, const void* x, const void* w, const int64_t* target, int64_t ignore,
+                  const float* lse, const float* dloss, int reduction, void* dx, void* dw, int num_sms, cudaStream_t s) {
+    if (cudaMemsetAsync(p.most, 0, 4, s) != cudaSuccess) {
+        cudaGetLastError();
+        return SNK_ERR_CUDA;
+    }
+    RowsArgs r = {};
+    r.x = x;
+    r.target = target;
+    r.ignore = ignore;
+    r.rows = h.rows;
+    r.cols = h.cols;
+    r.vocab = h.vocab;
+    r.ld = h.ld;
+    r.padded = h.padded;
+    r.xc = p.xc;
+    r.index = p.index;
+    r.at = p.at;
+    r.tc = p.tc;
+    r.count = p.count;
+    r.lse = lse;
+    r.dloss = dloss;
+    r.reduction = reduction;
+    r.lse2 = p.lse2;
+    r.g = p.g;
+    r.most = p.most;
+    k_vocab_rows<T><<<(unsigned)ceil_div(h.rows, kGatherRows), 256, 0, s>>>(r);
+    if (int st = launched(); st != SNK_OK) return st;
+    const void* wt = w;
+    if (h.pads()) {
+        if (int st = pad_weight<T>(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
+        wt = p.wc;
+    }
+    return p.cg == 2 ? backward<2, T>(h, p, wt, dx, dw, num_sms, s) : backward<1, T>(h, p, wt, dx, dw, num_sms, s);
+}
+
+bool unaligned(const void* p, uintptr_t n) { return p && ((uintptr_t)p & (n - 1)); }
+// 1: bad, 2: too large
+int bad_shape(int dtype, int64_t rows, int64_t cols, int64_t vocab, int reduction) {
+    if ((dtype != SNK_F16 && dtype != SNK_BF16) || rows < 0 || cols < 1 || vocab < 1 || reduction < 0 || reduction > 2)
+        return SNK_ERR_ARG;
+    const int64_t lim = INT32_MAX - 512;
+    if (rows > lim || cols > lim || vocab > lim) return SNK_ERR_LIMIT;
+    // tiles are counted in 32 bits
+    if ((double)ceil_div(rows, 128) * (double)ceil_div(vocab, 64) * 2 > 2.0e9 ||
+        (double)ceil_div(vocab, 128) * (double)ceil_div(cols, 64) > 2.0e9 ||
+        (double)ceil_div(rows, 128) * (double)ceil_div(cols, 64) * 512 > 2.0e9)
+        return SNK_ERR_LIMIT;
+    return SNK_OK;
+}
+
+}  // namespace
+}  // namespace snk
+
+using namespace snk;
+
+extern "C" {
+
+int64_t snk_vocab_loss_scratch(int64_t rows, int64_t cols, int64_t vocab, int backward) {
+    if (rows < 1 || bad_shape(SNK_BF16, rows, cols, vocab, 0) != SNK_OK) return 0;
+    const int n = sms();
+    if (n < 1) return 0;
+    const Shape h(rows, cols, vocab);
+    return backward ? BackwardPlan(h, n, nullptr).bytes : ForwardPlan(h, n, nullptr).bytes;
+}
+
+int snk_vocab_loss(const void* x, const void* weight, int dtype, const int64_t* target, int64_t ignore, int64_t rows,
+                   int64_t cols, int64_t vocab, int reduction, float* loss, float* lse, void* scratch, void* stream) {
+    if (int st = bad_shape(dtype, rows, cols, vocab, reduction); st != SNK_OK) return st;
+    if (!weight || unaligned(weight, 16) || unaligned(x, 16) || unaligned(target, 8) || unaligned(loss, 4) || unaligned(lse, 4) ||
+        unaligned(scratch, 256))
+        return SNK_ERR_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (rows == 0) {
+        if (reduction == 0) return SNK_OK;
+        if (!loss) return SNK_ERR_ARG;
+        // the sum of no rows is 0, their mean NaN (all bits set is one)
+        return cudaMemsetAsync(loss, reduction == 1 ? 0 : 0xff, 4, s) == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
+    }
+    if (!x || !target || !loss || !scratch) return SNK_ERR_ARG;
+    const int n = sms();
+    if (n < 1) return SNK_ERR_CUDA;
+    const Shape h(rows, cols, vocab);
+    return dtype == SNK_F16
+               ? forward<__half>(h, x, weight, target, ignore, reduction, loss, lse, scratch, n, s)
+               : forward<__nv_bfloat16>(h, x, weight, target, ignore, reduction, loss, lse, scratch, n, s);
+}
+
+int snk_vocab_loss_backward(const void* x, const void* weight, int dtype, const int64_t* target, int64_t ignore,
+                            const float* lse, const float* dloss, int64_t rows, int64_t cols, int64_t vocab, int reduction,
+                            void* dx, void* dweight, void* scratch, void* stream) {
+    if (int st = bad_shape(dtype, rows, cols, vocab, reduction); st != SNK_OK) return st;
+    if (!weight || unaligned(weight, 16) || unaligned(x, 16) || unaligned(target, 8) || unaligned(lse, 4) ||
+        unaligned(dloss, 4) || unaligned(dx, 16) || unaligned(dweight, 16) || unaligned(scratch, 256))
+        return SNK_ERR_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (rows == 0) {
+        if (!dweight) return SNK_OK;
+        return cudaMemsetAsync(dweight, 0, (size_t)(vocab * cols * 2), s) == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
+    }
+    if (!x || !target || !lse || !dloss || !scratch) return SNK_ERR_ARG;
+    if (!dx && !dweight) return SNK_OK;
+    const int n = sms();
+    if (n < 1) return SNK_ERR_CUDA;
+    const Shape h(rows, cols, vocab);
+    const BackwardPlan p(h, n, scratch);
+    return dtype == SNK_F16
+               ? backward_rows<__half>(h, p, x, weight, target, ignore, lse, dloss, reduction, dx, dweight, n, s)
+               : backward_rows<__nv_bfloat16>(h, p, x, weight, target, ignore, lse, dloss, reduction, dx, dweight, n, s);
+}
+
+}  // extern "C"
