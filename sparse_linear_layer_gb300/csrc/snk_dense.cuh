@@ -182,6 +182,29 @@ __device__ __forceinline__ void dense_read(uint32_t taddr, const DenseTile& t, f
     }
 }
 
+// Position in a ring of N slots: the slot and its phase's parity (counted, not divided:
+// the issuing threads pass here for every stage).
+template <int N>
+struct Stages {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+// The stages that a producer filled last have landed.
+template <int N>
+__device__ __forceinline__ void drain_last(uint64_t* full, Stages<N> r, bool all) {
+    for (int i = 0; i < N; ++i) {   // oldest first: slots before r.slot are of this round
+        const bool older = r.slot + i >= N;
+        const int slot = older ? r.slot + i - N : r.slot + i;
+        if (older || all) mbar_wait(&full[slot], older ? r.parity : r.parity ^ 1, kTcDrainCycles);
+    }
+}
+
 // Epilogue: a type with Args and static __device__ void run(const Args&, const DenseTile&,
 // uint32_t taddr), taddr the TMEM address of the half's first column on the warp's lanes.
 template <int CG, bool A_MN, bool B_MN, class Epilogue>
@@ -235,15 +258,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            bool ok = true;
-            int64_t w = 0;   // stages filled
+            bool ok = true, used = false;   // used: every slot has been filled once
+            Stages<S> r;
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int k0 = (int)((int64_t)n_k * it.split / a.splits), k1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
                 const int m0 = (it.mt * CG + rank) * kDenseM, n0 = it.nt * a.bn + rank * half_b;
-                for (int k = k0; k < k1; ++k, ++w) {
-                    const int s = (int)(w % S);
-                    if (w >= S && !mbar_wait(&empty[s], (uint32_t)(w / S - 1) & 1)) {
+                for (int k = k0; k < k1; ++k) {
+                    const int s = r.slot;
+                    if (used && !mbar_wait(&empty[s], r.parity ^ 1)) {
                         ok = false;
                         break;
                     }
@@ -264,29 +287,30 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     } else {
                         dense_load<CG>(sb, &map_b, kc, n0, bar);
                     }
+                    r.next();
+                    used |= r.slot == 0;
                 }
             }
-            if (!ok && rank == 0)   // what still lands here, the other CTA's copies among it
-                for (int64_t v = w > S ? w - S : 0; v < w; ++v) mbar_wait(&full[v % S], (uint32_t)(v / S) & 1, kTcDrainCycles);
+            if (!ok && rank == 0) drain_last(full, r, used);   // (the other CTA's copies among them)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             bool ok = true;
-            int64_t w = 0;
-            int q = 0;   // accumulators filled
+            Stages<S> r;
+            uint32_t q = 0;   // accumulators filled
             for (int id = first; id < items && ok; id += step, ++q) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int k0 = (int)((int64_t)n_k * it.split / a.splits), k1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
                 const int ab = q & 1;
-                if (q >= 2 && !mbar_wait(&acce[ab], (uint32_t)((q >> 1) - 1) & 1)) {
+                if (q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + ab * kDenseN;
-                for (int k = k0; k < k1; ++k, ++w) {
-                    const int s = (int)(w % S);
-                    if (!mbar_wait(&full[s], (uint32_t)(w / S) & 1)) {
+                for (int k = k0; k < k1; ++k, r.next()) {
+                    const int s = r.slot;
+                    if (!mbar_wait(&full[s], r.parity)) {
                         ok = false;
                         break;
                     }
@@ -312,11 +336,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int half = warp >= 6 ? 1 : 0, quarter = warp & 3;
         const int hc = a.bn / 2;
         bool ok = true;
-        int q = 0;
+        uint32_t q = 0;
         for (int id = first; id < items; id += step, ++q) {
             const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
-            const int ab = q & 1;
-            if (ok) ok = mbar_wait(&accf[ab], (uint32_t)(q >> 1) & 1);
+            const int ab = (int)(q & 1);
+            if (ok) ok = mbar_wait(&accf[ab], (q >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             DenseTile tile;

@@ -5,9 +5,9 @@
 //     y_mn = sum_g sa[m, g] sb[n or n / 128, g] (sum_{k in group g} a_mk b_nk) + bias_n
 // Products of two codes are exact in fp32; the sum of a group is the tensor cores' (four
 // MMA steps of 32 columns), the sum over groups is fp32 with rounding, in order.  Since a
-// scale changes every 128 columns, an accumulator lasts one group: two of them in TMEM
-// take turns, and while the tensor cores fill one the epilogue warps multiply the other
-// by its scales into registers.
+// scale changes every 128 columns, an accumulator lasts one group: two or more of them in
+// TMEM take turns, and while the tensor cores fill one the
+// epilogue warps multiply another by its scales into registers.
 //
 // k_q8_dense has the same parts as k_dense (snk_dense.cuh): a stage is one group, 128
 // bytes of a row.  k_q8_rows is for up to 16 rows of A, where the codes of B are read
@@ -94,17 +94,24 @@ __device__ __forceinline__ void store16(T* out, int c, int lim, int vec, const f
     }
 }
 
+// Scales of B by row: the tile's, this many groups at a time, two batches in shared memory.
+constexpr int kScaleBatch = 8;
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <int CG, int BN, bool ROWS>
 __global__ void __launch_bounds__(kQ8Threads, 1)
     k_q8_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Q8DenseArgs a) {
     constexpr int S = kDenseStages<CG>, kStage = kDenseStageBytes<CG>;
-    constexpr int HB = BN / CG;   // rows of B that a CTA loads
     constexpr int HC = BN / 2;    // columns of an epilogue warp
+    constexpr int HB = BN / CG;   // rows of B that a CTA loads
+    constexpr int NB = BN == 256 ? 2 : 4;   // accumulators
     extern __shared__ __align__(1024) unsigned char q8_raw[];
     unsigned char* sm = q8_raw + ((1024 - (smem_u32(q8_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin;
+    float* sb_s = reinterpret_cast<float*>(sm + S * kStage);   // ROWS: [2][kScaleBatch][BN]
+    __shared__ uint64_t full[S], empty[S], accf[NB], acce[NB], fin;
     __shared__ uint32_t tmem_base;
-    __shared__ __align__(16) float sb_s[ROWS ? 2 : 1][BN];   // ROWS: the tile's scales of B, of the current and the next group
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int rank = CG == 1 ? 0 : (int)cluster_rank();
@@ -113,7 +120,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NB; ++i) {
             mbar_init(&accf[i], 1);
             mbar_init(&acce[i], kDenseEpilogueWarps * CG);
         }
@@ -132,48 +139,50 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     if (warp < 4) {
         fewer_registers<kQ8RoleRegs>();
         if (warp == 0 && lane == 0) {
-            bool ok = true;
-            int64_t w = 0;
+            bool ok = true, used = false;   // used: every slot has been filled once
+            Stages<S> r;
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
                 const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
                 const int m0 = (it.mt * CG + rank) * kDenseM, n0 = it.nt * BN + rank * HB;
-                for (int g = g0; g < g1; ++g, ++w) {
-                    const int s = (int)(w % S);
-                    if (w >= S && !mbar_wait(&empty[s], (uint32_t)(w / S - 1) & 1)) {
+                for (int g = g0; g < g1; ++g) {
+                    const int s = r.slot;
+                    if (used && !mbar_wait(&empty[s], r.parity ^ 1)) {
                         ok = false;
                         break;
                     }
                     unsigned char* sa = sm + s * kStage;
+                    unsigned char* sb = sa + kDenseM * 128;
                     if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(kDenseM + HB) * 128 * CG);
                     const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : first_cta(&full[s]);
                     dense_load<CG>(sa, &map_a, g * 128, m0, bar);
-                    dense_load<CG>(sa + kDenseM * 128, &map_b, g * 128, n0, bar);
+                    dense_load<CG>(sb, &map_b, g * 128, n0, bar);
+                    r.next();
+                    used |= r.slot == 0;
                 }
             }
-            if (!ok && rank == 0)
-                for (int64_t v = w > S ? w - S : 0; v < w; ++v) mbar_wait(&full[v % S], (uint32_t)(v / S) & 1, kTcDrainCycles);
+            if (!ok && rank == 0) drain_last(full, r, used);
         }
         if (warp == 1 && lane == 0 && rank == 0) {
             bool ok = true;
-            int64_t w = 0;
+            Stages<S> r;
+            uint32_t w = 0;   // groups done
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
                 const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
-                for (int g = g0; g < g1; ++g, ++w) {
-                    const int s = (int)(w % S), ab = (int)(w & 1);
-                    if ((w >= 2 && !mbar_wait(&acce[ab], (uint32_t)((w >> 1) - 1) & 1)) ||
-                        !mbar_wait(&full[s], (uint32_t)(w / S) & 1)) {
+                for (int g = g0; g < g1; ++g, ++w, r.next()) {
+                    const int s = r.slot, ab = (int)(w % NB);
+                    if ((w >= NB && !mbar_wait(&acce[ab], (w / NB - 1) & 1)) || !mbar_wait(&full[s], r.parity)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kDenseM * 128, d = tmem + ab * kDenseN;
+                    const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kDenseM * 128;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        q8_mma<CG>(d, desc_sw128(sa + kk * 32), desc_sw128(sb + kk * 32), a.idesc, kk > 0 ? 1u : 0u);
-                    dense_commit<CG>(&empty[s]);
+                        q8_mma<CG>(tmem + ab * BN, desc_sw128(sa + kk * 32), desc_sw128(sb + kk * 32), a.idesc, kk > 0 ? 1u : 0u);
                     dense_commit<CG>(&accf[ab]);
+                    dense_commit<CG>(&empty[s]);
                 }
             }
             if (!ok) {
@@ -185,7 +194,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         more_registers<kQ8SumRegs>();
         const int half = warp >= 8 ? 1 : 0, quarter = warp & 3, et = t - 128;
         bool ok = true;
-        int64_t w = 0;
+        uint32_t w = 0;   // groups done
         for (int id = first; id < items; id += step) {
             const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
             const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
@@ -193,54 +202,78 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             const int64_t col = (int64_t)it.nt * BN + half * HC;
             // rows and columns outside the matrix read the last ones' scales and are not stored
             const float* pa = a.sa + min(row, a.M - 1) * a.n_g;
-            const float* pb = ROWS ? a.sb + min((int64_t)it.nt * BN + (et < BN ? et : 0), a.N - 1) * a.n_g
+            const float* pb = ROWS ? a.sb + min((int64_t)it.nt * BN + (et & (BN - 1)), a.N - 1) * a.n_g
                                    : a.sb + (min(col, a.N - 1) >> 7) * a.n_g;
+            // ROWS: scales of groups [g, g + kScaleBatch) into a batch
+            auto fetch = [&](int g, int batch) {
+                if (et < BN) {
+#pragma unroll
+                    for (int i = 0; i < kScaleBatch; ++i)
+                        if (g + i < g1) copy4(sb_s + (batch * kScaleBatch + i) * BN + et, pb + g + i);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
             float2 acc[HC / 2];
 #pragma unroll
             for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(0.f, 0.f);
             float na = 0.f, nb = 0.f;
             if (g0 < g1) {
                 na = __ldg(pa + g0);
-                nb = __ldg(pb + g0);
+                if (!ROWS) nb = __ldg(pb + g0);
+            }
+            if constexpr (ROWS) {
+                asm volatile("bar.sync 1, 256;" ::: "memory");   // the last tile's batches have been read
+                fetch(g0, 0);
             }
             for (int g = g0; g < g1; ++g, ++w) {
-                const int ab = (int)(w & 1);
+                const int ab = (int)(w % NB);
                 const float ca = na, cb = nb;
                 if (g + 1 < g1) {
                     na = __ldg(pa + g + 1);
-                    nb = __ldg(pb + g + 1);
+                    if (!ROWS) nb = __ldg(pb + g + 1);
                 }
                 const float* sbp = nullptr;
-                if constexpr (ROWS) {   // (two buffers: a warp may still read the last group's)
-                    if (et < BN) sb_s[ab][et] = cb;
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
-                    sbp = &sb_s[ab][half * HC];
+                if constexpr (ROWS) {
+                    const int i = g - g0, batch = (i / kScaleBatch) & 1;
+                    if (i % kScaleBatch == 0) {   // this batch is here for all; the other one has been read by all
+                        asm volatile("cp.async.wait_group 0;\n bar.sync 1, 256;" ::: "memory");
+                        fetch(g + kScaleBatch, batch ^ 1);
+                    }
+                    sbp = sb_s + (batch * kScaleBatch + i % kScaleBatch) * BN + half * HC;
                 }
-                if (ok) ok = mbar_wait(&accf[ab], (uint32_t)(w >> 1) & 1);
+                if (ok) ok = mbar_wait(&accf[ab], (w / NB) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
-                const uint32_t ta = tmem + ab * kDenseN + half * HC + ((uint32_t)(quarter * 32) << 16);
+                const uint32_t ta = tmem + ab * BN + half * HC + ((uint32_t)(quarter * 32) << 16);
                 const float s = ROWS ? ca : ca * cb;
                 uint32_t r[2][32];   // the next 32 columns are read while these are added
                 tmem_ld32_async(ta, r[0]);
 #pragma unroll
                 for (int c = 0; c < HC; c += 32) {
                     tmem_wait_ld();
-                    if (c + 32 < HC) tmem_ld32_async(ta + c + 32, r[(c / 32 + 1) & 1]);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const uint32_t(&u)[32] = r[(c / 32) & 1];
-                        const float2 v = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-                        float2 f = make_float2(s, s);
-                        if constexpr (ROWS) f = __fmul2_rn(f, *reinterpret_cast<const float2*>(sbp + c + 2 * j));
-                        acc[c / 2 + j] = __ffma2_rn(v, f, acc[c / 2 + j]);
+                    if (c + 32 < HC) {
+                        tmem_ld32_async(ta + c + 32, r[(c / 32 + 1) & 1]);
+                    } else {   // all read: the accumulator is free before its last columns are added
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (CG == 1) mbar_arrive(&acce[ab]);
+                            else mbar_arrive_cluster(first_cta(&acce[ab]));
+                        }
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 1) mbar_arrive(&acce[ab]);
-                    else mbar_arrive_cluster(first_cta(&acce[ab]));
+                    const uint32_t(&u)[32] = r[(c / 32) & 1];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        float2 f0 = make_float2(s, s), f1 = f0;
+                        if constexpr (ROWS) {
+                            const float4 b4 = *reinterpret_cast<const float4*>(sbp + c + j);
+                            f0 = __fmul2_rn(f0, make_float2(b4.x, b4.y));
+                            f1 = __fmul2_rn(f1, make_float2(b4.z, b4.w));
+                        }
+                        float2 &x = acc[(c + j) / 2], &y = acc[(c + j) / 2 + 1];
+                        x = __ffma2_rn(make_float2(__uint_as_float(u[j]), __uint_as_float(u[j + 1])), f0, x);
+                        y = __ffma2_rn(make_float2(__uint_as_float(u[j + 2]), __uint_as_float(u[j + 3])), f1, y);
+                    }
                 }
             }
             const int lim = row < a.M ? (int)min((int64_t)HC, a.N - col) : 0;
@@ -268,6 +301,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
             }
         }
+        if constexpr (ROWS) asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
     tc_fence_before();
@@ -276,6 +310,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     tc_fence_after();
     if (warp == 1) tmem_free<CG>(tmem, 512);
 }
+template <int CG, int BN, bool ROWS>
+constexpr int kQ8Smem = kDenseSmem<CG> + (ROWS ? 2 * kScaleBatch * BN * 4 : 0);
 
 // The sum of the splits' parts, in order, and the bias.
 template <typename T>
@@ -469,7 +505,7 @@ struct Q8Plan {
 template <int CG, int BN, bool ROWS>
 int launch_dense(const CUtensorMap& ma, const CUtensorMap& mb, const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
     auto* f = k_q8_dense<CG, BN, ROWS>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem<CG>) != cudaSuccess) {
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kQ8Smem<CG, BN, ROWS>)) != cudaSuccess) {
         cudaGetLastError();
         return SNK_ERR_CUDA;
     }
@@ -477,7 +513,7 @@ int launch_dense(const CUtensorMap& ma, const CUtensorMap& mb, const Q8DenseArgs
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));
     c.blockDim = dim3(kQ8Threads);
-    c.dynamicSmemBytes = kDenseSmem<CG>;
+    c.dynamicSmemBytes = kQ8Smem<CG, BN, ROWS>;
     c.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
