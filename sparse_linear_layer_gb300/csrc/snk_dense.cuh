@@ -308,22 +308,27 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + ab * kDenseN;
-                for (int k = k0; k < k1; ++k, r.next()) {
-                    const int s = r.slot;
-                    if (!mbar_wait(&full[s], r.parity)) {
-                        ok = false;
-                        break;
-                    }
+                if (k0 < k1 && !mbar_wait(&full[r.slot], r.parity)) {
+                    ok = false;
+                    break;
+                }
+                for (int k = k0; k < k1; ++k) {
                     tc_fence_after();
+                    const int s = r.slot;
                     const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kDenseM * 128;
+                    r.next();
 #pragma unroll
                     for (int kk = 0; kk < kDenseK / 16; ++kk) {
                         // 16 columns of K: 32 bytes along a K-major row, two atoms of an MN-major box
                         const uint64_t da = A_MN ? desc_mn128(sa + kk * 2048) : desc_sw128(sa + kk * 32);
                         const uint64_t db = B_MN ? desc_mn128(sb + kk * 2048) : desc_sw128(sb + kk * 32);
                         dense_mma<CG>(d, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
+                        // the next stage is waited for while the tensor cores are busy (a wait
+                        // costs a hundred cycles even when there is nothing to wait for)
+                        if (kk == 1 && k + 1 < k1 && !mbar_wait(&full[r.slot], r.parity)) ok = false;
                     }
                     dense_commit<CG>(&empty[s]);
+                    if (!ok) break;
                 }
                 if (ok) dense_commit<CG>(&accf[ab]);
             }

@@ -19,7 +19,7 @@
 namespace snk {
 namespace {
 
-// Threads: four warps of roles (TMA, MMA, two that only give up registers) and eight of the
+// Threads: four warps of roles (TMA, two that issue MMAs, one that allocates) and eight of the
 // epilogue, whose threads keep 128 sums each.  168 registers a thread at launch, redistributed.
 constexpr int kQ8Threads = 384;
 constexpr int kQ8RoleRegs = 72, kQ8SumRegs = 216;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     extern __shared__ __align__(1024) unsigned char q8_raw[];
     unsigned char* sm = q8_raw + ((1024 - (smem_u32(q8_raw) & 1023)) & 1023);
     float* sb_s = reinterpret_cast<float*>(sm + S * kStage);   // ROWS: [2][kScaleBatch][BN]
-    __shared__ uint64_t full[S], empty[S], accf[NB], acce[NB], fin;
+    __shared__ uint64_t full[S], empty[S], accf[NB], acce[NB], fin[2];
     __shared__ uint32_t tmem_base;
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -124,10 +124,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             mbar_init(&accf[i], 1);
             mbar_init(&acce[i], kDenseEpilogueWarps * CG);
         }
-        mbar_init(&fin, 1);
+        mbar_init(&fin[0], 1);
+        mbar_init(&fin[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<CG>(&tmem_base, 512);
+    if (warp == 3) tmem_alloc<CG>(&tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
@@ -163,7 +164,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             }
             if (!ok && rank == 0) drain_last(full, r, used);
         }
-        if (warp == 1 && lane == 0 && rank == 0) {
+        // Two threads issue, one the even groups and one the odd ones: a group takes the tensor
+        // cores 512 cycles, but its thread 1000 (issue blocks while they are busy, and two
+        // waits and two commits add what they take even when nothing is to be waited for).
+        if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
+            const uint32_t mine = warp - 1;
             bool ok = true;
             Stages<S> r;
             uint32_t w = 0;   // groups done
@@ -171,8 +176,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
                 const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
                 for (int g = g0; g < g1; ++g, ++w, r.next()) {
+                    if ((w & 1) != mine) continue;
                     const int s = r.slot, ab = (int)(w % NB);
-                    if ((w >= NB && !mbar_wait(&acce[ab], (w / NB - 1) & 1)) || !mbar_wait(&full[s], r.parity)) {
+                    if (!mbar_wait(&full[s], r.parity) || (w >= NB && !mbar_wait(&acce[ab], (w / NB - 1) & 1))) {
                         ok = false;
                         break;
                     }
@@ -186,8 +192,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
             }
             if (!ok) {
-                dense_commit<CG>(&fin);
-                mbar_wait(&fin, 0, kTcDrainCycles);
+                dense_commit<CG>(&fin[mine]);
+                mbar_wait(&fin[mine], 0, kTcDrainCycles);
             }
         }
     } else {
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_free<CG>(tmem, 512);
+    if (warp == 3) tmem_free<CG>(tmem, 512);
 }
 template <int CG, int BN, bool ROWS>
 constexpr int kQ8Smem = kDenseSmem<CG> + (ROWS ? 2 * kScaleBatch * BN * 4 : 0);
