@@ -533,7 +533,7 @@ int snk_q8_pack_blocks(const void* w, int dtype, int64_t rows, int64_t cols, voi
  * bits.  A wait in a kernel that runs out (about two seconds) leaves NaN.
  * Errors: SNK_ERR_ARG, SNK_ERR_LIMIT, SNK_ERR_CUDA.
  */
-int64_t snk_q8_matmul_scratch(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb);
+int64_t snk_q8_matmul_scratch(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int b_blocks);
 int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void* b, int64_t ldb,
                   const float* b_scales, int b_blocks, int64_t M, int64_t N, int64_t K, const float* bias,
                   void* y, int dtype, void* scratch, void* stream);

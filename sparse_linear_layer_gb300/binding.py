@@ -85,7 +85,7 @@ def lib():
         L.snk_q8_pack_both_scratch.restype = i64
         L.snk_q8_pack_both.argtypes = [P, I, i64, i64, P, i64, P, P, i64, P, P, P, P]
         L.snk_q8_pack_blocks.argtypes = [P, I, i64, i64, P, i64, P, P, i64, P, P]
-        L.snk_q8_matmul_scratch.argtypes = [i64, i64, i64, i64, i64]
+        L.snk_q8_matmul_scratch.argtypes = [i64, i64, i64, i64, i64, I]
         L.snk_q8_matmul_scratch.restype = i64
         L.snk_q8_matmul.argtypes = [P, i64, P, P, i64, P, I, i64, i64, i64, P, P, I, P, P]
         L.snk_vocab_loss_scratch.argtypes = [i64, i64, i64, I]
@@ -364,9 +364,9 @@ def snk_q8_pack_blocks(w, dtype: int, rows: int, cols: int, codes=None, scales=N
                                     _ptr(scales_t), _stream(stream)), "snk_q8_pack_blocks")
 
 
-def snk_q8_matmul_scratch(m: int, n: int, k: int, lda: int, ldb: int) -> int:
+def snk_q8_matmul_scratch(m: int, n: int, k: int, lda: int, ldb: int, b_blocks: bool) -> int:
     """Bytes of scratch that snk_q8_matmul needs."""
-    return lib().snk_q8_matmul_scratch(m, n, k, lda, ldb)
+    return lib().snk_q8_matmul_scratch(m, n, k, lda, ldb, int(b_blocks))
 
 
 def snk_q8_matmul(a, a_scales, b, b_scales, b_blocks: bool, m: int, n: int, k: int, bias, y, dtype: int, scratch=None,

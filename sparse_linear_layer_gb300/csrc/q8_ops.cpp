@@ -504,7 +504,7 @@ PyObject* op_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t lda = x.codes.is_contiguous() ? x.cols : x.codes.stride(0);
         const int64_t ldb = w.codes.is_contiguous() ? w.cols : w.codes.stride(0);
         at::Tensor scratch;
-        const int64_t bytes = g.matmul_scratch(x.rows, w.rows, x.cols, lda, ldb);
+        const int64_t bytes = g.matmul_scratch(x.rows, w.rows, x.cols, lda, ldb, blocks);
         if (bytes > 0) scratch = at::empty({bytes}, options.dtype(at::kByte));
         check(g.matmul(x.codes.data_ptr(), lda, (const float*)x.scales.data_ptr(), w.codes.data_ptr(), ldb,
                        (const float*)w.scales.data_ptr(), blocks, x.rows, w.rows, x.cols, (const float*)ptr(bias), y.data_ptr(),

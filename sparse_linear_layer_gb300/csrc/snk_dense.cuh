@@ -182,6 +182,56 @@ __device__ __forceinline__ void dense_read(uint32_t taddr, const DenseTile& t, f
     }
 }
 
+// Rows of an epilogue warp's tile, 128 bytes each, turned in shared memory so that a store
+// instruction writes 128 contiguous bytes of a row instead of 32 bytes of 32 rows (the
+// output of 128 x 256 bf16 took 4900 cycles that way).
+constexpr int kTurnPitch = 144;                   // bytes of a row: 16-byte accesses by rows and by columns meet no bank twice
+constexpr int kTurnBytes = 32 * kTurnPitch;       // of a warp
+template <typename T>
+struct Turn {
+    static constexpr int kCols = 128 / (int)sizeof(T);
+    // lane's row
+    __device__ __forceinline__ static void put(unsigned char* buf, int lane, const float (&v)[kCols]) {
+        uint4* p = reinterpret_cast<uint4*>(buf + lane * kTurnPitch);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(v[4 * i + k]);
+                else w[k] = pack2<T>(make_float2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]));
+            }
+            p[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+    }
+    // the warp's first `rows` rows, their first `cols` columns, to out (row stride ld); vec: 16-byte
+    // aligned rows and whole 16-byte chunks
+    __device__ __forceinline__ static void flush(const unsigned char* buf, int lane, T* out, int64_t ld, int rows, int cols, bool vec) {
+        if (vec) {
+            const int seg = lane & 7;
+            if (seg * (16 / (int)sizeof(T)) < cols) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    if (r < rows)
+                        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(out + r * ld) + 16 * seg) =
+                            *reinterpret_cast<const uint4*>(buf + r * kTurnPitch + 16 * seg);
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+                const T* p = reinterpret_cast<const T*>(buf + r * kTurnPitch);
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32)
+                    if (c + lane < cols) out[r * ld + c + lane] = p[c + lane];
+            }
+        }
+        __syncwarp();
+    }
+};
+
 // Position in a ring of N slots: the slot and its phase's parity (counted, not divided:
 // the issuing threads pass here for every stage).
 template <int N>

@@ -13,6 +13,7 @@
 // bytes of a row.  k_q8_rows is for up to 16 rows of A, where the codes of B are read
 // once and nothing else counts.
 #include <algorithm>
+#include <type_traits>
 
 #include "snk_dense.cuh"
 
@@ -39,7 +40,7 @@ struct Q8DenseArgs {
     const float* bias;     // [N] or null
     void* y;               // [M, N]
     int dtype;
-    int vec;               // bytes of a store: 32, 16 or an element's, by the rows' alignment
+    int vec;               // rows of y (slab) are aligned to 16 bytes
     float* slab;           // splits > 1: [splits][M, N] sums without bias
 };
 
@@ -58,58 +59,33 @@ __device__ __forceinline__ void q8_mma(uint32_t d, uint64_t a, uint64_t b, uint3
             "l"(a), "l"(b), "r"(idesc), "r"(acc)
             : "memory");
 }
-__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
+// ROWS: scales of A's and B's rows, [groups][rows] in the call's scratch, come with the
+// stages, into a ring of their own: an epilogue warp reads those of a group after the
+// stage of that group may have been filled again, but never as late as the ring is long (it
+// frees an accumulator, of which there are up to 4, before it reads the last of them, and TMA
+// is up to 6 stages ahead of the MMAs).
+constexpr int kScaleSlots = 16;
 
-// Sixteen values of a row from column c on, of which those before `lim` exist.
-template <typename T>
-__device__ __forceinline__ void store16(T* out, int c, int lim, int vec, const float (&v)[16]) {
-    constexpr int E = sizeof(T);
-    uint32_t w[4 * E];
-#pragma unroll
-    for (int i = 0; i < 4 * E; ++i)
-        w[i] = E == 4 ? __float_as_uint(v[i]) : pack2<typename std::conditional<E == 2, T, __half>::type>(
-                                                    make_float2(v[(2 * i) & 15], v[(2 * i + 1) & 15]));
-    if (vec == 32 && c + 16 <= lim) {
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            uint32_t u[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = w[8 * i + k];
-            st32(reinterpret_cast<char*>(out + c) + 32 * i, u);
-        }
-    } else if (vec >= 16) {   // whole 16-byte chunks
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (c + i * (16 / E) < lim)
-                *reinterpret_cast<uint4*>(reinterpret_cast<char*>(out + c) + 16 * i) =
-                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (c + i < lim) out[c + i] = from_f32<T>(v[i]);
-    }
-}
-
-// Scales of B by row: the tile's, this many groups at a time, two batches in shared memory.
-constexpr int kScaleBatch = 8;
-__device__ __forceinline__ void copy4(float* dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
+template <int CG, int BN>
+constexpr int kQ8StageBytes = (kDenseM + BN / CG) * 128;
+template <int CG, int BN>
+constexpr int kQ8Stages = std::min(6, 160 * 1024 / kQ8StageBytes<CG, BN>);
+template <int CG, int BN, bool ROWS>
+constexpr int kQ8Smem = kQ8Stages<CG, BN> * kQ8StageBytes<CG, BN> + kDenseEpilogueWarps * kTurnBytes +
+                        (ROWS ? kScaleSlots * (kDenseM + BN) * 4 : 0) + 1024;
 
 template <int CG, int BN, bool ROWS>
 __global__ void __launch_bounds__(kQ8Threads, 1)
-    k_q8_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Q8DenseArgs a) {
-    constexpr int S = kDenseStages<CG>, kStage = kDenseStageBytes<CG>;
+    k_q8_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb, const Q8DenseArgs a) {
+    constexpr int S = kQ8Stages<CG, BN>, kStage = kQ8StageBytes<CG, BN>;
     constexpr int HC = BN / 2;    // columns of an epilogue warp
     constexpr int HB = BN / CG;   // rows of B that a CTA loads
     constexpr int NB = BN == 256 ? 2 : 4;   // accumulators
     extern __shared__ __align__(1024) unsigned char q8_raw[];
     unsigned char* sm = q8_raw + ((1024 - (smem_u32(q8_raw) & 1023)) & 1023);
-    float* sb_s = reinterpret_cast<float*>(sm + S * kStage);   // ROWS: [2][kScaleBatch][BN]
+    unsigned char* turn = sm + S * kStage;                                              // of each epilogue warp
+    float* scales = reinterpret_cast<float*>(turn + kDenseEpilogueWarps * kTurnBytes);   // ROWS: [kScaleSlots][kDenseM + BN]
     __shared__ uint64_t full[S], empty[S], accf[NB], acce[NB], fin[2];
     __shared__ uint32_t tmem_base;
 
@@ -142,11 +118,12 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         if (warp == 0 && lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
             Stages<S> r;
+            uint32_t w = 0;   // groups loaded
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
                 const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
                 const int m0 = (it.mt * CG + rank) * kDenseM, n0 = it.nt * BN + rank * HB;
-                for (int g = g0; g < g1; ++g) {
+                for (int g = g0; g < g1; ++g, ++w) {
                     const int s = r.slot;
                     if (used && !mbar_wait(&empty[s], r.parity ^ 1)) {
                         ok = false;
@@ -154,10 +131,15 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     }
                     unsigned char* sa = sm + s * kStage;
                     unsigned char* sb = sa + kDenseM * 128;
-                    if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(kDenseM + HB) * 128 * CG);
+                    if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)((kDenseM + HB) * 128 + (ROWS ? (kDenseM + BN) * 4 : 0)) * CG);
                     const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : first_cta(&full[s]);
                     dense_load<CG>(sa, &map_a, g * 128, m0, bar);
                     dense_load<CG>(sb, &map_b, g * 128, n0, bar);
+                    if constexpr (ROWS) {
+                        float* at = scales + (w % kScaleSlots) * (kDenseM + BN);
+                        dense_load<CG>(at, &map_sa, m0, g, bar);
+                        dense_load<CG>(at + kDenseM, &map_sb, it.nt * BN, g, bar);
+                    }
                     r.next();
                     used |= r.slot == 0;
                 }
@@ -198,7 +180,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         }
     } else {
         more_registers<kQ8SumRegs>();
-        const int half = warp >= 8 ? 1 : 0, quarter = warp & 3, et = t - 128;
+        const int half = warp >= 8 ? 1 : 0, quarter = warp & 3;
         bool ok = true;
         uint32_t w = 0;   // groups done
         for (int id = first; id < items; id += step) {
@@ -208,50 +190,29 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             const int64_t col = (int64_t)it.nt * BN + half * HC;
             // rows and columns outside the matrix read the last ones' scales and are not stored
             const float* pa = a.sa + min(row, a.M - 1) * a.n_g;
-            const float* pb = ROWS ? a.sb + min((int64_t)it.nt * BN + (et & (BN - 1)), a.N - 1) * a.n_g
-                                   : a.sb + (min(col, a.N - 1) >> 7) * a.n_g;
-            // ROWS: scales of groups [g, g + kScaleBatch) into a batch
-            auto fetch = [&](int g, int batch) {
-                if (et < BN) {
-#pragma unroll
-                    for (int i = 0; i < kScaleBatch; ++i)
-                        if (g + i < g1) copy4(sb_s + (batch * kScaleBatch + i) * BN + et, pb + g + i);
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            };
+            const float* pb = a.sb + (min(col, a.N - 1) >> 7) * a.n_g;
             float2 acc[HC / 2];
 #pragma unroll
             for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-            float na = 0.f, nb = 0.f;
-            if (g0 < g1) {
+            float na = 0.f, nb = 0.f;   // the next group's scales
+            if (!ROWS && g0 < g1) {
                 na = __ldg(pa + g0);
-                if (!ROWS) nb = __ldg(pb + g0);
-            }
-            if constexpr (ROWS) {
-                asm volatile("bar.sync 1, 256;" ::: "memory");   // the last tile's batches have been read
-                fetch(g0, 0);
+                nb = __ldg(pb + g0);
             }
             for (int g = g0; g < g1; ++g, ++w) {
                 const int ab = (int)(w % NB);
-                const float ca = na, cb = nb;
-                if (g + 1 < g1) {
+                float s = na * nb;
+                if (!ROWS && g + 1 < g1) {
                     na = __ldg(pa + g + 1);
-                    if (!ROWS) nb = __ldg(pb + g + 1);
+                    nb = __ldg(pb + g + 1);
                 }
-                const float* sbp = nullptr;
-                if constexpr (ROWS) {
-                    const int i = g - g0, batch = (i / kScaleBatch) & 1;
-                    if (i % kScaleBatch == 0) {   // this batch is here for all; the other one has been read by all
-                        asm volatile("cp.async.wait_group 0;\n bar.sync 1, 256;" ::: "memory");
-                        fetch(g + kScaleBatch, batch ^ 1);
-                    }
-                    sbp = sb_s + (batch * kScaleBatch + i % kScaleBatch) * BN + half * HC;
-                }
+                const float* at = scales + (w % kScaleSlots) * (kDenseM + BN);
+                const float* sbp = at + kDenseM + half * HC;
                 if (ok) ok = mbar_wait(&accf[ab], (w / NB) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
+                if constexpr (ROWS) s = at[quarter * 32 + lane];
                 const uint32_t ta = tmem + ab * BN + half * HC + ((uint32_t)(quarter * 32) << 16);
-                const float s = ROWS ? ca : ca * cb;
                 uint32_t r[2][32];   // the next 32 columns are read while these are added
                 tmem_ld32_async(ta, r[0]);
 #pragma unroll
@@ -282,32 +243,38 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     }
                 }
             }
-            const int lim = row < a.M ? (int)min((int64_t)HC, a.N - col) : 0;
             if (!ok) {
 #pragma unroll
                 for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
             }
-            const bool whole = a.splits == 1;
-            const int64_t at = row * a.N + col;
+            const int64_t row0 = row - lane;
+            const int rows = (int)max((int64_t)0, min((int64_t)32, a.M - row0)), cols = (int)min((int64_t)HC, a.N - col);
+            unsigned char* buf = turn + (warp - 4) * kTurnBytes;
+            auto store = [&](auto* y, const float* bias) {
+                using T = typename std::remove_pointer<decltype(y)>::type;
+                constexpr int E = Turn<T>::kCols;
+                y += row0 * a.N + col;
 #pragma unroll
-            for (int c = 0; c < HC; c += 16) {
-                if (c < lim) {
-                    float v[16];
+                for (int c = 0; c < HC; c += E) {
+                    if (c < cols) {
+                        float v[E];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = (j & 1) ? acc[(c + j) / 2].y : acc[(c + j) / 2].x;
-                    if (whole && a.bias) {
+                        for (int j = 0; j < E; ++j) v[j] = c + j >= HC ? 0.f : ((j & 1) ? acc[(c + j) / 2 % (HC / 2)].y : acc[(c + j) / 2 % (HC / 2)].x);
+                        if (bias) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c + j < lim) v[j] += __ldg(a.bias + col + c + j);
+                            for (int j = 0; j < E; ++j)
+                                if (c + j < cols) v[j] += __ldg(bias + col + c + j);
+                        }
+                        Turn<T>::put(buf, lane, v);
+                        Turn<T>::flush(buf, lane, y + c, a.N, rows, cols - c, a.vec);
                     }
-                    if (!whole) store16(a.slab + it.split * a.M * a.N + at, c, lim, a.vec, v);
-                    else if (a.dtype == SNK_F32) store16(static_cast<float*>(a.y) + at, c, lim, a.vec, v);
-                    else if (a.dtype == SNK_F16) store16(static_cast<__half*>(a.y) + at, c, lim, a.vec, v);
-                    else store16(static_cast<__nv_bfloat16*>(a.y) + at, c, lim, a.vec, v);
                 }
-            }
+            };
+            if (a.splits > 1) store(a.slab + it.split * a.M * a.N, nullptr);
+            else if (a.dtype == SNK_F32) store(static_cast<float*>(a.y), a.bias);
+            else if (a.dtype == SNK_F16) store(static_cast<__half*>(a.y), a.bias);
+            else store(static_cast<__nv_bfloat16*>(a.y), a.bias);
         }
-        if constexpr (ROWS) asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
     tc_fence_before();
@@ -316,8 +283,29 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     tc_fence_after();
     if (warp == 3) tmem_free<CG>(tmem, 512);
 }
-template <int CG, int BN, bool ROWS>
-constexpr int kQ8Smem = kDenseSmem<CG> + (ROWS ? 2 * kScaleBatch * BN * 4 : 0);
+// Scales [rows, n_g] of A (blockIdx.y 0) or B (1) as [n_g][padded], zeros behind the rows.
+__global__ void __launch_bounds__(256) k_q8_scales(const float* __restrict__ sa, int64_t M, int64_t padded_m, float* __restrict__ ta,
+                                                   const float* __restrict__ sb, int64_t N, int64_t padded_n, float* __restrict__ tb,
+                                                   int n_g) {
+    __shared__ float sm[32][33];
+    const bool second = blockIdx.y == 1;
+    const float* src = second ? sb : sa;
+    float* dst = second ? tb : ta;
+    const int64_t rows = second ? N : M, padded = second ? padded_n : padded_m;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t tiles_g = (n_g + 31) / 32, tiles = padded / 32 * tiles_g;
+    for (int64_t id = blockIdx.x; id < tiles; id += gridDim.x) {
+        const int64_t r0 = id / tiles_g * 32;
+        const int g0 = (int)(id % tiles_g) * 32;
+#pragma unroll
+        for (int i = warp; i < 32; i += 8) sm[i][lane] = r0 + i < rows && g0 + lane < n_g ? __ldg(src + (r0 + i) * n_g + g0 + lane) : 0.f;
+        __syncthreads();
+#pragma unroll
+        for (int i = warp; i < 32; i += 8)
+            if (g0 + i < n_g) dst[(int64_t)(g0 + i) * padded + r0 + lane] = sm[lane][i];
+        __syncthreads();
+    }
+}
 
 // The sum of the splits' parts, in order, and the bias.
 template <typename T>
@@ -459,6 +447,18 @@ int sms() {
 }
 int launched() { return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA; }
 
+// Scales [n_g][padded] in boxes of one group and `box` rows.
+bool scales_map(CUtensorMap* map, const float* base, int64_t padded, int n_g, int box_rows) {
+    EncodeTiledFn fn = encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)padded, (cuuint64_t)n_g};
+    cuuint64_t strides[1] = {(cuuint64_t)padded * 4};
+    cuuint32_t box[2] = {(cuuint32_t)box_rows, 1u};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool q8_map(CUtensorMap* map, const uint8_t* base, int64_t len, int64_t rows, int64_t ld, int box_rows) {
     EncodeTiledFn fn = encoder();
     if (!fn) return false;
@@ -478,22 +478,40 @@ struct Q8Plan {
     int64_t ld;              // of the copies
     uint8_t *a, *b;
     float* slab;
+    int64_t padded_m, padded_n;   // scales by rows: their transposed copies' rows
+    float *ta, *tb;
     int64_t bytes;
-    Q8Plan(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int num_sms, void* scratch) {
+    Q8Plan(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, bool blocks, int num_sms, void* scratch) {
         rows = M <= kRowsMax;
         copy_a = lda % 16 != 0;
         copy_b = ldb % 16 != 0;
         ld = up(K, 16);
         const int n_g = (int)ceil_div(K, 128);
-        cg = M > 128 && ceil_div(M, 256) * ceil_div(N, 256) >= num_sms / 4 ? 2 : 1;
-        bn = 256;
-        if (cg == 1)
-            while (bn > 64 && ceil_div(M, 128) * ceil_div(N, bn) < num_sms) bn /= 2;
+        // The tile and the ranges of K whose waves take least. Times in us as measured: of a group,
+        // of a tile beside its groups, of joining ranges (and their sums, written and read).
+        struct Form {
+            int cg, bn;
+            double group;
+        };
+        constexpr Form forms[] = {{2, 256, 0.33}, {1, 256, 0.40}, {1, 128, 0.26}, {1, 64, 0.24}};
+        double best = 1e30;
+        for (const Form& f : forms) {
+            if (f.cg == 2 && M <= 128) continue;
+            const int64_t mt = ceil_div(M, 128 * f.cg), nt = ceil_div(N, f.bn), units = num_sms / f.cg;
+            for (int sp = 1; sp <= 16 && (sp == 1 || n_g / sp >= 4); ++sp) {
+                const double waves = (double)ceil_div(mt * nt * sp, units);
+                const double t = waves * ((double)ceil_div(n_g, sp) * f.group + 1.5) + (sp > 1 ? 3.0 + 2e-6 * sp * M * N : 0.0);
+                if (t < best) {
+                    best = t;
+                    cg = f.cg;
+                    bn = f.bn;
+                    splits = sp;
+                }
+            }
+        }
+        if (rows) splits = 1;
         n_mt = (int)ceil_div(M, 128 * cg);
         n_nt = (int)ceil_div(N, bn);
-        const int64_t tiles = (int64_t)n_mt * n_nt, units = num_sms / cg;
-        splits = 1;
-        if (!rows && 2 * tiles <= units) splits = (int)std::max<int64_t>(1, std::min<int64_t>(units / tiles, n_g / 8));
         char* p = static_cast<char*>(scratch);
         int64_t used = 0;
         auto take = [&](int64_t n) {
@@ -504,12 +522,17 @@ struct Q8Plan {
         a = reinterpret_cast<uint8_t*>(take(copy_a ? M * ld : 0));
         b = reinterpret_cast<uint8_t*>(take(copy_b ? N * ld : 0));
         slab = reinterpret_cast<float*>(take(splits > 1 ? 4 * splits * M * N : 0));
+        padded_m = up(M, 128 * cg);
+        padded_n = up(N, bn);
+        const bool turn = !rows && !blocks;
+        ta = reinterpret_cast<float*>(take(turn ? 4 * n_g * padded_m : 0));
+        tb = reinterpret_cast<float*>(take(turn ? 4 * n_g * padded_n : 0));
         bytes = used;
     }
 };
 
 template <int CG, int BN, bool ROWS>
-int launch_dense(const CUtensorMap& ma, const CUtensorMap& mb, const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
+int launch_dense(const CUtensorMap (&m)[4], const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
     auto* f = k_q8_dense<CG, BN, ROWS>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kQ8Smem<CG, BN, ROWS>)) != cudaSuccess) {
         cudaGetLastError();
@@ -527,18 +550,18 @@ int launch_dense(const CUtensorMap& ma, const CUtensorMap& mb, const Q8DenseArgs
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = CG == 1 ? 0 : 1;
-    if (cudaLaunchKernelEx(&c, f, ma, mb, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&c, f, m[0], m[1], m[2], m[3], a) != cudaSuccess) {
         cudaGetLastError();
         return SNK_ERR_CUDA;
     }
     return SNK_OK;
 }
 template <bool ROWS>
-int launch_dense(const Q8Plan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
-    if (p.cg == 2) return launch_dense<2, 256, ROWS>(ma, mb, a, num_sms, s);
-    if (p.bn == 256) return launch_dense<1, 256, ROWS>(ma, mb, a, num_sms, s);
-    if (p.bn == 128) return launch_dense<1, 128, ROWS>(ma, mb, a, num_sms, s);
-    return launch_dense<1, 64, ROWS>(ma, mb, a, num_sms, s);
+int launch_dense(const Q8Plan& p, const CUtensorMap (&m)[4], const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
+    if (p.cg == 2) return launch_dense<2, 256, ROWS>(m, a, num_sms, s);
+    if (p.bn == 256) return launch_dense<1, 256, ROWS>(m, a, num_sms, s);
+    if (p.bn == 128) return launch_dense<1, 128, ROWS>(m, a, num_sms, s);
+    return launch_dense<1, 64, ROWS>(m, a, num_sms, s);
 }
 template <typename T>
 int launch_rows(const Q8RowsArgs& r, cudaStream_t s) {
@@ -568,10 +591,10 @@ using namespace snk;
 
 extern "C" {
 
-int64_t snk_q8_matmul_scratch(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
+int64_t snk_q8_matmul_scratch(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int b_blocks) {
     if (M < 1 || bad_product(M, N, K) != SNK_OK) return 0;
     const int n = sms();
-    return n < 1 ? 0 : Q8Plan(M, N, K, lda, ldb, n, nullptr).bytes;
+    return n < 1 ? 0 : Q8Plan(M, N, K, lda, ldb, b_blocks, n, nullptr).bytes;
 }
 
 int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void* b, int64_t ldb, const float* b_scales,
@@ -587,7 +610,7 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
     if (!a || !a_scales || !y) return SNK_ERR_ARG;
     const int n = sms();
     if (n < 1) return SNK_ERR_CUDA;
-    const Q8Plan p(M, N, K, lda, ldb, n, scratch);
+    const Q8Plan p(M, N, K, lda, ldb, b_blocks, n, scratch);
     if (p.bytes > 0 && !scratch) return SNK_ERR_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     auto copy = [&](const void* src, int64_t ld, uint8_t* dst, int64_t rows) {
@@ -611,8 +634,16 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
         const Q8RowsArgs r{pa, pb, lda, ldb, M, N, K, n_g, a_scales, b_scales, bias, y, dtype, b_blocks};
         return dtype == SNK_F32 ? launch_rows<float>(r, s) : dtype == SNK_F16 ? launch_rows<__half>(r, s) : launch_rows<__nv_bfloat16>(r, s);
     }
-    CUtensorMap ma, mb;
-    if (!q8_map(&ma, pa, K, M, lda, kDenseM) || !q8_map(&mb, pb, K, N, ldb, p.bn / p.cg)) return SNK_ERR_CUDA;
+    CUtensorMap m[4];
+    if (!q8_map(&m[0], pa, K, M, lda, kDenseM) || !q8_map(&m[1], pb, K, N, ldb, p.bn / p.cg)) return SNK_ERR_CUDA;
+    m[2] = m[3] = m[0];
+    if (!b_blocks) {
+        if (!scales_map(&m[2], p.ta, p.padded_m, n_g, kDenseM) || !scales_map(&m[3], p.tb, p.padded_n, n_g, p.bn)) return SNK_ERR_CUDA;
+        const int64_t tiles = std::max(p.padded_m, p.padded_n) / 32 * ceil_div(n_g, 32);
+        k_q8_scales<<<dim3((unsigned)std::min<int64_t>(tiles, 16 * n), 2), 256, 0, s>>>(a_scales, M, p.padded_m, p.ta, b_scales, N,
+                                                                                     p.padded_n, p.tb, n_g);
+        if (int st = launched(); st != SNK_OK) return st;
+    }
     Q8DenseArgs q = {};
     q.M = M;
     q.N = N;
@@ -630,8 +661,8 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
     q.slab = p.slab;
     const int e = p.splits > 1 || dtype == SNK_F32 ? 4 : 2;
     const uintptr_t base = (uintptr_t)(p.splits > 1 ? (void*)p.slab : y) | (uintptr_t)(N * e);
-    q.vec = (base & 31) == 0 ? 32 : ((base & 15) == 0 ? 16 : e);
-    const int st = b_blocks ? launch_dense<false>(p, ma, mb, q, n, s) : launch_dense<true>(p, ma, mb, q, n, s);
+    q.vec = (base & 15) == 0;
+    const int st = b_blocks ? launch_dense<false>(p, m, q, n, s) : launch_dense<true>(p, m, q, n, s);
     if (st != SNK_OK || p.splits == 1) return st;
     return dtype == SNK_F32   ? launch_join<float>(p, M, N, bias, y, n, s)
            : dtype == SNK_F16 ? launch_join<__half>(p, M, N, bias, y, n, s)
