@@ -562,7 +562,7 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
  * Ignored rows get dx = 0; a row whose target is out of range gets NaN.
  *
  * scratch: snk_vocab_loss_scratch(rows, cols, vocab, backward) bytes (backward 0 or 1)
- * on the current device, 256-byte aligned: at most about 256 MB (or 512 bytes a row) for
+ * on the current device, 256-byte aligned: at most about 512 MB (or 512 bytes a row) for
  * dz, and some copies of x and dx; where cols is no multiple of 8, also copies of x and
  * weight with padded rows.  No state and no allocation: the calls only enqueue work, may be captured into
  * a graph, and give the same bits when repeated.  rows == 0: dweight and a sum are zero,

@@ -28,16 +28,15 @@ constexpr int kDenseK = 64;              // columns of K per stage: 128 bytes
 constexpr int kDenseThreads = 320;
 constexpr int kDenseEpilogueWarps = 8;
 constexpr int kDenseBoxBytes = 64 * 128;   // an MN-major box: 64 rows of K, 64 columns
-template <int CG>
-constexpr int kDenseStages = CG == 1 ? 4 : 6;
-template <int CG>
-constexpr int kDenseStageBytes = (kDenseM + kDenseN / CG) * 128;
-template <int CG>
-constexpr int kDenseSmem = kDenseStages<CG> * kDenseStageBytes<CG> + 1024;
+constexpr int kDenseStages = 8;          // at most
+constexpr int kDenseStageRoom = 192 * 1024;
+constexpr int kDenseSmem = kDenseStageRoom + 1024;
 
 struct DenseArgs {
     int n_mt, n_nt;        // tiles
     int bn;                // columns of a tile
+    int a_rows;            // rows of A that a CTA loads of a tile: 128, or fewer where there is one tile of fewer
+    int stages;
     int splits;            // ranges of K, each an item of its own
     int64_t K;
     uint32_t idesc;
@@ -63,6 +62,13 @@ struct DenseItem {
         return t;
     }
 };
+
+// Stages that fit: A's rows (what the MMA reads behind them is another operand's, for rows
+// that nobody reads) and B's.
+inline int dense_stages(int cg, int a_rows, int bn) {
+    const int bytes = (a_rows + bn / cg) * 128, room = kDenseStageRoom - (kDenseM - a_rows) * 128;
+    return room / bytes < kDenseStages ? room / bytes : kDenseStages;
+}
 
 // kind::f16 instruction descriptor: D fp32, A and B fp16 (0) or bf16 (1).
 inline uint32_t dense_idesc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
@@ -232,25 +238,25 @@ struct Turn {
     }
 };
 
-// Position in a ring of N slots: the slot and its phase's parity (counted, not divided:
+// Position in a ring of slots: the slot and its phase's parity (counted, not divided:
 // the issuing threads pass here for every stage).
-template <int N>
 struct Stages {
+    const int n;
     int slot = 0;
     uint32_t parity = 0;
+    __device__ explicit Stages(int slots) : n(slots) {}
     __device__ __forceinline__ void next() {
-        if (++slot == N) {
+        if (++slot == n) {
             slot = 0;
             parity ^= 1;
         }
     }
 };
 // The stages that a producer filled last have landed.
-template <int N>
-__device__ __forceinline__ void drain_last(uint64_t* full, Stages<N> r, bool all) {
-    for (int i = 0; i < N; ++i) {   // oldest first: slots before r.slot are of this round
-        const bool older = r.slot + i >= N;
-        const int slot = older ? r.slot + i - N : r.slot + i;
+__device__ __forceinline__ void drain_last(uint64_t* full, const Stages& r, bool all) {
+    for (int i = 0; i < r.n; ++i) {   // oldest first: slots before r.slot are of this round
+        const bool older = r.slot + i >= r.n;
+        const int slot = older ? r.slot + i - r.n : r.slot + i;
         if (older || all) mbar_wait(&full[slot], older ? r.parity : r.parity ^ 1, kTcDrainCycles);
     }
 }
@@ -261,7 +267,7 @@ template <int CG, bool A_MN, bool B_MN, class Epilogue>
 __global__ void __launch_bounds__(kDenseThreads, 1)
     k_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const DenseArgs a,
             const typename Epilogue::Args ea) {
-    constexpr int S = kDenseStages<CG>, kStage = kDenseStageBytes<CG>;
+    constexpr int S = kDenseStages;
     extern __shared__ __align__(1024) unsigned char dense_raw[];
     unsigned char* sm = dense_raw + ((1024 - (smem_u32(dense_raw) & 1023)) & 1023);
     __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin;
@@ -304,12 +310,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const int items = n_mt * a.n_nt * a.splits;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
     const int half_b = a.bn / CG;   // rows of B that this CTA loads
-    const uint32_t tx = (uint32_t)(kDenseM + half_b) * 128 * CG;
+    const uint32_t tx = (uint32_t)(a.a_rows + half_b) * 128 * CG;
+    const int a_bytes = a.a_rows * 128, stage = (a.a_rows + half_b) * 128;
 
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
-            Stages<S> r;
+            Stages r(a.stages);
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int k0 = (int)((int64_t)n_k * it.split / a.splits), k1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
@@ -320,8 +327,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                         ok = false;
                         break;
                     }
-                    unsigned char* sa = sm + s * kStage;
-                    unsigned char* sb = sa + kDenseM * 128;
+                    unsigned char* sa = sm + s * stage;
+                    unsigned char* sb = sa + a_bytes;
                     if (rank == 0) mbar_expect_tx(&full[s], tx);
                     const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : first_cta(&full[s]);
                     const int kc = k * kDenseK;
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             bool ok = true;
-            Stages<S> r;
+            Stages r(a.stages);
             uint32_t q = 0;   // accumulators filled
             for (int id = first; id < items && ok; id += step, ++q) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                 for (int k = k0; k < k1; ++k) {
                     tc_fence_after();
                     const int s = r.slot;
-                    const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kDenseM * 128;
+                    const uint32_t sa = smem_u32(sm + s * stage), sb = sa + a_bytes;
                     r.next();
 #pragma unroll
                     for (int kk = 0; kk < kDenseK / 16; ++kk) {
@@ -445,7 +452,7 @@ template <int CG, bool A_MN, bool B_MN, class Epilogue>
 int dense_launch(const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& ea, int num_sms,
                  cudaStream_t s) {
     auto* f = k_dense<CG, A_MN, B_MN, Epilogue>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem<CG>) != cudaSuccess) {
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem) != cudaSuccess) {
         cudaGetLastError();
         return SNK_ERR_CUDA;
     }
@@ -453,7 +460,7 @@ int dense_launch(const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& 
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));
     c.blockDim = dim3(kDenseThreads);
-    c.dynamicSmemBytes = kDenseSmem<CG>;
+    c.dynamicSmemBytes = kDenseSmem;
     c.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         fewer_registers<kQ8RoleRegs>();
         if (warp == 0 && lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
-            Stages<S> r;
+            Stages r(S);
             uint32_t w = 0;   // groups loaded
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
             const uint32_t mine = warp - 1;
             bool ok = true;
-            Stages<S> r;
+            Stages r(S);
             uint32_t w = 0;   // groups done
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
@@ -260,7 +260,16 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                         float v[E];
 #pragma unroll
                         for (int j = 0; j < E; ++j) v[j] = c + j >= HC ? 0.f : ((j & 1) ? acc[(c + j) / 2 % (HC / 2)].y : acc[(c + j) / 2 % (HC / 2)].x);
-                        if (bias) {
+                        if (bias && c + E <= cols && HC >= E && ((uintptr_t)(bias + col) & 15) == 0) {
+#pragma unroll
+                            for (int j = 0; j < E; j += 4) {
+                                const float4 b4 = __ldg(reinterpret_cast<const float4*>(bias + col + c + j));
+                                v[j] += b4.x;
+                                v[j + 1] += b4.y;
+                                v[j + 2] += b4.z;
+                                v[j + 3] += b4.w;
+                            }
+                        } else if (bias) {
 #pragma unroll
                             for (int j = 0; j < E; ++j)
                                 if (c + j < cols) v[j] += __ldg(bias + col + c + j);
@@ -437,14 +446,6 @@ __global__ void __launch_bounds__(256) k_q8_pad(const uint8_t* __restrict__ src,
 // ---- host ------------------------------------------------------------------------------
 
 int64_t up(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
-int sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
-}
 int launched() { return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA; }
 
 // Scales [n_g][padded] in boxes of one group and `box` rows.
@@ -593,7 +594,7 @@ extern "C" {
 
 int64_t snk_q8_matmul_scratch(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int b_blocks) {
     if (M < 1 || bad_product(M, N, K) != SNK_OK) return 0;
-    const int n = sms();
+    const int n = device_sms();
     return n < 1 ? 0 : Q8Plan(M, N, K, lda, ldb, b_blocks, n, nullptr).bytes;
 }
 
@@ -608,7 +609,7 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
         return SNK_ERR_ARG;
     if (M == 0) return SNK_OK;
     if (!a || !a_scales || !y) return SNK_ERR_ARG;
-    const int n = sms();
+    const int n = device_sms();
     if (n < 1) return SNK_ERR_CUDA;
     const Q8Plan p(M, N, K, lda, ldb, b_blocks, n, scratch);
     if (p.bytes > 0 && !scratch) return SNK_ERR_ARG;

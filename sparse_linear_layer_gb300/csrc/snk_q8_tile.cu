@@ -2,12 +2,14 @@
 // columns and, transposed, along the rows (what the three products of a dense layer's
 // training step take), the column sums, and codes with one scale for each block.
 //
-// A block of threads takes a tile: its values go into shared memory once, rows are packed
-// on the way in, columns from there.  Bound by memory: every element is read once and
+// A block of threads takes a tile: its values go into shared memory once, rows and columns are
+// packed from there.  Bound by memory: every element is read once and
 // written as one byte per form.
 #include <algorithm>
+#include <type_traits>
 
 #include "snk_q8.cuh"
+#include "snk_tcgen.cuh"
 
 namespace snk {
 namespace {
@@ -25,92 +27,117 @@ struct TileArgs {
     float* part;                   // [tiles_r, cols] sums of the tile's columns, or null
 };
 
-// Pitch of a tile's row in shared memory: columns lie in different banks.
-template <typename T>
-constexpr int kPitch = sizeof(T) == 4 ? kTile + 1 : kTile + 2;
-template <typename T>
-constexpr int kTileSmem = kTile * kPitch<T> * (int)sizeof(T);
+// How a tile comes in: by TMA, the next one while this one is worked on (16-bit types; of
+// 32-bit ones a block holds one, and two blocks take turns on an SM), or, where rows are not
+// whole 16-byte chunks, by plain loads.
+enum TileLoad { kTileTma, kTilePlain };
+template <typename T, TileLoad LOAD>
+constexpr int kTileBuffers = LOAD == kTileTma && sizeof(T) == 2 ? 2 : 1;
+// The tiles, and a tile's codes along the rows (turned there, so that a column's 128 bytes leave
+// together: as 32-byte stores of 32 columns the training step's packs took 2.3 times as long).
+template <typename T, TileLoad LOAD>
+constexpr int kTileSmem = kTile * kTile * (kTileBuffers<T, LOAD> * (int)sizeof(T) + 1) + 128;
 
-// BLOCKS: one scale for the whole tile.  VEC: rows are read four columns a lane.
-template <typename T, bool BLOCKS, bool VEC>
-__global__ void __launch_bounds__(kTileThreads) k_q8_tile(const TileArgs a) {
-    extern __shared__ __align__(16) unsigned char tile_raw[];
-    T* sm = reinterpret_cast<T*>(tile_raw);
-    __shared__ float most_s[kTileThreads];
-    __shared__ float sums_s[kTile];
+// BLOCKS: one scale for the whole tile.
+template <typename T, bool BLOCKS, TileLoad LOAD>
+__global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_constant__ CUtensorMap map, const TileArgs a) {
+    // along the rows, a thread takes a word (CW columns) of RT rows; every access to the tile is then
+    // of consecutive words by the lanes of a warp
+    constexpr int CW = 4 / (int)sizeof(T), WORDS = kTile / CW, RT = kTile * WORDS / kTileThreads;
+    constexpr int BUFS = kTileBuffers<T, LOAD>, BYTES = kTile * kTile * (int)sizeof(T);
+    extern __shared__ __align__(128) unsigned char tile_raw[];
+    unsigned char* tiles = tile_raw + ((128 - (smem_u32(tile_raw) & 127)) & 127);
+    unsigned char* turned = tiles + BUFS * BYTES;   // [column][16-byte chunk of rows, exclusive-or (column / CW) % 8]
+    __shared__ float most_s[CW][kTileThreads], sums_s[CW][kTileThreads];
+    __shared__ uint64_t full[BUFS];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    for (int64_t id = blockIdx.x; id < a.tiles_r * a.tiles_c; id += gridDim.x) {
+    const int64_t n_tiles = a.tiles_r * a.tiles_c;
+    auto fetch = [&](int64_t id, int b) {
+        const int64_t tr = id / a.tiles_c, tc = id - tr * a.tiles_c;
+        mbar_expect_tx(&full[b], BYTES);
+        tma_load_2d(tiles + b * BYTES, &map, (int)(tc * kTile), (int)(tr * kTile), &full[b]);
+    };
+    if constexpr (LOAD == kTileTma) {
+        if (t == 0) {
+            for (int b = 0; b < BUFS; ++b) mbar_init(&full[b], 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            for (int b = 0; b < BUFS; ++b)
+                if (blockIdx.x + (int64_t)b * gridDim.x < n_tiles) fetch(blockIdx.x + (int64_t)b * gridDim.x, b);
+        }
+        __syncthreads();
+    }
+    int buf = 0;
+    uint32_t parity = 0;
+    for (int64_t id = blockIdx.x; id < n_tiles; id += gridDim.x) {
         const int64_t tr = id / a.tiles_c, tc = id - tr * a.tiles_c;
         const int64_t r0 = tr * kTile, c0 = tc * kTile;
         const int nr = (int)min((int64_t)kTile, a.rows - r0), nc = (int)min((int64_t)kTile, a.cols - c0);
-        const T* x = static_cast<const T*>(a.x) + r0 * a.cols + c0;
+        T* sm = reinterpret_cast<T*>(tiles + buf * BYTES);
         float most = 0.f;
-        // ---- in: a warp's 16 rows, 8 in flight
+        bool ok = true;
+        if constexpr (LOAD == kTileTma) {
+            ok = mbar_wait(&full[buf], parity);   // (a wait that runs out: the tile reads as NaN)
+        } else {
+            const T* x = static_cast<const T*>(a.x) + r0 * a.cols + c0;
+#pragma unroll 4
+            for (int r = warp; r < kTile; r += kTileThreads / 32) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            float v[8][4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = warp * 16 + b * 8 + i;
-                if (VEC) {
-                    const int c = 4 * lane;
-                    if (r < nr && c < nc) {   // (columns come in fours)
-                        if constexpr (sizeof(T) == 4) {
-                            const float4 f = __ldg(reinterpret_cast<const float4*>(x + r * a.cols + c));
-                            v[i][0] = f.x;
-                            v[i][1] = f.y;
-                            v[i][2] = f.z;
-                            v[i][3] = f.w;
-                        } else {
-                            const uint2 w = __ldg(reinterpret_cast<const uint2*>(x + r * a.cols + c));
-                            const float2 p = unpack2<T>(w.x), q = unpack2<T>(w.y);
-                            v[i][0] = p.x;
-                            v[i][1] = p.y;
-                            v[i][2] = q.x;
-                            v[i][3] = q.y;
-                        }
-                    } else {
-                        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[i][j] = r < nr && lane + 32 * j < nc ? to_f32(x[r * a.cols + lane + 32 * j]) : 0.f;
-                }
+                for (int j = 0; j < 4; ++j)
+                    sm[r * kTile + lane + 32 * j] = r < nr && lane + 32 * j < nc ? x[r * a.cols + lane + 32 * j] : from_f32<T>(0.f);
             }
+            __syncthreads();
+        }
+        if (!ok) most = __int_as_float(0x7fc00000);
+        // ---- along the columns: a warp's 16 rows, four columns a lane
+        const bool words = a.codes && a.ld % 4 == 0 && ((uintptr_t)a.codes & 3) == 0;
+        auto read4 = [&](int r, float2& p, float2& q) {
+            if constexpr (sizeof(T) == 4) {
+                const float4 f = *reinterpret_cast<const float4*>(sm + r * kTile + 4 * lane);
+                p = make_float2(f.x, f.y);
+                q = make_float2(f.z, f.w);
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(sm + r * kTile + 4 * lane);
+                p = unpack2<T>(w.x);
+                q = unpack2<T>(w.y);
+            }
+        };
+        auto write4 = [&](int r, float2 p, float2 q, float inv) {
+            const float2 i2 = make_float2(inv, inv);
+            uint32_t w = q_codes4(__fmul2_rn(p, i2), __fmul2_rn(q, i2), SNK_Q8_E4M3);
+            if (inv == 0.f) w = 0;
+            uint8_t* out = a.codes + (r0 + r) * a.ld + c0 + 4 * lane;
+            if (r >= nr) return;
+            if (words && 4 * lane + 4 <= nc) {
+                *reinterpret_cast<uint32_t*>(out) = w;
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = warp * 16 + b * 8 + i;
-                float m = max_abs(max_abs(0.f, v[i][0], v[i][1]), v[i][2], v[i][3]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sm[r * kPitch<T> + (VEC ? 4 * lane + j : lane + 32 * j)] = from_f32<T>(v[i][j]);
+                for (int j = 0; j < 4; ++j)
+                    if (4 * lane + j < nc) out[j] = (uint8_t)(w >> (8 * j));
+            }
+        };
+        if (BLOCKS || a.codes) {
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int r = warp * 16 + i;
+                float2 p, q;
+                read4(r, p, q);
+                float m = max_abs(max_abs(0.f, p.x, p.y), q.x, q.y);
                 if constexpr (BLOCKS) {
                     most = max_nan(most, m);
-                } else if (a.codes) {
-                    m = warp_amax(m);
-                    const QScale q = q_scale(m, SNK_Q8_E4M3);
-                    if (r < nr) {
-                        uint8_t* out = a.codes + (r0 + r) * a.ld + c0;
-                        uint32_t w = q_codes4(make_float2(__fmul_rn(v[i][0], q.inv), __fmul_rn(v[i][1], q.inv)),
-                                              make_float2(__fmul_rn(v[i][2], q.inv), __fmul_rn(v[i][3], q.inv)), SNK_Q8_E4M3);
-                        if (q.inv == 0.f) w = 0;
-                        if (VEC) {
-                            if (4 * lane < nc) *reinterpret_cast<uint32_t*>(out + 4 * lane) = w;
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (lane + 32 * j < nc) out[lane + 32 * j] = (uint8_t)(w >> (8 * j));
-                        }
-                        if (lane == 0) a.scales[(r0 + r) * a.tiles_c + tc] = q.scale;
-                    }
+                } else {
+                    m = warp_amax(max_nan(m, most));
+                    const QScale s = q_scale(m, SNK_Q8_E4M3);
+                    write4(r, p, q, s.inv);
+                    if (lane == 0 && r < nr) a.scales[(r0 + r) * a.tiles_c + tc] = s.scale;
                 }
             }
         }
         QScale block{0.f, 0.f};
         if constexpr (BLOCKS) {
             most = warp_amax(most);
-            if (lane == 0) most_s[warp] = most;
+            if (lane == 0) most_s[0][warp] = most;
             __syncthreads();
-            most = most_s[lane & 7];
+            most = most_s[0][lane & 7];
             most = warp_amax(most);
             block = q_scale(most, SNK_Q8_E4M3);
             if (t == 0) {
@@ -120,80 +147,104 @@ __global__ void __launch_bounds__(kTileThreads) k_q8_tile(const TileArgs a) {
             if (a.codes) {
 #pragma unroll 4
                 for (int i = 0; i < 16; ++i) {
-                    const int r = warp * 16 + i;
-                    float v[4];
+                    float2 p, q;
+                    read4(warp * 16 + i, p, q);
+                    write4(warp * 16 + i, p, q, block.inv);
+                }
+            }
+        }
+        // ---- along the rows
+        if (a.codes_t || a.part) {
+            const int word = t % WORDS, h = t / WORDS;   // rows h RT .. + RT - 1
+            const uint32_t* col = reinterpret_cast<const uint32_t*>(sm) + h * RT * WORDS + word;
+            uint32_t raw[RT];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[j] = __fmul_rn(to_f32(sm[r * kPitch<T> + (VEC ? 4 * lane + j : lane + 32 * j)]), block.inv);
-                    uint32_t w = q_codes4(make_float2(v[0], v[1]), make_float2(v[2], v[3]), SNK_Q8_E4M3);
-                    if (block.inv == 0.f) w = 0;
-                    if (r < nr) {
-                        uint8_t* out = a.codes + (r0 + r) * a.ld + c0;
-                        if (VEC) {
-                            if (4 * lane < nc) *reinterpret_cast<uint32_t*>(out + 4 * lane) = w;
+            for (int i = 0; i < RT; ++i) raw[i] = col[i * WORDS];
+            auto value = [&](int i, int k) {
+                if constexpr (CW == 1) return __uint_as_float(raw[i]);
+                else return k ? unpack2<T>(raw[i]).y : unpack2<T>(raw[i]).x;
+            };
+            QScale q[CW];
+#pragma unroll
+            for (int k = 0; k < CW; ++k) q[k] = block;
+            if constexpr (!BLOCKS) {
+#pragma unroll
+                for (int k = 0; k < CW; ++k) {
+                    float m = ok ? 0.f : __int_as_float(0x7fc00000), s = 0.f;
+#pragma unroll
+                    for (int i = 0; i < RT; i += 2) {
+                        m = max_abs(m, value(i, k), value(i + 1, k));
+                        s += value(i, k) + value(i + 1, k);
+                    }
+                    most_s[k][t] = m;
+                    sums_s[k][t] = s;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < CW; ++k) {
+                    float m = 0.f, s = 0.f;
+#pragma unroll
+                    for (int u = word; u < kTileThreads; u += WORDS) {
+                        m = max_nan(m, most_s[k][u]);
+                        s += sums_s[k][u];
+                    }
+                    q[k] = q_scale(m, SNK_Q8_E4M3);
+                    const int c = word * CW + k;
+                    if (h == 0 && c < nc) {
+                        if (a.codes_t) a.scales_t[(c0 + c) * a.tiles_r + tr] = q[k].scale;
+                        if (a.part) a.part[tr * a.cols + c0 + c] = s;
+                    }
+                }
+            }
+            if (a.codes_t) {
+#pragma unroll
+                for (int k = 0; k < CW; ++k) {
+                    unsigned char* out = turned + (word * CW + k) * kTile;
+#pragma unroll
+                    for (int b = 0; b < RT; b += 16) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = b + 4 * i;
+                            w[i] = q_codes4(make_float2(__fmul_rn(value(r, k), q[k].inv), __fmul_rn(value(r + 1, k), q[k].inv)),
+                                            make_float2(__fmul_rn(value(r + 2, k), q[k].inv), __fmul_rn(value(r + 3, k), q[k].inv)),
+                                            SNK_Q8_E4M3);
+                            if (q[k].inv == 0.f) w[i] = 0;
+                        }
+                        *reinterpret_cast<uint4*>(out + 16 * (((h * RT + b) / 16) ^ (word & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                __syncthreads();
+                uint8_t* to = a.codes_t + c0 * a.ld_t + r0;
+                if (a.ld_t % 16 == 0 && ((uintptr_t)a.codes_t & 15) == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = (t + kTileThreads * i) >> 3, chunk = t & 7;
+                        const unsigned char* from = turned + c * kTile + 16 * (chunk ^ ((c / CW) & 7));
+                        if (c >= nc || 16 * chunk >= nr) continue;
+                        if (16 * chunk + 16 <= nr) {
+                            *reinterpret_cast<uint4*>(to + c * a.ld_t + 16 * chunk) = *reinterpret_cast<const uint4*>(from);
                         } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (lane + 32 * j < nc) out[lane + 32 * j] = (uint8_t)(w >> (8 * j));
+                            for (int k = 0; k < nr - 16 * chunk; ++k) to[c * a.ld_t + 16 * chunk + k] = from[k];
                         }
                     }
-                }
-            }
-        } else {
-            __syncthreads();
-        }
-        // ---- out along the rows: a thread has half of a column
-        if (a.codes_t || a.part) {
-            const int c = t & (kTile - 1), h = t >> 7;
-            const T* col = sm + (h * 64) * kPitch<T> + c;
-            QScale q = block;
-            if (!BLOCKS || a.part) {
-                float m = 0.f, s = 0.f;
-#pragma unroll 8
-                for (int i = 0; i < 64; i += 2) {
-                    const float u = to_f32(col[i * kPitch<T>]), v = to_f32(col[(i + 1) * kPitch<T>]);
-                    m = max_abs(m, u, v);
-                    s += u + v;
-                }
-                if constexpr (!BLOCKS) {
-                    most_s[t] = m;
-                    if (h) sums_s[c] = s;
-                    __syncthreads();
-                    q = q_scale(max_nan(m, most_s[t ^ kTile]), SNK_Q8_E4M3);
-                    if (!h && c < nc) {
-                        if (a.codes_t) a.scales_t[(c0 + c) * a.tiles_r + tr] = q.scale;
-                        if (a.part) a.part[tr * a.cols + c0 + c] = s + sums_s[c];
-                    }
-                }
-            }
-            if (a.codes_t && c < nc) {
-                uint8_t* out = a.codes_t + (c0 + c) * a.ld_t + r0 + h * 64;
-                const int left = nr - h * 64;
+                } else {
+                    for (int c = warp; c < nc; c += kTileThreads / 32) {
 #pragma unroll
-                for (int b = 0; b < 64; b += 32) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const T* p = col + (b + 4 * k) * kPitch<T>;
-                        w[k] = q_codes4(make_float2(__fmul_rn(to_f32(p[0]), q.inv), __fmul_rn(to_f32(p[kPitch<T>]), q.inv)),
-                                        make_float2(__fmul_rn(to_f32(p[2 * kPitch<T>]), q.inv),
-                                                    __fmul_rn(to_f32(p[3 * kPitch<T>]), q.inv)),
-                                        SNK_Q8_E4M3);
-                        if (q.inv == 0.f) w[k] = 0;
-                    }
-                    if (b + 32 <= left && ((uintptr_t)(out + b) & 31) == 0) {
-                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + b), "r"(w[0]), "r"(w[1]),
-                                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                                     : "memory");
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (b + k < left) out[b + k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+                        for (int r = lane; r < kTile; r += 32)
+                            if (r < nr) to[c * a.ld_t + r] = turned[c * kTile + 16 * ((r >> 4) ^ ((c / CW) & 7)) + (r & 15)];
                     }
                 }
             }
         }
         __syncthreads();   // the tile and the exchanged maxima are free
+        if constexpr (LOAD == kTileTma) {
+            if (t == 0 && id + (int64_t)BUFS * gridDim.x < n_tiles) fetch(id + (int64_t)BUFS * gridDim.x, buf);
+            if (++buf == BUFS) {
+                buf = 0;
+                parity ^= 1;
+            }
+        }
     }
 }
 
@@ -214,23 +265,34 @@ __global__ void __launch_bounds__(256) k_q8_sums(const float* __restrict__ part,
     }
 }
 
-template <typename T, bool BLOCKS, bool VEC>
-int launch_tile(const TileArgs& a, cudaStream_t s) {
-    auto* f = k_q8_tile<T, BLOCKS, VEC>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem<T>) != cudaSuccess) {
+template <typename T, bool BLOCKS, TileLoad LOAD>
+int launch_tile(const CUtensorMap& map, const TileArgs& a, int num_sms, cudaStream_t s) {
+    auto* f = k_q8_tile<T, BLOCKS, LOAD>;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kTileSmem<T, LOAD>)) != cudaSuccess) {
         cudaGetLastError();
         return SNK_ERR_CUDA;
     }
-    const unsigned blocks = (unsigned)std::min<int64_t>(a.tiles_r * a.tiles_c, 1 << 20);
-    f<<<blocks, kTileThreads, kTileSmem<T>, s>>>(a);
+    const unsigned blocks = (unsigned)std::min<int64_t>(a.tiles_r * a.tiles_c, 2 * num_sms);
+    f<<<blocks, kTileThreads, kTileSmem<T, LOAD>, s>>>(map, a);
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
 }
 template <typename T>
 int launch_tile(const TileArgs& a, bool blocks, cudaStream_t s) {
-    const bool vec = a.cols % 4 == 0 && ((uintptr_t)a.x & (4 * sizeof(T) - 1)) == 0 &&
-                     (!a.codes || (a.ld % 4 == 0 && ((uintptr_t)a.codes & 3) == 0));
-    if (blocks) return vec ? launch_tile<T, true, true>(a, s) : launch_tile<T, true, false>(a, s);
-    return vec ? launch_tile<T, false, true>(a, s) : launch_tile<T, false, false>(a, s);
+    const int n = device_sms();
+    if (n < 1) return SNK_ERR_CUDA;
+    CUtensorMap map = {};
+    if (a.cols * sizeof(T) % 16 || ((uintptr_t)a.x & 15))
+        return blocks ? launch_tile<T, true, kTilePlain>(map, a, n, s) : launch_tile<T, false, kTilePlain>(map, a, n, s);
+    EncodeTiledFn fn = encoder();
+    const CUtensorMapDataType type = sizeof(T) == 4                     ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    cuuint64_t dims[2] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.cols * sizeof(T)};
+    cuuint32_t box[2] = {kTile, kTile}, estr[2] = {1, 1};
+    if (!fn || fn(&map, type, 2, const_cast<void*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return SNK_ERR_CUDA;
+    return blocks ? launch_tile<T, true, kTileTma>(map, a, n, s) : launch_tile<T, false, kTileTma>(map, a, n, s);
 }
 int run_tile(const TileArgs& a, int dtype, bool blocks, cudaStream_t s) {
     switch (dtype) {

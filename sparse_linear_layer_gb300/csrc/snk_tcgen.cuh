@@ -129,4 +129,17 @@ inline EncodeTiledFn encoder() {
     return fn;
 }
 
+// SMs of the current device (0: an error).  Also makes the device's context current to the
+// thread: the encoder needs one, and a thread that has only been given existing memory, such
+// as autograd's, may have none yet.
+inline int device_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
 }  // namespace snk

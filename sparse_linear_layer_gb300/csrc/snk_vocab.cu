@@ -28,7 +28,7 @@ namespace snk {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kGatherRows = 64;     // rows per block of k_vocab_rows
+constexpr int kGatherRows = 16;     // rows per block of k_vocab_rows
 constexpr int kDirectRows = 128;    // up to these the forward reads x itself: one row tile either way
 constexpr float kDzScale = 8192.f;  // 2^13
 
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
         int n = 0;
         uint32_t most = 0;
         for (int i = 0; i < kGatherRows; i += 32) {
-            const int64_t r = r0 + i + lane;
+            const int64_t r = i + lane < kGatherRows ? r0 + i + lane : a.rows;
             const int64_t tg = r < a.rows ? a.target[r] : a.ignore;
             const bool in = r < a.rows && tg != a.ignore;
             const uint32_t mask = __ballot_sync(0xffffffffu, in);
@@ -307,17 +307,16 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
     const int mine = mine_s;
     T* xc = static_cast<T*>(a.xc);
     const T* x = static_cast<const T*>(a.x);
-    if (a.ld == a.cols) {   // whole 16-byte chunks
-        const int64_t n16 = a.ld / 8;
-        for (int64_t i = t; i < mine * n16; i += 256) {
-            const int64_t k = i / n16, c = i - k * n16;
-            reinterpret_cast<uint4*>(xc + (before + k) * a.ld)[c] =
-                __ldg(reinterpret_cast<const uint4*>(x + (r0 + list[k]) * a.cols) + c);
-        }
-    } else {
-        for (int64_t i = t; i < mine * a.ld; i += 256) {
-            const int64_t k = i / a.ld, c = i - k * a.ld;
-            xc[(before + k) * a.ld + c] = c < a.cols ? x[(r0 + list[k]) * a.cols + c] : from_f32<T>(0.f);
+    for (int k = warp; k < mine; k += 8) {
+        const T* from = x + (r0 + list[k]) * a.cols;
+        T* to = xc + (before + k) * a.ld;
+        if (a.ld == a.cols) {   // whole 16-byte chunks
+            const int64_t n16 = a.ld / 8;
+#pragma unroll 4
+            for (int64_t c = lane; c < n16; c += 32) reinterpret_cast<uint4*>(to)[c] = __ldg(reinterpret_cast<const uint4*>(from) + c);
+        } else {
+#pragma unroll 4
+            for (int64_t c = lane; c < a.ld; c += 32) to[c] = c < a.cols ? from[c] : from_f32<T>(0.f);
         }
     }
     // zeros from the last row that counts up to the last tile that holds one
@@ -403,17 +402,23 @@ __global__ void __launch_bounds__(256) k_vocab_finish(const FinishArgs a) {
                     const T* x = static_cast<const T*>(a.x) + c * a.ldx;
                     const T* w = static_cast<const T*>(a.w) + tg * a.cols;
                     float d0 = 0.f, d1 = 0.f;
-                    int64_t j = 2 * lane;
-                    if ((a.cols & 1) == 0) {
+                    if ((a.cols & 7) == 0) {   // (rows are whole 16-byte chunks)
+                        F8 sum;
+                        sum.clear();
 #pragma unroll 4
-                        for (; j < a.cols; j += 64) {
-                            const float2 p = unpack2<T>(*reinterpret_cast<const uint32_t*>(x + j));
-                            const float2 q = unpack2<T>(*reinterpret_cast<const uint32_t*>(w + j));
-                            d0 = fmaf(p.x, q.x, d0);
-                            d1 = fmaf(p.y, q.y, d1);
+                        for (int64_t j = 8 * lane; j < a.cols; j += 256) {
+                            F8 p, q;
+                            load8(x + j, p);
+                            load8(w + j, q);
+                            sum.fma(p, q);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            d0 += sum.p[i].x;
+                            d1 += sum.p[i].y;
                         }
                     } else {
-                        for (j = lane; j < a.cols; j += 32) d0 = fmaf(to_f32(x[j]), to_f32(w[j]), d0);
+                        for (int64_t j = lane; j < a.cols; j += 32) d0 = fmaf(to_f32(x[j]), to_f32(w[j]), d0);
                     }
                     d0 += d1;
 #pragma unroll
@@ -472,27 +477,44 @@ __global__ void __launch_bounds__(256) k_vocab_finish(const FinishArgs a) {
     if (t == 0) *a.out = (float)(a.reduction == 2 ? ds[0] / (double)counts[0] : ds[0]);
 }
 
-// dx of every row of x from the slabs; ignored rows zero.
-template <typename T>
+// dx of every row of x from the slabs; ignored rows zero. WARPS: how many warps share the slabs of an
+// element (many slabs of few rows: one thread's chain of loads would be the call's longest part).
+template <typename T, int WARPS>
 __global__ void __launch_bounds__(256) k_vocab_dx(const float* __restrict__ slab, int splits, int64_t stride, int64_t ld,
                                                   const int32_t* __restrict__ at, const uint32_t* most, int64_t rows, int64_t cols,
                                                   T* __restrict__ dx) {
+    __shared__ F8 part[WARPS > 1 ? WARPS : 1][WARPS > 1 ? 32 : 1];
     const float scale = 1.f / (GradEpilogue<T>::grad_factor(*most) * kDzScale);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = WARPS > 1 ? warp : 0;
+    constexpr int E = WARPS > 1 ? 32 : 256;   // elements (of 8 columns) of a block
     const int64_t n8 = ld / 8, n = rows * n8;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / n8, c = (i - r * n8) * 8;
-        const int k = __ldg(at + r);
+    for (int64_t i0 = (int64_t)blockIdx.x * E; i0 < n; i0 += (int64_t)gridDim.x * E) {
+        const int64_t i = i0 + (WARPS > 1 ? lane : (int)threadIdx.x);
+        const bool in = i < n;
+        const int64_t r = in ? i / n8 : 0, c = in ? (i - r * n8) * 8 : 0;
+        const int k = in ? __ldg(at + r) : -1;
         F8 f;
         f.clear();
         if (k >= 0) {
             const float* p = slab + (int64_t)k * ld + c;
-            for (int s = 0; s < splits; ++s) {
+#pragma unroll 4
+            for (int s = first; s < splits; s += WARPS) {
                 F8 o;
                 load8(p + s * stride, o);
                 f.add(o);
             }
-            f.mul(scale);
         }
+        if constexpr (WARPS > 1) {
+            part[warp][lane] = f;
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < WARPS; ++w) f.add(part[w][lane]);
+            }
+            __syncthreads();
+        }
+        if (!in || first > 0) continue;
+        f.mul(scale);
         T* out = dx + r * cols + c;
         if (ld == cols) {
             store8(out, f);
@@ -507,26 +529,36 @@ __global__ void __launch_bounds__(256) k_vocab_dx(const float* __restrict__ slab
 // ---- host -----------------------------------------------------------------------------
 
 int64_t up(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
-int sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
-}
 int launched() { return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA; }
 
-// Tile width of a product over `n` columns with few row tiles: the width whose last wave
-// of tiles is fullest.
-int narrow_bn(int64_t n, int units) {
-    int best = 256;
-    int64_t cost = INT64_MAX;
-    for (int bn = 256; bn >= 64; bn -= 32) {
-        const int64_t waves = ceil_div(ceil_div(n, bn), units), c = waves * (bn + 16);
-        if (c < cost) {
-            cost = c;
-            best = bn;
+// A product's tile and ranges of K: the form whose waves take least by this account.  A stage
+// takes its MMAs (us as measured, fewer columns than 128 at the same cost) or, where all SMs are
+// busy, the bytes that they all fetch for it from the L2 (12.5 TB/s as measured); a tile has a
+// microsecond beside its stages; a range's sums are written and read.
+struct Form {
+    int cg = 1, bn = 256, splits = 1;
+};
+// m x n over n_k stages; rows: of A that a tile loads; width: multiples of it (per CTA of a pair)
+// are possible as tile widths; most: ranges of K at most; sums: bytes of one range's sums.
+Form pick_form(int64_t m, int64_t n, int64_t n_k, int rows, int width, int most, double sums, int num_sms) {
+    Form best;
+    double least = 1e30;
+    for (int cg = 2; cg >= 1; --cg) {
+        if (cg == 2 && m <= 128) continue;
+        const int step = std::max(32, width * cg);
+        for (int bn = 256; bn >= std::max(64, step); bn -= step) {
+            const int64_t tiles = ceil_div(m, 128 * cg) * ceil_div(n, bn), units = num_sms / cg;
+            for (int sp = 1; sp <= most && (sp == 1 || n_k / sp >= 8); ++sp) {
+                const double busy = (double)std::min(units, tiles * sp) * cg;
+                const double stage = std::max(cg == 2 ? 0.34 : std::max(0.18, 0.36 * bn / 256), (rows + bn / cg) * 128 * busy / 12.5e6);
+                const double t = (double)ceil_div(tiles * sp, units) * ((double)ceil_div(n_k, sp) * stage + 1.0) + sp * sums / 3.3e6;
+                if (t < 0.99 * least) {
+                    least = t;
+                    best.cg = cg;
+                    best.bn = bn;
+                    best.splits = sp;
+                }
+            }
         }
     }
     return best;
@@ -549,11 +581,13 @@ struct Shape {
     int64_t rows, cols, vocab, ld, padded;   // ld: columns in whole 16-byte chunks
     Shape(int64_t r, int64_t c, int64_t v) : rows(r), cols(c), vocab(v), ld(up(c, 8)), padded(up(r, 256)) {}
     bool pads() const { return ld != cols; }
+    int tile_rows() const { return (int)std::min<int64_t>(kDenseM, up(rows, 8)); }   // that a row tile loads
 };
 
 struct ForwardPlan {
     bool gather;
-    int cg, bn, n_nt, per_block, blocks;
+    Form form;
+    int n_nt, per_block, blocks;
     void *xc, *wc;
     int32_t *index, *at, *count, *arrived;
     int64_t* tc;
@@ -562,11 +596,10 @@ struct ForwardPlan {
     int64_t bytes;
     ForwardPlan(const Shape& h, int num_sms, void* scratch) {
         gather = h.rows > kDirectRows || h.pads();
-        cg = h.rows > kDirectRows ? 2 : 1;
-        bn = cg == 2 ? 256 : narrow_bn(h.vocab, num_sms);
-        n_nt = (int)ceil_div(h.vocab, bn);
+        form = pick_form(h.rows, h.vocab, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms);
+        n_nt = (int)ceil_div(h.vocab, form.bn);
         per_block = 1;
-        while (per_block < 32 && ceil_div(h.rows, per_block) > num_sms) per_block *= 2;
+        while (per_block < 8 && ceil_div(h.rows, per_block) > num_sms) per_block *= 2;
         blocks = (int)ceil_div(h.rows, per_block);
         Scratch s(scratch);
         count = s.take<int32_t>(2);
@@ -584,10 +617,10 @@ struct ForwardPlan {
 };
 
 // Columns of the vocabulary whose dz is held at a time.
-constexpr int64_t kPieceBytes = 256ll << 20;
+constexpr int64_t kPieceBytes = 512ll << 20;
 
 struct BackwardPlan {
-    int cg, bn_z, bn_x, bn_w, splits;
+    Form z, x, w;
     int64_t piece;
     void *xc, *wc, *dz;
     int32_t *index, *at, *count;
@@ -596,26 +629,12 @@ struct BackwardPlan {
     float *lse2, *g, *slab;
     int64_t bytes;
     BackwardPlan(const Shape& h, int num_sms, void* scratch) {
-        cg = h.rows > kDirectRows ? 2 : 1;
         const int64_t whole = up(h.vocab, 256);
         piece = std::max<int64_t>(256, std::min(whole, kPieceBytes / (2 * h.padded) / 256 * 256));
         piece = up(ceil_div(whole, ceil_div(whole, piece)), 256);   // equal ones
-        bn_z = cg == 2 ? 256 : narrow_bn(piece, num_sms);
-        const int step = 64 * cg;
-        bn_x = bn_w = (int)std::min<int64_t>(256, up(h.ld, step));
-        const int units = num_sms / cg;
-        const int64_t tiles = ceil_div(h.rows, 128 * cg) * ceil_div(h.ld, bn_x);
-        // ranges of K for dx: the number, up to one per 512 columns, whose waves are fullest; each costs a slab of dx
-        splits = 1;
-        double best = 0;
-        const int most_splits = (int)std::max<int64_t>(1, std::min<int64_t>(piece / 512, std::max<int64_t>(4, 2 * units / tiles)));
-        for (int n = 1; n <= most_splits; ++n) {
-            const double full = (double)(tiles * n) / (double)(ceil_div(tiles * n, units) * units) - 0.01 * n * (tiles >= units);
-            if (full > best + 0.02) {
-                best = full;
-                splits = n;
-            }
-        }
+        z = pick_form(h.rows, piece, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms);
+        x = pick_form(h.rows, h.ld, piece / 64, h.tile_rows(), 64, 64, 8.0 * h.rows * h.ld, num_sms);
+        w = pick_form(piece, h.ld, ceil_div(h.rows, 64), kDenseM, 64, 1, 0, num_sms);
         Scratch s(scratch);
         count = s.take<int32_t>(2);
         most = reinterpret_cast<uint32_t*>(count + 1);
@@ -627,10 +646,30 @@ struct BackwardPlan {
         xc = s.take<uint16_t>(h.padded * h.ld);
         wc = s.take<uint16_t>(h.pads() ? h.vocab * h.ld : 0);
         dz = s.take<uint16_t>(h.padded * piece);
-        slab = s.take<float>((int64_t)splits * h.padded * h.ld);
+        slab = s.take<float>((int64_t)x.splits * h.padded * h.ld);
         bytes = s.used;
     }
 };
+
+DenseArgs dense_args(const Form& f, bool bf16, bool a_mn, bool b_mn, int64_t m, int64_t n, int64_t k, int a_rows = kDenseM) {
+    DenseArgs a = {};
+    a.n_mt = (int)ceil_div(m, 128 * f.cg);
+    a.n_nt = (int)ceil_div(n, f.bn);
+    a.bn = f.bn;
+    a.a_rows = a_rows;
+    a.stages = dense_stages(f.cg, a_rows, f.bn);
+    a.splits = f.splits;
+    a.K = k;
+    a.idesc = dense_idesc(bf16, a_mn, b_mn, 128 * f.cg, f.bn);
+    a.group = 16 / f.cg;
+    return a;
+}
+template <bool A_MN, bool B_MN, class Epilogue>
+int launch(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& e, int num_sms,
+           cudaStream_t s) {
+    return f.cg == 2 ? dense_launch<2, A_MN, B_MN, Epilogue>(ma, mb, a, e, num_sms, s)
+                     : dense_launch<1, A_MN, B_MN, Epilogue>(ma, mb, a, e, num_sms, s);
+}
 
 template <typename T>
 int pad_weight(const Shape& h, const void* w, void* wc, int num_sms, cudaStream_t s) {
@@ -672,23 +711,16 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
     }
     CUtensorMap ma, mb;
     const void* xt = p.gather ? p.xc : x;
-    if (!dense_map(&ma, xt, bf, h.ld, p.gather ? h.padded : h.rows, h.ld, kDenseM) ||
-        !dense_map(&mb, wt, bf, h.ld, h.vocab, h.ld, p.bn / p.cg))
+    const int a_rows = h.tile_rows();
+    if (!dense_map(&ma, xt, bf, h.ld, p.gather ? h.padded : h.rows, h.ld, a_rows) ||
+        !dense_map(&mb, wt, bf, h.ld, h.vocab, h.ld, p.form.bn / p.form.cg))
         return SNK_ERR_CUDA;
-    DenseArgs a = {};
-    a.n_mt = (int)ceil_div(h.rows, 128 * p.cg);
-    a.n_nt = p.n_nt;
-    a.bn = p.bn;
-    a.splits = 1;
-    a.K = h.ld;
-    a.idesc = dense_idesc(bf, false, false, 128 * p.cg, p.bn);
+    DenseArgs a = dense_args(p.form, bf, false, false, h.rows, h.vocab, h.ld, a_rows);
     a.rows = p.gather ? p.count : nullptr;
-    a.group = 16 / p.cg;
     a.zero = p.arrived;
-    const LseEpilogue::Args ea{p.part, h.padded, h.vocab};
-    const int st = p.cg == 2 ? dense_launch<2, false, false, LseEpilogue>(ma, mb, a, ea, num_sms, s)
-                             : dense_launch<1, false, false, LseEpilogue>(ma, mb, a, ea, num_sms, s);
-    if (st != SNK_OK) return st;
+    if (int st = launch<false, false, LseEpilogue>(p.form, ma, mb, a, LseEpilogue::Args{p.part, h.padded, h.vocab}, num_sms, s);
+        st != SNK_OK)
+        return st;
     FinishArgs f = {};
     f.part = p.part;
     f.ld = h.padded;
@@ -714,59 +746,50 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
     return launched();
 }
 
-template <int CG, typename T>
+template <typename T>
 int backward(const Shape& h, const BackwardPlan& p, const void* wt, void* dx, void* dw, int num_sms, cudaStream_t s) {
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-    const int m_tiles = (int)ceil_div(h.rows, 128 * CG);
-    CUtensorMap mx, mx_t, mz, mz_t;
-    if (!dense_map(&mx, p.xc, bf, h.ld, h.padded, h.ld, kDenseM) || !dense_map(&mx_t, p.xc, bf, h.ld, h.padded, h.ld, 64) ||
-        !dense_map(&mz, p.dz, bf, p.piece, h.padded, p.piece, kDenseM) ||
-        !dense_map(&mz_t, p.dz, bf, p.piece, h.padded, p.piece, 64))
+    CUtensorMap mx, mx_t, mz, mz_t;   // _t: read along the rows
+    if (!dense_map(&mx, p.xc, bf, h.ld, h.padded, h.ld, h.tile_rows()) || !dense_map(&mx_t, p.xc, bf, h.ld, h.padded, h.ld, 64))
         return SNK_ERR_CUDA;
     for (int64_t v0 = 0; v0 < h.vocab; v0 += p.piece) {
         const int64_t width = std::min(p.piece, h.vocab - v0);
         const T* wp = static_cast<const T*>(wt) + v0 * h.ld;
         CUtensorMap mw, mw_t;
-        if (!dense_map(&mw, wp, bf, h.ld, width, h.ld, p.bn_z / CG) || !dense_map(&mw_t, wp, bf, h.ld, width, h.ld, 64))
+        // (dz's columns behind the piece's width are not written everywhere: they read as zeros)
+        if (!dense_map(&mw, wp, bf, h.ld, width, h.ld, p.z.bn / p.z.cg) || !dense_map(&mw_t, wp, bf, h.ld, width, h.ld, 64) ||
+            !dense_map(&mz, p.dz, bf, width, h.padded, p.piece, h.tile_rows()) ||
+            !dense_map(&mz_t, p.dz, bf, width, h.padded, p.piece, 64))
             return SNK_ERR_CUDA;
-        DenseArgs a = {};
-        a.splits = 1;
-        // dz of the piece
-        a.n_mt = m_tiles;
-        a.n_nt = (int)ceil_div(width, p.bn_z);
-        a.bn = p.bn_z;
-        a.K = h.ld;
-        a.idesc = dense_idesc(bf, false, false, 128 * CG, p.bn_z);
+        DenseArgs a = dense_args(p.z, bf, false, false, h.rows, width, h.ld, h.tile_rows());   // dz of the piece
         a.rows = p.count;
-        a.group = 16 / CG;
         const typename GradEpilogue<T>::Args eg{static_cast<T*>(p.dz), p.piece, width, v0, p.lse2, p.g, p.tc, p.most};
-        if (int st = dense_launch<CG, false, false, GradEpilogue<T>>(mx, mw, a, eg, num_sms, s); st != SNK_OK) return st;
+        if (int st = launch<false, false, GradEpilogue<T>>(p.z, mx, mw, a, eg, num_sms, s); st != SNK_OK) return st;
         if (dx) {
-            a.n_nt = (int)ceil_div(h.ld, p.bn_x);
-            a.bn = p.bn_x;
-            a.K = width;
-            a.splits = p.splits;
-            a.idesc = dense_idesc(bf, false, true, 128 * CG, p.bn_x);
+            a = dense_args(p.x, bf, false, true, h.rows, h.ld, width, h.tile_rows());
+            a.rows = p.count;
             const SumEpilogue::Args es{p.slab, h.padded, h.ld, v0 > 0};
-            if (int st = dense_launch<CG, false, true, SumEpilogue>(mz, mw_t, a, es, num_sms, s); st != SNK_OK) return st;
+            if (int st = launch<false, true, SumEpilogue>(p.x, mz, mw_t, a, es, num_sms, s); st != SNK_OK) return st;
         }
         if (dw) {
             T* out = static_cast<T*>(dw) + v0 * h.cols;
-            a.n_mt = (int)ceil_div(width, 128 * CG);
-            a.n_nt = (int)ceil_div(h.cols, p.bn_w);
-            a.bn = p.bn_w;
-            a.K = h.rows;
-            a.splits = 1;
+            a = dense_args(p.w, bf, true, true, width, h.cols, h.rows);
+            a.rows = p.count;
             a.rows_k = 1;
-            a.idesc = dense_idesc(bf, true, true, 128 * CG, p.bn_w);
             const int vec = h.pads() ? 1 : (h.cols % 16 == 0 && ((uintptr_t)out & 31) == 0 ? 16 : 8);
             const typename StoreEpilogue<T>::Args eo{out, width, h.cols, p.most, vec};
-            if (int st = dense_launch<CG, true, true, StoreEpilogue<T>>(mz_t, mx_t, a, eo, num_sms, s); st != SNK_OK) return st;
+            if (int st = launch<true, true, StoreEpilogue<T>>(p.w, mz_t, mx_t, a, eo, num_sms, s); st != SNK_OK) return st;
         }
     }
     if (dx) {
-        k_vocab_dx<T><<<(unsigned)std::min<int64_t>(ceil_div(h.rows * (h.ld / 8), 256), 16 * num_sms), 256, 0, s>>>(
-            p.slab, p.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, static_cast<T*>(dx));
+        const int64_t n = h.rows * (h.ld / 8);
+        T* out = static_cast<T*>(dx);
+        if (p.x.splits > 8)
+            k_vocab_dx<T, 8><<<(unsigned)std::min<int64_t>(ceil_div(n, 32), 64 * num_sms), 256, 0, s>>>(
+                p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, out);
+        else
+            k_vocab_dx<T, 1><<<(unsigned)std::min<int64_t>(ceil_div(n, 256), 16 * num_sms), 256, 0, s>>>(
+                p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, out);
         return launched();
     }
     return SNK_OK;
@@ -806,7 +829,7 @@ int backward_rows(const Shape& h, const BackwardPlan& p, const void* x, const vo
         if (int st = pad_weight<T>(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
         wt = p.wc;
     }
-    return p.cg == 2 ? backward<2, T>(h, p, wt, dx, dw, num_sms, s) : backward<1, T>(h, p, wt, dx, dw, num_sms, s);
+    return backward<T>(h, p, wt, dx, dw, num_sms, s);
 }
 
 bool unaligned(const void* p, uintptr_t n) { return p && ((uintptr_t)p & (n - 1)); }
@@ -833,7 +856,7 @@ extern "C" {
 
 int64_t snk_vocab_loss_scratch(int64_t rows, int64_t cols, int64_t vocab, int backward) {
     if (rows < 1 || bad_shape(SNK_BF16, rows, cols, vocab, 0) != SNK_OK) return 0;
-    const int n = sms();
+    const int n = device_sms();
     if (n < 1) return 0;
     const Shape h(rows, cols, vocab);
     return backward ? BackwardPlan(h, n, nullptr).bytes : ForwardPlan(h, n, nullptr).bytes;
@@ -853,7 +876,7 @@ int snk_vocab_loss(const void* x, const void* weight, int dtype, const int64_t* 
         return cudaMemsetAsync(loss, reduction == 1 ? 0 : 0xff, 4, s) == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
     }
     if (!x || !target || !loss || !scratch) return SNK_ERR_ARG;
-    const int n = sms();
+    const int n = device_sms();
     if (n < 1) return SNK_ERR_CUDA;
     const Shape h(rows, cols, vocab);
     return dtype == SNK_F16
@@ -875,7 +898,7 @@ int snk_vocab_loss_backward(const void* x, const void* weight, int dtype, const 
     }
     if (!x || !target || !lse || !dloss || !scratch) return SNK_ERR_ARG;
     if (!dx && !dweight) return SNK_OK;
-    const int n = sms();
+    const int n = device_sms();
     if (n < 1) return SNK_ERR_CUDA;
     const Shape h(rows, cols, vocab);
     const BackwardPlan p(h, n, scratch);

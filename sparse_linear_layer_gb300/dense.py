@@ -52,7 +52,10 @@ def linear_cross_entropy(x, weight, target, ignore: int = -100, reduction: str =
     r = _REDUCTIONS.get(reduction)
     if r is None:
         raise ValueError(f"reduction is one of {tuple(_REDUCTIONS)}: got {reduction!r}")
-    return _LinearCrossEntropyFn.apply(x.contiguous(), weight.contiguous(), target.contiguous(), ignore, r)
+    x, weight, target = x.contiguous(), weight.contiguous(), target.contiguous()
+    if not (torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad)):
+        return binding.ops().vocab_loss(x, weight, target, ignore, r, None)[0]
+    return _LinearCrossEntropyFn.apply(x, weight, target, ignore, r)
 
 
 class _LinearQ8Fn(torch.autograd.Function):

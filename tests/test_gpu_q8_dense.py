@@ -12,7 +12,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from sparse_linear_layer_gb300 import dense, q8  # noqa: E402
+from sparse_linear_layer_gb300 import binding, dense, q8  # noqa: E402
 from tests import dense_ref  # noqa: E402
 from tests.gpu_util import need_gpu  # noqa: E402
 
@@ -257,6 +257,32 @@ def test_captured_linear_step():
     got = [o.detach().clone() for o in outs]
     for a, b in zip(got, step()):
         assert torch.equal(a, b.detach())
+
+
+def test_calls_from_threads():
+    """Several threads at once, on streams of their own, each call the first CUDA work of its thread."""
+    import threading
+    x, w, wb = matrix(300, 512), matrix(400, 512, seed=1), matrix(400, 512, seed=1).bfloat16()
+    xb, t = x.bfloat16(), torch.arange(300, device="cuda")
+    x8, w8 = q8.pack(x, "e4m3", 128), q8.pack_blocks(w)
+    calls = [lambda s: q8.matmul(x8, w8, stream=s), lambda s: q8.pack_both(x, stream=s)[1].codes.view(torch.uint8),
+             lambda s: q8.pack_blocks(w, stream=s).codes.view(torch.uint8),
+             lambda s: binding.ops().vocab_loss(xb, wb, t, -100, 0, s)[0]] * 2
+    want = [f(None) for f in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [None] * len(calls)
+
+    def work(i):
+        got[i] = calls[i](streams[i])
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
 
 
 def test_refusals():
