@@ -34,13 +34,14 @@ struct Q8DenseArgs {
     int64_t M, N;
     int n_g;               // groups along K
     int n_mt, n_nt, splits, group;
+    int a_rows, stages;
     uint32_t idesc;
     const float* sa;       // [M, n_g]
     const float* sb;       // [N, n_g] or [ceil(N / 128), n_g]
     const float* bias;     // [N] or null
     void* y;               // [M, N]
     int dtype;
-    int vec;               // rows of y (slab) are aligned to 16 bytes
+    int vec;               // rows of y (slab) are aligned to 16 bytes: TMA writes them, by map_y
     float* slab;           // splits > 1: [splits][M, N] sums without bias
 };
 
@@ -63,29 +64,58 @@ __device__ __forceinline__ void q8_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 // stages, into a ring of their own: an epilogue warp reads those of a group after the
 // stage of that group may have been filled again, but never as late as the ring is long (it
 // frees an accumulator, of which there are up to 4, before it reads the last of them, and TMA
-// is up to 6 stages ahead of the MMAs).
+// is up to 8 stages ahead of the MMAs).
 constexpr int kScaleSlots = 16;
 
-template <int CG, int BN>
-constexpr int kQ8StageBytes = (kDenseM + BN / CG) * 128;
-template <int CG, int BN>
-constexpr int kQ8Stages = std::min(6, 160 * 1024 / kQ8StageBytes<CG, BN>);
-template <int CG, int BN, bool ROWS>
-constexpr int kQ8Smem = kQ8Stages<CG, BN> * kQ8StageBytes<CG, BN> + kDenseEpilogueWarps * kTurnBytes +
-                        (ROWS ? kScaleSlots * (kDenseM + BN) * 4 : 0) + 1024;
+// A lane's row of a box, 128 bytes with the 128-byte swizzle, and the box's way out.
+template <typename T>
+__device__ __forceinline__ void put_box(unsigned char* box, int lane, const float (&v)[Turn<T>::kCols]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(v[4 * i + k]);
+            else w[k] = pack2<T>(make_float2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]));
+        }
+        *reinterpret_cast<uint4*>(box + lane * 128 + 16 * (i ^ (lane & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void store_box(const void* box, const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(smem_u32(box))
+                 : "memory");
+}
+
+// What an epilogue warp's outputs go through: two boxes of 32 rows by 128 bytes.
+constexpr int kOutBytes = 2 * 4096;
+static_assert(kTurnBytes <= kOutBytes, "the other way out uses the same memory");
+constexpr int kQ8Smem = 227 * 1024 - 4096;   // (beside the static part)
+// Stages: what fits beside the outputs and the scales' ring, 4 for a pair (5 were slower: each of
+// the two issuing threads keeps to its own half of an even number).  a_rows as in dense_stages.
+constexpr int kQ8Stages = 8;
+inline int q8_stages(int cg, int bn, int a_rows, bool by_rows) {
+    const int room = kQ8Smem - 1024 - kDenseEpilogueWarps * kOutBytes - (by_rows ? kScaleSlots * (kDenseM + bn) * 4 : 0) -
+                     (kDenseM - a_rows) * 128;
+    return cg == 2 ? 4 : std::min(kQ8Stages, room / ((a_rows + bn) * 128));
+}
 
 template <int CG, int BN, bool ROWS>
 __global__ void __launch_bounds__(kQ8Threads, 1)
     k_q8_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-               const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb, const Q8DenseArgs a) {
-    constexpr int S = kQ8Stages<CG, BN>, kStage = kQ8StageBytes<CG, BN>;
+               const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
+               const __grid_constant__ CUtensorMap map_y, const Q8DenseArgs a) {
+    constexpr int S = kQ8Stages;
     constexpr int HC = BN / 2;    // columns of an epilogue warp
     constexpr int HB = BN / CG;   // rows of B that a CTA loads
     constexpr int NB = BN == 256 ? 2 : 4;   // accumulators
     extern __shared__ __align__(1024) unsigned char q8_raw[];
     unsigned char* sm = q8_raw + ((1024 - (smem_u32(q8_raw) & 1023)) & 1023);
-    unsigned char* turn = sm + S * kStage;                                              // of each epilogue warp
-    float* scales = reinterpret_cast<float*>(turn + kDenseEpilogueWarps * kTurnBytes);   // ROWS: [kScaleSlots][kDenseM + BN]
+    // outputs of each epilogue warp; ROWS: scales [kScaleSlots][kDenseM + BN]; stages
+    unsigned char* turn = sm;
+    float* scales = reinterpret_cast<float*>(turn + kDenseEpilogueWarps * kOutBytes);
+    unsigned char* stages = turn + kDenseEpilogueWarps * kOutBytes + (ROWS ? kScaleSlots * (kDenseM + BN) * 4 : 0);
+    const int a_bytes = a.a_rows * 128, stage = a_bytes + HB * 128;
     __shared__ uint64_t full[S], empty[S], accf[NB], acce[NB], fin[2];
     __shared__ uint32_t tmem_base;
 
@@ -117,7 +147,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         fewer_registers<kQ8RoleRegs>();
         if (warp == 0 && lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
-            Stages r(S);
+            Stages r(a.stages);
             uint32_t w = 0;   // groups loaded
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
@@ -129,9 +159,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                         ok = false;
                         break;
                     }
-                    unsigned char* sa = sm + s * kStage;
-                    unsigned char* sb = sa + kDenseM * 128;
-                    if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)((kDenseM + HB) * 128 + (ROWS ? (kDenseM + BN) * 4 : 0)) * CG);
+                    unsigned char* sa = stages + s * stage;
+                    unsigned char* sb = sa + a_bytes;
+                    if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(stage + (ROWS ? (kDenseM + BN) * 4 : 0)) * CG);
                     const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : first_cta(&full[s]);
                     dense_load<CG>(sa, &map_a, g * 128, m0, bar);
                     dense_load<CG>(sb, &map_b, g * 128, n0, bar);
@@ -152,7 +182,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
             const uint32_t mine = warp - 1;
             bool ok = true;
-            Stages r(S);
+            Stages r(a.stages);
             uint32_t w = 0;   // groups done
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
@@ -165,7 +195,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(sm + s * kStage), sb = sa + kDenseM * 128;
+                    const uint32_t sa = smem_u32(stages + s * stage), sb = sa + a_bytes;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         q8_mma<CG>(tmem + ab * BN, desc_sw128(sa + kk * 32), desc_sw128(sb + kk * 32), a.idesc, kk > 0 ? 1u : 0u);
@@ -249,7 +279,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             }
             const int64_t row0 = row - lane;
             const int rows = (int)max((int64_t)0, min((int64_t)32, a.M - row0)), cols = (int)min((int64_t)HC, a.N - col);
-            unsigned char* buf = turn + (warp - 4) * kTurnBytes;
+            unsigned char* buf = turn + (warp - 4) * kOutBytes;
+            if (a.vec && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the last tile's boxes have left
+            __syncwarp();
             auto store = [&](auto* y, const float* bias) {
                 using T = typename std::remove_pointer<decltype(y)>::type;
                 constexpr int E = Turn<T>::kCols;
@@ -274,8 +306,24 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                             for (int j = 0; j < E; ++j)
                                 if (c + j < cols) v[j] += __ldg(bias + col + c + j);
                         }
-                        Turn<T>::put(buf, lane, v);
-                        Turn<T>::flush(buf, lane, y + c, a.N, rows, cols - c, a.vec);
+                        if (E <= HC && a.vec) {
+                            // the writes leave while the next tile's groups are added
+                            unsigned char* box = buf + (c / E & 1) * 4096;
+                            if (c >= 2 * E) {
+                                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                                __syncwarp();
+                            }
+                            put_box<T>(box, lane, v);
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (rows > 0) store_box(box, &map_y, (int)(col + c), (int)row0, it.split);
+                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                            }
+                        } else {
+                            Turn<T>::put(buf, lane, v);
+                            Turn<T>::flush(buf, lane, y + c, a.N, rows, cols - c, a.vec);
+                        }
                     }
                 }
             };
@@ -284,6 +332,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             else if (a.dtype == SNK_F16) store(static_cast<__half*>(a.y), a.bias);
             else store(static_cast<__nv_bfloat16*>(a.y), a.bias);
         }
+        if (a.vec && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
     tc_fence_before();
@@ -330,7 +379,8 @@ __global__ void __launch_bounds__(256) k_q8_join(const float* __restrict__ slab,
 
 // ---- few rows ---------------------------------------------------------------------
 // Up to 16 rows of A: the call reads B's codes once, N K bytes, and little else, so it is
-// bound by memory and, for small layers, by latency.  A warp takes 16 rows of B and some
+// bound by memory and, for small layers, by latency (one row, 2304 x 768: 1.8 us; 50257 x 768:
+// 9 us, 4.3 TB/s).  A warp takes 16 rows of B and some
 // of the groups; the block's warps share the groups and are added through shared memory.
 // The products are mma.sync m16n8k32 (B's rows as its 16, A's as its 8): a dot product
 // does not care for the order of its columns, so each lane takes 16 consecutive bytes of
@@ -368,7 +418,7 @@ struct Q8RowsArgs {
 };
 // NT: tiles of 8 rows of A.
 template <int NT, typename T>
-__global__ void __launch_bounds__(32 * kRowsWarps) k_q8_rows(const Q8RowsArgs a) {
+__global__ void __launch_bounds__(32 * kRowsWarps, NT == 1 ? 4 : 2) k_q8_rows(const Q8RowsArgs a) {
     __shared__ float part[kRowsWarps][16][8 * NT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
@@ -460,6 +510,22 @@ bool scales_map(CUtensorMap* map, const float* base, int64_t padded, int n_g, in
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// y (or each split's sums) in boxes of 32 rows by 128 bytes.
+bool out_map(CUtensorMap* map, void* base, int dtype, int64_t rows, int64_t cols, int splits) {
+    EncodeTiledFn fn = encoder();
+    if (!fn) return false;
+    const int e = dtype == SNK_F32 ? 4 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)splits};
+    cuuint64_t strides[2] = {(cuuint64_t)cols * e, (cuuint64_t)(rows * cols) * e};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / e), 32u, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map,
+              dtype == SNK_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+              : dtype == SNK_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool q8_map(CUtensorMap* map, const uint8_t* base, int64_t len, int64_t rows, int64_t ld, int box_rows) {
     EncodeTiledFn fn = encoder();
     if (!fn) return false;
@@ -483,7 +549,9 @@ struct Q8Plan {
     float *ta, *tb;
     int64_t bytes;
     Q8Plan(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, bool blocks, int num_sms, void* scratch) {
-        rows = M <= kRowsMax;
+        // Few rows: B's codes once by mma.sync, or the tiles below (us, 10000 x 10000, 8 rows: 24 against
+        // 21, 16 rows: 36 against 22; 4096 x 4096: 4.8 against 8.8, 5.8 against 8.4; 2304 x 768: 2 against 5).
+        rows = M <= 8 || (M <= kRowsMax && N * K <= 32000000);
         copy_a = lda % 16 != 0;
         copy_b = ldb % 16 != 0;
         ld = up(K, 16);
@@ -533,9 +601,9 @@ struct Q8Plan {
 };
 
 template <int CG, int BN, bool ROWS>
-int launch_dense(const CUtensorMap (&m)[4], const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
+int launch_dense(const CUtensorMap (&m)[5], const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
     auto* f = k_q8_dense<CG, BN, ROWS>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kQ8Smem<CG, BN, ROWS>)) != cudaSuccess) {
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8Smem) != cudaSuccess) {
         cudaGetLastError();
         return SNK_ERR_CUDA;
     }
@@ -543,7 +611,7 @@ int launch_dense(const CUtensorMap (&m)[4], const Q8DenseArgs& a, int num_sms, c
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));
     c.blockDim = dim3(kQ8Threads);
-    c.dynamicSmemBytes = kQ8Smem<CG, BN, ROWS>;
+    c.dynamicSmemBytes = kQ8Smem;
     c.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -551,14 +619,14 @@ int launch_dense(const CUtensorMap (&m)[4], const Q8DenseArgs& a, int num_sms, c
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = CG == 1 ? 0 : 1;
-    if (cudaLaunchKernelEx(&c, f, m[0], m[1], m[2], m[3], a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&c, f, m[0], m[1], m[2], m[3], m[4], a) != cudaSuccess) {
         cudaGetLastError();
         return SNK_ERR_CUDA;
     }
     return SNK_OK;
 }
 template <bool ROWS>
-int launch_dense(const Q8Plan& p, const CUtensorMap (&m)[4], const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
+int launch_dense(const Q8Plan& p, const CUtensorMap (&m)[5], const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
     if (p.cg == 2) return launch_dense<2, 256, ROWS>(m, a, num_sms, s);
     if (p.bn == 256) return launch_dense<1, 256, ROWS>(m, a, num_sms, s);
     if (p.bn == 128) return launch_dense<1, 128, ROWS>(m, a, num_sms, s);
@@ -635,9 +703,10 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
         const Q8RowsArgs r{pa, pb, lda, ldb, M, N, K, n_g, a_scales, b_scales, bias, y, dtype, b_blocks};
         return dtype == SNK_F32 ? launch_rows<float>(r, s) : dtype == SNK_F16 ? launch_rows<__half>(r, s) : launch_rows<__nv_bfloat16>(r, s);
     }
-    CUtensorMap m[4];
-    if (!q8_map(&m[0], pa, K, M, lda, kDenseM) || !q8_map(&m[1], pb, K, N, ldb, p.bn / p.cg)) return SNK_ERR_CUDA;
-    m[2] = m[3] = m[0];
+    CUtensorMap m[5];
+    const int a_rows = (int)std::min<int64_t>(kDenseM, up(M, 8));
+    if (!q8_map(&m[0], pa, K, M, lda, a_rows) || !q8_map(&m[1], pb, K, N, ldb, p.bn / p.cg)) return SNK_ERR_CUDA;
+    m[2] = m[3] = m[4] = m[0];
     if (!b_blocks) {
         if (!scales_map(&m[2], p.ta, p.padded_m, n_g, kDenseM) || !scales_map(&m[3], p.tb, p.padded_n, n_g, p.bn)) return SNK_ERR_CUDA;
         const int64_t tiles = std::max(p.padded_m, p.padded_n) / 32 * ceil_div(n_g, 32);
@@ -649,6 +718,8 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
     q.M = M;
     q.N = N;
     q.n_g = n_g;
+    q.a_rows = a_rows;
+    q.stages = q8_stages(p.cg, p.bn, a_rows, !b_blocks);
     q.n_mt = p.n_mt;
     q.n_nt = p.n_nt;
     q.splits = p.splits;
@@ -663,6 +734,7 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
     const int e = p.splits > 1 || dtype == SNK_F32 ? 4 : 2;
     const uintptr_t base = (uintptr_t)(p.splits > 1 ? (void*)p.slab : y) | (uintptr_t)(N * e);
     q.vec = (base & 15) == 0;
+    if (q.vec && !out_map(&m[4], p.splits > 1 ? p.slab : y, p.splits > 1 ? SNK_F32 : dtype, M, N, p.splits)) return SNK_ERR_CUDA;
     const int st = b_blocks ? launch_dense<false>(p, m, q, n, s) : launch_dense<true>(p, m, q, n, s);
     if (st != SNK_OK || p.splits == 1) return st;
     return dtype == SNK_F32   ? launch_join<float>(p, M, N, bias, y, n, s)
