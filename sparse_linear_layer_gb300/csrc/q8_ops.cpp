@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
@@ -39,6 +40,7 @@ struct Calls {
     decltype(&snk_vocab_loss_scratch) vocab_scratch = nullptr;
     decltype(&snk_vocab_loss) vocab_loss = nullptr;
     decltype(&snk_vocab_loss_backward) vocab_loss_backward = nullptr;
+    decltype(&snk_status_string) status_string = nullptr;
 } g;
 
 struct Wrong : std::runtime_error {   // becomes ValueError
@@ -514,15 +516,16 @@ PyObject* op_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// The operands of the vocabulary loss.
+// ---- the vocabulary loss, with autograd
+
+// Its operands.
 struct Head {
     at::Tensor x, weight;
-    const at::Tensor& target;
-    int dtype;
+    const at::Tensor target;
+    int dtype, reduction;
     int64_t ignore, rows, cols, vocab;
-    int reduction;
-    Head(PyObject* px, PyObject* pw, PyObject* pt, PyObject* pi, PyObject* pr)
-        : x(tensor(px, "x")), weight(tensor(pw, "weight")), target(tensor(pt, "target")), ignore(integer(pi)) {
+    Head(const at::Tensor& x_, const at::Tensor& w_, const at::Tensor& t_, int64_t ignore_, int64_t reduction_)
+        : x(x_), weight(w_), target(t_), ignore(ignore_) {
         const Matrix m(x), w(weight);
         if ((x.scalar_type() != at::kHalf && x.scalar_type() != at::kBFloat16) || x.scalar_type() != weight.scalar_type())
             throw Wrong("x and weight are both float16 or both bfloat16: " + what(x) + "; " + what(weight));
@@ -535,9 +538,8 @@ struct Head {
         rows = m.rows;
         cols = m.cols;
         vocab = w.rows;
-        const int64_t r = integer(pr);
-        if (r < 0 || r > 2) throw Wrong("reduction is 0 (none), 1 (sum) or 2 (mean)");
-        reduction = (int)r;
+        if (reduction_ < 0 || reduction_ > 2) throw Wrong("reduction is 0 (none), 1 (sum) or 2 (mean)");
+        reduction = (int)reduction_;
     }
     // on the call's stream: copies where an operand is not aligned, and scratch
     at::Tensor scratch(bool backward) {
@@ -545,21 +547,40 @@ struct Head {
         weight = aligned(weight);
         return at::empty({g.vocab_scratch(rows, cols, vocab, backward)}, x.options().requires_grad(false).dtype(at::kByte));
     }
+    // (loss, lse) on the current stream
+    std::pair<at::Tensor, at::Tensor> forward(void* stream) {
+        const auto options = x.options().requires_grad(false).dtype(at::kFloat);
+        at::Tensor lse = at::empty(target.sizes(), options);
+        at::Tensor loss = reduction == 0 ? at::empty(target.sizes(), options) : at::empty({}, options);
+        const at::Tensor s = scratch(false);
+        check(g.vocab_loss(x.data_ptr(), weight.data_ptr(), dtype, (const int64_t*)target.data_ptr(), ignore, rows, cols, vocab,
+                           reduction, (float*)loss.data_ptr(), (float*)lse.data_ptr(), ptr(s), stream),
+              "snk_vocab_loss");
+        return {loss, lse};
+    }
+    // (dx, dweight), undefined for what is not wanted
+    std::pair<at::Tensor, at::Tensor> backward(const at::Tensor& lse, const at::Tensor& dloss, bool want_x, bool want_w, void* stream) {
+        require_f32(lse, rows, x.device(), "lse");
+        require_f32(dloss, reduction == 0 ? rows : 1, x.device(), "dloss");
+        const auto options = x.options().requires_grad(false);
+        at::Tensor dx, dw;
+        if (want_x) dx = at::empty(x.sizes(), options);
+        if (want_w) dw = at::empty(weight.sizes(), options);
+        const at::Tensor s = scratch(true);
+        check(g.vocab_loss_backward(x.data_ptr(), weight.data_ptr(), dtype, (const int64_t*)target.data_ptr(), ignore,
+                                    (const float*)lse.data_ptr(), (const float*)dloss.data_ptr(), rows, cols, vocab, reduction,
+                                    ptr(dx), ptr(dw), ptr(s), stream),
+              "snk_vocab_loss_backward");
+        return {dx, dw};
+    }
 };
 
 // vocab_loss(x, weight, target, ignore, reduction, stream) -> (loss, lse)
 PyObject* op_vocab_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 6, [&] {
-        Head h(a[0], a[1], a[2], a[3], a[4]);
+        Head h(tensor(a[0], "x"), tensor(a[1], "weight"), tensor(a[2], "target"), integer(a[3]), integer(a[4]));
         const OnStream on(a[5], h.x.device());
-        const auto options = h.x.options().requires_grad(false).dtype(at::kFloat);
-        at::Tensor lse = at::empty(h.target.sizes(), options);
-        at::Tensor loss = h.reduction == 0 ? at::empty(h.target.sizes(), options) : at::empty({}, options);
-        const at::Tensor scratch = h.scratch(false);
-        check(g.vocab_loss(h.x.data_ptr(), h.weight.data_ptr(), h.dtype, (const int64_t*)h.target.data_ptr(), h.ignore, h.rows,
-                           h.cols, h.vocab, h.reduction, (float*)loss.data_ptr(), (float*)lse.data_ptr(),
-                           ptr(scratch), on.get()),
-              "snk_vocab_loss");
+        auto [loss, lse] = h.forward(on.get());
         return tuple(std::move(loss), std::move(lse));
     });
 }
@@ -568,22 +589,212 @@ PyObject* op_vocab_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
 //   -> (dx or None, dweight or None)
 PyObject* op_vocab_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 10, [&] {
-        Head h(a[0], a[1], a[2], a[3], a[4]);
-        const at::Tensor& lse = tensor(a[5], "lse");
-        const at::Tensor& dloss = tensor(a[6], "dloss");
-        require_f32(lse, h.rows, h.x.device(), "lse");
-        require_f32(dloss, h.reduction == 0 ? h.rows : 1, h.x.device(), "dloss");
+        Head h(tensor(a[0], "x"), tensor(a[1], "weight"), tensor(a[2], "target"), integer(a[3]), integer(a[4]));
         const OnStream on(a[9], h.x.device());
-        const auto options = h.x.options().requires_grad(false);
-        at::Tensor dx, dw;
-        if (PyObject_IsTrue(a[7])) dx = at::empty(h.x.sizes(), options);
-        if (PyObject_IsTrue(a[8])) dw = at::empty(h.weight.sizes(), options);
-        const at::Tensor scratch = h.scratch(true);
-        check(g.vocab_loss_backward(h.x.data_ptr(), h.weight.data_ptr(), h.dtype, (const int64_t*)h.target.data_ptr(), h.ignore,
-                                    (const float*)lse.data_ptr(), (const float*)dloss.data_ptr(), h.rows, h.cols, h.vocab,
-                                    h.reduction, ptr(dx), ptr(dw), ptr(scratch), on.get()),
-              "snk_vocab_loss_backward");
+        auto [dx, dw] = h.backward(tensor(a[5], "lse"), tensor(a[6], "dloss"), PyObject_IsTrue(a[7]), PyObject_IsTrue(a[8]), on.get());
         return tuple(std::move(dx), std::move(dw));
+    });
+}
+
+using torch::autograd::AutogradContext;
+using torch::autograd::variable_list;
+
+// A backward pass: f's errors as exceptions that the engine passes on, and no second derivative.
+template <typename F>
+variable_list backward_pass(const variable_list& grads, F f) {
+    for (const auto& t : grads)
+        if (at::GradMode::is_enabled() && t.defined() && t.requires_grad())
+            throw std::runtime_error("this operation has no second derivative");
+    try {
+        return f();
+    } catch (const Status& s) {
+        throw std::runtime_error(std::string(s.call) + " failed: " + g.status_string(s.status) + " (status " +
+                                 std::to_string(s.status) + ")");
+    }
+}
+bool wants_gradient(const at::Tensor& t) { return at::GradMode::is_enabled() && t.defined() && t.requires_grad(); }
+void* current_stream(const at::Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
+
+struct HeadFunction : torch::autograd::Function<HeadFunction> {
+    static at::Tensor forward(AutogradContext* ctx, const at::Tensor& x, const at::Tensor& weight, const at::Tensor& target,
+                              int64_t ignore, int64_t reduction) {
+        Head h(x, weight, target, ignore, reduction);
+        const c10::cuda::CUDAGuard on(x.device());
+        auto [loss, lse] = h.forward(current_stream(x));
+        ctx->save_for_backward({x, weight, target, lse});
+        ctx->saved_data["ignore"] = ignore;
+        ctx->saved_data["reduction"] = reduction;
+        return loss;
+    }
+    static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+        return backward_pass(grads, [&]() -> variable_list {
+            if (!grads[0].defined()) return {{}, {}, {}, {}, {}};
+            const auto saved = ctx->get_saved_variables();
+            Head h(saved[0], saved[1], saved[2], ctx->saved_data["ignore"].toInt(), ctx->saved_data["reduction"].toInt());
+            const c10::cuda::CUDAGuard on(h.x.device());
+            auto [dx, dw] = h.backward(saved[3], grads[0].contiguous(), ctx->needs_input_grad(0), ctx->needs_input_grad(1),
+                                       current_stream(h.x));
+            return {dx, dw, {}, {}, {}};
+        });
+    }
+};
+
+// linear_cross_entropy(x, weight, target, ignore, reduction) -> loss, on the current stream, differentiable
+PyObject* op_linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&] {
+        const at::Tensor x = tensor(a[0], "x").contiguous(), w = tensor(a[1], "weight").contiguous();
+        const at::Tensor target = tensor(a[2], "target").contiguous();
+        const int64_t ignore = integer(a[3]), reduction = integer(a[4]);
+        if (wants_gradient(x) || wants_gradient(w))
+            return THPVariable_Wrap(HeadFunction::apply(x, w, target, ignore, reduction));
+        Head h(x, w, target, ignore, reduction);
+        const c10::cuda::CUDAGuard on(x.device());
+        return THPVariable_Wrap(h.forward(current_stream(x)).first);
+    });
+}
+
+// ---- a dense layer on 8-bit matrices, with autograd
+
+int64_t padded(int64_t n) { return up(n, 32); }
+// Pieces of one allocation, 256-byte aligned.
+struct Pieces {
+    at::Tensor memory;
+    char* at = nullptr;
+    explicit Pieces(std::initializer_list<int64_t> bytes, const at::TensorOptions& options) {
+        int64_t n = 0;
+        for (int64_t b : bytes) n += up(b, 256);
+        memory = at::empty({n}, options.dtype(at::kByte));
+        at = (char*)memory.data_ptr();
+    }
+    template <typename T = void>
+    T* take(int64_t bytes) {
+        T* p = (T*)at;
+        at += up(bytes, 256);
+        return p;
+    }
+};
+void product(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb, const float* sb, bool blocks, int64_t m, int64_t n,
+             int64_t k, const float* bias, const at::Tensor& y, const at::TensorOptions& options, void* stream) {
+    const int64_t bytes = g.matmul_scratch(m, n, k, lda, ldb, blocks);
+    at::Tensor scratch;
+    if (bytes > 0) scratch = at::empty({bytes}, options.dtype(at::kByte));
+    check(g.matmul(a, lda, sa, b, ldb, sb, blocks, m, n, k, bias, y.data_ptr(), dtype_of(y), ptr(scratch), stream), "snk_q8_matmul");
+}
+
+// x [rows, cols] and weight [out, cols], checked.
+void require_layer(const at::Tensor& x, const at::Tensor& w, const at::Tensor& bias) {
+    const Matrix mx(x), mw(w);
+    dtype_of(x);
+    dtype_of(w);
+    if (w.dim() != 2 || mw.cols != mx.cols || mw.rows < 1 || w.device() != x.device())
+        throw Wrong("weight is [out, " + std::to_string(mx.cols) + "] with out >= 1 on x's device: " + what(w));
+    if (bias.defined()) require_f32(bias, mw.rows, x.device(), "bias");
+}
+struct LayerOut {
+    at::Tensor y, xt, xt_scales, wt, wt_scales;   // transposed forms: what the gradients take
+};
+LayerOut layer_forward(const at::Tensor& x, const at::Tensor& w, const at::Tensor& bias, bool keep_x, bool keep_w, void* stream) {
+    const int64_t rows = x.size(0), cols = x.size(1), out = w.size(0), gk = groups(cols, 128);
+    const auto options = x.options().requires_grad(false);
+    LayerOut o;
+    o.y = at::empty({rows, out}, options);
+    if (keep_x) {
+        o.xt = at::empty({cols, padded(rows)}, options.dtype(at::kFloat8_e4m3fn));
+        o.xt_scales = at::empty({cols, groups(rows, 128)}, options.dtype(at::kFloat));
+    }
+    if (keep_w) {
+        o.wt = at::empty({cols, padded(out)}, options.dtype(at::kFloat8_e4m3fn));
+        o.wt_scales = at::empty({gk, groups(out, 128)}, options.dtype(at::kFloat));
+    }
+    const int64_t ld = padded(cols), nx = rows * ld, nw = out * ld, nsx = 4 * rows * gk, nsw = 4 * groups(out, 128) * gk;
+    Pieces p({nx, nw, nsx, nsw}, options);
+    void *cx = p.take(nx), *cw = p.take(nw);
+    float *sx = p.take<float>(nsx), *sw = p.take<float>(nsw);
+    if (rows == 0) return o;
+    check(g.pack_both(x.data_ptr(), dtype_of(x), rows, cols, cx, ld, sx, ptr(o.xt), padded(rows), (float*)ptr(o.xt_scales), nullptr,
+                      nullptr, stream),
+          "snk_q8_pack_both");
+    check(g.pack_blocks(w.data_ptr(), dtype_of(w), out, cols, cw, ld, sw, ptr(o.wt), padded(out), (float*)ptr(o.wt_scales), stream),
+          "snk_q8_pack_blocks");
+    product(cx, ld, sx, cw, ld, sw, true, rows, out, cols, (const float*)ptr(bias), o.y, options, stream);
+    return o;
+}
+
+struct LayerFunction : torch::autograd::Function<LayerFunction> {
+    static at::Tensor forward(AutogradContext* ctx, const at::Tensor& x, const at::Tensor& w, const std::optional<at::Tensor>& bias,
+                              bool keep_x, bool keep_w) {
+        const c10::cuda::CUDAGuard on(x.device());
+        LayerOut o = layer_forward(x, w, bias ? *bias : at::Tensor(), keep_x, keep_w, current_stream(x));
+        ctx->saved_data["bias"] = bias.has_value();
+        ctx->save_for_backward({o.xt, o.xt_scales, o.wt, o.wt_scales});
+        ctx->saved_data["rows"] = x.size(0);
+        ctx->saved_data["cols"] = x.size(1);
+        ctx->saved_data["out"] = w.size(0);
+        ctx->saved_data["weight"] = (int64_t)w.scalar_type();
+        return o.y;
+    }
+    static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+        return backward_pass(grads, [&]() -> variable_list {
+            if (!grads[0].defined()) return {{}, {}, {}, {}, {}};
+            const int64_t rows = ctx->saved_data["rows"].toInt(), cols = ctx->saved_data["cols"].toInt();
+            const int64_t out = ctx->saved_data["out"].toInt();
+            const auto weight = (at::ScalarType)ctx->saved_data["weight"].toInt();
+            const auto saved = ctx->get_saved_variables();
+            const at::Tensor &xt = saved[0], &xt_scales = saved[1], &wt = saved[2], &wt_scales = saved[3];
+            const at::Tensor dy = grads[0].contiguous();
+            const bool want_x = ctx->needs_input_grad(0), want_w = ctx->needs_input_grad(1);
+            const bool want_b = ctx->saved_data["bias"].toBool() && ctx->needs_input_grad(2);
+            const c10::cuda::CUDAGuard on(dy.device());
+            void* stream = current_stream(dy);
+            const auto options = dy.options().requires_grad(false);
+            at::Tensor dx, dw, db;
+            if (want_x) dx = at::empty({rows, cols}, options);
+            if (want_w) dw = rows ? at::empty({out, cols}, options.dtype(weight)) : at::zeros({out, cols}, options.dtype(weight));
+            if (want_b) db = at::empty({out}, options.dtype(at::kFloat));
+            const int64_t ld = padded(out), ldt = padded(rows), gn = groups(out, 128), gm = groups(rows, 128);
+            const int64_t nr = want_x ? rows * ld : 0, nt = want_w ? out * ldt : 0, nb = want_b ? g.both_scratch(rows, out) : 0;
+            Pieces p({nr, nt, want_x ? 4 * rows * gn : 0, want_w ? 4 * out * gm : 0, nb}, options);
+            void *c = p.take(nr), *ct = p.take(nt);
+            float *s = p.take<float>(want_x ? 4 * rows * gn : 0), *st = p.take<float>(want_w ? 4 * out * gm : 0);
+            void* parts = p.take(nb);
+            const bool rx = want_x && rows, rw = want_w && rows;
+            check(g.pack_both(dy.data_ptr(), dtype_of(dy), rows, out, rx ? c : nullptr, ld, rx ? s : nullptr, rw ? ct : nullptr, ldt,
+                              rw ? st : nullptr, (float*)ptr(db), parts, stream),
+                  "snk_q8_pack_both");
+            if (rx)
+                product(c, ld, s, wt.data_ptr(), padded(out), (const float*)wt_scales.data_ptr(), true, rows, cols, out, nullptr, dx,
+                        options, stream);
+            if (rw)
+                product(ct, ldt, st, xt.data_ptr(), ldt, (const float*)xt_scales.data_ptr(), false, out, cols, rows, nullptr, dw,
+                        options, stream);
+            return {dx, dw, db, {}, {}};
+        });
+    }
+};
+
+// linear_q8(x, weight, bias or None) -> y, on the current stream, differentiable
+PyObject* op_linear_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 3, [&] {
+        const at::Tensor& x = tensor(a[0], "x");
+        const at::Tensor w = tensor(a[1], "weight").contiguous();
+        const at::Tensor bias = optional(a[2], "bias");
+        if (x.dim() < 1 || x.size(-1) < 1 || !x.is_cuda()) throw Wrong("x is a CUDA tensor [..., cols] with cols >= 1: " + what(x));
+        const at::Tensor x2 = x.dim() == 2 && x.is_contiguous() ? x : x.reshape({x.numel() / x.size(-1), x.size(-1)}).contiguous();
+        require_layer(x2, w, bias);
+        at::Tensor y;
+        if (wants_gradient(x) || wants_gradient(w) || wants_gradient(bias)) {
+            y = LayerFunction::apply(x2, w, bias.defined() ? std::optional<at::Tensor>(bias) : std::nullopt, wants_gradient(w),
+                                     wants_gradient(x));
+        } else {
+            const c10::cuda::CUDAGuard on(x.device());
+            y = layer_forward(x2, w, bias, false, false, current_stream(x)).y;
+        }
+        if (x.dim() != 2) {
+            c10::SmallVector<int64_t, 5> shape(x.sizes().begin(), x.sizes().end());
+            shape.back() = w.size(0);
+            y = y.reshape(shape);
+        }
+        return THPVariable_Wrap(std::move(y));
     });
 }
 
@@ -623,6 +834,7 @@ PyObject* op_load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     find(c.vocab_scratch, "snk_vocab_loss_scratch");
     find(c.vocab_loss, "snk_vocab_loss");
     find(c.vocab_loss_backward, "snk_vocab_loss_backward");
+    find(c.status_string, "snk_status_string");
     if (!ok) {
         PyErr_SetString(PyExc_RuntimeError, "libsnk.so lacks a call of this module");
         return nullptr;
@@ -647,6 +859,8 @@ PyMethodDef methods[] = {OP("load", op_load),
                          OP("matmul", op_matmul),
                          OP("vocab_loss", op_vocab_loss),
                          OP("vocab_loss_backward", op_vocab_loss_backward),
+                         OP("linear_cross_entropy", op_linear_cross_entropy),
+                         OP("linear_q8", op_linear_q8),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q8ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

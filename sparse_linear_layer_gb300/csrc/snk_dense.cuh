@@ -38,6 +38,7 @@ struct DenseArgs {
     int a_rows;            // rows of A that a CTA loads of a tile: 128, or fewer where there is one tile of fewer
     int stages;
     int splits;            // ranges of K, each an item of its own
+    int turns;             // accumulators that share an item's K (k_dense<.., TURNS>; else 1)
     int64_t K;
     uint32_t idesc;
     const int32_t* rows;   // on the device: the rows of A (rows_k = 0) or the length of K (1) that count; null: all
@@ -176,17 +177,28 @@ struct DenseTile {
     bool none;         // no columns of K: zero
     int rows;          // rows of A that count (all of them without a device count)
 };
-// 32 accumulator columns.
-__device__ __forceinline__ void dense_read(uint32_t taddr, const DenseTile& t, float (&v)[32]) {
-    uint32_t r[32];
-    tmem_ld32(taddr, r);
+// An epilogue reads its half's columns 32 at a time, c = 0, 32, 64, 96, from the accumulator ...
+struct FromTmem {
+    uint32_t taddr;   // of the half's first column on the warp's lanes
+    __device__ __forceinline__ void get(int c, const DenseTile& t, float (&v)[32]) const {
+        uint32_t r[32];
+        tmem_ld32(taddr + c, r);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-    if (!t.ok || t.none) {
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        if (!t.ok || t.none) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = t.ok ? 0.f : __int_as_float(0x7fc00000);
+            for (int j = 0; j < 32; ++j) v[j] = t.ok ? 0.f : __int_as_float(0x7fc00000);
+        }
     }
-}
+};
+// ... or from the sums of several.
+struct FromSums {
+    const float (&sum)[kDenseN / 2];
+    __device__ __forceinline__ void get(int c, const DenseTile& t, float (&v)[32]) const {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = t.ok ? sum[c + j] : __int_as_float(0x7fc00000);
+    }
+};
 
 // Rows of an epilogue warp's tile, 128 bytes each, turned in shared memory so that a store
 // instruction writes 128 contiguous bytes of a row instead of 32 bytes of 32 rows (the
@@ -262,8 +274,9 @@ __device__ __forceinline__ void drain_last(uint64_t* full, const Stages& r, bool
 }
 
 // Epilogue: a type with Args and static __device__ void run(const Args&, const DenseTile&,
-// uint32_t taddr), taddr the TMEM address of the half's first column on the warp's lanes.
-template <int CG, bool A_MN, bool B_MN, class Epilogue>
+// const Source&).  TURNS: the tensor cores' additions truncate, so a long K is shared by
+// accumulators, which the epilogue's threads add with rounding in registers.
+template <int CG, bool A_MN, bool B_MN, bool TURNS, class Epilogue>
 __global__ void __launch_bounds__(kDenseThreads, 1)
     k_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const DenseArgs a,
             const typename Epilogue::Args ea) {
@@ -355,39 +368,38 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             bool ok = true;
             Stages r(a.stages);
             uint32_t q = 0;   // accumulators filled
-            for (int id = first; id < items && ok; id += step, ++q) {
+            const int turns = TURNS ? a.turns : 1;
+            for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
-                const int k0 = (int)((int64_t)n_k * it.split / a.splits), k1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
-                const int ab = q & 1;
-                if (q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem + ab * kDenseN;
-                if (k0 < k1 && !mbar_wait(&full[r.slot], r.parity)) {
-                    ok = false;
-                    break;
-                }
-                for (int k = k0; k < k1; ++k) {
-                    tc_fence_after();
-                    const int s = r.slot;
-                    const uint32_t sa = smem_u32(sm + s * stage), sb = sa + a_bytes;
-                    r.next();
-#pragma unroll
-                    for (int kk = 0; kk < kDenseK / 16; ++kk) {
-                        // 16 columns of K: 32 bytes along a K-major row, two atoms of an MN-major box
-                        const uint64_t da = A_MN ? desc_mn128(sa + kk * 2048) : desc_sw128(sa + kk * 32);
-                        const uint64_t db = B_MN ? desc_mn128(sb + kk * 2048) : desc_sw128(sb + kk * 32);
-                        dense_mma<CG>(d, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
-                        // the next stage is waited for while the tensor cores are busy (a wait
-                        // costs a hundred cycles even when there is nothing to wait for)
-                        if (kk == 1 && k + 1 < k1 && !mbar_wait(&full[r.slot], r.parity)) ok = false;
+                const int i0 = (int)((int64_t)n_k * it.split / a.splits), i1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
+                for (int turn = 0; turn < turns && ok; ++turn, ++q) {
+                    const int k0 = i0 + (i1 - i0) * turn / turns, k1 = i0 + (i1 - i0) * (turn + 1) / turns;
+                    const int ab = q & 1;
+                    if ((q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1)) || (k0 < k1 && !mbar_wait(&full[r.slot], r.parity))) {
+                        ok = false;
+                        break;
                     }
-                    dense_commit<CG>(&empty[s]);
-                    if (!ok) break;
+                    const uint32_t d = tmem + ab * kDenseN;
+                    for (int k = k0; k < k1; ++k) {
+                        tc_fence_after();
+                        const int s = r.slot;
+                        const uint32_t sa = smem_u32(sm + s * stage), sb = sa + a_bytes;
+                        r.next();
+#pragma unroll
+                        for (int kk = 0; kk < kDenseK / 16; ++kk) {
+                            // 16 columns of K: 32 bytes along a K-major row, two atoms of an MN-major box
+                            const uint64_t da = A_MN ? desc_mn128(sa + kk * 2048) : desc_sw128(sa + kk * 32);
+                            const uint64_t db = B_MN ? desc_mn128(sb + kk * 2048) : desc_sw128(sb + kk * 32);
+                            dense_mma<CG>(d, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
+                            // the next stage is waited for while the tensor cores are busy (a wait
+                            // costs a hundred cycles even when there is nothing to wait for)
+                            if (kk == 1 && k + 1 < k1 && !mbar_wait(&full[r.slot], r.parity)) ok = false;
+                        }
+                        dense_commit<CG>(&empty[s]);
+                        if (!ok) break;
+                    }
+                    if (ok) dense_commit<CG>(&accf[ab]);
                 }
-                if (ok) dense_commit<CG>(&accf[ab]);
             }
             if (!ok) {   // no MMA may still run when the memory is given back
                 dense_commit<CG>(&fin);
@@ -397,14 +409,26 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     } else {
         const int half = warp >= 6 ? 1 : 0, quarter = warp & 3;
         const int hc = a.bn / 2;
+        const uint32_t lanes = tmem + half * hc + ((uint32_t)(quarter * 32) << 16);
         bool ok = true;
         uint32_t q = 0;
-        for (int id = first; id < items; id += step, ++q) {
-            const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
-            const int ab = (int)(q & 1);
-            if (ok) ok = mbar_wait(&accf[ab], (q >> 1) & 1);
+        auto wait = [&] {
+            if (ok) ok = mbar_wait(&accf[q & 1], (q >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
+            return lanes + (q & 1) * kDenseN;
+        };
+        auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 1) mbar_arrive(&acce[q & 1]);
+                else mbar_arrive_cluster(first_cta(&acce[q & 1]));
+            }
+            ++q;
+        };
+        for (int id = first; id < items; id += step) {
+            const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
             DenseTile tile;
             tile.row = (int64_t)(it.mt * CG + rank) * kDenseM + quarter * 32 + lane;
             tile.col = (int64_t)it.nt * a.bn + half * hc;
@@ -413,15 +437,32 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             tile.nt = it.nt;
             tile.half = half;
             tile.split = it.split;
-            tile.ok = ok;
             tile.none = (int64_t)n_k * it.split / a.splits == (int64_t)n_k * (it.split + 1) / a.splits;
             tile.rows = rows;
-            Epilogue::run(ea, tile, tmem + ab * kDenseN + half * hc + ((uint32_t)(quarter * 32) << 16));
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 1) mbar_arrive(&acce[ab]);
-                else mbar_arrive_cluster(first_cta(&acce[ab]));
+            if constexpr (TURNS) {
+                float sum[kDenseN / 2];
+#pragma unroll
+                for (int j = 0; j < kDenseN / 2; ++j) sum[j] = 0.f;
+                for (int turn = 0; turn < a.turns; ++turn) {
+                    const uint32_t taddr = wait();
+#pragma unroll
+                    for (int c = 0; c < kDenseN / 2; c += 32) {
+                        if (c < hc) {
+                            uint32_t r[32];
+                            tmem_ld32(taddr + c, r);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[c + j] += __uint_as_float(r[j]);
+                        }
+                    }
+                    release();
+                }
+                tile.ok = ok;
+                Epilogue::run(ea, tile, FromSums{sum});
+            } else {
+                const FromTmem source{wait()};
+                tile.ok = ok;
+                Epilogue::run(ea, tile, source);
+                release();
             }
         }
     }
@@ -448,14 +489,11 @@ inline bool dense_map(CUtensorMap* map, const void* base, bool bf16, int64_t len
 }
 
 // Launch: items run by as many CTAs (pairs) as there are SMs (pairs of SMs), or fewer.
-template <int CG, bool A_MN, bool B_MN, class Epilogue>
+template <int CG, bool A_MN, bool B_MN, bool TURNS, class Epilogue>
 int dense_launch(const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& ea, int num_sms,
                  cudaStream_t s) {
-    auto* f = k_dense<CG, A_MN, B_MN, Epilogue>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmem) != cudaSuccess) {
-        cudaGetLastError();
-        return SNK_ERR_CUDA;
-    }
+    constexpr auto f = k_dense<CG, A_MN, B_MN, TURNS, Epilogue>;
+    if (!allow_smem<f>(kDenseSmem)) return SNK_ERR_CUDA;
     const int64_t items = (int64_t)a.n_mt * a.n_nt * a.splits;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));

@@ -602,11 +602,8 @@ struct Q8Plan {
 
 template <int CG, int BN, bool ROWS>
 int launch_dense(const CUtensorMap (&m)[5], const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
-    auto* f = k_q8_dense<CG, BN, ROWS>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8Smem) != cudaSuccess) {
-        cudaGetLastError();
-        return SNK_ERR_CUDA;
-    }
+    constexpr auto f = k_q8_dense<CG, BN, ROWS>;
+    if (!allow_smem<f>(kQ8Smem)) return SNK_ERR_CUDA;
     const int64_t items = (int64_t)a.n_mt * a.n_nt * a.splits;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));

@@ -267,11 +267,8 @@ __global__ void __launch_bounds__(256) k_q8_sums(const float* __restrict__ part,
 
 template <typename T, bool BLOCKS, TileLoad LOAD>
 int launch_tile(const CUtensorMap& map, const TileArgs& a, int num_sms, cudaStream_t s) {
-    auto* f = k_q8_tile<T, BLOCKS, LOAD>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kTileSmem<T, LOAD>)) != cudaSuccess) {
-        cudaGetLastError();
-        return SNK_ERR_CUDA;
-    }
+    constexpr auto f = k_q8_tile<T, BLOCKS, LOAD>;
+    if (!allow_smem<f>(kTileSmem<T, LOAD>)) return SNK_ERR_CUDA;
     const unsigned blocks = (unsigned)std::min<int64_t>(a.tiles_r * a.tiles_c, 2 * num_sms);
     f<<<blocks, kTileThreads, kTileSmem<T, LOAD>, s>>>(map, a);
     return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;

@@ -31,6 +31,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kGatherRows = 16;     // rows per block of k_vocab_rows
 constexpr int kDirectRows = 128;    // up to these the forward reads x itself: one row tile either way
 constexpr float kDzScale = 8192.f;  // 2^13
+// Stages of an accumulator's turn in the loss (64 MMA steps, whose additions truncate): at 4096
+// columns the logits of one accumulator left the mean loss off by LOSS_ERR_ONE, turns by LOSS_ERR.
+constexpr int kTurnStages = 16;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
@@ -47,12 +50,15 @@ struct LseEpilogue {
         int64_t ld;
         int64_t vocab;
     };
-    __device__ static void run(const Args& a, const DenseTile& t, uint32_t taddr) {
+    template <class Source>
+    __device__ static void run(const Args& a, const DenseTile& t, const Source& from) {
         const int lim = (int)min((int64_t)t.cols, a.vocab - t.col);   // (may be negative: nothing here)
         float m = __int_as_float(0xff800000), s = 0.f;
-        for (int c = 0; c < lim; c += 32) {
+#pragma unroll
+        for (int c = 0; c < kDenseN / 2; c += 32) {
+            if (c >= lim) break;
             float v[32];
-            dense_read(taddr + c, t, v);
+            from.get(c, t, v);
             if (c + 32 > lim) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -98,7 +104,8 @@ struct GradEpilogue {
         const int64_t* target;    // [rows]
         const uint32_t* most;     // bits of the largest finite |g|
     };
-    __device__ static void run(const Args& a, const DenseTile& t, uint32_t taddr) {
+    template <class Source>
+    __device__ static void run(const Args& a, const DenseTile& t, const Source& from) {
         float c = 0.f, l2 = 0.f;
         int64_t at = -1;
         if (t.row < t.rows) {
@@ -111,7 +118,7 @@ struct GradEpilogue {
         T* out = a.dz + t.row * a.ld + t.col;
         for (int b = 0; b < top; b += 32) {
             float v[32];
-            dense_read(taddr + b, t, v);
+            from.get(b, t, v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = c * exp2_fast(fmaf(v[j], kLog2e, -l2));
             if (at >= b && at < b + 32) {
@@ -150,12 +157,13 @@ struct SumEpilogue {
         int64_t rows, ld;
         int add;           // to what is there
     };
-    __device__ static void run(const Args& a, const DenseTile& t, uint32_t taddr) {
+    template <class Source>
+    __device__ static void run(const Args& a, const DenseTile& t, const Source& from) {
         const int lim = (int)min((int64_t)t.cols, a.ld - t.col);   // (a multiple of 8)
         float* out = a.slab + ((int64_t)t.split * a.rows + t.row) * a.ld + t.col;
         for (int b = 0; b < lim; b += 32) {
             float v[32];
-            dense_read(taddr + b, t, v);
+            from.get(b, t, v);
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
                 if (b + j < lim) {
@@ -182,14 +190,15 @@ struct StoreEpilogue {
         const uint32_t* most;
         int vec;                 // elements per store: 16, 8 or 1, by the rows' alignment
     };
-    __device__ static void run(const Args& a, const DenseTile& t, uint32_t taddr) {
+    template <class Source>
+    __device__ static void run(const Args& a, const DenseTile& t, const Source& from) {
         const int lim = t.row < a.width ? (int)min((int64_t)t.cols, a.cols - t.col) : 0;
         const float scale = 1.f / (GradEpilogue<T>::grad_factor(*a.most) * kDzScale);
         T* out = a.out + t.row * a.cols + t.col;
         const int top = (int)min((int64_t)t.cols, a.cols - t.col);   // the same in all lanes
         for (int b = 0; b < top; b += 32) {
             float v[32];
-            dense_read(taddr + b, t, v);
+            from.get(b, t, v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= scale;
 #pragma unroll
@@ -664,11 +673,11 @@ DenseArgs dense_args(const Form& f, bool bf16, bool a_mn, bool b_mn, int64_t m, 
     a.group = 16 / f.cg;
     return a;
 }
-template <bool A_MN, bool B_MN, class Epilogue>
+template <bool A_MN, bool B_MN, class Epilogue, bool TURNS = false>
 int launch(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& e, int num_sms,
            cudaStream_t s) {
-    return f.cg == 2 ? dense_launch<2, A_MN, B_MN, Epilogue>(ma, mb, a, e, num_sms, s)
-                     : dense_launch<1, A_MN, B_MN, Epilogue>(ma, mb, a, e, num_sms, s);
+    return f.cg == 2 ? dense_launch<2, A_MN, B_MN, TURNS, Epilogue>(ma, mb, a, e, num_sms, s)
+                     : dense_launch<1, A_MN, B_MN, TURNS, Epilogue>(ma, mb, a, e, num_sms, s);
 }
 
 template <typename T>
@@ -718,9 +727,11 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
     DenseArgs a = dense_args(p.form, bf, false, false, h.rows, h.vocab, h.ld, a_rows);
     a.rows = p.gather ? p.count : nullptr;
     a.zero = p.arrived;
-    if (int st = launch<false, false, LseEpilogue>(p.form, ma, mb, a, LseEpilogue::Args{p.part, h.padded, h.vocab}, num_sms, s);
-        st != SNK_OK)
-        return st;
+    const LseEpilogue::Args ea{p.part, h.padded, h.vocab};
+    a.turns = (int)ceil_div(ceil_div(h.ld, kDenseK), kTurnStages);
+    const int st = a.turns > 1 ? launch<false, false, LseEpilogue, true>(p.form, ma, mb, a, ea, num_sms, s)
+                               : launch<false, false, LseEpilogue>(p.form, ma, mb, a, ea, num_sms, s);
+    if (st != SNK_OK) return st;
     FinishArgs f = {};
     f.part = p.part;
     f.ld = h.padded;
