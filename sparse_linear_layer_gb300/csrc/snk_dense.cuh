@@ -44,6 +44,7 @@ struct DenseArgs {
     const int32_t* rows;   // on the device: the rows of A (rows_k = 0) or the length of K (1) that count; null: all
     int rows_k;
     int group;             // row tiles that sweep the columns together (L2 reuse)
+    int64_t m_held;        // rows that the output has memory for: those behind them are not handed to the epilogue
     int32_t* zero;         // a word that the first CTA clears, or null
 };
 
@@ -67,7 +68,7 @@ struct DenseItem {
 // Stages that fit: A's rows (what the MMA reads behind them is another operand's, for rows
 // that nobody reads) and B's.
 inline int dense_stages(int cg, int a_rows, int bn) {
-    const int bytes = (a_rows + bn / cg) * 128, room = kDenseStageRoom - (kDenseM - a_rows) * 128;
+    const int bytes = (a_rows + bn / cg) * 128, room = kDenseStageRoom - (a_rows < kDenseM ? kDenseM - a_rows : 0) * 128;
     return room / bytes < kDenseStages ? room / bytes : kDenseStages;
 }
 
@@ -275,12 +276,16 @@ __device__ __forceinline__ void drain_last(uint64_t* full, const Stages& r, bool
 
 // Epilogue: a type with Args and static __device__ void run(const Args&, const DenseTile&,
 // const Source&).  TURNS: the tensor cores' additions truncate, so a long K is shared by
-// accumulators, which the epilogue's threads add with rounding in registers.
-template <int CG, bool A_MN, bool B_MN, bool TURNS, class Epilogue>
+// accumulators, which the epilogue's threads add with rounding in registers.  DUAL: a pair's tile
+// is 512 rows, two MMAs of 256 that share B, each with its own accumulator; a stage is then worth
+// two for 1.5 times the bytes from the L2, which bound the single tile (12.5 TB/s), and the
+// accumulators are drained between tiles instead of beside them.
+template <int CG, bool A_MN, bool B_MN, bool TURNS, bool DUAL, class Epilogue>
 __global__ void __launch_bounds__(kDenseThreads, 1)
     k_dense(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const DenseArgs a,
             const typename Epilogue::Args ea) {
-    constexpr int S = kDenseStages;
+    static_assert(!DUAL || (CG == 2 && !TURNS), "a dual tile is a pair's, and has no accumulator to take turns");
+    constexpr int S = kDenseStages, SUBS = DUAL ? 2 : 1;
     extern __shared__ __align__(1024) unsigned char dense_raw[];
     unsigned char* sm = dense_raw + ((1024 - (smem_u32(dense_raw) & 1023)) & 1023);
     __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin;
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int n = __ldg(a.rows);
         if (a.rows_k) K = min(K, (int64_t)n);
         else {
-            n_mt = min(n_mt, (n + kDenseM * CG - 1) / (kDenseM * CG));
+            n_mt = min(n_mt, (n + kDenseM * CG * SUBS - 1) / (kDenseM * CG * SUBS));
             rows = n;
         }
     }
@@ -323,8 +328,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const int items = n_mt * a.n_nt * a.splits;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
     const int half_b = a.bn / CG;   // rows of B that this CTA loads
-    const uint32_t tx = (uint32_t)(a.a_rows + half_b) * 128 * CG;
-    const int a_bytes = a.a_rows * 128, stage = (a.a_rows + half_b) * 128;
+    const int a_bytes = a.a_rows * 128, stage = (a.a_rows * SUBS + half_b) * 128;
+    const uint32_t tx = (uint32_t)stage * CG;
+    // first row of A of a tile's part in this CTA
+    auto row_of = [&](int mt, int sub) { return ((mt * SUBS + sub) * CG + rank) * kDenseM; };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int k0 = (int)((int64_t)n_k * it.split / a.splits), k1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
-                const int m0 = (it.mt * CG + rank) * kDenseM, n0 = it.nt * a.bn + rank * half_b;
+                const int n0 = it.nt * a.bn + rank * half_b;
                 for (int k = k0; k < k1; ++k) {
                     const int s = r.slot;
                     if (used && !mbar_wait(&empty[s], r.parity ^ 1)) {
@@ -341,15 +348,19 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                         break;
                     }
                     unsigned char* sa = sm + s * stage;
-                    unsigned char* sb = sa + a_bytes;
+                    unsigned char* sb = sa + SUBS * a_bytes;
                     if (rank == 0) mbar_expect_tx(&full[s], tx);
                     const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : first_cta(&full[s]);
                     const int kc = k * kDenseK;
-                    if constexpr (A_MN) {
-                        dense_load<CG>(sa, &map_a, m0, kc, bar);
-                        dense_load<CG>(sa + kDenseBoxBytes, &map_a, m0 + 64, kc, bar);
-                    } else {
-                        dense_load<CG>(sa, &map_a, kc, m0, bar);
+#pragma unroll
+                    for (int sub = 0; sub < SUBS; ++sub) {
+                        const int m0 = row_of(it.mt, sub);
+                        if constexpr (A_MN) {
+                            dense_load<CG>(sa + sub * a_bytes, &map_a, m0, kc, bar);
+                            dense_load<CG>(sa + sub * a_bytes + kDenseBoxBytes, &map_a, m0 + 64, kc, bar);
+                        } else {
+                            dense_load<CG>(sa + sub * a_bytes, &map_a, kc, m0, bar);
+                        }
                     }
                     if constexpr (B_MN) {
                         for (int j = 0; j < half_b; j += 64)
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int i0 = (int)((int64_t)n_k * it.split / a.splits), i1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
-                for (int turn = 0; turn < turns && ok; ++turn, ++q) {
+                for (int turn = 0; turn < turns && ok; ++turn, q += SUBS) {
                     const int k0 = i0 + (i1 - i0) * turn / turns, k1 = i0 + (i1 - i0) * (turn + 1) / turns;
                     const int ab = q & 1;
                     if ((q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1)) || (k0 < k1 && !mbar_wait(&full[r.slot], r.parity))) {
@@ -383,22 +394,33 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     for (int k = k0; k < k1; ++k) {
                         tc_fence_after();
                         const int s = r.slot;
-                        const uint32_t sa = smem_u32(sm + s * stage), sb = sa + a_bytes;
+                        const uint32_t sa = smem_u32(sm + s * stage), sb = sa + SUBS * a_bytes;
                         r.next();
 #pragma unroll
-                        for (int kk = 0; kk < kDenseK / 16; ++kk) {
-                            // 16 columns of K: 32 bytes along a K-major row, two atoms of an MN-major box
-                            const uint64_t da = A_MN ? desc_mn128(sa + kk * 2048) : desc_sw128(sa + kk * 32);
-                            const uint64_t db = B_MN ? desc_mn128(sb + kk * 2048) : desc_sw128(sb + kk * 32);
-                            dense_mma<CG>(d, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
-                            // the next stage is waited for while the tensor cores are busy (a wait
-                            // costs a hundred cycles even when there is nothing to wait for)
-                            if (kk == 1 && k + 1 < k1 && !mbar_wait(&full[r.slot], r.parity)) ok = false;
+                        for (int sub = 0; sub < SUBS; ++sub) {
+                            if (DUAL && sub == 1 && k == k0 && q >= 2) {   // the second accumulator, drained after the first
+                                if (!mbar_wait(&acce[1], ((q >> 1) - 1) & 1)) ok = false;
+                                tc_fence_after();
+                            }
+#pragma unroll
+                            for (int kk = 0; kk < kDenseK / 16; ++kk) {
+                                // 16 columns of K: 32 bytes along a K-major row, two atoms of an MN-major box
+                                const uint32_t so = sa + sub * a_bytes;
+                                const uint64_t da = A_MN ? desc_mn128(so + kk * 2048) : desc_sw128(so + kk * 32);
+                                const uint64_t db = B_MN ? desc_mn128(sb + kk * 2048) : desc_sw128(sb + kk * 32);
+                                dense_mma<CG>(d + sub * kDenseN, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
+                                // the next stage is waited for while the tensor cores are busy (a wait
+                                // costs a hundred cycles even when there is nothing to wait for)
+                                if (sub == SUBS - 1 && kk == 1 && k + 1 < k1 && !mbar_wait(&full[r.slot], r.parity)) ok = false;
+                            }
                         }
                         dense_commit<CG>(&empty[s]);
                         if (!ok) break;
                     }
-                    if (ok) dense_commit<CG>(&accf[ab]);
+                    if (ok) {
+                        dense_commit<CG>(&accf[ab]);
+                        if constexpr (DUAL) dense_commit<CG>(&accf[1]);
+                    }
                 }
             }
             if (!ok) {   // no MMA may still run when the memory is given back
@@ -430,7 +452,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         for (int id = first; id < items; id += step) {
             const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
             DenseTile tile;
-            tile.row = (int64_t)(it.mt * CG + rank) * kDenseM + quarter * 32 + lane;
             tile.col = (int64_t)it.nt * a.bn + half * hc;
             tile.cols = hc;
             tile.mt = it.mt;
@@ -457,12 +478,17 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     release();
                 }
                 tile.ok = ok;
-                Epilogue::run(ea, tile, FromSums{sum});
+                tile.row = row_of(it.mt, 0) + quarter * 32 + lane;
+                if (tile.row - lane < a.m_held) Epilogue::run(ea, tile, FromSums{sum});
             } else {
-                const FromTmem source{wait()};
-                tile.ok = ok;
-                Epilogue::run(ea, tile, source);
-                release();
+#pragma unroll 1
+                for (int sub = 0; sub < SUBS; ++sub) {
+                    tile.row = row_of(it.mt, sub) + quarter * 32 + lane;
+                    const FromTmem source{wait()};
+                    tile.ok = ok;
+                    if (tile.row - lane < a.m_held) Epilogue::run(ea, tile, source);
+                    release();
+                }
             }
         }
     }
@@ -489,10 +515,10 @@ inline bool dense_map(CUtensorMap* map, const void* base, bool bf16, int64_t len
 }
 
 // Launch: items run by as many CTAs (pairs) as there are SMs (pairs of SMs), or fewer.
-template <int CG, bool A_MN, bool B_MN, bool TURNS, class Epilogue>
+template <int CG, bool A_MN, bool B_MN, bool TURNS, bool DUAL, class Epilogue>
 int dense_launch(const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& ea, int num_sms,
                  cudaStream_t s) {
-    constexpr auto f = k_dense<CG, A_MN, B_MN, TURNS, Epilogue>;
+    constexpr auto f = k_dense<CG, A_MN, B_MN, TURNS, DUAL, Epilogue>;
     if (!allow_smem<f>(kDenseSmem)) return SNK_ERR_CUDA;
     const int64_t items = (int64_t)a.n_mt * a.n_nt * a.splits;
     cudaLaunchConfig_t c = {};

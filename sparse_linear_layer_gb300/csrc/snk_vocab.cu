@@ -546,29 +546,39 @@ int launched() { return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUD
 // microsecond beside its stages; a range's sums are written and read.
 struct Form {
     int cg = 1, bn = 256, splits = 1;
+    bool dual = false;
+    int rows() const { return 128 * cg * (dual ? 2 : 1); }   // of a tile
 };
 // m x n over n_k stages; rows: of A that a tile loads; width: multiples of it (per CTA of a pair)
-// are possible as tile widths; most: ranges of K at most; sums: bytes of one range's sums.
-Form pick_form(int64_t m, int64_t n, int64_t n_k, int rows, int width, int most, double sums, int num_sms) {
+// are possible as tile widths; most: ranges of K at most; sums: bytes of one range's sums; dual: us that
+// a dual tile has beside its stages (0: no dual tiles), its epilogue's time.
+Form pick_form(int64_t m, int64_t n, int64_t n_k, int rows, int width, int most, double sums, int num_sms, double dual) {
     Form best;
     double least = 1e30;
-    for (int cg = 2; cg >= 1; --cg) {
-        if (cg == 2 && m <= 128) continue;
-        const int step = std::max(32, width * cg);
-        for (int bn = 256; bn >= std::max(64, step); bn -= step) {
-            const int64_t tiles = ceil_div(m, 128 * cg) * ceil_div(n, bn), units = num_sms / cg;
-            for (int sp = 1; sp <= most && (sp == 1 || n_k / sp >= 8); ++sp) {
-                const double busy = (double)std::min(units, tiles * sp) * cg;
-                const double stage = std::max(cg == 2 ? 0.34 : std::max(0.18, 0.36 * bn / 256), (rows + bn / cg) * 128 * busy / 12.5e6);
-                const double t = (double)ceil_div(tiles * sp, units) * ((double)ceil_div(n_k, sp) * stage + 1.0) + sp * sums / 3.3e6;
-                if (t < 0.99 * least) {
-                    least = t;
-                    best.cg = cg;
-                    best.bn = bn;
-                    best.splits = sp;
-                }
+    auto look = [&](const Form& f0, double mmas, double fixed) {
+        Form f = f0;
+        const int64_t tiles = ceil_div(m, f.rows()) * ceil_div(n, f.bn), units = num_sms / f.cg;
+        for (f.splits = 1; f.splits <= most && (f.splits == 1 || n_k / f.splits >= 8); ++f.splits) {
+            const double busy = (double)std::min(units, tiles * f.splits) * f.cg;
+            const double stage = std::max(mmas, (rows * (f.dual ? 2 : 1) + f.bn / f.cg) * 128 * busy / 12.5e6);
+            const double t = (double)ceil_div(tiles * f.splits, units) * ((double)ceil_div(n_k, f.splits) * stage + fixed) +
+                             f.splits * sums / 3.3e6;
+            if (t < 0.99 * least) {
+                least = t;
+                best = f;
             }
         }
+    };
+    Form f;
+    if (m > 256 && dual > 0 && 256 % (2 * width) == 0) {
+        f.cg = 2;
+        f.dual = true;
+        look(f, 0.62, dual);
+        f.dual = false;
+    }
+    for (f.cg = m > 128 ? 2 : 1; f.cg >= 1; --f.cg) {
+        const int step = std::max(32, width * f.cg);
+        for (f.bn = 256; f.bn >= std::max(64, step); f.bn -= step) look(f, f.cg == 2 ? 0.34 : std::max(0.18, 0.36 * f.bn / 256), 1.0);
     }
     return best;
 }
@@ -605,7 +615,8 @@ struct ForwardPlan {
     int64_t bytes;
     ForwardPlan(const Shape& h, int num_sms, void* scratch) {
         gather = h.rows > kDirectRows || h.pads();
-        form = pick_form(h.rows, h.vocab, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms);
+        form = pick_form(h.rows, h.vocab, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms,
+                         ceil_div(h.ld, kDenseK) <= kTurnStages ? 2 : 0);
         n_nt = (int)ceil_div(h.vocab, form.bn);
         per_block = 1;
         while (per_block < 8 && ceil_div(h.rows, per_block) > num_sms) per_block *= 2;
@@ -641,9 +652,9 @@ struct BackwardPlan {
         const int64_t whole = up(h.vocab, 256);
         piece = std::max<int64_t>(256, std::min(whole, kPieceBytes / (2 * h.padded) / 256 * 256));
         piece = up(ceil_div(whole, ceil_div(whole, piece)), 256);   // equal ones
-        z = pick_form(h.rows, piece, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms);
-        x = pick_form(h.rows, h.ld, piece / 64, h.tile_rows(), 64, 64, 8.0 * h.rows * h.ld, num_sms);
-        w = pick_form(piece, h.ld, ceil_div(h.rows, 64), kDenseM, 64, 1, 0, num_sms);
+        z = pick_form(h.rows, piece, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms, 4.5);
+        x = pick_form(h.rows, h.ld, piece / 64, h.tile_rows(), 64, 64, 8.0 * h.rows * h.ld, num_sms, 2);
+        w = pick_form(piece, h.ld, ceil_div(h.rows, 64), kDenseM, 64, 1, 0, num_sms, 2);
         Scratch s(scratch);
         count = s.take<int32_t>(2);
         most = reinterpret_cast<uint32_t*>(count + 1);
@@ -662,11 +673,12 @@ struct BackwardPlan {
 
 DenseArgs dense_args(const Form& f, bool bf16, bool a_mn, bool b_mn, int64_t m, int64_t n, int64_t k, int a_rows = kDenseM) {
     DenseArgs a = {};
-    a.n_mt = (int)ceil_div(m, 128 * f.cg);
+    a.n_mt = (int)ceil_div(m, f.rows());
     a.n_nt = (int)ceil_div(n, f.bn);
     a.bn = f.bn;
     a.a_rows = a_rows;
-    a.stages = dense_stages(f.cg, a_rows, f.bn);
+    a.stages = dense_stages(f.cg, f.dual ? 2 * a_rows : a_rows, f.bn);
+    a.m_held = up(m, 256);
     a.splits = f.splits;
     a.K = k;
     a.idesc = dense_idesc(bf16, a_mn, b_mn, 128 * f.cg, f.bn);
@@ -676,8 +688,11 @@ DenseArgs dense_args(const Form& f, bool bf16, bool a_mn, bool b_mn, int64_t m, 
 template <bool A_MN, bool B_MN, class Epilogue, bool TURNS = false>
 int launch(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& e, int num_sms,
            cudaStream_t s) {
-    return f.cg == 2 ? dense_launch<2, A_MN, B_MN, TURNS, Epilogue>(ma, mb, a, e, num_sms, s)
-                     : dense_launch<1, A_MN, B_MN, TURNS, Epilogue>(ma, mb, a, e, num_sms, s);
+    if constexpr (!TURNS) {
+        if (f.dual) return dense_launch<2, A_MN, B_MN, false, true, Epilogue>(ma, mb, a, e, num_sms, s);
+    }
+    return f.cg == 2 ? dense_launch<2, A_MN, B_MN, TURNS, false, Epilogue>(ma, mb, a, e, num_sms, s)
+                     : dense_launch<1, A_MN, B_MN, TURNS, false, Epilogue>(ma, mb, a, e, num_sms, s);
 }
 
 template <typename T>
