@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         }
         mbar_init(&fin, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (a.zero && blockIdx.x == 0) *a.zero = 0;
     }
     if (warp == 1) tmem_alloc<CG>(&tmem_base, 512);
     tc_fence_before();
@@ -312,6 +311,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if constexpr (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    after_previous();
+    let_next_start();
+    if (a.zero && blockIdx.x == 0 && t == 0) *a.zero = 0;
 
     // a device count of rows shortens M or K; each role finds the same items
     int n_mt = a.n_mt, rows = 0x7fffffff;
@@ -521,22 +523,7 @@ int dense_launch(const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& 
     constexpr auto f = k_dense<CG, A_MN, B_MN, TURNS, DUAL, Epilogue>;
     if (!allow_smem<f>(kDenseSmem)) return SNK_ERR_CUDA;
     const int64_t items = (int64_t)a.n_mt * a.n_nt * a.splits;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));
-    c.blockDim = dim3(kDenseThreads);
-    c.dynamicSmemBytes = kDenseSmem;
-    c.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    c.attrs = at;
-    c.numAttrs = CG == 1 ? 0 : 1;
-    if (cudaLaunchKernelEx(&c, f, ma, mb, a, ea) != cudaSuccess) {
-        cudaGetLastError();
-        return SNK_ERR_CUDA;
-    }
-    return SNK_OK;
+    return launch_after(f, (unsigned)(CG * std::min<int64_t>(items, num_sms / CG)), kDenseThreads, kDenseSmem, CG, s, ma, mb, a, ea);
 }
 
 }  // namespace snk

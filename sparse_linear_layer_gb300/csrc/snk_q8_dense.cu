@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     if constexpr (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    after_previous();
+    let_next_start();
     const int items = a.n_mt * a.n_nt * a.splits;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(256) k_q8_scales(const float* __restrict__ sa,
                                                    const float* __restrict__ sb, int64_t N, int64_t padded_n, float* __restrict__ tb,
                                                    int n_g) {
     __shared__ float sm[32][33];
+    let_next_start();
     const bool second = blockIdx.y == 1;
     const float* src = second ? sb : sa;
     float* dst = second ? tb : ta;
@@ -370,6 +373,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_q8_join(const float* __restrict__ slab, int splits, int64_t M, int64_t N,
                                                  const float* __restrict__ bias, T* __restrict__ y) {
     const int64_t n = M * N;
+    after_previous();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         float v = 0.f;
         for (int s = 0; s < splits; ++s) v += __ldg(slab + s * n + i);
@@ -421,6 +425,8 @@ template <int NT, typename T>
 __global__ void __launch_bounds__(32 * kRowsWarps, NT == 1 ? 4 : 2) k_q8_rows(const Q8RowsArgs a) {
     __shared__ float part[kRowsWarps][16][8 * NT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, r = lane >> 2;
+    after_previous();
+    let_next_start();
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t nr0 = n0 + r, nr1 = n0 + r + 8;
     const uint8_t* b0 = a.b + min(nr0, a.N - 1) * a.ldb;
@@ -489,6 +495,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, NT == 1 ? 4 : 2) k_q8_rows(co
 // Codes [rows, cols] at row stride ld, with rows of whole 16-byte chunks and zeros behind the columns.
 __global__ void __launch_bounds__(256) k_q8_pad(const uint8_t* __restrict__ src, int64_t ld, uint8_t* __restrict__ dst, int64_t rows,
                                                 int64_t cols, int64_t to) {
+    let_next_start();
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8)
         for (int64_t c = threadIdx.x & 31; c < to; c += 32) dst[r * to + c] = c < cols ? src[r * ld + c] : (uint8_t)0;
 }
@@ -605,22 +612,8 @@ int launch_dense(const CUtensorMap (&m)[5], const Q8DenseArgs& a, int num_sms, c
     constexpr auto f = k_q8_dense<CG, BN, ROWS>;
     if (!allow_smem<f>(kQ8Smem)) return SNK_ERR_CUDA;
     const int64_t items = (int64_t)a.n_mt * a.n_nt * a.splits;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, num_sms / CG)));
-    c.blockDim = dim3(kQ8Threads);
-    c.dynamicSmemBytes = kQ8Smem;
-    c.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    c.attrs = at;
-    c.numAttrs = CG == 1 ? 0 : 1;
-    if (cudaLaunchKernelEx(&c, f, m[0], m[1], m[2], m[3], m[4], a) != cudaSuccess) {
-        cudaGetLastError();
-        return SNK_ERR_CUDA;
-    }
-    return SNK_OK;
+    return launch_after(f, (unsigned)(CG * std::min<int64_t>(items, num_sms / CG)), kQ8Threads, kQ8Smem, CG, s, m[0], m[1], m[2], m[3],
+                        m[4], a);
 }
 template <bool ROWS>
 int launch_dense(const Q8Plan& p, const CUtensorMap (&m)[5], const Q8DenseArgs& a, int num_sms, cudaStream_t s) {
@@ -632,15 +625,13 @@ int launch_dense(const Q8Plan& p, const CUtensorMap (&m)[5], const Q8DenseArgs& 
 template <typename T>
 int launch_rows(const Q8RowsArgs& r, cudaStream_t s) {
     const unsigned blocks = (unsigned)ceil_div(r.N, 16);
-    if (r.M <= 8) k_q8_rows<1, T><<<blocks, 32 * kRowsWarps, 0, s>>>(r);
-    else k_q8_rows<2, T><<<blocks, 32 * kRowsWarps, 0, s>>>(r);
-    return launched();
+    return r.M <= 8 ? launch_after(k_q8_rows<1, T>, blocks, 32 * kRowsWarps, 0, 1, s, r)
+                    : launch_after(k_q8_rows<2, T>, blocks, 32 * kRowsWarps, 0, 1, s, r);
 }
 template <typename T>
 int launch_join(const Q8Plan& p, int64_t M, int64_t N, const float* bias, void* y, int num_sms, cudaStream_t s) {
-    k_q8_join<T><<<(unsigned)std::min<int64_t>(ceil_div(M * N, 256), 8 * num_sms), 256, 0, s>>>(p.slab, p.splits, M, N, bias,
-                                                                                               static_cast<T*>(y));
-    return launched();
+    return launch_after(k_q8_join<T>, (unsigned)std::min<int64_t>(ceil_div(M * N, 256), 8 * num_sms), 256, 0, 1, s, p.slab, p.splits, M, N,
+                        bias, static_cast<T*>(y));
 }
 
 int bad_product(int64_t M, int64_t N, int64_t K) {

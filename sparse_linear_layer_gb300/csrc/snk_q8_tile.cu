@@ -52,6 +52,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
     __shared__ uint64_t full[BUFS];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int64_t n_tiles = a.tiles_r * a.tiles_c;
+    after_previous();
+    let_next_start();
     auto fetch = [&](int64_t id, int b) {
         const int64_t tr = id / a.tiles_c, tc = id - tr * a.tiles_c;
         mbar_expect_tx(&full[b], BYTES);
@@ -251,6 +253,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
 // sums[c] = the parts of column c, in order.
 __global__ void __launch_bounds__(256) k_q8_sums(const float* __restrict__ part, int64_t tiles, int64_t cols, float* __restrict__ sums) {
     __shared__ float sm[8][33];
+    after_previous();
+    let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
@@ -270,8 +274,7 @@ int launch_tile(const CUtensorMap& map, const TileArgs& a, int num_sms, cudaStre
     constexpr auto f = k_q8_tile<T, BLOCKS, LOAD>;
     if (!allow_smem<f>(kTileSmem<T, LOAD>)) return SNK_ERR_CUDA;
     const unsigned blocks = (unsigned)std::min<int64_t>(a.tiles_r * a.tiles_c, 2 * num_sms);
-    f<<<blocks, kTileThreads, kTileSmem<T, LOAD>, s>>>(map, a);
-    return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
+    return launch_after(f, blocks, kTileThreads, kTileSmem<T, LOAD>, 1, s, map, a);
 }
 template <typename T>
 int launch_tile(const TileArgs& a, bool blocks, cudaStream_t s) {
@@ -333,8 +336,7 @@ int snk_q8_pack_both(const void* x, int dtype, int64_t rows, int64_t cols, void*
     const TileArgs a{x, rows, cols, ceil_div(rows, kTile), ceil_div(cols, kTile), static_cast<uint8_t*>(codes),
                      static_cast<uint8_t*>(codes_t), ld, ld_t, scales, scales_t, sums ? static_cast<float*>(scratch) : nullptr};
     if (int st = run_tile(a, dtype, false, s); st != SNK_OK || !sums) return st;
-    k_q8_sums<<<(unsigned)ceil_div(cols, 32), 256, 0, s>>>(a.part, a.tiles_r, cols, sums);
-    return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA;
+    return launch_after(k_q8_sums, (unsigned)ceil_div(cols, 32), 256, 0, 1, s, a.part, a.tiles_r, cols, sums);
 }
 
 int snk_q8_pack_blocks(const void* w, int dtype, int64_t rows, int64_t cols, void* codes, int64_t ld, float* scales,

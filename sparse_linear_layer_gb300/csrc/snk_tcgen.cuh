@@ -166,4 +166,31 @@ bool allow_smem(int bytes) {
     return true;
 }
 
+// A kernel launched by launch_after may be set up while the one before it in the stream still
+// runs; after_previous() waits until that has finished and its writes are seen, and stands
+// before the first access to device memory.  let_next_start() allows the next kernel's set-up.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+int launch_after(void (*f)(P...), unsigned grid, unsigned block, int smem, int cluster, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = (size_t)smem;
+    c.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&c, f, static_cast<P>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return SNK_ERR_CUDA;
+    }
+    return SNK_OK;
+}
+
 }  // namespace snk

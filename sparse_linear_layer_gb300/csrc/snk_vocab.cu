@@ -250,6 +250,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
     __shared__ int before_s[8], all_s[8], list[kGatherRows];
     __shared__ int mine_s;
+    after_previous();
+    let_next_start();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int64_t r0 = (int64_t)blockIdx.x * kGatherRows;
     int before = 0, all = 0;
@@ -339,6 +341,8 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(256) k_vocab_pad(const T* __restrict__ src, T* __restrict__ dst, int64_t rows, int64_t cols,
                                                    int64_t ld) {
+    after_previous();
+    let_next_start();
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8)
         for (int64_t c = threadIdx.x & 31; c < ld; c += 32) dst[r * ld + c] = c < cols ? src[r * cols + c] : from_f32<T>(0.f);
 }
@@ -369,6 +373,8 @@ __global__ void __launch_bounds__(256) k_vocab_finish(const FinishArgs a) {
     __shared__ float row_loss[32];
     __shared__ int row_in[32];
     __shared__ bool last;
+    after_previous();
+    let_next_start();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int R = a.per_block, W = 256 / R;   // threads of a row
     const int64_t n = a.count ? (int64_t)*a.count : a.rows;
@@ -493,6 +499,8 @@ __global__ void __launch_bounds__(256) k_vocab_dx(const float* __restrict__ slab
                                                   const int32_t* __restrict__ at, const uint32_t* most, int64_t rows, int64_t cols,
                                                   T* __restrict__ dx) {
     __shared__ F8 part[WARPS > 1 ? WARPS : 1][WARPS > 1 ? 32 : 1];
+    after_previous();
+    let_next_start();
     const float scale = 1.f / (GradEpilogue<T>::grad_factor(*most) * kDzScale);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = WARPS > 1 ? warp : 0;
     constexpr int E = WARPS > 1 ? 32 : 256;   // elements (of 8 columns) of a block
@@ -538,7 +546,6 @@ __global__ void __launch_bounds__(256) k_vocab_dx(const float* __restrict__ slab
 // ---- host -----------------------------------------------------------------------------
 
 int64_t up(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
-int launched() { return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA; }
 
 // A product's tile and ranges of K: the form whose waves take least by this account.  A stage
 // takes its MMAs (us as measured, fewer columns than 128 at the same cost) or, where all SMs are
@@ -697,9 +704,8 @@ int launch(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const De
 
 template <typename T>
 int pad_weight(const Shape& h, const void* w, void* wc, int num_sms, cudaStream_t s) {
-    k_vocab_pad<T><<<(unsigned)std::min<int64_t>(ceil_div(h.vocab, 8), 8 * num_sms), 256, 0, s>>>(
-        static_cast<const T*>(w), static_cast<T*>(wc), h.vocab, h.cols, h.ld);
-    return launched();
+    return launch_after(k_vocab_pad<T>, (unsigned)std::min<int64_t>(ceil_div(h.vocab, 8), 8 * num_sms), 256, 0, 1, s,
+                        static_cast<const T*>(w), static_cast<T*>(wc), h.vocab, h.cols, h.ld);
 }
 
 template <typename T>
@@ -725,8 +731,7 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
         r.count = p.count;
         r.loss = row_loss;
         r.lse_zero = lse;
-        k_vocab_rows<T><<<(unsigned)ceil_div(h.rows, kGatherRows), 256, 0, s>>>(r);
-        if (int st = launched(); st != SNK_OK) return st;
+        if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, kGatherRows), 256, 0, 1, s, r); st != SNK_OK) return st;
     }
     const void* wt = w;
     if (h.pads()) {
@@ -768,8 +773,7 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
     f.sums = p.sums;
     f.arrived = p.arrived;
     f.out = loss;
-    k_vocab_finish<T><<<(unsigned)p.blocks, 256, 0, s>>>(f);
-    return launched();
+    return launch_after(k_vocab_finish<T>, (unsigned)p.blocks, 256, 0, 1, s, f);
 }
 
 template <typename T>
@@ -810,13 +814,10 @@ int backward(const Shape& h, const BackwardPlan& p, const void* wt, void* dx, vo
     if (dx) {
         const int64_t n = h.rows * (h.ld / 8);
         T* out = static_cast<T*>(dx);
-        if (p.x.splits > 8)
-            k_vocab_dx<T, 8><<<(unsigned)std::min<int64_t>(ceil_div(n, 32), 64 * num_sms), 256, 0, s>>>(
-                p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, out);
-        else
-            k_vocab_dx<T, 1><<<(unsigned)std::min<int64_t>(ceil_div(n, 256), 16 * num_sms), 256, 0, s>>>(
-                p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, out);
-        return launched();
+        return p.x.splits > 8 ? launch_after(k_vocab_dx<T, 8>, (unsigned)std::min<int64_t>(ceil_div(n, 32), 64 * num_sms), 256, 0, 1, s,
+                                             p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, out)
+                              : launch_after(k_vocab_dx<T, 1>, (unsigned)std::min<int64_t>(ceil_div(n, 256), 16 * num_sms), 256, 0, 1, s,
+                                             p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, out);
     }
     return SNK_OK;
 }
@@ -848,8 +849,7 @@ int backward_rows(const Shape& h, const BackwardPlan& p, const void* x, const vo
     r.lse2 = p.lse2;
     r.g = p.g;
     r.most = p.most;
-    k_vocab_rows<T><<<(unsigned)ceil_div(h.rows, kGatherRows), 256, 0, s>>>(r);
-    if (int st = launched(); st != SNK_OK) return st;
+    if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, kGatherRows), 256, 0, 1, s, r); st != SNK_OK) return st;
     const void* wt = w;
     if (h.pads()) {
         if (int st = pad_weight<T>(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
