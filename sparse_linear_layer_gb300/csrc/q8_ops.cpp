@@ -599,12 +599,11 @@ PyObject* op_vocab_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 using torch::autograd::AutogradContext;
 using torch::autograd::variable_list;
 
-// A backward pass: f's errors as exceptions that the engine passes on, and no second derivative.
+// A backward pass: f's errors as exceptions that the engine passes on, and no second derivative
+// (gradients are on in a backward pass only where one is asked for: create_graph).
 template <typename F>
-variable_list backward_pass(const variable_list& grads, F f) {
-    for (const auto& t : grads)
-        if (at::GradMode::is_enabled() && t.defined() && t.requires_grad())
-            throw std::runtime_error("this operation has no second derivative");
+variable_list backward_pass(F f) {
+    if (at::GradMode::is_enabled()) throw std::runtime_error("this operation has no second derivative (create_graph)");
     try {
         return f();
     } catch (const Status& s) {
@@ -627,7 +626,7 @@ struct HeadFunction : torch::autograd::Function<HeadFunction> {
         return loss;
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
-        return backward_pass(grads, [&]() -> variable_list {
+        return backward_pass([&]() -> variable_list {
             if (!grads[0].defined()) return {{}, {}, {}, {}, {}};
             const auto saved = ctx->get_saved_variables();
             Head h(saved[0], saved[1], saved[2], ctx->saved_data["ignore"].toInt(), ctx->saved_data["reduction"].toInt());
@@ -734,7 +733,7 @@ struct LayerFunction : torch::autograd::Function<LayerFunction> {
         return o.y;
     }
     static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
-        return backward_pass(grads, [&]() -> variable_list {
+        return backward_pass([&]() -> variable_list {
             if (!grads[0].defined()) return {{}, {}, {}, {}, {}};
             const int64_t rows = ctx->saved_data["rows"].toInt(), cols = ctx->saved_data["cols"].toInt();
             const int64_t out = ctx->saved_data["out"].toInt();

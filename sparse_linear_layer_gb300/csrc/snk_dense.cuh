@@ -385,10 +385,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int i0 = (int)((int64_t)n_k * it.split / a.splits), i1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
+                bool here = false;   // the next stage has been waited for
                 for (int turn = 0; turn < turns && ok; ++turn, q += SUBS) {
                     const int k0 = i0 + (i1 - i0) * turn / turns, k1 = i0 + (i1 - i0) * (turn + 1) / turns;
                     const int ab = q & 1;
-                    if ((q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1)) || (k0 < k1 && !mbar_wait(&full[r.slot], r.parity))) {
+                    if ((q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1)) || (k0 < k1 && !here && !mbar_wait(&full[r.slot], r.parity))) {
                         ok = false;
                         break;
                     }
@@ -413,7 +414,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                                 dense_mma<CG>(d + sub * kDenseN, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
                                 // the next stage is waited for while the tensor cores are busy (a wait
                                 // costs a hundred cycles even when there is nothing to wait for)
-                                if (sub == SUBS - 1 && kk == 1 && k + 1 < k1 && !mbar_wait(&full[r.slot], r.parity)) ok = false;
+                                if (sub == SUBS - 1 && kk == 1 && k + 1 < i1) {
+                                    here = true;
+                                    if (!mbar_wait(&full[r.slot], r.parity)) ok = false;
+                                }
                             }
                         }
                         dense_commit<CG>(&empty[s]);

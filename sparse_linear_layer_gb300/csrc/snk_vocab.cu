@@ -28,11 +28,13 @@ namespace snk {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kGatherRows = 16;     // rows per block of k_vocab_rows
+constexpr int kGatherRows = 256;    // rows per block of k_vocab_rows at most
 constexpr int kDirectRows = 128;    // up to these the forward reads x itself: one row tile either way
 constexpr float kDzScale = 8192.f;  // 2^13
-// Stages of an accumulator's turn in the loss (64 MMA steps, whose additions truncate): at 4096
-// columns the logits of one accumulator left the mean loss off by LOSS_ERR_ONE, turns by LOSS_ERR.
+// Stages of an accumulator's turn in the loss: 64 MMA steps, whose additions truncate, towards
+// zero. At 4096 columns one accumulator leaves the mean loss off by 1.2e-6 of it, turns of 32
+// stages by 6e-7, of 16 by 2.9e-7 (768 columns, one turn: 1.7e-7); one accumulator and dual tiles
+// would take 858 us for 2867 x 4096 x 65536, these take 1019.
 constexpr int kTurnStages = 16;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -240,12 +242,14 @@ struct RowsArgs {
     const float* lse;                 // [rows]
     const float* dloss;               // [rows] (reduction 0) or [1]
     int reduction;
+    int per_block;                    // rows of a block
     float* lse2;                      // [rows]
     float* g;                         // [rows]
     uint32_t* most;                   // cleared before; the largest finite |g|'s bits
 };
-// A block takes kGatherRows rows; how many count before it and in all it finds out by
-// itself (targets are 8 bytes a row: a second launch would cost more up to about 10^5 rows).
+// A block takes a.per_block rows; how many count before it and in all it finds out by itself:
+// targets are 8 bytes a row, and the more rows there are the more a block takes (gather_rows), so
+// that all blocks together read 4096 rows' worth for each row at most.
 template <typename T>
 __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
     __shared__ int before_s[8], all_s[8], list[kGatherRows];
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
     after_previous();
     let_next_start();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int64_t r0 = (int64_t)blockIdx.x * kGatherRows;
+    const int64_t r0 = (int64_t)blockIdx.x * a.per_block;
     int before = 0, all = 0;
 #pragma unroll 4
     for (int64_t r = t; r < a.rows; r += 256) {
@@ -277,8 +281,8 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
     if (warp == 0) {   // this block's rows, in order
         int n = 0;
         uint32_t most = 0;
-        for (int i = 0; i < kGatherRows; i += 32) {
-            const int64_t r = i + lane < kGatherRows ? r0 + i + lane : a.rows;
+        for (int i = 0; i < a.per_block; i += 32) {
+            const int64_t r = i + lane < a.per_block ? r0 + i + lane : a.rows;
             const int64_t tg = r < a.rows ? a.target[r] : a.ignore;
             const bool in = r < a.rows && tg != a.ignore;
             const uint32_t mask = __ballot_sync(0xffffffffu, in);
@@ -546,6 +550,9 @@ __global__ void __launch_bounds__(256) k_vocab_dx(const float* __restrict__ slab
 // ---- host -----------------------------------------------------------------------------
 
 int64_t up(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
+// Rows of a block of k_vocab_rows: few, so that the copies spread (8192 x 768: 64 rows 21 us, 16 rows 10),
+// but not more than 4096 blocks that all read all targets until a block has its most.
+int gather_rows(int64_t rows) { return (int)std::min<int64_t>(kGatherRows, std::max<int64_t>(16, up(ceil_div(rows, 4096), 16))); }
 
 // A product's tile and ranges of K: the form whose waves take least by this account.  A stage
 // takes its MMAs (us as measured, fewer columns than 128 at the same cost) or, where all SMs are
@@ -724,6 +731,7 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
         r.vocab = h.vocab;
         r.ld = h.ld;
         r.padded = h.padded;
+        r.per_block = gather_rows(h.rows);
         r.xc = p.xc;
         r.index = p.index;
         r.at = p.at;
@@ -731,7 +739,7 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
         r.count = p.count;
         r.loss = row_loss;
         r.lse_zero = lse;
-        if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, kGatherRows), 256, 0, 1, s, r); st != SNK_OK) return st;
+        if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, r.per_block), 256, 0, 1, s, r); st != SNK_OK) return st;
     }
     const void* wt = w;
     if (h.pads()) {
@@ -838,6 +846,7 @@ int backward_rows(const Shape& h, const BackwardPlan& p, const void* x, const vo
     r.vocab = h.vocab;
     r.ld = h.ld;
     r.padded = h.padded;
+    r.per_block = gather_rows(h.rows);
     r.xc = p.xc;
     r.index = p.index;
     r.at = p.at;
@@ -849,7 +858,7 @@ int backward_rows(const Shape& h, const BackwardPlan& p, const void* x, const vo
     r.lse2 = p.lse2;
     r.g = p.g;
     r.most = p.most;
-    if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, kGatherRows), 256, 0, 1, s, r); st != SNK_OK) return st;
+    if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, r.per_block), 256, 0, 1, s, r); st != SNK_OK) return st;
     const void* wt = w;
     if (h.pads()) {
         if (int st = pad_weight<T>(h, w, p.wc, num_sms, s); st != SNK_OK) return st;

@@ -81,7 +81,7 @@ def test_packing_of_what_has_no_scale():
 
 
 SHAPES = [(1, 1, 1), (1, 2304, 768), (3, 100, 17), (8, 64, 1000), (16, 130, 2000), (17, 64, 128), (100, 200, 4096),
-          (128, 1001, 130), (129, 300, 1000), (333, 1001, 1000), (600, 2000, 300), (2600, 2100, 260)]
+          (128, 1001, 130), (129, 300, 1000), (333, 1001, 1000), (600, 2000, 300), (2600, 2100, 260), (1000, 700, 20000), (500, 500, 6400)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
@@ -141,6 +141,26 @@ def test_nan_codes_reach_their_outputs_only():
         y = q8.matmul(a, b)
         nan = y.isnan()
         assert bool(nan[2].all()) and bool(nan[:, 50].all()) and int(nan.sum()) == 90 + rows - 1
+
+
+def test_offsets_past_32_bits():
+    """An output of more than 2^31 elements, written and checked at both ends; codes as many."""
+    a, b = q8.pack(matrix(50_000, 128), "e4m3", 128), q8.pack_blocks(matrix(45_056, 128, seed=1))
+    y = q8.matmul(a, b, dtype=torch.bfloat16)
+    vb = dense_ref.values(b.codes, b.scales, True)
+    for r in (slice(0, 3), slice(25_000, 25_003), slice(49_997, 50_000)):
+        check_product(y[r], dense_ref.values(a.codes[r], a.scales[r]), vb)
+    del y, vb
+    x = torch.randn(1_100_000, 2048, device="cuda", dtype=torch.bfloat16)
+    _, xt = q8.pack_both(x)
+    part = slice(1_099_776, 1_100_000)   # (the last two groups of rows, the second one short)
+    want = q8.pack(x[part].T.contiguous(), "e4m3", 128)
+    assert torch.equal(xt.codes[:, part].contiguous().view(torch.uint8), bits(want))
+    assert torch.equal(xt.scales[:, -2:], want.scales)
+    w8 = q8.pack_blocks(x)
+    y = q8.matmul(q8.pack(matrix(3, 2048), "e4m3", 128), w8)
+    tail = dense_ref.values(w8.codes[part], w8.scales[-2:], True)
+    check_product(y[:, part], dense_ref.values(*(lambda q: (q.codes, q.scales))(q8.pack(matrix(3, 2048), "e4m3", 128))), tail)
 
 
 def test_more_dimensions_streams_and_empty():
@@ -228,6 +248,15 @@ def test_linear_asks_only_for_what_is_needed():
         one = [v.detach().requires_grad_(k == i) for k, v in enumerate((x, w, b))]
         got, = torch.autograd.grad(dense.linear_q8(*one).square().sum(), one[i])
         assert torch.equal(got, grads[i])
+    assert torch.equal(dense.linear_q8(x[0], w, b), dense.linear_q8(x[:1], w, b)[0])
+    assert torch.equal(dense.linear_q8(x.view(4, 10, 100), w, b), dense.linear_q8(x, w, b).view(4, 10, 50))
+    wide = torch.zeros(40, 200, device="cuda")
+    wide[:, ::2] = x
+    wide.requires_grad_()
+    dwide, = torch.autograd.grad(dense.linear_q8(wide[:, ::2], w, b).square().sum(), wide)
+    assert torch.equal(dwide[:, ::2], grads[0]) and bool((dwide[:, 1::2] == 0).all())
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad(dense.linear_q8(leaves[0], w, b).sum(), leaves[0], create_graph=True)
     xe = torch.empty(0, 100, device="cuda", requires_grad=True)
     ye = dense.linear_q8(xe, leaves[1], leaves[2])
     dx, dw, db = torch.autograd.grad(ye.sum(), (xe, leaves[1], leaves[2]))

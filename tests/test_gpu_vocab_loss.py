@@ -87,6 +87,89 @@ def test_loss_and_gradients(rows, cols, vocab, dtype):
     assert bool((dx[t == -100] == 0).all())
 
 
+# several row tiles and pairs of them, columns for one accumulator and for several
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,cols,vocab", [(2, 1, 3), (2000, 640, 30000), (1500, 1100, 20000), (1030, 2056, 9001)])
+def test_larger_shapes(rows, cols, vocab, dtype):
+    x, w, t = case(rows, cols, vocab, dtype, ignored=0.1)
+    t[0] = 1
+    x.requires_grad_()
+    w.requires_grad_()
+    each = dense.linear_cross_entropy(x, w, t, reduction="none")
+    check_loss(each.detach(), x.detach(), w.detach(), t)
+    g = torch.randn(rows, device="cuda")
+    check_gradients(*torch.autograd.grad(each, (x, w), g), x.detach(), w.detach(), t, g)
+
+
+def test_offsets_past_32_bits():
+    """A weight and its gradient of more than 2^31 elements, and a batch whose logits have as many:
+    sampled rows against 64 bits."""
+    rows, cols, vocab = 3000, 4096, 800_000
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(rows, cols, device="cuda", generator=g).bfloat16()
+    w = torch.empty(vocab, cols, device="cuda", dtype=torch.bfloat16)
+    for i in range(0, vocab, 100_000):
+        w[i:i + 100_000] = torch.randn(100_000, cols, device="cuda", generator=g) / 64
+    t = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    t[rows - 1], t[0] = vocab - 1, 0
+    x.requires_grad_()
+    w.requires_grad_()
+    each = dense.linear_cross_entropy(x, w, t, reduction="none")
+    dx, dw = torch.autograd.grad(each.sum(), (x, w))
+    pick = torch.tensor([0, 1, 1500, rows - 1], device="cuda")
+    xs, z = x.detach()[pick].double(), torch.empty(4, vocab, device="cuda", dtype=torch.float64)
+    for i in range(0, vocab, 100_000):
+        z[:, i:i + 100_000] = xs @ w.detach()[i:i + 100_000].double().T
+    lse = z.logsumexp(1)
+    want = lse - z.gather(1, t[pick][:, None])[:, 0]
+    assert (each.detach()[pick].double() - want).abs().max() < 1e-4
+    p = (z - lse[:, None]).exp()
+    p[torch.arange(4), t[pick]] -= 1
+    want_dx = sum(p[:, i:i + 100_000] @ w.detach()[i:i + 100_000].double() for i in range(0, vocab, 100_000))
+    assert ((dx[pick].double() - want_dx).norm(dim=1) <= 4 * UNIT[torch.bfloat16] * want_dx.norm(dim=1)).all()
+    cols_at = torch.tensor([0, 5, vocab // 2, vocab - 1], device="cuda")
+    zc = x.detach().double() @ w.detach()[cols_at].double().T
+    # every row's lse from the loss itself, which is checked above on a sample
+    at = (x.detach().double() * w.detach()[t].double()).sum(1)
+    pc = (zc - (each.detach().double() + at)[:, None]).exp()
+    for k, c in enumerate(cols_at.tolist()):
+        pc[t == c, k] -= 1
+    want_dw = pc.T @ x.detach().double()
+    assert ((dw[cols_at].double() - want_dw).norm(dim=1) <= 4 * UNIT[torch.bfloat16] * want_dw.norm(dim=1)).all()
+
+
+def test_another_ignored_value_and_strided_inputs():
+    x, w, t = case(60, 48, 90, torch.bfloat16, ignored=0)
+    t[:10] = 5
+    want = dense_ref.loss(x, w, t, ignore=5)[0]
+    got = dense.linear_cross_entropy(x, w, t, ignore=5, reduction="none")
+    assert bool((got[:10] == 0).all()) and (got.double() - want).abs().max() < 1e-4
+    # gradients reach the storage that strided inputs are views of
+    base = torch.zeros(48, 120, device="cuda", dtype=torch.bfloat16)
+    base[:, ::2] = x.T
+    base.requires_grad_()
+    wide = torch.zeros(90, 96, device="cuda", dtype=torch.bfloat16)
+    wide[:, 48:] = w
+    wide.requires_grad_()
+    leaf_x, leaf_w = x.clone().requires_grad_(), w.clone().requires_grad_()
+    dx, dw = torch.autograd.grad(dense.linear_cross_entropy(leaf_x, leaf_w, t), (leaf_x, leaf_w))
+    db, dwide = torch.autograd.grad(dense.linear_cross_entropy(base[:, ::2].T, wide[:, 48:], t.repeat(2)[::1][:60]), (base, wide))
+    assert torch.equal(db[:, ::2], dx.T) and bool((db[:, 1::2] == 0).all())
+    assert torch.equal(dwide[:, 48:], dw) and bool((dwide[:, :48] == 0).all())
+
+
+def test_no_second_derivative():
+    x, w, t = case(10, 32, 40, torch.bfloat16)
+    x.requires_grad_()
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad(dense.linear_cross_entropy(x, w, t), x, create_graph=True)
+    loss = dense.linear_cross_entropy(x, w.requires_grad_(), t)
+    with torch.no_grad():
+        w.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
 @pytest.mark.parametrize("rows", [5, 300])
 def test_reductions_and_upstream_gradients(rows):
     x, w, t = case(rows, 96, 1000, torch.bfloat16)
