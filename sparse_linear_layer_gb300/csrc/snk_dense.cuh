@@ -6,10 +6,11 @@
 // brings 128-byte wide boxes with the 128-byte swizzle.  A tile is 128 CG rows by `bn`
 // columns, CG the CTAs that share it: a pair (CG = 2) runs one MMA of 256 rows over both
 // SMs, each holding its 128 rows of A and half of B's columns, so that B crosses the L2
-// once per pair.  Persistent CTAs, ten warps:
+// once per pair.  Persistent CTAs, eleven warps:
 //   warp 0     TMA loads into a ring of stages (64 columns of K each);
-//   warp 1     issues the MMAs (one thread, of the pair's first CTA) and owns the TMEM
-//              allocation, two accumulators of up to 256 columns that take turns;
+//   warps 1, 10  issue the MMAs (a thread each, of the pair's first CTA), one the even
+//              accumulator turns and one the odd ones; warp 1 owns the TMEM allocation, two
+//              accumulators of up to 256 columns that take turns;
 //   warps 2-9  the epilogue: warp w reads the TMEM lanes 32 (w % 4) .. + 31 and, by
 //              w < 6 or not, the first or second half of the columns.
 // Every wait is bounded (kTcWaitCycles); a role whose wait ran out stops, waits for the
@@ -25,7 +26,7 @@ namespace snk {
 constexpr int kDenseM = 128;             // rows of a tile per CTA (TMEM lanes)
 constexpr int kDenseN = 256;             // columns of a tile at most
 constexpr int kDenseK = 64;              // columns of K per stage: 128 bytes
-constexpr int kDenseThreads = 320;
+constexpr int kDenseThreads = 352;
 constexpr int kDenseEpilogueWarps = 8;
 constexpr int kDenseBoxBytes = 64 * 128;   // an MN-major box: 64 rows of K, 64 columns
 constexpr int kDenseStages = 8;          // at most
@@ -264,6 +265,11 @@ struct Stages {
             parity ^= 1;
         }
     }
+    __device__ __forceinline__ void skip(int count) {
+        const int laps = (slot + count) / n;
+        slot += count - laps * n;
+        parity ^= (uint32_t)laps & 1;
+    }
 };
 // The stages that a producer filled last have landed.
 __device__ __forceinline__ void drain_last(uint64_t* full, const Stages& r, bool all) {
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     constexpr int S = kDenseStages, SUBS = DUAL ? 2 : 1;
     extern __shared__ __align__(1024) unsigned char dense_raw[];
     unsigned char* sm = dense_raw + ((1024 - (smem_u32(dense_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin;
+    __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin[2], hand[2];
     __shared__ uint32_t tmem_base;
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -301,8 +307,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accf[i], 1);
             mbar_init(&acce[i], kDenseEpilogueWarps * CG);
+            mbar_init(&fin[i], 1);
+            mbar_init(&hand[i], 1);
         }
-        mbar_init(&fin, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc<CG>(&tmem_base, 512);
@@ -376,25 +383,41 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             }
             if (!ok && rank == 0) drain_last(full, r, used);   // (the other CTA's copies among them)
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 10) {
+        // One thread for all turns left the tensor cores idle for 850 cycles where they changed the
+        // accumulator: its waits and commits, with nothing queued behind the last MMA.  The other
+        // thread makes its waits beside the last MMAs of a turn.  It is told when to (hand): a
+        // barrier's phase is known by its parity only, so nobody may wait for one while an earlier
+        // phase of that barrier is still open.  The word comes when all stages but the turn's last
+        // have been waited for; the next turn's first stage is then at most the second in the ring
+        // that is open, and its accumulators' earlier phases are past.
         if (lane == 0 && rank == 0) {
+            const uint32_t mine = warp == 1 ? 0 : 1;
             bool ok = true;
             Stages r(a.stages);
-            uint32_t q = 0;   // accumulators filled
+            uint32_t q = 0;   // accumulators filled, by both threads
+            uint32_t u = 0;   // turns
             const int turns = TURNS ? a.turns : 1;
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int i0 = (int)((int64_t)n_k * it.split / a.splits), i1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
-                bool here = false;   // the next stage has been waited for
-                for (int turn = 0; turn < turns && ok; ++turn, q += SUBS) {
+                for (int turn = 0; turn < turns; ++turn, ++u, q += SUBS) {
                     const int k0 = i0 + (i1 - i0) * turn / turns, k1 = i0 + (i1 - i0) * (turn + 1) / turns;
+                    if ((u & 1) != mine) {
+                        r.skip(k1 - k0);
+                        continue;
+                    }
                     const int ab = q & 1;
-                    if ((q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1)) || (k0 < k1 && !here && !mbar_wait(&full[r.slot], r.parity))) {
+                    if ((u > 0 && !mbar_wait(&hand[mine], ((u - 1) >> 1) & 1)) ||
+                        (q >= 2 && !mbar_wait(&acce[ab], ((q >> 1) - 1) & 1)) || (k0 < k1 && !mbar_wait(&full[r.slot], r.parity))) {
                         ok = false;
                         break;
                     }
                     const uint32_t d = tmem + ab * kDenseN;
+                    const int last = max(k0, k1 - 2);
+                    if (k0 == k1) mbar_arrive(&hand[mine ^ 1]);
                     for (int k = k0; k < k1; ++k) {
+                        if (k == last) mbar_arrive(&hand[mine ^ 1]);
                         tc_fence_after();
                         const int s = r.slot;
                         const uint32_t sa = smem_u32(sm + s * stage), sb = sa + SUBS * a_bytes;
@@ -414,24 +437,20 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                                 dense_mma<CG>(d + sub * kDenseN, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
                                 // the next stage is waited for while the tensor cores are busy (a wait
                                 // costs a hundred cycles even when there is nothing to wait for)
-                                if (sub == SUBS - 1 && kk == 1 && k + 1 < i1) {
-                                    here = true;
-                                    if (!mbar_wait(&full[r.slot], r.parity)) ok = false;
-                                }
+                                if (sub == SUBS - 1 && kk == 1 && k + 1 < k1 && !mbar_wait(&full[r.slot], r.parity)) ok = false;
                             }
                         }
                         dense_commit<CG>(&empty[s]);
                         if (!ok) break;
                     }
-                    if (ok) {
-                        dense_commit<CG>(&accf[ab]);
-                        if constexpr (DUAL) dense_commit<CG>(&accf[1]);
-                    }
+                    if (!ok) break;
+                    dense_commit<CG>(&accf[ab]);
+                    if constexpr (DUAL) dense_commit<CG>(&accf[1]);
                 }
             }
             if (!ok) {   // no MMA may still run when the memory is given back
-                dense_commit<CG>(&fin);
-                mbar_wait(&fin, 0, kTcDrainCycles);
+                dense_commit<CG>(&fin[mine]);
+                mbar_wait(&fin[mine], 0, kTcDrainCycles);
             }
         }
     } else {

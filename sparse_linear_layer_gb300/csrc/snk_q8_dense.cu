@@ -91,13 +91,15 @@ __device__ __forceinline__ void store_box(const void* box, const CUtensorMap* ma
 constexpr int kOutBytes = 2 * 4096;
 static_assert(kTurnBytes <= kOutBytes, "the other way out uses the same memory");
 constexpr int kQ8Smem = 227 * 1024 - 4096;   // (beside the static part)
-// Stages: what fits beside the outputs and the scales' ring, 4 for a pair (5 were slower: each of
-// the two issuing threads keeps to its own half of an even number).  a_rows as in dense_stages.
+// Stages: what fits beside the outputs and the scales' ring, 4 for a pair (5 were slower), and an even
+// number: each issuing thread then keeps to its own half of the ring and sees every phase of its
+// barriers (known by their parity only, a phase may not be waited for while an earlier one is
+// open).  a_rows as in dense_stages.
 constexpr int kQ8Stages = 8;
 inline int q8_stages(int cg, int bn, int a_rows, bool by_rows) {
     const int room = kQ8Smem - 1024 - kDenseEpilogueWarps * kOutBytes - (by_rows ? kScaleSlots * (kDenseM + bn) * 4 : 0) -
                      (kDenseM - a_rows) * 128;
-    return cg == 2 ? 4 : std::min(kQ8Stages, room / ((a_rows + bn) * 128));
+    return cg == 2 ? 4 : std::min(kQ8Stages, room / ((a_rows + bn) * 128)) & ~1;
 }
 
 template <int CG, int BN, bool ROWS>
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     constexpr int S = kQ8Stages;
     constexpr int HC = BN / 2;    // columns of an epilogue warp
     constexpr int HB = BN / CG;   // rows of B that a CTA loads
-    constexpr int NB = BN == 256 ? 2 : 4;   // accumulators
+    constexpr int NB = BN == 256 ? 2 : 4;   // accumulators (an even number, as the stages)
     extern __shared__ __align__(1024) unsigned char q8_raw[];
     unsigned char* sm = q8_raw + ((1024 - (smem_u32(q8_raw) & 1023)) & 1023);
     // outputs of each epilogue warp; ROWS: scales [kScaleSlots][kDenseM + BN]; stages

@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
         }
         if (!ok) most = __int_as_float(0x7fc00000);
         // ---- along the columns: a warp's 16 rows, four columns a lane
-        const bool words = a.codes && a.ld % 4 == 0 && ((uintptr_t)a.codes & 3) == 0;
+        uint8_t* row_codes = a.codes + r0 * a.ld + c0 + 4 * lane;
+        const bool words = a.ld % 4 == 0 && ((uintptr_t)a.codes & 3) == 0 && 4 * lane + 4 <= nc;
         auto read4 = [&](int r, float2& p, float2& q) {
             if constexpr (sizeof(T) == 4) {
                 const float4 f = *reinterpret_cast<const float4*>(sm + r * kTile + 4 * lane);
@@ -107,9 +108,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
             const float2 i2 = make_float2(inv, inv);
             uint32_t w = q_codes4(__fmul2_rn(p, i2), __fmul2_rn(q, i2), SNK_Q8_E4M3);
             if (inv == 0.f) w = 0;
-            uint8_t* out = a.codes + (r0 + r) * a.ld + c0 + 4 * lane;
             if (r >= nr) return;
-            if (words && 4 * lane + 4 <= nc) {
+            uint8_t* out = row_codes + r * a.ld;
+            if (words) {
                 *reinterpret_cast<uint32_t*>(out) = w;
             } else {
 #pragma unroll
@@ -117,21 +118,30 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
                     if (4 * lane + j < nc) out[j] = (uint8_t)(w >> (8 * j));
             }
         };
-        if (BLOCKS || a.codes) {
+        if constexpr (BLOCKS) {
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {
-                const int r = warp * 16 + i;
                 float2 p, q;
-                read4(r, p, q);
-                float m = max_abs(max_abs(0.f, p.x, p.y), q.x, q.y);
-                if constexpr (BLOCKS) {
-                    most = max_nan(most, m);
-                } else {
-                    m = warp_amax(max_nan(m, most));
-                    const QScale s = q_scale(m, SNK_Q8_E4M3);
-                    write4(r, p, q, s.inv);
-                    if (lane == 0 && r < nr) a.scales[(r0 + r) * a.tiles_c + tc] = s.scale;
-                }
+                read4(warp * 16 + i, p, q);
+                most = max_abs(max_abs(most, p.x, p.y), q.x, q.y);
+            }
+        } else if (a.codes) {
+            // lane i (and i + 16) finds the scale of row i, once for the warp's 16 rows
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float2 p, q;
+                read4(warp * 16 + i, p, q);
+                const float r = warp_amax(max_abs(max_abs(most, p.x, p.y), q.x, q.y));
+                if ((lane & 15) == i) m = r;
+            }
+            const QScale s = q_scale(m, SNK_Q8_E4M3);
+            if (lane < 16 && warp * 16 + lane < nr) a.scales[(r0 + warp * 16 + lane) * a.tiles_c + tc] = s.scale;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float2 p, q;
+                read4(warp * 16 + i, p, q);
+                write4(warp * 16 + i, p, q, __shfl_sync(0xffffffffu, s.inv, i));
             }
         }
         QScale block{0.f, 0.f};
@@ -174,9 +184,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
                 for (int k = 0; k < CW; ++k) {
                     float m = ok ? 0.f : __int_as_float(0x7fc00000), s = 0.f;
 #pragma unroll
-                    for (int i = 0; i < RT; i += 2) {
-                        m = max_abs(m, value(i, k), value(i + 1, k));
-                        s += value(i, k) + value(i + 1, k);
+                    for (int i = 0; i < RT; i += 2) m = max_abs(m, value(i, k), value(i + 1, k));
+                    if (a.part) {
+#pragma unroll
+                        for (int i = 0; i < RT; i += 2) s += value(i, k) + value(i + 1, k);
                     }
                     most_s[k][t] = m;
                     sums_s[k][t] = s;
@@ -208,9 +219,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int r = b + 4 * i;
-                            w[i] = q_codes4(make_float2(__fmul_rn(value(r, k), q[k].inv), __fmul_rn(value(r + 1, k), q[k].inv)),
-                                            make_float2(__fmul_rn(value(r + 2, k), q[k].inv), __fmul_rn(value(r + 3, k), q[k].inv)),
-                                            SNK_Q8_E4M3);
+                            const float2 i2 = make_float2(q[k].inv, q[k].inv);
+                            w[i] = q_codes4(__fmul2_rn(make_float2(value(r, k), value(r + 1, k)), i2),
+                                            __fmul2_rn(make_float2(value(r + 2, k), value(r + 3, k)), i2), SNK_Q8_E4M3);
                             if (q[k].inv == 0.f) w[i] = 0;
                         }
                         *reinterpret_cast<uint4*>(out + 16 * (((h * RT + b) / 16) ^ (word & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -259,6 +270,7 @@ __global__ void __launch_bounds__(256) k_q8_sums(const float* __restrict__ part,
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < cols)
+#pragma unroll 8
         for (int64_t i = warp; i < tiles; i += 8) s += __ldg(part + i * cols + c);
     sm[warp][lane] = s;
     __syncthreads();
