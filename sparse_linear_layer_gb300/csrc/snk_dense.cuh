@@ -525,6 +525,44 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if (warp == 1) tmem_free<CG>(tmem, 512);
 }
 
+// Rows of `bytes` bytes, `ld` apart and of any alignment (the first one of 16), to rows of `to` bytes, a
+// multiple of 16, with zeros behind: what TMA can read.  A lane makes 16 bytes from the five aligned words
+// that hold them; nothing outside a row's words is read.
+static __global__ void __launch_bounds__(256) k_pad_rows(const uint8_t* __restrict__ src, int64_t ld, uint8_t* __restrict__ dst,
+                                                         int64_t rows, int64_t bytes, int64_t to) {
+    after_previous();
+    let_next_start();
+    // (a warp takes 32 chunks of a row; chunks of all rows, so that short rows fill the device too)
+    const int64_t per_row = (to / 16 + 31) / 32, n = rows * per_row;
+    for (int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); id < n; id += (int64_t)gridDim.x * 8) {
+        const int64_t r = id / per_row, c = (id - r * per_row) * 32 + (threadIdx.x & 31);
+        if (c >= to / 16) continue;
+        const uint8_t* row = src + r * ld;
+        const int off = (int)((uintptr_t)row & 3);
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(row - off) + 4 * c;   // (in front of a row lies the one before it)
+        const int64_t left = bytes + off - 16 * c;   // bytes from the first word to the row's end
+        uint32_t w[5];
+        if (left >= 20) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = __ldg(words + i);
+        } else {
+            const uint8_t* b = reinterpret_cast<const uint8_t*>(words);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                w[i] = 0;
+                for (int k = 0; k < 4; ++k)
+                    if (4 * i + k < left) w[i] |= (uint32_t)b[4 * i + k] << (8 * k);
+            }
+        }
+        uint4 o;
+        o.x = __funnelshift_r(w[0], w[1], 8 * off);
+        o.y = __funnelshift_r(w[1], w[2], 8 * off);
+        o.z = __funnelshift_r(w[2], w[3], 8 * off);
+        o.w = __funnelshift_r(w[3], w[4], 8 * off);
+        reinterpret_cast<uint4*>(dst + r * to)[c] = o;
+    }
+}
+
 // 16-bit [rows][len] at row stride ld (a multiple of 8), in boxes of 64 columns by
 // box_rows rows with the 128-byte swizzle; what lies past len or rows reads as zero.
 inline bool dense_map(CUtensorMap* map, const void* base, bool bf16, int64_t len, int64_t rows, int64_t ld, int box_rows) {

@@ -345,19 +345,20 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     tc_fence_after();
     if (warp == 3) tmem_free<CG>(tmem, 512);
 }
-// Scales [rows, n_g] of A (blockIdx.y 0) or B (1) as [n_g][padded], zeros behind the rows.
+// Scales [rows, n_g] of A (even blocks) or B (odd ones) as [n_g][padded], zeros behind the rows.
 __global__ void __launch_bounds__(256) k_q8_scales(const float* __restrict__ sa, int64_t M, int64_t padded_m, float* __restrict__ ta,
                                                    const float* __restrict__ sb, int64_t N, int64_t padded_n, float* __restrict__ tb,
                                                    int n_g) {
     __shared__ float sm[32][33];
+    after_previous();
     let_next_start();
-    const bool second = blockIdx.y == 1;
+    const bool second = blockIdx.x & 1;
     const float* src = second ? sb : sa;
     float* dst = second ? tb : ta;
     const int64_t rows = second ? N : M, padded = second ? padded_n : padded_m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t tiles_g = (n_g + 31) / 32, tiles = padded / 32 * tiles_g;
-    for (int64_t id = blockIdx.x; id < tiles; id += gridDim.x) {
+    for (int64_t id = blockIdx.x >> 1; id < tiles; id += gridDim.x >> 1) {
         const int64_t r0 = id / tiles_g * 32;
         const int g0 = (int)(id % tiles_g) * 32;
 #pragma unroll
@@ -494,18 +495,9 @@ __global__ void __launch_bounds__(32 * kRowsWarps, NT == 1 ? 4 : 2) k_q8_rows(co
     }
 }
 
-// Codes [rows, cols] at row stride ld, with rows of whole 16-byte chunks and zeros behind the columns.
-__global__ void __launch_bounds__(256) k_q8_pad(const uint8_t* __restrict__ src, int64_t ld, uint8_t* __restrict__ dst, int64_t rows,
-                                                int64_t cols, int64_t to) {
-    let_next_start();
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8)
-        for (int64_t c = threadIdx.x & 31; c < to; c += 32) dst[r * to + c] = c < cols ? src[r * ld + c] : (uint8_t)0;
-}
-
 // ---- host ------------------------------------------------------------------------------
 
 int64_t up(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
-int launched() { return cudaGetLastError() == cudaSuccess ? SNK_OK : SNK_ERR_CUDA; }
 
 // Scales [n_g][padded] in boxes of one group and `box` rows.
 bool scales_map(CUtensorMap* map, const float* base, int64_t padded, int n_g, int box_rows) {
@@ -673,9 +665,8 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
     if (p.bytes > 0 && !scratch) return SNK_ERR_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     auto copy = [&](const void* src, int64_t ld, uint8_t* dst, int64_t rows) {
-        k_q8_pad<<<(unsigned)std::min<int64_t>(ceil_div(rows, 8), 8 * n), 256, 0, s>>>(static_cast<const uint8_t*>(src), ld, dst,
-                                                                                    rows, K, p.ld);
-        return launched();
+        return launch_after(k_pad_rows, (unsigned)std::min<int64_t>(ceil_div(rows * ceil_div(p.ld, 512), 8), 1 << 20), 256, 0, 1, s, static_cast<const uint8_t*>(src),
+                            ld, dst, rows, K, p.ld);
     };
     const uint8_t *pa = static_cast<const uint8_t*>(a), *pb = static_cast<const uint8_t*>(b);
     if (p.copy_a) {
@@ -700,9 +691,10 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
     if (!b_blocks) {
         if (!scales_map(&m[2], p.ta, p.padded_m, n_g, kDenseM) || !scales_map(&m[3], p.tb, p.padded_n, n_g, p.bn)) return SNK_ERR_CUDA;
         const int64_t tiles = std::max(p.padded_m, p.padded_n) / 32 * ceil_div(n_g, 32);
-        k_q8_scales<<<dim3((unsigned)std::min<int64_t>(tiles, 16 * n), 2), 256, 0, s>>>(a_scales, M, p.padded_m, p.ta, b_scales, N,
-                                                                                     p.padded_n, p.tb, n_g);
-        if (int st = launched(); st != SNK_OK) return st;
+        if (int st = launch_after(k_q8_scales, 2 * (unsigned)std::min<int64_t>(tiles, 16 * n), 256, 0, 1, s, a_scales, M, p.padded_m, p.ta,
+                                  b_scales, N, p.padded_n, p.tb, n_g);
+            st != SNK_OK)
+            return st;
     }
     Q8DenseArgs q = {};
     q.M = M;

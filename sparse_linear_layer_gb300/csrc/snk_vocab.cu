@@ -341,16 +341,6 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + t; i < nz; i += (int64_t)gridDim.x * 256) z[i] = make_uint4(0, 0, 0, 0);
 }
 
-// [rows, cols] at row stride ld > cols, zeros behind the columns.
-template <typename T>
-__global__ void __launch_bounds__(256) k_vocab_pad(const T* __restrict__ src, T* __restrict__ dst, int64_t rows, int64_t cols,
-                                                   int64_t ld) {
-    after_previous();
-    let_next_start();
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8)
-        for (int64_t c = threadIdx.x & 31; c < ld; c += 32) dst[r * ld + c] = c < cols ? src[r * cols + c] : from_f32<T>(0.f);
-}
-
 // ---- the loss from its partial sums -------------------------------------------------
 
 struct FinishArgs {
@@ -709,10 +699,9 @@ int launch(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const De
                      : dense_launch<1, A_MN, B_MN, TURNS, false, Epilogue>(ma, mb, a, e, num_sms, s);
 }
 
-template <typename T>
 int pad_weight(const Shape& h, const void* w, void* wc, int num_sms, cudaStream_t s) {
-    return launch_after(k_vocab_pad<T>, (unsigned)std::min<int64_t>(ceil_div(h.vocab, 8), 8 * num_sms), 256, 0, 1, s,
-                        static_cast<const T*>(w), static_cast<T*>(wc), h.vocab, h.cols, h.ld);
+    return launch_after(k_pad_rows, (unsigned)std::min<int64_t>(ceil_div(h.vocab * ceil_div(h.ld, 256), 8), 1 << 20), 256, 0, 1, s,
+                        static_cast<const uint8_t*>(w), 2 * h.cols, static_cast<uint8_t*>(wc), h.vocab, 2 * h.cols, 2 * h.ld);
 }
 
 template <typename T>
@@ -743,7 +732,7 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
     }
     const void* wt = w;
     if (h.pads()) {
-        if (int st = pad_weight<T>(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
+        if (int st = pad_weight(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
         wt = p.wc;
     }
     CUtensorMap ma, mb;
@@ -861,7 +850,7 @@ int backward_rows(const Shape& h, const BackwardPlan& p, const void* x, const vo
     if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, r.per_block), 256, 0, 1, s, r); st != SNK_OK) return st;
     const void* wt = w;
     if (h.pads()) {
-        if (int st = pad_weight<T>(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
+        if (int st = pad_weight(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
         wt = p.wc;
     }
     return backward<T>(h, p, wt, dx, dw, num_sms, s);
