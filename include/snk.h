@@ -12,7 +12,9 @@
  *                      uniform regrow of as many new zero-valued entries
  *                      (nnz unchanged); prune_regrow_gradient grows at the
  *                      largest-|gradient| positions instead
- * with hand-written CUDA kernels.  The caller owns every buffer it passes;
+ * with hand-written CUDA kernels.  Beside the layer stand calls without a handle for
+ * the rest of a model: 8-bit activations, dense products on 8-bit matrices, and the loss
+ * of a vocabulary head (further below).  The caller owns every buffer it passes;
  * the library owns only the workspace behind the handle.
  *
  * Sources (page titles; sections, figures and tables as printed there):

@@ -6,7 +6,9 @@ input gradient, the weight gradient on the support (SDDMM) and the in-place
 prune/regrow restructure.  This package holds the C-ABI binding to it
 (``binding``), 8-bit activations with scales, the norm that writes them and the
 activation that keeps them (``q8``), a torch.nn front end with autograd and the
-SET schedule (``module``, and ``mlp``: a whole block on 8-bit activations), and the seeded synthetic input generators (``synth``).  The
+SET schedule (``module``, and ``mlp``: a whole block on 8-bit activations), the dense
+part of a model around such blocks (``dense``: projections on 8-bit matrices and the
+vocabulary head's loss), and the seeded synthetic input generators (``synth``).  The
 binding is loaded on first use, so importing the package (or ``synth``) does
 not touch the GPU.
 """
