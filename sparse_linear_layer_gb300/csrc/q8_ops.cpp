@@ -394,9 +394,11 @@ PyObject* op_backward_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
 at::Tensor aligned(const at::Tensor& t) { return ((uintptr_t)t.data_ptr() & 15) ? t.clone() : t; }
 
 int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
-// New E4M3 codes [rows, cols] (padded: rows 32 bytes apart, as the products like them, else contiguous).
-at::Tensor new_codes(int64_t rows, int64_t cols, bool padded, const at::TensorOptions& options) {
-    const int64_t ld = padded ? up(cols, 32) : cols;
+// Row stride of codes that only products read: whole 128-byte lines.
+int64_t padded(int64_t n) { return up(n, 128); }
+// New E4M3 codes [rows, cols] (pad: rows at that stride, else contiguous).
+at::Tensor new_codes(int64_t rows, int64_t cols, bool pad, const at::TensorOptions& options) {
+    const int64_t ld = pad ? padded(cols) : cols;
     at::Tensor t = at::empty({rows, ld}, options.dtype(at::kFloat8_e4m3fn));
     return ld == cols ? t : t.narrow(1, 0, cols);
 }
@@ -408,16 +410,16 @@ PyObject* op_pack_both(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& x = tensor(a[0], "x");
         const int d = dtype_of(x);
         const Matrix m(x);
-        const bool padded = PyObject_IsTrue(a[4]);
+        const bool pad = PyObject_IsTrue(a[4]);
         const OnStream on(a[5], x.device());
         const auto options = x.options().requires_grad(false);
         at::Tensor codes, scales, codes_t, scales_t, sums, scratch;
         if (PyObject_IsTrue(a[1])) {
-            codes = new_codes(m.rows, m.cols, padded, options);
+            codes = new_codes(m.rows, m.cols, pad, options);
             scales = at::empty({m.rows, groups(m.cols, 128)}, options.dtype(at::kFloat));
         }
         if (PyObject_IsTrue(a[2])) {
-            codes_t = new_codes(m.cols, m.rows, padded, options);
+            codes_t = new_codes(m.cols, m.rows, pad, options);
             scales_t = at::empty({m.cols, groups(m.rows, 128)}, options.dtype(at::kFloat));
         }
         if (PyObject_IsTrue(a[3])) {
@@ -654,7 +656,6 @@ PyObject* op_linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ---- a dense layer on 8-bit matrices, with autograd
 
-int64_t padded(int64_t n) { return up(n, 32); }
 // Pieces of one allocation, 256-byte aligned.
 struct Pieces {
     at::Tensor memory;

@@ -87,9 +87,10 @@ __device__ __forceinline__ void store_box(const void* box, const CUtensorMap* ma
                  : "memory");
 }
 
-// What an epilogue warp's outputs go through: two boxes of 32 rows by 128 bytes.
-constexpr int kOutBytes = 2 * 4096;
-static_assert(kTurnBytes <= kOutBytes, "the other way out uses the same memory");
+// What an epilogue warp's outputs go through: boxes of 32 rows by 128 bytes, two for a pair; one for a CTA
+// by itself, whose stages need the room (64 x 768 -> 50257: 17.3 us with two boxes and two stages).
+constexpr int out_bytes(int cg) { return cg == 2 ? 2 * 4096 : 5 * 1024; }
+static_assert(kTurnBytes <= out_bytes(1) && kTurnBytes <= out_bytes(2), "the other way out uses the same memory");
 constexpr int kQ8Smem = 227 * 1024 - 4096;   // (beside the static part)
 // Stages: what fits beside the outputs and the scales' ring, 4 for a pair (5 were slower), and an even
 // number: each issuing thread then keeps to its own half of the ring and sees every phase of its
@@ -97,7 +98,7 @@ constexpr int kQ8Smem = 227 * 1024 - 4096;   // (beside the static part)
 // open).  a_rows as in dense_stages.
 constexpr int kQ8Stages = 8;
 inline int q8_stages(int cg, int bn, int a_rows, bool by_rows) {
-    const int room = kQ8Smem - 1024 - kDenseEpilogueWarps * kOutBytes - (by_rows ? kScaleSlots * (kDenseM + bn) * 4 : 0) -
+    const int room = kQ8Smem - 1024 - kDenseEpilogueWarps * out_bytes(cg) - (by_rows ? kScaleSlots * (kDenseM + bn) * 4 : 0) -
                      (kDenseM - a_rows) * 128;
     return cg == 2 ? 4 : std::min(kQ8Stages, room / ((a_rows + bn) * 128)) & ~1;
 }
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     constexpr int S = kQ8Stages;
     constexpr int HC = BN / 2;    // columns of an epilogue warp
     constexpr int HB = BN / CG;   // rows of B that a CTA loads
+    constexpr int kOutBytes = out_bytes(CG), BOXES = kOutBytes / 4096;
     constexpr int NB = BN == 256 ? 2 : 4;   // accumulators (an even number, as the stages)
     extern __shared__ __align__(1024) unsigned char q8_raw[];
     unsigned char* sm = q8_raw + ((1024 - (smem_u32(q8_raw) & 1023)) & 1023);
@@ -312,9 +314,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                         }
                         if (E <= HC && a.vec) {
                             // the writes leave while the next tile's groups are added
-                            unsigned char* box = buf + (c / E & 1) * 4096;
-                            if (c >= 2 * E) {
-                                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                            unsigned char* box = buf + (c / E % BOXES) * 4096;
+                            if (c >= BOXES * E) {   // the box's last content has left
+                                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BOXES - 1) : "memory");
                                 __syncwarp();
                             }
                             put_box<T>(box, lane, v);
