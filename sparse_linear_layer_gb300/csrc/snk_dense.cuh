@@ -6,13 +6,13 @@
 // brings 128-byte wide boxes with the 128-byte swizzle.  A tile is 128 CG rows by `bn`
 // columns, CG the CTAs that share it: a pair (CG = 2) runs one MMA of 256 rows over both
 // SMs, each holding its 128 rows of A and half of B's columns, so that B crosses the L2
-// once per pair.  Persistent CTAs, eleven warps:
+// once per pair.  Persistent CTAs, twelve warps:
 //   warp 0     TMA loads into a ring of stages (64 columns of K each);
-//   warps 1, 10  issue the MMAs (a thread each, of the pair's first CTA), one the even
-//              accumulator turns and one the odd ones; warp 1 owns the TMEM allocation, two
-//              accumulators of up to 256 columns that take turns;
-//   warps 2-9  the epilogue: warp w reads the TMEM lanes 32 (w % 4) .. + 31 and, by
-//              w < 6 or not, the first or second half of the columns.
+//   warps 1, 2 issue the MMAs (a thread each, of the pair's first CTA), one the even
+//              accumulator turns and one the odd ones;
+//   warp 3     owns the TMEM allocation, two accumulators of up to 256 columns that take turns;
+//   warps 4-11 the epilogue: warp w reads the TMEM lanes 32 (w % 4) .. + 31 and, by
+//              w < 8 or not, the first or second half of the columns.
 // Every wait is bounded (kTcWaitCycles); a role whose wait ran out stops, waits for the
 // copies and MMAs that it has issued, and the epilogue writes NaN for every tile that it
 // has not been given.
@@ -26,7 +26,15 @@ namespace snk {
 constexpr int kDenseM = 128;             // rows of a tile per CTA (TMEM lanes)
 constexpr int kDenseN = 256;             // columns of a tile at most
 constexpr int kDenseK = 64;              // columns of K per stage: 128 bytes
-constexpr int kDenseThreads = 352;
+// Four warps of roles and eight of the epilogue, whose threads may keep 128 sums; registers as launched
+// (168 a thread) and as redistributed.
+constexpr int kDenseThreads = 384;
+constexpr int kRoleRegs = 40, kSumRegs = 232;
+static_assert(128 * kRoleRegs + 256 * kSumRegs <= kDenseThreads * 168, "the shares come out of the launch's registers");
+template <int R>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 constexpr int kDenseEpilogueWarps = 8;
 constexpr int kDenseBoxBytes = 64 * 128;   // an MN-major box: 64 rows of K, 64 columns
 constexpr int kDenseStages = 8;          // at most
@@ -176,29 +184,35 @@ struct DenseTile {
     int cols;          // columns of the half
     int mt, nt, half, split;
     bool ok;           // false: a wait ran out, write NaN
-    bool none;         // no columns of K: zero
     int rows;          // rows of A that count (all of them without a device count)
 };
-// An epilogue reads its half's columns 32 at a time, c = 0, 32, 64, 96, from the accumulator ...
+// An epilogue reads its half's columns 32 at a time, c = 0, 32, 64, 96 (constants, in an unrolled
+// loop), from the accumulator ...
 struct FromTmem {
     uint32_t taddr;   // of the half's first column on the warp's lanes
+    bool none;        // no columns of K: zeros
     __device__ __forceinline__ void get(int c, const DenseTile& t, float (&v)[32]) const {
         uint32_t r[32];
         tmem_ld32(taddr + c, r);
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        if (!t.ok || t.none) {
+        if (!t.ok || none) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = t.ok ? 0.f : __int_as_float(0x7fc00000);
         }
     }
 };
-// ... or from the sums of several.
+// ... or from registers, so that the accumulator is free before it is worked on.
 struct FromSums {
     const float (&sum)[kDenseN / 2];
+    bool none;
     __device__ __forceinline__ void get(int c, const DenseTile& t, float (&v)[32]) const {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = t.ok ? sum[c + j] : __int_as_float(0x7fc00000);
+        for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
+        if (!t.ok || none) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = t.ok ? 0.f : __int_as_float(0x7fc00000);
+        }
     }
 };
 
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<CG>(&tmem_base, 512);
+    if (warp == 3) tmem_alloc<CG>(&tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
@@ -342,8 +356,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     // first row of A of a tile's part in this CTA
     auto row_of = [&](int mt, int sub) { return ((mt * SUBS + sub) * CG + rank) * kDenseM; };
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        fewer_registers<kRoleRegs>();
+        if (warp == 0 && lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
             Stages r(a.stages);
             for (int id = first; id < items && ok; id += step) {
@@ -383,7 +398,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             }
             if (!ok && rank == 0) drain_last(full, r, used);   // (the other CTA's copies among them)
         }
-    } else if (warp == 1 || warp == 10) {
         // One thread for all turns left the tensor cores idle for 850 cycles where they changed the
         // accumulator: its waits and commits, with nothing queued behind the last MMA.  The other
         // thread makes its waits beside the last MMAs of a turn.  It is told when to (hand): a
@@ -391,8 +405,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         // phase of that barrier is still open.  The word comes when all stages but the turn's last
         // have been waited for; the next turn's first stage is then at most the second in the ring
         // that is open, and its accumulators' earlier phases are past.
-        if (lane == 0 && rank == 0) {
-            const uint32_t mine = warp == 1 ? 0 : 1;
+        if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
+            const uint32_t mine = warp - 1;
             bool ok = true;
             Stages r(a.stages);
             uint32_t q = 0;   // accumulators filled, by both threads
@@ -454,7 +468,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             }
         }
     } else {
-        const int half = warp >= 6 ? 1 : 0, quarter = warp & 3;
+        more_registers<kSumRegs>();
+        const int half = warp >= 8 ? 1 : 0, quarter = warp & 3;
         const int hc = a.bn / 2;
         const uint32_t lanes = tmem + half * hc + ((uint32_t)(quarter * 32) << 16);
         bool ok = true;
@@ -483,35 +498,46 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             tile.nt = it.nt;
             tile.half = half;
             tile.split = it.split;
-            tile.none = (int64_t)n_k * it.split / a.splits == (int64_t)n_k * (it.split + 1) / a.splits;
+            const bool none = (int64_t)n_k * it.split / a.splits == (int64_t)n_k * (it.split + 1) / a.splits;   // no columns of K
             tile.rows = rows;
-            if constexpr (TURNS) {
-                float sum[kDenseN / 2];
-#pragma unroll
-                for (int j = 0; j < kDenseN / 2; ++j) sum[j] = 0.f;
-                for (int turn = 0; turn < a.turns; ++turn) {
-                    const uint32_t taddr = wait();
-#pragma unroll
-                    for (int c = 0; c < kDenseN / 2; c += 32) {
-                        if (c < hc) {
-                            uint32_t r[32];
-                            tmem_ld32(taddr + c, r);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) sum[c + j] += __uint_as_float(r[j]);
-                        }
-                    }
-                    release();
-                }
-                tile.ok = ok;
-                tile.row = row_of(it.mt, 0) + quarter * 32 + lane;
-                if (tile.row - lane < a.m_held) Epilogue::run(ea, tile, FromSums{sum});
-            } else {
 #pragma unroll 1
-                for (int sub = 0; sub < SUBS; ++sub) {
-                    tile.row = row_of(it.mt, sub) + quarter * 32 + lane;
-                    const FromTmem source{wait()};
+            for (int sub = 0; sub < SUBS; ++sub) {
+                tile.row = row_of(it.mt, sub) + quarter * 32 + lane;
+                const bool held = tile.row - lane < a.m_held;
+                if constexpr (TURNS || DUAL) {
+                    float sum[kDenseN / 2];
+                    if constexpr (TURNS) {
+#pragma unroll
+                        for (int j = 0; j < kDenseN / 2; ++j) sum[j] = 0.f;
+                        for (int turn = 0; turn < a.turns; ++turn) {
+                            const uint32_t taddr = wait();
+#pragma unroll
+                            for (int c = 0; c < kDenseN / 2; c += 32) {
+                                if (c < hc) {
+                                    uint32_t r[32];
+                                    tmem_ld32(taddr + c, r);
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) sum[c + j] += __uint_as_float(r[j]);
+                                }
+                            }
+                            release();
+                        }
+                    } else {   // (tiles of 256 columns)
+                        const uint32_t taddr = wait();
+                        uint32_t r[kDenseN / 64][32];
+#pragma unroll
+                        for (int c = 0; c < kDenseN / 2; c += 32) tmem_ld32_async(taddr + c, r[c / 32]);
+                        tmem_wait_ld();
+                        release();
+#pragma unroll
+                        for (int c = 0; c < kDenseN / 2; ++c) sum[c] = __uint_as_float(r[c / 32][c % 32]);
+                    }
                     tile.ok = ok;
-                    if (tile.row - lane < a.m_held) Epilogue::run(ea, tile, source);
+                    if (held) Epilogue::run(ea, tile, FromSums{sum, none});
+                } else {
+                    const FromTmem source{wait(), none};
+                    tile.ok = ok;
+                    if (held) Epilogue::run(ea, tile, source);
                     release();
                 }
             }
@@ -522,7 +548,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();   // no barrier or tile of a CTA goes while the other may still touch it
     tc_fence_after();
-    if (warp == 1) tmem_free<CG>(tmem, 512);
+    if (warp == 3) tmem_free<CG>(tmem, 512);
 }
 
 // Rows of `bytes` bytes, `ld` apart and of any alignment (the first one of 16), to rows of `to` bytes, a

@@ -20,16 +20,9 @@
 namespace snk {
 namespace {
 
-// Threads: four warps of roles (TMA, two that issue MMAs, one that allocates) and eight of the
-// epilogue, whose threads keep 128 sums each.  168 registers a thread at launch, redistributed so
-// that nothing spills (216 for the sums did: 8192 x 10000 x 10000 639 us against 612).
-constexpr int kQ8Threads = 384;
-constexpr int kQ8RoleRegs = 40, kQ8SumRegs = 232;
-static_assert(128 * kQ8RoleRegs + 256 * kQ8SumRegs <= kQ8Threads * 168, "the shares come out of the launch's registers");
-template <int R>
-__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R>
-__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+// Threads as in k_dense; with 216 registers for the sums' threads instead of 232 some spilled
+// (8192 x 10000 x 10000 639 us against 612).
+constexpr int kQ8Threads = kDenseThreads;
 
 struct Q8DenseArgs {
     int64_t M, N;
@@ -152,7 +145,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (warp < 4) {
-        fewer_registers<kQ8RoleRegs>();
+        fewer_registers<kRoleRegs>();
         if (warp == 0 && lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
             Stages r(a.stages);
@@ -217,7 +210,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             }
         }
     } else {
-        more_registers<kQ8SumRegs>();
+        more_registers<kSumRegs>();
         const int half = warp >= 8 ? 1 : 0, quarter = warp & 3;
         const uint32_t lanes = tmem + half * HC + ((uint32_t)(quarter * 32) << 16);
         const uint32_t free0 = CG == 1 ? 0 : first_cta(&acce[0]);

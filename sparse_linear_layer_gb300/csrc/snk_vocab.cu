@@ -118,7 +118,9 @@ struct GradEpilogue {
         const int lim = (int)min((int64_t)t.cols, a.width - t.col);
         const int top = (int)min((int64_t)t.cols, a.ld - t.col);   // a multiple of 16
         T* out = a.dz + t.row * a.ld + t.col;
-        for (int b = 0; b < top; b += 32) {
+#pragma unroll
+        for (int b = 0; b < kDenseN / 2; b += 32) {
+            if (b >= top) break;
             float v[32];
             from.get(b, t, v);
 #pragma unroll
@@ -163,7 +165,9 @@ struct SumEpilogue {
     __device__ static void run(const Args& a, const DenseTile& t, const Source& from) {
         const int lim = (int)min((int64_t)t.cols, a.ld - t.col);   // (a multiple of 8)
         float* out = a.slab + ((int64_t)t.split * a.rows + t.row) * a.ld + t.col;
-        for (int b = 0; b < lim; b += 32) {
+#pragma unroll
+        for (int b = 0; b < kDenseN / 2; b += 32) {
+            if (b >= lim) break;
             float v[32];
             from.get(b, t, v);
 #pragma unroll
@@ -198,7 +202,9 @@ struct StoreEpilogue {
         const float scale = 1.f / (GradEpilogue<T>::grad_factor(*a.most) * kDzScale);
         T* out = a.out + t.row * a.cols + t.col;
         const int top = (int)min((int64_t)t.cols, a.cols - t.col);   // the same in all lanes
-        for (int b = 0; b < top; b += 32) {
+#pragma unroll
+        for (int b = 0; b < kDenseN / 2; b += 32) {
+            if (b >= top) break;
             float v[32];
             from.get(b, t, v);
 #pragma unroll
