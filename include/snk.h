@@ -560,7 +560,8 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
  *   dz_rv = g_r (exp(z_rv - lse_r) - [v = target(r)]),  dx = dz W,  dweight = dz^T x
  * from logits computed again, a piece of the vocabulary at a time; dx [rows, cols] and
  * dweight [vocab, cols] have the type `dtype`; either may be NULL.  dz is rounded to
- * `dtype` (scaled by a power of two) before the two products, which accumulate in fp32.
+ * `dtype` (scaled by a power of two, and for reductions 1 and 2 without g, which multiplies
+ * the results) before the two products, which accumulate in fp32.
  * Ignored rows get dx = 0; a row whose target is out of range gets NaN.
  *
  * scratch: snk_vocab_loss_scratch(rows, cols, vocab, backward) bytes (backward 0 or 1)

@@ -16,10 +16,13 @@
 //   StoreEpilogue  the piece's rows of dW = dz^T x, complete
 // The gradient's rows are gathered first (k_vocab_rows): the rows that count, side by
 // side, zeros up to a whole tile; ignored rows then cost nothing, and the count stays on
-// the device.  dz is held as c_r 2^13 (p - [v = t]) with c_r = g_r / G, G the power of two
-// next to the largest |g|, so that probabilities down to 2^-37 stay normal fp16 numbers;
-// the rounding of dz to 16 bits is one rounding of half a unit per term of a sum whose
-// result is rounded to the same type.
+// the device.  dz is held as c_r 2^13 (p - [v = t]), rounded to 16 bits, so that probabilities
+// down to 2^-27 stay normal fp16 numbers.  For a sum or a mean c_r = 1 and the upstream gradient
+// multiplies the finished products: the largest term of most rows, p - 1 with p small, then
+// lies just below a power of two, where a rounding costs least, and not wherever g puts it (the
+// gradients' errors against 64 bits are 1.00 to 1.17 of those of fp32 sums rounded to the same
+// type; with a power of two near g in its place draws of 1.5 were seen).  For losses that go out
+// row by row c_r = g_r / G, G the power of two next to the largest |g|.
 #include <algorithm>
 
 #include "snk_dense.cuh"
@@ -94,6 +97,19 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
+// What dz is multiplied by, and the products of dz.
+struct GradScale {
+    const uint32_t* most;     // bits of the largest finite |g_r|
+    const float* uniform;     // the upstream gradient of all rows, or null
+    // 1 / G, G the power of two at or above the largest finite |g| (1 where that is 0 or too small to invert)
+    __device__ __forceinline__ float inverse() const {
+        const int e = (int)(__ldg(most) >> 23);   // biased exponent: |g| < 2^(e - 126)
+        return e < 2 || e > 252 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
+    }
+    __device__ __forceinline__ float in() const { return uniform ? kDzScale : inverse() * kDzScale; }
+    __device__ __forceinline__ float out() const { return uniform ? __ldg(uniform) * (1.f / kDzScale) : 1.f / (inverse() * kDzScale); }
+};
+
 template <typename T>
 struct GradEpilogue {
     struct Args {
@@ -102,16 +118,16 @@ struct GradEpilogue {
         int64_t width;            // columns of the piece that exist
         int64_t first;            // vocabulary index of its first column
         const float* lse2;        // [rows] log2 e times lse
-        const float* g;           // [rows] upstream gradient
+        const float* g;           // [rows] factor of the row
         const int64_t* target;    // [rows]
-        const uint32_t* most;     // bits of the largest finite |g|
+        GradScale scale;
     };
     template <class Source>
     __device__ static void run(const Args& a, const DenseTile& t, const Source& from) {
         float c = 0.f, l2 = 0.f;
         int64_t at = -1;
         if (t.row < t.rows) {
-            c = a.g[t.row] * grad_factor(*a.most) * kDzScale;
+            c = a.g[t.row] * a.scale.in();
             l2 = a.lse2[t.row];
             at = a.target[t.row] - a.first - t.col;
         }
@@ -147,11 +163,6 @@ struct GradEpilogue {
                 if (b + j < top) store32(out + b + j, w);
             }
         }
-    }
-    // 1 / G, G the power of two at or above the largest finite |g| (1 where that is 0 or too small to invert)
-    __device__ static float grad_factor(uint32_t bits) {
-        const int e = (int)(bits >> 23);   // biased exponent: |g| < 2^(e - 126)
-        return e < 2 || e > 252 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
     }
 };
 
@@ -193,13 +204,13 @@ struct StoreEpilogue {
     struct Args {
         T* out;                  // [width, cols]
         int64_t width, cols;
-        const uint32_t* most;
+        GradScale scale;
         int vec;                 // elements per store: 16, 8 or 1, by the rows' alignment
     };
     template <class Source>
     __device__ static void run(const Args& a, const DenseTile& t, const Source& from) {
         const int lim = t.row < a.width ? (int)min((int64_t)t.cols, a.cols - t.col) : 0;
-        const float scale = 1.f / (GradEpilogue<T>::grad_factor(*a.most) * kDzScale);
+        const float scale = a.scale.out();
         T* out = a.out + t.row * a.cols + t.col;
         const int top = (int)min((int64_t)t.cols, a.cols - t.col);   // the same in all lanes
 #pragma unroll
@@ -252,6 +263,7 @@ struct RowsArgs {
     float* lse2;                      // [rows]
     float* g;                         // [rows]
     uint32_t* most;                   // cleared before; the largest finite |g|'s bits
+    float* uniform;                   // reductions 1, 2: the upstream gradient of every row (g is then 1)
 };
 // A block takes a.per_block rows; how many count before it and in all it finds out by itself:
 // targets are 8 bytes a row, and the more rows there are the more a block takes (gather_rows), so
@@ -299,8 +311,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
                 a.index[to] = (int32_t)r;
                 a.tc[to] = tg;
                 if (a.g) {
-                    float g = a.reduction == 0 ? a.dloss[r] : a.dloss[0];
-                    if (a.reduction == 2) g /= (float)all;
+                    float g = a.reduction == 0 ? a.dloss[r] : 1.f;
                     if (tg < 0 || tg >= a.vocab) g = nan_f();
                     a.g[to] = g;
                     a.lse2[to] = a.lse[r] * kLog2e;
@@ -321,7 +332,10 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
         }
         if (lane == 0) {
             mine_s = n;
-            if (blockIdx.x == 0) *a.count = all;
+            if (blockIdx.x == 0) {
+                *a.count = all;
+                if (a.g && a.reduction) *a.uniform = all == 0 ? 0.f : (a.reduction == 2 ? a.dloss[0] / (float)all : a.dloss[0]);
+            }
         }
     }
     __syncthreads();
@@ -496,12 +510,12 @@ __global__ void __launch_bounds__(256) k_vocab_finish(const FinishArgs a) {
 // element (many slabs of few rows: one thread's chain of loads would be the call's longest part).
 template <typename T, int WARPS>
 __global__ void __launch_bounds__(256) k_vocab_dx(const float* __restrict__ slab, int splits, int64_t stride, int64_t ld,
-                                                  const int32_t* __restrict__ at, const uint32_t* most, int64_t rows, int64_t cols,
+                                                  const int32_t* __restrict__ at, const GradScale by, int64_t rows, int64_t cols,
                                                   T* __restrict__ dx) {
     __shared__ F8 part[WARPS > 1 ? WARPS : 1][WARPS > 1 ? 32 : 1];
     after_previous();
     let_next_start();
-    const float scale = 1.f / (GradEpilogue<T>::grad_factor(*most) * kDzScale);
+    const float scale = by.out();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = WARPS > 1 ? warp : 0;
     constexpr int E = WARPS > 1 ? 32 : 256;   // elements (of 8 columns) of a block
     const int64_t n8 = ld / 8, n = rows * n8;
@@ -655,6 +669,7 @@ struct BackwardPlan {
     void *xc, *wc, *dz;
     int32_t *index, *at, *count;
     uint32_t* most;
+    float* uniform;
     int64_t* tc;
     float *lse2, *g, *slab;
     int64_t bytes;
@@ -666,8 +681,9 @@ struct BackwardPlan {
         x = pick_form(h.rows, h.ld, piece / 64, h.tile_rows(), 64, 64, 8.0 * h.rows * h.ld, num_sms, 2);
         w = pick_form(piece, h.ld, ceil_div(h.rows, 64), kDenseM, 64, 1, 0, num_sms, 2);
         Scratch s(scratch);
-        count = s.take<int32_t>(2);
+        count = s.take<int32_t>(4);
         most = reinterpret_cast<uint32_t*>(count + 1);
+        uniform = reinterpret_cast<float*>(count + 2);
         index = s.take<int32_t>(h.rows);
         at = s.take<int32_t>(h.rows);
         tc = s.take<int64_t>(h.rows);
@@ -780,7 +796,8 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
 }
 
 template <typename T>
-int backward(const Shape& h, const BackwardPlan& p, const void* wt, void* dx, void* dw, int num_sms, cudaStream_t s) {
+int backward(const Shape& h, const BackwardPlan& p, const void* wt, int reduction, void* dx, void* dw, int num_sms, cudaStream_t s) {
+    const GradScale scale{p.most, reduction ? p.uniform : nullptr};
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
     CUtensorMap mx, mx_t, mz, mz_t;   // _t: read along the rows
     if (!dense_map(&mx, p.xc, bf, h.ld, h.padded, h.ld, h.tile_rows()) || !dense_map(&mx_t, p.xc, bf, h.ld, h.padded, h.ld, 64))
@@ -796,7 +813,7 @@ int backward(const Shape& h, const BackwardPlan& p, const void* wt, void* dx, vo
             return SNK_ERR_CUDA;
         DenseArgs a = dense_args(p.z, bf, false, false, h.rows, width, h.ld, h.tile_rows());   // dz of the piece
         a.rows = p.count;
-        const typename GradEpilogue<T>::Args eg{static_cast<T*>(p.dz), p.piece, width, v0, p.lse2, p.g, p.tc, p.most};
+        const typename GradEpilogue<T>::Args eg{static_cast<T*>(p.dz), p.piece, width, v0, p.lse2, p.g, p.tc, scale};
         if (int st = launch<false, false, GradEpilogue<T>>(p.z, mx, mw, a, eg, num_sms, s); st != SNK_OK) return st;
         if (dx) {
             a = dense_args(p.x, bf, false, true, h.rows, h.ld, width, h.tile_rows());
@@ -810,7 +827,7 @@ int backward(const Shape& h, const BackwardPlan& p, const void* wt, void* dx, vo
             a.rows = p.count;
             a.rows_k = 1;
             const int vec = h.pads() ? 1 : (h.cols % 16 == 0 && ((uintptr_t)out & 31) == 0 ? 16 : 8);
-            const typename StoreEpilogue<T>::Args eo{out, width, h.cols, p.most, vec};
+            const typename StoreEpilogue<T>::Args eo{out, width, h.cols, scale, vec};
             if (int st = launch<true, true, StoreEpilogue<T>>(p.w, mz_t, mx_t, a, eo, num_sms, s); st != SNK_OK) return st;
         }
     }
@@ -818,9 +835,9 @@ int backward(const Shape& h, const BackwardPlan& p, const void* wt, void* dx, vo
         const int64_t n = h.rows * (h.ld / 8);
         T* out = static_cast<T*>(dx);
         return p.x.splits > 8 ? launch_after(k_vocab_dx<T, 8>, (unsigned)std::min<int64_t>(ceil_div(n, 32), 64 * num_sms), 256, 0, 1, s,
-                                             p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, out)
+                                             p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, scale, h.rows, h.cols, out)
                               : launch_after(k_vocab_dx<T, 1>, (unsigned)std::min<int64_t>(ceil_div(n, 256), 16 * num_sms), 256, 0, 1, s,
-                                             p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, p.most, h.rows, h.cols, out);
+                                             p.slab, p.x.splits, h.padded * h.ld, h.ld, p.at, scale, h.rows, h.cols, out);
     }
     return SNK_OK;
 }
@@ -853,13 +870,14 @@ int backward_rows(const Shape& h, const BackwardPlan& p, const void* x, const vo
     r.lse2 = p.lse2;
     r.g = p.g;
     r.most = p.most;
+    r.uniform = p.uniform;
     if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, r.per_block), 256, 0, 1, s, r); st != SNK_OK) return st;
     const void* wt = w;
     if (h.pads()) {
         if (int st = pad_weight(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
         wt = p.wc;
     }
-    return backward<T>(h, p, wt, dx, dw, num_sms, s);
+    return backward<T>(h, p, wt, reduction, dx, dw, num_sms, s);
 }
 
 bool unaligned(const void* p, uintptr_t n) { return p && ((uintptr_t)p & (n - 1)); }

@@ -185,6 +185,29 @@ def test_reductions_and_upstream_gradients(rows):
                     torch.full((rows,), -3.0, device="cuda"))
 
 
+@pytest.mark.parametrize("g", [0.53014, 1.0, 700.0])
+def test_upstream_gradient_costs_no_rounding(g):
+    """Targets of probability about 1 / 5000 and an upstream gradient that puts 2^13 g (1 - p) halfway between
+    two fp16 numbers just above a power of two.  Without g, p - 1 lies in [2^-1, 1) next to 1, where half a unit
+    is 2^-12 of it: dw of a target is then within u of itself (its own rounding) plus 2^-12 of |g x_t| plus u of
+    the other rows' terms; fp32 sums and logits add less than 2^-16 of the terms."""
+    u = UNIT[torch.float16]
+    x, w, _ = case(64, 128, 5000, torch.float16, ignored=0, seed=5, spread=0.05)
+    t = torch.randperm(5000, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6))[:64]
+    leaf = w.clone().requires_grad_()
+    dw, = torch.autograd.grad(dense.linear_cross_entropy(x, leaf, t, reduction="sum"), leaf, torch.tensor(g, device="cuda"))
+    xd = x.double()
+    p = torch.softmax(xd @ w.double().T, 1)[:, t]           # [row, target]
+    own = torch.diag(torch.diag(p) - 1)
+    others = p - torch.diag(torch.diag(p))
+    want = g * (own + others).T @ xd
+    sizes = g * others.T @ xd.abs()
+    first = g * xd.abs()
+    tol = u * want.abs() + 2.0 ** -12 * first + u * sizes + 2.0 ** -16 * (first + sizes) + 2.0 ** -25
+    err = (dw[t].double() - want).abs()
+    assert bool((err <= tol).all()), f"off by {(err / tol).max().item():.2f} of the tolerance"
+
+
 def test_gradient_against_differences():
     """Central differences of the loss along random directions.  With a step of h |direction| the
     fp64 loss of the rounded points is exact; the gradient is the kernel's."""
