@@ -429,7 +429,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     }
                     const uint32_t d = tmem + ab * kDenseN;
                     const int last = max(k0, k1 - 2);
-                    if (k0 == k1) mbar_arrive(&hand[mine ^ 1]);
+                    if (k0 == k1) {   // nothing to add (no row counts): both accumulators are handed on, so both must be drained
+                        if (DUAL && q >= 2 && !mbar_wait(&acce[1], ((q >> 1) - 1) & 1)) ok = false;
+                        if (ok) mbar_arrive(&hand[mine ^ 1]);
+                    }
                     for (int k = k0; k < k1; ++k) {
                         if (k == last) mbar_arrive(&hand[mine ^ 1]);
                         tc_fence_after();

@@ -243,6 +243,18 @@ def test_all_rows_ignored():
         assert bool((dx == 0).all()) and bool((dw == 0).all())
 
 
+@pytest.mark.parametrize("rows", [100, 300])
+def test_all_rows_ignored_many_tiles(rows):
+    """Several tiles of dW per pair of processors, each a sum over no rows."""
+    x, w, t = case(rows, 768, 50257, torch.float16)
+    t.fill_(-100)
+    x.requires_grad_()
+    w.requires_grad_()
+    for _ in range(3):
+        dx, dw = torch.autograd.grad(dense.linear_cross_entropy(x, w, t, reduction="sum"), (x, w))
+        assert bool((dx == 0).all()) and bool((dw == 0).all())
+
+
 @pytest.mark.parametrize("rows", [60, 400])
 def test_what_ignored_rows_hold_reaches_nothing(rows):
     x, w, t = case(rows, 80, 500, torch.float16)
