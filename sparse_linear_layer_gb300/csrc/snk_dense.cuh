@@ -269,7 +269,7 @@ struct Turn {
 // Position in a ring of slots: the slot and its phase's parity (counted, not divided:
 // the issuing threads pass here for every stage).
 struct Stages {
-    const int n;
+    int n;
     int slot = 0;
     uint32_t parity = 0;
     __device__ explicit Stages(int slots) : n(slots) {}
@@ -293,6 +293,10 @@ __device__ __forceinline__ void drain_last(uint64_t* full, const Stages& r, bool
         if (older || all) mbar_wait(&full[slot], older ? r.parity : r.parity ^ 1, kTcDrainCycles);
     }
 }
+
+// Stages by which a dual tile's first accumulator goes ahead of its second at a tile's start (8192 x 768 ->
+// 50257, the loss: 391 us before it did, 386 with 1, 380 with 2 or 3, 385 with 4, which is all there are).
+constexpr int kDenseLead = 3;
 
 // Epilogue: a type with Args and static __device__ void run(const Args&, const DenseTile&,
 // const Source&).  TURNS: the tensor cores' additions truncate, so a long K is shared by
@@ -433,35 +437,64 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                         if (DUAL && q >= 2 && !mbar_wait(&acce[1], ((q >> 1) - 1) & 1)) ok = false;
                         if (ok) mbar_arrive(&hand[mine ^ 1]);
                     }
-                    for (int k = k0; k < k1; ++k) {
+                    // the MMAs of a stage with one accumulator; next: another stage's come after them, which is
+                    // waited for while the tensor cores are busy (a wait costs a hundred cycles even when there
+                    // is nothing to wait for)
+                    auto multiply = [&](int s, int sub, bool more, bool next, const Stages& then) {
+                        const uint32_t sa = smem_u32(sm + s * stage), so = sa + sub * a_bytes, sb = sa + SUBS * a_bytes;
+#pragma unroll
+                        for (int kk = 0; kk < kDenseK / 16; ++kk) {
+                            // 16 columns of K: 32 bytes along a K-major row, two atoms of an MN-major box
+                            const uint64_t da = A_MN ? desc_mn128(so + kk * 2048) : desc_sw128(so + kk * 32);
+                            const uint64_t db = B_MN ? desc_mn128(sb + kk * 2048) : desc_sw128(sb + kk * 32);
+                            dense_mma<CG>(d + sub * kDenseN, da, db, a.idesc, (more || kk > 0) ? 1u : 0u);
+                            if (kk == 1 && next && !mbar_wait(&full[then.slot], then.parity)) ok = false;
+                        }
+                    };
+                    int k = k0;
+                    if constexpr (DUAL) {
+                        // A tile's first accumulator is drained before its second: its MMAs go ahead with the first
+                        // stages.  (accf[0] is told after acce[1] has been waited for: nobody then waits for a
+                        // phase of acce[1] while an earlier one is open.)
+                        if (q >= 2 && k0 < k1) {
+                            const int ahead = min(k1, k0 + min(kDenseLead, a.stages));
+                            const Stages begin = r;
+#pragma unroll 1
+                            for (int sub = 0; sub < 2 && ok; ++sub) {
+                                if (sub == 1) {
+                                    if (!mbar_wait(&acce[1], ((q >> 1) - 1) & 1)) {
+                                        ok = false;
+                                        break;
+                                    }
+                                    if (ahead == k1) dense_commit<CG>(&accf[0]);
+                                }
+                                r = begin;
+#pragma unroll 1
+                                for (k = k0; k < ahead && ok; ++k) {
+                                    if (sub == 0 && k == last) mbar_arrive(&hand[mine ^ 1]);
+                                    tc_fence_after();
+                                    const int s = r.slot;
+                                    r.next();
+                                    multiply(s, sub, k > k0, (k + 1 == ahead) == (sub == 1) && k + 1 < k1, r);
+                                    if (sub == 1) dense_commit<CG>(&empty[s]);
+                                }
+                            }
+                        }
+                    }
+                    for (; k < k1 && ok; ++k) {
                         if (k == last) mbar_arrive(&hand[mine ^ 1]);
                         tc_fence_after();
                         const int s = r.slot;
-                        const uint32_t sa = smem_u32(sm + s * stage), sb = sa + SUBS * a_bytes;
                         r.next();
-#pragma unroll
-                        for (int sub = 0; sub < SUBS; ++sub) {
-                            if (DUAL && sub == 1 && k == k0 && q >= 2) {   // the second accumulator, drained after the first
-                                if (!mbar_wait(&acce[1], ((q >> 1) - 1) & 1)) ok = false;
-                                tc_fence_after();
-                            }
-#pragma unroll
-                            for (int kk = 0; kk < kDenseK / 16; ++kk) {
-                                // 16 columns of K: 32 bytes along a K-major row, two atoms of an MN-major box
-                                const uint32_t so = sa + sub * a_bytes;
-                                const uint64_t da = A_MN ? desc_mn128(so + kk * 2048) : desc_sw128(so + kk * 32);
-                                const uint64_t db = B_MN ? desc_mn128(sb + kk * 2048) : desc_sw128(sb + kk * 32);
-                                dense_mma<CG>(d + sub * kDenseN, da, db, a.idesc, (k > k0 || kk > 0) ? 1u : 0u);
-                                // the next stage is waited for while the tensor cores are busy (a wait
-                                // costs a hundred cycles even when there is nothing to wait for)
-                                if (sub == SUBS - 1 && kk == 1 && k + 1 < k1 && !mbar_wait(&full[r.slot], r.parity)) ok = false;
-                            }
+                        multiply(s, 0, k > k0, !DUAL && k + 1 < k1, r);
+                        if constexpr (DUAL) {
+                            if (k + 1 == k1) dense_commit<CG>(&accf[0]);
+                            multiply(s, 1, k > k0, k + 1 < k1, r);
                         }
                         dense_commit<CG>(&empty[s]);
-                        if (!ok) break;
                     }
                     if (!ok) break;
-                    dense_commit<CG>(&accf[ab]);
+                    if (!DUAL || k0 == k1) dense_commit<CG>(&accf[ab]);
                     if constexpr (DUAL) dense_commit<CG>(&accf[1]);
                 }
             }
