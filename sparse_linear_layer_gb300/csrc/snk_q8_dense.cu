@@ -81,6 +81,12 @@ __device__ __forceinline__ void store_box(const void* box, const CUtensorMap* ma
                  : "memory");
 }
 
+// First of the n groups of a range of K, in 32 bits (n < 2^24, at most 16 splits): 64-bit divisions
+// took each tile's start about 0.25 us (32768 x 768 -> 2304: 72 us, now 68).
+__device__ __forceinline__ int range_first(int n, int split, int splits) {
+    return splits == 1 ? n * split : (int)((uint32_t)n * (uint32_t)split / (uint32_t)splits);
+}
+
 // What an epilogue warp's outputs go through: boxes of 32 rows by 128 bytes, two for a pair; one for a CTA
 // by itself, whose stages need the room (64 x 768 -> 50257: 17.3 us with two boxes and two stages).
 constexpr int out_bytes(int cg) { return cg == 2 ? 2 * 4096 : 5 * 1024; }
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             uint32_t w = 0;   // groups loaded
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
-                const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
+                const int g0 = range_first(a.n_g, it.split, a.splits), g1 = range_first(a.n_g, it.split + 1, a.splits);
                 const int m0 = (it.mt * CG + rank) * kDenseM, n0 = it.nt * BN + rank * HB;
                 for (int g = g0; g < g1; ++g, ++w) {
                     const int s = r.slot;
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             uint32_t w = 0;   // groups done
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
-                const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
+                const int g0 = range_first(a.n_g, it.split, a.splits), g1 = range_first(a.n_g, it.split + 1, a.splits);
                 for (int g = g0; g < g1; ++g, ++w, r.next()) {
                     if ((w & 1) != mine) continue;
                     const int s = r.slot, ab = (int)(w % NB);
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         uint32_t w = 0;   // groups done
         for (int id = first; id < items; id += step) {
             const DenseItem it = DenseItem::of(id, a.n_mt, a.n_nt, a.splits, a.group);
-            const int g0 = (int)((int64_t)a.n_g * it.split / a.splits), g1 = (int)((int64_t)a.n_g * (it.split + 1) / a.splits);
+            const int g0 = range_first(a.n_g, it.split, a.splits), g1 = range_first(a.n_g, it.split + 1, a.splits);
             const int64_t row = (int64_t)(it.mt * CG + rank) * kDenseM + quarter * 32 + lane;
             const int64_t col = (int64_t)it.nt * BN + half * HC;
             // rows and columns outside the matrix read the last ones' scales and are not stored
@@ -560,7 +566,8 @@ struct Q8Plan {
         ld = up(K, 16);
         const int n_g = (int)ceil_div(K, 128);
         // The tile and the ranges of K whose waves take least. Times in us as measured: of a group,
-        // of a tile beside its groups, of joining ranges (and their sums, written and read).
+        // of a tile beside its groups, of joining ranges and their sums, written and read: 8 bytes at 8 TB/s
+        // from the L2 (2304 x 768 over 32768: 5 ranges 79 us, 2 ranges 87), at half of it where they do not stay there.
         struct Form {
             int cg, bn;
             double group;
@@ -572,7 +579,7 @@ struct Q8Plan {
             const int64_t mt = ceil_div(M, 128 * f.cg), nt = ceil_div(N, f.bn), units = num_sms / f.cg;
             for (int sp = 1; sp <= 16 && (sp == 1 || n_g / sp >= 4); ++sp) {
                 const double waves = (double)ceil_div(mt * nt * sp, units);
-                const double t = waves * ((double)ceil_div(n_g, sp) * f.group + 1.5) + (sp > 1 ? 3.0 + 2e-6 * sp * M * N : 0.0);
+                const double t = waves * ((double)ceil_div(n_g, sp) * f.group + 1.5) + (sp > 1 ? 3.0 + (4.0 * sp * M * N < 64e6 ? 1e-6 : 2e-6) * sp * M * N : 0.0);
                 if (t < best) {
                     best = t;
                     cg = f.cg;
