@@ -587,9 +587,31 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if (warp == 3) tmem_free<CG>(tmem, 512);
 }
 
+// 16 bytes of a row of any alignment from byte 16 c on, zeros behind its `bytes`: from the five aligned
+// words that hold them.  Nothing outside the row's words is read; the first row's start is one of a word.
+__device__ __forceinline__ uint4 padded_chunk(const uint8_t* row, int64_t bytes, int64_t c) {
+    const int off = (int)((uintptr_t)row & 3);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(row - off) + 4 * c;   // (in front of a row lies the one before it)
+    const int64_t left = bytes + off - 16 * c;   // bytes from the first word to the row's end
+    uint32_t w[5];
+    if (left >= 20) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = __ldg(words + i);
+    } else {
+        const uint8_t* b = reinterpret_cast<const uint8_t*>(words);
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            w[i] = 0;
+            for (int k = 0; k < 4; ++k)
+                if (4 * i + k < left) w[i] |= (uint32_t)b[4 * i + k] << (8 * k);
+        }
+    }
+    return make_uint4(__funnelshift_r(w[0], w[1], 8 * off), __funnelshift_r(w[1], w[2], 8 * off),
+                      __funnelshift_r(w[2], w[3], 8 * off), __funnelshift_r(w[3], w[4], 8 * off));
+}
+
 // Rows of `bytes` bytes, `ld` apart and of any alignment (the first one of 16), to rows of `to` bytes, a
-// multiple of 16, with zeros behind: what TMA can read.  A lane makes 16 bytes from the five aligned words
-// that hold them; nothing outside a row's words is read.
+// multiple of 16, with zeros behind: what TMA can read.
 static __global__ void __launch_bounds__(256) k_pad_rows(const uint8_t* __restrict__ src, int64_t ld, uint8_t* __restrict__ dst,
                                                          int64_t rows, int64_t bytes, int64_t to) {
     after_previous();
@@ -598,30 +620,37 @@ static __global__ void __launch_bounds__(256) k_pad_rows(const uint8_t* __restri
     const int64_t per_row = (to / 16 + 31) / 32, n = rows * per_row;
     for (int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); id < n; id += (int64_t)gridDim.x * 8) {
         const int64_t r = id / per_row, c = (id - r * per_row) * 32 + (threadIdx.x & 31);
-        if (c >= to / 16) continue;
-        const uint8_t* row = src + r * ld;
-        const int off = (int)((uintptr_t)row & 3);
-        const uint32_t* words = reinterpret_cast<const uint32_t*>(row - off) + 4 * c;   // (in front of a row lies the one before it)
-        const int64_t left = bytes + off - 16 * c;   // bytes from the first word to the row's end
-        uint32_t w[5];
-        if (left >= 20) {
+        if (c < to / 16) reinterpret_cast<uint4*>(dst + r * to)[c] = padded_chunk(src + r * ld, bytes, c);
+    }
+}
+// The way back, for rows of 16-bit elements: rows of `cols` elements, ld (more, a multiple of 8) apart and
+// aligned, side by side.  A thread writes 8 elements of the whole; they lie in one row mostly, in five
+// words of it.
+static __global__ void __launch_bounds__(256) k_join_rows(const uint16_t* __restrict__ src, int64_t ld, uint16_t* __restrict__ dst,
+                                                          int64_t rows, int64_t cols) {
+    after_previous();
+    let_next_start();
+    const int64_t n = rows * cols, chunks = (n + 7) / 8;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < chunks; q += (int64_t)gridDim.x * 256) {
+        int64_t r = 8 * q / cols, c = 8 * q - r * cols;
+        if (c + 8 <= cols && 8 * q + 8 <= n) {
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(src + r * ld) + c / 2;   // (the fifth ends within ld, as cols < ld)
+            const int off = (int)(c & 1) * 16;
+            uint32_t w[5];
 #pragma unroll
-            for (int i = 0; i < 5; ++i) w[i] = __ldg(words + i);
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(words + i);
+            w[4] = off ? __ldg(words + 4) : 0;
+            reinterpret_cast<uint4*>(dst)[q] = make_uint4(__funnelshift_r(w[0], w[1], off), __funnelshift_r(w[1], w[2], off),
+                                                          __funnelshift_r(w[2], w[3], off), __funnelshift_r(w[3], w[4], off));
         } else {
-            const uint8_t* b = reinterpret_cast<const uint8_t*>(words);
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                w[i] = 0;
-                for (int k = 0; k < 4; ++k)
-                    if (4 * i + k < left) w[i] |= (uint32_t)b[4 * i + k] << (8 * k);
+            for (int k = 0; k < 8 && 8 * q + k < n; ++k) {
+                dst[8 * q + k] = src[r * ld + c];
+                if (++c == cols) {
+                    c = 0;
+                    ++r;
+                }
             }
         }
-        uint4 o;
-        o.x = __funnelshift_r(w[0], w[1], 8 * off);
-        o.y = __funnelshift_r(w[1], w[2], 8 * off);
-        o.z = __funnelshift_r(w[2], w[3], 8 * off);
-        o.w = __funnelshift_r(w[3], w[4], 8 * off);
-        reinterpret_cast<uint4*>(dst + r * to)[c] = o;
     }
 }
 

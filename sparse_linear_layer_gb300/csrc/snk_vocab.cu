@@ -203,9 +203,9 @@ template <typename T>
 struct StoreEpilogue {
     struct Args {
         T* out;                  // [width, cols]
-        int64_t width, cols;
+        int64_t width, cols;     // (cols a multiple of 8)
         GradScale scale;
-        int vec;                 // elements per store: 16, 8 or 1, by the rows' alignment
+        int vec;                 // elements per store: 16 or 8, by the rows' alignment
     };
     template <class Source>
     __device__ static void run(const Args& a, const DenseTile& t, const Source& from) {
@@ -227,13 +227,9 @@ struct StoreEpilogue {
                 for (int i = 0; i < 8; ++i) w[i] = two<T>(v[j + 2 * i], v[j + 2 * i + 1]);
                 if (a.vec == 16 && b + j + 16 <= lim) {
                     store32(out + b + j, w);
-                } else if (a.vec >= 8) {   // (cols is then a multiple of 8, and so is lim)
+                } else {   // (lim is a multiple of 8 too)
                     if (b + j < lim) *reinterpret_cast<uint4*>(out + b + j) = make_uint4(w[0], w[1], w[2], w[3]);
                     if (b + j + 8 < lim) *reinterpret_cast<uint4*>(out + b + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (b + j + i < lim) out[b + j + i] = from_f32<T>(v[j + i]);
                 }
             }
         }
@@ -350,8 +346,8 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const RowsArgs a) {
 #pragma unroll 4
             for (int64_t c = lane; c < n16; c += 32) reinterpret_cast<uint4*>(to)[c] = __ldg(reinterpret_cast<const uint4*>(from) + c);
         } else {
-#pragma unroll 4
-            for (int64_t c = lane; c < a.ld; c += 32) to[c] = c < a.cols ? from[c] : from_f32<T>(0.f);
+            for (int64_t c = lane; c < a.ld / 8; c += 32)
+                reinterpret_cast<uint4*>(to)[c] = padded_chunk(reinterpret_cast<const uint8_t*>(from), 2 * a.cols, c);
         }
     }
     // zeros from the last row that counts up to the last tile that holds one
@@ -821,13 +817,23 @@ int backward(const Shape& h, const BackwardPlan& p, const void* wt, int reductio
             if (int st = launch<false, true, SumEpilogue>(p.x, mz, mw_t, a, es, num_sms, s); st != SNK_OK) return st;
         }
         if (dw) {
-            T* out = static_cast<T*>(dw) + v0 * h.cols;
-            a = dense_args(p.w, bf, true, true, width, h.cols, h.rows);
+            // Rows that are not whole 16-byte chunks go over the weight's padded copy, of which this piece has
+            // been read, and from there side by side (20 x 1001 -> 50257, written from the tiles by 2 bytes: 557 us).
+            T* end = static_cast<T*>(dw) + v0 * h.cols;
+            T* out = h.pads() ? static_cast<T*>(p.wc) + v0 * h.ld : end;
+            a = dense_args(p.w, bf, true, true, width, h.ld, h.rows);
             a.rows = p.count;
             a.rows_k = 1;
-            const int vec = h.pads() ? 1 : (h.cols % 16 == 0 && ((uintptr_t)out & 31) == 0 ? 16 : 8);
-            const typename StoreEpilogue<T>::Args eo{out, width, h.cols, scale, vec};
+            const int vec = h.ld % 16 == 0 && ((uintptr_t)out & 31) == 0 ? 16 : 8;
+            const typename StoreEpilogue<T>::Args eo{out, width, h.ld, scale, vec};
             if (int st = launch<true, true, StoreEpilogue<T>>(p.w, mz_t, mx_t, a, eo, num_sms, s); st != SNK_OK) return st;
+            if (h.pads()) {
+                const int64_t blocks = std::min<int64_t>(ceil_div(width * h.cols, 2048), 1 << 20);
+                if (int st = launch_after(k_join_rows, (unsigned)blocks, 256, 0, 1, s, reinterpret_cast<const uint16_t*>(out), h.ld,
+                                          reinterpret_cast<uint16_t*>(end), width, h.cols);
+                    st != SNK_OK)
+                    return st;
+            }
         }
     }
     if (dx) {

@@ -323,6 +323,26 @@ def test_several_pieces():
     check_gradients(dx, dw, xd, wd, t, torch.ones(rows, device="cuda"))
 
 
+@pytest.mark.parametrize("cols", [9, 1])
+def test_several_pieces_of_odd_rows(cols):
+    x, w, t = case(2000, cols, 140001, torch.float16, ignored=0.1, seed=11)
+    x.requires_grad_()
+    w.requires_grad_()
+    g = torch.randn(2000, device="cuda")
+    dx, dw = torch.autograd.grad(dense.linear_cross_entropy(x, w, t, reduction="none"), (x, w), g)
+    check_gradients(dx, dw, x.detach(), w.detach(), t, g)
+
+
+@pytest.mark.parametrize("rows,cols,vocab", [(1, 1001, 50257), (300, 7, 4001), (40, 15, 9), (5, 3, 1), (64, 2047, 3000)])
+def test_odd_rows(rows, cols, vocab):
+    """Gradients whose rows begin anywhere in a word."""
+    x, w, t = case(rows, cols, vocab, torch.bfloat16, ignored=0, seed=rows)
+    x.requires_grad_()
+    w.requires_grad_()
+    dx, dw = torch.autograd.grad(dense.linear_cross_entropy(x, w, t, reduction="sum"), (x, w))
+    check_gradients(dx, dw, x.detach(), w.detach(), t, torch.ones(rows, device="cuda"))
+
+
 def test_repeats_views_and_streams():
     x, w, t = case(300, 72, 900, torch.bfloat16)
     a = dense.linear_cross_entropy(x, w, t, reduction="none")
