@@ -413,6 +413,32 @@ def test_one_gradient_only():
     assert torch.equal(dw, torch.autograd.grad(dense.linear_cross_entropy(x, a, t), a)[0])
 
 
+def test_one_gradient_only_of_odd_rows():
+    x, w, t = case(150, 77, 500, torch.bfloat16)
+    both = [v.detach().requires_grad_() for v in (x, w)]
+    dx, dw = torch.autograd.grad(dense.linear_cross_entropy(*both, t), both)
+    check_gradients(dx, dw, x, w, t, torch.full((150,), 1.0 / (t != -100).sum().item(), device="cuda"))
+    a = x.detach().requires_grad_()
+    assert torch.equal(dx, torch.autograd.grad(dense.linear_cross_entropy(a, w, t), a)[0])
+    a = w.detach().requires_grad_()
+    assert torch.equal(dw, torch.autograd.grad(dense.linear_cross_entropy(x, a, t), a)[0])
+
+
+@pytest.mark.parametrize("rows,cols,vocab", [(1, 768, 20000), (300, 256, 4000), (40, 129, 3000)])
+def test_inputs_written_right_before_the_call(rows, cols, vocab):
+    """Nothing of a call may be read before the kernels in front of it have written it."""
+    sets = [case(rows, cols, vocab, torch.bfloat16, ignored=0, seed=s) for s in range(4)]
+    want = [dense.linear_cross_entropy(*s, reduction="none") for s in sets]
+    x, w, t = (v.clone() for v in sets[0])
+    got = []
+    for i in range(24):
+        for to, v in zip((x, w, t), sets[i % 4]):
+            to.copy_(v)
+        got.append(dense.linear_cross_entropy(x, w, t, reduction="none"))
+    for i, l in enumerate(got):
+        assert torch.equal(l, want[i % 4])
+
+
 def test_refusals():
     x, w, t = case(4, 16, 50, torch.bfloat16)
     for bad in [(x.float(), w.float(), t), (x, w.half(), t), (x, w[:, :8], t), (x, w, t.int()), (x, w, t[:3]), (x.cpu(), w, t),
