@@ -100,6 +100,21 @@ def test_product(rows, out, cols, weight, dtype):
     assert torch.equal(y, q8.matmul(a, b, bias=bias, dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("weight", ["blocks", "rows"])
+@pytest.mark.parametrize("rows,out,cols,shift", [(512, 2048, 8192, 0), (512, 2048, 8192, 2), (520, 1030, 8000, 0), (2304, 768, 16384, 0)])
+def test_product_in_ranges(rows, out, cols, shift, weight, dtype):
+    """Few tiles and a long K: the sums of several ranges, joined by fours, or by ones where the output is not aligned."""
+    g = torch.Generator(device="cuda").manual_seed(rows + out)
+    a = q8.pack(torch.randn(rows, cols, device="cuda", generator=g), "e4m3", 128)
+    w = torch.randn(out, cols, device="cuda", generator=g)
+    b = q8.pack_blocks(w) if weight == "blocks" else q8.pack(w, "e4m3", 128)
+    bias = torch.randn(out, device="cuda", generator=g)
+    y = torch.empty(rows * out + 16, device="cuda", dtype=dtype)[shift:shift + rows * out].view(rows, out)
+    q8.matmul(a, b, bias=bias, dtype=dtype, out=y)
+    check_product(y, dense_ref.values(a.codes, a.scales), dense_ref.values(b.codes, b.scales, blocks=weight == "blocks"), bias)
+
+
 @pytest.mark.parametrize("rows", [2, 40, 300])
 def test_product_of_strided_and_shifted_codes(rows):
     """Rows further apart than they are long, with NaN codes between them, and codes that do not
