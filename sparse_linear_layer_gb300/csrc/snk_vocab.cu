@@ -32,7 +32,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kGatherRows = 256;    // rows per block of k_vocab_rows at most
-constexpr int kDirectRows = 128;    // up to these the forward reads x itself: one row tile either way
 constexpr float kDzScale = 8192.f;  // 2^13
 // Stages of an accumulator's turn in the loss: 64 MMA steps, whose additions truncate, towards
 // zero. At 4096 columns one accumulator leaves the mean loss off by 1.2e-6 of it, turns of 32
@@ -633,9 +632,11 @@ struct ForwardPlan {
     float *sums, *row_lse;
     int64_t bytes;
     ForwardPlan(const Shape& h, int num_sms, void* scratch) {
-        gather = h.rows > kDirectRows || h.pads();
         form = pick_form(h.rows, h.vocab, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms,
                          ceil_div(h.ld, kDenseK) <= kTurnStages ? 2 : 0);
+        // one row tile is one row tile whatever is left out: it reads x itself (333 x 1000 -> 32003, a dual
+        // tile: 31.8 us, with its rows gathered 38.0; 200 x 768 -> 32003 18.7 and 22.4)
+        gather = h.rows > form.rows() || h.pads();
         n_nt = (int)ceil_div(h.vocab, form.bn);
         per_block = 1;
         while (per_block < 8 && ceil_div(h.rows, per_block) > num_sms) per_block *= 2;

@@ -275,6 +275,18 @@ def test_what_ignored_rows_hold_reaches_nothing(rows):
         assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("rows,cols,vocab", [(200, 256, 9000), (500, 768, 20001), (513, 128, 20001), (250, 2048, 5000)])
+def test_what_ignored_rows_hold_reaches_no_loss(rows, cols, vocab):
+    """One row tile of any kind, which reads x as it is, and one row more."""
+    x, w, t = case(rows, cols, vocab, torch.bfloat16, seed=rows)
+    want = dense.linear_cross_entropy(x, w, t, reduction="none")
+    mean = dense.linear_cross_entropy(x, w, t)
+    check_loss(want, x, w, t)
+    x[t == -100] = float("nan")
+    assert torch.equal(dense.linear_cross_entropy(x, w, t, reduction="none"), want)
+    assert torch.equal(dense.linear_cross_entropy(x, w, t), mean)
+
+
 def test_other_targets_and_infinite_logits():
     x, w, t = case(150, 64, 300, torch.bfloat16, ignored=0)
     t[3], t[140] = 300, -1                       # out of range: NaN, and only there
