@@ -419,8 +419,17 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int i0 = (int)((int64_t)n_k * it.split / a.splits), i1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
+                // a turn's stages: from floor(n turn / turns) on, counted (the product of a long K's stages and its
+                // turns passes 32 bits)
+                const int whole = TURNS ? (i1 - i0) / turns : i1 - i0, rest = i1 - i0 - whole * turns;
+                int k1 = i0, over = 0;
                 for (int turn = 0; turn < turns; ++turn, ++u, q += SUBS) {
-                    const int k0 = i0 + (i1 - i0) * turn / turns, k1 = i0 + (i1 - i0) * (turn + 1) / turns;
+                    const int k0 = k1;
+                    k1 += whole;
+                    if (TURNS && (over += rest) >= turns) {
+                        over -= turns;
+                        ++k1;
+                    }
                     if ((u & 1) != mine) {
                         r.skip(k1 - k0);
                         continue;
