@@ -15,9 +15,16 @@ namespace snk {
 // may shorten it (SNK_TC_WAIT_CYCLES) to exercise the abort path.  A wait
 // that runs out stops the CTA's pipeline: every role then waits, with the
 // fixed drain limit, for the copies and MMAs it has issued, the outputs are
-// written as NaN and the status word records kStatLimit.
+// written as NaN and the status word records kStatLimit.  (mbarrier.try_wait may
+// itself suspend a thread for longer than a short limit; with SNK_TC_WAIT_POLL
+// waits ask without suspending.)
 #ifndef SNK_TC_WAIT_CYCLES
 #define SNK_TC_WAIT_CYCLES 4000000000LL
+#endif
+#ifdef SNK_TC_WAIT_POLL
+#define SNK_TC_WAIT "test_wait"
+#else
+#define SNK_TC_WAIT "try_wait"
 #endif
 constexpr long long kTcWaitCycles = SNK_TC_WAIT_CYCLES;
 constexpr long long kTcDrainCycles = 4000000000LL;
@@ -49,7 +56,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, long lon
     for (int spin = 0;; ++spin) {
         uint32_t ok;
         asm volatile(
-            "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+            "{ .reg .pred p; mbarrier." SNK_TC_WAIT ".parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
             : "=r"(ok)
             : "r"(smem_u32(b)), "r"(parity)
             : "memory");
