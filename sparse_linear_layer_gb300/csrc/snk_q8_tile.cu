@@ -6,10 +6,10 @@
 // packed from there.  Bound by memory: every element is read once and
 // written as one byte per form.
 //
-// A wait for a tile that runs out (kTcWaitCycles) leaves NaN: in the scales and sums of what
-// the waiting thread reads of it.  The thread that brings the tiles waits on, with
-// kTcDrainCycles, before it brings another one to the same place; if that runs out too it brings
-// no more, and all that the block still has to write is NaN.
+// A wait for a tile that runs out (kTcWaitCycles) leaves NaN, in the scales and sums of what
+// the waiting thread reads of this tile and of all that follow.  The thread that brings the tiles
+// then brings no more, so that nothing comes to a place whose last copy may still be on its way,
+// and waits at its end, with kTcDrainCycles, for the copies that it has started.
 #include <algorithm>
 #include <type_traits>
 
@@ -55,7 +55,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
     unsigned char* turned = tiles + BUFS * BYTES;   // [column][16-byte chunk of rows, exclusive-or (column / CW) % 8]
     __shared__ float most_s[CW][kTileThreads], sums_s[CW][kTileThreads];
     __shared__ uint64_t full[BUFS];
-    __shared__ bool lost;   // a copy never came
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int64_t n_tiles = a.tiles_r * a.tiles_c;
     after_previous();
@@ -67,7 +66,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
     };
     if constexpr (LOAD == kTileTma) {
         if (t == 0) {
-            lost = false;
             for (int b = 0; b < BUFS; ++b) mbar_init(&full[b], 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             for (int b = 0; b < BUFS; ++b)
@@ -77,15 +75,19 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
     }
     int buf = 0;
     uint32_t parity = 0;
+    bool ok = true;     // no wait of this thread's has run out
+    int64_t lost = 0;   // else the tile that it waited for
     for (int64_t id = blockIdx.x; id < n_tiles; id += gridDim.x) {
         const int64_t tr = id / a.tiles_c, tc = id - tr * a.tiles_c;
         const int64_t r0 = tr * kTile, c0 = tc * kTile;
         const int nr = (int)min((int64_t)kTile, a.rows - r0), nc = (int)min((int64_t)kTile, a.cols - c0);
         T* sm = reinterpret_cast<T*>(tiles + buf * BYTES);
-        float most;
-        bool ok = true;
+        float most = 0.f;
         if constexpr (LOAD == kTileTma) {
-            ok = !lost && (mbar_wait(&full[buf], parity) || (t == 0 && mbar_wait(&full[buf], parity, kTcDrainCycles)));
+            if (ok && !mbar_wait(&full[buf], parity)) {
+                ok = false;
+                lost = id;
+            }
         } else {
             const T* x = static_cast<const T*>(a.x) + r0 * a.cols + c0;
 #pragma unroll 4
@@ -96,8 +98,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
             }
             __syncthreads();
         }
-        const float start = ok ? 0.f : __int_as_float(0x7fc00000);   // of this thread's maxima and sums
-        most = start;
+        if (!ok) most = __int_as_float(0x7fc00000);
         // ---- along the columns: a warp's 16 rows, four columns a lane
         uint8_t* row_codes = a.codes + r0 * a.ld + c0 + 4 * lane;
         const bool words = a.ld % 4 == 0 && ((uintptr_t)a.codes & 3) == 0 && 4 * lane + 4 <= nc;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
             if constexpr (!BLOCKS) {
 #pragma unroll
                 for (int k = 0; k < CW; ++k) {
-                    float m = start, s = start;
+                    float m = ok ? 0.f : __int_as_float(0x7fc00000), s = 0.f;
 #pragma unroll
                     for (int i = 0; i < RT; i += 2) m = max_abs(m, value(i, k), value(i + 1, k));
                     if (a.part) {
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
                     const int c = word * CW + k;
                     if (h == 0 && c < nc) {
                         if (a.codes_t) a.scales_t[(c0 + c) * a.tiles_r + tr] = q[k].scale;
-                        if (a.part) a.part[tr * a.cols + c0 + c] = s;
+                        if (a.part) a.part[tr * a.cols + c0 + c] = m == m ? s : m;   // (a wait ran out, or a value is NaN)
                     }
                 }
             }
@@ -258,18 +259,20 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_q8_tile(const __grid_consta
                 }
             }
         }
-        if constexpr (LOAD == kTileTma) {
-            if (t == 0 && !ok && !lost) {   // nothing is brought after this; what may still be on its way is the other place's
-                if (BUFS == 2 && id + gridDim.x < n_tiles) mbar_wait(&full[buf ^ 1], buf ? parity ^ 1 : parity, kTcDrainCycles);
-                lost = true;
-            }
-        }
         __syncthreads();   // the tile and the exchanged maxima are free
         if constexpr (LOAD == kTileTma) {
             if (t == 0 && ok && id + (int64_t)BUFS * gridDim.x < n_tiles) fetch(id + (int64_t)BUFS * gridDim.x, buf);
             if (++buf == BUFS) {
                 buf = 0;
                 parity ^= 1;
+            }
+        }
+    }
+    if constexpr (LOAD == kTileTma) {
+        if (t == 0 && !ok) {
+            for (int b = 0; b < BUFS && lost < n_tiles; ++b, lost += gridDim.x) {
+                const uint32_t j = (uint32_t)((lost - blockIdx.x) / gridDim.x);   // the block's how manieth
+                mbar_wait(&full[j % BUFS], (j / BUFS) & 1, kTcDrainCycles);
             }
         }
     }
