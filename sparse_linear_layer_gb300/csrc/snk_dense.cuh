@@ -13,9 +13,11 @@
 //   warp 3     owns the TMEM allocation, two accumulators of up to 256 columns that take turns;
 //   warps 4-11 the epilogue: warp w reads the TMEM lanes 32 (w % 4) .. + 31 and, by
 //              w < 8 or not, the first or second half of the columns.
-// Every wait is bounded (kTcWaitCycles); a role whose wait ran out stops, waits for the
-// copies and MMAs that it has issued, and the epilogue writes NaN for every tile that it
-// has not been given.
+// Every wait is bounded (kTcWaitCycles). A producer or an issuing thread whose wait ran out
+// stops; an epilogue warp whose wait ran out writes NaN for that tile and all that it still has,
+// and gives no accumulator back any more: arrivals are only counted, and one too many would
+// stand for a warp that still reads. The others then run out too. No CTA ends before its copies
+// have landed (land_all) and its MMAs are done (fin), whoever stopped.
 #pragma once
 
 #include "snk_q8.cuh"
@@ -140,6 +142,55 @@ __device__ __forceinline__ void dense_commit(uint64_t* bar) {
                 smem_u32(bar)),
             "h"((uint16_t)3)
             : "memory");
+}
+// All MMAs of an issuing thread, whether it has stopped or not, arrive on fin; the TMEM's owner
+// waits for both threads' before it gives the memory back (each of them ends after a few
+// bounded waits).
+__device__ __forceinline__ void wait_for_mmas(uint64_t (&fin)[2]) {
+    for (int i = 0; i < 2; ++i) mbar_wait(&fin[i], 0, 4 * kTcDrainCycles);
+}
+// What the second CTA's producer tells the first one at its end, in the first one's memory.
+struct PairEnd {
+    uint64_t bar;      // one arrival
+    uint32_t issued;   // stages that it has loaded
+};
+// Every copy of the stages that the CTA (pair) has loaded has landed.  Called by each producer at its end with
+// the number of stages that it has loaded; w % stages is stage w's slot, bytes what a CTA loads of a stage.  The
+// first CTA's barriers count the copies of both.  Where one CTA stopped earlier than the other (the issuing
+// threads have stopped too then, and are waited for first), the stages that only one of them has loaded
+// are counted as far as they were loaded.
+template <int CG>
+__device__ __forceinline__ void land_all(uint64_t* full, uint64_t (&fin)[2], PairEnd& peer, int rank, uint32_t issued, int stages,
+                                         uint32_t bytes) {
+    uint32_t other = issued;
+    if constexpr (CG == 2) {
+        if (rank == 1) {
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first_cta(&peer.issued)), "r"(issued) : "memory");
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_cta(&peer.bar)) : "memory");
+            return;
+        }
+        bool told = false;
+        for (const long long t0 = clock64(); !told && clock64() - t0 < 4 * kTcDrainCycles;) {
+            uint32_t ok;
+            asm volatile(
+                "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0; selp.u32 %0, 1, 0, p; }"
+                : "=r"(ok)
+                : "r"(smem_u32(&peer.bar))
+                : "memory");
+            told = ok;
+        }
+        if (told) other = *reinterpret_cast<volatile uint32_t*>(&peer.issued);
+        if (other != issued) {
+            wait_for_mmas(fin);
+            for (uint32_t w = other; w < issued; ++w)
+                asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[w % stages])), "r"(bytes)
+                             : "memory");
+            for (uint32_t w = issued; w < other; ++w) mbar_expect_tx(&full[w % stages], bytes);
+        }
+    }
+    const uint32_t end = max(issued, other);
+    for (uint32_t w = end > (uint32_t)stages ? end - stages : 0; w < end; ++w)
+        mbar_wait(&full[w % stages], (w / stages) & 1, kTcDrainCycles);
 }
 // A 2-d box into this CTA's memory, counted on `bar` (of a pair: the first CTA's).
 template <int CG>
@@ -285,15 +336,6 @@ struct Stages {
         parity ^= (uint32_t)laps & 1;
     }
 };
-// The stages that a producer filled last have landed.
-__device__ __forceinline__ void drain_last(uint64_t* full, const Stages& r, bool all) {
-    for (int i = 0; i < r.n; ++i) {   // oldest first: slots before r.slot are of this round
-        const bool older = r.slot + i >= r.n;
-        const int slot = older ? r.slot + i - r.n : r.slot + i;
-        if (older || all) mbar_wait(&full[slot], older ? r.parity : r.parity ^ 1, kTcDrainCycles);
-    }
-}
-
 // Stages by which a dual tile's first accumulator goes ahead of its second at a tile's start (8192 x 768 ->
 // 50257, the loss: 391 us before it did, 386 with 1, 380 with 2 or 3, 385 with 4, which is all there are).
 constexpr int kDenseLead = 3;
@@ -313,6 +355,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     extern __shared__ __align__(1024) unsigned char dense_raw[];
     unsigned char* sm = dense_raw + ((1024 - (smem_u32(dense_raw) & 1023)) & 1023);
     __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin[2], hand[2];
+    __shared__ PairEnd peer;
     __shared__ uint32_t tmem_base;
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -328,6 +371,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             mbar_init(&fin[i], 1);
             mbar_init(&hand[i], 1);
         }
+        mbar_init(&peer.bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 3) tmem_alloc<CG>(&tmem_base, 512);
@@ -364,6 +408,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         fewer_registers<kRoleRegs>();
         if (warp == 0 && lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
+            uint32_t issued = 0;
             Stages r(a.stages);
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
@@ -398,9 +443,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     }
                     r.next();
                     used |= r.slot == 0;
+                    ++issued;
                 }
             }
-            if (!ok && rank == 0) drain_last(full, r, used);   // (the other CTA's copies among them)
+            land_all<CG>(full, fin, peer, rank, issued, a.stages, stage);
         }
         // One thread for all turns left the tensor cores idle for 850 cycles where they changed the
         // accumulator: its waits and commits, with nothing queued behind the last MMA.  The other
@@ -408,7 +454,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         // barrier's phase is known by its parity only, so nobody may wait for one while an earlier
         // phase of that barrier is still open.  The word comes when all stages but the turn's last
         // have been waited for; the next turn's first stage is then at most the second in the ring
-        // that is open, and its accumulators' earlier phases are past.
+        // that is open, and its accumulators' earlier phases are past.  (A stage is given back after the
+        // next one has been waited for, or not at all: the ring does not come around to one that nobody saw.)
         if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
             const uint32_t mine = warp - 1;
             bool ok = true;
@@ -485,7 +532,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                                     const int s = r.slot;
                                     r.next();
                                     multiply(s, sub, k > k0, (k + 1 == ahead) == (sub == 1) && k + 1 < k1, r);
-                                    if (sub == 1) dense_commit<CG>(&empty[s]);
+                                    if (sub == 1 && ok) dense_commit<CG>(&empty[s]);
                                 }
                             }
                         }
@@ -500,18 +547,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                             if (k + 1 == k1) dense_commit<CG>(&accf[0]);
                             multiply(s, 1, k > k0, k + 1 < k1, r);
                         }
-                        dense_commit<CG>(&empty[s]);
+                        if (ok) dense_commit<CG>(&empty[s]);
                     }
                     if (!ok) break;
                     if (!DUAL || k0 == k1) dense_commit<CG>(&accf[ab]);
                     if constexpr (DUAL) dense_commit<CG>(&accf[1]);
                 }
             }
-            if (!ok) {   // no MMA may still run when the memory is given back
-                dense_commit<CG>(&fin[mine]);
-                mbar_wait(&fin[mine], 0, kTcDrainCycles);
-            }
+            dense_commit<CG>(&fin[mine]);
         }
+        if (warp == 3 && lane == 0) wait_for_mmas(fin);
     } else {
         more_registers<kSumRegs>();
         const int half = warp >= 8 ? 1 : 0, quarter = warp & 3;
@@ -528,7 +573,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         auto release = [&] {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && ok) {
                 if constexpr (CG == 1) mbar_arrive(&acce[q & 1]);
                 else mbar_arrive_cluster(first_cta(&acce[q & 1]));
             }

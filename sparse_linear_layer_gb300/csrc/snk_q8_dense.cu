@@ -121,7 +121,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     float* scales = reinterpret_cast<float*>(turn + kDenseEpilogueWarps * kOutBytes);
     unsigned char* stages = turn + kDenseEpilogueWarps * kOutBytes + (ROWS ? kScaleSlots * (kDenseM + BN) * 4 : 0);
     const int a_bytes = a.a_rows * 128, stage = a_bytes + HB * 128;
+    const uint32_t stage_tx = (uint32_t)(stage + (ROWS ? (kDenseM + BN) * 4 : 0));   // with its scales
     __shared__ uint64_t full[S], empty[S], accf[NB], acce[NB], fin[2];
+    __shared__ PairEnd peer;
     __shared__ uint32_t tmem_base;
 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         }
         mbar_init(&fin[0], 1);
         mbar_init(&fin[1], 1);
+        mbar_init(&peer.bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 3) tmem_alloc<CG>(&tmem_base, 512);
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     }
                     unsigned char* sa = stages + s * stage;
                     unsigned char* sb = sa + a_bytes;
-                    if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(stage + (ROWS ? (kDenseM + BN) * 4 : 0)) * CG);
+                    if (rank == 0) mbar_expect_tx(&full[s], stage_tx * CG);
                     const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : first_cta(&full[s]);
                     dense_load<CG>(sa, &map_a, g * 128, m0, bar);
                     dense_load<CG>(sb, &map_b, g * 128, n0, bar);
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     used |= r.slot == 0;
                 }
             }
-            if (!ok && rank == 0) drain_last(full, r, used);
+            land_all<CG>(full, fin, peer, rank, w, a.stages, stage_tx);
         }
         // Two threads issue, one the even groups and one the odd ones: a group takes the tensor
         // cores 512 cycles, but its thread 1000 (issue blocks while they are busy, and two
@@ -210,11 +213,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     dense_commit<CG>(&empty[s]);
                 }
             }
-            if (!ok) {
-                dense_commit<CG>(&fin[mine]);
-                mbar_wait(&fin[mine], 0, kTcDrainCycles);
-            }
+            dense_commit<CG>(&fin[mine]);
         }
+        if (warp == 3 && lane == 0) wait_for_mmas(fin);
     } else {
         more_registers<kSumRegs>();
         const int half = warp >= 8 ? 1 : 0, quarter = warp & 3;
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     } else {   // all read: the accumulator is free before its last columns are added
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (lane == 0 && ok) {   // (no arrival after a wait that ran out, as in k_dense)
                             if constexpr (CG == 1) mbar_arrive(&acce[ab]);
                             else mbar_arrive_cluster(free0 + 8 * ab);
                         }
