@@ -46,6 +46,9 @@ struct Calls {
 struct Wrong : std::runtime_error {   // becomes ValueError
     using std::runtime_error::runtime_error;
 };
+struct NoTangent : std::runtime_error {   // becomes NotImplementedError
+    using std::runtime_error::runtime_error;
+};
 struct Status {
     int status;
     const char* call;
@@ -198,6 +201,8 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
         Py_XDECREF(args);
     } catch (const Wrong& e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, e.what());
+    } catch (const NoTangent& e) {
+        PyErr_SetString(PyExc_NotImplementedError, e.what());
     } catch (const c10::OutOfMemoryError& e) {
         PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
     } catch (const std::exception& e) {
@@ -614,6 +619,14 @@ variable_list backward_pass(F f) {
     }
 }
 bool wants_gradient(const at::Tensor& t) { return at::GradMode::is_enabled() && t.defined() && t.requires_grad(); }
+// A tensor of forward-mode differentiation needs no gradient: without this its result would have no tangent, which
+// counts as a derivative of zero.
+void refuse_tangents(std::initializer_list<const at::Tensor*> inputs) {
+    if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+    for (const at::Tensor* t : inputs)
+        if (t->defined() && t->_fw_grad(0).defined())
+            throw NoTangent("this operation has no forward-mode derivative (its gradients are those of the backward pass)");
+}
 void* current_stream(const at::Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
 
 struct HeadFunction : torch::autograd::Function<HeadFunction> {
@@ -646,6 +659,7 @@ PyObject* op_linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor x = tensor(a[0], "x").contiguous(), w = tensor(a[1], "weight").contiguous();
         const at::Tensor target = tensor(a[2], "target").contiguous();
         const int64_t ignore = integer(a[3]), reduction = integer(a[4]);
+        refuse_tangents({&x, &w});
         if (wants_gradient(x) || wants_gradient(w))
             return THPVariable_Wrap(HeadFunction::apply(x, w, target, ignore, reduction));
         Head h(x, w, target, ignore, reduction);
@@ -778,6 +792,7 @@ PyObject* op_linear_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& x = tensor(a[0], "x");
         const at::Tensor w = tensor(a[1], "weight").contiguous();
         const at::Tensor bias = optional(a[2], "bias");
+        refuse_tangents({&x, &w, &bias});
         if (x.dim() < 1 || x.size(-1) < 1 || !x.is_cuda()) throw Wrong("x is a CUDA tensor [..., cols] with cols >= 1: " + what(x));
         const at::Tensor x2 = x.dim() == 2 && x.is_contiguous() ? x : x.reshape({x.numel() / x.size(-1), x.size(-1)}).contiguous();
         require_layer(x2, w, bias);
