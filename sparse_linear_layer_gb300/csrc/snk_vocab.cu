@@ -100,13 +100,14 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 struct GradScale {
     const uint32_t* most;     // bits of the largest finite |g_r|
     const float* uniform;     // the upstream gradient of all rows, or null
-    // 1 / G, G the power of two at or above the largest finite |g| (1 where that is 0 or too small to invert)
-    __device__ __forceinline__ float inverse() const {
-        const int e = (int)(__ldg(most) >> 23);   // biased exponent: |g| < 2^(e - 126)
-        return e < 2 || e > 252 ? 1.f : __uint_as_float((uint32_t)(253 - e) << 23);
+    // Row by row: in() = 2^13 / G = 2^(139 - e), G the power of two above the largest finite |g|, e that one's
+    // biased exponent (|g| < 2^(e - 126)), and out() = 2^(e - 139).  From e = 13 on both are normal numbers, for all
+    // finite g; below (|g| < 2^-114) in() stays at 2^126, and |g in()| < 2^12.
+    __device__ __forceinline__ uint32_t exponent() const { return max(__ldg(most) >> 23, 13u); }
+    __device__ __forceinline__ float in() const { return uniform ? kDzScale : __uint_as_float((266 - exponent()) << 23); }
+    __device__ __forceinline__ float out() const {
+        return uniform ? __ldg(uniform) * (1.f / kDzScale) : __uint_as_float((exponent() - 12) << 23);
     }
-    __device__ __forceinline__ float in() const { return uniform ? kDzScale : inverse() * kDzScale; }
-    __device__ __forceinline__ float out() const { return uniform ? __ldg(uniform) * (1.f / kDzScale) : 1.f / (inverse() * kDzScale); }
 };
 
 template <typename T>

@@ -36,3 +36,43 @@ def test_loss_of_rows_whose_turns_pass_32_bits(cols):
     want = z.logsumexp(0) - z[:2]
     tol = 2 * (128 + 0.005 * cols) * 2.0 ** -24 * z.abs().max() + 1e-6
     assert tol < 0.05 and bool(((got - want).abs() <= tol).all()), (got, want, tol)
+
+
+def reference(x, w, t, g):
+    """(dx, dw, |dz| |w|, |dz|^T |x|) in 64 bits."""
+    x, w = x.double(), w.double()
+    p = torch.softmax(x @ w.T, 1)
+    p[torch.arange(len(t)), t.clamp_min(0)] -= 1
+    dz = torch.where((t >= 0)[:, None], p * g.double()[:, None], 0)
+    return dz @ w, dz.T @ x, dz.abs() @ w.abs(), dz.abs().T @ x.abs()
+
+
+def within(got, want, magnitudes, dtype, least):
+    """Two roundings to 16 bits (dz and the result) and fp32 sums of a few hundred terms, the latter within
+    2^-14 of the terms' magnitudes; least: what the type's (or dz's) smallest steps add."""
+    tol = 1.01 * UNIT[dtype] * (magnitudes + want.abs()) + 2.0 ** -14 * magnitudes + least
+    return bool(((got.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("size", [2.0 ** -149, 1e-42, 1e-38, 3e-37, 1.4e-36, 2.4e-35, 1e-30, 1.0, 1e30, 1.7e38, 3.4e38])
+def test_upstream_gradients_at_the_ends_of_fp32(dtype, size):
+    """Losses row by row, upstream gradients up to `size`, one of them zero, one row left out.  Whether a result
+    is a number of the type or an infinity is the reference's, rounded."""
+    torch.manual_seed(1)
+    x, w = torch.randn(6, 40, device="cuda").to(dtype), (0.5 * torch.randn(30, 40, device="cuda")).to(dtype)
+    t = torch.tensor([3, 0, -100, 29, 7, 7], device="cuda")
+    g = torch.tensor([1.0, 0.0, 3e38, -1.0, 0.5, 0.25], device="cuda") * torch.tensor([size] * 2 + [1.0] + [size] * 3, device="cuda")
+    a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+    dx, dw = torch.autograd.grad(dense.linear_cross_entropy(a, b, t, reduction="none"), (a, b), g)
+    assert bool((dx[1] == 0).all()) and bool((dx[2] == 0).all())
+    want_x, want_w, mx, mw = reference(x, w, t, g)
+    top = torch.finfo(dtype).max
+    # steps of the type below its normal numbers; dz in fp16 has steps of 2^-24 / 8192 of G, the sum's fp32 of 2^-149
+    least = torch.finfo(dtype).tiny * torch.finfo(dtype).eps + 2.0 ** -149 + (2 * size * 2.0 ** -37 * 30 * 4 if dtype == torch.float16 else 0)
+    for got, want, m in ((dx, want_x, mx), (dw, want_w, mw)):
+        assert not bool(got.isnan().any())
+        fits = (want.abs() + 4 * UNIT[dtype] * m) < top
+        assert within(got[fits], want[fits], m[fits], dtype, least), (got, want)
+        over = (want.abs() - 4 * UNIT[dtype] * m) > 1.01 * top
+        assert bool(got[over].isinf().all())
