@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(256) k_vocab_dx(const float* __restrict__ slab
             __syncthreads();
         }
         if (!in || first > 0) continue;
-        f.mul(scale);
+        if (k >= 0) f.mul(scale);   // (an ignored row stays zero whatever the scale is)
         T* out = dx + r * cols + c;
         if (ld == cols) {
             store8(out, f);

@@ -1,6 +1,8 @@
 """The dense operators at the edges of what their calls take: very long rows and sums, upstream
 gradients at the ends of fp32, forward-mode differentiation, layers converted to 16 bits, and the
 entry points by the names of the C calls."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -76,3 +78,17 @@ def test_upstream_gradients_at_the_ends_of_fp32(dtype, size):
         assert within(got[fits], want[fits], m[fits], dtype, least), (got, want)
         over = (want.abs() - 4 * UNIT[dtype] * m) > 1.01 * top
         assert bool(got[over].isinf().all())
+
+
+@pytest.mark.parametrize("rows,cols", [(6, 40), (6, 41), (400, 64), (3, 2048)])
+@pytest.mark.parametrize("upstream", [math.inf, -math.inf, math.nan])
+def test_upstream_gradients_that_are_no_numbers_reach_no_ignored_row(rows, cols, upstream):
+    """A sum's or mean's upstream gradient multiplies every row that counts (an overflowed loss scale), and those only."""
+    torch.manual_seed(2)
+    x, w = torch.randn(rows, cols, device="cuda").bfloat16(), (0.5 * torch.randn(5000, cols, device="cuda")).bfloat16()
+    t = torch.arange(rows, device="cuda")
+    t[1::3] = -100
+    for reduction in ("sum", "mean"):
+        a = x.clone().requires_grad_()
+        dx, = torch.autograd.grad(dense.linear_cross_entropy(a, w, t, reduction=reduction), a, torch.tensor(upstream, device="cuda"))
+        assert bool((dx[t == -100] == 0).all()) and not bool(dx[t != -100].isfinite().any())
