@@ -791,8 +791,11 @@ PyObject* op_linear_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 3, [&] {
         const at::Tensor& x = tensor(a[0], "x");
         const at::Tensor w = tensor(a[1], "weight").contiguous();
-        const at::Tensor bias = optional(a[2], "bias");
+        at::Tensor bias = optional(a[2], "bias");
         refuse_tangents({&x, &w, &bias});
+        // a bias in 16 bits (a model converted as a whole) is added as the fp32 numbers that it holds; autograd rounds
+        // its gradient, a sum in fp32, to its type
+        if (bias.defined() && (bias.scalar_type() == at::kHalf || bias.scalar_type() == at::kBFloat16)) bias = bias.to(at::kFloat);
         if (x.dim() < 1 || x.size(-1) < 1 || !x.is_cuda()) throw Wrong("x is a CUDA tensor [..., cols] with cols >= 1: " + what(x));
         const at::Tensor x2 = x.dim() == 2 && x.is_contiguous() ? x : x.reshape({x.numel() / x.size(-1), x.size(-1)}).contiguous();
         require_layer(x2, w, bias);

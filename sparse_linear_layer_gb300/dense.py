@@ -44,15 +44,16 @@ def linear_q8(x, weight, bias=None):
     or each 128 x 128 block (weight); for the weight's gradient x and the upstream
     gradient have a scale for each 128 rows of a column.
 
-    x [..., cols] and weight [out, cols] are float32, float16 or bfloat16, each its own
-    type; bias [out] is float32.  The result and x's gradient have x's type, the weight's
-    gradient the weight's.  Sums are fp32; roundings to 8 bits are passed through as the
+    x [..., cols], weight [out, cols] and bias [out] are float32, float16 or bfloat16, each
+    its own type.  The result and x's gradient have x's type, the others' gradients theirs.
+    Sums are fp32; roundings to 8 bits are passed through as the
     identity, and x is kept for the backward pass as one byte per element."""
     return binding.ops().linear_q8(x, weight, bias)
 
 
 class Q8Linear(torch.nn.Module):
-    """linear_q8 as a layer: weight [out_features, in_features] and bias float32."""
+    """linear_q8 as a layer: weight [out_features, in_features] and bias float32, or what
+    the layer is converted to (.bfloat16(), .half())."""
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True, device=None):
         super().__init__()

@@ -92,3 +92,31 @@ def test_upstream_gradients_that_are_no_numbers_reach_no_ignored_row(rows, cols,
         a = x.clone().requires_grad_()
         dx, = torch.autograd.grad(dense.linear_cross_entropy(a, w, t, reduction=reduction), a, torch.tensor(upstream, device="cuda"))
         assert bool((dx[t == -100] == 0).all()) and not bool(dx[t != -100].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_projection_converted_to_16_bits(dtype):
+    """A converted layer gives what one with the same numbers in fp32 gives, and gradients rounded once."""
+    torch.manual_seed(3)
+    layer = dense.Q8Linear(200, 136).to(dtype)
+    with torch.no_grad():
+        layer.bias.normal_()
+    same = dense.Q8Linear(200, 136)
+    same.load_state_dict({k: v.float() for k, v in layer.state_dict().items()})
+    x = torch.randn(3, 50, 200, device="cuda").to(dtype)
+    dy = torch.randn(3, 50, 136, device="cuda").to(dtype)
+    outs = []
+    for m in (layer, same):
+        a = x.clone().requires_grad_()
+        y = m(a)
+        y.backward(dy)
+        outs.append((y, a.grad, m.weight.grad, m.bias.grad))
+    assert outs[0][2].dtype == dtype and outs[0][3].dtype == dtype
+    for got, want in zip(*outs):
+        assert torch.equal(got, want.to(dtype))
+    with torch.no_grad():
+        assert torch.equal(layer(x), outs[0][0])
+    with pytest.raises(ValueError):
+        dense.linear_q8(x, layer.weight, torch.zeros(136, device="cuda", dtype=torch.float64))
+    with pytest.raises(ValueError):
+        dense.linear_q8(x, layer.weight, torch.zeros(135, device="cuda", dtype=dtype))
