@@ -49,7 +49,7 @@ struct DenseArgs {
     int a_rows;            // rows of A that a CTA loads of a tile: 128, or fewer where there is one tile of fewer
     int stages;
     int splits;            // ranges of K, each an item of its own
-    int turns;             // accumulators that share an item's K (k_dense<.., TURNS>; else 1)
+    int turn_stages;       // k_dense<.., TURNS>: stages that an accumulator adds at most
     int64_t K;
     uint32_t idesc;
     const int32_t* rows;   // on the device: the rows of A (rows_k = 0) or the length of K (1) that count; null: all
@@ -401,6 +401,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const int half_b = a.bn / CG;   // rows of B that this CTA loads
     const int a_bytes = a.a_rows * 128, stage = (a.a_rows * SUBS + half_b) * 128;
     const uint32_t tx = (uint32_t)stage * CG;
+    // accumulators that share the stages of an item (one at least: an item without stages hands its accumulator on too)
+    auto turns_of = [&](int n) { return TURNS ? max(1, (n + a.turn_stages - 1) / a.turn_stages) : 1; };
     // first row of A of a tile's part in this CTA
     auto row_of = [&](int mt, int sub) { return ((mt * SUBS + sub) * CG + rank) * kDenseM; };
 
@@ -462,12 +464,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             Stages r(a.stages);
             uint32_t q = 0;   // accumulators filled, by both threads
             uint32_t u = 0;   // turns
-            const int turns = TURNS ? a.turns : 1;
             for (int id = first; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int i0 = (int)((int64_t)n_k * it.split / a.splits), i1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
                 // a turn's stages: from floor(n turn / turns) on, counted (the product of a long K's stages and its
                 // turns passes 32 bits)
+                const int turns = turns_of(i1 - i0);
                 const int whole = TURNS ? (i1 - i0) / turns : i1 - i0, rest = i1 - i0 - whole * turns;
                 int k1 = i0, over = 0;
                 for (int turn = 0; turn < turns; ++turn, ++u, q += SUBS) {
@@ -588,7 +590,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             tile.nt = it.nt;
             tile.half = half;
             tile.split = it.split;
-            const bool none = (int64_t)n_k * it.split / a.splits == (int64_t)n_k * (it.split + 1) / a.splits;   // no columns of K
+            const int n = (int)((int64_t)n_k * (it.split + 1) / a.splits) - (int)((int64_t)n_k * it.split / a.splits);
+            const bool none = n == 0;   // no columns of K
             tile.rows = rows;
 #pragma unroll 1
             for (int sub = 0; sub < SUBS; ++sub) {
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     if constexpr (TURNS) {
 #pragma unroll
                         for (int j = 0; j < kDenseN / 2; ++j) sum[j] = 0.f;
-                        for (int turn = 0; turn < a.turns; ++turn) {
+                        for (int turn = turns_of(n); turn > 0; --turn) {
                             const uint32_t taddr = wait();
 #pragma unroll
                             for (int c = 0; c < kDenseN / 2; c += 32) {

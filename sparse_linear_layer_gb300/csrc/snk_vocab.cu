@@ -38,6 +38,13 @@ constexpr float kDzScale = 8192.f;  // 2^13
 // stages by 6e-7, of 16 by 2.9e-7 (768 columns, one turn: 1.7e-7); one accumulator and dual tiles
 // would take 858 us for 2867 x 4096 x 65536, these take 946.
 constexpr int kTurnStages = 16;
+// Stages that an accumulator adds at most in the gradients' products: 1024 MMA steps, 16384 rows of dW or
+// columns of the vocabulary in dx.  What truncation takes off a sum of terms of one sign: 1.7e-4 of it
+// after 256 stages, 3.5e-4 after 1024 (dW of 65536 rows in fp16: error 4.2e-4 where one rounding of the
+// exact result is 2.2e-4; so 2.4e-4).  More rows of dW and wider rows' logits therefore take turns, and
+// dx has ranges of K: 8192 x 768 -> 50257 1.3% of the step, 32768 rows 8%; 128 stages would take 4% and 8% for
+// errors within 2% of a rounding's instead of 12%.
+constexpr int kSumStages = 256;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
@@ -570,14 +577,15 @@ struct Form {
 };
 // m x n over n_k stages; rows: of A that a tile loads; width: multiples of it (per CTA of a pair)
 // are possible as tile widths; most: ranges of K at most; sums: bytes of one range's sums; dual: us that
-// a dual tile has beside its stages (0: no dual tiles), its epilogue's time.
-Form pick_form(int64_t m, int64_t n, int64_t n_k, int rows, int width, int most, double sums, int num_sms, double dual) {
+// a dual tile has beside its stages (0: no dual tiles), its epilogue's time; longest: stages of a range at most.
+Form pick_form(int64_t m, int64_t n, int64_t n_k, int rows, int width, int most, double sums, int num_sms, double dual,
+               int64_t longest = INT64_MAX) {
     Form best;
     double least = 1e30;
     auto look = [&](const Form& f0, double mmas, double fixed) {
         Form f = f0;
         const int64_t tiles = ceil_div(m, f.rows()) * ceil_div(n, f.bn), units = num_sms / f.cg;
-        for (f.splits = 1; f.splits <= most && (f.splits == 1 || n_k / f.splits >= 8); ++f.splits) {
+        for (f.splits = (int)std::max<int64_t>(1, ceil_div(n_k, longest)); f.splits <= most && (f.splits == 1 || n_k / f.splits >= 8); ++f.splits) {
             const double busy = (double)std::min(units, tiles * f.splits) * f.cg;
             const double stage = std::max(mmas, (rows * (f.dual ? 2 : 1) + f.bn / f.cg) * 128 * busy / 12.5e6);
             const double t = (double)ceil_div(tiles * f.splits, units) * ((double)ceil_div(n_k, f.splits) * stage + fixed) +
@@ -659,9 +667,11 @@ struct ForwardPlan {
 
 // Columns of the vocabulary whose dz is held at a time.
 constexpr int64_t kPieceBytes = 512ll << 20;
+constexpr int kRangesMost = 64;   // of K, in dx
 
 struct BackwardPlan {
     Form z, x, w;
+    bool z_turns, w_turns;
     int64_t piece;
     void *xc, *wc, *dz;
     int32_t *index, *at, *count;
@@ -672,11 +682,13 @@ struct BackwardPlan {
     int64_t bytes;
     BackwardPlan(const Shape& h, int num_sms, void* scratch) {
         const int64_t whole = up(h.vocab, 256);
-        piece = std::max<int64_t>(256, std::min(whole, kPieceBytes / (2 * h.padded) / 256 * 256));
+        piece = std::max<int64_t>(256, std::min({whole, kPieceBytes / (2 * h.padded) / 256 * 256, (int64_t)kRangesMost * kSumStages * kDenseK}));
         piece = up(ceil_div(whole, ceil_div(whole, piece)), 256);   // equal ones
-        z = pick_form(h.rows, piece, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms, 4.5);
-        x = pick_form(h.rows, h.ld, piece / 64, h.tile_rows(), 64, 64, 8.0 * h.rows * h.ld, num_sms, 2);
-        w = pick_form(piece, h.ld, ceil_div(h.rows, 64), kDenseM, 64, 1, 0, num_sms, 2);
+        z_turns = ceil_div(h.ld, kDenseK) > kSumStages;
+        w_turns = ceil_div(h.rows, kDenseK) > kSumStages;
+        z = pick_form(h.rows, piece, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms, z_turns ? 0 : 4.5);
+        x = pick_form(h.rows, h.ld, piece / 64, h.tile_rows(), 64, kRangesMost, 8.0 * h.rows * h.ld, num_sms, 2, kSumStages);
+        w = pick_form(piece, h.ld, ceil_div(h.rows, 64), kDenseM, 64, 1, 0, num_sms, w_turns ? 0 : 2);
         Scratch s(scratch);
         count = s.take<int32_t>(4);
         most = reinterpret_cast<uint32_t*>(count + 1);
@@ -708,14 +720,21 @@ DenseArgs dense_args(const Form& f, bool bf16, bool a_mn, bool b_mn, int64_t m, 
     a.group = 16 / f.cg;
     return a;
 }
-template <bool A_MN, bool B_MN, class Epilogue, bool TURNS = false>
-int launch(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& e, int num_sms,
+template <bool A_MN, bool B_MN, bool TURNS, class Epilogue>
+int launch_form(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& e, int num_sms,
            cudaStream_t s) {
     if constexpr (!TURNS) {
         if (f.dual) return dense_launch<2, A_MN, B_MN, false, true, Epilogue>(ma, mb, a, e, num_sms, s);
     }
     return f.cg == 2 ? dense_launch<2, A_MN, B_MN, TURNS, false, Epilogue>(ma, mb, a, e, num_sms, s)
                      : dense_launch<1, A_MN, B_MN, TURNS, false, Epilogue>(ma, mb, a, e, num_sms, s);
+}
+// (turn_stages 0: one accumulator for all of K)
+template <bool A_MN, bool B_MN, class Epilogue>
+int launch(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const DenseArgs& a, const typename Epilogue::Args& e, int num_sms,
+           cudaStream_t s) {
+    return a.turn_stages ? launch_form<A_MN, B_MN, true, Epilogue>(f, ma, mb, a, e, num_sms, s)
+                         : launch_form<A_MN, B_MN, false, Epilogue>(f, ma, mb, a, e, num_sms, s);
 }
 
 int pad_weight(const Shape& h, const void* w, void* wc, int num_sms, cudaStream_t s) {
@@ -764,10 +783,8 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
     a.rows = p.gather ? p.count : nullptr;
     a.zero = p.arrived;
     const LseEpilogue::Args ea{p.part, h.padded, h.vocab};
-    a.turns = (int)ceil_div(ceil_div(h.ld, kDenseK), kTurnStages);
-    const int st = a.turns > 1 ? launch<false, false, LseEpilogue, true>(p.form, ma, mb, a, ea, num_sms, s)
-                               : launch<false, false, LseEpilogue>(p.form, ma, mb, a, ea, num_sms, s);
-    if (st != SNK_OK) return st;
+    if (ceil_div(h.ld, kDenseK) > kTurnStages) a.turn_stages = kTurnStages;
+    if (int st = launch<false, false, LseEpilogue>(p.form, ma, mb, a, ea, num_sms, s); st != SNK_OK) return st;
     FinishArgs f = {};
     f.part = p.part;
     f.ld = h.padded;
@@ -810,13 +827,14 @@ int backward(const Shape& h, const BackwardPlan& p, const void* wt, int reductio
             return SNK_ERR_CUDA;
         DenseArgs a = dense_args(p.z, bf, false, false, h.rows, width, h.ld, h.tile_rows());   // dz of the piece
         a.rows = p.count;
+        if (p.z_turns) a.turn_stages = kSumStages;
         const typename GradEpilogue<T>::Args eg{static_cast<T*>(p.dz), p.piece, width, v0, p.lse2, p.g, p.tc, scale};
         if (int st = launch<false, false, GradEpilogue<T>>(p.z, mx, mw, a, eg, num_sms, s); st != SNK_OK) return st;
         if (dx) {
             a = dense_args(p.x, bf, false, true, h.rows, h.ld, width, h.tile_rows());
             a.rows = p.count;
             const SumEpilogue::Args es{p.slab, h.padded, h.ld, v0 > 0};
-            if (int st = launch<false, true, SumEpilogue>(p.x, mz, mw_t, a, es, num_sms, s); st != SNK_OK) return st;
+            if (int st = launch_form<false, true, false, SumEpilogue>(p.x, mz, mw_t, a, es, num_sms, s); st != SNK_OK) return st;
         }
         if (dw) {
             // Rows that are not whole 16-byte chunks go over the weight's padded copy, of which this piece has
@@ -826,6 +844,7 @@ int backward(const Shape& h, const BackwardPlan& p, const void* wt, int reductio
             a = dense_args(p.w, bf, true, true, width, h.ld, h.rows);
             a.rows = p.count;
             a.rows_k = 1;
+            if (p.w_turns) a.turn_stages = kSumStages;
             const int vec = h.ld % 16 == 0 && ((uintptr_t)out & 31) == 0 ? 16 : 8;
             const typename StoreEpilogue<T>::Args eo{out, width, h.ld, scale, vec};
             if (int st = launch<true, true, StoreEpilogue<T>>(p.w, mz_t, mx_t, a, eo, num_sms, s); st != SNK_OK) return st;

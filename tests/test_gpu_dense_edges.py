@@ -120,3 +120,79 @@ def test_projection_converted_to_16_bits(dtype):
         dense.linear_q8(x, layer.weight, torch.zeros(136, device="cuda", dtype=torch.float64))
     with pytest.raises(ValueError):
         dense.linear_q8(x, layer.weight, torch.zeros(135, device="cuda", dtype=dtype))
+
+
+def slope(got, want):
+    """By how much `got` is longer than `want`, along it."""
+    return ((got.double() * want).sum() / (want * want).sum() - 1).item()
+
+
+def test_weight_gradient_of_many_rows_keeps_its_length():
+    """The tensor cores' additions truncate, toward zero: a sum of terms of one sign loses up to two units of
+    2^-23 of itself a step (a step's 16 products are added in two parts), which for an accumulator of 1024 steps is
+    2^-12 of it, and adds up to nothing where accumulators are added with rounding.  The roundings to 16 bits of dz and of the result have no
+    sign: over thousands of elements they leave less than 2^-13 of the length."""
+    rows, cols, vocab = 262144, 32, 400
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = (1 + 0.3 * torch.randn(rows, cols, device="cuda", generator=g)).half()
+    w = (0.5 * torch.randn(vocab, cols, device="cuda", generator=g)).half().requires_grad_()
+    t = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    dw, = torch.autograd.grad(dense.linear_cross_entropy(x, w, t), w)
+    want = torch.zeros(vocab, cols, device="cuda", dtype=torch.float64)
+    for i in range(0, rows, 65536):
+        p = torch.softmax(x[i:i + 65536].double() @ w.detach().double().T, 1)
+        p[torch.arange(len(p)), t[i:i + 65536]] -= 1
+        want += p.T @ x[i:i + 65536].double() / rows
+    assert abs(slope(dw, want)) < 2.0 ** -12 + 2.0 ** -13
+
+
+def test_input_gradient_over_a_long_vocabulary():
+    """Weights around 1 and targets in the last columns: each element's sum over the vocabulary grows to 1 before the
+    target takes about 1 off it.  Truncation of 1024 steps at most (as above) takes less than 2^-12 off the
+    first, always of the same sign; the mean over a row's elements of what dz's roundings leave is far below."""
+    rows, cols, vocab = 4096, 1024, 65536
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = (0.05 * torch.randn(rows, cols, device="cuda", generator=g)).half().requires_grad_()
+    w = (1 + 0.05 * torch.randn(vocab, cols, device="cuda", generator=g)).half()
+    t = torch.randint(vocab - 100, vocab, (rows,), device="cuda", generator=g)
+    dx, = torch.autograd.grad(dense.linear_cross_entropy(x, w, t, reduction="sum"), x)
+    off = []
+    for i in range(0, rows, 1024):
+        p = torch.softmax(x.detach()[i:i + 1024].double() @ w.double().T, 1)
+        p[torch.arange(len(p)), t[i:i + 1024]] -= 1
+        off.append(dx[i:i + 1024].double() - p @ w.double())
+    assert abs(torch.cat(off).mean().item()) < 2.0 ** -12
+
+
+def test_gradients_of_wide_fp16_rows_over_several_pieces():
+    """fp16, rows of ordinary width, a vocabulary in two pieces of 25 000 columns: within what one rounding of the exact
+    result is off and a fifth, norm against norm (dz's rounding alone: a twelfth at most)."""
+    rows, cols, vocab = 8192, 512, 50001
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(rows, cols, device="cuda", generator=g).half().requires_grad_()
+    w = (2 / cols ** 0.5 * torch.randn(vocab, cols, device="cuda", generator=g)).half().requires_grad_()
+    t = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    dx, dw = torch.autograd.grad(dense.linear_cross_entropy(x, w, t, reduction="sum"), (x, w))
+    want_x, want_w = torch.empty_like(x, dtype=torch.float64), torch.zeros_like(w, dtype=torch.float64)
+    for i in range(0, rows, 2048):
+        xd = x.detach()[i:i + 2048].double()
+        p = torch.softmax(xd @ w.detach().double().T, 1)
+        p[torch.arange(len(p)), t[i:i + 2048]] -= 1
+        want_x[i:i + 2048] = p @ w.detach().double()
+        want_w += p.T @ xd
+    for got, want in ((dx, want_x), (dw, want_w)):
+        assert (got.double() - want).norm() <= 1.2 * (want.half().double() - want).norm()
+
+
+def test_gradients_of_very_wide_rows():
+    """Logits of more columns than one accumulator adds: p from the same kind of sums as the loss."""
+    rows, cols, vocab = 200, 40000, 600
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(rows, cols, device="cuda", generator=g).bfloat16().requires_grad_()
+    w = (2 / cols ** 0.5 * torch.randn(vocab, cols, device="cuda", generator=g)).bfloat16().requires_grad_()
+    t = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    t[5] = -100
+    outs = torch.autograd.grad(dense.linear_cross_entropy(x, w, t, reduction="sum"), (x, w))
+    want = reference(x.detach(), w.detach(), t, torch.ones(rows, device="cuda"))
+    for got, exact, magnitudes in zip(outs, want[:2], want[2:]):
+        assert within(got, exact, magnitudes, torch.bfloat16, 0)
