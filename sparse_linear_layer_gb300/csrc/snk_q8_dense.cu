@@ -590,21 +590,26 @@ struct Q8Plan {
         copy_b = ldb % 16 != 0;
         ld = up(K, 16);
         const int n_g = (int)ceil_div(K, 128);
-        // The tile and the ranges of K whose waves take least. Times in us as measured: of a group,
-        // of a tile beside its groups, of joining ranges and their sums, written and read: 8 bytes at 8 TB/s
-        // from the L2 (2304 x 768 over 32768: 5 ranges 79 us, 2 ranges 87), at half of it where they do not stay there.
+        // The tile and the ranges of K whose waves take least. Times in us as measured where all SMs are busy (full
+        // waves of tiles, K = 512 to 16384): of a group, with scales of blocks and of rows; of a tile beside its groups; of
+        // joining ranges and their sums, written and read: 8 bytes at 8 TB/s from the L2 (2304 x 768 over 32768: 5 ranges
+        // 77 us, 2 ranges 87), at half of it where they do not stay there.  A CTA by itself with 256 columns is bound by
+        // the L2's bytes (0.8 for all SMs), by its own accumulators where few are busy.  Over 62 shapes (17 to
+        // 16384 rows) times both kinds of scales the form so chosen takes 1% more than the best one, 19% at most.
         struct Form {
             int cg, bn;
-            double group;
+            double blocks, rows;
         };
-        constexpr Form forms[] = {{2, 256, 0.33}, {1, 256, 0.40}, {1, 128, 0.26}, {1, 64, 0.24}};
+        constexpr Form forms[] = {{2, 256, 0.44, 0.60}, {1, 256, 0.50, 0.75}, {1, 128, 0.36, 0.41}, {1, 64, 0.30, 0.335}};
         double best = 1e30;
         for (const Form& f : forms) {
             if (f.cg == 2 && M <= 128) continue;
             const int64_t mt = ceil_div(M, 128 * f.cg), nt = ceil_div(N, f.bn), units = num_sms / f.cg;
             for (int sp = 1; sp <= 16 && (sp == 1 || n_g / sp >= 4); ++sp) {
-                const double waves = (double)ceil_div(mt * nt * sp, units);
-                const double t = waves * ((double)ceil_div(n_g, sp) * f.group + 1.5) + (sp > 1 ? 3.0 + (4.0 * sp * M * N < 64e6 ? 1e-6 : 2e-6) * sp * M * N : 0.0);
+                const double waves = (double)ceil_div(mt * nt * sp, units), busy = std::min(1.0, (double)(mt * nt * sp) / (double)units);
+                const double group = std::max(blocks ? f.blocks : f.rows, f.cg == 1 && f.bn == 256 ? 0.8 * busy : 0.0);
+                const double t = waves * ((double)ceil_div(n_g, sp) * group + 1.5) +
+                                 (sp > 1 ? 2.0 + (4.0 * sp * M * N < 64e6 ? 1e-6 : 2e-6) * sp * M * N : 0.0);
                 if (t < best) {
                     best = t;
                     cg = f.cg;
