@@ -583,9 +583,6 @@ struct Q8Plan {
     float *ta, *tb;
     int64_t bytes;
     Q8Plan(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, bool blocks, int num_sms, void* scratch) {
-        // Few rows: B's codes once by mma.sync, or the tiles below (us, 10000 x 10000, 8 rows: 24 against
-        // 21, 16 rows: 36 against 22; 4096 x 4096: 4.8 against 8.8, 5.8 against 8.4; 2304 x 768: 2 against 5).
-        rows = M <= 8 || (M <= kRowsMax && N * K <= 32000000);
         copy_a = lda % 16 != 0;
         copy_b = ldb % 16 != 0;
         ld = up(K, 16);
@@ -618,6 +615,14 @@ struct Q8Plan {
                 }
             }
         }
+        // Few rows: B's codes once by mma.sync, by the waves of its blocks (4 to an SM, 2 with two tiles of rows) and the
+        // rounds of a block's warps over the groups.  us, W from memory, blocks' scales, this and the tiles: 8 rows
+        // 768 -> 2304 1.8 and 4.4, 4096 -> 4096 6.6 and 10.3, 768 -> 50257 12.0 and 13.4, 12288 -> 8192 21.0 and 23.9, 10000 -> 10000
+        // 29.9 and 24.4; 16 rows 4096 -> 4096 7.4 and 10.6, 768 -> 50257 19.2 and 14.0.  Tiles take 2 us beside the account
+        // above, 4 with the turning of rows' scales.
+        const double few = 1.3 + (M <= 8 ? 1.5 : 1.35) * (double)ceil_div(ceil_div(N, 16), (M <= 8 ? 4 : 2) * num_sms) *
+                                     (double)ceil_div(n_g, kRowsWarps);
+        rows = M <= kRowsMax && few <= best + (blocks ? 2.0 : 4.0);
         if (rows) splits = 1;
         n_mt = (int)ceil_div(M, 128 * cg);
         n_nt = (int)ceil_div(N, bn);

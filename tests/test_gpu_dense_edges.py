@@ -8,7 +8,8 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from sparse_linear_layer_gb300 import dense  # noqa: E402
+from sparse_linear_layer_gb300 import dense, q8  # noqa: E402
+from tests import dense_ref  # noqa: E402
 from tests.gpu_util import need_gpu  # noqa: E402
 
 
@@ -196,3 +197,21 @@ def test_gradients_of_very_wide_rows():
     want = reference(x.detach(), w.detach(), t, torch.ones(rows, device="cuda"))
     for got, exact, magnitudes in zip(outs, want[:2], want[2:]):
         assert within(got, exact, magnitudes, torch.bfloat16, 0)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 8, 9, 16, 17])
+@pytest.mark.parametrize("cols,out", [(10000, 10000), (768, 50257), (4096, 6001)])
+@pytest.mark.parametrize("blocks", [True, False])
+def test_few_rows_of_large_weights(rows, cols, out, blocks):
+    """Products of few rows by whichever kernel the weight's size and the scales call for: each group of 128 is exact up to the tensor
+    cores' additions (within 10 * 2^-23 of its terms' magnitudes), the groups are added with rounding (or by eight warps and
+    then added)."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    a = q8.pack(torch.randn(rows, cols, device="cuda", generator=g), "e4m3", 128)
+    w = torch.randn(out, cols, device="cuda", generator=g)
+    b = q8.pack_blocks(w) if blocks else q8.pack(w, "e4m3", 128)
+    y = q8.matmul(a, b)
+    assert torch.equal(y, q8.matmul(a, b))
+    va, vb = dense_ref.values(a.codes, a.scales), dense_ref.values(b.codes, b.scales, blocks)
+    tol = (10 + -(-cols // 128)) * 2.0 ** -23 * (va.abs() @ vb.abs().T)
+    assert bool(((y.double() - va @ vb.T).abs() <= tol).all())
