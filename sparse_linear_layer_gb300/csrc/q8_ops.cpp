@@ -592,17 +592,6 @@ PyObject* op_vocab_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// vocab_loss_backward(x, weight, target, ignore, reduction, lse, dloss, want dx, want dweight, stream)
-//   -> (dx or None, dweight or None)
-PyObject* op_vocab_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 10, [&] {
-        Head h(tensor(a[0], "x"), tensor(a[1], "weight"), tensor(a[2], "target"), integer(a[3]), integer(a[4]));
-        const OnStream on(a[9], h.x.device());
-        auto [dx, dw] = h.backward(tensor(a[5], "lse"), tensor(a[6], "dloss"), PyObject_IsTrue(a[7]), PyObject_IsTrue(a[8]), on.get());
-        return tuple(std::move(dx), std::move(dw));
-    });
-}
-
 using torch::autograd::AutogradContext;
 using torch::autograd::variable_list;
 
@@ -876,7 +865,6 @@ PyMethodDef methods[] = {OP("load", op_load),
                          OP("pack_blocks", op_pack_blocks),
                          OP("matmul", op_matmul),
                          OP("vocab_loss", op_vocab_loss),
-                         OP("vocab_loss_backward", op_vocab_loss_backward),
                          OP("linear_cross_entropy", op_linear_cross_entropy),
                          OP("linear_q8", op_linear_q8),
                          {nullptr, nullptr, 0, nullptr}};

@@ -453,7 +453,6 @@ struct Q8RowsArgs {
     const float *sa, *sb;
     const float* bias;
     void* y;
-    int dtype;
     int blocks_b;          // B's scales are of 128 x 128 blocks
 };
 // NT: tiles of 8 rows of A.
@@ -726,7 +725,7 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
     }
     const int n_g = (int)ceil_div(K, 128);
     if (p.rows) {
-        const Q8RowsArgs r{pa, pb, lda, ldb, M, N, K, n_g, a_scales, b_scales, bias, y, dtype, b_blocks};
+        const Q8RowsArgs r{pa, pb, lda, ldb, M, N, K, n_g, a_scales, b_scales, bias, y, b_blocks};
         return dtype == SNK_F32 ? launch_rows<float>(r, s) : dtype == SNK_F16 ? launch_rows<__half>(r, s) : launch_rows<__nv_bfloat16>(r, s);
     }
     CUtensorMap m[5];

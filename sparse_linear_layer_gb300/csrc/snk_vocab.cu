@@ -638,7 +638,7 @@ struct ForwardPlan {
     int32_t *index, *at, *count, *arrived;
     int64_t* tc;
     float2* part;
-    float *sums, *row_lse;
+    float* sums;
     int64_t bytes;
     ForwardPlan(const Shape& h, int num_sms, void* scratch) {
         form = pick_form(h.rows, h.vocab, ceil_div(h.cols, 64), h.tile_rows(), 32, 1, 0, num_sms,
@@ -660,7 +660,6 @@ struct ForwardPlan {
         wc = s.take<uint16_t>(h.pads() ? h.vocab * h.ld : 0);
         part = s.take<float2>((int64_t)2 * n_nt * h.padded);
         sums = s.take<float>(2 * (int64_t)blocks);
-        row_lse = nullptr;
         bytes = s.used;
     }
 };
@@ -737,7 +736,7 @@ int launch(const Form& f, const CUtensorMap& ma, const CUtensorMap& mb, const De
                          : launch_form<A_MN, B_MN, false, Epilogue>(f, ma, mb, a, e, num_sms, s);
 }
 
-int pad_weight(const Shape& h, const void* w, void* wc, int num_sms, cudaStream_t s) {
+int pad_weight(const Shape& h, const void* w, void* wc, cudaStream_t s) {
     return launch_after(k_pad_rows, (unsigned)std::min<int64_t>(ceil_div(h.vocab * ceil_div(h.ld, 256), 8), 1 << 20), 256, 0, 1, s,
                         static_cast<const uint8_t*>(w), 2 * h.cols, static_cast<uint8_t*>(wc), h.vocab, 2 * h.cols, 2 * h.ld);
 }
@@ -770,7 +769,7 @@ int forward(const Shape& h, const void* x, const void* w, const int64_t* target,
     }
     const void* wt = w;
     if (h.pads()) {
-        if (int st = pad_weight(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
+        if (int st = pad_weight(h, w, p.wc, s); st != SNK_OK) return st;
         wt = p.wc;
     }
     CUtensorMap ma, mb;
@@ -900,7 +899,7 @@ int backward_rows(const Shape& h, const BackwardPlan& p, const void* x, const vo
     if (int st = launch_after(k_vocab_rows<T>, (unsigned)ceil_div(h.rows, r.per_block), 256, 0, 1, s, r); st != SNK_OK) return st;
     const void* wt = w;
     if (h.pads()) {
-        if (int st = pad_weight(h, w, p.wc, num_sms, s); st != SNK_OK) return st;
+        if (int st = pad_weight(h, w, p.wc, s); st != SNK_OK) return st;
         wt = p.wc;
     }
     return backward<T>(h, p, wt, reduction, dx, dw, num_sms, s);

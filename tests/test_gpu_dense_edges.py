@@ -8,7 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from sparse_linear_layer_gb300 import dense, q8  # noqa: E402
+from sparse_linear_layer_gb300 import binding, dense, q8  # noqa: E402
 from tests import dense_ref  # noqa: E402
 from tests.gpu_util import need_gpu  # noqa: E402
 
@@ -215,3 +215,48 @@ def test_few_rows_of_large_weights(rows, cols, out, blocks):
     va, vb = dense_ref.values(a.codes, a.scales), dense_ref.values(b.codes, b.scales, blocks)
     tol = (10 + -(-cols // 128)) * 2.0 ** -23 * (va.abs() @ vb.abs().T)
     assert bool(((y.double() - va @ vb.T).abs() <= tol).all())
+
+
+def test_entry_points_by_the_c_calls_names():
+    """binding's functions of the dense calls give the bits of the calls on tensors."""
+    rows, cols, vocab = 150, 200, 1000
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(rows, cols, device="cuda", generator=g).bfloat16()
+    w = (0.1 * torch.randn(vocab, cols, device="cuda", generator=g)).bfloat16()
+    t = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    t[3] = -100
+
+    def scratch(n):
+        return torch.empty(n, device="cuda", dtype=torch.uint8) if n else None
+    for reduction, name in enumerate(("none", "sum", "mean")):
+        a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+        want = dense.linear_cross_entropy(a, b, t, reduction=name)
+        up = torch.randn(want.shape, device="cuda", generator=g)
+        wants = torch.autograd.grad(want, (a, b), up)
+        loss, lse = torch.empty_like(want), torch.empty(rows, device="cuda")
+        binding.snk_vocab_loss(x, w, binding.SNK_BF16, t, -100, rows, cols, vocab, reduction, loss, lse,
+                               scratch(binding.snk_vocab_loss_scratch(rows, cols, vocab, False)))
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        binding.snk_vocab_loss_backward(x, w, binding.SNK_BF16, t, -100, lse, up, rows, cols, vocab, reduction, dx, dw,
+                                        scratch(binding.snk_vocab_loss_scratch(rows, cols, vocab, True)))
+        assert torch.equal(loss, want) and torch.equal(dx, wants[0]) and torch.equal(dw, wants[1])
+    q, qt = q8.pack_both(x)
+    codes, codes_t = torch.empty(rows, 256, device="cuda", dtype=torch.uint8)[:, :cols], torch.empty(cols, rows, device="cuda", dtype=torch.uint8)
+    scales, scales_t, sums = torch.empty_like(q.scales), torch.empty_like(qt.scales), torch.empty(cols, device="cuda")
+    binding.snk_q8_pack_both(x, binding.SNK_BF16, rows, cols, codes, scales, codes_t, scales_t, sums,
+                             scratch(binding.snk_q8_pack_both_scratch(rows, cols)))
+    assert torch.equal(codes, q.codes.view(torch.uint8)) and torch.equal(codes_t, qt.codes.view(torch.uint8))
+    assert torch.equal(scales, q.scales) and torch.equal(scales_t, qt.scales)
+    assert bool(((sums.double() - x.double().sum(0)).abs() <= rows * 2.0 ** -24 * x.double().abs().sum(0)).all())
+    b8, b8t = q8.pack_blocks(w, transposed=True)
+    bc, bt = torch.empty(vocab, cols, device="cuda", dtype=torch.uint8), torch.empty(cols, vocab, device="cuda", dtype=torch.uint8)
+    bs, bst = torch.empty_like(b8.scales), torch.empty_like(b8t.scales)
+    binding.snk_q8_pack_blocks(w, binding.SNK_BF16, vocab, cols, bc, bs, bt, bst)
+    assert torch.equal(bc, b8.codes.contiguous().view(torch.uint8)) and torch.equal(bt, b8t.codes.contiguous().view(torch.uint8))
+    assert torch.equal(bs, b8.scales) and torch.equal(bst, b8t.scales)
+    for m in (rows, 5):
+        y = torch.empty(m, vocab, device="cuda", dtype=torch.bfloat16)
+        a = codes[:m]   # rows 256 bytes apart, the weight's 200, which is no multiple of 16
+        binding.snk_q8_matmul(a, scales, bc, bs, True, m, vocab, cols, None, y, binding.SNK_BF16,
+                              scratch(binding.snk_q8_matmul_scratch(m, vocab, cols, 256, 200, True)))
+        assert torch.equal(y, q8.matmul(q8.Q8Tensor(q.codes[:m], q.scales[:m], 128), b8, dtype=torch.bfloat16))
