@@ -260,3 +260,17 @@ def test_entry_points_by_the_c_calls_names():
         binding.snk_q8_matmul(a, scales, bc, bs, True, m, vocab, cols, None, y, binding.SNK_BF16,
                               scratch(binding.snk_q8_matmul_scratch(m, vocab, cols, 256, 200, True)))
         assert torch.equal(y, q8.matmul(q8.Q8Tensor(q.codes[:m], q.scales[:m], 128), b8, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("cols", [16, 9])
+def test_few_rows_of_a_vocabulary_of_more_than_a_million(cols):
+    """More columns than dx's ranges of K hold at a time: pieces of the vocabulary, for few rows too."""
+    rows, vocab = 3, 1_300_001
+    g = torch.Generator(device="cuda").manual_seed(10)
+    x = torch.randn(rows, cols, device="cuda", generator=g).bfloat16().requires_grad_()
+    w = torch.randn(vocab, cols, device="cuda", generator=g).bfloat16().requires_grad_()
+    t = torch.tensor([vocab - 1, 0, 1_048_576], device="cuda")
+    outs = torch.autograd.grad(dense.linear_cross_entropy(x, w, t, reduction="sum"), (x, w))
+    want = reference(x.detach(), w.detach(), t, torch.ones(rows, device="cuda"))
+    for got, exact, magnitudes in zip(outs, want[:2], want[2:]):
+        assert within(got, exact, magnitudes, torch.bfloat16, 0)
