@@ -15,7 +15,7 @@
 //              w < 8 or not, the first or second half of the columns.
 // Every wait is bounded (kTcWaitCycles). A producer or an issuing thread whose wait ran out
 // stops; an epilogue warp whose wait ran out writes NaN for that tile and all that it still has,
-// and gives no accumulator back any more: arrivals are only counted, and one too many would
+// and gives no accumulator back any more (it arrives on the sink): arrivals are only counted, and one too many would
 // stand for a warp that still reads. The others then run out too. No CTA ends before its copies
 // have landed (land_all) and its MMAs are done (fin), whoever stopped.
 #pragma once
@@ -29,10 +29,11 @@ constexpr int kDenseM = 128;             // rows of a tile per CTA (TMEM lanes)
 constexpr int kDenseN = 256;             // columns of a tile at most
 constexpr int kDenseK = 64;              // columns of K per stage: 128 bytes
 // Four warps of roles and eight of the epilogue, whose threads may keep 128 sums; registers as launched
-// (168 a thread) and as redistributed.
+// (168 a thread) and as redistributed (with 40 and 232 the dual tiles' roles spill: dW of 100 x 768 -> 50257 37.5 us, 34.7 without).
 constexpr int kDenseThreads = 384;
-constexpr int kRoleRegs = 40, kSumRegs = 232;
-static_assert(128 * kRoleRegs + 256 * kSumRegs <= kDenseThreads * 168, "the shares come out of the launch's registers");
+constexpr int kRoleRegs = 48, kSumRegs = 224;
+constexpr bool shares_fit(int role, int sum) { return 128 * role + 256 * sum <= kDenseThreads * 168; }
+static_assert(shares_fit(kRoleRegs, kSumRegs), "the shares come out of the launch's registers");
 template <int R>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -125,11 +126,20 @@ __device__ __forceinline__ uint32_t first_cta(const void* p) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
     return r;
 }
+// An epilogue warp gives accumulators back by arriving at `base` + 8 times the accumulator's number; after a wait that ran
+// out base is that of the CTA's sink, barriers that nobody waits for (a test of `ok` at each arrival instead cost the
+// 8-bit product 2%).
+constexpr int kSinkCount = 1 << 19;
 // (relaxed: what the arrival orders are accumulator reads, by tcgen05.fence; a release at
 // cluster scope waits for all of the warp's memory accesses first, spills and scales among
 // them, and was a third of the 8-bit product's stall cycles)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void give_back(uint32_t bar) {
+    if constexpr (CG == 1) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+    else mbar_arrive_cluster(bar);
 }
 // The MMAs issued so far arrive on the barrier, in both CTAs of a pair.
 template <int CG>
@@ -147,6 +157,7 @@ __device__ __forceinline__ void dense_commit(uint64_t* bar) {
 // waits for both threads' before it gives the memory back (each of them ends after a few
 // bounded waits).
 __device__ __forceinline__ void wait_for_mmas(uint64_t (&fin)[2]) {
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) mbar_wait(&fin[i], 0, 4 * kTcDrainCycles);
 }
 // What the second CTA's producer tells the first one at its end, in the first one's memory.
@@ -182,13 +193,16 @@ __device__ __forceinline__ void land_all(uint64_t* full, uint64_t (&fin)[2], Pai
         if (told) other = *reinterpret_cast<volatile uint32_t*>(&peer.issued);
         if (other != issued) {
             wait_for_mmas(fin);
+#pragma unroll 1
             for (uint32_t w = other; w < issued; ++w)
                 asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[w % stages])), "r"(bytes)
                              : "memory");
+#pragma unroll 1
             for (uint32_t w = issued; w < other; ++w) mbar_expect_tx(&full[w % stages], bytes);
         }
     }
     const uint32_t end = max(issued, other);
+#pragma unroll 1
     for (uint32_t w = end > (uint32_t)stages ? end - stages : 0; w < end; ++w)
         mbar_wait(&full[w % stages], (w / stages) & 1, kTcDrainCycles);
 }
@@ -354,7 +368,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     constexpr int S = kDenseStages, SUBS = DUAL ? 2 : 1;
     extern __shared__ __align__(1024) unsigned char dense_raw[];
     unsigned char* sm = dense_raw + ((1024 - (smem_u32(dense_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin[2], hand[2];
+    __shared__ uint64_t full[S], empty[S], accf[2], acce[2], fin[2], hand[2], sink[2];
     __shared__ PairEnd peer;
     __shared__ uint32_t tmem_base;
 
@@ -370,6 +384,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             mbar_init(&acce[i], kDenseEpilogueWarps * CG);
             mbar_init(&fin[i], 1);
             mbar_init(&hand[i], 1);
+            mbar_init(&sink[i], kSinkCount);
         }
         mbar_init(&peer.bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -410,9 +425,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         fewer_registers<kRoleRegs>();
         if (warp == 0 && lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
-            uint32_t issued = 0;
+            int id = first, left = 0;       // left: stages of the last item that have not been loaded
             Stages r(a.stages);
-            for (int id = first; id < items && ok; id += step) {
+            for (; id < items && ok; id += step) {
                 const DenseItem it = DenseItem::of(id, n_mt, a.n_nt, a.splits, a.group);
                 const int k0 = (int)((int64_t)n_k * it.split / a.splits), k1 = (int)((int64_t)n_k * (it.split + 1) / a.splits);
                 const int n0 = it.nt * a.bn + rank * half_b;
@@ -420,6 +435,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     const int s = r.slot;
                     if (used && !mbar_wait(&empty[s], r.parity ^ 1)) {
                         ok = false;
+                        left = k1 - k;
                         break;
                     }
                     unsigned char* sa = sm + s * stage;
@@ -445,9 +461,19 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     }
                     r.next();
                     used |= r.slot == 0;
-                    ++issued;
                 }
             }
+            // (counted afterwards: a counter in the loop spilled registers there)
+            uint32_t issued = 0;
+            if (a.splits == 1) {
+                issued = (uint32_t)((id - first) / step) * (uint32_t)n_k;
+            } else {
+                for (int i = first; i < id; i += step) {
+                    const int split = DenseItem::of(i, n_mt, a.n_nt, a.splits, a.group).split;
+                    issued += (uint32_t)((int64_t)n_k * (split + 1) / a.splits - (int64_t)n_k * split / a.splits);
+                }
+            }
+            issued -= (uint32_t)left;
             land_all<CG>(full, fin, peer, rank, issued, a.stages, stage);
         }
         // One thread for all turns left the tensor cores idle for 850 cycles where they changed the
@@ -558,27 +584,24 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             }
             dense_commit<CG>(&fin[mine]);
         }
-        if (warp == 3 && lane == 0) wait_for_mmas(fin);
     } else {
         more_registers<kSumRegs>();
         const int half = warp >= 8 ? 1 : 0, quarter = warp & 3;
         const int hc = a.bn / 2;
         const uint32_t lanes = tmem + half * hc + ((uint32_t)(quarter * 32) << 16);
         bool ok = true;
-        uint32_t q = 0;
+        uint32_t q = 0, base = CG == 1 ? smem_u32(acce) : first_cta(acce);
         auto wait = [&] {
             if (ok) ok = mbar_wait(&accf[q & 1], (q >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
+            if (!ok) base = smem_u32(sink);
             tc_fence_after();
             return lanes + (q & 1) * kDenseN;
         };
         auto release = [&] {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && ok) {
-                if constexpr (CG == 1) mbar_arrive(&acce[q & 1]);
-                else mbar_arrive_cluster(first_cta(&acce[q & 1]));
-            }
+            if (lane == 0) give_back<CG>(base + 8 * (q & 1));
             ++q;
         };
         for (int id = first; id < items; id += step) {
@@ -636,6 +659,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             }
         }
     }
+    if (warp == 3) wait_for_mmas(fin);
     __syncwarp();
     tc_fence_before();
     __syncthreads();

@@ -21,8 +21,11 @@ namespace snk {
 namespace {
 
 // Threads as in k_dense; with 216 registers for the sums' threads instead of 232 some spilled
-// (8192 x 10000 x 10000 639 us against 612).
+// (8192 x 10000 x 10000 639 us against 612).  With 232 the two kernels of 128 columns spill 12 and 24 bytes, those of
+// row scales and 256 columns 4, the others nothing.
 constexpr int kQ8Threads = kDenseThreads;
+constexpr int kQ8RoleRegs = 40, kQ8SumRegs = 232;
+static_assert(shares_fit(kQ8RoleRegs, kQ8SumRegs), "the shares come out of the launch's registers");
 
 struct Q8DenseArgs {
     int64_t M, N;
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     unsigned char* stages = turn + kDenseEpilogueWarps * kOutBytes + (ROWS ? kScaleSlots * (kDenseM + BN) * 4 : 0);
     const int a_bytes = a.a_rows * 128, stage = a_bytes + HB * 128;
     const uint32_t stage_tx = (uint32_t)(stage + (ROWS ? (kDenseM + BN) * 4 : 0));   // with its scales
-    __shared__ uint64_t full[S], empty[S], accf[NB], acce[NB], fin[2];
+    __shared__ uint64_t full[S], empty[S], accf[NB], acce[NB], fin[2], sink[NB];
     __shared__ PairEnd peer;
     __shared__ uint32_t tmem_base;
 
@@ -136,6 +139,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         for (int i = 0; i < NB; ++i) {
             mbar_init(&accf[i], 1);
             mbar_init(&acce[i], kDenseEpilogueWarps * CG);
+            mbar_init(&sink[i], kSinkCount);
         }
         mbar_init(&fin[0], 1);
         mbar_init(&fin[1], 1);
@@ -154,7 +158,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (warp < 4) {
-        fewer_registers<kRoleRegs>();
+        fewer_registers<kQ8RoleRegs>();
         if (warp == 0 && lane == 0) {
             bool ok = true, used = false;   // used: every slot has been filled once
             Stages r(a.stages);
@@ -215,12 +219,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             }
             dense_commit<CG>(&fin[mine]);
         }
-        if (warp == 3 && lane == 0) wait_for_mmas(fin);
     } else {
-        more_registers<kSumRegs>();
+        more_registers<kQ8SumRegs>();
         const int half = warp >= 8 ? 1 : 0, quarter = warp & 3;
         const uint32_t lanes = tmem + half * HC + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t free0 = CG == 1 ? 0 : first_cta(&acce[0]);
+        uint32_t base = CG == 1 ? smem_u32(acce) : first_cta(acce);
         bool ok = true;
         uint32_t w = 0;   // groups done
         for (int id = first; id < items; id += step) {
@@ -249,9 +252,16 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
                 const float* at = scales + (w % kScaleSlots) * (kDenseM + BN);
                 const float* sbp = at + kDenseM + half * HC;
-                if (ok) ok = mbar_wait(&accf[ab], (w / NB) & 1);
-                if constexpr (ROWS) ok = __all_sync(0xffffffffu, ok);
-                else __syncwarp();   // (the lanes agree on ok at the end: 8192^3 416 -> 396 us)
+                if (ok && !mbar_wait(&accf[ab], (w / NB) & 1)) {
+                    ok = false;
+                    base = smem_u32(sink);
+                }
+                if constexpr (ROWS) {
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) base = smem_u32(sink);
+                } else {   // (the lanes agree on ok at the end: 8192^3 416 -> 396 us; what lane 0, which gives back, has
+                    __syncwarp();   // waited for is there for all)
+                }
                 tc_fence_after();
                 if constexpr (ROWS) s = at[quarter * 32 + lane];
                 const uint32_t ta = lanes + ab * BN;
@@ -265,10 +275,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     } else {   // all read: the accumulator is free before its last columns are added
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0 && ok) {   // (no arrival after a wait that ran out, as in k_dense)
-                            if constexpr (CG == 1) mbar_arrive(&acce[ab]);
-                            else mbar_arrive_cluster(free0 + 8 * ab);
-                        }
+                        if (lane == 0) give_back<CG>(base + 8 * ab);
                     }
                     const uint32_t(&u)[32] = r[(c / 32) & 1];
 #pragma unroll
@@ -287,6 +294,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
+                base = smem_u32(sink);
 #pragma unroll
                 for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
             }
@@ -347,6 +355,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         }
         if (a.vec && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    if (warp == 3) wait_for_mmas(fin);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
