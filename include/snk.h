@@ -551,7 +551,8 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
  * part: its loss and lse are zero, and nothing of it, a NaN least of all, reaches
  * another output.  A target outside [0, vocab) that is not `ignore` gives the loss NaN.
  * Logits, sums and losses are fp32 (products of 16-bit numbers, exact, accumulated by
- * the tensor cores, whose fp32 additions truncate).
+ * the tensor cores, whose fp32 additions truncate; 64 steps of 16 products at most, then with
+ * rounding: the loss is off by 2e-7 to 1e-6 of itself).  Logits from 2.3e38 on count as infinite.
  * reduction 0: loss [rows]; 1: [1], their sum; 2: [1], their mean over the rows that
  * count (NaN where none does).  lse [rows] or NULL is what the gradient needs.
  *
@@ -561,12 +562,16 @@ int snk_q8_matmul(const void* a, int64_t lda, const float* a_scales, const void*
  * from logits computed again, a piece of the vocabulary at a time; dx [rows, cols] and
  * dweight [vocab, cols] have the type `dtype`; either may be NULL.  dz is rounded to
  * `dtype` (scaled by a power of two, and for reductions 1 and 2 without g, which multiplies
- * the results) before the two products, which accumulate in fp32.
- * Ignored rows get dx = 0; a row whose target is out of range gets NaN.
+ * the results) before the two products, which accumulate in fp32, 1024 truncating steps at most
+ * before a rounded addition (a sum of terms of one sign is short by up to 2e-4 of itself).
+ * Ignored rows get dx = 0, whatever dloss is; a row whose target is out of range gets NaN.
  *
  * scratch: snk_vocab_loss_scratch(rows, cols, vocab, backward) bytes (backward 0 or 1)
- * on the current device, 256-byte aligned: at most about 512 MB (or 512 bytes a row) for
- * dz, and some copies of x and dx; where cols is no multiple of 8, also copies of x and
+ * on the current device, 256-byte aligned.  Forward: the logits' partial sums, 16 bytes for a row and each
+ * 256 columns of the vocabulary or fewer (64 at the least), which no bound keeps small (65536 rows of
+ * 131072 columns: 537 MB), and, where rows are gathered, a copy of x.  Backward: at most about 512 MB (or 512 bytes a row) for
+ * dz, a copy of x, and dx in fp32 for each range of the vocabulary that is added by itself (64 at most, of
+ * 16384 columns or fewer).  Where cols is no multiple of 8, also copies of x and
  * weight with padded rows.  No state and no allocation: the calls only enqueue work, may be captured into
  * a graph, and give the same bits when repeated.  rows == 0: dweight and a sum are zero,
  * a mean is NaN.  A wait in a kernel that runs out (about two seconds) leaves NaN.

@@ -1,5 +1,5 @@
 """The dense operators at the edges of what their calls take: very long rows and sums, upstream
-gradients at the ends of fp32, forward-mode differentiation, layers converted to 16 bits, and the
+gradients at the ends of fp32, layers converted to 16 bits, few rows of large weights, and the
 entry points by the names of the C calls."""
 import math
 
